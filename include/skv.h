@@ -571,6 +571,97 @@ skv_status skv_paris_decode_step(const skv_problem *p, const skv_paris *paris, c
                                  int32_t *idx, void *out, float *lse, void *ws, size_t ws_bytes,
                                  int32_t *dev_status, void *stream);
 
+/* ------------------------------------------------------------------------------------
+ * New tokens: the norm and rotation of queries and keys, and their append to the cache.
+ *
+ * A row x of one head (d_qk entries) becomes, in fp32 and rounded once at the end,
+ *   norm      y_j = gamma_j x_j / sqrt(mean_{i < norm_dim} x_i^2 + eps)   for j < norm_dim
+ *             (the other entries, and every entry where gamma is NULL, are taken as they are);
+ *   rotation  by the token's position t: the pairs (a, b) of the rotated span
+ *             [rot_start, rot_start + rot_dim) turn by the angle t * inv_freq[i],
+ *             (a, b) -> (a cos - b sin, b cos + a sin); pair i is
+ *               SKV_ROPE_HALF   (rot_start + i, rot_start + i + rot_dim / 2)
+ *               SKV_ROPE_PAIR   (rot_start + 2 i, rot_start + 2 i + 1).
+ * inv_freq is taken as exact and the angle is reduced to a turn in 64-bit fixed point
+ * before any fp32 arithmetic, so far positions lose nothing.
+ * ------------------------------------------------------------------------------------ */
+#define SKV_ROPE_HALF 0
+#define SKV_ROPE_PAIR 1
+
+/*
+ *   rot_start, rot_dim  the rotated span, inside [0, d_qk]; rot_dim 0: no rotation (inv_freq may be NULL).
+ *   style               SKV_ROPE_HALF or SKV_ROPE_PAIR.
+ *   norm_dim            entries the norm covers, in [1, d_qk]; 0: all d_qk.
+ *   eps                 added to the mean square; >= 0.
+ *   inv_freq            device fp32 [rot_dim / 2]: radians a position.
+ *   q_gamma, k_gamma    device [norm_dim] of the element type, 16-byte aligned: the norm's
+ *                       weights, shared by the heads; NULL: that side is not normed.
+ * rot_start, norm_dim and d_qk multiples of 8, rot_dim a multiple of 8 (16 for SKV_ROPE_HALF),
+ * d_qk and d_v at most 1024, else SKV_ERR_UNSUPPORTED.
+ */
+typedef struct skv_rotary {
+  int32_t rot_start;
+  int32_t rot_dim;
+  int32_t style;
+  int32_t norm_dim;
+  float eps;
+  const float *inv_freq;
+  const void *q_gamma;
+  const void *k_gamma;
+} skv_rotary;
+
+/*
+ * The tokens of one call.  q, k and v are rows of n_q_heads * d_qk, n_kv_heads * d_qk and
+ * n_kv_heads * d_v entries (the heads packed), q_stride / k_stride / v_stride elements
+ * apart from token to token: column ranges of one fused projection output are fine.
+ * Base pointers are 16-byte aligned and strides are multiples of 16 bytes.
+ *   q           NULL: the call has no queries.
+ *   positions   device int32 [n_tokens]; a negative one marks a padding token, of which
+ *               nothing is read or written.  NULL: token i ends its request's history,
+ *               position seq_lens[request] - 1 (a history of length 0: a padding token).
+ *   requests    device int32 [n_tokens]: the request (slot-table row) of each token, a
+ *               negative one again padding.  NULL: token i is request i's.
+ * A position outside [0, max_len) sets SKV_DEV_BAD_LENGTH and a request past the batch
+ * SKV_DEV_BAD_INDEX; such tokens are skipped like padding.
+ */
+typedef struct skv_tokens {
+  int32_t n_tokens;
+  int32_t reserved;               /* 0 */
+  const void *q;
+  const void *k;
+  const void *v;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  const int32_t *positions;
+  const int32_t *requests;
+} skv_tokens;
+
+/*
+ * Norm and rotation alone: q_out [n_tokens, n_q_heads, d_qk] and k_out [n_tokens,
+ * n_kv_heads, d_qk], packed -- or q_out == tokens->q and k_out == tokens->k, in place at
+ * their strides; no other overlap.  tokens->v is ignored; either side may be NULL with
+ * its output.  Of p, batch, the head counts, d_qk, dtype, max_len and (positions NULL)
+ * seq_lens are used.  Without positions, requests NULL needs n_tokens <= batch.
+ */
+skv_status skv_qk_norm_rope(const skv_problem *p, const skv_rotary *rotary, const skv_tokens *tokens, void *q_out,
+                            void *k_out, int32_t *dev_status, void *stream);
+
+/*
+ * Append: for every token, its K rows (normed and rotated) and its V rows (as they are)
+ * of every KV head go to the pool row that the slot table names for (request, position),
+ * in the GPU pool or the pinned host pool; its query rows, where tokens->q is given, are
+ * normed and rotated into q_out [n_tokens, n_q_heads, d_qk] (or in place).  A table entry
+ * outside its pool sets SKV_DEV_BAD_SLOT and that token's K/V rows are not written.  Rows
+ * that no token names are left as they are.  The latent layout (pool->gpu_v == NULL) takes
+ * no V (tokens->v is ignored).  Both table forms (table_heads 0 and 1), block sizes of any
+ * length.  The pools are written (they must be writable, and read by no other work
+ * meanwhile); two tokens of one call must not name the same pool row.  requests NULL
+ * needs n_tokens <= batch.  n_tokens 0 enqueues nothing.
+ */
+skv_status skv_append_kv(const skv_problem *p, const skv_rotary *rotary, const skv_tokens *tokens,
+                         const skv_kv_pool *pool, void *q_out, int32_t *dev_status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,14 +18,18 @@ from .binding import (  # noqa: F401
     SKV_DTYPE_F32,
     SKV_INDEX_CONTIG,
     SKV_INDEX_PAGED,
+    SKV_ROPE_HALF,
+    SKV_ROPE_PAIR,
     IndexSrc,
     Pool,
     Paris,
     Prefetch,
     SlotCache,
     Problem,
+    Rotary,
     SkvError,
     lib,
+    skv_append_kv,
     skv_block_decode_step,
     skv_block_select,
     skv_block_summaries,
@@ -43,12 +47,13 @@ from .binding import (  # noqa: F401
     skv_gather,
     skv_check_wait_timeout,
     skv_launch_count,
+    skv_qk_norm_rope,
     skv_score,
     skv_sparse_attn,
     skv_status_string,
     skv_topk,
     skv_workspace_size,
 )
-from .step import BlockStep, DecodeStep, ParisStep  # noqa: F401
+from .step import BlockStep, DecodeStep, ParisStep, TokenStep  # noqa: F401
 
 lib()  # load now: a missing library is an import error, never a silent fallback

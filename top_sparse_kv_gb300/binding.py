@@ -28,6 +28,7 @@ SKV_AGG_MEAN = 0
 SKV_AGG_MAX = 1
 SKV_AGG_HEAD = 2  # every query head selects its own top-k
 SKV_INDEX_PAGED, SKV_INDEX_CONTIG = 0, 1
+SKV_ROPE_HALF, SKV_ROPE_PAIR = 0, 1
 
 
 class SkvError(RuntimeError):
@@ -67,6 +68,19 @@ class CParisIndex(ctypes.Structure):
     _fields_ = [("cent", ctypes.c_void_p), ("rec", ctypes.c_void_p), ("hist", ctypes.c_void_p)]
 
 
+class CRotary(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rot_start", "rot_dim", "style", "norm_dim")] + [
+        ("eps", ctypes.c_float), ("inv_freq", ctypes.c_void_p), ("q_gamma", ctypes.c_void_p),
+        ("k_gamma", ctypes.c_void_p)]
+
+
+class CTokens(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int32), ("reserved", ctypes.c_int32), ("q", ctypes.c_void_p),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("positions", ctypes.c_void_p),
+                ("requests", ctypes.c_void_p)]
+
+
 class CPrefetch(ctypes.Structure):
     _fields_ = [("tau_ema", ctypes.c_void_p), ("epoch", ctypes.c_void_p), ("map", ctypes.c_void_p),
                 ("staging", ctypes.c_void_p), ("count", ctypes.c_void_p), ("stats", ctypes.c_void_p),
@@ -103,6 +117,8 @@ def _load():
                              ctypes.POINTER(CPool), VP, VP, SZ, VP, VP],
         "skv_paris_decode_step": [P, ctypes.POINTER(CParis), VP, VP, ctypes.POINTER(CIndex),
                                   ctypes.POINTER(CParisIndex), ctypes.POINTER(CPool), VP, VP, VP, VP, SZ, VP, VP],
+        "skv_qk_norm_rope": [P, ctypes.POINTER(CRotary), ctypes.POINTER(CTokens), VP, VP, VP, VP],
+        "skv_append_kv": [P, ctypes.POINTER(CRotary), ctypes.POINTER(CTokens), ctypes.POINTER(CPool), VP, VP, VP],
         "skv_block_workspace_size": [P, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t),
                                      ctypes.POINTER(ctypes.c_int32)],
         "skv_block_summaries": [P, ctypes.POINTER(CPool), VP, VP, VP],
@@ -468,6 +484,103 @@ def skv_paris_decode_step(p: Problem, paris: Paris, q, q_score, index: IndexSrc,
         ctypes.byref(cp), ctypes.byref(cpr), _ptr(q), _ptr(q_score), ctypes.byref(ci), ctypes.byref(cix),
         ctypes.byref(cpool), _ptr(idx), _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(),
         _ptr(dev_status), _stream(stream)))
+
+
+@dataclass
+class Rotary:
+    """Norm and rotation of a model's queries and keys; see skv_rotary in include/skv.h."""
+
+    inv_freq: Optional[torch.Tensor]        # device float32 [rot_dim / 2]; None with rot_dim 0
+    rot_dim: int = 0
+    rot_start: int = 0
+    style: int = SKV_ROPE_HALF
+    norm_dim: int = 0                       # 0: the whole row
+    eps: float = 1e-6
+    q_gamma: Optional[torch.Tensor] = None  # device [norm_dim] of the element type; None: not normed
+    k_gamma: Optional[torch.Tensor] = None
+
+    def check(self, p: Problem) -> None:
+        """The tensors' types and sizes, which the C side cannot see."""
+        if self.rot_dim and (self.inv_freq is None or self.inv_freq.dtype != torch.float32
+                             or self.inv_freq.numel() != self.rot_dim // 2 or not self.inv_freq.is_contiguous()):
+            raise ValueError("inv_freq: contiguous float32 [rot_dim / 2]")
+        for g in (self.q_gamma, self.k_gamma):
+            if g is not None and (g.dtype != element_type(p) or g.numel() != (self.norm_dim or p.d_qk)
+                                  or not g.is_contiguous()):
+                raise ValueError("gamma: contiguous [norm_dim] of the element type")
+
+    def c(self) -> CRotary:
+        return CRotary(self.rot_start, self.rot_dim, self.style, self.norm_dim, float(self.eps),
+                       None if self.inv_freq is None else self.inv_freq.data_ptr(),
+                       None if self.q_gamma is None else self.q_gamma.data_ptr(),
+                       None if self.k_gamma is None else self.k_gamma.data_ptr())
+
+
+def element_type(p: Problem) -> torch.dtype:
+    return torch.float32 if p.dtype == SKV_DTYPE_F32 else torch.bfloat16
+
+
+def _rows(name: str, t: Optional[torch.Tensor], n: int, heads: int, d: int, dtype: torch.dtype):
+    """(pointer, token stride) of [n, heads, d] rows whose heads are packed."""
+    if t is None:
+        return None, 0
+    if t.dtype != dtype or t.dim() != 3 or t.shape[0] != n or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{name}: {dtype} [{n}, {heads}, {d}] expected, got {t.dtype} {tuple(t.shape)}")
+    st = t.stride()
+    if (st[2] != 1 and d > 1) or (st[1] != d and heads > 1):
+        raise ValueError(f"{name}: a token's heads must be packed")
+    return t.data_ptr(), st[0]
+
+
+def _ids(name: str, t: Optional[torch.Tensor], n: int):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous int32 [{n}] expected")
+    return t.data_ptr()
+
+
+def c_tokens(p: Problem, q, k, v, positions, requests) -> CTokens:
+    """skv_tokens of [n, heads, d] tensors (column ranges of a fused projection included)."""
+    first = k if k is not None else q
+    if first is None:
+        raise ValueError("q or k is needed")
+    n, dtype = first.shape[0], element_type(p)
+    qp, qs = _rows("q", q, n, p.n_q_heads, p.d_qk, dtype)
+    kp, ks = _rows("k", k, n, p.n_kv_heads, p.d_qk, dtype)
+    vp, vs = _rows("v", v, n, p.n_kv_heads, p.d_v, dtype)
+    return CTokens(n, 0, qp, kp, vp, qs, ks, vs, _ids("positions", positions, n), _ids("requests", requests, n))
+
+
+def _out_rows(name: str, out, src, heads: int, d: int, dtype: torch.dtype):
+    """Pointer of an output: packed rows, or the input itself (in place at its stride)."""
+    if out is None:
+        return None
+    _, stride = _rows(name, out, src.shape[0], heads, d, dtype)
+    if out.data_ptr() == src.data_ptr() and stride == src.stride(0):
+        return out.data_ptr()
+    if stride != heads * d and src.shape[0] > 1:
+        raise ValueError(f"{name}: packed rows, or the input itself")
+    return out.data_ptr()
+
+
+def skv_qk_norm_rope(p: Problem, rotary: Rotary, q, k, q_out, k_out, positions=None, requests=None, dev_status=None,
+                     stream=None):
+    rotary.check(p)
+    cp, cr, ct = p.c(), rotary.c(), c_tokens(p, q, k, None, positions, requests)
+    qo = _out_rows("q_out", q_out, q, p.n_q_heads, p.d_qk, element_type(p))
+    ko = _out_rows("k_out", k_out, k, p.n_kv_heads, p.d_qk, element_type(p))
+    _check("skv_qk_norm_rope", lib().skv_qk_norm_rope(ctypes.byref(cp), ctypes.byref(cr), ctypes.byref(ct), qo, ko,
+                                                      _ptr(dev_status), _stream(stream)))
+
+
+def skv_append_kv(p: Problem, rotary: Rotary, q, k, v, pool: Pool, q_out, positions=None, requests=None,
+                  dev_status=None, stream=None):
+    rotary.check(p)
+    cp, cr, ct, cpool = p.c(), rotary.c(), c_tokens(p, q, k, v, positions, requests), pool.c()
+    qo = _out_rows("q_out", q_out, q, p.n_q_heads, p.d_qk, element_type(p))
+    _check("skv_append_kv", lib().skv_append_kv(ctypes.byref(cp), ctypes.byref(cr), ctypes.byref(ct),
+                                                ctypes.byref(cpool), qo, _ptr(dev_status), _stream(stream)))
 
 
 def skv_status_string(status: int) -> str:

@@ -689,6 +689,62 @@ skv_status skv_paris_decode_step(const skv_problem* p, const skv_paris* paris, c
   return launch_attn(*p, q, view(pool), idx, out, lse, ws, dev_status, st, false);
 }
 
+// ---------------------------------------------------------------- new tokens
+
+// strides and pointers of one side's rows: `row` entries a token
+static skv_status check_rows(const void* ptr, int64_t stride, long long row, int elem, int32_t n_tokens) {
+  if (!aligned16(ptr)) return SKV_ERR_INVALID_ARGUMENT;
+  if (n_tokens > 1 && stride < row) return SKV_ERR_INVALID_ARGUMENT;
+  if (stride < 0 || stride > (1LL << 40) || (stride * elem) % 16) return SKV_ERR_INVALID_ARGUMENT;
+  return SKV_OK;
+}
+
+static skv_status check_tokens(const skv_problem* p, const skv_rotary* r, const skv_tokens* t, const void* q_out) {
+  SKV_TRY(check_problem(p));
+  if (!r || !t || t->n_tokens < 0 || t->reserved != 0) return SKV_ERR_INVALID_ARGUMENT;
+  if (r->style != SKV_ROPE_HALF && r->style != SKV_ROPE_PAIR) return SKV_ERR_INVALID_ARGUMENT;
+  if (r->rot_start < 0 || r->rot_dim < 0 || r->norm_dim < 0 || !(r->eps >= 0.f)) return SKV_ERR_INVALID_ARGUMENT;
+  if ((long long)r->rot_start + r->rot_dim > p->d_qk || r->norm_dim > p->d_qk) return SKV_ERR_INVALID_ARGUMENT;
+  if (r->rot_dim > 0 && (!r->inv_freq || ((uintptr_t)r->inv_freq & 3u))) return SKV_ERR_INVALID_ARGUMENT;
+  if (!aligned16(r->q_gamma) || !aligned16(r->k_gamma)) return SKV_ERR_INVALID_ARGUMENT;
+  const int elem = p->dtype == SKV_DTYPE_F32 ? 4 : 2;
+  if ((t->q == nullptr) != (q_out == nullptr) || !aligned16(q_out)) return SKV_ERR_INVALID_ARGUMENT;
+  if (t->q) SKV_TRY(check_rows(t->q, t->q_stride, (long long)p->n_q_heads * p->d_qk, elem, t->n_tokens));
+  if (t->k) SKV_TRY(check_rows(t->k, t->k_stride, (long long)p->n_kv_heads * p->d_qk, elem, t->n_tokens));
+  // vectors of 8 entries lie wholly inside or outside every span
+  if (p->d_qk % 8 || p->d_qk > 1024 || r->rot_start % 8 || r->norm_dim % 8) return SKV_ERR_UNSUPPORTED;
+  if (r->rot_dim % (r->style == SKV_ROPE_HALF ? 16 : 8)) return SKV_ERR_UNSUPPORTED;
+  return SKV_OK;
+}
+
+skv_status skv_qk_norm_rope(const skv_problem* p, const skv_rotary* rotary, const skv_tokens* tokens, void* q_out,
+                            void* k_out, int32_t* dev_status, void* stream) {
+  SKV_TRY(check_tokens(p, rotary, tokens, q_out));
+  if ((tokens->k == nullptr) != (k_out == nullptr) || !aligned16(k_out)) return SKV_ERR_INVALID_ARGUMENT;
+  if (!tokens->q && !tokens->k) return SKV_ERR_INVALID_ARGUMENT;
+  if (!tokens->positions && !tokens->requests && tokens->n_tokens > p->batch) return SKV_ERR_INVALID_ARGUMENT;
+  if (tokens->n_tokens == 0) return SKV_OK;
+  return launch_token_rows(*p, *rotary, *tokens, PoolView{}, q_out, k_out, dev_status, (cudaStream_t)stream);
+}
+
+skv_status skv_append_kv(const skv_problem* p, const skv_rotary* rotary, const skv_tokens* tokens,
+                         const skv_kv_pool* pool, void* q_out, int32_t* dev_status, void* stream) {
+  SKV_TRY(check_tokens(p, rotary, tokens, q_out));
+  SKV_TRY(check_pool(*p, pool));
+  if (!tokens->k) return SKV_ERR_INVALID_ARGUMENT;
+  if (pool->gpu_v != nullptr) {
+    const int elem = p->dtype == SKV_DTYPE_F32 ? 4 : 2;
+    if (!tokens->v) return SKV_ERR_INVALID_ARGUMENT;
+    SKV_TRY(check_rows(tokens->v, tokens->v_stride, (long long)p->n_kv_heads * p->d_v, elem, tokens->n_tokens));
+    if (p->d_v % 8 || p->d_v > 1024) return SKV_ERR_UNSUPPORTED;
+  } else if (p->n_kv_heads != 1 || p->d_v > p->d_qk) {
+    return SKV_ERR_INVALID_ARGUMENT;  // the latent layout: one row a token
+  }
+  if (!tokens->requests && tokens->n_tokens > p->batch) return SKV_ERR_INVALID_ARGUMENT;
+  if (tokens->n_tokens == 0) return SKV_OK;
+  return launch_token_rows(*p, *rotary, *tokens, view(pool), q_out, nullptr, dev_status, (cudaStream_t)stream);
+}
+
 const char* skv_status_string(skv_status s) {
   switch (s) {
     case SKV_OK: return "ok";

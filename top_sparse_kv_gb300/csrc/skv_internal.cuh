@@ -501,6 +501,11 @@ skv_status launch_cache_update(const skv_problem& p, const PoolView& pool, const
                                unsigned long long* stats, const void* attn_ws, void* cws, int32_t* status,
                                cudaStream_t st);
 
+// new tokens: norm, rotation and the append to the pool (tokens.cu).  pool.table == nullptr:
+// no append, the keys go to k_out.
+skv_status launch_token_rows(const skv_problem& p, const skv_rotary& r, const skv_tokens& t, const PoolView& pool,
+                             void* q_out, void* k_out, int32_t* status, cudaStream_t st);
+
 // block selection from per-block key summaries (blocks.cu)
 int block_list_len(const skv_problem& p, int topk_blocks);
 size_t block_summary_bytes(const skv_problem& p);

@@ -7,6 +7,7 @@ single skv_decode_step call enqueued on the current stream.
 
 from __future__ import annotations
 
+import ctypes
 from typing import Optional
 
 import torch
@@ -183,3 +184,46 @@ class ParisStep:
                      "cand_score": ((rows, c_cap), torch.float32)}[name]
         n = int(torch.tensor(shape).prod().item()) * torch.tensor([], dtype=dt).element_size()
         return self.ws[self.offsets[k]: self.offsets[k] + n].view(dt).view(shape)
+
+
+class TokenStep:
+    """New tokens of a layer: `norm_rope()` norms and rotates queries and keys, `append()` also
+    writes keys and values to the pool.  The problem, the rotary parameters and the pool are
+    marshalled once, here; every call marshals only its tokens.  Status bits add up in `status`."""
+
+    def __init__(self, problem: B.Problem, rotary: B.Rotary, pool: Optional[B.Pool] = None):
+        rotary.check(problem)
+        self.p, self.rotary, self.pool = problem, rotary, pool
+        dev = problem.seq_lens.device
+        self.status = torch.zeros((1,), dtype=torch.int32, device=dev)
+        self._p, self._r = ctypes.byref(problem.c()), ctypes.byref(rotary.c())
+        self._pool = None if pool is None else ctypes.byref(pool.c())
+        self._st = ctypes.c_void_p(self.status.data_ptr())
+        self._dtype = B.element_type(problem)
+
+    def _out(self, name, out, src, heads):
+        if src is None:
+            return None, None
+        if out is None:
+            out = torch.empty((src.shape[0], heads, self.p.d_qk), dtype=src.dtype, device=src.device)
+        return out, B._out_rows(name, out, src, heads, self.p.d_qk, self._dtype)
+
+    def norm_rope(self, q, k, positions=None, requests=None, q_out=None, k_out=None, stream=None):
+        """(q_out, k_out): new tensors unless given; pass q and k themselves to work in place.
+        Padding tokens' rows are not written."""
+        ct = B.c_tokens(self.p, q, k, None, positions, requests)
+        q_out, qo = self._out("q_out", q_out, q, self.p.n_q_heads)
+        k_out, ko = self._out("k_out", k_out, k, self.p.n_kv_heads)
+        B._check("skv_qk_norm_rope", B.lib().skv_qk_norm_rope(self._p, self._r, ctypes.byref(ct), qo, ko, self._st,
+                                                              B._stream(stream)))
+        return q_out, k_out
+
+    def append(self, q, k, v, positions=None, requests=None, q_out=None, stream=None):
+        """Appends k and v to the pool; returns q_out (None without q)."""
+        if self._pool is None:
+            raise ValueError("append() needs a pool")
+        ct = B.c_tokens(self.p, q, k, v, positions, requests)
+        q_out, qo = self._out("q_out", q_out, q, self.p.n_q_heads)
+        B._check("skv_append_kv", B.lib().skv_append_kv(self._p, self._r, ctypes.byref(ct), self._pool, qo, self._st,
+                                                        B._stream(stream)))
+        return q_out
