@@ -662,6 +662,40 @@ skv_status skv_qk_norm_rope(const skv_problem *p, const skv_rotary *rotary, cons
 skv_status skv_append_kv(const skv_problem *p, const skv_rotary *rotary, const skv_tokens *tokens,
                          const skv_kv_pool *pool, void *q_out, int32_t *dev_status, void *stream);
 
+/* ------------------------------------------------------------------------------------
+ * Attention of a batch that shares a prefix: every request attends its whole history,
+ * and the keys of the shared positions [0, len) are read once for all requests.
+ *   z_t = sm_scale * <q[b][j], K_t>,  out[b][j] = sum_t softmax(z)_t V_t,
+ *   lse[b][j] = log sum_t exp(z_t)   over every t < L_b = seq_lens[b];
+ * position t < len resolves through prefix->table[t / block_size], t >= len through the
+ * request's own slot-table row (whose entries below len / block_size are not read; a
+ * block that len ends inside may be shared or the request's own copy -- each side reads
+ * the table it is named by).  Entries of either sign: GPU or pinned host blocks.
+ *   table  device int32 [ceil(len / block_size)]; may be a row of the slot table; NULL
+ *          with len 0 (every request then attends through its own row alone).
+ *   len    in [0, max_len].
+ * A request is of length 0 (an unused row of the batch: out 0, lse -inf) or holds the
+ * whole prefix (L_b >= len); a length between sets SKV_DEV_BAD_LENGTH and leaves out 0
+ * and lse -inf.  An entry outside its pool sets SKV_DEV_BAD_SLOT and its rows get zero
+ * weight.  What lies in a pool past a history's end or the prefix's end is never used.
+ * Of p, batch, the head counts, d_qk, d_v, max_len, block_size, dtype, sm_scale and
+ * seq_lens are used.  bf16, d_qk = d_v = 128, K and V pools with one table row a request
+ * (table_heads 0), at most 128 query heads per KV head, else SKV_ERR_UNSUPPORTED.
+ * out [batch, n_q_heads, 128], lse fp32 [batch, n_q_heads] or NULL.  Deterministic: the
+ * same inputs give the same bits.
+ * ------------------------------------------------------------------------------------ */
+typedef struct skv_prefix {
+  const int32_t *table;
+  int32_t len;
+  int32_t reserved;               /* 0 */
+} skv_prefix;
+
+/* Bytes of workspace skv_prefix_attn needs for this problem and prefix length. */
+skv_status skv_prefix_workspace_size(const skv_problem *p, int32_t prefix_len, size_t *bytes);
+
+skv_status skv_prefix_attn(const skv_problem *p, const void *q, const skv_kv_pool *pool, const skv_prefix *prefix,
+                           void *out, float *lse, void *ws, size_t ws_bytes, int32_t *dev_status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -24,6 +24,7 @@ from .binding import (  # noqa: F401
     Pool,
     Paris,
     Prefetch,
+    Prefix,
     SlotCache,
     Problem,
     Rotary,
@@ -47,6 +48,8 @@ from .binding import (  # noqa: F401
     skv_gather,
     skv_check_wait_timeout,
     skv_launch_count,
+    skv_prefix_attn,
+    skv_prefix_workspace_size,
     skv_qk_norm_rope,
     skv_score,
     skv_sparse_attn,
@@ -54,6 +57,6 @@ from .binding import (  # noqa: F401
     skv_topk,
     skv_workspace_size,
 )
-from .step import BlockStep, DecodeStep, ParisStep, TokenStep  # noqa: F401
+from .step import BlockStep, DecodeStep, ParisStep, PrefixStep, TokenStep  # noqa: F401
 
 lib()  # load now: a missing library is an import error, never a silent fallback

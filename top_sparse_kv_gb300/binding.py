@@ -81,6 +81,10 @@ class CTokens(ctypes.Structure):
                 ("requests", ctypes.c_void_p)]
 
 
+class CPrefix(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("len", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class CPrefetch(ctypes.Structure):
     _fields_ = [("tau_ema", ctypes.c_void_p), ("epoch", ctypes.c_void_p), ("map", ctypes.c_void_p),
                 ("staging", ctypes.c_void_p), ("count", ctypes.c_void_p), ("stats", ctypes.c_void_p),
@@ -119,6 +123,8 @@ def _load():
                                   ctypes.POINTER(CParisIndex), ctypes.POINTER(CPool), VP, VP, VP, VP, SZ, VP, VP],
         "skv_qk_norm_rope": [P, ctypes.POINTER(CRotary), ctypes.POINTER(CTokens), VP, VP, VP, VP],
         "skv_append_kv": [P, ctypes.POINTER(CRotary), ctypes.POINTER(CTokens), ctypes.POINTER(CPool), VP, VP, VP],
+        "skv_prefix_workspace_size": [P, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)],
+        "skv_prefix_attn": [P, VP, ctypes.POINTER(CPool), ctypes.POINTER(CPrefix), VP, VP, VP, SZ, VP, VP],
         "skv_block_workspace_size": [P, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t),
                                      ctypes.POINTER(ctypes.c_int32)],
         "skv_block_summaries": [P, ctypes.POINTER(CPool), VP, VP, VP],
@@ -581,6 +587,39 @@ def skv_append_kv(p: Problem, rotary: Rotary, q, k, v, pool: Pool, q_out, positi
     qo = _out_rows("q_out", q_out, q, p.n_q_heads, p.d_qk, element_type(p))
     _check("skv_append_kv", lib().skv_append_kv(ctypes.byref(cp), ctypes.byref(cr), ctypes.byref(ct),
                                                 ctypes.byref(cpool), qo, _ptr(dev_status), _stream(stream)))
+
+
+@dataclass
+class Prefix:
+    """The positions a batch shares; see skv_prefix in include/skv.h."""
+
+    table: Optional[torch.Tensor]  # device int32 [ceil(len / block_size)]; None with len 0
+    len: int
+
+    def check(self, p: Problem) -> None:
+        need = (self.len + p.block_size - 1) // p.block_size
+        if need and (self.table is None or self.table.dtype != torch.int32 or self.table.numel() < need
+                     or not self.table.is_contiguous()):
+            raise ValueError(f"prefix table: contiguous int32 [{need}] expected")
+
+    def c(self) -> CPrefix:
+        return CPrefix(None if self.table is None else self.table.data_ptr(), int(self.len), 0)
+
+
+def skv_prefix_workspace_size(p: Problem, prefix_len: int) -> int:
+    n = ctypes.c_size_t(0)
+    cp = p.c()
+    _check("skv_prefix_workspace_size", lib().skv_prefix_workspace_size(ctypes.byref(cp), int(prefix_len),
+                                                                        ctypes.byref(n)))
+    return n.value
+
+
+def skv_prefix_attn(p: Problem, q, pool: Pool, prefix: Prefix, out, lse, ws, dev_status=None, stream=None):
+    prefix.check(p)
+    cp, cpool, cx = p.c(), pool.c(), prefix.c()
+    _check("skv_prefix_attn", lib().skv_prefix_attn(
+        ctypes.byref(cp), _ptr(q), ctypes.byref(cpool), ctypes.byref(cx), _ptr(out), _ptr(lse), _ptr(ws),
+        ws.numel() * ws.element_size(), _ptr(dev_status), _stream(stream)))
 
 
 def skv_status_string(status: int) -> str:

@@ -745,6 +745,42 @@ skv_status skv_append_kv(const skv_problem* p, const skv_rotary* rotary, const s
   return launch_token_rows(*p, *rotary, *tokens, view(pool), q_out, nullptr, dev_status, (cudaStream_t)stream);
 }
 
+// ---------------------------------------------------------------- shared prefix
+
+static skv_status check_prefix_problem(const skv_problem* p, int32_t prefix_len) {
+  SKV_TRY(check_problem(p));
+  if (prefix_len < 0 || prefix_len > p->max_len) return SKV_ERR_INVALID_ARGUMENT;
+  if (p->dtype != SKV_DTYPE_BF16 || p->d_qk != 128 || p->d_v != 128) return SKV_ERR_UNSUPPORTED;
+  if (p->n_q_heads / p->n_kv_heads > 128) return SKV_ERR_UNSUPPORTED;
+  if (p->max_len > (1 << 30)) return SKV_ERR_UNSUPPORTED;  // tile positions stay in 32 bits
+  // merge blocks index grid.x
+  if (((long long)p->batch * (p->n_q_heads / p->n_kv_heads) + 31) / 32 * p->n_kv_heads > 0x7fffffffLL)
+    return SKV_ERR_UNSUPPORTED;
+  return SKV_OK;
+}
+
+skv_status skv_prefix_workspace_size(const skv_problem* p, int32_t prefix_len, size_t* bytes) {
+  SKV_TRY(check_prefix_problem(p, prefix_len));
+  if (!bytes) return SKV_ERR_INVALID_ARGUMENT;
+  *bytes = prefix_workspace_bytes(*p, prefix_len);
+  return SKV_OK;
+}
+
+skv_status skv_prefix_attn(const skv_problem* p, const void* q, const skv_kv_pool* pool, const skv_prefix* prefix,
+                           void* out, float* lse, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
+  SKV_TRY(check_problem(p));
+  SKV_TRY(check_pool(*p, pool));
+  if (!prefix || prefix->reserved != 0) return SKV_ERR_INVALID_ARGUMENT;
+  if (prefix->len > 0 && (!prefix->table || ((uintptr_t)prefix->table & 3u))) return SKV_ERR_INVALID_ARGUMENT;
+  SKV_TRY(check_prefix_problem(p, prefix->len));
+  SKV_TRY(no_head_table(pool));
+  if (!pool->gpu_v) return SKV_ERR_UNSUPPORTED;  // latent rows
+  if (!q || !out || !aligned16(q) || !aligned16(out)) return SKV_ERR_INVALID_ARGUMENT;
+  if (ws_bytes < prefix_workspace_bytes(*p, prefix->len)) return SKV_ERR_WORKSPACE_TOO_SMALL;
+  if (!ws || !aligned16(ws)) return SKV_ERR_INVALID_ARGUMENT;
+  return launch_prefix_attn(*p, q, view(pool), *prefix, out, lse, ws, dev_status, (cudaStream_t)stream);
+}
+
 const char* skv_status_string(skv_status s) {
   switch (s) {
     case SKV_OK: return "ok";

@@ -1,0 +1,791 @@
+// Attention of a batch over a shared prefix and every request's own tail.
+//
+//   out[b][j] = sum_{t < L_b} softmax(z)_t V_t,  z_t = sm_scale <q[b][j], K_t>
+//
+// The keys of the shared positions [0, P) are the same for every request, so the queries
+// of all requests of a KV head -- row b * G + g of B * G rows -- meet them in matrix
+// products on the tcgen05 tensor cores, and the prefix crosses HBM once; a tail [P, L_b)
+// meets the G rows of its own request the same way.  Both are cut into tiles of 128 keys.
+//
+// prefix_attn_kernel, one persistent CTA an SM, 16 warps in four roles:
+//   warps 0-3, 4-7   softmax of slot 0 / slot 1 (a thread a query row)
+//   warps 8-11       gather: every K and V row through the table (GPU pool, or pinned host
+//                    pool over UVA), 16-byte cp.async into a ring of 32 KB stages in the
+//                    128-byte-swizzled layout that the MMA reads
+//   warp 12          one thread issues every MMA
+// A *step* is one (128 query rows, 128 keys) tile: S = Q K^T (M128 N128, fp32 in TMEM),
+// P = 2^(z - m) in bf16 over S's own columns, O += P V (A from TMEM, V read MN-major).
+// Steps alternate between two slots of TMEM (S 128 + O 128 columns each), so that one
+// slot's MMAs run under the other's softmax: with more than 128 rows the two slots hold
+// two row tiles and share the keys; with up to 128 rows they take alternate key tiles.
+// The running maximum is renewed only when it grows by more than 2^8 (P stays below 2^8
+// relative to it, l and O in fp32 lose nothing), so O is rarely rescaled.
+//
+// Work is cut by key tiles: the CTAs form gangs (one member per pair of row tiles, so
+// that members read the same keys at the same time) and gang c takes the tiles
+// [c T / C, (c + 1) T / C) of all heads' prefixes; then CTA c takes its share of all
+// tails' tiles.  Each cut leaves every CTA that takes part a tile at least, so the segments
+// of a unit -- runs of tiles of one head's prefix, or of one tail -- are those of
+// consecutive CTAs.  A segment's O, m and l go to the workspace, at an index that grows
+// with both the CTA and the unit, so no two segments share one and no atomics are needed.
+// prefix_merge_kernel joins a row's partials by log-sum-exp, in a fixed order.
+#include "attn_common.cuh"
+#include "tcgen05.cuh"
+
+namespace skv {
+namespace {
+
+namespace px {
+constexpr int kCtas = 152;             // one CTA an SM of a GB300 (a function of the problem alone: sizes the workspace)
+constexpr int kThreads = 512;
+constexpr int kTile = 128;             // keys a tile, query rows a tile
+constexpr int kHalfB = kTile * 128;    // 128 rows x 64 dims, 16 KB
+constexpr int kStageB = 2 * kHalfB;    // a K, V or Q tile: 32 KB
+constexpr int kRing = 5;               // K / V stages
+constexpr int kQBufs = 2;
+constexpr int kMasks = 8;              // key masks of the last tiles
+constexpr int kSmem = (kQBufs + kRing) * kStageB + 1024;
+constexpr int kMaxGang = 4;            // pairs of row tiles that read the same keys together
+constexpr float kGrow = 8.f;           // log2 growth of a row's maximum that renews it
+constexpr uint32_t kTmemCols = 512;    // S0 S1 O0 O1, 128 columns each
+
+// How the row tiles and the CTAs are arranged (host and device alike)
+struct Plan {
+  int rows, tiles, pairs, groups, gang, gangs;  // query rows, row tiles, pairs of them, groups of pairs, pairs a group
+  int ntp;                                       // key tiles of the prefix
+  int rp;                                        // rows of a prefix partial
+};
+__host__ __device__ inline Plan plan_of(int B, int H, int G, int P) {
+  Plan pl;
+  pl.rows = B * G;
+  pl.tiles = (pl.rows + kTile - 1) / kTile;
+  pl.pairs = (pl.tiles + 1) / 2;
+  pl.groups = (pl.pairs + kMaxGang - 1) / kMaxGang;
+  pl.gang = (pl.pairs + pl.groups - 1) / pl.groups;
+  pl.ntp = (P + kTile - 1) / kTile;
+  pl.gangs = kCtas / pl.gang;
+  const long long tp = (long long)H * pl.groups * pl.ntp;
+  if (tp < pl.gangs) pl.gangs = (int)tp;  // a gang has a tile at least: a unit's partials are consecutive
+  pl.rp = pl.rows < kTile ? pl.rows : kTile;
+  return pl;
+}
+
+struct Args {
+  const unsigned char* q;
+  PoolView pool;
+  const int32_t *ptable, *seq_lens;
+  int B, H, Hq, G, P, max_len, bs;
+  float scale_log2;
+  Plan pl;
+  float *po, *pml;     // prefix partials: [(gang + unit) * members + member][2][...]
+  float *so, *sml;     // tail partials: [cta + unit][2][...]
+  int *first, *last;   // [H * B]: the CTAs of a tail's first and last segment
+  void* out;
+  float* lse;
+  int32_t* status;
+};
+
+// the tail's key tiles of request b (none for an empty request or one that ends inside the prefix)
+__device__ __forceinline__ int tail_len(const Args& a, int b) {
+  int L = a.seq_lens[b];
+  L = L > a.max_len ? a.max_len : L;
+  return L > a.P ? L - a.P : 0;
+}
+
+struct Seg {
+  int tail, h, b;      // a tail's segment (of request b), or the prefix's
+  int row0, n0, n1;    // first query row; live rows of the two row tiles (n1 = 0: one tile)
+  int t0, n, hi;       // first key position, key tiles, end of the valid positions
+  bool begins, ends;   // the tail's first / last segment
+  long long part;      // the partial's index
+};
+
+// A CTA's segments in order, the same sequence for every role.
+struct Walk {
+  long long p0, p1;          // prefix tiles left: flattened (head, group, tile)
+  long long srem;            // tail tiles left
+  int scta;                  // the CTA's place among those with tail tiles
+  int sh, sb, stile;         // the next tail tile
+  __device__ bool next(const Args& a, Seg& s) {
+    const Plan& pl = a.pl;
+    const int c = blockIdx.x / pl.gang, member = blockIdx.x - c * pl.gang;
+    while (p0 < p1) {
+      const int up = (int)(p0 / pl.ntp), tile = (int)(p0 - (long long)up * pl.ntp);
+      const long long left = p1 - p0;
+      const int n = left < pl.ntp - tile ? (int)left : pl.ntp - tile;
+      p0 += n;
+      const int h = up / pl.groups, pair = (up - h * pl.groups) * pl.gang + member;
+      if (pair >= pl.pairs) continue;  // the last group may be short of pairs
+      s.tail = 0;
+      s.h = h;
+      s.b = 0;
+      s.row0 = pair * 2 * kTile;
+      const int r = pl.rows - s.row0;
+      s.n0 = r < kTile ? r : kTile;
+      s.n1 = r <= kTile ? 0 : (r - kTile < kTile ? r - kTile : kTile);
+      s.t0 = tile * kTile;
+      s.n = n;
+      s.hi = a.P;
+      s.begins = s.ends = false;
+      s.part = (long long)(c + up) * pl.gang + member;
+      return true;
+    }
+    while (srem > 0) {
+      const int len = tail_len(a, sb), nt = (len + kTile - 1) / kTile;
+      if (stile >= nt) {
+        stile = 0;
+        if (++sb == a.B) {
+          sb = 0;
+          ++sh;
+        }
+        continue;
+      }
+      const int n = srem < nt - stile ? (int)srem : nt - stile;
+      s.tail = 1;
+      s.h = sh;
+      s.b = sb;
+      s.row0 = sb * a.G;
+      s.n0 = a.G;
+      s.n1 = 0;
+      s.t0 = a.P + stile * kTile;
+      s.n = n;
+      s.hi = a.P + len;
+      s.begins = stile == 0;
+      s.ends = stile + n == nt;
+      s.part = (long long)scta + (long long)sh * a.B + sb;
+      stile += n;
+      srem -= n;
+      return true;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+struct Bars {
+  uint64_t full[kRing], empty[kRing], qfull[kQBufs], qempty[kQBufs], mask[kMasks], s[2], p[2], o[2], drain;
+};
+
+// ---------------------------------------------------------------------------- gather warps
+struct Gather {
+  const Args& a;
+  Bars& bar;
+  uint32_t base;
+  unsigned char* gbase;
+  volatile int* abort;
+  uint64_t* pend[2];  // barriers of the copy groups that are not announced yet
+  int w, lane;
+  bool ok;
+
+  __device__ void announce(uint64_t* b) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b);
+  }
+  // a new copy group; the one two back has landed
+  __device__ void commit(uint64_t* b) {
+    cp_async_commit();
+    cp_async_wait<2>();
+    if (pend[0]) announce(pend[0]);
+    pend[0] = pend[1];
+    pend[1] = b;
+  }
+  __device__ void flush() {
+    cp_async_wait<0>();
+    if (pend[0]) announce(pend[0]);
+    if (pend[1]) announce(pend[1]);
+    pend[0] = pend[1] = nullptr;
+  }
+  // Wait for a free buffer.  Everything in flight is announced first when it is not free
+  // yet: what frees it may need those tiles.
+  __device__ void wait_free(uint64_t* b, uint32_t parity) {
+    if (!ok) return;
+    bool free = mbar_try_wait(b, parity);
+    if (__any_sync(0xffffffffu, !free)) {
+      flush();
+      ok = wait_or_abort(b, parity, abort, a.status);
+      ok = !__any_sync(0xffffffffu, !ok);
+    }
+  }
+};
+
+// Row references of a tile: lane l holds rows 4 l + (two of 0..3, by the warp's parity).
+// A reference is the row's index in its pool, bit 62 for the host pool, -1 for none.
+__device__ __forceinline__ void load_entries(const Args& a, const int32_t* table, int t, int hi, int lane, int* e) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int tt = t + 4 * lane + j;
+    e[j] = tt < hi ? table[tt / a.bs] : 0;
+  }
+}
+__device__ __forceinline__ long long row_ref(const Args& a, int h, int e, int t, int hi) {
+  if (t >= hi) return -1;
+  if (e >= 0) return e < a.pool.n_gpu ? ((long long)e * a.H + h) * a.bs + t % a.bs : -1;
+  const long long hb = -(long long)e - 1;
+  if (a.pool.host_k == nullptr || hb >= a.pool.n_host) return -1;
+  return tc::kHostBit | ((hb * a.H + h) * a.bs + t % a.bs);
+}
+
+__device__ __forceinline__ void gather_role(const Args& a, Walk walk, Bars& bar, uint32_t base, unsigned char* gbase, uint4* masks,
+                            volatile int* abort) {
+  const int w = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31;
+  Gather g{a, bar, base, gbase, abort, {nullptr, nullptr}, w, lane, true};
+  const int c = lane & 15;  // the row's 16-byte chunk this thread copies
+  const int rlow = 2 * w + (lane >> 4);
+  const uint32_t dst0 = (uint32_t)((c >> 3) * kHalfB) + t5::sw128(rlow, c & 7);  // row rlow of each group of 8
+  Seg s;
+  int T = 0, nq = 0;
+  while (g.ok && walk.next(a, s)) {
+    if (s.tail && w == 0 && lane == 0) {
+      if (s.begins) a.first[s.h * a.B + s.b] = walk.scta;
+      if (s.ends) a.last[s.h * a.B + s.b] = walk.scta;
+    }
+    const int32_t* table = s.tail ? a.pool.table + (size_t)s.b * a.pool.stride : a.ptable;
+    int e[4];
+    load_entries(a, table, s.t0, s.hi, lane, e);
+    // query rows
+    for (int u = 0; u < (s.n1 > 0 ? 2 : 1); ++u, ++nq) {
+      const int buf = nq & 1;
+      g.wait_free(&bar.qempty[buf], (uint32_t)((nq >> 1) & 1) ^ 1u);
+      if (!g.ok) break;
+      const int live = u ? s.n1 : s.n0;
+      unsigned char* dst = gbase + buf * kStageB + dst0;
+      for (int pass = 0; pass < 16; ++pass) {
+        const int r = 8 * pass + rlow;
+        if (r < live) {
+          const int row = s.row0 + u * kTile + r, b = row / a.G, gg = row - b * a.G;
+          cp_async16(dst + pass * 1024, a.q + (((size_t)b * a.Hq + (size_t)s.h * a.G + gg) * kD + c * 8) * 2);
+        }
+      }
+      g.commit(&bar.qfull[buf]);
+    }
+    for (int i = 0; g.ok && i < s.n; ++i, ++T) {
+      const int t = s.t0 + i * kTile;
+      long long ref[2];
+      unsigned okm[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const long long r = row_ref(a, s.h, e[j], t + 4 * lane + j, s.hi);
+        if (j == 2 * (w & 1)) ref[0] = r;
+        if (j == 2 * (w & 1) + 1) ref[1] = r;
+        okm[j] = __ballot_sync(0xffffffffu, r >= 0);
+        if (w == 0 && r < 0 && t + 4 * lane + j < s.hi) flag(a.status, SKV_DEV_BAD_SLOT);
+      }
+      if (i + 1 < s.n) load_entries(a, table, t + kTile, s.hi, lane, e);
+#pragma unroll 1
+      for (int kv = 0; kv < 2 && g.ok; ++kv) {
+        const int seq = 2 * T + kv, st = seq % kRing;
+        g.wait_free(&bar.empty[st], (uint32_t)((seq / kRing) & 1) ^ 1u);
+        if (!g.ok) break;
+        if (kv == 0 && w == 0 && lane == 0) {
+          masks[T % kMasks] = make_uint4(okm[0], okm[1], okm[2], okm[3]);
+          mbar_arrive(&bar.mask[T % kMasks]);
+        }
+        const unsigned char* gp = (const unsigned char*)(kv ? a.pool.gpu_v : a.pool.gpu_k) + c * 16;
+        const unsigned char* hp = (const unsigned char*)(kv ? a.pool.host_v : a.pool.host_k) + c * 16;
+        unsigned char* dst = gbase + (kQBufs + st) * kStageB + dst0;
+#pragma unroll 8
+        for (int pass = 0; pass < 16; ++pass) {
+          const int from = 2 * pass + (w >> 1);
+          const long long ra = __shfl_sync(0xffffffffu, ref[0], from), rb = __shfl_sync(0xffffffffu, ref[1], from);
+          const long long r = lane < 16 ? ra : rb;
+          const unsigned char* src = (r & tc::kHostBit) ? hp : gp;
+          const bool live = r >= 0;
+          src = live ? src + (size_t)(r & tc::kRefRowMask) * tc::kRowBytes : gp - c * 16;
+          tc::cp_async16_zfill(dst + pass * 1024, src, live);
+        }
+        g.commit(&bar.full[st]);
+      }
+    }
+  }
+  g.flush();
+}
+
+// ---------------------------------------------------------------------------- MMA thread
+struct Step {
+  int T, slot, q;                                // key tile, TMEM slot, Q buffer sequence number
+  bool k_first, k_last, q_first, q_last;         // first / last use of the K stage (the V stage alike) and of the Q buffer
+  bool o_first, o_last;                          // first / last step of its slot in the segment
+};
+struct Steps {
+  Walk walk;
+  Seg s;
+  int i, sub, T, x, nq;
+  bool have;
+  __device__ bool next(const Args& a, Step& o) {
+    if (!have) {
+      if (!walk.next(a, s)) return false;
+      have = true;
+      i = sub = 0;
+    }
+    const bool two = s.n1 > 0;
+    o.T = T;
+    o.slot = x & 1;
+    o.q = nq + (two ? sub : 0);
+    o.k_first = sub == 0;
+    o.k_last = !two || sub == 1;
+    o.q_first = i == 0;
+    o.q_last = i == s.n - 1;
+    o.o_first = two ? i == 0 : i < 2;
+    o.o_last = two ? i == s.n - 1 : i >= s.n - 2;
+    ++x;
+    if (two && sub == 0) {
+      sub = 1;
+    } else {
+      sub = 0;
+      ++T;
+      if (++i == s.n) {
+        have = false;
+        nq += two ? 2 : 1;
+      }
+    }
+    return true;
+  }
+};
+
+__device__ __forceinline__ void mma_role(const Args& a, Walk walk, Bars& bar, uint32_t base, uint32_t tm, volatile int* abort) {
+  const uint32_t id_s = t5::idesc_bf16(128, 128, false), id_o = t5::idesc_bf16(128, 128, true);
+  Steps gen;
+  gen.walk = walk;
+  gen.T = gen.x = gen.nq = gen.i = gen.sub = 0;
+  gen.have = false;
+  Step pend[2];
+  bool live[2] = {false, false}, ok = true;
+  int np[2] = {0, 0};
+  auto wait = [&](uint64_t* b, uint32_t parity) {
+    if (ok) ok = wait_or_abort(b, parity, abort, a.status);
+  };
+  auto issue_s = [&](const Step& st) {
+    const int seq = 2 * st.T, ks = seq % kRing, qb = st.q & 1;
+    if (st.q_first) wait(&bar.qfull[qb], (uint32_t)(st.q >> 1) & 1u);
+    if (st.k_first) wait(&bar.full[ks], (uint32_t)(seq / kRing) & 1u);
+    if (!ok) return;
+    t5::fence_after();
+    const uint32_t qa = base + qb * kStageB, ka = base + (kQBufs + ks) * kStageB;
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {  // 16 of the 128 dims each
+      const uint32_t off = (uint32_t)(kk >> 2) * kHalfB + (kk & 3) * 32;
+      t5::mma(tm + st.slot * 128, t5::desc_sw128(qa + off, 16, 1024), t5::desc_sw128(ka + off, 16, 1024), id_s,
+              kk > 0 ? 1u : 0u);
+    }
+    t5::commit(&bar.s[st.slot]);
+    if (st.k_last) t5::commit(&bar.empty[ks]);
+    if (st.q_last) t5::commit(&bar.qempty[qb]);
+  };
+  auto issue_o = [&](const Step& st) {
+    const int seq = 2 * st.T + 1, vs = seq % kRing;
+    wait(&bar.p[st.slot], (uint32_t)(np[st.slot]++ & 1));
+    if (st.k_first) wait(&bar.full[vs], (uint32_t)(seq / kRing) & 1u);
+    if (!ok) return;
+    t5::fence_after();
+    const uint32_t va = base + (kQBufs + vs) * kStageB;
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)  // 16 of the 128 keys each
+      t5::mma_ts(tm + 256 + st.slot * 128, tm + st.slot * 128 + kk * 8, t5::desc_sw128(va + kk * 2048, kHalfB, 1024),
+                 id_o, (st.o_first && kk == 0) ? 0u : 1u);
+    if (st.k_last) t5::commit(&bar.empty[vs]);
+    if (st.o_last) t5::commit(&bar.o[st.slot]);
+  };
+  for (int u = 0; u < 2; ++u)
+    if (gen.next(a, pend[u])) {
+      live[u] = true;
+      issue_s(pend[u]);
+    }
+  for (int u = 0; ok && live[u]; u ^= 1) {
+    issue_o(pend[u]);
+    live[u] = ok && gen.next(a, pend[u]);
+    if (live[u]) issue_s(pend[u]);
+  }
+  // the operands in shared memory and TMEM outlive every MMA issued
+  t5::commit(&bar.drain);
+  mbar_wait_bounded(&bar.drain, 0u);
+}
+
+// ---------------------------------------------------------------------------- softmax warps
+__device__ __forceinline__ void softmax_role(const Args& a, Walk walk, Bars& bar, uint32_t tm, const uint4* masks,
+                             volatile int* abort) {
+  const int slot = threadIdx.x >> 7, wq = (threadIdx.x >> 5) & 3, row = threadIdx.x & 127;
+  const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+  const uint32_t ts = tm + lanes + slot * 128, to = tm + lanes + 256 + slot * 128;
+  Seg s;
+  int x = 0, T = 0, ns = 0, no = 0;
+  bool ok = true;
+  while (ok && walk.next(a, s)) {
+    const bool two = s.n1 > 0;
+    const int sub = slot ^ (x & 1);
+    const int mine = two ? s.n : (s.n + 1 - sub) / 2;
+    const int live_rows = two && sub ? s.n1 : s.n0;
+    const bool warp_live = wq * 32 < live_rows;
+    float m = -INFINITY, l = 0.f;
+    for (int j = 0; ok && j < mine; ++j, ++ns) {
+      const int tile = T + (two ? j : 2 * j + sub);
+      ok = wait_or_abort(&bar.mask[tile % kMasks], (uint32_t)(tile / kMasks) & 1u, abort, a.status);
+      ok = ok && wait_or_abort(&bar.s[slot], (uint32_t)ns & 1u, abort, a.status);
+      ok = !__any_sync(0xffffffffu, !ok);
+      if (!ok) break;
+      t5::fence_after();
+      if (warp_live) {
+        const uint4 mk = masks[tile % kMasks];
+        uint32_t v[128];
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) t5::ld32_async(ts + ch * 32, v + ch * 32);
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) t5::ld_wait32(v + ch * 32);
+        if ((mk.x & mk.y & mk.z & mk.w) != 0xffffffffu) {
+          const uint32_t mw[4] = {mk.x, mk.y, mk.z, mk.w};
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (!((mw[i & 3] >> (i >> 2)) & 1u)) v[i] = 0xff800000u;  // -inf
+        }
+        float mx[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) mx[u] = __uint_as_float(v[u]);
+#pragma unroll
+        for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(v[i]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+        if (j == 0) {
+          m = top;
+        } else if (__any_sync(0xffffffffu, row < live_rows && top > m + kGrow)) {
+          // O of this slot is complete: S was issued after the last P V and committed after it.
+          // A row's own maximum decides for it, so its bits do not depend on its neighbours.
+          const bool grow = top > m + kGrow;
+          const float f = grow ? ex2(m - top) : 1.f;
+          m = grow ? top : m;
+          l *= f;
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t o[32];
+            t5::ld32(to + ch * 32, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            t5::st32(to + ch * 32, o);
+          }
+        }
+        const float mb = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float p0 = ex2(fmaf(__uint_as_float(v[ch * 64 + 2 * i]), a.scale_log2, -mb));
+            const float p1 = ex2(fmaf(__uint_as_float(v[ch * 64 + 2 * i + 1]), a.scale_log2, -mb));
+            sum[(2 * i) & 3] += p0;
+            sum[(2 * i + 1) & 3] += p1;
+            pk[i] = tc::pack_bf16(p0, p1);
+          }
+          t5::st32(ts + ch * 32, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        t5::st_wait();
+      }
+      t5::fence_before();
+      mbar_arrive(&bar.p[slot]);
+    }
+    if (ok && mine > 0) {
+      ok = wait_or_abort(&bar.o[slot], (uint32_t)(no++) & 1u, abort, a.status);
+      ok = !__any_sync(0xffffffffu, !ok);
+      t5::fence_after();
+    }
+    // the segment's partial, head-fastest in groups of 4 dims: [dim / 4][row][4]
+    const int rp = s.tail ? a.G : a.pl.rp;
+    float* po = (s.tail ? a.so : a.po) + (size_t)(2 * s.part + sub) * rp * kD;
+    float* ml = (s.tail ? a.sml : a.pml) + (size_t)(2 * s.part + sub) * rp * 2;
+    if (ok && warp_live && (sub == 0 || two || mine > 0 || s.n1 == 0)) {
+      if (mine > 0) {
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t o[32];
+          t5::ld32(to + ch * 32, o);
+          if (row < live_rows)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(po + ((size_t)(ch * 8 + i) * rp + row) * 4) =
+                  make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+      }
+      if (row < live_rows) {
+        ml[row] = mine > 0 ? m : -INFINITY;  // no tile: an empty partial
+        ml[rp + row] = l;
+      }
+    }
+    x += two ? 2 * s.n : s.n;
+    T += s.n;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const Args a) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(8) Bars bar;
+  __shared__ __align__(16) uint4 masks[kMasks];
+  __shared__ long long s_scan[kThreads / 32];
+  __shared__ int s_at[3];
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  unsigned char* gbase = smem_raw + (base - raw);
+  if (t == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&bar.full[i], 4);
+      mbar_init(&bar.empty[i], 1);
+    }
+    for (int i = 0; i < kQBufs; ++i) {
+      mbar_init(&bar.qfull[i], 4);
+      mbar_init(&bar.qempty[i], 1);
+    }
+    for (int i = 0; i < kMasks; ++i) mbar_init(&bar.mask[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.s[i], 1);
+      mbar_init(&bar.p[i], 128);
+      mbar_init(&bar.o[i], 1);
+    }
+    mbar_init(&bar.drain, 1);
+    fence_barrier_init();
+    s_abort = 0;
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_release();
+  pdl_wait();
+  // this CTA's share: the gang's prefix tiles, and its range of the tails' tiles, whose
+  // first tile is found by a scan of the requests' tile counts
+  Walk walk;
+  const Plan& pl = a.pl;
+  const int gang = blockIdx.x / pl.gang;
+  const long long tp = (long long)a.H * pl.groups * pl.ntp;
+  walk.p0 = gang < pl.gangs ? gang * tp / pl.gangs : 0;
+  walk.p1 = gang < pl.gangs ? (gang + 1) * tp / pl.gangs : 0;
+  const int per = (a.B + kThreads - 1) / kThreads;
+  long long mine = 0;
+  for (int b = t * per; b < (t + 1) * per && b < a.B; ++b) mine += (tail_len(a, b) + kTile - 1) / kTile;
+  long long incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += o;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  t5::fence_before();
+  __syncthreads();
+  t5::fence_after();
+  long long before = 0, total = 0;
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < warp) before += s_scan[i];
+    total += s_scan[i];
+  }
+  const long long ts = total * a.H;
+  // the last CTAs take the tails (the first ones the prefix, where there are few tiles)
+  walk.scta = kCtas - 1 - (int)blockIdx.x;
+  const int sn = ts < kCtas ? (int)ts : kCtas;
+  const long long s0 = walk.scta < sn ? walk.scta * ts / sn : 0, s1 = walk.scta < sn ? (walk.scta + 1) * ts / sn : 0;
+  walk.srem = s1 - s0;
+  walk.sh = walk.sb = walk.stile = 0;
+  if (walk.srem > 0) {
+    const long long at = s0 % total;
+    long long lo = before + incl - mine;
+    if (at >= lo && at < lo + mine) {
+      for (int b = t * per; b < (t + 1) * per && b < a.B; ++b) {
+        const int n = (tail_len(a, b) + kTile - 1) / kTile;
+        if (at < lo + n) {
+          s_at[0] = (int)(s0 / total);
+          s_at[1] = b;
+          s_at[2] = (int)(at - lo);
+          break;
+        }
+        lo += n;
+      }
+    }
+  }
+  __syncthreads();
+  if (walk.srem > 0) {
+    walk.sh = s_at[0];
+    walk.sb = s_at[1];
+    walk.stile = s_at[2];
+  }
+  const uint32_t tm = s_tmem;
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    softmax_role(a, walk, bar, tm, masks, &s_abort);
+  } else {
+    // 2 x 128 x 200 + 2 x 128 x 56 = 65,536 registers, what 512 threads of 128 were launched with
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp < 12)
+      gather_role(a, walk, bar, base, gbase, masks, &s_abort);
+    else if (warp == 12 && lane == 0)
+      mma_role(a, walk, bar, base, tm, &s_abort);
+  }
+  t5::fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    t5::fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(kTmemCols) : "memory");
+  }
+}
+
+// Joins the partials of 32 query rows of one KV head, 32 of the 128 dims a CTA: lane = row,
+// warp = 4 dims, so every partial load is a coalesced float4.  Two passes: the row's
+// maximum over its partials, then the weighted sums.
+__global__ void __launch_bounds__(256) prefix_merge_kernel(const Args a) {
+  __shared__ float s_m[8][32];
+  pdl_release();
+  pdl_wait();
+  const Plan& pl = a.pl;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int blocks = (pl.rows + 31) / 32;
+  const int h = blockIdx.x / blocks, row = (blockIdx.x - h * blocks) * 32 + lane;
+  const bool live = row < pl.rows;
+  const int b = live ? row / a.G : 0, g = row - b * a.G;
+  int L = live ? a.seq_lens[b] : 0;
+  if (L < 0 || L > a.max_len || (L > 0 && L < a.P)) {
+    if (blockIdx.y == 0 && warp == 0) flag(a.status, SKV_DEV_BAD_LENGTH);
+    L = L > a.max_len ? a.max_len : 0;
+  }
+  const bool on = L > 0;
+  // the prefix's partials of this row: gangs c0..c1 of its unit
+  const int pair = row / (2 * kTile), pg = pair / pl.gang, member = pair - pg * pl.gang;
+  const int up = h * pl.groups + pg;
+  const bool two = pl.rows - pair * 2 * kTile > kTile;
+  const int r_in = row & (kTile - 1), sub0 = two ? (row / kTile) & 1 : 0, nsub = two ? 1 : 2;
+  const long long tp = (long long)a.H * pl.groups * pl.ntp, u0 = (long long)up * pl.ntp, u1 = u0 + pl.ntp;
+  int c0 = 0, c1 = -1;
+  if (pl.ntp > 0) {
+    c0 = (int)(((u0 + 1) * pl.gangs - 1) / tp);
+    c1 = (int)((u1 * pl.gangs - 1) / tp);
+  }
+  const int nc = c1 - c0 + 1;
+  // the tail's: CTAs f..e of its unit
+  const int unit = h * a.B + b;
+  int f = 0, e = -1;
+  if (on && L > a.P) {
+    f = a.first[unit];
+    e = a.last[unit];
+    if (f < 0 || e >= kCtas || f > e) f = 0, e = -1;  // never written (an aborted launch)
+  }
+  auto p_at = [&](int c, int u) { return 2 * ((long long)(c + up) * pl.gang + member) + sub0 + u; };
+  auto s_at = [&](int c, int u) { return 2 * ((long long)c + unit) + u; };
+  float m = -INFINITY;
+  if (on) {
+    for (int i = warp; i < nc * nsub; i += 8) {
+      const int c = c0 + i / nsub;
+      m = fmaxf(m, a.pml[p_at(c, i % nsub) * pl.rp * 2 + r_in]);
+    }
+    for (int i = warp; i < 2 * (e - f + 1); i += 8) m = fmaxf(m, a.sml[s_at(f + i / 2, i % 2) * a.G * 2 + g]);
+  }
+  s_m[warp][lane] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, s_m[i][lane]);
+  const int d4 = blockIdx.y * 8 + warp;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](const float* ml, const float* po, int rp, int r) {
+    const float mp = ml[r], lp = ml[rp + r];
+    if (mp == -INFINITY) return;  // an empty partial: its O was never written
+    const float w = exp2f(mp - m);
+    const float4 v = *reinterpret_cast<const float4*>(po + ((size_t)d4 * rp + r) * 4);
+    l = fmaf(w, lp, l);
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+  };
+  if (on) {
+#pragma unroll 4
+    for (int i = 0; i < nc * nsub; ++i) {
+      const int c = c0 + i / nsub;
+      const long long at = p_at(c, i % nsub) * pl.rp;
+      add(a.pml + at * 2, a.po + at * kD, pl.rp, r_in);
+    }
+    for (int i = 0; i < 2 * (e - f + 1); ++i) {
+      const long long at = s_at(f + i / 2, i % 2) * a.G;
+      add(a.sml + at * 2, a.so + at * kD, a.G, g);
+    }
+  }
+  if (!live) return;
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // NaN stays NaN; no key at all: 0
+  const size_t hq = (size_t)b * a.Hq + (size_t)h * a.G + g;
+  uint2 r;
+  r.x = tc::pack_bf16(o.x * inv, o.y * inv);
+  r.y = tc::pack_bf16(o.z * inv, o.w * inv);
+  *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out + hq * kD + d4 * 4) = r;
+  if (a.lse && d4 == 0) a.lse[hq] = l > 0.f || l != l ? kLn2 * (m + log2f(l)) : -INFINITY;
+}
+
+struct Layout {
+  size_t po, pml, so, sml, first, last, total;
+};
+Layout layout_of(const skv_problem& p, int P) {
+  const int G = p.n_q_heads / p.n_kv_heads;
+  const Plan pl = plan_of(p.batch, p.n_kv_heads, G, P);
+  const size_t units = (size_t)p.n_kv_heads * p.batch;
+  const size_t pp = pl.ntp > 0 ? 2 * (size_t)(pl.gangs + (size_t)p.n_kv_heads * pl.groups) * pl.gang * pl.rp : 0;
+  const size_t sp = P < p.max_len ? 2 * (kCtas + units) * G : 0;
+  Layout l;
+  l.po = 0;
+  l.pml = l.po + align256(pp * kD * 4);
+  l.so = l.pml + align256(pp * 2 * 4);
+  l.sml = l.so + align256(sp * kD * 4);
+  l.first = l.sml + align256(sp * 2 * 4);
+  l.last = l.first + align256(units * 4);
+  l.total = l.last + align256(units * 4);
+  return l;
+}
+
+}  // namespace px
+}  // namespace
+
+size_t prefix_workspace_bytes(const skv_problem& p, int prefix_len) { return px::layout_of(p, prefix_len).total; }
+
+skv_status launch_prefix_attn(const skv_problem& p, const void* q, const PoolView& pool, const skv_prefix& prefix,
+                              void* out, float* lse, void* ws, int32_t* status, cudaStream_t st) {
+  using namespace px;
+  const int G = p.n_q_heads / p.n_kv_heads;
+  const Layout lay = layout_of(p, prefix.len);
+  unsigned char* w = (unsigned char*)ws;
+  Args a;
+  a.q = (const unsigned char*)q;
+  a.pool = pool;
+  a.ptable = prefix.table;
+  a.seq_lens = p.seq_lens;
+  a.B = p.batch;
+  a.H = p.n_kv_heads;
+  a.Hq = p.n_q_heads;
+  a.G = G;
+  a.P = prefix.len;
+  a.max_len = p.max_len;
+  a.bs = p.block_size;
+  a.scale_log2 = (p.sm_scale > 0.f ? p.sm_scale : 1.f / sqrtf((float)p.d_qk)) * kLog2e;
+  a.pl = plan_of(p.batch, p.n_kv_heads, G, prefix.len);
+  a.po = (float*)(w + lay.po);
+  a.pml = (float*)(w + lay.pml);
+  a.so = (float*)(w + lay.so);
+  a.sml = (float*)(w + lay.sml);
+  a.first = (int*)(w + lay.first);
+  a.last = (int*)(w + lay.last);
+  a.out = out;
+  a.lse = lse;
+  a.status = status;
+  const skv_status prep = prepare_kernel((const void*)prefix_attn_kernel, px::kSmem);
+  if (prep != SKV_OK) return prep;
+  if (launch_dependent(prefix_attn_kernel, dim3(kCtas), dim3(px::kThreads), px::kSmem, st, 1, a) != cudaSuccess)
+    return SKV_ERR_CUDA;
+  SKV_LAUNCH_CHECK();
+  const long long blocks = (long long)((a.pl.rows + 31) / 32) * a.H;
+  if (launch_dependent(prefix_merge_kernel, dim3((unsigned)blocks, 4), dim3(256), 0, st, 1, a) != cudaSuccess)
+    return SKV_ERR_CUDA;
+  SKV_LAUNCH_CHECK();
+  return SKV_OK;
+}
+
+}  // namespace skv

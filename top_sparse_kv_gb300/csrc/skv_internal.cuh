@@ -506,6 +506,11 @@ skv_status launch_cache_update(const skv_problem& p, const PoolView& pool, const
 skv_status launch_token_rows(const skv_problem& p, const skv_rotary& r, const skv_tokens& t, const PoolView& pool,
                              void* q_out, void* k_out, int32_t* status, cudaStream_t st);
 
+// attention over a shared prefix and every request's own tail (attn_prefix.cu)
+size_t prefix_workspace_bytes(const skv_problem& p, int prefix_len);
+skv_status launch_prefix_attn(const skv_problem& p, const void* q, const PoolView& pool, const skv_prefix& prefix,
+                              void* out, float* lse, void* ws, int32_t* status, cudaStream_t st);
+
 // block selection from per-block key summaries (blocks.cu)
 int block_list_len(const skv_problem& p, int topk_blocks);
 size_t block_summary_bytes(const skv_problem& p);

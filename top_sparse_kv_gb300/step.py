@@ -227,3 +227,32 @@ class TokenStep:
         B._check("skv_append_kv", B.lib().skv_append_kv(self._p, self._r, ctypes.byref(ct), self._pool, qo, self._st,
                                                         B._stream(stream)))
         return q_out
+
+
+class PrefixStep:
+    """Attention of a batch over a shared prefix and every request's own tail: owns the output,
+    lse, workspace and status; `run(q)` is one skv_prefix_attn.  The problem, the pool and the
+    prefix are marshalled once, here."""
+
+    def __init__(self, problem: B.Problem, pool: B.Pool, prefix: B.Prefix):
+        prefix.check(problem)
+        self.p, self.pool, self.prefix = problem, pool, prefix
+        dev = problem.seq_lens.device
+        self._shape = (problem.batch, problem.n_q_heads, problem.d_qk)
+        self._p, self._pool, self._prefix = (ctypes.byref(x.c()) for x in (problem, pool, prefix))
+        self.out = torch.empty((problem.batch, problem.n_q_heads, problem.d_v), dtype=pool.gpu_k.dtype, device=dev)
+        self.lse = torch.empty((problem.batch, problem.n_q_heads), dtype=torch.float32, device=dev)
+        self.ws = torch.empty((max(B.skv_prefix_workspace_size(problem, prefix.len), 16),), dtype=torch.uint8,
+                              device=dev)
+        self.status = torch.zeros((1,), dtype=torch.int32, device=dev)
+        self._tail = (ctypes.c_void_p(self.out.data_ptr()), ctypes.c_void_p(self.lse.data_ptr()),
+                      ctypes.c_void_p(self.ws.data_ptr()), self.ws.numel(),
+                      ctypes.c_void_p(self.status.data_ptr()))
+
+    def run(self, q, stream=None):
+        """(out, lse), the step's own buffers."""
+        if q.shape != self._shape or q.dtype != self.out.dtype or not q.is_contiguous():
+            raise ValueError(f"q: contiguous {self.out.dtype} {list(self._shape)} expected")
+        B._check("skv_prefix_attn", B.lib().skv_prefix_attn(self._p, q.data_ptr(), self._pool, self._prefix,
+                                                            *self._tail, B._stream(stream)))
+        return self.out, self.lse
