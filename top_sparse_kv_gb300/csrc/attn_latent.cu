@@ -19,8 +19,6 @@
 //   latent_merge_kernel    log-sum-exp merge of the blocks' partials.
 #include <cuda.h>  // CUtensorMap and its enums (the encoder is fetched from the driver at run time)
 
-#include <mutex>
-
 #include "attn_common.cuh"
 #include "tcgen05.cuh"
 
@@ -471,25 +469,6 @@ LatentLayout latent_layout(const skv_problem& p) {
   l.tickets = l.ml + align256(B * p.n_q_heads * S * 2 * 4);
   l.total = l.tickets + align256(B * 4);
   return l;
-}
-
-// cuTensorMapEncodeTiled, fetched once from the driver through the runtime
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-  });
-  return fn;
 }
 
 // A [d2][d1][d0] bf16 tensor (rows of d0 elements, packed) in boxes of 64 x box1 x 1,

@@ -9,9 +9,11 @@
 //
 // prefix_attn_kernel, one persistent CTA an SM, 16 warps in four roles:
 //   warps 0-3, 4-7   softmax of slot 0 / slot 1 (a thread a query row)
-//   warps 8-11       gather: every K and V row through the table (GPU pool, or pinned host
-//                    pool over UVA), 16-byte cp.async into a ring of 32 KB stages in the
-//                    128-byte-swizzled layout that the MMA reads
+//   warps 8-11       gather: K and V through the table into a ring of 32 KB stages, in the
+//                    128-byte-swizzled layout that the MMA reads: 16 keys of a block by one
+//                    4 KB TMA copy; keys at a history's edge, in the host pool (over UVA) or
+//                    of blocks that 16 does not divide row by row, 16-byte cp.async with
+//                    zeros for what is not attended
 //   warp 12          one thread issues every MMA
 // A *step* is one (128 query rows, 128 keys) tile: S = Q K^T (M128 N128, fp32 in TMEM),
 // P = 2^(z - m) in bf16 over S's own columns, O += P V (A from TMEM, V read MN-major).
@@ -29,6 +31,8 @@
 // consecutive CTAs.  A segment's O, m and l go to the workspace, at an index that grows
 // with both the CTA and the unit, so no two segments share one and no atomics are needed.
 // prefix_merge_kernel joins a row's partials by log-sum-exp, in a fixed order.
+#include <cuda.h>  // CUtensorMap and its enums
+
 #include "attn_common.cuh"
 #include "tcgen05.cuh"
 
@@ -39,8 +43,10 @@ namespace px {
 constexpr int kCtas = 152;             // one CTA an SM of a GB300 (a function of the problem alone: sizes the workspace)
 constexpr int kThreads = 512;
 constexpr int kTile = 128;             // keys a tile, query rows a tile
-constexpr int kHalfB = kTile * 128;    // 128 rows x 64 dims, 16 KB
-constexpr int kStageB = 2 * kHalfB;    // a K, V or Q tile: 32 KB
+constexpr int kStageB = kTile * 256;   // a K, V or Q tile, 32 KB: [group of 8 rows][half of the dims][8 rows][128 bytes]
+constexpr int kGroupB = 2048;          // a group of 8 rows
+constexpr int kHalfB = 1024;           // one half of its dims
+constexpr int kChunk = 16;             // keys of one TMA copy
 constexpr int kRing = 5;               // K / V stages
 constexpr int kQBufs = 2;
 constexpr int kMasks = 8;              // key masks of the last tiles
@@ -75,6 +81,7 @@ struct Args {
   PoolView pool;
   const int32_t *ptable, *seq_lens;
   int B, H, Hq, G, P, max_len, bs;
+  int tma;             // blocks are whole chunks of 16 keys
   float scale_log2;
   Plan pl;
   float *po, *pml;     // prefix partials: [(gang + unit) * members + member][2][...]
@@ -85,17 +92,22 @@ struct Args {
   int32_t* status;
 };
 
-// the tail's key tiles of request b (none for an empty request or one that ends inside the prefix)
-__device__ __forceinline__ int tail_len(const Args& a, int b) {
+// A tail's tiles start at the chunk of 16 that the prefix ends inside.
+__host__ __device__ __forceinline__ int tail_base(int P) { return P & ~(kChunk - 1); }
+// end of request b's tail (P: none, an empty request or one that ends inside the prefix), and its tiles
+__device__ __forceinline__ int tail_end(const Args& a, int b) {
   int L = a.seq_lens[b];
   L = L > a.max_len ? a.max_len : L;
-  return L > a.P ? L - a.P : 0;
+  return L > a.P ? L : a.P;
+}
+__device__ __forceinline__ int tail_tiles(const Args& a, int end) {
+  return end > a.P ? (end - tail_base(a.P) + kTile - 1) / kTile : 0;
 }
 
 struct Seg {
   int tail, h, b;      // a tail's segment (of request b), or the prefix's
   int row0, n0, n1;    // first query row; live rows of the two row tiles (n1 = 0: one tile)
-  int t0, n, hi;       // first key position, key tiles, end of the valid positions
+  int t0, n, lo, hi;   // first key position, key tiles, the valid positions [lo, hi)
   bool begins, ends;   // the tail's first / last segment
   long long part;      // the partial's index
 };
@@ -125,13 +137,14 @@ struct Walk {
       s.n1 = r <= kTile ? 0 : (r - kTile < kTile ? r - kTile : kTile);
       s.t0 = tile * kTile;
       s.n = n;
+      s.lo = 0;
       s.hi = a.P;
       s.begins = s.ends = false;
       s.part = (long long)(c + up) * pl.gang + member;
       return true;
     }
     while (srem > 0) {
-      const int len = tail_len(a, sb), nt = (len + kTile - 1) / kTile;
+      const int end = tail_end(a, sb), nt = tail_tiles(a, end);
       if (stile >= nt) {
         stile = 0;
         if (++sb == a.B) {
@@ -147,9 +160,10 @@ struct Walk {
       s.row0 = sb * a.G;
       s.n0 = a.G;
       s.n1 = 0;
-      s.t0 = a.P + stile * kTile;
+      s.t0 = tail_base(a.P) + stile * kTile;
       s.n = n;
-      s.hi = a.P + len;
+      s.lo = a.P;
+      s.hi = end;
       s.begins = stile == 0;
       s.ends = stile + n == nt;
       s.part = (long long)scta + (long long)sh * a.B + sb;
@@ -172,72 +186,82 @@ struct Bars {
 };
 
 // ---------------------------------------------------------------------------- gather warps
+// A gather warp's copies: TMA copies complete on their stage's barrier by themselves; rows
+// copied by cp.async are announced there by the warp once they have landed.  Announcements
+// are put off (the copies keep flying) until a buffer is waited for: what frees it may need
+// the tiles in flight, so the oldest are announced, one at a time, until it is free.
 struct Gather {
   const Args& a;
-  Bars& bar;
-  uint32_t base;
-  unsigned char* gbase;
   volatile int* abort;
-  uint64_t* pend[2];  // barriers of the copy groups that are not announced yet
-  int w, lane;
+  uint64_t* pend[kRing + kQBufs];  // barriers of unannounced copy groups, oldest first
+  int n;
   bool ok;
 
-  __device__ void announce(uint64_t* b) {
+  __device__ __forceinline__ void announce_oldest() {
+    switch (n) {  // cp.async.wait_group takes a constant
+      case 1: cp_async_wait<0>(); break;
+      case 2: cp_async_wait<1>(); break;
+      case 3: cp_async_wait<2>(); break;
+      case 4: cp_async_wait<3>(); break;
+      case 5: cp_async_wait<4>(); break;
+      case 6: cp_async_wait<5>(); break;
+      default: cp_async_wait<6>(); break;
+    }
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(b);
+    if ((threadIdx.x & 31) == 0) mbar_arrive(pend[0]);
+    --n;
+#pragma unroll
+    for (int i = 0; i + 1 < kRing + kQBufs; ++i) pend[i] = pend[i + 1];
   }
-  // a new copy group; the one two back has landed
-  __device__ void commit(uint64_t* b) {
+  __device__ __forceinline__ void commit(uint64_t* b) {
     cp_async_commit();
-    cp_async_wait<2>();
-    if (pend[0]) announce(pend[0]);
-    pend[0] = pend[1];
-    pend[1] = b;
+    if (n == kRing + kQBufs) announce_oldest();
+#pragma unroll
+    for (int i = 0; i < kRing + kQBufs; ++i)
+      if (i == n) pend[i] = b;
+    ++n;
   }
-  __device__ void flush() {
-    cp_async_wait<0>();
-    if (pend[0]) announce(pend[0]);
-    if (pend[1]) announce(pend[1]);
-    pend[0] = pend[1] = nullptr;
-  }
-  // Wait for a free buffer.  Everything in flight is announced first when it is not free
-  // yet: what frees it may need those tiles.
-  __device__ void wait_free(uint64_t* b, uint32_t parity) {
-    if (!ok) return;
-    bool free = mbar_try_wait(b, parity);
-    if (__any_sync(0xffffffffu, !free)) {
-      flush();
+  __device__ __forceinline__ void wait_free(uint64_t* b, uint32_t parity) {
+    while (__any_sync(0xffffffffu, !mbar_try_wait(b, parity))) {
+      if (n > 0) {
+        announce_oldest();
+        continue;
+      }
       ok = wait_or_abort(b, parity, abort, a.status);
       ok = !__any_sync(0xffffffffu, !ok);
+      return;
     }
+  }
+  __device__ __forceinline__ void flush() {
+    while (n > 0) announce_oldest();
   }
 };
 
-// Row references of a tile: lane l holds rows 4 l + (two of 0..3, by the warp's parity).
-// A reference is the row's index in its pool, bit 62 for the host pool, -1 for none.
-__device__ __forceinline__ void load_entries(const Args& a, const int32_t* table, int t, int hi, int lane, int* e) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int tt = t + 4 * lane + j;
-    e[j] = tt < hi ? table[tt / a.bs] : 0;
-  }
-}
-__device__ __forceinline__ long long row_ref(const Args& a, int h, int e, int t, int hi) {
-  if (t >= hi) return -1;
+// Reference of position t's row: its index in its pool, bit 62 for the host pool, -1 for none.
+__device__ __forceinline__ long long row_ref(const Args& a, int h, int e, int t) {
   if (e >= 0) return e < a.pool.n_gpu ? ((long long)e * a.H + h) * a.bs + t % a.bs : -1;
   const long long hb = -(long long)e - 1;
   if (a.pool.host_k == nullptr || hb >= a.pool.n_host) return -1;
   return tc::kHostBit | ((hb * a.H + h) * a.bs + t % a.bs);
 }
 
-__device__ __forceinline__ void gather_role(const Args& a, Walk walk, Bars& bar, uint32_t base, unsigned char* gbase, uint4* masks,
-                            volatile int* abort) {
+// 16 keys' rows of 256 bytes of a pool viewed as [rows / 8][2 halves][8 rows][64 dims]
+__device__ __forceinline__ void tma_chunk(uint32_t dst, const CUtensorMap* map, int group, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], "
+      "[%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(group), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void gather_role(const Args& a, const CUtensorMap* tk, const CUtensorMap* tv, Walk walk,
+                                            Bars& bar, uint32_t base, unsigned char* gbase, uint16_t* masks,
+                                            volatile int* abort) {
   const int w = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31;
-  Gather g{a, bar, base, gbase, abort, {nullptr, nullptr}, w, lane, true};
-  const int c = lane & 15;  // the row's 16-byte chunk this thread copies
-  const int rlow = 2 * w + (lane >> 4);
-  const uint32_t dst0 = (uint32_t)((c >> 3) * kHalfB) + t5::sw128(rlow, c & 7);  // row rlow of each group of 8
+  Gather g{a, abort, {}, 0, true};
+  const int r16 = lane >> 1, half = lane & 1;  // cp.async: a lane copies half a row
+  const uint32_t row_off = (uint32_t)((r16 >> 3) * kGroupB + half * kHalfB + (r16 & 7) * 128);
   Seg s;
   int T = 0, nq = 0;
   while (g.ok && walk.next(a, s)) {
@@ -245,61 +269,93 @@ __device__ __forceinline__ void gather_role(const Args& a, Walk walk, Bars& bar,
       if (s.begins) a.first[s.h * a.B + s.b] = walk.scta;
       if (s.ends) a.last[s.h * a.B + s.b] = walk.scta;
     }
-    const int32_t* table = s.tail ? a.pool.table + (size_t)s.b * a.pool.stride : a.ptable;
-    int e[4];
-    load_entries(a, table, s.t0, s.hi, lane, e);
-    // query rows
+    // query rows: this warp copies the chunks w and w + 4 of 16 rows
     for (int u = 0; u < (s.n1 > 0 ? 2 : 1); ++u, ++nq) {
       const int buf = nq & 1;
       g.wait_free(&bar.qempty[buf], (uint32_t)((nq >> 1) & 1) ^ 1u);
       if (!g.ok) break;
       const int live = u ? s.n1 : s.n0;
-      unsigned char* dst = gbase + buf * kStageB + dst0;
-      for (int pass = 0; pass < 16; ++pass) {
-        const int r = 8 * pass + rlow;
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const int r = kChunk * (w + 4 * v) + r16;
         if (r < live) {
           const int row = s.row0 + u * kTile + r, b = row / a.G, gg = row - b * a.G;
-          cp_async16(dst + pass * 1024, a.q + (((size_t)b * a.Hq + (size_t)s.h * a.G + gg) * kD + c * 8) * 2);
+          const unsigned char* src = a.q + (((size_t)b * a.Hq + (size_t)s.h * a.G + gg) * 2 + half) * 128;
+          unsigned char* dst = gbase + buf * kStageB + (w + 4 * v) * 2 * kGroupB + row_off;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) cp_async16(dst + ((c ^ (r16 & 7)) << 4), src + c * 16);
         }
       }
       g.commit(&bar.qfull[buf]);
     }
+    const int32_t* table = s.tail ? a.pool.table + (size_t)s.b * a.pool.stride : a.ptable;
     for (int i = 0; g.ok && i < s.n; ++i, ++T) {
-      const int t = s.t0 + i * kTile;
+      const int t0 = s.t0 + i * kTile;
+      // the warp's two chunks: a whole block part of the GPU pool by TMA, else row by row
+      int group[2];
       long long ref[2];
-      unsigned okm[4];
+      uint32_t valid[2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const long long r = row_ref(a, s.h, e[j], t + 4 * lane + j, s.hi);
-        if (j == 2 * (w & 1)) ref[0] = r;
-        if (j == 2 * (w & 1) + 1) ref[1] = r;
-        okm[j] = __ballot_sync(0xffffffffu, r >= 0);
-        if (w == 0 && r < 0 && t + 4 * lane + j < s.hi) flag(a.status, SKV_DEV_BAD_SLOT);
+      for (int v = 0; v < 2; ++v) {
+        const int tc0 = t0 + kChunk * (w + 4 * v);
+        group[v] = -1;
+        ref[v] = -1;
+        valid[v] = 0xffffu;
+        if (a.tma && tc0 >= s.lo && tc0 + kChunk <= s.hi) {
+          const int e = table[tc0 / a.bs];
+          if (e >= 0 && e < a.pool.n_gpu) group[v] = (int)((((long long)e * a.H + s.h) * a.bs + tc0 % a.bs) >> 3);
+        }
+        if (group[v] < 0) {
+          const int t = tc0 + r16;
+          if (t >= s.lo && t < s.hi) {
+            ref[v] = row_ref(a, s.h, table[t / a.bs], t);
+            if (ref[v] < 0) flag(a.status, SKV_DEV_BAD_SLOT);
+          }
+          const int mine = __shfl_sync(0xffffffffu, (int)(ref[v] >= 0), (2 * lane) & 31);  // lane r < 16: row r
+          valid[v] = __ballot_sync(0xffffffffu, mine && lane < kChunk);
+        }
       }
-      if (i + 1 < s.n) load_entries(a, table, t + kTile, s.hi, lane, e);
+      const bool rows = group[0] < 0 || group[1] < 0;
+      const uint32_t bytes = ((group[0] >= 0) + (group[1] >= 0)) * 2 * kGroupB;
 #pragma unroll 1
-      for (int kv = 0; kv < 2 && g.ok; ++kv) {
+      for (int kv = 0; kv < 2; ++kv) {
         const int seq = 2 * T + kv, st = seq % kRing;
         g.wait_free(&bar.empty[st], (uint32_t)((seq / kRing) & 1) ^ 1u);
         if (!g.ok) break;
-        if (kv == 0 && w == 0 && lane == 0) {
-          masks[T % kMasks] = make_uint4(okm[0], okm[1], okm[2], okm[3]);
+        if (kv == 0 && lane == 0) {
+          masks[(T % kMasks) * 8 + w] = (uint16_t)valid[0];
+          masks[(T % kMasks) * 8 + w + 4] = (uint16_t)valid[1];
           mbar_arrive(&bar.mask[T % kMasks]);
         }
-        const unsigned char* gp = (const unsigned char*)(kv ? a.pool.gpu_v : a.pool.gpu_k) + c * 16;
-        const unsigned char* hp = (const unsigned char*)(kv ? a.pool.host_v : a.pool.host_k) + c * 16;
-        unsigned char* dst = gbase + (kQBufs + st) * kStageB + dst0;
-#pragma unroll 8
-        for (int pass = 0; pass < 16; ++pass) {
-          const int from = 2 * pass + (w >> 1);
-          const long long ra = __shfl_sync(0xffffffffu, ref[0], from), rb = __shfl_sync(0xffffffffu, ref[1], from);
-          const long long r = lane < 16 ? ra : rb;
-          const unsigned char* src = (r & tc::kHostBit) ? hp : gp;
-          const bool live = r >= 0;
-          src = live ? src + (size_t)(r & tc::kRefRowMask) * tc::kRowBytes : gp - c * 16;
-          tc::cp_async16_zfill(dst + pass * 1024, src, live);
+        uint64_t* full = &bar.full[st];
+        const uint32_t off = (uint32_t)((kQBufs + st) * kStageB);
+        if (lane == 0 && bytes > 0) {
+          if (rows)
+            mbar_expect_tx(full, bytes);  // the arrival follows when the rows have landed
+          else
+            mbar_arrive_expect_tx(full, bytes);
+#pragma unroll
+          for (int v = 0; v < 2; ++v)
+            if (group[v] >= 0) tma_chunk(base + off + (w + 4 * v) * 2 * kGroupB, kv ? tv : tk, group[v], full);
         }
-        g.commit(&bar.full[st]);
+        if (rows) {
+          __syncwarp();  // the bytes are expected before the arrival
+          const unsigned char* gp = (const unsigned char*)(kv ? a.pool.gpu_v : a.pool.gpu_k);
+          const unsigned char* hp = (const unsigned char*)(kv ? a.pool.host_v : a.pool.host_k);
+#pragma unroll
+          for (int v = 0; v < 2; ++v)
+            if (group[v] < 0) {
+              const bool live = ref[v] >= 0;
+              const unsigned char* src =
+                  live ? ((ref[v] & tc::kHostBit) ? hp : gp) + (size_t)(ref[v] & tc::kRefRowMask) * tc::kRowBytes + half * 128
+                       : gp;
+              unsigned char* dst = gbase + off + (w + 4 * v) * 2 * kGroupB + row_off;
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                tc::cp_async16_zfill(dst + ((c ^ (r16 & 7)) << 4), live ? src + c * 16 : src, live);
+            }
+          g.commit(full);
+        }
       }
     }
   }
@@ -370,7 +426,7 @@ __device__ __forceinline__ void mma_role(const Args& a, Walk walk, Bars& bar, ui
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) {  // 16 of the 128 dims each
       const uint32_t off = (uint32_t)(kk >> 2) * kHalfB + (kk & 3) * 32;
-      t5::mma(tm + st.slot * 128, t5::desc_sw128(qa + off, 16, 1024), t5::desc_sw128(ka + off, 16, 1024), id_s,
+      t5::mma(tm + st.slot * 128, t5::desc_sw128(qa + off, 16, kGroupB), t5::desc_sw128(ka + off, 16, kGroupB), id_s,
               kk > 0 ? 1u : 0u);
     }
     t5::commit(&bar.s[st.slot]);
@@ -386,7 +442,7 @@ __device__ __forceinline__ void mma_role(const Args& a, Walk walk, Bars& bar, ui
     const uint32_t va = base + (kQBufs + vs) * kStageB;
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)  // 16 of the 128 keys each
-      t5::mma_ts(tm + 256 + st.slot * 128, tm + st.slot * 128 + kk * 8, t5::desc_sw128(va + kk * 2048, kHalfB, 1024),
+      t5::mma_ts(tm + 256 + st.slot * 128, tm + st.slot * 128 + kk * 8, t5::desc_sw128(va + kk * 2 * kGroupB, kHalfB, kGroupB),
                  id_o, (st.o_first && kk == 0) ? 0u : 1u);
     if (st.k_last) t5::commit(&bar.empty[vs]);
     if (st.o_last) t5::commit(&bar.o[st.slot]);
@@ -440,7 +496,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Walk walk, Bars& bar
           const uint32_t mw[4] = {mk.x, mk.y, mk.z, mk.w};
 #pragma unroll
           for (int i = 0; i < 128; ++i)
-            if (!((mw[i & 3] >> (i >> 2)) & 1u)) v[i] = 0xff800000u;  // -inf
+            if (!((mw[i >> 5] >> (i & 31)) & 1u)) v[i] = 0xff800000u;  // -inf
         }
         float mx[4];
 #pragma unroll
@@ -519,7 +575,9 @@ __device__ __forceinline__ void softmax_role(const Args& a, Walk walk, Bars& bar
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_constant__ CUtensorMap tk,
+                                                                  const __grid_constant__ CUtensorMap tv,
+                                                                  const Args a) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) Bars bar;
   __shared__ __align__(16) uint4 masks[kMasks];
@@ -540,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const Args a) 
       mbar_init(&bar.qfull[i], 4);
       mbar_init(&bar.qempty[i], 1);
     }
-    for (int i = 0; i < kMasks; ++i) mbar_init(&bar.mask[i], 1);
+    for (int i = 0; i < kMasks; ++i) mbar_init(&bar.mask[i], 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.s[i], 1);
       mbar_init(&bar.p[i], 128);
@@ -568,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const Args a) 
   walk.p1 = gang < pl.gangs ? (gang + 1) * tp / pl.gangs : 0;
   const int per = (a.B + kThreads - 1) / kThreads;
   long long mine = 0;
-  for (int b = t * per; b < (t + 1) * per && b < a.B; ++b) mine += (tail_len(a, b) + kTile - 1) / kTile;
+  for (int b = t * per; b < (t + 1) * per && b < a.B; ++b) mine += tail_tiles(a, tail_end(a, b));
   long long incl = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -596,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const Args a) 
     long long lo = before + incl - mine;
     if (at >= lo && at < lo + mine) {
       for (int b = t * per; b < (t + 1) * per && b < a.B; ++b) {
-        const int n = (tail_len(a, b) + kTile - 1) / kTile;
+        const int n = tail_tiles(a, tail_end(a, b));
         if (at < lo + n) {
           s_at[0] = (int)(s0 / total);
           s_at[1] = b;
@@ -621,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const Args a) 
     // 2 x 128 x 200 + 2 x 128 x 56 = 65,536 registers, what 512 threads of 128 were launched with
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp < 12)
-      gather_role(a, walk, bar, base, gbase, masks, &s_abort);
+      gather_role(a, &tk, &tv, walk, bar, base, gbase, reinterpret_cast<uint16_t*>(masks), &s_abort);
     else if (warp == 12 && lane == 0)
       mma_role(a, walk, bar, base, tm, &s_abort);
   }
@@ -722,6 +780,19 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const Args a) {
   if (a.lse && d4 == 0) a.lse[hq] = l > 0.f || l != l ? kLn2 * (m + log2f(l)) : -INFINITY;
 }
 
+// A pool's K or V rows as [rows / 8][2 halves of the dims][8 rows][64 dims], in boxes of 16
+// rows: one copy lands in the layout the MMA reads.
+bool encode_pool(CUtensorMap* map, const void* ptr, long long rows) {
+  const cuuint64_t dims[4] = {64, 8, 2, (cuuint64_t)(rows / 8)};
+  const cuuint64_t strides[3] = {256, 128, 2048};
+  const cuuint32_t box[4] = {64, 8, 2, 2};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const EncodeTiledFn fn = encode_tiled();
+  return fn != nullptr && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct Layout {
   size_t po, pml, so, sml, first, last, total;
 };
@@ -778,7 +849,11 @@ skv_status launch_prefix_attn(const skv_problem& p, const void* q, const PoolVie
   a.status = status;
   const skv_status prep = prepare_kernel((const void*)prefix_attn_kernel, px::kSmem);
   if (prep != SKV_OK) return prep;
-  if (launch_dependent(prefix_attn_kernel, dim3(kCtas), dim3(px::kThreads), px::kSmem, st, 1, a) != cudaSuccess)
+  CUtensorMap tk, tv;
+  const long long rows = pool.n_gpu * p.n_kv_heads * p.block_size;
+  a.tma = p.block_size % kChunk == 0 && rows > 0 && rows / 8 < (1LL << 31);
+  if (a.tma && (!encode_pool(&tk, pool.gpu_k, rows) || !encode_pool(&tv, pool.gpu_v, rows))) return SKV_ERR_CUDA;
+  if (launch_dependent(prefix_attn_kernel, dim3(kCtas), dim3(px::kThreads), px::kSmem, st, 1, tk, tv, a) != cudaSuccess)
     return SKV_ERR_CUDA;
   SKV_LAUNCH_CHECK();
   const long long blocks = (long long)((a.pl.rows + 31) / 32) * a.H;

@@ -1,6 +1,7 @@
 // Internal helpers shared by the sm_103a kernels of libskv (not part of the ABI).
 #pragma once
 
+#include <cuda.h>  // CUtensorMap and its enums
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -150,6 +151,11 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
                : "memory");
+}
+
+// expected bytes without an arrival
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -427,6 +433,12 @@ skv_status prepare_kernel(const void* kernel, int dyn_smem, int threads = 0, int
 // CUDA context.  The kernel's dynamic shared-memory limit must already be set
 // (prepare_kernel).
 skv_status max_active_clusters(const void* kernel, int dyn_smem, int threads, int cluster, int* clusters);
+
+// cuTensorMapEncodeTiled, fetched once from the driver through the runtime (null: not found)
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled();
 
 // pf: optional; scoring then also stages the host rows of keys above the prediction
 // (contiguous index keys with a per-token slot map only).
