@@ -363,99 +363,110 @@ __device__ __forceinline__ void gather_role(const Args& a, const CUtensorMap* tk
 }
 
 // ---------------------------------------------------------------------------- MMA thread
-struct Step {
-  int T, slot, q;                                // key tile, TMEM slot, Q buffer sequence number
-  bool k_first, k_last, q_first, q_last;         // first / last use of the K stage (the V stage alike) and of the Q buffer
-  bool o_first, o_last;                          // first / last step of its slot in the segment
-};
+// A step as the issuing thread needs it, one word: ring stages and parities, first and last uses.
+namespace step {
+constexpr uint32_t kStage = 7u, kKPar = 3, kVStage = 4, kVPar = 7, kQBuf = 8, kQPar = 9;
+constexpr uint32_t kKFirst = 1u << 10, kKLast = 1u << 11, kQFirst = 1u << 12, kQLast = 1u << 13, kOFirst = 1u << 14,
+                   kOLast = 1u << 15, kLive = 1u << 16;
+}  // namespace step
 struct Steps {
   Walk walk;
-  Seg s;
-  int i, sub, T, x, nq;
-  bool have;
-  __device__ bool next(const Args& a, Step& o) {
+  int n, i, nq;            // the segment's key tiles, the next one, Q buffers used before it
+  uint32_t stage, par;     // ring position of the next tile's K
+  bool two, second, have;  // two row tiles; the second one is next; inside a segment
+  __device__ __forceinline__ uint32_t next(const Args& a) {
     if (!have) {
-      if (!walk.next(a, s)) return false;
+      Seg s;
+      if (!walk.next(a, s)) return 0u;
       have = true;
-      i = sub = 0;
+      n = s.n;
+      two = s.n1 > 0;
+      i = 0;
+      second = false;
     }
-    const bool two = s.n1 > 0;
-    o.T = T;
-    o.slot = x & 1;
-    o.q = nq + (two ? sub : 0);
-    o.k_first = sub == 0;
-    o.k_last = !two || sub == 1;
-    o.q_first = i == 0;
-    o.q_last = i == s.n - 1;
-    o.o_first = two ? i == 0 : i < 2;
-    o.o_last = two ? i == s.n - 1 : i >= s.n - 2;
-    ++x;
-    if (two && sub == 0) {
-      sub = 1;
+    const uint32_t wrap = stage + 1 == kRing, q = (uint32_t)nq + (second ? 1u : 0u);
+    uint32_t c = step::kLive | stage | par << step::kKPar | (wrap ? 0u : stage + 1) << step::kVStage |
+                 (par ^ wrap) << step::kVPar | (q & 1u) << step::kQBuf | ((q >> 1) & 1u) << step::kQPar;
+    if (!second) c |= step::kKFirst;
+    if (!two || second) c |= step::kKLast;
+    if (i == 0) c |= step::kQFirst;
+    if (i == n - 1) c |= step::kQLast;
+    if (i < (two ? 1 : 2)) c |= step::kOFirst;
+    if (i >= n - (two ? 1 : 2)) c |= step::kOLast;
+    if (two && !second) {
+      second = true;
     } else {
-      sub = 0;
-      ++T;
-      if (++i == s.n) {
+      second = false;
+      stage += 2;
+      if (stage >= kRing) {
+        stage -= kRing;
+        par ^= 1u;
+      }
+      if (++i == n) {
         have = false;
         nq += two ? 2 : 1;
       }
     }
-    return true;
+    return c;
   }
 };
 
-__device__ __forceinline__ void mma_role(const Args& a, Walk walk, Bars& bar, uint32_t base, uint32_t tm, volatile int* abort) {
+__device__ __forceinline__ void mma_role(const Args& a, const Walk& walk, Bars& bar, uint32_t base, uint32_t tm,
+                                         volatile int* abort) {
   const uint32_t id_s = t5::idesc_bf16(128, 128, false), id_o = t5::idesc_bf16(128, 128, true);
-  Steps gen;
-  gen.walk = walk;
-  gen.T = gen.x = gen.nq = gen.i = gen.sub = 0;
-  gen.have = false;
-  Step pend[2];
-  bool live[2] = {false, false}, ok = true;
-  int np[2] = {0, 0};
+  // descriptors of buffer 0; a buffer is kStageB / 16 further in the address field
+  const uint64_t dq = t5::desc_sw128(base, 16, kGroupB), dk = t5::desc_sw128(base + kQBufs * kStageB, 16, kGroupB);
+  const uint64_t dv = t5::desc_sw128(base + kQBufs * kStageB, kHalfB, kGroupB);
+  Steps gen{walk, 0, 0, 0, 0u, 0u, false, false, false};
+  bool ok = true;
   auto wait = [&](uint64_t* b, uint32_t parity) {
     if (ok) ok = wait_or_abort(b, parity, abort, a.status);
   };
-  auto issue_s = [&](const Step& st) {
-    const int seq = 2 * st.T, ks = seq % kRing, qb = st.q & 1;
-    if (st.q_first) wait(&bar.qfull[qb], (uint32_t)(st.q >> 1) & 1u);
-    if (st.k_first) wait(&bar.full[ks], (uint32_t)(seq / kRing) & 1u);
+  auto issue_s = [&](uint32_t c, uint32_t slot) {
+    const uint32_t ks = c & step::kStage, qb = (c >> step::kQBuf) & 1u;
+    if (c & step::kQFirst) wait(&bar.qfull[qb], (c >> step::kQPar) & 1u);
+    if (c & step::kKFirst) wait(&bar.full[ks], (c >> step::kKPar) & 1u);
     if (!ok) return;
     t5::fence_after();
-    const uint32_t qa = base + qb * kStageB, ka = base + (kQBufs + ks) * kStageB;
+    const uint64_t qd = dq + qb * (kStageB >> 4), kd = dk + ks * (kStageB >> 4);
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) {  // 16 of the 128 dims each
-      const uint32_t off = (uint32_t)(kk >> 2) * kHalfB + (kk & 3) * 32;
-      t5::mma(tm + st.slot * 128, t5::desc_sw128(qa + off, 16, kGroupB), t5::desc_sw128(ka + off, 16, kGroupB), id_s,
-              kk > 0 ? 1u : 0u);
+      const uint32_t off = ((uint32_t)(kk >> 2) * kHalfB + (kk & 3) * 32) >> 4;
+      t5::mma(tm + slot * 128, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
     }
-    t5::commit(&bar.s[st.slot]);
-    if (st.k_last) t5::commit(&bar.empty[ks]);
-    if (st.q_last) t5::commit(&bar.qempty[qb]);
+    t5::commit(&bar.s[slot]);
+    if (c & step::kKLast) t5::commit(&bar.empty[ks]);
+    if (c & step::kQLast) t5::commit(&bar.qempty[qb]);
   };
-  auto issue_o = [&](const Step& st) {
-    const int seq = 2 * st.T + 1, vs = seq % kRing;
-    wait(&bar.p[st.slot], (uint32_t)(np[st.slot]++ & 1));
-    if (st.k_first) wait(&bar.full[vs], (uint32_t)(seq / kRing) & 1u);
+  auto issue_o = [&](uint32_t c, uint32_t slot, uint32_t p_par) {
+    const uint32_t vs = (c >> step::kVStage) & step::kStage;
+    if (c & step::kKFirst) wait(&bar.full[vs], (c >> step::kVPar) & 1u);
+    wait(&bar.p[slot], p_par);
     if (!ok) return;
     t5::fence_after();
-    const uint32_t va = base + (kQBufs + vs) * kStageB;
+    const uint64_t vd = dv + vs * (kStageB >> 4);
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)  // 16 of the 128 keys each
-      t5::mma_ts(tm + 256 + st.slot * 128, tm + st.slot * 128 + kk * 8, t5::desc_sw128(va + kk * 2 * kGroupB, kHalfB, kGroupB),
-                 id_o, (st.o_first && kk == 0) ? 0u : 1u);
-    if (st.k_last) t5::commit(&bar.empty[vs]);
-    if (st.o_last) t5::commit(&bar.o[st.slot]);
+      t5::mma_ts(tm + 256 + slot * 128, tm + slot * 128 + kk * 8, vd + ((kk * 2 * kGroupB) >> 4), id_o,
+                 kk > 0 ? 1u : ((c & step::kOFirst) ? 0u : 1u));
+    if (c & step::kKLast) t5::commit(&bar.empty[vs]);
+    if (c & step::kOLast) t5::commit(&bar.o[slot]);
   };
-  for (int u = 0; u < 2; ++u)
-    if (gen.next(a, pend[u])) {
-      live[u] = true;
-      issue_s(pend[u]);
-    }
-  for (int u = 0; ok && live[u]; u ^= 1) {
-    issue_o(pend[u]);
-    live[u] = ok && gen.next(a, pend[u]);
-    if (live[u]) issue_s(pend[u]);
+  uint32_t c0 = gen.next(a), c1 = 0u, p_par = 0u;
+  if (c0) issue_s(c0, 0);
+  if (c0) c1 = gen.next(a);
+  if (c1) issue_s(c1, 1);
+  while (ok && c0) {  // slots in turn: O of a step, then S of its slot's next one
+    uint32_t nx = gen.next(a);
+    issue_o(c0, 0, p_par);
+    if (ok && nx) issue_s(nx, 0);
+    c0 = nx;
+    if (!ok || !c1) break;
+    nx = gen.next(a);
+    issue_o(c1, 1, p_par);
+    if (ok && nx) issue_s(nx, 1);
+    c1 = nx;
+    p_par ^= 1u;
   }
   // the operands in shared memory and TMEM outlive every MMA issued
   t5::commit(&bar.drain);
@@ -673,11 +684,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
   }
   const uint32_t tm = s_tmem;
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     softmax_role(a, walk, bar, tm, masks, &s_abort);
   } else {
-    // 2 x 128 x 200 + 2 x 128 x 56 = 65,536 registers, what 512 threads of 128 were launched with
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    // 2 x 128 x 192 + 2 x 128 x 64 = 65,536 registers, what 512 threads of 128 were launched with
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp < 12)
       gather_role(a, &tk, &tv, walk, bar, base, gbase, reinterpret_cast<uint16_t*>(masks), &s_abort);
     else if (warp == 12 && lane == 0)
@@ -691,86 +702,105 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
   }
 }
 
-// Joins the partials of 32 query rows of one KV head, 32 of the 128 dims a CTA: lane = row,
-// warp = 4 dims, so every partial load is a coalesced float4.  Two passes: the row's
-// maximum over its partials, then the weighted sums.
-__global__ void __launch_bounds__(256) prefix_merge_kernel(const Args a) {
-  __shared__ float s_m[8][32];
+// Joins the partials of 32 query rows of one KV head, kMergeDims of the 128 dims a CTA:
+// lane = row, warp = (4 dims, one of kMergeParts shares of the partials), so every load of
+// a partial is a coalesced float4 and a thread's loads are independent.  Two passes: the
+// row's maximum over its partials, then the weighted sums, joined in a fixed order.
+constexpr int kMergeParts = 4;
+constexpr int kMergeDims = 16;
+constexpr int kMergeWarps = kMergeParts * kMergeDims / 4;
+
+__global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Args a) {
+  __shared__ float s_m[kMergeWarps][32];
+  __shared__ float4 s_o[kMergeWarps][32];
+  __shared__ float s_l[kMergeWarps][32];
   pdl_release();
-  pdl_wait();
   const Plan& pl = a.pl;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int blocks = (pl.rows + 31) / 32;
   const int h = blockIdx.x / blocks, row = (blockIdx.x - h * blocks) * 32 + lane;
   const bool live = row < pl.rows;
   const int b = live ? row / a.G : 0, g = row - b * a.G;
+  // the prefix's partials of this row: gangs c0 .. c0 + nc - 1 of its unit
+  const int pair = row / (2 * kTile), pg = pair / pl.gang, member = pair - pg * pl.gang;
+  const int up = h * pl.groups + pg;
+  const bool two = pl.rows - pair * 2 * kTile > kTile;
+  const int r_in = row & (kTile - 1);
+  const long long tp = (long long)a.H * pl.groups * pl.ntp, u0 = (long long)up * pl.ntp;
+  int c0 = 0, np = 0;
+  if (pl.ntp > 0) {
+    c0 = (int)(((u0 + 1) * pl.gangs - 1) / tp);
+    np = (int)(((u0 + pl.ntp) * pl.gangs - 1) / tp) - c0 + 1;
+    if (!two) np *= 2;  // both slots' partials are of this row tile
+  }
+  // partial i: (gang c0 + i, this row tile), or (gang c0 + i / 2, slot i % 2)
+  const long long first_p = 2 * ((long long)(c0 + up) * pl.gang + member) + (two ? (row / kTile) & 1 : 0);
+  const long long step_p = 2 * pl.gang;
+  auto p_at = [&](int i) { return two ? first_p + i * step_p : first_p + (i >> 1) * step_p + (i & 1); };
+  pdl_wait();
   int L = live ? a.seq_lens[b] : 0;
   if (L < 0 || L > a.max_len || (L > 0 && L < a.P)) {
     if (blockIdx.y == 0 && warp == 0) flag(a.status, SKV_DEV_BAD_LENGTH);
     L = L > a.max_len ? a.max_len : 0;
   }
   const bool on = L > 0;
-  // the prefix's partials of this row: gangs c0..c1 of its unit
-  const int pair = row / (2 * kTile), pg = pair / pl.gang, member = pair - pg * pl.gang;
-  const int up = h * pl.groups + pg;
-  const bool two = pl.rows - pair * 2 * kTile > kTile;
-  const int r_in = row & (kTile - 1), sub0 = two ? (row / kTile) & 1 : 0, nsub = two ? 1 : 2;
-  const long long tp = (long long)a.H * pl.groups * pl.ntp, u0 = (long long)up * pl.ntp, u1 = u0 + pl.ntp;
-  int c0 = 0, c1 = -1;
-  if (pl.ntp > 0) {
-    c0 = (int)(((u0 + 1) * pl.gangs - 1) / tp);
-    c1 = (int)((u1 * pl.gangs - 1) / tp);
-  }
-  const int nc = c1 - c0 + 1;
-  // the tail's: CTAs f..e of its unit
+  if (!on) np = 0;
+  // the tail's: 2 (e - f + 1) consecutive ones of its unit
   const int unit = h * a.B + b;
-  int f = 0, e = -1;
+  int nt = 0;
+  long long first_t = 0;
   if (on && L > a.P) {
-    f = a.first[unit];
-    e = a.last[unit];
-    if (f < 0 || e >= kCtas || f > e) f = 0, e = -1;  // never written (an aborted launch)
-  }
-  auto p_at = [&](int c, int u) { return 2 * ((long long)(c + up) * pl.gang + member) + sub0 + u; };
-  auto s_at = [&](int c, int u) { return 2 * ((long long)c + unit) + u; };
-  float m = -INFINITY;
-  if (on) {
-    for (int i = warp; i < nc * nsub; i += 8) {
-      const int c = c0 + i / nsub;
-      m = fmaxf(m, a.pml[p_at(c, i % nsub) * pl.rp * 2 + r_in]);
+    const int f = a.first[unit], e = a.last[unit];
+    if (f >= 0 && e < kCtas && f <= e) {  // else never written: an aborted launch
+      nt = 2 * (e - f + 1);
+      first_t = 2 * ((long long)f + unit);
     }
-    for (int i = warp; i < 2 * (e - f + 1); i += 8) m = fmaxf(m, a.sml[s_at(f + i / 2, i % 2) * a.G * 2 + g]);
   }
+  float m = -INFINITY;
+  for (int i = warp; i < np; i += kMergeWarps) m = fmaxf(m, a.pml[p_at(i) * pl.rp * 2 + r_in]);
+  for (int i = warp; i < nt; i += kMergeWarps) m = fmaxf(m, a.sml[(first_t + i) * a.G * 2 + g]);
   s_m[warp][lane] = m;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, s_m[i][lane]);
-  const int d4 = blockIdx.y * 8 + warp;
+  for (int i = 0; i < kMergeWarps; ++i) m = fmaxf(m, s_m[i][lane]);
+  const int part = warp / (kMergeDims / 4), d4 = blockIdx.y * (kMergeDims / 4) + warp % (kMergeDims / 4);
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   auto add = [&](const float* ml, const float* po, int rp, int r) {
     const float mp = ml[r], lp = ml[rp + r];
+    const float4 v = *reinterpret_cast<const float4*>(po + ((size_t)d4 * rp + r) * 4);
     if (mp == -INFINITY) return;  // an empty partial: its O was never written
     const float w = exp2f(mp - m);
-    const float4 v = *reinterpret_cast<const float4*>(po + ((size_t)d4 * rp + r) * 4);
     l = fmaf(w, lp, l);
     o.x = fmaf(w, v.x, o.x);
     o.y = fmaf(w, v.y, o.y);
     o.z = fmaf(w, v.z, o.z);
     o.w = fmaf(w, v.w, o.w);
   };
-  if (on) {
 #pragma unroll 4
-    for (int i = 0; i < nc * nsub; ++i) {
-      const int c = c0 + i / nsub;
-      const long long at = p_at(c, i % nsub) * pl.rp;
-      add(a.pml + at * 2, a.po + at * kD, pl.rp, r_in);
-    }
-    for (int i = 0; i < 2 * (e - f + 1); ++i) {
-      const long long at = s_at(f + i / 2, i % 2) * a.G;
-      add(a.sml + at * 2, a.so + at * kD, a.G, g);
-    }
+  for (int i = part; i < np; i += kMergeParts) {
+    const long long at = p_at(i) * pl.rp;
+    add(a.pml + at * 2, a.po + at * kD, pl.rp, r_in);
   }
-  if (!live) return;
+#pragma unroll 2
+  for (int i = part; i < nt; i += kMergeParts) {
+    const long long at = (first_t + i) * a.G;
+    add(a.sml + at * 2, a.so + at * kD, a.G, g);
+  }
+  s_o[warp][lane] = o;
+  s_l[warp][lane] = l;
+  __syncthreads();
+  if (part > 0 || !live) return;
+#pragma unroll
+  for (int i = 1; i < kMergeParts; ++i) {
+    const int from = i * (kMergeDims / 4) + warp;
+    const float4 v = s_o[from][lane];
+    l += s_l[from][lane];
+    o.x += v.x;
+    o.y += v.y;
+    o.z += v.z;
+    o.w += v.w;
+  }
   const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // NaN stays NaN; no key at all: 0
   const size_t hq = (size_t)b * a.Hq + (size_t)h * a.G + g;
   uint2 r;
@@ -857,7 +887,8 @@ skv_status launch_prefix_attn(const skv_problem& p, const void* q, const PoolVie
     return SKV_ERR_CUDA;
   SKV_LAUNCH_CHECK();
   const long long blocks = (long long)((a.pl.rows + 31) / 32) * a.H;
-  if (launch_dependent(prefix_merge_kernel, dim3((unsigned)blocks, 4), dim3(256), 0, st, 1, a) != cudaSuccess)
+  if (launch_dependent(prefix_merge_kernel, dim3((unsigned)blocks, kD / kMergeDims),
+                       dim3(kMergeWarps * 32), 0, st, 1, a) != cudaSuccess)
     return SKV_ERR_CUDA;
   SKV_LAUNCH_CHECK();
   return SKV_OK;
