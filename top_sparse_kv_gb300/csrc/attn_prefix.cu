@@ -7,14 +7,16 @@
 // products on the tcgen05 tensor cores, and the prefix crosses HBM once; a tail [P, L_b)
 // meets the G rows of its own request the same way.  Both are cut into tiles of 128 keys.
 //
-// prefix_attn_kernel, one persistent CTA an SM, 16 warps in four roles:
+// prefix_attn_kernel, one persistent CTA an SM, 12 warps in four roles:
 //   warps 0-3, 4-7   softmax of slot 0 / slot 1 (a thread a query row)
-//   warps 8-11       gather: K and V through the table into a ring of 32 KB stages, in the
+//   warps 8, 9       gather: K and V through the table into a ring of 32 KB stages, in the
 //                    128-byte-swizzled layout that the MMA reads: 16 keys of a block by one
 //                    4 KB TMA copy; keys at a history's edge, in the host pool (over UVA) or
 //                    of blocks that 16 does not divide row by row, 16-byte cp.async with
 //                    zeros for what is not attended
-//   warp 12          one thread issues every MMA
+//   warp 10          query rows, by cp.async
+//   warp 11          issues every MMA (converged, one elected lane: the operands' uniform
+//                    registers then cost no per-lane serialisation; 100 cycles an MMA before)
 // A *step* is one (128 query rows, 128 keys) tile: S = Q K^T (M128 N128, fp32 in TMEM),
 // P = 2^(z - m) in bf16 over S's own columns, O += P V (A from TMEM, V read MN-major).
 // Steps alternate between two slots of TMEM (S 128 + O 128 columns each), so that one
@@ -41,7 +43,9 @@ namespace {
 
 namespace px {
 constexpr int kCtas = 152;             // one CTA an SM of a GB300 (a function of the problem alone: sizes the workspace)
-constexpr int kThreads = 512;
+constexpr int kThreads = 384;
+constexpr int kGatherWarps = 2;
+constexpr int kChunks = 8 / kGatherWarps;  // chunks of a tile a gather warp copies
 constexpr int kTile = 128;             // keys a tile, query rows a tile
 constexpr int kStageB = kTile * 256;   // a K, V or Q tile, 32 KB: [group of 8 rows][half of the dims][8 rows][128 bytes]
 constexpr int kGroupB = 2048;          // a group of 8 rows
@@ -82,6 +86,7 @@ struct Args {
   const int32_t *ptable, *seq_lens;
   int B, H, Hq, G, P, max_len, bs;
   int tma;             // blocks are whole chunks of 16 keys
+  int shift;           // log2 of the block size, -1: not a power of two
   float scale_log2;
   Plan pl;
   float *po, *pml;     // prefix partials: [(gang + unit) * members + member][2][...]
@@ -188,12 +193,12 @@ struct Bars {
 // ---------------------------------------------------------------------------- gather warps
 // A gather warp's copies: TMA copies complete on their stage's barrier by themselves; rows
 // copied by cp.async are announced there by the warp once they have landed.  Announcements
-// are put off (the copies keep flying) until a buffer is waited for: what frees it may need
+// are put off (the copies keep flying) until a stage is waited for: what frees it may need
 // the tiles in flight, so the oldest are announced, one at a time, until it is free.
 struct Gather {
   const Args& a;
   volatile int* abort;
-  uint64_t* pend[kRing + kQBufs];  // barriers of unannounced copy groups, oldest first
+  uint64_t* pend[kRing];  // barriers of unannounced copy groups, oldest first
   int n;
   bool ok;
 
@@ -203,22 +208,20 @@ struct Gather {
       case 2: cp_async_wait<1>(); break;
       case 3: cp_async_wait<2>(); break;
       case 4: cp_async_wait<3>(); break;
-      case 5: cp_async_wait<4>(); break;
-      case 6: cp_async_wait<5>(); break;
-      default: cp_async_wait<6>(); break;
+      default: cp_async_wait<4>(); break;
     }
     fence_proxy_async_smem();
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(pend[0]);
     --n;
 #pragma unroll
-    for (int i = 0; i + 1 < kRing + kQBufs; ++i) pend[i] = pend[i + 1];
+    for (int i = 0; i + 1 < kRing; ++i) pend[i] = pend[i + 1];
   }
   __device__ __forceinline__ void commit(uint64_t* b) {
     cp_async_commit();
-    if (n == kRing + kQBufs) announce_oldest();
+    if (n == kRing) announce_oldest();
 #pragma unroll
-    for (int i = 0; i < kRing + kQBufs; ++i)
+    for (int i = 0; i < kRing; ++i)
       if (i == n) pend[i] = b;
     ++n;
   }
@@ -238,12 +241,17 @@ struct Gather {
   }
 };
 
+__device__ __forceinline__ int block_of(const Args& a, int t) { return a.shift >= 0 ? t >> a.shift : t / a.bs; }
+__device__ __forceinline__ int in_block(const Args& a, int t) {
+  return a.shift >= 0 ? t & (a.bs - 1) : t % a.bs;
+}
+
 // Reference of position t's row: its index in its pool, bit 62 for the host pool, -1 for none.
 __device__ __forceinline__ long long row_ref(const Args& a, int h, int e, int t) {
-  if (e >= 0) return e < a.pool.n_gpu ? ((long long)e * a.H + h) * a.bs + t % a.bs : -1;
+  if (e >= 0) return e < a.pool.n_gpu ? ((long long)e * a.H + h) * a.bs + in_block(a, t) : -1;
   const long long hb = -(long long)e - 1;
   if (a.pool.host_k == nullptr || hb >= a.pool.n_host) return -1;
-  return tc::kHostBit | ((hb * a.H + h) * a.bs + t % a.bs);
+  return tc::kHostBit | ((hb * a.H + h) * a.bs + in_block(a, t));
 }
 
 // 16 keys' rows of 256 bytes of a pool viewed as [rows / 8][2 halves][8 rows][64 dims]
@@ -263,98 +271,94 @@ __device__ __forceinline__ void gather_role(const Args& a, const CUtensorMap* tk
   const int r16 = lane >> 1, half = lane & 1;  // cp.async: a lane copies half a row
   const uint32_t row_off = (uint32_t)((r16 >> 3) * kGroupB + half * kHalfB + (r16 & 7) * 128);
   Seg s;
-  int T = 0, nq = 0;
+  int T = 0;
+  uint32_t st = 0, par = 1;  // ring stage, parity of its free phase
   while (g.ok && walk.next(a, s)) {
     if (s.tail && w == 0 && lane == 0) {
       if (s.begins) a.first[s.h * a.B + s.b] = walk.scta;
       if (s.ends) a.last[s.h * a.B + s.b] = walk.scta;
     }
-    // query rows: this warp copies the chunks w and w + 4 of 16 rows
-    for (int u = 0; u < (s.n1 > 0 ? 2 : 1); ++u, ++nq) {
-      const int buf = nq & 1;
-      g.wait_free(&bar.qempty[buf], (uint32_t)((nq >> 1) & 1) ^ 1u);
-      if (!g.ok) break;
-      const int live = u ? s.n1 : s.n0;
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const int r = kChunk * (w + 4 * v) + r16;
-        if (r < live) {
-          const int row = s.row0 + u * kTile + r, b = row / a.G, gg = row - b * a.G;
-          const unsigned char* src = a.q + (((size_t)b * a.Hq + (size_t)s.h * a.G + gg) * 2 + half) * 128;
-          unsigned char* dst = gbase + buf * kStageB + (w + 4 * v) * 2 * kGroupB + row_off;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) cp_async16(dst + ((c ^ (r16 & 7)) << 4), src + c * 16);
-        }
-      }
-      g.commit(&bar.qfull[buf]);
-    }
     const int32_t* table = s.tail ? a.pool.table + (size_t)s.b * a.pool.stride : a.ptable;
+    // lane v < kChunks: the table entry of chunk w * kChunks + v, where it is whole (-1: row by row)
+    auto entry = [&](int t0) {
+      const int t = t0 + kChunk * (w * kChunks + lane);
+      return a.tma && lane < kChunks && t >= s.lo && t + kChunk <= s.hi ? table[block_of(a, t)] : -1;
+    };
+    int e = entry(s.t0);
     for (int i = 0; g.ok && i < s.n; ++i, ++T) {
       const int t0 = s.t0 + i * kTile;
-      // the warp's two chunks: a whole block part of the GPU pool by TMA, else row by row
-      int group[2];
-      long long ref[2];
-      uint32_t valid[2];
+      // this warp's chunks: part of a block of the GPU pool by TMA, else row by row
+      int mine = -1;  // lane v: chunk v's group of 8 rows
+      if (e >= 0 && e < a.pool.n_gpu)
+        mine = (int)((((long long)e * a.H + s.h) * a.bs + in_block(a, t0 + kChunk * (w * kChunks + lane))) >> 3);
+      const uint32_t whole = __ballot_sync(0xffffffffu, mine >= 0);
+      if (i + 1 < s.n) e = entry(t0 + kTile);
+      int group[kChunks];
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const int tc0 = t0 + kChunk * (w + 4 * v);
-        group[v] = -1;
+      for (int v = 0; v < kChunks; ++v) group[v] = __shfl_sync(0xffffffffu, mine, v);
+      const bool rows = whole != (1u << kChunks) - 1u;
+      const uint32_t bytes = __popc(whole) * 2 * kGroupB;
+      long long ref[kChunks];
+      uint32_t valid[kChunks];
+#pragma unroll
+      for (int v = 0; v < kChunks; ++v) {
         ref[v] = -1;
         valid[v] = 0xffffu;
-        if (a.tma && tc0 >= s.lo && tc0 + kChunk <= s.hi) {
-          const int e = table[tc0 / a.bs];
-          if (e >= 0 && e < a.pool.n_gpu) group[v] = (int)((((long long)e * a.H + s.h) * a.bs + tc0 % a.bs) >> 3);
-        }
-        if (group[v] < 0) {
-          const int t = tc0 + r16;
-          if (t >= s.lo && t < s.hi) {
-            ref[v] = row_ref(a, s.h, table[t / a.bs], t);
-            if (ref[v] < 0) flag(a.status, SKV_DEV_BAD_SLOT);
-          }
-          const int mine = __shfl_sync(0xffffffffu, (int)(ref[v] >= 0), (2 * lane) & 31);  // lane r < 16: row r
-          valid[v] = __ballot_sync(0xffffffffu, mine && lane < kChunk);
-        }
       }
-      const bool rows = group[0] < 0 || group[1] < 0;
-      const uint32_t bytes = ((group[0] >= 0) + (group[1] >= 0)) * 2 * kGroupB;
+      if (rows) {
+#pragma unroll
+        for (int v = 0; v < kChunks; ++v)
+          if (group[v] < 0) {
+            const int t = t0 + kChunk * (w * kChunks + v) + r16;
+            if (t >= s.lo && t < s.hi) {
+              ref[v] = row_ref(a, s.h, table[block_of(a, t)], t);
+              if (ref[v] < 0) flag(a.status, SKV_DEV_BAD_SLOT);
+            }
+            const int live = __shfl_sync(0xffffffffu, (int)(ref[v] >= 0), (2 * lane) & 31);  // lane r < 16: row r
+            valid[v] = __ballot_sync(0xffffffffu, live && lane < kChunk);
+          }
+      }
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
-        const int seq = 2 * T + kv, st = seq % kRing;
-        g.wait_free(&bar.empty[st], (uint32_t)((seq / kRing) & 1) ^ 1u);
+        g.wait_free(&bar.empty[st], par);
         if (!g.ok) break;
         if (kv == 0 && lane == 0) {
-          masks[(T % kMasks) * 8 + w] = (uint16_t)valid[0];
-          masks[(T % kMasks) * 8 + w + 4] = (uint16_t)valid[1];
+#pragma unroll
+          for (int v = 0; v < kChunks; ++v) masks[(T % kMasks) * 8 + w * kChunks + v] = (uint16_t)valid[v];
           mbar_arrive(&bar.mask[T % kMasks]);
         }
         uint64_t* full = &bar.full[st];
-        const uint32_t off = (uint32_t)((kQBufs + st) * kStageB);
-        if (lane == 0 && bytes > 0) {
+        const uint32_t off = (kQBufs + st) * kStageB + w * kChunks * 2 * kGroupB;
+        if (bytes > 0 && t5::elect_one()) {
           if (rows)
             mbar_expect_tx(full, bytes);  // the arrival follows when the rows have landed
           else
             mbar_arrive_expect_tx(full, bytes);
 #pragma unroll
-          for (int v = 0; v < 2; ++v)
-            if (group[v] >= 0) tma_chunk(base + off + (w + 4 * v) * 2 * kGroupB, kv ? tv : tk, group[v], full);
+          for (int v = 0; v < kChunks; ++v)
+            if (group[v] >= 0) tma_chunk(base + off + v * 2 * kGroupB, kv ? tv : tk, group[v], full);
         }
         if (rows) {
           __syncwarp();  // the bytes are expected before the arrival
           const unsigned char* gp = (const unsigned char*)(kv ? a.pool.gpu_v : a.pool.gpu_k);
           const unsigned char* hp = (const unsigned char*)(kv ? a.pool.host_v : a.pool.host_k);
 #pragma unroll
-          for (int v = 0; v < 2; ++v)
+          for (int v = 0; v < kChunks; ++v)
             if (group[v] < 0) {
               const bool live = ref[v] >= 0;
               const unsigned char* src =
                   live ? ((ref[v] & tc::kHostBit) ? hp : gp) + (size_t)(ref[v] & tc::kRefRowMask) * tc::kRowBytes + half * 128
                        : gp;
-              unsigned char* dst = gbase + off + (w + 4 * v) * 2 * kGroupB + row_off;
+              unsigned char* dst = gbase + off + v * 2 * kGroupB + row_off;
 #pragma unroll
               for (int c = 0; c < 8; ++c)
                 tc::cp_async16_zfill(dst + ((c ^ (r16 & 7)) << 4), live ? src + c * 16 : src, live);
             }
           g.commit(full);
+        }
+        if (++st == kRing) {
+          st = 0;
+          par ^= 1u;
         }
       }
     }
@@ -362,8 +366,41 @@ __device__ __forceinline__ void gather_role(const Args& a, const CUtensorMap* tk
   g.flush();
 }
 
-// ---------------------------------------------------------------------------- MMA thread
-// A step as the issuing thread needs it, one word: ring stages and parities, first and last uses.
+// ---------------------------------------------------------------------------- query warp
+__device__ __forceinline__ void query_role(const Args& a, Walk walk, Bars& bar, unsigned char* gbase,
+                                           volatile int* abort) {
+  const int lane = threadIdx.x & 31;
+  const int r16 = lane >> 1, half = lane & 1;
+  const uint32_t row_off = (uint32_t)((r16 >> 3) * kGroupB + half * kHalfB + (r16 & 7) * 128);
+  Seg s;
+  int nq = 0;
+  while (walk.next(a, s)) {
+    for (int u = 0; u < (s.n1 > 0 ? 2 : 1); ++u, ++nq) {
+      const int buf = nq & 1;
+      bool ok = wait_or_abort(&bar.qempty[buf], (uint32_t)((nq >> 1) & 1) ^ 1u, abort, a.status);
+      if (__any_sync(0xffffffffu, !ok)) return;
+      const int live = u ? s.n1 : s.n0;
+      for (int v = 0; v * kChunk < live; ++v) {
+        const int r = kChunk * v + r16;
+        if (r < live) {
+          const int row = s.row0 + u * kTile + r, b = row / a.G, gg = row - b * a.G;
+          const unsigned char* src = a.q + (((size_t)b * a.Hq + (size_t)s.h * a.G + gg) * 2 + half) * 128;
+          unsigned char* dst = gbase + buf * kStageB + v * 2 * kGroupB + row_off;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) cp_async16(dst + ((c ^ (r16 & 7)) << 4), src + c * 16);
+        }
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.qfull[buf]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------- MMA warp
+// A step as the issuing warp needs it, one word: ring stages and parities, first and last uses.
 namespace step {
 constexpr uint32_t kStage = 7u, kKPar = 3, kVStage = 4, kVPar = 7, kQBuf = 8, kQPar = 9;
 constexpr uint32_t kKFirst = 1u << 10, kKLast = 1u << 11, kQFirst = 1u << 12, kQLast = 1u << 13, kOFirst = 1u << 14,
@@ -421,6 +458,7 @@ __device__ __forceinline__ void mma_role(const Args& a, const Walk& walk, Bars& 
   bool ok = true;
   auto wait = [&](uint64_t* b, uint32_t parity) {
     if (ok) ok = wait_or_abort(b, parity, abort, a.status);
+    ok = __all_sync(0xffffffffu, ok);
   };
   auto issue_s = [&](uint32_t c, uint32_t slot) {
     const uint32_t ks = c & step::kStage, qb = (c >> step::kQBuf) & 1u;
@@ -429,6 +467,7 @@ __device__ __forceinline__ void mma_role(const Args& a, const Walk& walk, Bars& 
     if (!ok) return;
     t5::fence_after();
     const uint64_t qd = dq + qb * (kStageB >> 4), kd = dk + ks * (kStageB >> 4);
+    if (t5::elect_one()) {
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) {  // 16 of the 128 dims each
       const uint32_t off = ((uint32_t)(kk >> 2) * kHalfB + (kk & 3) * 32) >> 4;
@@ -437,6 +476,7 @@ __device__ __forceinline__ void mma_role(const Args& a, const Walk& walk, Bars& 
     t5::commit(&bar.s[slot]);
     if (c & step::kKLast) t5::commit(&bar.empty[ks]);
     if (c & step::kQLast) t5::commit(&bar.qempty[qb]);
+    }
   };
   auto issue_o = [&](uint32_t c, uint32_t slot, uint32_t p_par) {
     const uint32_t vs = (c >> step::kVStage) & step::kStage;
@@ -445,12 +485,14 @@ __device__ __forceinline__ void mma_role(const Args& a, const Walk& walk, Bars& 
     if (!ok) return;
     t5::fence_after();
     const uint64_t vd = dv + vs * (kStageB >> 4);
+    if (t5::elect_one()) {
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)  // 16 of the 128 keys each
       t5::mma_ts(tm + 256 + slot * 128, tm + slot * 128 + kk * 8, vd + ((kk * 2 * kGroupB) >> 4), id_o,
                  kk > 0 ? 1u : ((c & step::kOFirst) ? 0u : 1u));
     if (c & step::kKLast) t5::commit(&bar.empty[vs]);
     if (c & step::kOLast) t5::commit(&bar.o[slot]);
+    }
   };
   uint32_t c0 = gen.next(a), c1 = 0u, p_par = 0u;
   if (c0) issue_s(c0, 0);
@@ -469,7 +511,8 @@ __device__ __forceinline__ void mma_role(const Args& a, const Walk& walk, Bars& 
     p_par ^= 1u;
   }
   // the operands in shared memory and TMEM outlive every MMA issued
-  t5::commit(&bar.drain);
+  __syncwarp();
+  if (t5::elect_one()) t5::commit(&bar.drain);
   mbar_wait_bounded(&bar.drain, 0u);
 }
 
@@ -602,14 +645,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
   unsigned char* gbase = smem_raw + (base - raw);
   if (t == 0) {
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(&bar.full[i], 4);
+      mbar_init(&bar.full[i], kGatherWarps);
       mbar_init(&bar.empty[i], 1);
     }
     for (int i = 0; i < kQBufs; ++i) {
-      mbar_init(&bar.qfull[i], 4);
+      mbar_init(&bar.qfull[i], 1);
       mbar_init(&bar.qempty[i], 1);
     }
-    for (int i = 0; i < kMasks; ++i) mbar_init(&bar.mask[i], 4);
+    for (int i = 0; i < kMasks; ++i) mbar_init(&bar.mask[i], kGatherWarps);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.s[i], 1);
       mbar_init(&bar.p[i], 128);
@@ -683,15 +726,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
     walk.stile = s_at[2];
   }
   const uint32_t tm = s_tmem;
+  // 2 x 128 x 208 + 128 x 88 = 64,512 registers, what 384 threads of 168 were launched with
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     softmax_role(a, walk, bar, tm, masks, &s_abort);
   } else {
-    // 2 x 128 x 192 + 2 x 128 x 64 = 65,536 registers, what 512 threads of 128 were launched with
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp < 12)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp < 8 + kGatherWarps)
       gather_role(a, &tk, &tv, walk, bar, base, gbase, reinterpret_cast<uint16_t*>(masks), &s_abort);
-    else if (warp == 12 && lane == 0)
+    else if (warp == 10)
+      query_role(a, walk, bar, gbase, &s_abort);
+    else
       mma_role(a, walk, bar, base, tm, &s_abort);
   }
   t5::fence_before();
@@ -881,6 +926,9 @@ skv_status launch_prefix_attn(const skv_problem& p, const void* q, const PoolVie
   if (prep != SKV_OK) return prep;
   CUtensorMap tk, tv;
   const long long rows = pool.n_gpu * p.n_kv_heads * p.block_size;
+  a.shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (p.block_size == 1 << i) a.shift = i;
   a.tma = p.block_size % kChunk == 0 && rows > 0 && rows / 8 < (1LL << 31);
   if (a.tma && (!encode_pool(&tk, pool.gpu_k, rows) || !encode_pool(&tv, pool.gpu_v, rows))) return SKV_ERR_CUDA;
   if (launch_dependent(prefix_attn_kernel, dim3(kCtas), dim3(px::kThreads), px::kSmem, st, 1, tk, tv, a) != cudaSuccess)
