@@ -9,12 +9,14 @@
 //
 // prefix_attn_kernel, one persistent CTA an SM, 12 warps in four roles:
 //   warps 0-3, 4-7   softmax of slot 0 / slot 1 (a thread a query row)
-//   warps 8, 9       gather: K and V through the table into a ring of 32 KB stages, in the
-//                    128-byte-swizzled layout that the MMA reads: 16 keys of a block by one
-//                    4 KB TMA copy; keys at a history's edge, in the host pool (over UVA) or
-//                    of blocks that 16 does not divide row by row, 16-byte cp.async with
-//                    zeros for what is not attended
-//   warp 10          query rows, by cp.async
+//   warp 8           16 keys of a block of the GPU pool by one 4 KB TMA copy, into a ring of
+//                    32 KB K / V stages in the 128-byte-swizzled layout that the MMA reads
+//   warp 9           every other key -- at a history's edge, in the host pool (over UVA), of
+//                    blocks that 16 does not divide -- row by row, 16-byte cp.async with
+//                    zeros for what is not attended; and the key masks.  A warp of its own,
+//                    so that waiting for its rows to land holds back no TMA copy.
+//   warp 10          cuts the CTA's share into segments, published in a ring for the other
+//                    roles, and copies their query rows, by cp.async
 //   warp 11          issues every MMA (converged, one elected lane: the operands' uniform
 //                    registers then cost no per-lane serialisation; 100 cycles an MMA before)
 // A *step* is one (128 query rows, 128 keys) tile: S = Q K^T (M128 N128, fp32 in TMEM),
@@ -44,20 +46,21 @@ namespace {
 namespace px {
 constexpr int kCtas = 152;             // one CTA an SM of a GB300 (a function of the problem alone: sizes the workspace)
 constexpr int kThreads = 384;
-constexpr int kGatherWarps = 2;
-constexpr int kChunks = 8 / kGatherWarps;  // chunks of a tile a gather warp copies
 constexpr int kTile = 128;             // keys a tile, query rows a tile
 constexpr int kStageB = kTile * 256;   // a K, V or Q tile, 32 KB: [group of 8 rows][half of the dims][8 rows][128 bytes]
 constexpr int kGroupB = 2048;          // a group of 8 rows
 constexpr int kHalfB = 1024;           // one half of its dims
 constexpr int kChunk = 16;             // keys of one TMA copy
+constexpr int kChunks = kTile / kChunk;
 constexpr int kRing = 5;               // K / V stages
 constexpr int kQBufs = 2;
 constexpr int kMasks = 8;              // key masks of the last tiles
+constexpr int kSegs = 8;               // segments published ahead
+constexpr int kSegReaders = 11;        // warps that read them: 8 softmax, TMA, rows, MMA
 constexpr int kSmem = (kQBufs + kRing) * kStageB + 1024;
 constexpr int kMaxGang = 4;            // pairs of row tiles that read the same keys together
 constexpr float kGrow = 8.f;           // log2 growth of a row's maximum that renews it
-constexpr uint32_t kTmemCols = 512;    // S0 S1 O0 O1, 128 columns each
+constexpr uint32_t kTmemCols = 512;    // S0 S1 O0 O1, 128 columns each; P over the first 64 columns of S
 
 // How the row tiles and the CTAs are arranged (host and device alike)
 struct Plan {
@@ -109,21 +112,73 @@ __device__ __forceinline__ int tail_tiles(const Args& a, int end) {
   return end > a.P ? (end - tail_base(a.P) + kTile - 1) / kTile : 0;
 }
 
-struct Seg {
-  int tail, h, b;      // a tail's segment (of request b), or the prefix's
-  int row0, n0, n1;    // first query row; live rows of the two row tiles (n1 = 0: one tile)
-  int t0, n, lo, hi;   // first key position, key tiles, the valid positions [lo, hi)
-  bool begins, ends;   // the tail's first / last segment
-  long long part;      // the partial's index
+struct alignas(16) Seg {
+  const int32_t* table;  // the positions' table row
+  long long part;        // the partial's index
+  int n;                 // key tiles; 0: the CTA's share is done
+  int t0, lo, hi;        // first key position, the valid positions [lo, hi)
+  int h, row0, n0, n1;   // KV head; first query row; live rows of the two row tiles (n1 = 0: one tile)
+  int tail;              // a tail's segment, or the prefix's
 };
 
-// A CTA's segments in order, the same sequence for every role.
+// A CTA's segments in order (the walker warp's: every lane holds the same).
 struct Walk {
   long long p0, p1;          // prefix tiles left: flattened (head, group, tile)
   long long srem;            // tail tiles left
   int scta;                  // the CTA's place among those with tail tiles
   int sh, sb, stile;         // the next tail tile
-  __device__ bool next(const Args& a, Seg& s) {
+  bool scanned;
+  __device__ __forceinline__ void init(const Args& a) {
+    const Plan& pl = a.pl;
+    const int gang = blockIdx.x / pl.gang;
+    const long long tp = (long long)a.H * pl.groups * pl.ntp;
+    p0 = gang < pl.gangs ? gang * tp / pl.gangs : 0;
+    p1 = gang < pl.gangs ? (gang + 1) * tp / pl.gangs : 0;
+    srem = 0;
+    scta = kCtas - 1 - (int)blockIdx.x;  // the last CTAs take the tails (the first the prefix, where there are few tiles)
+    sh = sb = stile = 0;
+    scanned = false;
+  }
+  // this CTA's range of the tails' tiles; its first tile by a scan of the requests' tile counts
+  __device__ __forceinline__ void scan(const Args& a) {
+    scanned = true;
+    if (a.P >= a.max_len) return;
+    const int lane = threadIdx.x & 31;
+    const int per = (a.B + 31) / 32, b0 = lane * per < a.B ? lane * per : a.B, b1 = b0 + per < a.B ? b0 + per : a.B;
+    long long mine = 0;
+#pragma unroll 4
+    for (int b = b0; b < b1; ++b) mine += tail_tiles(a, tail_end(a, b));
+    long long incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += o;
+    }
+    const long long total = __shfl_sync(0xffffffffu, incl, 31), ts = total * a.H;
+    const int sn = ts < kCtas ? (int)ts : kCtas;
+    if (scta >= sn) return;
+    const long long s0 = scta * ts / sn;
+    srem = (scta + 1) * ts / sn - s0;
+    const long long at = s0 % total;
+    long long lo = incl - mine;
+    int fb = 0, ft = 0;
+    const bool here = at >= lo && at < incl;
+    if (here)
+      for (int b = b0; b < b1; ++b) {
+        const int n = tail_tiles(a, tail_end(a, b));
+        if (at < lo + n) {
+          fb = b;
+          ft = (int)(at - lo);
+          break;
+        }
+        lo += n;
+      }
+    const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+    sh = (int)(s0 / total);
+    sb = __shfl_sync(0xffffffffu, fb, src);
+    stile = __shfl_sync(0xffffffffu, ft, src);
+  }
+  __device__ __forceinline__ void next(const Args& a, Seg& s) {
     const Plan& pl = a.pl;
     const int c = blockIdx.x / pl.gang, member = blockIdx.x - c * pl.gang;
     while (p0 < p1) {
@@ -133,21 +188,21 @@ struct Walk {
       p0 += n;
       const int h = up / pl.groups, pair = (up - h * pl.groups) * pl.gang + member;
       if (pair >= pl.pairs) continue;  // the last group may be short of pairs
-      s.tail = 0;
-      s.h = h;
-      s.b = 0;
-      s.row0 = pair * 2 * kTile;
-      const int r = pl.rows - s.row0;
-      s.n0 = r < kTile ? r : kTile;
-      s.n1 = r <= kTile ? 0 : (r - kTile < kTile ? r - kTile : kTile);
-      s.t0 = tile * kTile;
+      const int r = pl.rows - pair * 2 * kTile;
+      s.table = a.ptable;
+      s.part = (long long)(c + up) * pl.gang + member;
       s.n = n;
+      s.t0 = tile * kTile;
       s.lo = 0;
       s.hi = a.P;
-      s.begins = s.ends = false;
-      s.part = (long long)(c + up) * pl.gang + member;
-      return true;
+      s.h = h;
+      s.row0 = pair * 2 * kTile;
+      s.n0 = r < kTile ? r : kTile;
+      s.n1 = r <= kTile ? 0 : (r - kTile < kTile ? r - kTile : kTile);
+      s.tail = 0;
+      return;
     }
+    if (!scanned) scan(a);
     while (srem > 0) {
       const int end = tail_end(a, sb), nt = tail_tiles(a, end);
       if (stile >= nt) {
@@ -158,25 +213,27 @@ struct Walk {
         }
         continue;
       }
-      const int n = srem < nt - stile ? (int)srem : nt - stile;
-      s.tail = 1;
+      const int n = srem < nt - stile ? (int)srem : nt - stile, unit = sh * a.B + sb;
+      if ((threadIdx.x & 31) == 0) {  // which CTAs hold the unit's partials
+        if (stile == 0) a.first[unit] = scta;
+        if (stile + n == nt) a.last[unit] = scta;
+      }
+      s.table = a.pool.table + (size_t)sb * a.pool.stride;
+      s.part = (long long)scta + unit;
+      s.n = n;
+      s.t0 = tail_base(a.P) + stile * kTile;
+      s.lo = a.P;
+      s.hi = end;
       s.h = sh;
-      s.b = sb;
       s.row0 = sb * a.G;
       s.n0 = a.G;
       s.n1 = 0;
-      s.t0 = tail_base(a.P) + stile * kTile;
-      s.n = n;
-      s.lo = a.P;
-      s.hi = end;
-      s.begins = stile == 0;
-      s.ends = stile + n == nt;
-      s.part = (long long)scta + (long long)sh * a.B + sb;
+      s.tail = 1;
       stile += n;
       srem -= n;
-      return true;
+      return;
     }
-    return false;
+    s.n = 0;
   }
 };
 
@@ -186,16 +243,62 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3(uint32_t x, uint32_t y, uint32_t z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(__uint_as_float(x)), "f"(__uint_as_float(y)), "f"(__uint_as_float(z)));
+  return r;
+}
+// two fp32 in one 64-bit register, and the packed operations on them
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+
 struct Bars {
-  uint64_t full[kRing], empty[kRing], qfull[kQBufs], qempty[kQBufs], mask[kMasks], s[2], p[2], o[2], drain;
+  uint64_t seg[kSegs], seg_free[kSegs], full[kRing], empty[kRing], qfull[kQBufs], qempty[kQBufs], mask[kMasks], s[2], p[2][2], o[2], drain;
+};
+
+// A role's place in the published segments.  next() waits for one (false: the share is
+// done, or the launch gives up); done() hands it back, once per warp.
+struct Segs {
+  const Args& a;
+  Bars& bar;
+  const Seg* ring;
+  volatile int* abort;
+  int k;
+  __device__ __forceinline__ const Seg* next() {
+    const int i = k % kSegs;
+    bool ok = wait_or_abort(&bar.seg[i], (uint32_t)(k / kSegs) & 1u, abort, a.status);
+    if (__any_sync(0xffffffffu, !ok)) return nullptr;
+    return ring[i].n > 0 ? &ring[i] : nullptr;
+  }
+  __device__ __forceinline__ void done() {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bar.seg_free[k % kSegs]);
+    ++k;
+  }
 };
 
 // ---------------------------------------------------------------------------- gather warps
-// A gather warp's copies: TMA copies complete on their stage's barrier by themselves; rows
-// copied by cp.async are announced there by the warp once they have landed.  Announcements
-// are put off (the copies keep flying) until a stage is waited for: what frees it may need
-// the tiles in flight, so the oldest are announced, one at a time, until it is free.
-struct Gather {
+// The row warp's copies are announced on their stage's barrier by the warp once they have
+// landed.  While the next stage has rows too, announcements are put off (the copies keep
+// flying) until a stage is waited for: what frees it may need the tiles in flight, so the
+// oldest are announced, one at a time, until it is free.
+struct Rows {
   const Args& a;
   volatile int* abort;
   uint64_t* pend[kRing];  // barriers of unannounced copy groups, oldest first
@@ -263,98 +366,48 @@ __device__ __forceinline__ void tma_chunk(uint32_t dst, const CUtensorMap* map, 
       : "memory");
 }
 
-__device__ __forceinline__ void gather_role(const Args& a, const CUtensorMap* tk, const CUtensorMap* tv, Walk walk,
-                                            Bars& bar, uint32_t base, unsigned char* gbase, uint16_t* masks,
-                                            volatile int* abort) {
-  const int w = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31;
-  Gather g{a, abort, {}, 0, true};
-  const int r16 = lane >> 1, half = lane & 1;  // cp.async: a lane copies half a row
-  const uint32_t row_off = (uint32_t)((r16 >> 3) * kGroupB + half * kHalfB + (r16 & 7) * 128);
-  Seg s;
-  int T = 0;
+// The chunks of four key tiles from t0 on, a lane each: the chunk's group of 8 rows in the
+// GPU pool where a TMA copy takes it, else -1.
+__device__ __forceinline__ int chunk_entry(const Args& a, const Seg* s, int t0, int lane) {
+  const int t = t0 + kChunk * lane;
+  return a.tma && t >= s->lo && t + kChunk <= s->hi ? s->table[block_of(a, t)] : -1;
+}
+__device__ __forceinline__ int chunk_group(const Args& a, int h, int e, int t0, int lane) {
+  return e >= 0 && e < a.pool.n_gpu ? (e * a.H + h) * (a.bs >> 3) + (in_block(a, t0 + kChunk * lane) >> 3) : -1;
+}
+
+__device__ __forceinline__ void tma_role(const Args& a, const CUtensorMap* tk, const CUtensorMap* tv, Segs segs,
+                                         Bars& bar, uint32_t base, volatile int* abort) {
+  const int lane = threadIdx.x & 31;
   uint32_t st = 0, par = 1;  // ring stage, parity of its free phase
-  while (g.ok && walk.next(a, s)) {
-    if (s.tail && w == 0 && lane == 0) {
-      if (s.begins) a.first[s.h * a.B + s.b] = walk.scta;
-      if (s.ends) a.last[s.h * a.B + s.b] = walk.scta;
-    }
-    const int32_t* table = s.tail ? a.pool.table + (size_t)s.b * a.pool.stride : a.ptable;
-    // lane v < kChunks: the table entry of chunk w * kChunks + v, where it is whole (-1: row by row)
-    auto entry = [&](int t0) {
-      const int t = t0 + kChunk * (w * kChunks + lane);
-      return a.tma && lane < kChunks && t >= s.lo && t + kChunk <= s.hi ? table[block_of(a, t)] : -1;
-    };
-    int e = entry(s.t0);
-    for (int i = 0; g.ok && i < s.n; ++i, ++T) {
-      const int t0 = s.t0 + i * kTile;
-      // this warp's chunks: part of a block of the GPU pool by TMA, else row by row
-      int mine = -1;  // lane v: chunk v's group of 8 rows
-      if (e >= 0 && e < a.pool.n_gpu)
-        mine = (int)((((long long)e * a.H + s.h) * a.bs + in_block(a, t0 + kChunk * (w * kChunks + lane))) >> 3);
-      const uint32_t whole = __ballot_sync(0xffffffffu, mine >= 0);
-      if (i + 1 < s.n) e = entry(t0 + kTile);
+  while (const Seg* s = segs.next()) {
+    const int n = s->n, h = s->h;
+    int t0 = s->t0, e = chunk_entry(a, s, t0, lane), mine = -1;
+    for (int i = 0; i < n; ++i, t0 += kTile) {
+      if ((i & 3) == 0) {  // four tiles' entries at once, the next four already on their way
+        mine = chunk_group(a, h, e, t0, lane);
+        e = chunk_entry(a, s, t0 + 4 * kTile, lane);
+      }
+      const uint32_t whole = (__ballot_sync(0xffffffffu, mine >= 0) >> (8 * (i & 3))) & 0xffu;
       int group[kChunks];
 #pragma unroll
-      for (int v = 0; v < kChunks; ++v) group[v] = __shfl_sync(0xffffffffu, mine, v);
-      const bool rows = whole != (1u << kChunks) - 1u;
+      for (int v = 0; v < kChunks; ++v) group[v] = __shfl_sync(0xffffffffu, mine, 8 * (i & 3) + v);
       const uint32_t bytes = __popc(whole) * 2 * kGroupB;
-      long long ref[kChunks];
-      uint32_t valid[kChunks];
-#pragma unroll
-      for (int v = 0; v < kChunks; ++v) {
-        ref[v] = -1;
-        valid[v] = 0xffffu;
-      }
-      if (rows) {
-#pragma unroll
-        for (int v = 0; v < kChunks; ++v)
-          if (group[v] < 0) {
-            const int t = t0 + kChunk * (w * kChunks + v) + r16;
-            if (t >= s.lo && t < s.hi) {
-              ref[v] = row_ref(a, s.h, table[block_of(a, t)], t);
-              if (ref[v] < 0) flag(a.status, SKV_DEV_BAD_SLOT);
-            }
-            const int live = __shfl_sync(0xffffffffu, (int)(ref[v] >= 0), (2 * lane) & 31);  // lane r < 16: row r
-            valid[v] = __ballot_sync(0xffffffffu, live && lane < kChunk);
-          }
-      }
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
-        g.wait_free(&bar.empty[st], par);
-        if (!g.ok) break;
-        if (kv == 0 && lane == 0) {
-#pragma unroll
-          for (int v = 0; v < kChunks; ++v) masks[(T % kMasks) * 8 + w * kChunks + v] = (uint16_t)valid[v];
-          mbar_arrive(&bar.mask[T % kMasks]);
-        }
-        uint64_t* full = &bar.full[st];
-        const uint32_t off = (kQBufs + st) * kStageB + w * kChunks * 2 * kGroupB;
-        if (bytes > 0 && t5::elect_one()) {
-          if (rows)
-            mbar_expect_tx(full, bytes);  // the arrival follows when the rows have landed
-          else
+        bool ok = wait_or_abort(&bar.empty[st], par, abort, a.status);
+        if (__any_sync(0xffffffffu, !ok)) return;
+        if (t5::elect_one()) {
+          uint64_t* full = &bar.full[st];
+          const uint32_t dst = base + (kQBufs + st) * kStageB;
+          const CUtensorMap* map = kv ? tv : tk;
+          if (bytes > 0)
             mbar_arrive_expect_tx(full, bytes);
+          else
+            mbar_arrive(full);
 #pragma unroll
           for (int v = 0; v < kChunks; ++v)
-            if (group[v] >= 0) tma_chunk(base + off + v * 2 * kGroupB, kv ? tv : tk, group[v], full);
-        }
-        if (rows) {
-          __syncwarp();  // the bytes are expected before the arrival
-          const unsigned char* gp = (const unsigned char*)(kv ? a.pool.gpu_v : a.pool.gpu_k);
-          const unsigned char* hp = (const unsigned char*)(kv ? a.pool.host_v : a.pool.host_k);
-#pragma unroll
-          for (int v = 0; v < kChunks; ++v)
-            if (group[v] < 0) {
-              const bool live = ref[v] >= 0;
-              const unsigned char* src =
-                  live ? ((ref[v] & tc::kHostBit) ? hp : gp) + (size_t)(ref[v] & tc::kRefRowMask) * tc::kRowBytes + half * 128
-                       : gp;
-              unsigned char* dst = gbase + off + v * 2 * kGroupB + row_off;
-#pragma unroll
-              for (int c = 0; c < 8; ++c)
-                tc::cp_async16_zfill(dst + ((c ^ (r16 & 7)) << 4), live ? src + c * 16 : src, live);
-            }
-          g.commit(full);
+            if (group[v] >= 0) tma_chunk(dst + v * 2 * kGroupB, map, group[v], full);
         }
         if (++st == kRing) {
           st = 0;
@@ -362,24 +415,111 @@ __device__ __forceinline__ void gather_role(const Args& a, const CUtensorMap* tk
         }
       }
     }
+    segs.done();
+  }
+}
+
+__device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, unsigned char* gbase, uint4* masks,
+                                          volatile int* abort) {
+  const int lane = threadIdx.x & 31;
+  Rows g{a, abort, {}, 0, true};
+  const int r16 = lane >> 1, half = lane & 1;  // a lane copies half a row
+  const uint32_t row_off = (uint32_t)((r16 >> 3) * kGroupB + half * kHalfB + (r16 & 7) * 128);
+  int T = 0;
+  uint32_t st = 0, par = 1;
+  while (const Seg* s = segs.next()) {
+    const int n = s->n, h = s->h;
+    int t0 = s->t0, e = chunk_entry(a, s, t0, lane);
+    uint32_t all = 0;
+    for (int i = 0; i < n; ++i, ++T, t0 += kTile) {
+      if ((i & 3) == 0) {
+        all = __ballot_sync(0xffffffffu, chunk_group(a, h, e, t0, lane) >= 0);
+        e = chunk_entry(a, s, t0 + 4 * kTile, lane);
+      }
+      const uint32_t whole = all & 0xffu;
+      all >>= 8;
+      const bool rows = whole != 0xffu;
+      const bool more = i + 1 < n && (i & 3) < 3 && (all & 0xffu) != 0xffu;  // the next tile too
+      long long ref[4];
+      uint32_t mask[4] = {~0u, ~0u, ~0u, ~0u};
+      if (rows) {  // lane l: rows l, l + 32, l + 64, l + 96
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int t = t0 + 32 * j + lane;
+          const bool in = t >= s->lo && t < s->hi;
+          ref[j] = in ? row_ref(a, h, s->table[block_of(a, t)], t) : -1;
+          if (in && ref[j] < 0) flag(a.status, SKV_DEV_BAD_SLOT);
+          mask[j] = __ballot_sync(0xffffffffu, ref[j] >= 0);
+        }
+      }
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        g.wait_free(&bar.empty[st], par);
+        if (!g.ok) {
+          g.flush();
+          return;
+        }
+        if (kv == 0 && lane == 0) {
+          masks[T % kMasks] = make_uint4(mask[0], mask[1], mask[2], mask[3]);
+          mbar_arrive(&bar.mask[T % kMasks]);
+        }
+        uint64_t* full = &bar.full[st];
+        if (rows) {
+          const unsigned char* gp = (const unsigned char*)(kv ? a.pool.gpu_v : a.pool.gpu_k);
+          const unsigned char* hp = (const unsigned char*)(kv ? a.pool.host_v : a.pool.host_k);
+          unsigned char* to = gbase + (kQBufs + st) * kStageB + row_off;
+#pragma unroll
+          for (int v = 0; v < kChunks; ++v) {
+            if (whole >> v & 1u) continue;
+            const long long r = __shfl_sync(0xffffffffu, ref[v >> 1], 16 * (v & 1) + r16);
+            const bool live = r >= 0;
+            const unsigned char* src =
+                live ? ((r & tc::kHostBit) ? hp : gp) + (size_t)(r & tc::kRefRowMask) * tc::kRowBytes + half * 128 : gp;
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              tc::cp_async16_zfill(to + v * 2 * kGroupB + ((c ^ (r16 & 7)) << 4), live ? src + c * 16 : src, live);
+          }
+          g.commit(full);
+          if (kv == 1 && !more) g.flush();
+        } else if (lane == 0) {
+          mbar_arrive(full);
+        }
+        if (++st == kRing) {
+          st = 0;
+          par ^= 1u;
+        }
+      }
+    }
+    segs.done();
   }
   g.flush();
 }
 
-// ---------------------------------------------------------------------------- query warp
-__device__ __forceinline__ void query_role(const Args& a, Walk walk, Bars& bar, unsigned char* gbase,
-                                           volatile int* abort) {
+// ---------------------------------------------------------------------------- segments and query rows
+__device__ __forceinline__ void walk_role(const Args& a, Bars& bar, Seg* ring, unsigned char* gbase,
+                                          volatile int* abort) {
   const int lane = threadIdx.x & 31;
   const int r16 = lane >> 1, half = lane & 1;
   const uint32_t row_off = (uint32_t)((r16 >> 3) * kGroupB + half * kHalfB + (r16 & 7) * 128);
-  Seg s;
+  Walk walk;
+  walk.init(a);
   int nq = 0;
-  while (walk.next(a, s)) {
+  for (int k = 0;; ++k) {
+    Seg s;
+    walk.next(a, s);
+    bool ok = wait_or_abort(&bar.seg_free[k % kSegs], (uint32_t)((k / kSegs) & 1) ^ 1u, abort, a.status);
+    if (__any_sync(0xffffffffu, !ok)) return;
+    if (lane == 0) {
+      ring[k % kSegs] = s;
+      mbar_arrive(&bar.seg[k % kSegs]);
+    }
+    if (s.n == 0) return;
     for (int u = 0; u < (s.n1 > 0 ? 2 : 1); ++u, ++nq) {
       const int buf = nq & 1;
-      bool ok = wait_or_abort(&bar.qempty[buf], (uint32_t)((nq >> 1) & 1) ^ 1u, abort, a.status);
+      ok = wait_or_abort(&bar.qempty[buf], (uint32_t)((nq >> 1) & 1) ^ 1u, abort, a.status);
       if (__any_sync(0xffffffffu, !ok)) return;
       const int live = u ? s.n1 : s.n0;
+#pragma unroll 2
       for (int v = 0; v * kChunk < live; ++v) {
         const int r = kChunk * v + r16;
         if (r < live) {
@@ -406,109 +546,116 @@ constexpr uint32_t kStage = 7u, kKPar = 3, kVStage = 4, kVPar = 7, kQBuf = 8, kQ
 constexpr uint32_t kKFirst = 1u << 10, kKLast = 1u << 11, kQFirst = 1u << 12, kQLast = 1u << 13, kOFirst = 1u << 14,
                    kOLast = 1u << 15, kLive = 1u << 16;
 }  // namespace step
+// The step words of a segment, 32 at a time: lane j holds the j-th of them.
 struct Steps {
-  Walk walk;
-  int n, i, nq;            // the segment's key tiles, the next one, Q buffers used before it
-  uint32_t stage, par;     // ring position of the next tile's K
-  bool two, second, have;  // two row tiles; the second one is next; inside a segment
-  __device__ __forceinline__ uint32_t next(const Args& a) {
-    if (!have) {
-      Seg s;
-      if (!walk.next(a, s)) return 0u;
-      have = true;
-      n = s.n;
-      two = s.n1 > 0;
-      i = 0;
-      second = false;
-    }
-    const uint32_t wrap = stage + 1 == kRing, q = (uint32_t)nq + (second ? 1u : 0u);
-    uint32_t c = step::kLive | stage | par << step::kKPar | (wrap ? 0u : stage + 1) << step::kVStage |
-                 (par ^ wrap) << step::kVPar | (q & 1u) << step::kQBuf | ((q >> 1) & 1u) << step::kQPar;
-    if (!second) c |= step::kKFirst;
-    if (!two || second) c |= step::kKLast;
-    if (i == 0) c |= step::kQFirst;
-    if (i == n - 1) c |= step::kQLast;
-    if (i < (two ? 1 : 2)) c |= step::kOFirst;
-    if (i >= n - (two ? 1 : 2)) c |= step::kOLast;
-    if (two && !second) {
-      second = true;
-    } else {
-      second = false;
-      stage += 2;
-      if (stage >= kRing) {
-        stage -= kRing;
-        par ^= 1u;
+  Segs segs;
+  int total, base, pos, cnt;  // steps of the segment, of which base are behind this batch; the batch's next and count
+  int seq, nq;                // ring position (modulo two rounds) and Q buffers at the segment's start
+  bool two, open;
+  uint32_t words;
+  __device__ __forceinline__ uint32_t next() {
+    if (pos == cnt) {
+      base += cnt;
+      if (base == total) {
+        if (open) {
+          seq = (seq + 2 * (two ? total >> 1 : total)) % (2 * kRing);
+          nq += two ? 2 : 1;
+          segs.done();
+        }
+        const Seg* s = segs.next();
+        open = s != nullptr;
+        total = base = pos = cnt = 0;
+        if (!open) return 0u;
+        two = s->n1 > 0;
+        total = two ? 2 * s->n : s->n;
       }
-      if (++i == n) {
-        have = false;
-        nq += two ? 2 : 1;
-      }
+      cnt = total - base < 32 ? total - base : 32;
+      pos = 0;
+      const int j = base + (int)(threadIdx.x & 31);
+      const int tile = two ? j >> 1 : j;
+      const uint32_t second = two ? j & 1 : 0, per = two ? 2 : 1, q = (uint32_t)nq + second;
+      const uint32_t k = (uint32_t)(seq + 2 * tile) % (2 * kRing), v = k + 1 == 2 * kRing ? 0 : k + 1;
+      uint32_t c = step::kLive | k % kRing | (k / kRing) << step::kKPar | (v % kRing) << step::kVStage |
+                   (v / kRing) << step::kVPar | (q & 1u) << step::kQBuf | ((q >> 1) & 1u) << step::kQPar;
+      if (!second) c |= step::kKFirst;
+      if (!two || second) c |= step::kKLast;
+      if (j < (int)per) c |= step::kQFirst;
+      if (j >= total - (int)per) c |= step::kQLast;
+      if (j < 2) c |= step::kOFirst;
+      if (j >= total - 2) c |= step::kOLast;
+      words = c;
     }
-    return c;
+    return __shfl_sync(0xffffffffu, words, pos++);
   }
 };
 
-__device__ __forceinline__ void mma_role(const Args& a, const Walk& walk, Bars& bar, uint32_t base, uint32_t tm,
+__device__ __forceinline__ void mma_role(const Args& a, const Segs& segs, Bars& bar, uint32_t base, uint32_t tm,
                                          volatile int* abort) {
   const uint32_t id_s = t5::idesc_bf16(128, 128, false), id_o = t5::idesc_bf16(128, 128, true);
   // descriptors of buffer 0; a buffer is kStageB / 16 further in the address field
   const uint64_t dq = t5::desc_sw128(base, 16, kGroupB), dk = t5::desc_sw128(base + kQBufs * kStageB, 16, kGroupB);
   const uint64_t dv = t5::desc_sw128(base + kQBufs * kStageB, kHalfB, kGroupB);
-  Steps gen{walk, 0, 0, 0, 0u, 0u, false, false, false};
+  Steps gen{segs, 0, 0, 0, 0, 0, 0, false, false, 0u};
   bool ok = true;
   auto wait = [&](uint64_t* b, uint32_t parity) {
     if (ok) ok = wait_or_abort(b, parity, abort, a.status);
     ok = __all_sync(0xffffffffu, ok);
   };
-  auto issue_s = [&](uint32_t c, uint32_t slot) {
+  auto issue_s = [&](uint32_t c, uint32_t slot, bool k_there) {
     const uint32_t ks = c & step::kStage, qb = (c >> step::kQBuf) & 1u;
     if (c & step::kQFirst) wait(&bar.qfull[qb], (c >> step::kQPar) & 1u);
-    if (c & step::kKFirst) wait(&bar.full[ks], (c >> step::kKPar) & 1u);
+    if (!k_there) wait(&bar.full[ks], (c >> step::kKPar) & 1u);
     if (!ok) return;
     t5::fence_after();
     const uint64_t qd = dq + qb * (kStageB >> 4), kd = dk + ks * (kStageB >> 4);
     if (t5::elect_one()) {
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk) {  // 16 of the 128 dims each
-      const uint32_t off = ((uint32_t)(kk >> 2) * kHalfB + (kk & 3) * 32) >> 4;
-      t5::mma(tm + slot * 128, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
-    }
-    t5::commit(&bar.s[slot]);
-    if (c & step::kKLast) t5::commit(&bar.empty[ks]);
-    if (c & step::kQLast) t5::commit(&bar.qempty[qb]);
+      for (int kk = 0; kk < 8; ++kk) {  // 16 of the 128 dims each
+        const uint32_t off = ((uint32_t)(kk >> 2) * kHalfB + (kk & 3) * 32) >> 4;
+        t5::mma(tm + slot * 128, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
+      }
+      t5::commit(&bar.s[slot]);
+      if (c & step::kKLast) t5::commit(&bar.empty[ks]);
+      if (c & step::kQLast) t5::commit(&bar.qempty[qb]);
     }
   };
   auto issue_o = [&](uint32_t c, uint32_t slot, uint32_t p_par) {
     const uint32_t vs = (c >> step::kVStage) & step::kStage;
     if (c & step::kKFirst) wait(&bar.full[vs], (c >> step::kVPar) & 1u);
-    wait(&bar.p[slot], p_par);
-    if (!ok) return;
-    t5::fence_after();
     const uint64_t vd = dv + vs * (kStageB >> 4);
-    if (t5::elect_one()) {
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk)  // 16 of the 128 keys each
-      t5::mma_ts(tm + 256 + slot * 128, tm + slot * 128 + kk * 8, vd + ((kk * 2 * kGroupB) >> 4), id_o,
-                 kk > 0 ? 1u : ((c & step::kOFirst) ? 0u : 1u));
-    if (c & step::kKLast) t5::commit(&bar.empty[vs]);
-    if (c & step::kOLast) t5::commit(&bar.o[slot]);
+    for (int half = 0; half < 2; ++half) {  // 64 keys as soon as their P is there
+      wait(&bar.p[slot][half], p_par);
+      if (!ok) return;
+      t5::fence_after();
+      if (t5::elect_one()) {
+#pragma unroll
+        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)  // 16 of the 128 keys each
+          t5::mma_ts(tm + 256 + slot * 128, tm + slot * 128 + kk * 8, vd + ((kk * 2 * kGroupB) >> 4), id_o,
+                     kk > 0 ? 1u : ((c & step::kOFirst) ? 0u : 1u));
+        if (half) {
+          if (c & step::kKLast) t5::commit(&bar.empty[vs]);
+          if (c & step::kOLast) t5::commit(&bar.o[slot]);
+        }
+      }
     }
   };
-  uint32_t c0 = gen.next(a), c1 = 0u, p_par = 0u;
-  if (c0) issue_s(c0, 0);
-  if (c0) c1 = gen.next(a);
-  if (c1) issue_s(c1, 1);
-  while (ok && c0) {  // slots in turn: O of a step, then S of its slot's next one
-    uint32_t nx = gen.next(a);
-    issue_o(c0, 0, p_par);
-    if (ok && nx) issue_s(nx, 0);
-    c0 = nx;
-    if (!ok || !c1) break;
-    nx = gen.next(a);
-    issue_o(c1, 1, p_par);
-    if (ok && nx) issue_s(nx, 1);
-    c1 = nx;
-    p_par ^= 1u;
+  // whether a step's keys have landed (its K is shared with the step before, or the barrier says so)
+  auto k_there = [&](uint32_t c) {
+    return !(c & step::kKFirst) ||
+           __all_sync(0xffffffffu, mbar_try_wait(&bar.full[c & step::kStage], (c >> step::kKPar) & 1u));
+  };
+  // step y - 2's O, then S of step y in the same slot
+  uint32_t behind = 0u, last = 0u;  // steps y - 2 and y - 1, 0: none
+  for (uint32_t y = 0;; ++y) {
+    const uint32_t nx = last || y < 2 ? gen.next() : 0u;
+    if (!nx && !behind && !last) break;
+    const bool there = nx && k_there(nx);
+    if (behind) issue_o(behind, y & 1u, ((y >> 1) & 1u) ^ 1u);
+    if (ok && nx) issue_s(nx, y & 1u, there);
+    if (!ok) break;
+    behind = last;
+    last = nx;
   }
   // the operands in shared memory and TMEM outlive every MMA issued
   __syncwarp();
@@ -517,15 +664,16 @@ __device__ __forceinline__ void mma_role(const Args& a, const Walk& walk, Bars& 
 }
 
 // ---------------------------------------------------------------------------- softmax warps
-__device__ __forceinline__ void softmax_role(const Args& a, Walk walk, Bars& bar, uint32_t tm, const uint4* masks,
+__device__ __forceinline__ void softmax_role(const Args& a, Segs segs, Bars& bar, uint32_t tm, const uint4* masks,
                              volatile int* abort) {
   const int slot = threadIdx.x >> 7, wq = (threadIdx.x >> 5) & 3, row = threadIdx.x & 127;
   const uint32_t lanes = (uint32_t)(wq * 32) << 16;
   const uint32_t ts = tm + lanes + slot * 128, to = tm + lanes + 256 + slot * 128;
-  Seg s;
   int x = 0, T = 0, ns = 0, no = 0;
   bool ok = true;
-  while (ok && walk.next(a, s)) {
+  const Seg* sp;
+  while (ok && (sp = segs.next()) != nullptr) {
+    const Seg& s = *sp;
     const bool two = s.n1 > 0;
     const int sub = slot ^ (x & 1);
     const int mine = two ? s.n : (s.n + 1 - sub) / 2;
@@ -554,9 +702,13 @@ __device__ __forceinline__ void softmax_role(const Args& a, Walk walk, Bars& bar
         }
         float mx[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) mx[u] = __uint_as_float(v[u]);
+        for (int u = 0; u < 4; ++u) mx[u] = max3(v[u], v[u + 4], v[u + 8]);
 #pragma unroll
-        for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(v[i]));
+        for (int i = 12; i + 8 <= 128; i += 8)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mx[u] = max3(__float_as_uint(mx[u]), v[i + u], v[i + 4 + u]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], __uint_as_float(v[124 + u]));
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
         if (j == 0) {
           m = top;
@@ -567,7 +719,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Walk walk, Bars& bar
           const float f = grow ? ex2(m - top) : 1.f;
           m = grow ? top : m;
           l *= f;
-#pragma unroll
+#pragma unroll 1
           for (int ch = 0; ch < 4; ++ch) {
             uint32_t o[32];
             t5::ld32(to + ch * 32, o);
@@ -576,26 +728,36 @@ __device__ __forceinline__ void softmax_role(const Args& a, Walk walk, Bars& bar
             t5::st32(to + ch * 32, o);
           }
         }
-        const float mb = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const float mb = m == -INFINITY ? 0.f : -m;
+        const uint64_t sc2 = pack2(a.scale_log2, a.scale_log2), mb2 = pack2(mb, mb);
+        uint64_t sum[2] = {0ull, 0ull};  // pairs of +0.0
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch) {
           uint32_t pk[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float p0 = ex2(fmaf(__uint_as_float(v[ch * 64 + 2 * i]), a.scale_log2, -mb));
-            const float p1 = ex2(fmaf(__uint_as_float(v[ch * 64 + 2 * i + 1]), a.scale_log2, -mb));
-            sum[(2 * i) & 3] += p0;
-            sum[(2 * i + 1) & 3] += p1;
-            pk[i] = tc::pack_bf16(p0, p1);
+            float z0, z1;
+            unpack2(fma2(pack2(__uint_as_float(v[ch * 64 + 2 * i]), __uint_as_float(v[ch * 64 + 2 * i + 1])), sc2, mb2), z0, z1);
+            z0 = ex2(z0);
+            z1 = ex2(z1);
+            sum[i & 1] = add2(sum[i & 1], pack2(z0, z1));
+            pk[i] = tc::pack_bf16(z0, z1);
           }
           t5::st32(ts + ch * 32, pk);
+          t5::st_wait();
+          if (ch == 0) {  // the first 64 keys' P V may start
+            t5::fence_before();
+            mbar_arrive(&bar.p[slot][0]);
+          }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        t5::st_wait();
+        float l0, l1;
+        unpack2(add2(sum[0], sum[1]), l0, l1);
+        l += l0 + l1;
+      } else {
+        mbar_arrive(&bar.p[slot][0]);
       }
       t5::fence_before();
-      mbar_arrive(&bar.p[slot]);
+      mbar_arrive(&bar.p[slot][1]);
     }
     if (ok && mine > 0) {
       ok = wait_or_abort(&bar.o[slot], (uint32_t)(no++) & 1u, abort, a.status);
@@ -606,9 +768,9 @@ __device__ __forceinline__ void softmax_role(const Args& a, Walk walk, Bars& bar
     const int rp = s.tail ? a.G : a.pl.rp;
     float* po = (s.tail ? a.so : a.po) + (size_t)(2 * s.part + sub) * rp * kD;
     float* ml = (s.tail ? a.sml : a.pml) + (size_t)(2 * s.part + sub) * rp * 2;
-    if (ok && warp_live && (sub == 0 || two || mine > 0 || s.n1 == 0)) {
+    if (ok && warp_live) {
       if (mine > 0) {
-#pragma unroll
+#pragma unroll 1
         for (int ch = 0; ch < 4; ++ch) {
           uint32_t o[32];
           t5::ld32(to + ch * 32, o);
@@ -626,6 +788,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Walk walk, Bars& bar
     }
     x += two ? 2 * s.n : s.n;
     T += s.n;
+    segs.done();
   }
 }
 
@@ -635,27 +798,31 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) Bars bar;
   __shared__ __align__(16) uint4 masks[kMasks];
-  __shared__ long long s_scan[kThreads / 32];
-  __shared__ int s_at[3];
+  __shared__ Seg ring[kSegs];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int t = threadIdx.x, warp = t >> 5;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   unsigned char* gbase = smem_raw + (base - raw);
   if (t == 0) {
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(&bar.seg[i], 1);
+      mbar_init(&bar.seg_free[i], kSegReaders);
+    }
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(&bar.full[i], kGatherWarps);
+      mbar_init(&bar.full[i], 2);
       mbar_init(&bar.empty[i], 1);
     }
     for (int i = 0; i < kQBufs; ++i) {
       mbar_init(&bar.qfull[i], 1);
       mbar_init(&bar.qempty[i], 1);
     }
-    for (int i = 0; i < kMasks; ++i) mbar_init(&bar.mask[i], kGatherWarps);
+    for (int i = 0; i < kMasks; ++i) mbar_init(&bar.mask[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.s[i], 1);
-      mbar_init(&bar.p[i], 128);
+      mbar_init(&bar.p[i][0], 128);
+      mbar_init(&bar.p[i][1], 128);
       mbar_init(&bar.o[i], 1);
     }
     mbar_init(&bar.drain, 1);
@@ -668,76 +835,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  pdl_release();
-  pdl_wait();
-  // this CTA's share: the gang's prefix tiles, and its range of the tails' tiles, whose
-  // first tile is found by a scan of the requests' tile counts
-  Walk walk;
-  const Plan& pl = a.pl;
-  const int gang = blockIdx.x / pl.gang;
-  const long long tp = (long long)a.H * pl.groups * pl.ntp;
-  walk.p0 = gang < pl.gangs ? gang * tp / pl.gangs : 0;
-  walk.p1 = gang < pl.gangs ? (gang + 1) * tp / pl.gangs : 0;
-  const int per = (a.B + kThreads - 1) / kThreads;
-  long long mine = 0;
-  for (int b = t * per; b < (t + 1) * per && b < a.B; ++b) mine += tail_tiles(a, tail_end(a, b));
-  long long incl = mine;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += o;
-  }
-  if (lane == 31) s_scan[warp] = incl;
   t5::fence_before();
   __syncthreads();
   t5::fence_after();
-  long long before = 0, total = 0;
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < warp) before += s_scan[i];
-    total += s_scan[i];
-  }
-  const long long ts = total * a.H;
-  // the last CTAs take the tails (the first ones the prefix, where there are few tiles)
-  walk.scta = kCtas - 1 - (int)blockIdx.x;
-  const int sn = ts < kCtas ? (int)ts : kCtas;
-  const long long s0 = walk.scta < sn ? walk.scta * ts / sn : 0, s1 = walk.scta < sn ? (walk.scta + 1) * ts / sn : 0;
-  walk.srem = s1 - s0;
-  walk.sh = walk.sb = walk.stile = 0;
-  if (walk.srem > 0) {
-    const long long at = s0 % total;
-    long long lo = before + incl - mine;
-    if (at >= lo && at < lo + mine) {
-      for (int b = t * per; b < (t + 1) * per && b < a.B; ++b) {
-        const int n = tail_tiles(a, tail_end(a, b));
-        if (at < lo + n) {
-          s_at[0] = (int)(s0 / total);
-          s_at[1] = b;
-          s_at[2] = (int)(at - lo);
-          break;
-        }
-        lo += n;
-      }
-    }
-  }
-  __syncthreads();
-  if (walk.srem > 0) {
-    walk.sh = s_at[0];
-    walk.sb = s_at[1];
-    walk.stile = s_at[2];
-  }
+  pdl_release();
+  pdl_wait();
   const uint32_t tm = s_tmem;
+  const Segs segs{a, bar, ring, &s_abort, 0};
   // 2 x 128 x 208 + 128 x 88 = 64,512 registers, what 384 threads of 168 were launched with
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    softmax_role(a, walk, bar, tm, masks, &s_abort);
+    softmax_role(a, segs, bar, tm, masks, &s_abort);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp < 8 + kGatherWarps)
-      gather_role(a, &tk, &tv, walk, bar, base, gbase, reinterpret_cast<uint16_t*>(masks), &s_abort);
+    if (warp == 8)
+      tma_role(a, &tk, &tv, segs, bar, base, &s_abort);
+    else if (warp == 9)
+      rows_role(a, segs, bar, gbase, masks, &s_abort);
     else if (warp == 10)
-      query_role(a, walk, bar, gbase, &s_abort);
+      walk_role(a, bar, ring, gbase, &s_abort);
     else
-      mma_role(a, walk, bar, base, tm, &s_abort);
+      mma_role(a, segs, bar, base, tm, &s_abort);
   }
   t5::fence_before();
   __syncthreads();
