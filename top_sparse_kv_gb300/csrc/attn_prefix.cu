@@ -7,7 +7,7 @@
 // products on the tcgen05 tensor cores, and the prefix crosses HBM once; a tail [P, L_b)
 // meets the G rows of its own request the same way.  Both are cut into tiles of 128 keys.
 //
-// prefix_attn_kernel, one persistent CTA an SM, 12 warps in four roles:
+// prefix_attn_kernel, one persistent CTA an SM, 16 warps:
 //   warps 0-3, 4-7   softmax of slot 0 / slot 1 (a thread a query row)
 //   warp 8           16 keys of a block of the GPU pool by one 4 KB TMA copy, into a ring of
 //                    32 KB K / V stages in the 128-byte-swizzled layout that the MMA reads
@@ -17,8 +17,10 @@
 //                    so that waiting for its rows to land holds back no TMA copy.
 //   warp 10          cuts the CTA's share into segments, published in a ring for the other
 //                    roles, and copies their query rows, by cp.async
-//   warp 11          issues every MMA (converged, one elected lane: the operands' uniform
-//                    registers then cost no per-lane serialisation; 100 cycles an MMA before)
+//   warps 11, 12     issue the MMAs of slot 0 / slot 1 (converged, one elected lane: the
+//                    operands' uniform registers then cost no per-lane serialisation, 100
+//                    cycles an MMA otherwise; a warp a slot, so that one's bookkeeping runs
+//                    under the other's MMAs)
 // A *step* is one (128 query rows, 128 keys) tile: S = Q K^T (M128 N128, fp32 in TMEM),
 // P = 2^(z - m) in bf16 over S's own columns, O += P V (A from TMEM, V read MN-major).
 // Steps alternate between two slots of TMEM (S 128 + O 128 columns each), so that one
@@ -45,7 +47,7 @@ namespace {
 
 namespace px {
 constexpr int kCtas = 152;             // one CTA an SM of a GB300 (a function of the problem alone: sizes the workspace)
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kTile = 128;             // keys a tile, query rows a tile
 constexpr int kStageB = kTile * 256;   // a K, V or Q tile, 32 KB: [group of 8 rows][half of the dims][8 rows][128 bytes]
 constexpr int kGroupB = 2048;          // a group of 8 rows
@@ -56,7 +58,7 @@ constexpr int kRing = 5;               // K / V stages
 constexpr int kQBufs = 2;
 constexpr int kMasks = 8;              // key masks of the last tiles
 constexpr int kSegs = 8;               // segments published ahead
-constexpr int kSegReaders = 11;        // warps that read them: 8 softmax, TMA, rows, MMA
+constexpr int kSegReaders = 12;        // warps that read them: 8 softmax, TMA, rows, 2 MMA
 constexpr int kSmem = (kQBufs + kRing) * kStageB + 1024;
 constexpr int kMaxGang = 4;            // pairs of row tiles that read the same keys together
 constexpr float kGrow = 8.f;           // log2 growth of a row's maximum that renews it
@@ -268,8 +270,19 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
   return r;
 }
 
+// The ring's order of loads, for tile T of the CTA's tiles: K0 K1 V0 K2 V1 K3 V2 ... -- the
+// order of their first use when the slots take alternate tiles (S of step x + 2 follows
+// O of step x), so a load has two tiles' time to land.
+__device__ __forceinline__ int k_seq(int T) { return T > 0 ? 2 * T - 1 : 0; }
+__device__ __forceinline__ int v_seq(int T) { return 2 * T + 2; }
+
+// full: two barriers a stage, of alternate rounds of the ring.  A slot's warp waits for the
+// stages of its own steps only, so a stage may go through another round unseen by it; with
+// one barrier the parity it waits for could be that of two rounds before.  With two, the
+// round before on the same barrier (ten loads back) is over: the load that the warp saw
+// last was issued after it had been handed back.
 struct Bars {
-  uint64_t seg[kSegs], seg_free[kSegs], full[kRing], empty[kRing], qfull[kQBufs], qempty[kQBufs], mask[kMasks], s[2], p[2][2], o[2], drain;
+  uint64_t seg[kSegs], seg_free[kSegs], full[2 * kRing], empty[kRing], qfull[kQBufs], qempty[kQBufs], mask[kMasks], s[2], p[2][2], o[2], drain[2];
 };
 
 // A role's place in the published segments.  next() waits for one (false: the share is
@@ -379,7 +392,42 @@ __device__ __forceinline__ int chunk_group(const Args& a, int h, int e, int t0, 
 __device__ __forceinline__ void tma_role(const Args& a, const CUtensorMap* tk, const CUtensorMap* tv, Segs segs,
                                          Bars& bar, uint32_t base, volatile int* abort) {
   const int lane = threadIdx.x & 31;
-  uint32_t st = 0, par = 1;  // ring stage, parity of its free phase
+  uint32_t sq = 0, par = 1;  // place in two rounds of the ring, parity of the stage's free phase
+  auto advance = [&] {
+    if (++sq == 2 * kRing) sq = 0;
+    if (sq == 0 || sq == kRing) par ^= 1u;
+  };
+  // a stage of the chunks whose groups lanes 0-7 hold; false: the launch gives up
+  auto load = [&](const CUtensorMap* map, int mine) {
+    const uint32_t st = sq >= kRing ? sq - kRing : sq;
+    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine >= 0) & 0xffu) * 2 * kGroupB;
+    int group[kChunks];
+#pragma unroll
+    for (int v = 0; v < kChunks; ++v) group[v] = __shfl_sync(0xffffffffu, mine, v);
+    const bool ok = wait_or_abort(&bar.empty[st], par, abort, a.status);
+    if (__any_sync(0xffffffffu, !ok)) return false;
+    if (t5::elect_one()) {
+      uint64_t* full = &bar.full[sq];
+      const uint32_t dst = base + (kQBufs + st) * kStageB;
+      if (bytes > 0)
+        mbar_arrive_expect_tx(full, bytes);
+      else
+        mbar_arrive(full);
+#pragma unroll
+      for (int v = 0; v < kChunks; ++v)
+        if (group[v] >= 0) tma_chunk(dst + v * 2 * kGroupB, map, group[v], full);
+    }
+    advance();
+    return true;
+  };
+  // the launch gives up: the copies in flight land (or their time runs out) before the memory goes
+  int issued = 0;
+  auto drain = [&] {
+    for (int q = issued > kRing ? issued - kRing : 0; q < issued; ++q)
+      mbar_wait_bounded(&bar.full[q % (2 * kRing)], (uint32_t)(q / (2 * kRing)) & 1u, 20000000LL);
+  };
+  int before = 0;           // the tile before's groups: its V follows this tile's K
+  bool have = false;
   while (const Seg* s = segs.next()) {
     const int n = s->n, h = s->h;
     int t0 = s->t0, e = chunk_entry(a, s, t0, lane), mine = -1;
@@ -388,34 +436,25 @@ __device__ __forceinline__ void tma_role(const Args& a, const CUtensorMap* tk, c
         mine = chunk_group(a, h, e, t0, lane);
         e = chunk_entry(a, s, t0 + 4 * kTile, lane);
       }
-      const uint32_t whole = (__ballot_sync(0xffffffffu, mine >= 0) >> (8 * (i & 3))) & 0xffu;
-      int group[kChunks];
-#pragma unroll
-      for (int v = 0; v < kChunks; ++v) group[v] = __shfl_sync(0xffffffffu, mine, 8 * (i & 3) + v);
-      const uint32_t bytes = __popc(whole) * 2 * kGroupB;
+      const int now = __shfl_sync(0xffffffffu, mine, (8 * (i & 3) + lane) & 31);
 #pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv) {
-        bool ok = wait_or_abort(&bar.empty[st], par, abort, a.status);
-        if (__any_sync(0xffffffffu, !ok)) return;
-        if (t5::elect_one()) {
-          uint64_t* full = &bar.full[st];
-          const uint32_t dst = base + (kQBufs + st) * kStageB;
-          const CUtensorMap* map = kv ? tv : tk;
-          if (bytes > 0)
-            mbar_arrive_expect_tx(full, bytes);
-          else
-            mbar_arrive(full);
-#pragma unroll
-          for (int v = 0; v < kChunks; ++v)
-            if (group[v] >= 0) tma_chunk(dst + v * 2 * kGroupB, map, group[v], full);
+      for (int kv = have ? 0 : 1; kv < 2; ++kv)  // (the first tile: its K alone)
+        if (load(kv == (have ? 1 : 2) ? tv : tk, kv == (have ? 1 : 2) ? before : now)) {
+          ++issued;
+        } else {
+          drain();
+          return;
         }
-        if (++st == kRing) {
-          st = 0;
-          par ^= 1u;
-        }
-      }
+      before = now;
+      have = true;
     }
     segs.done();
+  }
+  if (have && !*abort) {
+    advance();  // no K follows the last tile: its place stays empty
+    load(tv, before);
+  } else if (have) {
+    drain();
   }
 }
 
@@ -426,8 +465,48 @@ __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, u
   const int r16 = lane >> 1, half = lane & 1;  // a lane copies half a row
   const uint32_t row_off = (uint32_t)((r16 >> 3) * kGroupB + half * kHalfB + (r16 & 7) * 128);
   int T = 0;
-  uint32_t st = 0, par = 1;
-  while (const Seg* s = segs.next()) {
+  uint32_t sq = 0, par = 1;
+  auto advance = [&] {
+    if (++sq == 2 * kRing) sq = 0;
+    if (sq == 0 || sq == kRing) par ^= 1u;
+  };
+  // the K or V stage of a tile: lane l holds the references of rows l, l + 32, l + 64, l + 96
+  auto load = [&](const long long* ref, uint32_t whole, const void* gpu, const void* host, const uint32_t* mask) {
+    const uint32_t st = sq >= kRing ? sq - kRing : sq;
+    if (whole == 0xffu) g.flush();  // nothing to put off: what is in flight comes first
+    g.wait_free(&bar.empty[st], par);
+    if (!g.ok) return;
+    if (mask && lane == 0) {
+      masks[T % kMasks] = make_uint4(mask[0], mask[1], mask[2], mask[3]);
+      mbar_arrive(&bar.mask[T % kMasks]);
+    }
+    uint64_t* full = &bar.full[sq];
+    if (whole != 0xffu) {
+      unsigned char* to = gbase + (kQBufs + st) * kStageB + row_off;
+#pragma unroll
+      for (int v = 0; v < kChunks; ++v) {
+        if (whole >> v & 1u) continue;
+        const long long r = __shfl_sync(0xffffffffu, ref[v >> 1], 16 * (v & 1) + r16);
+        const bool live = r >= 0;
+        const unsigned char* src = (const unsigned char*)((r & tc::kHostBit) && live ? host : gpu) +
+                                   (live ? (size_t)(r & tc::kRefRowMask) * tc::kRowBytes + half * 128 : 0);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          tc::cp_async16_zfill(to + v * 2 * kGroupB + ((c ^ (r16 & 7)) << 4), live ? src + c * 16 : src, live);
+      }
+      g.commit(full);
+    } else if (lane == 0) {
+      mbar_arrive(full);
+    }
+    advance();
+  };
+  long long before[4];
+  uint32_t whole_before = 0;
+  bool have = false;
+  while (true) {
+    g.flush();  // before a wait that does not announce
+    const Seg* s = segs.next();
+    if (s == nullptr) break;
     const int n = s->n, h = s->h;
     int t0 = s->t0, e = chunk_entry(a, s, t0, lane);
     uint32_t all = 0;
@@ -438,59 +517,34 @@ __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, u
       }
       const uint32_t whole = all & 0xffu;
       all >>= 8;
-      const bool rows = whole != 0xffu;
-      const bool more = i + 1 < n && (i & 3) < 3 && (all & 0xffu) != 0xffu;  // the next tile too
-      long long ref[4];
+      long long ref[4] = {-1, -1, -1, -1};
       uint32_t mask[4] = {~0u, ~0u, ~0u, ~0u};
-      if (rows) {  // lane l: rows l, l + 32, l + 64, l + 96
+      if (whole != 0xffu) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int t = t0 + 32 * j + lane;
           const bool in = t >= s->lo && t < s->hi;
-          ref[j] = in ? row_ref(a, h, s->table[block_of(a, t)], t) : -1;
+          if (in) ref[j] = row_ref(a, h, s->table[block_of(a, t)], t);
           if (in && ref[j] < 0) flag(a.status, SKV_DEV_BAD_SLOT);
           mask[j] = __ballot_sync(0xffffffffu, ref[j] >= 0);
         }
       }
-#pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv) {
-        g.wait_free(&bar.empty[st], par);
-        if (!g.ok) {
-          g.flush();
-          return;
-        }
-        if (kv == 0 && lane == 0) {
-          masks[T % kMasks] = make_uint4(mask[0], mask[1], mask[2], mask[3]);
-          mbar_arrive(&bar.mask[T % kMasks]);
-        }
-        uint64_t* full = &bar.full[st];
-        if (rows) {
-          const unsigned char* gp = (const unsigned char*)(kv ? a.pool.gpu_v : a.pool.gpu_k);
-          const unsigned char* hp = (const unsigned char*)(kv ? a.pool.host_v : a.pool.host_k);
-          unsigned char* to = gbase + (kQBufs + st) * kStageB + row_off;
-#pragma unroll
-          for (int v = 0; v < kChunks; ++v) {
-            if (whole >> v & 1u) continue;
-            const long long r = __shfl_sync(0xffffffffu, ref[v >> 1], 16 * (v & 1) + r16);
-            const bool live = r >= 0;
-            const unsigned char* src =
-                live ? ((r & tc::kHostBit) ? hp : gp) + (size_t)(r & tc::kRefRowMask) * tc::kRowBytes + half * 128 : gp;
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              tc::cp_async16_zfill(to + v * 2 * kGroupB + ((c ^ (r16 & 7)) << 4), live ? src + c * 16 : src, live);
-          }
-          g.commit(full);
-          if (kv == 1 && !more) g.flush();
-        } else if (lane == 0) {
-          mbar_arrive(full);
-        }
-        if (++st == kRing) {
-          st = 0;
-          par ^= 1u;
-        }
+      load(ref, whole, a.pool.gpu_k, a.pool.host_k, mask);
+      if (g.ok && have) load(before, whole_before, a.pool.gpu_v, a.pool.host_v, nullptr);
+      if (!g.ok) {
+        g.flush();
+        return;
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) before[j] = ref[j];
+      whole_before = whole;
+      have = true;
     }
     segs.done();
+  }
+  if (have && !*abort) {
+    advance();
+    load(before, whole_before, a.pool.gpu_v, a.pool.host_v, nullptr);
   }
   g.flush();
 }
@@ -503,20 +557,23 @@ __device__ __forceinline__ void walk_role(const Args& a, Bars& bar, Seg* ring, u
   const uint32_t row_off = (uint32_t)((r16 >> 3) * kGroupB + half * kHalfB + (r16 & 7) * 128);
   Walk walk;
   walk.init(a);
-  int nq = 0;
-  for (int k = 0;; ++k) {
-    Seg s;
-    walk.next(a, s);
-    bool ok = wait_or_abort(&bar.seg_free[k % kSegs], (uint32_t)((k / kSegs) & 1) ^ 1u, abort, a.status);
-    if (__any_sync(0xffffffffu, !ok)) return;
+  auto publish = [&](const Seg& x, int k) {
+    const bool ok = wait_or_abort(&bar.seg_free[k % kSegs], (uint32_t)((k / kSegs) & 1) ^ 1u, abort, a.status);
+    if (__any_sync(0xffffffffu, !ok)) return false;
     if (lane == 0) {
-      ring[k % kSegs] = s;
+      ring[k % kSegs] = x;
       mbar_arrive(&bar.seg[k % kSegs]);
     }
-    if (s.n == 0) return;
+    return true;
+  };
+  Seg s, s2;
+  walk.next(a, s);
+  int nq = 0, k = 0;
+  if (!publish(s, 0)) return;
+  while (s.n > 0) {
     for (int u = 0; u < (s.n1 > 0 ? 2 : 1); ++u, ++nq) {
       const int buf = nq & 1;
-      ok = wait_or_abort(&bar.qempty[buf], (uint32_t)((nq >> 1) & 1) ^ 1u, abort, a.status);
+      const bool ok = wait_or_abort(&bar.qempty[buf], (uint32_t)((nq >> 1) & 1) ^ 1u, abort, a.status);
       if (__any_sync(0xffffffffu, !ok)) return;
       const int live = u ? s.n1 : s.n0;
 #pragma unroll 2
@@ -531,58 +588,71 @@ __device__ __forceinline__ void walk_role(const Args& a, Bars& bar, Seg* ring, u
         }
       }
       cp_async_commit();
+      // the next segment goes out while the rows fly
+      if (u == (s.n1 > 0 ? 1 : 0)) {
+        walk.next(a, s2);
+        if (!publish(s2, ++k)) {
+          cp_async_wait<0>();
+          return;
+        }
+      }
       cp_async_wait<0>();
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.qfull[buf]);
     }
+    s = s2;
   }
 }
 
 // ---------------------------------------------------------------------------- MMA warp
-// A step as the issuing warp needs it, one word: ring stages and parities, first and last uses.
+// A step as its slot's issuing warp needs it, one word: ring stages and parities, the Q
+// buffer, first and last uses.  Every stage and Q buffer is handed back by two arrivals,
+// one of each slot, or both of one where the other does not use it.
 namespace step {
-constexpr uint32_t kStage = 7u, kKPar = 3, kVStage = 4, kVPar = 7, kQBuf = 8, kQPar = 9;
-constexpr uint32_t kKFirst = 1u << 10, kKLast = 1u << 11, kQFirst = 1u << 12, kQLast = 1u << 13, kOFirst = 1u << 14,
-                   kOLast = 1u << 15, kLive = 1u << 16;
+constexpr uint32_t kSeq = 15u, kKPar = 4, kV = 5, kVPar = 9, kQBuf = 10, kQPar = 11;  // kSeq: place in two rounds
+constexpr uint32_t kAlone = 1u << 12, kQAlone = 1u << 13, kFirst = 1u << 14, kLast = 1u << 15, kLive = 1u << 16;
 }  // namespace step
-// The step words of a segment, 32 at a time: lane j holds the j-th of them.
+// The slot's step words of a segment, 32 at a time: lane j holds the j-th of them.
 struct Steps {
   Segs segs;
   int total, base, pos, cnt;  // steps of the segment, of which base are behind this batch; the batch's next and count
-  int seq, nq;                // ring position (modulo two rounds) and Q buffers at the segment's start
+  int T, nq, x;               // tiles, Q buffers and steps (of both slots) before the segment
+  int n, sub, slot;
   bool two, open;
   uint32_t words;
   __device__ __forceinline__ uint32_t next() {
     if (pos == cnt) {
       base += cnt;
-      if (base == total) {
+      while (base == total) {  // a slot may have no step in a segment of one tile
         if (open) {
-          seq = (seq + 2 * (two ? total >> 1 : total)) % (2 * kRing);
+          T += n;
           nq += two ? 2 : 1;
+          x += two ? 2 * n : n;
           segs.done();
         }
         const Seg* s = segs.next();
         open = s != nullptr;
         total = base = pos = cnt = 0;
         if (!open) return 0u;
+        n = s->n;
         two = s->n1 > 0;
-        total = two ? 2 * s->n : s->n;
+        sub = slot ^ (x & 1);
+        total = two ? n : (n + 1 - sub) / 2;
       }
       cnt = total - base < 32 ? total - base : 32;
       pos = 0;
       const int j = base + (int)(threadIdx.x & 31);
-      const int tile = two ? j >> 1 : j;
-      const uint32_t second = two ? j & 1 : 0, per = two ? 2 : 1, q = (uint32_t)nq + second;
-      const uint32_t k = (uint32_t)(seq + 2 * tile) % (2 * kRing), v = k + 1 == 2 * kRing ? 0 : k + 1;
-      uint32_t c = step::kLive | k % kRing | (k / kRing) << step::kKPar | (v % kRing) << step::kVStage |
-                   (v / kRing) << step::kVPar | (q & 1u) << step::kQBuf | ((q >> 1) & 1u) << step::kQPar;
-      if (!second) c |= step::kKFirst;
-      if (!two || second) c |= step::kKLast;
-      if (j < (int)per) c |= step::kQFirst;
-      if (j >= total - (int)per) c |= step::kQLast;
-      if (j < 2) c |= step::kOFirst;
-      if (j >= total - 2) c |= step::kOLast;
+      const int tile = T + (two ? j : 2 * j + sub);
+      const uint32_t k = (uint32_t)k_seq(tile), v = (uint32_t)v_seq(tile);
+      constexpr uint32_t kTwo = 2 * kRing;
+      const uint32_t q = (uint32_t)(nq + (two ? sub : 0));
+      uint32_t c = step::kLive | k % kTwo | ((k / kTwo) & 1u) << step::kKPar | (v % kTwo) << step::kV |
+                   ((v / kTwo) & 1u) << step::kVPar | (q & 1u) << step::kQBuf | ((q >> 1) & 1u) << step::kQPar;
+      if (!two) c |= step::kAlone;
+      if (two || n == 1) c |= step::kQAlone;
+      if (j == 0) c |= step::kFirst;
+      if (j == total - 1) c |= step::kLast;
       words = c;
     }
     return __shfl_sync(0xffffffffu, words, pos++);
@@ -590,21 +660,22 @@ struct Steps {
 };
 
 __device__ __forceinline__ void mma_role(const Args& a, const Segs& segs, Bars& bar, uint32_t base, uint32_t tm,
-                                         volatile int* abort) {
+                                         int slot, volatile int* abort) {
   const uint32_t id_s = t5::idesc_bf16(128, 128, false), id_o = t5::idesc_bf16(128, 128, true);
   // descriptors of buffer 0; a buffer is kStageB / 16 further in the address field
   const uint64_t dq = t5::desc_sw128(base, 16, kGroupB), dk = t5::desc_sw128(base + kQBufs * kStageB, 16, kGroupB);
   const uint64_t dv = t5::desc_sw128(base + kQBufs * kStageB, kHalfB, kGroupB);
-  Steps gen{segs, 0, 0, 0, 0, 0, 0, false, false, 0u};
+  const uint32_t ts = tm + slot * 128, to = tm + 256 + slot * 128;
+  Steps gen{segs, 0, 0, 0, 0, 0, 0, 0, 0, 0, slot, false, false, 0u};
   bool ok = true;
   auto wait = [&](uint64_t* b, uint32_t parity) {
     if (ok) ok = wait_or_abort(b, parity, abort, a.status);
     ok = __all_sync(0xffffffffu, ok);
   };
-  auto issue_s = [&](uint32_t c, uint32_t slot, bool k_there) {
-    const uint32_t ks = c & step::kStage, qb = (c >> step::kQBuf) & 1u;
-    if (c & step::kQFirst) wait(&bar.qfull[qb], (c >> step::kQPar) & 1u);
-    if (!k_there) wait(&bar.full[ks], (c >> step::kKPar) & 1u);
+  auto issue_s = [&](uint32_t c, bool k_there) {
+    const uint32_t ksq = c & step::kSeq, ks = ksq >= kRing ? ksq - kRing : ksq, qb = (c >> step::kQBuf) & 1u;
+    if (c & step::kFirst) wait(&bar.qfull[qb], (c >> step::kQPar) & 1u);
+    if (!k_there) wait(&bar.full[ksq], (c >> step::kKPar) & 1u);
     if (!ok) return;
     t5::fence_after();
     const uint64_t qd = dq + qb * (kStageB >> 4), kd = dk + ks * (kStageB >> 4);
@@ -612,16 +683,20 @@ __device__ __forceinline__ void mma_role(const Args& a, const Segs& segs, Bars& 
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {  // 16 of the 128 dims each
         const uint32_t off = ((uint32_t)(kk >> 2) * kHalfB + (kk & 3) * 32) >> 4;
-        t5::mma(tm + slot * 128, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
+        t5::mma(ts, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
       }
       t5::commit(&bar.s[slot]);
-      if (c & step::kKLast) t5::commit(&bar.empty[ks]);
-      if (c & step::kQLast) t5::commit(&bar.qempty[qb]);
+      t5::commit(&bar.empty[ks]);
+      if (c & step::kAlone) t5::commit(&bar.empty[ks]);
+      if (c & step::kLast) {
+        t5::commit(&bar.qempty[qb]);
+        if (c & step::kQAlone) t5::commit(&bar.qempty[qb]);
+      }
     }
   };
-  auto issue_o = [&](uint32_t c, uint32_t slot, uint32_t p_par) {
-    const uint32_t vs = (c >> step::kVStage) & step::kStage;
-    if (c & step::kKFirst) wait(&bar.full[vs], (c >> step::kVPar) & 1u);
+  auto issue_o = [&](uint32_t c, uint32_t p_par) {
+    const uint32_t vsq = (c >> step::kV) & step::kSeq, vs = vsq >= kRing ? vsq - kRing : vsq;
+    wait(&bar.full[vsq], (c >> step::kVPar) & 1u);
     const uint64_t vd = dv + vs * (kStageB >> 4);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {  // 64 keys as soon as their P is there
@@ -631,36 +706,31 @@ __device__ __forceinline__ void mma_role(const Args& a, const Segs& segs, Bars& 
       if (t5::elect_one()) {
 #pragma unroll
         for (int kk = 4 * half; kk < 4 * half + 4; ++kk)  // 16 of the 128 keys each
-          t5::mma_ts(tm + 256 + slot * 128, tm + slot * 128 + kk * 8, vd + ((kk * 2 * kGroupB) >> 4), id_o,
-                     kk > 0 ? 1u : ((c & step::kOFirst) ? 0u : 1u));
+          t5::mma_ts(to, ts + kk * 8, vd + ((kk * 2 * kGroupB) >> 4), id_o,
+                     kk > 0 ? 1u : ((c & step::kFirst) ? 0u : 1u));
         if (half) {
-          if (c & step::kKLast) t5::commit(&bar.empty[vs]);
-          if (c & step::kOLast) t5::commit(&bar.o[slot]);
+          t5::commit(&bar.empty[vs]);
+          if (c & step::kAlone) t5::commit(&bar.empty[vs]);
+          if (c & step::kLast) t5::commit(&bar.o[slot]);
         }
       }
     }
   };
-  // whether a step's keys have landed (its K is shared with the step before, or the barrier says so)
-  auto k_there = [&](uint32_t c) {
-    return !(c & step::kKFirst) ||
-           __all_sync(0xffffffffu, mbar_try_wait(&bar.full[c & step::kStage], (c >> step::kKPar) & 1u));
-  };
-  // step y - 2's O, then S of step y in the same slot
-  uint32_t behind = 0u, last = 0u;  // steps y - 2 and y - 1, 0: none
-  for (uint32_t y = 0;; ++y) {
-    const uint32_t nx = last || y < 2 ? gen.next() : 0u;
-    if (!nx && !behind && !last) break;
-    const bool there = nx && k_there(nx);
-    if (behind) issue_o(behind, y & 1u, ((y >> 1) & 1u) ^ 1u);
-    if (ok && nx) issue_s(nx, y & 1u, there);
-    if (!ok) break;
-    behind = last;
-    last = nx;
+  uint32_t now = gen.next(), p_par = 0u;
+  if (now) issue_s(now, false);
+  while (ok && now) {  // O of a step, then S of the next one over its P
+    const uint32_t nx = gen.next();
+    const bool there =
+        nx && __all_sync(0xffffffffu, mbar_try_wait(&bar.full[nx & step::kSeq], (nx >> step::kKPar) & 1u));
+    issue_o(now, p_par);
+    if (ok && nx) issue_s(nx, there);
+    now = nx;
+    p_par ^= 1u;
   }
   // the operands in shared memory and TMEM outlive every MMA issued
   __syncwarp();
-  if (t5::elect_one()) t5::commit(&bar.drain);
-  mbar_wait_bounded(&bar.drain, 0u);
+  if (t5::elect_one()) t5::commit(&bar.drain[slot]);
+  mbar_wait_bounded(&bar.drain[slot], 0u);
 }
 
 // ---------------------------------------------------------------------------- softmax warps
@@ -812,11 +882,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&bar.full[i], 2);
-      mbar_init(&bar.empty[i], 1);
+      mbar_init(&bar.full[kRing + i], 2);
+      mbar_init(&bar.empty[i], 2);
     }
     for (int i = 0; i < kQBufs; ++i) {
       mbar_init(&bar.qfull[i], 1);
-      mbar_init(&bar.qempty[i], 1);
+      mbar_init(&bar.qempty[i], 2);
     }
     for (int i = 0; i < kMasks; ++i) mbar_init(&bar.mask[i], 1);
     for (int i = 0; i < 2; ++i) {
@@ -824,9 +895,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
       mbar_init(&bar.p[i][0], 128);
       mbar_init(&bar.p[i][1], 128);
       mbar_init(&bar.o[i], 1);
+      mbar_init(&bar.drain[i], 1);
     }
-    mbar_init(&bar.drain, 1);
-    fence_barrier_init();
+      fence_barrier_init();
     s_abort = 0;
   }
   if (warp == 0) {
@@ -842,20 +913,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
   pdl_wait();
   const uint32_t tm = s_tmem;
   const Segs segs{a, bar, ring, &s_abort, 0};
-  // 2 x 128 x 208 + 128 x 88 = 64,512 registers, what 384 threads of 168 were launched with
+  // 2 x 128 x 192 + 2 x 128 x 64 = 65,536 registers, what 512 threads of 128 were launched with
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     softmax_role(a, segs, bar, tm, masks, &s_abort);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 8)
       tma_role(a, &tk, &tv, segs, bar, base, &s_abort);
     else if (warp == 9)
       rows_role(a, segs, bar, gbase, masks, &s_abort);
     else if (warp == 10)
       walk_role(a, bar, ring, gbase, &s_abort);
-    else
-      mma_role(a, segs, bar, base, tm, &s_abort);
+    else if (warp < 13)
+      mma_role(a, segs, bar, base, tm, warp - 11, &s_abort);
   }
   t5::fence_before();
   __syncthreads();
