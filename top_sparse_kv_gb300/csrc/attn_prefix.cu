@@ -57,9 +57,8 @@ constexpr int kChunks = kTile / kChunk;
 constexpr int kRing = 5;               // K / V stages
 constexpr int kQBufs = 2;
 constexpr int kMasks = 8;              // key masks of the last tiles
-constexpr int kSegs = 8;               // segments published ahead
+constexpr int kSegs = 4;               // segments published ahead
 constexpr int kSegReaders = 12;        // warps that read them: 8 softmax, TMA, rows, 2 MMA
-constexpr int kSmem = (kQBufs + kRing) * kStageB + 1024;
 constexpr int kMaxGang = 4;            // pairs of row tiles that read the same keys together
 constexpr float kGrow = 8.f;           // log2 growth of a row's maximum that renews it
 constexpr uint32_t kTmemCols = 512;    // S0 S1 O0 O1, 128 columns each; P over the first 64 columns of S
@@ -94,8 +93,8 @@ struct Args {
   int shift;           // log2 of the block size, -1: not a power of two
   float scale_log2;
   Plan pl;
-  float *po, *pml;     // prefix partials: [(gang + unit) * members + member][2][...]
-  float *so, *sml;     // tail partials: [cta + unit][2][...]
+  float *po, *pml;     // prefix partials: [(gang + unit) * members + member][row tile, if two][...]
+  float *so, *sml;     // tail partials: [cta + unit][...]
   int *first, *last;   // [H * B]: the CTAs of a tail's first and last segment
   void* out;
   float* lse;
@@ -180,7 +179,8 @@ struct Walk {
     sb = __shfl_sync(0xffffffffu, fb, src);
     stile = __shfl_sync(0xffffffffu, ft, src);
   }
-  __device__ __forceinline__ void next(const Args& a, Seg& s) {
+  // the next segment of the prefix, which is cut without a look at memory
+  __device__ __forceinline__ bool next_prefix(const Args& a, Seg& s) {
     const Plan& pl = a.pl;
     const int c = blockIdx.x / pl.gang, member = blockIdx.x - c * pl.gang;
     while (p0 < p1) {
@@ -202,8 +202,12 @@ struct Walk {
       s.n0 = r < kTile ? r : kTile;
       s.n1 = r <= kTile ? 0 : (r - kTile < kTile ? r - kTile : kTile);
       s.tail = 0;
-      return;
+      return true;
     }
+    return false;
+  }
+  __device__ __forceinline__ void next(const Args& a, Seg& s) {
+    if (next_prefix(a, s)) return;
     if (!scanned) scan(a);
     while (srem > 0) {
       const int end = tail_end(a, sb), nt = tail_tiles(a, end);
@@ -270,11 +274,14 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
   return r;
 }
 
-// The ring's order of loads, for tile T of the CTA's tiles: K0 K1 V0 K2 V1 K3 V2 ... -- the
-// order of their first use when the slots take alternate tiles (S of step x + 2 follows
-// O of step x), so a load has two tiles' time to land.
-__device__ __forceinline__ int k_seq(int T) { return T > 0 ? 2 * T - 1 : 0; }
-__device__ __forceinline__ int v_seq(int T) { return 2 * T + 2; }
+// The ring's order of loads is that of their first use, so that each has about two tiles'
+// time to land.  Two row tiles: K0 V0 K1 V1 ...  One: K0 K1 V0 K2 V1 ... -- S of step x + 2
+// follows O of step x, so every V comes after the next tile's K, the segment's last one
+// after the K of the segment behind it (after the last segment that place stays empty).
+// A segment's places from its first one on, with `owed` = 1 where such a V comes into it:
+__device__ __forceinline__ int k_place(bool two, int owed, int i) { return i == 0 ? 0 : owed + 2 * i - (two ? 0 : 1); }
+__device__ __forceinline__ int v_place(bool two, int owed, int i) { return owed + 2 * i + (two ? 1 : 2); }
+__device__ __forceinline__ int places(bool two, int owed, int n) { return owed + 2 * n - (two ? 0 : 1); }
 
 // full: two barriers a stage, of alternate rounds of the ring.  A slot's warp waits for the
 // stages of its own steps only, so a stage may go through another round unseen by it; with
@@ -282,8 +289,20 @@ __device__ __forceinline__ int v_seq(int T) { return 2 * T + 2; }
 // round before on the same barrier (ten loads back) is over: the load that the warp saw
 // last was issued after it had been handed back.
 struct Bars {
-  uint64_t seg[kSegs], seg_free[kSegs], full[2 * kRing], empty[kRing], qfull[kQBufs], qempty[kQBufs], mask[kMasks], s[2], p[2][2], o[2], drain[2];
+  uint64_t seg[kSegs], seg_free[kSegs], full[2 * kRing], empty[kRing], qfull[kQBufs], qempty[kQBufs], mask[kMasks], s[2], p[2][2], o[2], x[2], drain[2];
 };
+
+struct Shared {
+  unsigned char buf[(kQBufs + kRing) * kStageB];  // first, on the 1 KB boundary of the swizzle
+  float2 xml[2 * kTile];                          // the slots' (m, l) of a row
+  uint4 masks[kMasks];
+  Seg ring[kSegs];
+  Bars bar;
+  uint32_t tmem;
+  volatile int abort;
+};
+static_assert(sizeof(Shared) <= 232448, "227 KB a CTA");
+constexpr int kSmem = (int)sizeof(Shared);
 
 // A role's place in the published segments.  next() waits for one (false: the share is
 // done, or the launch gives up); done() hands it back, once per warp.
@@ -293,6 +312,9 @@ struct Segs {
   const Seg* ring;
   volatile int* abort;
   int k;
+  __device__ __forceinline__ bool ready() const {
+    return __all_sync(0xffffffffu, mbar_try_wait(&bar.seg[k % kSegs], (uint32_t)(k / kSegs) & 1u));
+  }
   __device__ __forceinline__ const Seg* next() {
     const int i = k % kSegs;
     bool ok = wait_or_abort(&bar.seg[i], (uint32_t)(k / kSegs) & 1u, abort, a.status);
@@ -308,52 +330,44 @@ struct Segs {
 
 // ---------------------------------------------------------------------------- gather warps
 // The row warp's copies are announced on their stage's barrier by the warp once they have
-// landed.  While the next stage has rows too, announcements are put off (the copies keep
-// flying) until a stage is waited for: what frees it may need the tiles in flight, so the
-// oldest are announced, one at a time, until it is free.
+// landed: two copy groups fly while the next is issued, and a wait for a free stage
+// announces what is in flight first (what frees it may need those tiles).
 struct Rows {
   const Args& a;
   volatile int* abort;
-  uint64_t* pend[kRing];  // barriers of unannounced copy groups, oldest first
-  int n;
+  uint64_t *older, *newer;  // barriers of the unannounced copy groups (null: none)
   bool ok;
 
-  __device__ __forceinline__ void announce_oldest() {
-    switch (n) {  // cp.async.wait_group takes a constant
-      case 1: cp_async_wait<0>(); break;
-      case 2: cp_async_wait<1>(); break;
-      case 3: cp_async_wait<2>(); break;
-      case 4: cp_async_wait<3>(); break;
-      default: cp_async_wait<4>(); break;
-    }
+  __device__ __forceinline__ void announce(uint64_t* b) {
     fence_proxy_async_smem();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(pend[0]);
-    --n;
-#pragma unroll
-    for (int i = 0; i + 1 < kRing; ++i) pend[i] = pend[i + 1];
+    if ((threadIdx.x & 31) == 0) mbar_arrive(b);
   }
   __device__ __forceinline__ void commit(uint64_t* b) {
     cp_async_commit();
-    if (n == kRing) announce_oldest();
-#pragma unroll
-    for (int i = 0; i < kRing; ++i)
-      if (i == n) pend[i] = b;
-    ++n;
-  }
-  __device__ __forceinline__ void wait_free(uint64_t* b, uint32_t parity) {
-    while (__any_sync(0xffffffffu, !mbar_try_wait(b, parity))) {
-      if (n > 0) {
-        announce_oldest();
-        continue;
-      }
-      ok = wait_or_abort(b, parity, abort, a.status);
-      ok = !__any_sync(0xffffffffu, !ok);
-      return;
+    if (older) {
+      cp_async_wait<2>();
+      announce(older);
     }
+    older = newer;
+    newer = b;
   }
   __device__ __forceinline__ void flush() {
-    while (n > 0) announce_oldest();
+    if (older) {
+      cp_async_wait<1>();
+      announce(older);
+    }
+    if (newer) {
+      cp_async_wait<0>();
+      announce(newer);
+    }
+    older = newer = nullptr;
+  }
+  __device__ __forceinline__ void wait_free(uint64_t* b, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return;
+    flush();
+    ok = wait_or_abort(b, parity, abort, a.status);
+    ok = !__any_sync(0xffffffffu, !ok);
   }
 };
 
@@ -370,6 +384,9 @@ __device__ __forceinline__ long long row_ref(const Args& a, int h, int e, int t)
   return tc::kHostBit | ((hb * a.H + h) * a.bs + in_block(a, t));
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 // 16 keys' rows of 256 bytes of a pool viewed as [rows / 8][2 halves][8 rows][64 dims]
 __device__ __forceinline__ void tma_chunk(uint32_t dst, const CUtensorMap* map, int group, uint64_t* bar) {
   asm volatile(
@@ -392,8 +409,15 @@ __device__ __forceinline__ int chunk_group(const Args& a, int h, int e, int t0, 
 __device__ __forceinline__ void tma_role(const Args& a, const CUtensorMap* tk, const CUtensorMap* tv, Segs segs,
                                          Bars& bar, uint32_t base, volatile int* abort) {
   const int lane = threadIdx.x & 31;
+  if (a.tma && t5::elect_one()) {
+    prefetch_map(tk);
+    prefetch_map(tv);
+  }
+  pdl_wait();
   uint32_t sq = 0, par = 1;  // place in two rounds of the ring, parity of the stage's free phase
+  int issued = 0;
   auto advance = [&] {
+    ++issued;
     if (++sq == 2 * kRing) sq = 0;
     if (sq == 0 || sq == kRing) par ^= 1u;
   };
@@ -420,16 +444,13 @@ __device__ __forceinline__ void tma_role(const Args& a, const CUtensorMap* tk, c
     advance();
     return true;
   };
-  // the launch gives up: the copies in flight land (or their time runs out) before the memory goes
-  int issued = 0;
-  auto drain = [&] {
-    for (int q = issued > kRing ? issued - kRing : 0; q < issued; ++q)
-      mbar_wait_bounded(&bar.full[q % (2 * kRing)], (uint32_t)(q / (2 * kRing)) & 1u, 20000000LL);
-  };
-  int before = 0;           // the tile before's groups: its V follows this tile's K
-  bool have = false;
-  while (const Seg* s = segs.next()) {
+  int before = 0;           // groups of the tile whose V is owed
+  bool owed = false, ok = true;
+  while (ok) {
+    const Seg* s = segs.next();
+    if (s == nullptr) break;
     const int n = s->n, h = s->h;
+    const bool two = s->n1 > 0;
     int t0 = s->t0, e = chunk_entry(a, s, t0, lane), mine = -1;
     for (int i = 0; i < n; ++i, t0 += kTile) {
       if ((i & 3) == 0) {  // four tiles' entries at once, the next four already on their way
@@ -437,31 +458,31 @@ __device__ __forceinline__ void tma_role(const Args& a, const CUtensorMap* tk, c
         e = chunk_entry(a, s, t0 + 4 * kTile, lane);
       }
       const int now = __shfl_sync(0xffffffffu, mine, (8 * (i & 3) + lane) & 31);
+      // this tile's K, a V that is owed, this tile's V with two row tiles
+      const int loads = 1 + owed + two;
 #pragma unroll 1
-      for (int kv = have ? 0 : 1; kv < 2; ++kv)  // (the first tile: its K alone)
-        if (load(kv == (have ? 1 : 2) ? tv : tk, kv == (have ? 1 : 2) ? before : now)) {
-          ++issued;
-        } else {
-          drain();
-          return;
-        }
+      for (int u = 0; ok && u < loads; ++u) ok = load(u ? tv : tk, u == 1 && owed ? before : now);
+      if (!ok) break;
       before = now;
-      have = true;
+      owed = !two;
     }
     segs.done();
   }
-  if (have && !*abort) {
+  if (ok && owed && !*abort) {
     advance();  // no K follows the last tile: its place stays empty
-    load(tv, before);
-  } else if (have) {
-    drain();
+    ok = load(tv, before);
+  }
+  if (!ok || *abort) {  // the launch gives up: copies in flight land (or their time runs out) before the memory goes
+    for (int q = issued > kRing ? issued - kRing : 0; q < issued; ++q)
+      mbar_wait_bounded(&bar.full[q % (2 * kRing)], (uint32_t)(q / (2 * kRing)) & 1u, 20000000LL);
   }
 }
 
 __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, unsigned char* gbase, uint4* masks,
                                           volatile int* abort) {
   const int lane = threadIdx.x & 31;
-  Rows g{a, abort, {}, 0, true};
+  pdl_wait();
+  Rows g{a, abort, nullptr, nullptr, true};
   const int r16 = lane >> 1, half = lane & 1;  // a lane copies half a row
   const uint32_t row_off = (uint32_t)((r16 >> 3) * kGroupB + half * kHalfB + (r16 & 7) * 128);
   int T = 0;
@@ -500,17 +521,18 @@ __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, u
     }
     advance();
   };
-  long long before[4];
+  long long before[4];  // the tile whose V is owed
   uint32_t whole_before = 0;
-  bool have = false;
-  while (true) {
-    g.flush();  // before a wait that does not announce
+  bool owed = false;
+  while (g.ok) {
+    if (!segs.ready()) g.flush();  // a wait that does not announce
     const Seg* s = segs.next();
     if (s == nullptr) break;
     const int n = s->n, h = s->h;
+    const bool two = s->n1 > 0;
     int t0 = s->t0, e = chunk_entry(a, s, t0, lane);
     uint32_t all = 0;
-    for (int i = 0; i < n; ++i, ++T, t0 += kTile) {
+    for (int i = 0; g.ok && i < n; ++i, ++T, t0 += kTile) {
       if ((i & 3) == 0) {
         all = __ballot_sync(0xffffffffu, chunk_group(a, h, e, t0, lane) >= 0);
         e = chunk_entry(a, s, t0 + 4 * kTile, lane);
@@ -530,19 +552,16 @@ __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, u
         }
       }
       load(ref, whole, a.pool.gpu_k, a.pool.host_k, mask);
-      if (g.ok && have) load(before, whole_before, a.pool.gpu_v, a.pool.host_v, nullptr);
-      if (!g.ok) {
-        g.flush();
-        return;
-      }
+      if (g.ok && owed) load(before, whole_before, a.pool.gpu_v, a.pool.host_v, nullptr);
+      if (g.ok && two) load(ref, whole, a.pool.gpu_v, a.pool.host_v, nullptr);
 #pragma unroll
       for (int j = 0; j < 4; ++j) before[j] = ref[j];
       whole_before = whole;
-      have = true;
+      owed = !two;
     }
     segs.done();
   }
-  if (have && !*abort) {
+  if (g.ok && owed && !*abort) {
     advance();
     load(before, whole_before, a.pool.gpu_v, a.pool.host_v, nullptr);
   }
@@ -567,9 +586,14 @@ __device__ __forceinline__ void walk_role(const Args& a, Bars& bar, Seg* ring, u
     return true;
   };
   Seg s, s2;
-  walk.next(a, s);
   int nq = 0, k = 0;
-  if (!publish(s, 0)) return;
+  const bool early = walk.next_prefix(a, s);
+  if (early && !publish(s, 0)) return;
+  pdl_wait();
+  if (!early) {
+    walk.next(a, s);
+    if (!publish(s, 0)) return;
+  }
   while (s.n > 0) {
     for (int u = 0; u < (s.n1 > 0 ? 2 : 1); ++u, ++nq) {
       const int buf = nq & 1;
@@ -617,7 +641,8 @@ constexpr uint32_t kAlone = 1u << 12, kQAlone = 1u << 13, kFirst = 1u << 14, kLa
 struct Steps {
   Segs segs;
   int total, base, pos, cnt;  // steps of the segment, of which base are behind this batch; the batch's next and count
-  int T, nq, x;               // tiles, Q buffers and steps (of both slots) before the segment
+  int at, owed;               // the segment's first place in the ring, a V owed to it
+  int nq, x;                  // Q buffers and steps (of both slots) before the segment
   int n, sub, slot;
   bool two, open;
   uint32_t words;
@@ -626,7 +651,8 @@ struct Steps {
       base += cnt;
       while (base == total) {  // a slot may have no step in a segment of one tile
         if (open) {
-          T += n;
+          at += places(two, owed, n);
+          owed = two ? 0 : 1;
           nq += two ? 2 : 1;
           x += two ? 2 * n : n;
           segs.done();
@@ -643,8 +669,8 @@ struct Steps {
       cnt = total - base < 32 ? total - base : 32;
       pos = 0;
       const int j = base + (int)(threadIdx.x & 31);
-      const int tile = T + (two ? j : 2 * j + sub);
-      const uint32_t k = (uint32_t)k_seq(tile), v = (uint32_t)v_seq(tile);
+      const int tile = two ? j : 2 * j + sub;
+      const uint32_t k = (uint32_t)(at + k_place(two, owed, tile)), v = (uint32_t)(at + v_place(two, owed, tile));
       constexpr uint32_t kTwo = 2 * kRing;
       const uint32_t q = (uint32_t)(nq + (two ? sub : 0));
       uint32_t c = step::kLive | k % kTwo | ((k / kTwo) & 1u) << step::kKPar | (v % kTwo) << step::kV |
@@ -666,7 +692,7 @@ __device__ __forceinline__ void mma_role(const Args& a, const Segs& segs, Bars& 
   const uint64_t dq = t5::desc_sw128(base, 16, kGroupB), dk = t5::desc_sw128(base + kQBufs * kStageB, 16, kGroupB);
   const uint64_t dv = t5::desc_sw128(base + kQBufs * kStageB, kHalfB, kGroupB);
   const uint32_t ts = tm + slot * 128, to = tm + 256 + slot * 128;
-  Steps gen{segs, 0, 0, 0, 0, 0, 0, 0, 0, 0, slot, false, false, 0u};
+  Steps gen{segs, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, slot, false, false, 0u};
   bool ok = true;
   auto wait = [&](uint64_t* b, uint32_t parity) {
     if (ok) ok = wait_or_abort(b, parity, abort, a.status);
@@ -734,12 +760,13 @@ __device__ __forceinline__ void mma_role(const Args& a, const Segs& segs, Bars& 
 }
 
 // ---------------------------------------------------------------------------- softmax warps
-__device__ __forceinline__ void softmax_role(const Args& a, Segs segs, Bars& bar, uint32_t tm, const uint4* masks,
+__device__ __forceinline__ void softmax_role(const Args& a, Segs segs, Bars& bar, uint32_t tm, const uint4* masks, float2* xml,
                              volatile int* abort) {
   const int slot = threadIdx.x >> 7, wq = (threadIdx.x >> 5) & 3, row = threadIdx.x & 127;
   const uint32_t lanes = (uint32_t)(wq * 32) << 16;
   const uint32_t ts = tm + lanes + slot * 128, to = tm + lanes + 256 + slot * 128;
-  int x = 0, T = 0, ns = 0, no = 0;
+  pdl_wait();  // before the first partial: the workspace is the call before's until then
+  int x = 0, T = 0, ns = 0, no = 0, nx = 0;
   bool ok = true;
   const Seg* sp;
   while (ok && (sp = segs.next()) != nullptr) {
@@ -836,10 +863,11 @@ __device__ __forceinline__ void softmax_role(const Args& a, Segs segs, Bars& bar
     }
     // the segment's partial, head-fastest in groups of 4 dims: [dim / 4][row][4]
     const int rp = s.tail ? a.G : a.pl.rp;
-    float* po = (s.tail ? a.so : a.po) + (size_t)(2 * s.part + sub) * rp * kD;
-    float* ml = (s.tail ? a.sml : a.pml) + (size_t)(2 * s.part + sub) * rp * 2;
-    if (ok && warp_live) {
-      if (mine > 0) {
+    const size_t at = (size_t)(s.tail ? s.part : 2 * s.part + (two ? sub : 0)) * rp;
+    float* po = (s.tail ? a.so : a.po) + at * kD;
+    float* ml = (s.tail ? a.sml : a.pml) + at * 2;
+    if (two || s.n == 1) {  // the slot's own
+      if (ok && warp_live && mine > 0) {
 #pragma unroll 1
         for (int ch = 0; ch < 4; ++ch) {
           uint32_t o[32];
@@ -850,11 +878,48 @@ __device__ __forceinline__ void softmax_role(const Args& a, Segs segs, Bars& bar
               *reinterpret_cast<uint4*>(po + ((size_t)(ch * 8 + i) * rp + row) * 4) =
                   make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
+        if (row < live_rows) {
+          ml[row] = m;
+          ml[rp + row] = l;
+        }
       }
-      if (row < live_rows) {
-        ml[row] = mine > 0 ? m : -INFINITY;  // no tile: an empty partial
-        ml[rp + row] = l;
+    } else {
+      // the slots took alternate tiles of the same rows: each joins half of the dims of both
+      // (a row's TMEM lane is the same for the two slots' warps)
+      xml[slot * kTile + row] = make_float2(m, l);
+      mbar_arrive(&bar.x[0]);
+      ok = ok && wait_or_abort(&bar.x[0], (uint32_t)nx & 1u, abort, a.status);
+      ok = !__any_sync(0xffffffffu, !ok);
+      if (ok && warp_live) {
+        t5::fence_after();
+        const float2 m0 = xml[row], m1 = xml[kTile + row];
+        const float mm = m0.x != m0.x || m1.x != m1.x ? NAN : fmaxf(m0.x, m1.x);
+        const float w0 = m0.x == -INFINITY ? 0.f : ex2(m0.x - mm), w1 = m1.x == -INFINITY ? 0.f : ex2(m1.x - mm);
+#pragma unroll 1
+        for (int ch = 2 * slot; ch < 2 * slot + 2; ++ch) {
+          uint32_t o[32], o1[32];
+          t5::ld32(tm + lanes + 256 + ch * 32, o);
+          t5::ld32(tm + lanes + 384 + ch * 32, o1);
+          if (row < live_rows)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float c[4];
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                c[u] = w0 * __uint_as_float(o[4 * i + u]) + w1 * __uint_as_float(o1[4 * i + u]);
+              *reinterpret_cast<float4*>(po + ((size_t)(ch * 8 + i) * rp + row) * 4) = make_float4(c[0], c[1], c[2], c[3]);
+            }
+        }
+        if (slot == 0 && row < live_rows) {
+          ml[row] = mm;
+          ml[rp + row] = w0 * m0.y + w1 * m1.y;
+        }
       }
+      // neither slot's O is overwritten before both have read it
+      t5::fence_before();
+      mbar_arrive(&bar.x[1]);
+      ok = ok && wait_or_abort(&bar.x[1], (uint32_t)(nx++) & 1u, abort, a.status);
+      ok = !__any_sync(0xffffffffu, !ok);
     }
     x += two ? 2 * s.n : s.n;
     T += s.n;
@@ -865,16 +930,15 @@ __device__ __forceinline__ void softmax_role(const Args& a, Segs segs, Bars& bar
 __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_constant__ CUtensorMap tk,
                                                                   const __grid_constant__ CUtensorMap tv,
                                                                   const Args a) {
-  extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) Bars bar;
-  __shared__ __align__(16) uint4 masks[kMasks];
-  __shared__ Seg ring[kSegs];
-  __shared__ uint32_t s_tmem;
-  __shared__ volatile int s_abort;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  Shared& sh = *reinterpret_cast<Shared*>(smem);
+  Bars& bar = sh.bar;
   const int t = threadIdx.x, warp = t >> 5;
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  unsigned char* gbase = smem_raw + (base - raw);
+  const uint32_t base = smem_u32(smem);
+  if (base & 1023u) {  // the swizzle counts address bits from a 1 KB boundary
+    flag(a.status, SKV_DEV_TIMEOUT);
+    return;
+  }
   if (t == 0) {
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&bar.seg[i], 1);
@@ -895,13 +959,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
       mbar_init(&bar.p[i][0], 128);
       mbar_init(&bar.p[i][1], 128);
       mbar_init(&bar.o[i], 1);
+      mbar_init(&bar.x[i], 256);
       mbar_init(&bar.drain[i], 1);
     }
       fence_barrier_init();
-    s_abort = 0;
+    sh.abort = 0;
   }
   if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
                  "r"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -909,24 +974,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
   t5::fence_before();
   __syncthreads();
   t5::fence_after();
-  pdl_release();
-  pdl_wait();
-  const uint32_t tm = s_tmem;
-  const Segs segs{a, bar, ring, &s_abort, 0};
+  pdl_release();  // every role that touches global memory waits for the kernels before by itself
+  const uint32_t tm = sh.tmem;
+  const Segs segs{a, bar, sh.ring, &sh.abort, 0};
   // 2 x 128 x 192 + 2 x 128 x 64 = 65,536 registers, what 512 threads of 128 were launched with
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-    softmax_role(a, segs, bar, tm, masks, &s_abort);
+    softmax_role(a, segs, bar, tm, sh.masks, sh.xml, &sh.abort);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 8)
-      tma_role(a, &tk, &tv, segs, bar, base, &s_abort);
+      tma_role(a, &tk, &tv, segs, bar, base, &sh.abort);
     else if (warp == 9)
-      rows_role(a, segs, bar, gbase, masks, &s_abort);
+      rows_role(a, segs, bar, smem, sh.masks, &sh.abort);
     else if (warp == 10)
-      walk_role(a, bar, ring, gbase, &s_abort);
+      walk_role(a, bar, sh.ring, smem, &sh.abort);
     else if (warp < 13)
-      mma_role(a, segs, bar, base, tm, warp - 11, &s_abort);
+      mma_role(a, segs, bar, base, tm, warp - 11, &sh.abort);
   }
   t5::fence_before();
   __syncthreads();
@@ -938,16 +1002,33 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
 
 // Joins the partials of 32 query rows of one KV head, kMergeDims of the 128 dims a CTA:
 // lane = row, warp = (4 dims, one of kMergeParts shares of the partials), so every load of
-// a partial is a coalesced float4 and a thread's loads are independent.  Two passes: the
-// row's maximum over its partials, then the weighted sums, joined in a fixed order.
+// a partial is a coalesced float4.  A thread runs once over its share with a running
+// maximum, kMergeBatch partials' loads in flight at a time; the shares are joined through
+// shared memory.  The order is fixed.
 constexpr int kMergeParts = 4;
 constexpr int kMergeDims = 16;
 constexpr int kMergeWarps = kMergeParts * kMergeDims / 4;
+constexpr int kMergeBatch = 4;
+
+struct Joined {
+  float m, l;
+  float4 o;
+  __device__ __forceinline__ void add(float mp, float lp, float4 v) {
+    if (mp == -INFINITY) return;  // an empty partial: its O was never written
+    const float mn = mp != mp ? mp : fmaxf(m, mp);  // NaN stays: m, or the weights from then on
+    const float f = m == -INFINITY ? 0.f : ex2(m - mn), w = ex2(mp - mn);
+    m = mn;
+    l = fmaf(w, lp, l * f);
+    o.x = fmaf(w, v.x, o.x * f);
+    o.y = fmaf(w, v.y, o.y * f);
+    o.z = fmaf(w, v.z, o.z * f);
+    o.w = fmaf(w, v.w, o.w * f);
+  }
+};
 
 __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Args a) {
-  __shared__ float s_m[kMergeWarps][32];
   __shared__ float4 s_o[kMergeWarps][32];
-  __shared__ float s_l[kMergeWarps][32];
+  __shared__ float2 s_ml[kMergeWarps][32];
   pdl_release();
   const Plan& pl = a.pl;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -955,7 +1036,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Ar
   const int h = blockIdx.x / blocks, row = (blockIdx.x - h * blocks) * 32 + lane;
   const bool live = row < pl.rows;
   const int b = live ? row / a.G : 0, g = row - b * a.G;
-  // the prefix's partials of this row: gangs c0 .. c0 + nc - 1 of its unit
+  // the prefix's partials of this row: gangs c0 .. of its unit
   const int pair = row / (2 * kTile), pg = pair / pl.gang, member = pair - pg * pl.gang;
   const int up = h * pl.groups + pg;
   const bool two = pl.rows - pair * 2 * kTile > kTile;
@@ -965,83 +1046,71 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Ar
   if (pl.ntp > 0) {
     c0 = (int)(((u0 + 1) * pl.gangs - 1) / tp);
     np = (int)(((u0 + pl.ntp) * pl.gangs - 1) / tp) - c0 + 1;
-    if (!two) np *= 2;  // both slots' partials are of this row tile
   }
-  // partial i: (gang c0 + i, this row tile), or (gang c0 + i / 2, slot i % 2)
   const long long first_p = 2 * ((long long)(c0 + up) * pl.gang + member) + (two ? (row / kTile) & 1 : 0);
-  const long long step_p = 2 * pl.gang;
-  auto p_at = [&](int i) { return two ? first_p + i * step_p : first_p + (i >> 1) * step_p + (i & 1); };
+  const int step_p = 2 * pl.gang;
+  const int part = warp / (kMergeDims / 4), d4 = blockIdx.y * (kMergeDims / 4) + warp % (kMergeDims / 4);
+  const float* po = a.po + first_p * pl.rp * kD + ((size_t)d4 * pl.rp + r_in) * 4;
+  const float* pml = a.pml + first_p * pl.rp * 2 + r_in;
+  const int unit = h * a.B + b;
   pdl_wait();
   int L = live ? a.seq_lens[b] : 0;
+  const int f = a.first[unit], e = a.last[unit];  // of no meaning without a tail
+  Joined j{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int i = part; i < np; i += kMergeParts * kMergeBatch) {
+    float mp[kMergeBatch], lp[kMergeBatch];
+    float4 v[kMergeBatch];
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) {
+      const int k = i + u * kMergeParts;
+      mp[u] = -INFINITY;
+      if (k < np && live) {
+        const size_t at = (size_t)(k * step_p) * pl.rp;
+        mp[u] = pml[at * 2];
+        lp[u] = pml[at * 2 + pl.rp];
+        v[u] = *reinterpret_cast<const float4*>(po + at * kD);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) j.add(mp[u], lp[u], v[u]);
+  }
   if (L < 0 || L > a.max_len || (L > 0 && L < a.P)) {
     if (blockIdx.y == 0 && warp == 0) flag(a.status, SKV_DEV_BAD_LENGTH);
     L = L > a.max_len ? a.max_len : 0;
   }
-  const bool on = L > 0;
-  if (!on) np = 0;
-  // the tail's: 2 (e - f + 1) consecutive ones of its unit
-  const int unit = h * a.B + b;
-  int nt = 0;
-  long long first_t = 0;
-  if (on && L > a.P) {
-    const int f = a.first[unit], e = a.last[unit];
-    if (f >= 0 && e < kCtas && f <= e) {  // else never written: an aborted launch
-      nt = 2 * (e - f + 1);
-      first_t = 2 * ((long long)f + unit);
+  // the tail's partials: e - f + 1 consecutive ones of its unit
+  if (L > a.P && f >= 0 && e < kCtas && f <= e) {  // (else never written: an aborted launch)
+    const size_t at = (size_t)((long long)f + unit) * a.G;
+    const float* so = a.so + at * kD + ((size_t)d4 * a.G + g) * 4;
+    const float* sml = a.sml + at * 2 + g;
+    const int nt = e - f + 1;
+#pragma unroll 2
+    for (int i = part; i < nt; i += kMergeParts) {
+      const size_t k = (size_t)i * a.G;
+      j.add(sml[k * 2], sml[k * 2 + a.G], *reinterpret_cast<const float4*>(so + k * kD));
     }
   }
-  float m = -INFINITY;
-  for (int i = warp; i < np; i += kMergeWarps) m = fmaxf(m, a.pml[p_at(i) * pl.rp * 2 + r_in]);
-  for (int i = warp; i < nt; i += kMergeWarps) m = fmaxf(m, a.sml[(first_t + i) * a.G * 2 + g]);
-  s_m[warp][lane] = m;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kMergeWarps; ++i) m = fmaxf(m, s_m[i][lane]);
-  const int part = warp / (kMergeDims / 4), d4 = blockIdx.y * (kMergeDims / 4) + warp % (kMergeDims / 4);
-  float l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](const float* ml, const float* po, int rp, int r) {
-    const float mp = ml[r], lp = ml[rp + r];
-    const float4 v = *reinterpret_cast<const float4*>(po + ((size_t)d4 * rp + r) * 4);
-    if (mp == -INFINITY) return;  // an empty partial: its O was never written
-    const float w = exp2f(mp - m);
-    l = fmaf(w, lp, l);
-    o.x = fmaf(w, v.x, o.x);
-    o.y = fmaf(w, v.y, o.y);
-    o.z = fmaf(w, v.z, o.z);
-    o.w = fmaf(w, v.w, o.w);
-  };
-#pragma unroll 4
-  for (int i = part; i < np; i += kMergeParts) {
-    const long long at = p_at(i) * pl.rp;
-    add(a.pml + at * 2, a.po + at * kD, pl.rp, r_in);
-  }
-#pragma unroll 2
-  for (int i = part; i < nt; i += kMergeParts) {
-    const long long at = (first_t + i) * a.G;
-    add(a.sml + at * 2, a.so + at * kD, a.G, g);
-  }
-  s_o[warp][lane] = o;
-  s_l[warp][lane] = l;
+  s_o[warp][lane] = j.o;
+  s_ml[warp][lane] = make_float2(j.m, j.l);
   __syncthreads();
   if (part > 0 || !live) return;
 #pragma unroll
   for (int i = 1; i < kMergeParts; ++i) {
     const int from = i * (kMergeDims / 4) + warp;
-    const float4 v = s_o[from][lane];
-    l += s_l[from][lane];
-    o.x += v.x;
-    o.y += v.y;
-    o.z += v.z;
-    o.w += v.w;
+    const float2 ml = s_ml[from][lane];
+    j.add(ml.x, ml.y, s_o[from][lane]);
   }
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // NaN stays NaN; no key at all: 0
+  const bool on = L > 0;
+  // NaN stays NaN; an empty request, or no key at all: 0
+  const float inv = on && (j.l > 0.f || j.l != j.l) ? 1.f / j.l : 0.f;
   const size_t hq = (size_t)b * a.Hq + (size_t)h * a.G + g;
-  uint2 r;
-  r.x = tc::pack_bf16(o.x * inv, o.y * inv);
-  r.y = tc::pack_bf16(o.z * inv, o.w * inv);
+  uint2 r = make_uint2(0u, 0u);
+  if (on && inv != 0.f) {
+    r.x = tc::pack_bf16(j.o.x * inv, j.o.y * inv);
+    r.y = tc::pack_bf16(j.o.z * inv, j.o.w * inv);
+  }
   *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out + hq * kD + d4 * 4) = r;
-  if (a.lse && d4 == 0) a.lse[hq] = l > 0.f || l != l ? kLn2 * (m + log2f(l)) : -INFINITY;
+  if (a.lse && d4 == 0) a.lse[hq] = on && (j.l > 0.f || j.l != j.l) ? kLn2 * (j.m + log2f(j.l)) : -INFINITY;
 }
 
 // A pool's K or V rows as [rows / 8][2 halves of the dims][8 rows][64 dims], in boxes of 16
@@ -1065,7 +1134,7 @@ Layout layout_of(const skv_problem& p, int P) {
   const Plan pl = plan_of(p.batch, p.n_kv_heads, G, P);
   const size_t units = (size_t)p.n_kv_heads * p.batch;
   const size_t pp = pl.ntp > 0 ? 2 * (size_t)(pl.gangs + (size_t)p.n_kv_heads * pl.groups) * pl.gang * pl.rp : 0;
-  const size_t sp = P < p.max_len ? 2 * (kCtas + units) * G : 0;
+  const size_t sp = P < p.max_len ? (kCtas + units) * G : 0;
   Layout l;
   l.po = 0;
   l.pml = l.po + align256(pp * kD * 4);
