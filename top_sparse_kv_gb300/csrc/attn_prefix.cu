@@ -289,7 +289,7 @@ __device__ __forceinline__ int places(bool two, int owed, int n) { return owed +
 // round before on the same barrier (ten loads back) is over: the load that the warp saw
 // last was issued after it had been handed back.
 struct Bars {
-  uint64_t seg[kSegs], seg_free[kSegs], full[2 * kRing], empty[kRing], qfull[kQBufs], qempty[kQBufs], mask[kMasks], s[2], p[2][2], o[2], x[2], drain[2];
+  uint64_t seg[kSegs], seg_free[kSegs], full[2 * kRing], empty[kRing], qfull[kQBufs], qempty[kQBufs], mask[kMasks], s[2], p[2][2], o[2], x[2], turn[2], drain[2];
 };
 
 struct Shared {
@@ -720,6 +720,12 @@ __device__ __forceinline__ void mma_role(const Args& a, const Segs& segs, Bars& 
       }
     }
   };
+  // The slots' MMAs go in turns, O of a step and S of the next together: shared between the
+  // slots, the pipe would finish both late and the softmaxes would run, and wait, in phase
+  // (batch 64 on 128K keys: 322 us without turns).
+  auto pass_turn = [&] {
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bar.turn[slot ^ 1]);
+  };
   auto issue_o = [&](uint32_t c, uint32_t p_par) {
     const uint32_t vsq = (c >> step::kV) & step::kSeq, vs = vsq >= kRing ? vsq - kRing : vsq;
     wait(&bar.full[vsq], (c >> step::kVPar) & 1u);
@@ -727,6 +733,7 @@ __device__ __forceinline__ void mma_role(const Args& a, const Segs& segs, Bars& 
 #pragma unroll
     for (int half = 0; half < 2; ++half) {  // 64 keys as soon as their P is there
       wait(&bar.p[slot][half], p_par);
+      if (half == 0) wait(&bar.turn[slot], p_par ^ (slot ? 0u : 1u));
       if (!ok) return;
       t5::fence_after();
       if (t5::elect_one()) {
@@ -749,7 +756,9 @@ __device__ __forceinline__ void mma_role(const Args& a, const Segs& segs, Bars& 
     const bool there =
         nx && __all_sync(0xffffffffu, mbar_try_wait(&bar.full[nx & step::kSeq], (nx >> step::kKPar) & 1u));
     issue_o(now, p_par);
+    if (!there) pass_turn();  // nothing to follow yet: the other slot need not wait for it
     if (ok && nx) issue_s(nx, there);
+    if (there) pass_turn();
     now = nx;
     p_par ^= 1u;
   }
@@ -960,6 +969,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
       mbar_init(&bar.p[i][1], 128);
       mbar_init(&bar.o[i], 1);
       mbar_init(&bar.x[i], 256);
+      mbar_init(&bar.turn[i], 1);
       mbar_init(&bar.drain[i], 1);
     }
       fence_barrier_init();
