@@ -283,11 +283,40 @@ __device__ __forceinline__ int k_place(bool two, int owed, int i) { return i == 
 __device__ __forceinline__ int v_place(bool two, int owed, int i) { return owed + 2 * i + (two ? 1 : 2); }
 __device__ __forceinline__ int places(bool two, int owed, int n) { return owed + 2 * n - (two ? 0 : 1); }
 
+// wait_or_abort with the spin out of line: the roles' loops stay small (instruction fetch
+// is what the CTA's warps, at different places of the code, run short of first).
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
+  const long long t0 = clock64();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > 4000000000LL) {
+      *abort = 1;
+      if (status) atomicOr(status, SKV_DEV_TIMEOUT);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
+  return mbar_try_wait(bar, parity) || wait_slow(smem_u32(bar), parity, abort, status);
+}
+
 // full: two barriers a stage, of alternate rounds of the ring.  A slot's warp waits for the
 // stages of its own steps only, so a stage may go through another round unseen by it; with
 // one barrier the parity it waits for could be that of two rounds before.  With two, the
 // round before on the same barrier (ten loads back) is over: the load that the warp saw
 // last was issued after it had been handed back.
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr) : "memory");
+}
 struct Bars {
   uint64_t seg[kSegs], seg_free[kSegs], full[2 * kRing], empty[kRing], qfull[kQBufs], qempty[kQBufs], mask[kMasks], s[2], p[2][2], o[2], x[2], turn[2], drain[2];
 };
@@ -317,7 +346,7 @@ struct Segs {
   }
   __device__ __forceinline__ const Seg* next() {
     const int i = k % kSegs;
-    bool ok = wait_or_abort(&bar.seg[i], (uint32_t)(k / kSegs) & 1u, abort, a.status);
+    bool ok = wait_on(&bar.seg[i], (uint32_t)(k / kSegs) & 1u, abort, a.status);
     if (__any_sync(0xffffffffu, !ok)) return nullptr;
     return ring[i].n > 0 ? &ring[i] : nullptr;
   }
@@ -366,7 +395,7 @@ struct Rows {
   __device__ __forceinline__ void wait_free(uint64_t* b, uint32_t parity) {
     if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return;
     flush();
-    ok = wait_or_abort(b, parity, abort, a.status);
+    ok = wait_on(b, parity, abort, a.status);
     ok = !__any_sync(0xffffffffu, !ok);
   }
 };
@@ -428,7 +457,7 @@ __device__ __forceinline__ void tma_role(const Args& a, const CUtensorMap* tk, c
     int group[kChunks];
 #pragma unroll
     for (int v = 0; v < kChunks; ++v) group[v] = __shfl_sync(0xffffffffu, mine, v);
-    const bool ok = wait_or_abort(&bar.empty[st], par, abort, a.status);
+    const bool ok = wait_on(&bar.empty[st], par, abort, a.status);
     if (__any_sync(0xffffffffu, !ok)) return false;
     if (t5::elect_one()) {
       uint64_t* full = &bar.full[sq];
@@ -445,15 +474,19 @@ __device__ __forceinline__ void tma_role(const Args& a, const CUtensorMap* tk, c
     return true;
   };
   int before = 0;           // groups of the tile whose V is owed
-  bool owed = false, ok = true;
-  while (ok) {
+  bool owed = false, ok = true, more = true;
+  while (ok && more) {
     const Seg* s = segs.next();
-    if (s == nullptr) break;
-    const int n = s->n, h = s->h;
-    const bool two = s->n1 > 0;
-    int t0 = s->t0, e = chunk_entry(a, s, t0, lane), mine = -1;
-    for (int i = 0; i < n; ++i, t0 += kTile) {
-      if ((i & 3) == 0) {  // four tiles' entries at once, the next four already on their way
+    more = s != nullptr;
+    if (!more && (!owed || *abort)) break;
+    // (behind the last segment one empty tile: its K's place stays empty, the V owed follows)
+    const int n = more ? s->n : 1, h = more ? s->h : 0;
+    const bool two = more && s->n1 > 0;
+    int t0 = more ? s->t0 : 0, e = more ? chunk_entry(a, s, t0, lane) : -1, mine = -1;
+    if (!more) advance();
+#pragma unroll 1
+    for (int i = 0; ok && i < n; ++i, t0 += kTile) {
+      if (more && (i & 3) == 0) {  // four tiles' entries at once, the next four already on their way
         mine = chunk_group(a, h, e, t0, lane);
         e = chunk_entry(a, s, t0 + 4 * kTile, lane);
       }
@@ -461,16 +494,11 @@ __device__ __forceinline__ void tma_role(const Args& a, const CUtensorMap* tk, c
       // this tile's K, a V that is owed, this tile's V with two row tiles
       const int loads = 1 + owed + two;
 #pragma unroll 1
-      for (int u = 0; ok && u < loads; ++u) ok = load(u ? tv : tk, u == 1 && owed ? before : now);
-      if (!ok) break;
+      for (int u = more ? 0 : 1; ok && u < loads; ++u) ok = load(u ? tv : tk, u == 1 && owed ? before : now);
       before = now;
       owed = !two;
     }
-    segs.done();
-  }
-  if (ok && owed && !*abort) {
-    advance();  // no K follows the last tile: its place stays empty
-    ok = load(tv, before);
+    if (more) segs.done();
   }
   if (!ok || *abort) {  // the launch gives up: copies in flight land (or their time runs out) before the memory goes
     for (int q = issued > kRing ? issued - kRing : 0; q < issued; ++q)
@@ -491,79 +519,81 @@ __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, u
     if (++sq == 2 * kRing) sq = 0;
     if (sq == 0 || sq == kRing) par ^= 1u;
   };
-  // the K or V stage of a tile: lane l holds the references of rows l, l + 32, l + 64, l + 96
-  auto load = [&](const long long* ref, uint32_t whole, const void* gpu, const void* host, const uint32_t* mask) {
-    const uint32_t st = sq >= kRing ? sq - kRing : sq;
-    if (whole == 0xffu) g.flush();  // nothing to put off: what is in flight comes first
-    g.wait_free(&bar.empty[st], par);
-    if (!g.ok) return;
-    if (mask && lane == 0) {
-      masks[T % kMasks] = make_uint4(mask[0], mask[1], mask[2], mask[3]);
-      mbar_arrive(&bar.mask[T % kMasks]);
-    }
-    uint64_t* full = &bar.full[sq];
-    if (whole != 0xffu) {
-      unsigned char* to = gbase + (kQBufs + st) * kStageB + row_off;
-#pragma unroll
-      for (int v = 0; v < kChunks; ++v) {
-        if (whole >> v & 1u) continue;
-        const long long r = __shfl_sync(0xffffffffu, ref[v >> 1], 16 * (v & 1) + r16);
-        const bool live = r >= 0;
-        const unsigned char* src = (const unsigned char*)((r & tc::kHostBit) && live ? host : gpu) +
-                                   (live ? (size_t)(r & tc::kRefRowMask) * tc::kRowBytes + half * 128 : 0);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          tc::cp_async16_zfill(to + v * 2 * kGroupB + ((c ^ (r16 & 7)) << 4), live ? src + c * 16 : src, live);
-      }
-      g.commit(full);
-    } else if (lane == 0) {
-      mbar_arrive(full);
-    }
-    advance();
-  };
-  long long before[4];  // the tile whose V is owed
+  long long ref[4], before[4];  // lane l: rows l, l + 32, l + 64, l + 96 of this tile, of the tile whose V is owed
   uint32_t whole_before = 0;
-  bool owed = false;
-  while (g.ok) {
+  bool owed = false, more = true;
+  while (g.ok && more) {
     if (!segs.ready()) g.flush();  // a wait that does not announce
     const Seg* s = segs.next();
-    if (s == nullptr) break;
-    const int n = s->n, h = s->h;
-    const bool two = s->n1 > 0;
-    int t0 = s->t0, e = chunk_entry(a, s, t0, lane);
+    more = s != nullptr;
+    if (!more && (!owed || *abort)) break;
+    const int n = more ? s->n : 1, h = more ? s->h : 0;
+    const bool two = more && s->n1 > 0;
+    int t0 = more ? s->t0 : 0, e = more ? chunk_entry(a, s, t0, lane) : -1;
     uint32_t all = 0;
+    if (!more) advance();
+#pragma unroll 1
     for (int i = 0; g.ok && i < n; ++i, ++T, t0 += kTile) {
-      if ((i & 3) == 0) {
+      if (more && (i & 3) == 0) {
         all = __ballot_sync(0xffffffffu, chunk_group(a, h, e, t0, lane) >= 0);
         e = chunk_entry(a, s, t0 + 4 * kTile, lane);
       }
       const uint32_t whole = all & 0xffu;
       all >>= 8;
-      long long ref[4] = {-1, -1, -1, -1};
       uint32_t mask[4] = {~0u, ~0u, ~0u, ~0u};
-      if (whole != 0xffu) {
+      if (more && whole != 0xffu) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int t = t0 + 32 * j + lane;
           const bool in = t >= s->lo && t < s->hi;
-          if (in) ref[j] = row_ref(a, h, s->table[block_of(a, t)], t);
+          ref[j] = in ? row_ref(a, h, s->table[block_of(a, t)], t) : -1;
           if (in && ref[j] < 0) flag(a.status, SKV_DEV_BAD_SLOT);
           mask[j] = __ballot_sync(0xffffffffu, ref[j] >= 0);
         }
       }
-      load(ref, whole, a.pool.gpu_k, a.pool.host_k, mask);
-      if (g.ok && owed) load(before, whole_before, a.pool.gpu_v, a.pool.host_v, nullptr);
-      if (g.ok && two) load(ref, whole, a.pool.gpu_v, a.pool.host_v, nullptr);
+      // this tile's K, a V that is owed, this tile's V with two row tiles
+      const int loads = 1 + owed + two;
+#pragma unroll 1
+      for (int u = more ? 0 : 1; g.ok && u < loads; ++u) {
+        const bool old = u == 1 && owed;
+        const uint32_t st = sq >= kRing ? sq - kRing : sq, w = old ? whole_before : whole;
+        if (w == 0xffu) g.flush();  // nothing to put off: what is in flight comes first
+        g.wait_free(&bar.empty[st], par);
+        if (!g.ok) break;
+        if (u == 0 && lane == 0) {
+          masks[T % kMasks] = make_uint4(mask[0], mask[1], mask[2], mask[3]);
+          mbar_arrive(&bar.mask[T % kMasks]);
+        }
+        if (w != 0xffu) {
+          const unsigned char* gpu = (const unsigned char*)(u ? a.pool.gpu_v : a.pool.gpu_k);
+          const unsigned char* host = (const unsigned char*)(u ? a.pool.host_v : a.pool.host_k);
+          unsigned char* to = gbase + (kQBufs + st) * kStageB + row_off;
+#pragma unroll 1
+          for (int v = 0; v < kChunks; ++v, to += 2 * kGroupB) {
+            if (w >> v & 1u) continue;
+            const long long mine = old ? (v < 4 ? (v < 2 ? before[0] : before[1]) : (v < 6 ? before[2] : before[3]))
+                                       : (v < 4 ? (v < 2 ? ref[0] : ref[1]) : (v < 6 ? ref[2] : ref[3]));
+            const long long r = __shfl_sync(0xffffffffu, mine, 16 * (v & 1) + r16);
+            const bool live = r >= 0;
+            const unsigned char* src = live ? ((r & tc::kHostBit) ? host : gpu) +
+                                                  (size_t)(r & tc::kRefRowMask) * tc::kRowBytes + half * 128
+                                            : gpu;
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              tc::cp_async16_zfill(to + ((c ^ (r16 & 7)) << 4), live ? src + c * 16 : src, live);
+          }
+          g.commit(&bar.full[sq]);
+        } else if (lane == 0) {
+          mbar_arrive(&bar.full[sq]);
+        }
+        advance();
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) before[j] = ref[j];
       whole_before = whole;
       owed = !two;
     }
-    segs.done();
-  }
-  if (g.ok && owed && !*abort) {
-    advance();
-    load(before, whole_before, a.pool.gpu_v, a.pool.host_v, nullptr);
+    if (more) segs.done();
   }
   g.flush();
 }
@@ -577,7 +607,7 @@ __device__ __forceinline__ void walk_role(const Args& a, Bars& bar, Seg* ring, u
   Walk walk;
   walk.init(a);
   auto publish = [&](const Seg& x, int k) {
-    const bool ok = wait_or_abort(&bar.seg_free[k % kSegs], (uint32_t)((k / kSegs) & 1) ^ 1u, abort, a.status);
+    const bool ok = wait_on(&bar.seg_free[k % kSegs], (uint32_t)((k / kSegs) & 1) ^ 1u, abort, a.status);
     if (__any_sync(0xffffffffu, !ok)) return false;
     if (lane == 0) {
       ring[k % kSegs] = x;
@@ -597,7 +627,7 @@ __device__ __forceinline__ void walk_role(const Args& a, Bars& bar, Seg* ring, u
   while (s.n > 0) {
     for (int u = 0; u < (s.n1 > 0 ? 2 : 1); ++u, ++nq) {
       const int buf = nq & 1;
-      const bool ok = wait_or_abort(&bar.qempty[buf], (uint32_t)((nq >> 1) & 1) ^ 1u, abort, a.status);
+      const bool ok = wait_on(&bar.qempty[buf], (uint32_t)((nq >> 1) & 1) ^ 1u, abort, a.status);
       if (__any_sync(0xffffffffu, !ok)) return;
       const int live = u ? s.n1 : s.n0;
 #pragma unroll 2
@@ -695,7 +725,7 @@ __device__ __forceinline__ void mma_role(const Args& a, const Segs& segs, Bars& 
   Steps gen{segs, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, slot, false, false, 0u};
   bool ok = true;
   auto wait = [&](uint64_t* b, uint32_t parity) {
-    if (ok) ok = wait_or_abort(b, parity, abort, a.status);
+    if (ok) ok = wait_on(b, parity, abort, a.status);
     ok = __all_sync(0xffffffffu, ok);
   };
   auto issue_s = [&](uint32_t c, bool k_there) {
@@ -749,18 +779,21 @@ __device__ __forceinline__ void mma_role(const Args& a, const Segs& segs, Bars& 
       }
     }
   };
-  uint32_t now = gen.next(), p_par = 0u;
-  if (now) issue_s(now, false);
-  while (ok && now) {  // O of a step, then S of the next one over its P
+  uint32_t now = 0u, p_par = 0u;
+#pragma unroll 1
+  while (ok) {  // O of a step, then S of the next one over its P
     const uint32_t nx = gen.next();
+    if (!nx && !now) break;
     const bool there =
         nx && __all_sync(0xffffffffu, mbar_try_wait(&bar.full[nx & step::kSeq], (nx >> step::kKPar) & 1u));
-    issue_o(now, p_par);
-    if (!there) pass_turn();  // nothing to follow yet: the other slot need not wait for it
+    if (now) {
+      issue_o(now, p_par);
+      p_par ^= 1u;
+      if (!there) pass_turn();  // nothing to follow yet: the other slot need not wait for it
+    }
     if (ok && nx) issue_s(nx, there);
-    if (there) pass_turn();
+    if (now && there) pass_turn();
     now = nx;
-    p_par ^= 1u;
   }
   // the operands in shared memory and TMEM outlive every MMA issued
   __syncwarp();
@@ -788,33 +821,36 @@ __device__ __forceinline__ void softmax_role(const Args& a, Segs segs, Bars& bar
     float m = -INFINITY, l = 0.f;
     for (int j = 0; ok && j < mine; ++j, ++ns) {
       const int tile = T + (two ? j : 2 * j + sub);
-      ok = wait_or_abort(&bar.mask[tile % kMasks], (uint32_t)(tile / kMasks) & 1u, abort, a.status);
-      ok = ok && wait_or_abort(&bar.s[slot], (uint32_t)ns & 1u, abort, a.status);
+      ok = wait_on(&bar.mask[tile % kMasks], (uint32_t)(tile / kMasks) & 1u, abort, a.status);
+      ok = ok && wait_on(&bar.s[slot], (uint32_t)ns & 1u, abort, a.status);
       ok = !__any_sync(0xffffffffu, !ok);
       if (!ok) break;
       t5::fence_after();
       if (warp_live) {
         const uint4 mk = masks[tile % kMasks];
-        uint32_t v[128];
+        if ((mk.x & mk.y & mk.z & mk.w) != 0xffffffffu) {  // masked keys: -inf, in TMEM
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t v[32];
+            t5::ld32(ts + c, v);
+            const uint32_t mw = reinterpret_cast<const uint32_t*>(masks + tile % kMasks)[c >> 5];
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch) t5::ld32_async(ts + ch * 32, v + ch * 32);
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) t5::ld_wait32(v + ch * 32);
-        if ((mk.x & mk.y & mk.z & mk.w) != 0xffffffffu) {
-          const uint32_t mw[4] = {mk.x, mk.y, mk.z, mk.w};
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (!((mw[i >> 5] >> (i & 31)) & 1u)) v[i] = 0xff800000u;  // -inf
+            for (int i = 0; i < 32; ++i)
+              if (!((mw >> i) & 1u)) v[i] = 0xff800000u;
+            t5::st32(ts + c, v);
+          }
+          t5::st_wait();
         }
-        float mx[4];
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t v[32];
+          t5::ld32(ts + c, v);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) mx[u] = max3(v[u], v[u + 4], v[u + 8]);
+          for (int i = 0; i < 32; i += 8)
 #pragma unroll
-        for (int i = 12; i + 8 <= 128; i += 8)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) mx[u] = max3(__float_as_uint(mx[u]), v[i + u], v[i + 4 + u]);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], __uint_as_float(v[124 + u]));
+            for (int u = 0; u < 4; ++u) mx[u] = max3(__float_as_uint(mx[u]), v[i + u], v[i + 4 + u]);
+        }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
         if (j == 0) {
           m = top;
@@ -836,26 +872,31 @@ __device__ __forceinline__ void softmax_role(const Args& a, Segs segs, Bars& bar
         }
         const float mb = m == -INFINITY ? 0.f : -m;
         const uint64_t sc2 = pack2(a.scale_log2, a.scale_log2), mb2 = pack2(mb, mb);
-        uint64_t sum[2] = {0ull, 0ull};  // pairs of +0.0
+        uint64_t sum[2] = {0ull, 0ull};
+        uint32_t v[32];
+        t5::ld32_async(ts, v);
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t pk[16];
+          t5::ld_wait32(v);
 #pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
+          for (int i = 0; i < 16; ++i) {
             float z0, z1;
-            unpack2(fma2(pack2(__uint_as_float(v[ch * 64 + 2 * i]), __uint_as_float(v[ch * 64 + 2 * i + 1])), sc2, mb2), z0, z1);
+            unpack2(fma2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), sc2, mb2), z0, z1);
             z0 = ex2(z0);
             z1 = ex2(z1);
             sum[i & 1] = add2(sum[i & 1], pack2(z0, z1));
             pk[i] = tc::pack_bf16(z0, z1);
           }
-          t5::st32(ts + ch * 32, pk);
-          t5::st_wait();
-          if (ch == 0) {  // the first 64 keys' P V may start
+          st16(ts + (c >> 1), pk);  // P of these keys, over S columns that have been read
+          if (c < 96) t5::ld32_async(ts + c + 32, v);
+          if (c == 32) {  // the first 64 keys' P V may start
+            t5::st_wait();
             t5::fence_before();
             mbar_arrive(&bar.p[slot][0]);
           }
         }
+        t5::st_wait();
         float l0, l1;
         unpack2(add2(sum[0], sum[1]), l0, l1);
         l += l0 + l1;
@@ -866,10 +907,11 @@ __device__ __forceinline__ void softmax_role(const Args& a, Segs segs, Bars& bar
       mbar_arrive(&bar.p[slot][1]);
     }
     if (ok && mine > 0) {
-      ok = wait_or_abort(&bar.o[slot], (uint32_t)(no++) & 1u, abort, a.status);
+      ok = wait_on(&bar.o[slot], (uint32_t)(no++) & 1u, abort, a.status);
       ok = !__any_sync(0xffffffffu, !ok);
       t5::fence_after();
     }
+    if (l != l) m = NAN;  // a NaN key or query: the running maximum passes NaN over
     // the segment's partial, head-fastest in groups of 4 dims: [dim / 4][row][4]
     const int rp = s.tail ? a.G : a.pl.rp;
     const size_t at = (size_t)(s.tail ? s.part : 2 * s.part + (two ? sub : 0)) * rp;
@@ -897,7 +939,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Segs segs, Bars& bar
       // (a row's TMEM lane is the same for the two slots' warps)
       xml[slot * kTile + row] = make_float2(m, l);
       mbar_arrive(&bar.x[0]);
-      ok = ok && wait_or_abort(&bar.x[0], (uint32_t)nx & 1u, abort, a.status);
+      ok = ok && wait_on(&bar.x[0], (uint32_t)nx & 1u, abort, a.status);
       ok = !__any_sync(0xffffffffu, !ok);
       if (ok && warp_live) {
         t5::fence_after();
@@ -927,7 +969,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Segs segs, Bars& bar
       // neither slot's O is overwritten before both have read it
       t5::fence_before();
       mbar_arrive(&bar.x[1]);
-      ok = ok && wait_or_abort(&bar.x[1], (uint32_t)(nx++) & 1u, abort, a.status);
+      ok = ok && wait_on(&bar.x[1], (uint32_t)(nx++) & 1u, abort, a.status);
       ok = !__any_sync(0xffffffffu, !ok);
     }
     x += two ? 2 * s.n : s.n;
@@ -987,12 +1029,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
   pdl_release();  // every role that touches global memory waits for the kernels before by itself
   const uint32_t tm = sh.tmem;
   const Segs segs{a, bar, sh.ring, &sh.abort, 0};
-  // 2 x 128 x 192 + 2 x 128 x 64 = 65,536 registers, what 512 threads of 128 were launched with
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     softmax_role(a, segs, bar, tm, sh.masks, sh.xml, &sh.abort);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 8)
       tma_role(a, &tk, &tv, segs, bar, base, &sh.abort);
     else if (warp == 9)
