@@ -616,8 +616,8 @@ typedef struct skv_rotary {
  * apart from token to token: column ranges of one fused projection output are fine.
  * Base pointers are 16-byte aligned and strides are multiples of 16 bytes.
  *   q           NULL: the call has no queries.
- *   positions   device int32 [n_tokens]; a negative one marks a padding token, of which
- *               nothing is read or written.  NULL: token i ends its request's history,
+ *   positions   device int32 [n_tokens]; a negative one marks a padding token: its rows
+ *               (which must be there) may be read, nothing is written.  NULL: token i ends its request's history,
  *               position seq_lens[request] - 1 (a history of length 0: a padding token).
  *   requests    device int32 [n_tokens]: the request (slot-table row) of each token, a
  *               negative one again padding.  NULL: token i is request i's.

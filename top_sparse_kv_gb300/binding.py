@@ -169,6 +169,14 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def raw_stream(stream=None) -> int:
+    """The cudaStream_t of `stream`, or of the current stream, without building a Stream object
+    (torch.cuda.current_stream() costs more than a small kernel's launch)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
 def _check(fn: str, st: int):
     if st != SKV_OK:
         raise SkvError(fn, st)

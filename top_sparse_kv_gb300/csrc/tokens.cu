@@ -9,6 +9,11 @@
 // warp then walks rows of the token's heads -- queries, keys, values -- a row spread over
 // LPR lanes in 16-byte vectors, so loads and stores are whole 16-byte accesses of
 // consecutive lanes and the sum of squares is a butterfly over the row's lanes.
+//
+// Bound by instruction issue before it is by HBM (70 % of the issue slots at half of the
+// copy bandwidth, with everything per row), so what does not change from row to row comes
+// once a token: with g the weights an entry becomes f (x A + x' B), A = g cos,
+// B = -+ g' sin, x' its partner and f the row's 1 / rms.
 #include "skv_internal.cuh"
 
 namespace skv {
@@ -26,11 +31,12 @@ struct TokenArgs {
   const int32_t *positions, *requests, *seq_lens;
   int n_tokens, B, H, Hq, d, dv, max_len, bs;
   int rot_start, rot_dim, style, norm_dim;
-  float eps;
+  float eps, inv_norm;
   const float* inv_freq;
   const unsigned char *gq, *gk;
   int32_t* status;
   int parts;  // CTAs a token
+  int stage;  // bytes of a staged item's rows
 };
 
 // cos and sin of t * f: the turn t f / 2 pi as a 64-bit fraction, whose integer product
@@ -38,10 +44,12 @@ struct TokenArgs {
 // turn is off by less than 2^-24 at t = 2^31 and 2^-35 at t = 2^20.  The nearest quarter
 // turn comes off in integers too; what is left is at most an eighth of a turn, so its
 // fp32 rounding is at most 2^-25 of pi / 4.
-__device__ __forceinline__ float2 turn_cos_sin(int t, float f) {
+__device__ __forceinline__ unsigned long long turn_of(float f) {  // one position's turn, of 2^64
   double u = (double)f * 0.15915494309189533577;  // 1 / (2 pi)
   u -= floor(u);
-  const unsigned long long ph = __double2ull_rz(u * 18446744073709551616.0) * (unsigned long long)t;
+  return __double2ull_rz(u * 18446744073709551616.0);
+}
+__device__ __forceinline__ float2 cos_sin_of(unsigned long long ph) {
   const unsigned long long near = ph + (1ull << 61);
   const int quarter = (int)(near >> 62);
   const long long rem = (long long)(near & ((1ull << 62) - 1)) - (1ll << 61);
@@ -50,177 +58,475 @@ __device__ __forceinline__ float2 turn_cos_sin(int t, float f) {
   const float cc = (quarter & 1) ? s : c, ss = (quarter & 1) ? c : s;
   return make_float2(quarter == 1 || quarter == 2 ? -cc : cc, quarter >= 2 ? -ss : ss);
 }
+__device__ __forceinline__ float2 turn_cos_sin(int t, float f) {
+  return cos_sin_of(turn_of(f) * (unsigned long long)t);
+}
 
-// LPR lanes a row, NV vectors a lane: vector i of lane `sub` is vector sub + LPR * i.
-template <typename T, int LPR, int NV>
-__global__ void __launch_bounds__(kTokThreads) token_rows_kernel(const TokenArgs a) {
+// What a CTA's token needs once: its request, position and, for an append, the pool rows of
+// KV head 0 (null: none) and the bytes from head to head.
+struct Token {
+  int req, pos;
+  bool live;
+  unsigned char *k, *v;
+  size_t k_head, v_head;
+};
+
+__device__ __forceinline__ Token token_of(const TokenArgs& a, int tok, bool reports) {
+  Token t;
+  t.live = false;
+  t.req = a.requests ? a.requests[tok] : tok;
+  t.pos = -1;
+  t.k = t.v = nullptr;
+  t.k_head = t.v_head = 0;
+  if (a.requests && t.req < 0) return t;
+  const bool needs_req = a.pool.table != nullptr || a.positions == nullptr || a.requests != nullptr;
+  if (needs_req && t.req >= a.B) {
+    if (reports) flag(a.status, SKV_DEV_BAD_INDEX);
+    return t;
+  }
+  t.pos = a.positions ? a.positions[tok] : a.seq_lens[t.req] - 1;
+  if (t.pos < 0 || t.pos >= a.max_len) {
+    const bool bad = a.positions ? t.pos >= 0 : (t.pos < -1 || t.pos >= a.max_len);
+    if (bad && reports) flag(a.status, SKV_DEV_BAD_LENGTH);
+    return t;
+  }
+  t.live = true;
+  return t;
+}
+
+// The pool rows of the token in KV head h's blocks: row addresses, null for a bad entry.
+__device__ __forceinline__ void pool_rows(const TokenArgs& a, const Token& t, int h, int elem, unsigned char** k,
+                                          unsigned char** v) {
+  *k = *v = nullptr;
+  const int e = table_row(a.pool, t.req, h, a.H)[t.pos / a.bs];
+  const int off = t.pos % a.bs;
+  const bool gpu = e >= 0;
+  size_t row;
+  if (gpu && e < a.pool.n_gpu) {
+    row = gpu_block_row(a.pool, e, h, a.H, a.bs) + off;
+  } else if (!gpu && a.pool.host_k != nullptr && -(long long)e - 1 < a.pool.n_host) {
+    row = ((size_t)(-(long long)e - 1) * a.H + h) * a.bs + off;
+  } else {
+    flag(a.status, SKV_DEV_BAD_SLOT);
+    return;
+  }
+  *k = (unsigned char*)(gpu ? a.pool.gpu_k : a.pool.host_k) + row * a.d * elem;
+  if (a.v) *v = (unsigned char*)(gpu ? a.pool.gpu_v : a.pool.host_v) + row * a.dv * elem;
+}
+
+// Where row r of the token (queries, keys, values in order) comes from and goes to (null: nowhere).
+template <int ELEM>
+__device__ __forceinline__ const unsigned char* row_from(const TokenArgs& a, int tok, int r, int nq, int nk) {
+  if (r < nq) return a.q + tok * a.qs + (size_t)r * a.d * ELEM;
+  if (r < nq + nk) return a.k + tok * a.ks + (size_t)(r - nq) * a.d * ELEM;
+  return a.v + tok * a.vs + (size_t)(r - nq - nk) * a.dv * ELEM;
+}
+template <int ELEM>
+__device__ __forceinline__ unsigned char* row_to(const TokenArgs& a, const Token& t, int tok, int r, int nq, int nk) {
+  if (r < nq) return a.q_out + tok * a.qos + (size_t)r * a.d * ELEM;
+  const bool is_v = r >= nq + nk;
+  const int h = is_v ? r - nq - nk : r - nq;
+  if (a.pool.table == nullptr) return a.k_out + tok * a.kos + (size_t)h * a.d * ELEM;
+  if (a.pool.per_head) {
+    unsigned char *k, *v;
+    pool_rows(a, t, h, ELEM, &k, &v);
+    return is_v ? v : k;
+  }
+  unsigned char* base = is_v ? t.v : t.k;
+  return base ? base + h * (is_v ? t.v_head : t.k_head) : nullptr;
+}
+
+// One shared table entry serves every head: looked up once a token.
+template <int ELEM>
+__device__ __forceinline__ void find_pool_rows(const TokenArgs& a, Token& t) {
+  if (a.pool.table == nullptr || a.pool.per_head) return;
+  pool_rows(a, t, 0, ELEM, &t.k, &t.v);
+  t.k_head = (size_t)a.bs * a.d * ELEM;
+  t.v_head = (size_t)a.bs * a.dv * ELEM;
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 narrow(const float* x) {  // the one rounding
   constexpr int VE = Vec<T>::N;
-  constexpr int RPW = 32 / LPR;  // rows a warp handles at once
-  extern __shared__ float2 cs[];  // [rot_dim / 2] cos, sin; then, NV > 1, a rotated span a warp
+  __align__(16) T out[VE];
+#pragma unroll
+  for (int j = 0; j < VE; ++j) out[j] = from_float<T>(x[j]);
+  return *reinterpret_cast<uint4*>(out);
+}
+
+// Rows of at most LPR vectors: LPR lanes a row (a vector a lane), normed whole or not at
+// all, a token's rows staged in shared memory.  Persistent CTAs of eight row warps and one
+// that runs ahead: for every item -- a token, or a part of its rows where tokens are few --
+// it fetches the rows by bulk copies (they are consecutive in memory), looks up the
+// position and the pool rows and writes the coefficients A and B of queries and keys,
+// kTokStages items deep, so the row warps meet no latency but shared memory's.
+constexpr int kTokStages = 3;
+constexpr int kTokStageMax = 40 * 1024;
+
+struct StageInfo {
+  Token t;
+  int tok, r0, r1;  // the item's rows of the token
+};
+struct alignas(16) TokenBars {
+  unsigned char zeros[16];  // the partner of entries that are not turned
+  uint64_t full[kTokStages], empty[kTokStages];
+  int abort;
+};
+constexpr int kInfoBytes = 128;
+constexpr int kTokCtas = 3;  // resident CTAs a SM
+constexpr int kTokSmemMax = kInfoBytes + kTokStages * (kInfoBytes + 4096 + kTokStageMax);
+static_assert(sizeof(StageInfo) <= kInfoBytes && sizeof(TokenBars) <= kInfoBytes, "");
+
+// PAIR: partners are neighbours of the same vector, else `half` entries away.
+template <typename T, int LPR, bool PAIR>
+__global__ void __launch_bounds__(kTokThreads + 32, kTokCtas) token_rows_kernel(const TokenArgs a) {
+  constexpr int VE = Vec<T>::N, RPW = 32 / LPR, ELEM = sizeof(T);
+  extern __shared__ __align__(128) unsigned char smem[];
+  TokenBars& bar = *reinterpret_cast<TokenBars*>(smem);
+  const int half = a.rot_dim >> 1, d = a.d;
+  const int stage_bytes = kInfoBytes + 16 * d + a.stage;  // info; A, B of queries, of keys; rows
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nq = a.q ? a.Hq : 0, nk = a.k ? a.H : 0, nv = a.v ? a.H : 0;
+  const int rows = nq + nk + nv, per = (rows + a.parts - 1) / a.parts;
+  const long long items = (long long)a.n_tokens * a.parts;
+  const int rowb = d * ELEM, vrowb = a.dv * ELEM;
+  volatile int* abort = &bar.abort;
+  auto stage = [&](int s) { return smem + kInfoBytes + s * stage_bytes; };
+  auto weight = [&](const unsigned char* g, int j) -> float {
+    if (g == nullptr) return 1.f;
+    if constexpr (ELEM == 2)
+      return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(g)[j] << 16);
+    else
+      return reinterpret_cast<const float*>(g)[j];
+  };
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kTokStages; ++i) {
+      mbar_init(&bar.full[i], 1);
+      mbar_init(&bar.empty[i], kTokWarps);
+    }
+    fence_barrier_init();
+    bar.abort = 0;
+    *reinterpret_cast<uint4*>(bar.zeros) = make_uint4(0, 0, 0, 0);
+  }
+  pdl_release();
+  pdl_wait();
+  // entries that are not turned: A = g, B = 0 in every stage, for good
+  for (int i = threadIdx.x; i < 2 * d; i += kTokThreads + 32) {
+    const int k = i / d, j = i - k * d;
+    const float g = weight(k ? a.gk : a.gq, j);
+    for (int s = 0; s < kTokStages; ++s) {
+      float* t = reinterpret_cast<float*>(stage(s) + kInfoBytes) + 2 * k * d;
+      t[j] = g;
+      t[d + j] = 0.f;
+    }
+  }
+  __syncthreads();
+
+  if (warp == kTokWarps) {
+    constexpr int kAngles = LPR * VE / 64;  // of a lane: half is at most LPR * VE / 2
+    unsigned long long turn[kAngles];
+    float g[kAngles][4];  // the weights of an angle's pair: queries, keys
+    int at[kAngles][2];   // its entries
+#pragma unroll
+    for (int u = 0; u < kAngles; ++u) {
+      const int i = lane + 32 * u;
+      if (i < half) {
+        turn[u] = turn_of(a.inv_freq[i]);
+        at[u][0] = a.rot_start + (PAIR ? 2 * i : i);
+        at[u][1] = a.rot_start + (PAIR ? 2 * i + 1 : i + half);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) g[u][k] = weight(k < 2 ? a.gq : a.gk, at[u][k & 1]);
+      }
+    }
+    int n = 0;
+    for (long long it = blockIdx.x; it < items; it += gridDim.x, ++n) {
+      const int s = n % kTokStages;
+      const bool ok = wait_or_abort(&bar.empty[s], (uint32_t)((n / kTokStages) & 1) ^ 1u, abort, a.status);
+      if (__any_sync(0xffffffffu, !ok)) break;
+      const int tok = (int)(it / a.parts), r0 = (int)(it - (long long)tok * a.parts) * per;
+      const int r1 = r0 + per < rows ? r0 + per : rows;
+      unsigned char* st = stage(s);
+      float* co = reinterpret_cast<float*>(st + kInfoBytes);
+      if (lane == 0) {  // the rows: consecutive ranges of q, k and v
+        unsigned char* to = st + kInfoBytes + 16 * d;
+        const int q0 = r0 < nq ? r0 : nq, q1 = r1 < nq ? r1 : nq;
+        const int k0 = r0 > nq ? r0 - nq : 0, k1 = r1 > nq ? (r1 - nq < nk ? r1 - nq : nk) : 0;
+        const int v0 = r0 > nq + nk ? r0 - nq - nk : 0, v1 = r1 > nq + nk ? r1 - nq - nk : 0;
+        const uint32_t qb = q1 > q0 ? (q1 - q0) * rowb : 0, kb = k1 > k0 ? (k1 - k0) * rowb : 0;
+        const uint32_t vb = v1 > v0 ? (v1 - v0) * vrowb : 0;
+        mbar_expect_tx(&bar.full[s], qb + kb + vb);
+        if (qb) bulk_g2s(to, a.q + tok * a.qs + (size_t)q0 * rowb, qb, &bar.full[s]);
+        if (kb) bulk_g2s(to + qb, a.k + tok * a.ks + (size_t)k0 * rowb, kb, &bar.full[s]);
+        if (vb) bulk_g2s(to + qb + kb, a.v + tok * a.vs + (size_t)v0 * vrowb, vb, &bar.full[s]);
+      }
+      Token t = token_of(a, tok, lane == 0 && r0 == 0);
+      if (t.live) {
+        find_pool_rows<ELEM>(a, t);
+#pragma unroll
+        for (int u = 0; u < kAngles; ++u)
+          if (lane + 32 * u < half) {
+            const float2 c = cos_sin_of(turn[u] * (unsigned long long)t.pos);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              co[2 * k * d + at[u][0]] = g[u][2 * k] * c.x;
+              co[2 * k * d + at[u][1]] = g[u][2 * k + 1] * c.x;
+              co[(2 * k + 1) * d + at[u][0]] = -g[u][2 * k + 1] * c.y;
+              co[(2 * k + 1) * d + at[u][1]] = g[u][2 * k] * c.y;
+            }
+          }
+      }
+      if (lane == 0) {
+        StageInfo& f = *reinterpret_cast<StageInfo*>(st);
+        f.t = t;
+        f.tok = tok;
+        f.r0 = r0;
+        f.r1 = r1;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.full[s]);
+    }
+    if (*abort)  // copies in flight land (or their time runs out) before the memory goes
+      for (int i = n > kTokStages ? n - kTokStages : 0; i < n; ++i)
+        mbar_wait_bounded(&bar.full[i % kTokStages], (uint32_t)((i / kTokStages) & 1), 20000000LL);
+    return;
+  }
+
+  // this lane's entries e0 .. e0 + VE of a row and their partners'
+  const int sub = lane % LPR, mine = lane / LPR, e0 = sub * VE, w = e0 - a.rot_start;
+  const bool in = half > 0 && w >= 0 && w < a.rot_dim, has = e0 < d;
+  const int shift = w < half ? half : -half;
+  int n = 0;
+  for (long long it = blockIdx.x; it < items; it += gridDim.x, ++n) {
+    const int s = n % kTokStages;
+    const bool ok = wait_or_abort(&bar.full[s], (uint32_t)((n / kTokStages) & 1), abort, a.status);
+    if (__any_sync(0xffffffffu, !ok)) break;
+    const unsigned char* st = stage(s);
+    const StageInfo& f = *reinterpret_cast<const StageInfo*>(st);
+    if (f.t.live) {
+      const int r0 = f.r0, r1 = f.r1;
+      const unsigned char* data = st + kInfoBytes + 16 * d;
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {  // queries, keys
+        const int lo = k ? nq : 0, end = k ? nq + nk : nq, hi = end < r1 ? end : r1;
+        if (hi <= lo || hi <= r0) continue;
+        const bool norm = (k ? a.gk : a.gq) != nullptr;
+        float A[VE], B[VE];
+#pragma unroll
+        for (int j = 0; j < VE; j += 4) {
+          const float* co = reinterpret_cast<const float*>(st + kInfoBytes) + 2 * k * d + (has ? e0 + j : 0);
+          const float4 x = *reinterpret_cast<const float4*>(co), y = *reinterpret_cast<const float4*>(co + d);
+          A[j] = x.x, A[j + 1] = x.y, A[j + 2] = x.z, A[j + 3] = x.w;
+          B[j] = y.x, B[j + 1] = y.y, B[j + 2] = y.z, B[j + 3] = y.w;
+        }
+        // the first rows of this kind that the warp takes (it steps through all rows of the item)
+        const int skip = (lo - r0 - warp * RPW + kTokWarps * RPW - RPW) / (kTokWarps * RPW);
+        int rb = r0 + warp * RPW + (lo > r0 && skip > 0 ? skip : 0) * kTokWarps * RPW;
+        const unsigned char* src = data + (rb + mine - r0) * rowb + e0 * ELEM;
+        unsigned char* q_to = k ? nullptr : a.q_out + f.tok * a.qos + (size_t)(rb + mine) * rowb;
+#pragma unroll 2
+        for (; rb < hi; rb += kTokWarps * RPW) {
+          const int r = rb + mine;
+          const bool on = has && r >= lo && r < hi;
+          uint4 raw = make_uint4(0, 0, 0, 0), other = raw;
+          if (on) {
+            raw = *reinterpret_cast<const uint4*>(src);
+            if (!PAIR) other = *reinterpret_cast<const uint4*>(in ? src + shift * ELEM : bar.zeros);
+          }
+          float x[VE], y[VE], o[VE];
+          Vec<T>::widen(raw, x);
+          if (!PAIR) Vec<T>::widen(other, y);
+          float inv = 1.f;
+          if (norm) {
+            float ssq = 0.f;
+#pragma unroll
+            for (int j = 0; j < VE; ++j) ssq = fmaf(x[j], x[j], ssq);
+#pragma unroll
+            for (int off = LPR / 2; off >= 1; off >>= 1) ssq += __shfl_xor_sync(0xffffffffu, ssq, off);
+            inv = rsqrtf(fmaf(ssq, a.inv_norm, a.eps));
+          }
+#pragma unroll
+          for (int j = 0; j < VE; ++j) {
+            o[j] = x[j] * A[j];
+            if (!PAIR || in) o[j] = fmaf(PAIR ? x[j ^ 1] : y[j], B[j], o[j]);
+            o[j] *= inv;
+          }
+          unsigned char* dst = q_to;
+          if (k) dst = on ? row_to<ELEM>(a, f.t, f.tok, r, nq, nk) : nullptr;
+          if (on && dst != nullptr) *reinterpret_cast<uint4*>(dst + e0 * ELEM) = narrow<T>(o);
+          src += kTokWarps * RPW * rowb;
+          q_to += kTokWarps * RPW * rowb;
+        }
+      }
+      if (r1 > nq + nk) {  // values: as they are
+        const int v0 = r0 > nq + nk ? r0 : nq + nk;
+        const unsigned char* from = data + (r0 < nq + nk ? (nq + nk - r0) * rowb : 0);
+        for (int r = r0 + warp * RPW + mine; r < r1; r += kTokWarps * RPW)
+          if (r >= v0 && e0 < a.dv) {
+            unsigned char* dst = row_to<ELEM>(a, f.t, f.tok, r, nq, nk);
+            if (dst != nullptr)
+              *reinterpret_cast<uint4*>(dst + e0 * ELEM) =
+                  *reinterpret_cast<const uint4*>(from + (r - v0) * vrowb + e0 * ELEM);
+          }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar.empty[s]);
+  }
+}
+
+// Longer rows: a warp a row, NV vectors a lane -- vector i of lane l is vector l + 32 i.
+// Vectors that neither norm nor rotation touch go as they are.
+template <typename T, int NV>
+__global__ void __launch_bounds__(kTokThreads) token_long_rows_kernel(const TokenArgs a) {
+  constexpr int VE = Vec<T>::N;
+  extern __shared__ float2 cs[];  // [rot_dim / 2] cos, sin; then a rotated span a warp
   pdl_release();
   pdl_wait();
   const int tok = blockIdx.x / a.parts, part = blockIdx.x - tok * a.parts;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LPR;
-
-  // the token's request and position; padding and out-of-range tokens end here
-  const int req = a.requests ? a.requests[tok] : tok;
-  if (a.requests && req < 0) return;
-  const bool needs_req = a.pool.table != nullptr || a.positions == nullptr || a.requests != nullptr;
-  if (needs_req && req >= a.B) {
-    if (threadIdx.x == 0) flag(a.status, SKV_DEV_BAD_INDEX);
-    return;
-  }
-  const int pos = a.positions ? a.positions[tok] : a.seq_lens[req] - 1;
-  if (pos < 0 || pos >= a.max_len) {
-    const bool bad = a.positions ? pos >= 0 : (pos < -1 || pos >= a.max_len);
-    if (bad && threadIdx.x == 0) flag(a.status, SKV_DEV_BAD_LENGTH);
-    return;
-  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Token t = token_of(a, tok, threadIdx.x == 0);
+  if (!t.live) return;
+  find_pool_rows<sizeof(T)>(a, t);
   const int half = a.rot_dim >> 1;
-  for (int i = threadIdx.x; i < half; i += kTokThreads) cs[i] = turn_cos_sin(pos, a.inv_freq[i]);
+  for (int i = threadIdx.x; i < half; i += kTokThreads) cs[i] = turn_cos_sin(t.pos, a.inv_freq[i]);
   __syncthreads();
   float* span = reinterpret_cast<float*>(cs + half) + warp * a.rot_dim;
-
   const int nq = a.q ? a.Hq : 0, nk = a.k ? a.H : 0, nv = a.v ? a.H : 0;
-  const int rows = nq + nk + nv;
-  for (int r0 = (part * kTokWarps + warp) * RPW; r0 < rows; r0 += a.parts * kTokWarps * RPW) {
-    const int r = r0 + lane / LPR;
-    const bool is_q = r < nq, is_v = r >= nq + nk;
-    const int h = is_q ? r : is_v ? r - nq - nk : r - nq;
-    const int d = is_v ? a.dv : a.d;
-    const unsigned char* src = nullptr;
-    unsigned char* dst = nullptr;
-    if (r < rows) {
-      src = (is_q ? a.q + tok * a.qs : is_v ? a.v + tok * a.vs : a.k + tok * a.ks) + (size_t)h * d * sizeof(T);
-      if (is_q) {
-        dst = a.q_out + tok * a.qos + (size_t)h * d * sizeof(T);
-      } else if (a.pool.table == nullptr) {
-        dst = a.k_out + tok * a.kos + (size_t)h * d * sizeof(T);
-      } else {
-        const int e = table_row(a.pool, req, h, a.H)[pos / a.bs];
-        const int off = pos % a.bs;
-        if (e >= 0 && e < a.pool.n_gpu) {
-          dst = (unsigned char*)(is_v ? a.pool.gpu_v : a.pool.gpu_k) +
-                (gpu_block_row(a.pool, e, h, a.H, a.bs) + off) * d * sizeof(T);
-        } else if (e < 0 && a.pool.host_k != nullptr && -(long long)e - 1 < a.pool.n_host) {
-          dst = (unsigned char*)(is_v ? a.pool.host_v : a.pool.host_k) +
-                (((size_t)(-(long long)e - 1) * a.H + h) * a.bs + off) * d * sizeof(T);
-        } else if (sub == 0) {
-          flag(a.status, SKV_DEV_BAD_SLOT);
-        }
-      }
-    }
-    const unsigned char* gamma = is_q ? a.gq : is_v ? nullptr : a.gk;
-    float x[NV][VE];
-    float ssq = 0.f;
+  const int rows = nq + nk + nv, stride = a.parts * kTokWarps;
+  uint4 next[NV];
+  const unsigned char* src = nullptr;
+  unsigned char *dst = nullptr, *to = nullptr;
+  auto load = [&](int r) {  // the next row flies while this one is turned
+    if (r >= rows) return;
+    src = row_from<sizeof(T)>(a, tok, r, nq, nk);
+    dst = row_to<sizeof(T)>(a, t, tok, r, nq, nk);
+    const int d = r >= nq + nk ? a.dv : a.d;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e0 = (sub + LPR * i) * VE;
-      if (src != nullptr && e0 < d) {
-        Vec<T>::load(src + (size_t)e0 * sizeof(T), x[i]);
-        if (e0 < a.norm_dim)
-#pragma unroll
-          for (int j = 0; j < VE; ++j) ssq = fmaf(x[i][j], x[i][j], ssq);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VE; ++j) x[i][j] = 0.f;
-      }
+      const int e0 = (lane + 32 * i) * VE;
+      next[i] = e0 < d ? *reinterpret_cast<const uint4*>(src + (size_t)e0 * sizeof(T)) : make_uint4(0, 0, 0, 0);
     }
+  };
+  int r = part * kTokWarps + warp;
+  load(r);
+  for (; r < rows; r += stride) {
+    uint4 raw[NV];
 #pragma unroll
-    for (int off = LPR / 2; off >= 1; off >>= 1) ssq += __shfl_xor_sync(0xffffffffu, ssq, off);
+    for (int i = 0; i < NV; ++i) raw[i] = next[i];
+    to = dst;
+    load(r + stride);
+    const bool is_v = r >= nq + nk;
+    const int d = is_v ? a.dv : a.d;
+    const unsigned char* gamma = r < nq ? a.gq : is_v ? nullptr : a.gk;
+    float inv = 1.f;
     if (gamma != nullptr) {
-      const float inv = 1.f / sqrtf(ssq / (float)a.norm_dim + a.eps);
+      float ssq = 0.f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int e0 = (sub + LPR * i) * VE;
-        if (e0 < a.norm_dim) {
-          float g[VE];
-          Vec<T>::load(gamma + (size_t)e0 * sizeof(T), g);
+      for (int i = 0; i < NV; ++i)
+        if ((lane + 32 * i) * VE < a.norm_dim) {
+          float x[VE];
+          Vec<T>::widen(raw[i], x);
 #pragma unroll
-          for (int j = 0; j < VE; ++j) x[i][j] = x[i][j] * inv * g[j];
+          for (int j = 0; j < VE; ++j) ssq = fmaf(x[j], x[j], ssq);
         }
-      }
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) ssq += __shfl_xor_sync(0xffffffffu, ssq, off);
+      inv = rsqrtf(fmaf(ssq, a.inv_norm, a.eps));
     }
-    // rotation: vector-aligned spans, so a vector is inside or outside as a whole
-    if (half > 0 && a.style == SKV_ROPE_PAIR) {
+    const bool turn = half > 0 && !is_v, halves = turn && a.style == SKV_ROPE_HALF;
+    if (halves) __syncwarp();  // the row before's partners have been read
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int w = (sub + LPR * i) * VE - a.rot_start;
-        if (!is_v && w >= 0 && w < a.rot_dim) {
+    for (int i = 0; i < NV; ++i) {
+      const int e0 = (lane + 32 * i) * VE, w = e0 - a.rot_start;
+      const bool in = turn && w >= 0 && w < a.rot_dim, normed = gamma != nullptr && e0 < a.norm_dim;
+      if (!in && !normed) continue;
+      float x[VE];
+      Vec<T>::widen(raw[i], x);
+      if (normed) {
+        float g[VE];
+        Vec<T>::load(gamma + (size_t)e0 * sizeof(T), g);
 #pragma unroll
-          for (int j = 0; j < VE; j += 2) {
-            const float2 t = cs[(w + j) >> 1];
-            const float u = x[i][j], z = x[i][j + 1];
-            x[i][j] = u * t.x - z * t.y;
-            x[i][j + 1] = z * t.x + u * t.y;
-          }
+        for (int j = 0; j < VE; ++j) x[j] = x[j] * inv * g[j];
+      }
+      if (in && halves) {  // finished below, with the partners
+#pragma unroll
+        for (int j = 0; j < VE; ++j) span[w + j] = x[j];
+        continue;
+      }
+      if (in) {
+#pragma unroll
+        for (int j = 0; j < VE; j += 2) {
+          const float2 c = cs[(w + j) >> 1];
+          const float u = x[j], z = x[j + 1];
+          x[j] = u * c.x - z * c.y;
+          x[j + 1] = z * c.x + u * c.y;
         }
       }
-    } else if (half > 0) {
-      if constexpr (NV == 1) {
-        const int w = sub * VE - a.rot_start;
-        const bool in = w >= 0 && w < a.rot_dim, first = w < half;
-        const int from = in ? (first ? lane + half / VE : lane - half / VE) : lane;
+      raw[i] = narrow<T>(x);
+    }
+    if (halves) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int w = (lane + 32 * i) * VE - a.rot_start;
+        if (w < 0 || w >= a.rot_dim) continue;
+        const bool first = w < half;
+        float x[VE];
 #pragma unroll
         for (int j = 0; j < VE; ++j) {
-          const float o = __shfl_sync(0xffffffffu, x[0][j], from);
-          if (in && !is_v) {
-            const float2 t = cs[(first ? w : w - half) + j];
-            x[0][j] = x[0][j] * t.x + (first ? -o : o) * t.y;
-          }
+          const float2 c = cs[(first ? w : w - half) + j];
+          const float o = span[(first ? w + half : w - half) + j];
+          x[j] = span[w + j] * c.x + (first ? -o : o) * c.y;
         }
-      } else {
-        __syncwarp();  // the previous row's partners have been read
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int w = (sub + LPR * i) * VE - a.rot_start;
-          if (w >= 0 && w < a.rot_dim)
-#pragma unroll
-            for (int j = 0; j < VE; ++j) span[w + j] = x[i][j];
-        }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int w = (sub + LPR * i) * VE - a.rot_start;
-          if (!is_v && w >= 0 && w < a.rot_dim) {
-            const bool first = w < half;
-#pragma unroll
-            for (int j = 0; j < VE; ++j) {
-              const float2 t = cs[(first ? w : w - half) + j];
-              const float o = span[(first ? w + half : w - half) + j];
-              x[i][j] = x[i][j] * t.x + (first ? -o : o) * t.y;
-            }
-          }
-        }
+        raw[i] = narrow<T>(x);
       }
     }
-    if (dst != nullptr) {
+    if (to != nullptr) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int e0 = (sub + LPR * i) * VE;
-        if (e0 < d) {
-          __align__(16) T out[VE];
-#pragma unroll
-          for (int j = 0; j < VE; ++j) out[j] = from_float<T>(x[i][j]);  // the one rounding
-          *reinterpret_cast<uint4*>(dst + (size_t)e0 * sizeof(T)) = *reinterpret_cast<uint4*>(out);
-        }
+        const int e0 = (lane + 32 * i) * VE;
+        if (e0 < d) *reinterpret_cast<uint4*>(to + (size_t)e0 * sizeof(T)) = raw[i];
       }
     }
   }
 }
 
-template <typename T, int LPR, int NV>
-skv_status launch_rows(TokenArgs& a, cudaStream_t st) {
-  const int rows = (a.q ? a.Hq : 0) + (a.k ? a.H : 0) + (a.v ? a.H : 0);
-  const int per = kTokWarps * (32 / LPR);  // rows a CTA takes at once
-  const int most = (rows + per - 1) / per;
-  // few tokens: as many CTAs a token as it has rounds of rows, up to about two CTAs an SM
-  long long parts = (2LL * 152 + a.n_tokens - 1) / a.n_tokens;
-  a.parts = (int)(parts < most ? parts : most);
-  const size_t smem = (size_t)a.rot_dim * 4 + (NV > 1 ? (size_t)kTokWarps * a.rot_dim * 4 : 0);
+int rows_of(const TokenArgs& a) { return (a.q ? a.Hq : 0) + (a.k ? a.H : 0) + (a.v ? a.H : 0); }
+// few tokens: as many parts a token as it has rounds of `per` rows, up to about two CTAs an SM
+int parts_of(const TokenArgs& a, int per) {
+  const long long most = (rows_of(a) + per - 1) / per, want = (2LL * 152 + a.n_tokens - 1) / a.n_tokens;
+  return (int)(want < most ? want : most);
+}
+
+template <typename T, int LPR>
+skv_status launch_short(TokenArgs& a, cudaStream_t st, bool* taken) {
+  const int rows = rows_of(a);
+  a.parts = parts_of(a, kTokWarps * (32 / LPR));
+  const int per = (rows + a.parts - 1) / a.parts, wide = a.v != nullptr && a.dv > a.d ? a.dv : a.d;
+  const long long stage = (long long)per * wide * (int)sizeof(T);
+  *taken = stage <= kTokStageMax;
+  if (!*taken) return SKV_OK;
+  a.stage = (int)((stage + 127) & ~127LL);
+  const int smem = kInfoBytes + kTokStages * (kInfoBytes + 16 * a.d + a.stage);
+  const auto kernel = a.style == SKV_ROPE_PAIR ? token_rows_kernel<T, LPR, true> : token_rows_kernel<T, LPR, false>;
+  const skv_status prep = prepare_kernel((const void*)kernel, kTokSmemMax);
+  if (prep != SKV_OK) return prep;
+  const int fit = 228 * 1024 / (smem + 1024), blocks = fit < kTokCtas ? fit : kTokCtas;
+  const long long items = (long long)a.n_tokens * a.parts, slots = (long long)num_sms() * blocks;
+  if (launch_dependent(kernel, dim3((unsigned)(items < slots ? items : slots)), dim3(kTokThreads + 32), smem, st, 1, a) !=
+      cudaSuccess)
+    return SKV_ERR_CUDA;
+  SKV_LAUNCH_CHECK();
+  return SKV_OK;
+}
+
+template <typename T, int NV>
+skv_status launch_long(TokenArgs& a, cudaStream_t st) {
+  a.parts = parts_of(a, kTokWarps);
   const long long ctas = (long long)a.n_tokens * a.parts;
   if (ctas > 0x7fffffffLL) return SKV_ERR_UNSUPPORTED;
-  if (launch_dependent(token_rows_kernel<T, LPR, NV>, dim3((unsigned)ctas), dim3(kTokThreads), smem, st, 1, a) !=
+  const size_t smem = (size_t)a.rot_dim * 4 * (1 + kTokWarps);
+  if (launch_dependent(token_long_rows_kernel<T, NV>, dim3((unsigned)ctas), dim3(kTokThreads), smem, st, 1, a) !=
       cudaSuccess)
     return SKV_ERR_CUDA;
   SKV_LAUNCH_CHECK();
@@ -260,22 +566,34 @@ skv_status launch_token_rows(const skv_problem& p, const skv_rotary& r, const sk
   a.style = r.style;
   a.norm_dim = r.norm_dim > 0 ? r.norm_dim : p.d_qk;
   a.eps = r.eps;
+  a.inv_norm = 1.f / (float)a.norm_dim;
   a.inv_freq = r.inv_freq;
   a.gq = (const unsigned char*)r.q_gamma;
   a.gk = (const unsigned char*)r.k_gamma;
   a.status = status;
   a.parts = 1;
+  a.stage = 0;
   const int d = a.v != nullptr && p.d_v > p.d_qk ? p.d_v : p.d_qk;
+  // Staged where a row is a vector a lane, is normed whole or not at all, and a token's rows
+  // fit a stage; else a warp a row.
+  const bool whole = (r.q_gamma == nullptr && r.k_gamma == nullptr) || a.norm_dim == p.d_qk;
+  bool taken = false;
+  skv_status done = SKV_OK;
   if (p.dtype == SKV_DTYPE_F32) {
-    if (d <= 128) return launch_rows<float, 32, 1>(a, st);
-    if (d <= 256) return launch_rows<float, 32, 2>(a, st);
-    if (d <= 640) return launch_rows<float, 32, 5>(a, st);
-    return launch_rows<float, 32, 8>(a, st);
+    if (whole && d <= 128) done = launch_short<float, 32>(a, st, &taken);
+    if (taken || done != SKV_OK) return done;
+    if (d <= 256) return launch_long<float, 2>(a, st);
+    if (d <= 640) return launch_long<float, 5>(a, st);
+    return launch_long<float, 8>(a, st);
   }
-  if (d <= 128) return launch_rows<__nv_bfloat16, 16, 1>(a, st);
-  if (d <= 256) return launch_rows<__nv_bfloat16, 32, 1>(a, st);
-  if (d <= 768) return launch_rows<__nv_bfloat16, 32, 3>(a, st);
-  return launch_rows<__nv_bfloat16, 32, 4>(a, st);
+  if (whole && d <= 128)
+    done = launch_short<__nv_bfloat16, 16>(a, st, &taken);
+  else if (whole && d <= 256)
+    done = launch_short<__nv_bfloat16, 32>(a, st, &taken);
+  if (taken || done != SKV_OK) return done;
+  if (d <= 256) return launch_long<__nv_bfloat16, 1>(a, st);
+  if (d <= 768) return launch_long<__nv_bfloat16, 3>(a, st);
+  return launch_long<__nv_bfloat16, 4>(a, st);
 }
 
 }  // namespace skv

@@ -198,34 +198,55 @@ class TokenStep:
         self.status = torch.zeros((1,), dtype=torch.int32, device=dev)
         self._p, self._r = ctypes.byref(problem.c()), ctypes.byref(rotary.c())
         self._pool = None if pool is None else ctypes.byref(pool.c())
-        self._st = ctypes.c_void_p(self.status.data_ptr())
+        self._st = self.status.data_ptr()
         self._dtype = B.element_type(problem)
+        self._norm_rope, self._append = B.lib().skv_qk_norm_rope, B.lib().skv_append_kv
+        self._seen = {}  # token layouts (types, shapes, strides) that have been checked
 
-    def _out(self, name, out, src, heads):
-        if src is None:
-            return None, None
-        if out is None:
-            out = torch.empty((src.shape[0], heads, self.p.d_qk), dtype=src.dtype, device=src.device)
-        return out, B._out_rows(name, out, src, heads, self.p.d_qk, self._dtype)
+    def _tokens(self, q, k, v, positions, requests, q_out, k_out):
+        """skv_tokens and the outputs' pointers; a layout is checked in full when it first comes."""
+        key = tuple((t.dtype, t.shape, t.stride()) if t is not None else None
+                    for t in (q, k, v, positions, requests, q_out, k_out))
+        in_place = (q is not None and q_out.data_ptr() == q.data_ptr(), k_out is not None
+                    and k_out.data_ptr() == k.data_ptr())
+        n = self._seen.get((key, in_place))
+        if n is None:
+            n = B.c_tokens(self.p, q, k, v, positions, requests).n_tokens
+            if q_out is not None:
+                B._out_rows("q_out", q_out, q, self.p.n_q_heads, self.p.d_qk, self._dtype)
+            if k_out is not None:
+                B._out_rows("k_out", k_out, k, self.p.n_kv_heads, self.p.d_qk, self._dtype)
+            if len(self._seen) > 64:
+                self._seen.clear()
+            self._seen[key, in_place] = n
+        ptr = [None if t is None else t.data_ptr() for t in (q, k, v, positions, requests, q_out, k_out)]
+        strides = [0 if e is None else e[2][0] for e in key[:3]]
+        return B.CTokens(n, 0, ptr[0], ptr[1], ptr[2], strides[0], strides[1], strides[2], ptr[3], ptr[4]), ptr[5], ptr[6]
+
+    def _out(self, out, src, heads):
+        if src is None or out is not None:
+            return out
+        return torch.empty((src.shape[0], heads, self.p.d_qk), dtype=src.dtype, device=src.device)
 
     def norm_rope(self, q, k, positions=None, requests=None, q_out=None, k_out=None, stream=None):
         """(q_out, k_out): new tensors unless given; pass q and k themselves to work in place.
         Padding tokens' rows are not written."""
-        ct = B.c_tokens(self.p, q, k, None, positions, requests)
-        q_out, qo = self._out("q_out", q_out, q, self.p.n_q_heads)
-        k_out, ko = self._out("k_out", k_out, k, self.p.n_kv_heads)
-        B._check("skv_qk_norm_rope", B.lib().skv_qk_norm_rope(self._p, self._r, ctypes.byref(ct), qo, ko, self._st,
-                                                              B._stream(stream)))
+        q_out, k_out = self._out(q_out, q, self.p.n_q_heads), self._out(k_out, k, self.p.n_kv_heads)
+        ct, qo, ko = self._tokens(q, k, None, positions, requests, q_out, k_out)
+        st = self._norm_rope(self._p, self._r, ctypes.byref(ct), qo, ko, self._st, B.raw_stream(stream))
+        if st:
+            raise B.SkvError("skv_qk_norm_rope", st)
         return q_out, k_out
 
     def append(self, q, k, v, positions=None, requests=None, q_out=None, stream=None):
         """Appends k and v to the pool; returns q_out (None without q)."""
         if self._pool is None:
             raise ValueError("append() needs a pool")
-        ct = B.c_tokens(self.p, q, k, v, positions, requests)
-        q_out, qo = self._out("q_out", q_out, q, self.p.n_q_heads)
-        B._check("skv_append_kv", B.lib().skv_append_kv(self._p, self._r, ctypes.byref(ct), self._pool, qo, self._st,
-                                                        B._stream(stream)))
+        q_out = self._out(q_out, q, self.p.n_q_heads)
+        ct, qo, _ = self._tokens(q, k, v, positions, requests, q_out, None)
+        st = self._append(self._p, self._r, ctypes.byref(ct), self._pool, qo, self._st, B.raw_stream(stream))
+        if st:
+            raise B.SkvError("skv_append_kv", st)
         return q_out
 
 
@@ -245,14 +266,15 @@ class PrefixStep:
         self.ws = torch.empty((max(B.skv_prefix_workspace_size(problem, prefix.len), 16),), dtype=torch.uint8,
                               device=dev)
         self.status = torch.zeros((1,), dtype=torch.int32, device=dev)
-        self._tail = (ctypes.c_void_p(self.out.data_ptr()), ctypes.c_void_p(self.lse.data_ptr()),
-                      ctypes.c_void_p(self.ws.data_ptr()), self.ws.numel(),
-                      ctypes.c_void_p(self.status.data_ptr()))
+        self._tail = (self.out.data_ptr(), self.lse.data_ptr(), self.ws.data_ptr(), self.ws.numel(),
+                      self.status.data_ptr())
+        self._call = B.lib().skv_prefix_attn
 
     def run(self, q, stream=None):
         """(out, lse), the step's own buffers."""
         if q.shape != self._shape or q.dtype != self.out.dtype or not q.is_contiguous():
             raise ValueError(f"q: contiguous {self.out.dtype} {list(self._shape)} expected")
-        B._check("skv_prefix_attn", B.lib().skv_prefix_attn(self._p, q.data_ptr(), self._pool, self._prefix,
-                                                            *self._tail, B._stream(stream)))
+        st = self._call(self._p, q.data_ptr(), self._pool, self._prefix, *self._tail, B.raw_stream(stream))
+        if st:
+            raise B.SkvError("skv_prefix_attn", st)
         return self.out, self.lse
