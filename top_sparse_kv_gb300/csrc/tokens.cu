@@ -160,7 +160,7 @@ __device__ __forceinline__ uint4 narrow(const float* x) {  // the one rounding
 // it fetches the rows by bulk copies (they are consecutive in memory), looks up the
 // position and the pool rows and writes the coefficients A and B of queries and keys,
 // kTokStages items deep, so the row warps meet no latency but shared memory's.
-constexpr int kTokStages = 3;
+constexpr int kTokStages = 2;
 constexpr int kTokStageMax = 40 * 1024;
 
 struct StageInfo {
