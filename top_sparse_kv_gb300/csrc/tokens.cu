@@ -4,10 +4,9 @@
 //   norm      y_j = gamma_j x_j / sqrt(mean_{i < norm_dim} x_i^2 + eps)
 //   rotation  (a, b) -> (a cos - b sin, b cos + a sin) at the angle t * inv_freq[i]
 //
-// Each row is read once and written once.  One CTA holds one token (or a part of its
-// rows): the token's cosines and sines are computed once into shared memory and every
-// warp then walks rows of the token's heads -- queries, keys, values -- a row spread over
-// LPR lanes in 16-byte vectors, so loads and stores are whole 16-byte accesses of
+// Each row is read once and written once.  A CTA takes a token (or a part of its rows)
+// at a time: its cosines and sines are computed once into shared memory and the warps walk
+// the rows of its heads -- queries, keys, values -- a row spread over lanes in 16-byte vectors, so loads and stores are whole 16-byte accesses of
 // consecutive lanes and the sum of squares is a butterfly over the row's lanes.
 //
 // Bound by instruction issue before it is by HBM (70 % of the issue slots at half of the
@@ -19,8 +18,7 @@
 namespace skv {
 namespace {
 
-constexpr int kTokWarps = 8;
-constexpr int kTokThreads = 32 * kTokWarps;
+constexpr int kLongWarps = 4;
 
 struct TokenArgs {
   const unsigned char *q, *k, *v;
@@ -155,7 +153,7 @@ __device__ __forceinline__ uint4 narrow(const float* x) {  // the one rounding
 }
 
 // Rows of at most LPR vectors: LPR lanes a row (a vector a lane), normed whole or not at
-// all, a token's rows staged in shared memory.  Persistent CTAs of eight row warps and one
+// all, a token's rows staged in shared memory.  Persistent CTAs of W row warps and one
 // that runs ahead: for every item -- a token, or a part of its rows where tokens are few --
 // it fetches the rows by bulk copies (they are consecutive in memory), looks up the
 // position and the pool rows and writes the coefficients A and B of queries and keys,
@@ -173,13 +171,19 @@ struct alignas(16) TokenBars {
   int abort;
 };
 constexpr int kInfoBytes = 128;
-constexpr int kTokCtas = 3;  // resident CTAs a SM
+// Row warps and resident CTAs a SM: four warps of half-rows (bf16) share a token's fixed
+// costs better than eight (8,192 tokens 54 us against 59), whole-warp rows (fp32) take eight.
+template <int LPR>
+constexpr int kRowWarps = LPR == 16 ? 4 : 8;
+template <int LPR>
+constexpr int kTokCtas = LPR == 16 ? 4 : 3;
 constexpr int kTokSmemMax = kInfoBytes + kTokStages * (kInfoBytes + 4096 + kTokStageMax);
 static_assert(sizeof(StageInfo) <= kInfoBytes && sizeof(TokenBars) <= kInfoBytes, "");
 
 // PAIR: partners are neighbours of the same vector, else `half` entries away.
 template <typename T, int LPR, bool PAIR>
-__global__ void __launch_bounds__(kTokThreads + 32, kTokCtas) token_rows_kernel(const TokenArgs a) {
+__global__ void __launch_bounds__(32 * kRowWarps<LPR> + 32, kTokCtas<LPR>) token_rows_kernel(const TokenArgs a) {
+  constexpr int W = kRowWarps<LPR>;
   constexpr int VE = Vec<T>::N, RPW = 32 / LPR, ELEM = sizeof(T);
   extern __shared__ __align__(128) unsigned char smem[];
   TokenBars& bar = *reinterpret_cast<TokenBars*>(smem);
@@ -202,7 +206,7 @@ __global__ void __launch_bounds__(kTokThreads + 32, kTokCtas) token_rows_kernel(
   if (threadIdx.x == 0) {
     for (int i = 0; i < kTokStages; ++i) {
       mbar_init(&bar.full[i], 1);
-      mbar_init(&bar.empty[i], kTokWarps);
+      mbar_init(&bar.empty[i], W);
     }
     fence_barrier_init();
     bar.abort = 0;
@@ -211,7 +215,7 @@ __global__ void __launch_bounds__(kTokThreads + 32, kTokCtas) token_rows_kernel(
   pdl_release();
   pdl_wait();
   // entries that are not turned: A = g, B = 0 in every stage, for good
-  for (int i = threadIdx.x; i < 2 * d; i += kTokThreads + 32) {
+  for (int i = threadIdx.x; i < 2 * d; i += 32 * W + 32) {
     const int k = i / d, j = i - k * d;
     const float g = weight(k ? a.gk : a.gq, j);
     for (int s = 0; s < kTokStages; ++s) {
@@ -222,7 +226,7 @@ __global__ void __launch_bounds__(kTokThreads + 32, kTokCtas) token_rows_kernel(
   }
   __syncthreads();
 
-  if (warp == kTokWarps) {
+  if (warp == W) {
     constexpr int kAngles = LPR * VE / 64;  // of a lane: half is at most LPR * VE / 2
     unsigned long long turn[kAngles];
     float g[kAngles][4];  // the weights of an angle's pair: queries, keys
@@ -319,12 +323,12 @@ __global__ void __launch_bounds__(kTokThreads + 32, kTokCtas) token_rows_kernel(
           B[j] = y.x, B[j + 1] = y.y, B[j + 2] = y.z, B[j + 3] = y.w;
         }
         // the first rows of this kind that the warp takes (it steps through all rows of the item)
-        const int skip = (lo - r0 - warp * RPW + kTokWarps * RPW - RPW) / (kTokWarps * RPW);
-        int rb = r0 + warp * RPW + (lo > r0 && skip > 0 ? skip : 0) * kTokWarps * RPW;
+        const int skip = (lo - r0 - warp * RPW + W * RPW - RPW) / (W * RPW);
+        int rb = r0 + warp * RPW + (lo > r0 && skip > 0 ? skip : 0) * W * RPW;
         const unsigned char* src = data + (rb + mine - r0) * rowb + e0 * ELEM;
         unsigned char* q_to = k ? nullptr : a.q_out + f.tok * a.qos + (size_t)(rb + mine) * rowb;
-#pragma unroll 2
-        for (; rb < hi; rb += kTokWarps * RPW) {
+#pragma unroll 1
+        for (; rb < hi; rb += W * RPW) {
           const int r = rb + mine;
           const bool on = has && r >= lo && r < hi;
           uint4 raw = make_uint4(0, 0, 0, 0), other = raw;
@@ -353,14 +357,14 @@ __global__ void __launch_bounds__(kTokThreads + 32, kTokCtas) token_rows_kernel(
           unsigned char* dst = q_to;
           if (k) dst = on ? row_to<ELEM>(a, f.t, f.tok, r, nq, nk) : nullptr;
           if (on && dst != nullptr) *reinterpret_cast<uint4*>(dst + e0 * ELEM) = narrow<T>(o);
-          src += kTokWarps * RPW * rowb;
-          q_to += kTokWarps * RPW * rowb;
+          src += W * RPW * rowb;
+          q_to += W * RPW * rowb;
         }
       }
       if (r1 > nq + nk) {  // values: as they are
         const int v0 = r0 > nq + nk ? r0 : nq + nk;
         const unsigned char* from = data + (r0 < nq + nk ? (nq + nk - r0) * rowb : 0);
-        for (int r = r0 + warp * RPW + mine; r < r1; r += kTokWarps * RPW)
+        for (int r = r0 + warp * RPW + mine; r < r1; r += W * RPW)
           if (r >= v0 && e0 < a.dv) {
             unsigned char* dst = row_to<ELEM>(a, f.t, f.tok, r, nq, nk);
             if (dst != nullptr)
@@ -377,7 +381,7 @@ __global__ void __launch_bounds__(kTokThreads + 32, kTokCtas) token_rows_kernel(
 // Longer rows: a warp a row, NV vectors a lane -- vector i of lane l is vector l + 32 i.
 // Vectors that neither norm nor rotation touch go as they are.
 template <typename T, int NV>
-__global__ void __launch_bounds__(kTokThreads) token_long_rows_kernel(const TokenArgs a) {
+__global__ void __launch_bounds__(32 * kLongWarps) token_long_rows_kernel(const TokenArgs a) {
   constexpr int VE = Vec<T>::N;
   extern __shared__ float2 cs[];  // [rot_dim / 2] cos, sin; then a rotated span a warp
   pdl_release();
@@ -388,11 +392,11 @@ __global__ void __launch_bounds__(kTokThreads) token_long_rows_kernel(const Toke
   if (!t.live) return;
   find_pool_rows<sizeof(T)>(a, t);
   const int half = a.rot_dim >> 1;
-  for (int i = threadIdx.x; i < half; i += kTokThreads) cs[i] = turn_cos_sin(t.pos, a.inv_freq[i]);
+  for (int i = threadIdx.x; i < half; i += 32 * kLongWarps) cs[i] = turn_cos_sin(t.pos, a.inv_freq[i]);
   __syncthreads();
   float* span = reinterpret_cast<float*>(cs + half) + warp * a.rot_dim;
   const int nq = a.q ? a.Hq : 0, nk = a.k ? a.H : 0, nv = a.v ? a.H : 0;
-  const int rows = nq + nk + nv, stride = a.parts * kTokWarps;
+  const int rows = nq + nk + nv, stride = a.parts * kLongWarps;
   uint4 next[NV];
   const unsigned char* src = nullptr;
   unsigned char *dst = nullptr, *to = nullptr;
@@ -407,7 +411,7 @@ __global__ void __launch_bounds__(kTokThreads) token_long_rows_kernel(const Toke
       next[i] = e0 < d ? *reinterpret_cast<const uint4*>(src + (size_t)e0 * sizeof(T)) : make_uint4(0, 0, 0, 0);
     }
   };
-  int r = part * kTokWarps + warp;
+  int r = part * kLongWarps + warp;
   load(r);
   for (; r < rows; r += stride) {
     uint4 raw[NV];
@@ -501,7 +505,7 @@ int parts_of(const TokenArgs& a, int per) {
 template <typename T, int LPR>
 skv_status launch_short(TokenArgs& a, cudaStream_t st, bool* taken) {
   const int rows = rows_of(a);
-  a.parts = parts_of(a, kTokWarps * (32 / LPR));
+  a.parts = parts_of(a, kRowWarps<LPR> * (32 / LPR));
   const int per = (rows + a.parts - 1) / a.parts, wide = a.v != nullptr && a.dv > a.d ? a.dv : a.d;
   const long long stage = (long long)per * wide * (int)sizeof(T);
   *taken = stage <= kTokStageMax;
@@ -511,10 +515,10 @@ skv_status launch_short(TokenArgs& a, cudaStream_t st, bool* taken) {
   const auto kernel = a.style == SKV_ROPE_PAIR ? token_rows_kernel<T, LPR, true> : token_rows_kernel<T, LPR, false>;
   const skv_status prep = prepare_kernel((const void*)kernel, kTokSmemMax);
   if (prep != SKV_OK) return prep;
-  const int fit = 228 * 1024 / (smem + 1024), blocks = fit < kTokCtas ? fit : kTokCtas;
+  const int fit = 228 * 1024 / (smem + 1024), blocks = fit < kTokCtas<LPR> ? fit : kTokCtas<LPR>;
   const long long items = (long long)a.n_tokens * a.parts, slots = (long long)num_sms() * blocks;
-  if (launch_dependent(kernel, dim3((unsigned)(items < slots ? items : slots)), dim3(kTokThreads + 32), smem, st, 1, a) !=
-      cudaSuccess)
+  if (launch_dependent(kernel, dim3((unsigned)(items < slots ? items : slots)), dim3(32 * kRowWarps<LPR> + 32), smem,
+                       st, 1, a) != cudaSuccess)
     return SKV_ERR_CUDA;
   SKV_LAUNCH_CHECK();
   return SKV_OK;
@@ -522,11 +526,11 @@ skv_status launch_short(TokenArgs& a, cudaStream_t st, bool* taken) {
 
 template <typename T, int NV>
 skv_status launch_long(TokenArgs& a, cudaStream_t st) {
-  a.parts = parts_of(a, kTokWarps);
+  a.parts = parts_of(a, kLongWarps);
   const long long ctas = (long long)a.n_tokens * a.parts;
   if (ctas > 0x7fffffffLL) return SKV_ERR_UNSUPPORTED;
-  const size_t smem = (size_t)a.rot_dim * 4 * (1 + kTokWarps);
-  if (launch_dependent(token_long_rows_kernel<T, NV>, dim3((unsigned)ctas), dim3(kTokThreads), smem, st, 1, a) !=
+  const size_t smem = (size_t)a.rot_dim * 4 * (1 + kLongWarps);
+  if (launch_dependent(token_long_rows_kernel<T, NV>, dim3((unsigned)ctas), dim3(32 * kLongWarps), smem, st, 1, a) !=
       cudaSuccess)
     return SKV_ERR_CUDA;
   SKV_LAUNCH_CHECK();
