@@ -1050,14 +1050,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
 }
 
 // Joins the partials of 32 query rows of one KV head, kMergeDims of the 128 dims a CTA:
-// lane = row, warp = (4 dims, one of kMergeParts shares of the partials), so every load of
-// a partial is a coalesced float4.  A thread runs once over its share with a running
-// maximum, kMergeBatch partials' loads in flight at a time; the shares are joined through
-// shared memory.  The order is fixed.
-constexpr int kMergeParts = 4;
-constexpr int kMergeDims = 16;
-constexpr int kMergeWarps = kMergeParts * kMergeDims / 4;
-constexpr int kMergeBatch = 4;
+// lane = row, warp = (4 dims, one of PARTS shares of the partials), so every load of a
+// partial is a coalesced float4.  A thread runs once over its share with a running maximum,
+// kMergeBatch partials' loads in flight at a time (bound by their latency: one round for
+// most shapes); the shares are joined through shared memory.  The order is fixed.  Four
+// shares where the rows are few, two where the CTAs fill the device without.
+constexpr int kMergeDims = 8;
+constexpr int kMergeBatch = 5;
 
 struct Joined {
   float m, l;
@@ -1075,7 +1074,9 @@ struct Joined {
   }
 };
 
-__global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Args a) {
+template <int PARTS>
+__global__ void __launch_bounds__(PARTS * kMergeDims * 8, 8 / PARTS) prefix_merge_kernel(const Args a) {
+  constexpr int kMergeWarps = PARTS * kMergeDims / 4;
   __shared__ float4 s_o[kMergeWarps][32];
   __shared__ float2 s_ml[kMergeWarps][32];
   pdl_release();
@@ -1106,12 +1107,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Ar
   int L = live ? a.seq_lens[b] : 0;
   const int f = a.first[unit], e = a.last[unit];  // of no meaning without a tail
   Joined j{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  for (int i = part; i < np; i += kMergeParts * kMergeBatch) {
-    float mp[kMergeBatch], lp[kMergeBatch];
-    float4 v[kMergeBatch];
+  float mp[kMergeBatch], lp[kMergeBatch];
+  float4 v[kMergeBatch];
+  auto fetch = [&](int i) {
 #pragma unroll
     for (int u = 0; u < kMergeBatch; ++u) {
-      const int k = i + u * kMergeParts;
+      const int k = i + u * PARTS;
       mp[u] = -INFINITY;
       if (k < np && live) {
         const size_t at = (size_t)(k * step_p) * pl.rp;
@@ -1120,31 +1121,49 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Ar
         v[u] = *reinterpret_cast<const float4*>(po + at * kD);
       }
     }
-#pragma unroll
-    for (int u = 0; u < kMergeBatch; ++u) j.add(mp[u], lp[u], v[u]);
-  }
+  };
+  fetch(part);
+  // the tail's partials: e - f + 1 consecutive ones of its unit; the first of this share flies
+  // with the prefix's
   if (L < 0 || L > a.max_len || (L > 0 && L < a.P)) {
     if (blockIdx.y == 0 && warp == 0) flag(a.status, SKV_DEV_BAD_LENGTH);
     L = L > a.max_len ? a.max_len : 0;
   }
-  // the tail's partials: e - f + 1 consecutive ones of its unit
-  if (L > a.P && f >= 0 && e < kCtas && f <= e) {  // (else never written: an aborted launch)
-    const size_t at = (size_t)((long long)f + unit) * a.G;
-    const float* so = a.so + at * kD + ((size_t)d4 * a.G + g) * 4;
-    const float* sml = a.sml + at * 2 + g;
-    const int nt = e - f + 1;
-#pragma unroll 2
-    for (int i = part; i < nt; i += kMergeParts) {
+  const bool tail = L > a.P && f >= 0 && e < kCtas && f <= e;  // (else never written: an aborted launch)
+  const int nt = tail ? e - f + 1 : 0;
+  const size_t t_at = tail ? (size_t)((long long)f + unit) * a.G : 0;
+  const float* so = a.so + t_at * kD + ((size_t)d4 * a.G + g) * 4;
+  const float* sml = a.sml + t_at * 2 + g;
+  float tm = -INFINITY, tl = 0.f;
+  float4 to = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto fetch_tail = [&](int i) {
+    tm = -INFINITY;
+    if (i < nt) {
       const size_t k = (size_t)i * a.G;
-      j.add(sml[k * 2], sml[k * 2 + a.G], *reinterpret_cast<const float4*>(so + k * kD));
+      tm = sml[k * 2];
+      tl = sml[k * 2 + a.G];
+      to = *reinterpret_cast<const float4*>(so + k * kD);
     }
+  };
+  fetch_tail(part);
+#pragma unroll
+  for (int u = 0; u < kMergeBatch; ++u) j.add(mp[u], lp[u], v[u]);
+  for (int i = part + PARTS * kMergeBatch; i < np; i += PARTS * kMergeBatch) {
+    fetch(i);
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) j.add(mp[u], lp[u], v[u]);
+  }
+  j.add(tm, tl, to);
+  for (int i = part + PARTS; i < nt; i += PARTS) {
+    fetch_tail(i);
+    j.add(tm, tl, to);
   }
   s_o[warp][lane] = j.o;
   s_ml[warp][lane] = make_float2(j.m, j.l);
   __syncthreads();
   if (part > 0 || !live) return;
 #pragma unroll
-  for (int i = 1; i < kMergeParts; ++i) {
+  for (int i = 1; i < PARTS; ++i) {
     const int from = i * (kMergeDims / 4) + warp;
     const float2 ml = s_ml[from][lane];
     j.add(ml.x, ml.y, s_o[from][lane]);
@@ -1242,8 +1261,9 @@ skv_status launch_prefix_attn(const skv_problem& p, const void* q, const PoolVie
     return SKV_ERR_CUDA;
   SKV_LAUNCH_CHECK();
   const long long blocks = (long long)((a.pl.rows + 31) / 32) * a.H;
-  if (launch_dependent(prefix_merge_kernel, dim3((unsigned)blocks, kD / kMergeDims),
-                       dim3(kMergeWarps * 32), 0, st, 1, a) != cudaSuccess)
+  const bool few = blocks * (kD / kMergeDims) <= 2 * kCtas;
+  if (launch_dependent(few ? prefix_merge_kernel<4> : prefix_merge_kernel<2>, dim3((unsigned)blocks, kD / kMergeDims),
+                       dim3((few ? 4 : 2) * kMergeDims * 8), 0, st, 1, a) != cudaSuccess)
     return SKV_ERR_CUDA;
   SKV_LAUNCH_CHECK();
   return SKV_OK;
