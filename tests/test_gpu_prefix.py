@@ -155,6 +155,8 @@ CASES = [
     (6, 2, 8, 512, _tails(6, 512, 200, 13), dict(own_prefix_rows=True)),
     (2, 4, 8, 40, [5000, 9000], {}),                                # long tails, a short prefix
     (8, 8, 8, 20000, _tails(8, 20000, 500, 14), {}),
+    (700, 4, 2, 130, _tails(700, 130, 600, 15, 40), {}),            # some twenty short segments a CTA
+    (400, 3, 2, 0, _tails(400, 0, 300, 16, 30), {}),                # no prefix at all
 ]
 
 
@@ -335,3 +337,36 @@ def test_append_then_attend(skv):
         assert bool((err <= 2.0 ** -8 * want_q.abs() + 2.0 ** -14)[live].all())
         c.check(out, lse, q=q_out.cpu())
     assert int(tok.status.item()) == 0 and int(att.status.item()) == 0
+
+
+def test_a_loop_of_calls_longer_than_the_ring_of_launches(skv):
+    """Calls back to back on one stream, the workspace and the output shared: every launch waits for
+    the one before, so the last call's result is the last input's."""
+    c = Case(skv, 12, 2, 8, 700, _tails(12, 700, 200, 17), seed=17)
+    step = skv.PrefixStep(c.p, c.pool, c.prefix)
+    qs = [torch.randn(c.q.shape, generator=torch.Generator().manual_seed(i)).to(torch.bfloat16).cuda() for i in range(5)]
+    want = []
+    for q in qs:
+        out, lse = step.run(q)
+        torch.cuda.synchronize()
+        want.append((out.clone(), lse.clone()))
+    for i in range(40):
+        out, lse = step.run(qs[i % 5])
+        got = out.clone(), lse.clone()
+        assert torch.equal(got[0], want[i % 5][0]) and torch.equal(got[1], want[i % 5][1])
+    for i in range(40):
+        step.run(qs[i % 5])
+    assert torch.equal(step.out, want[4][0]) and int(step.status.item()) == 0
+
+
+def test_refuses_what_is_not_on_the_gpu(skv):
+    c = Case(skv, 2, 1, 4, 40, [50, 60], seed=18)
+    step = skv.PrefixStep(c.p, c.pool, c.prefix)
+    n0 = skv.lib().skv_launch_count()
+    with pytest.raises(ValueError):
+        step.run(c.q)
+    with pytest.raises(ValueError):
+        skv.PrefixStep(c.p, c.pool, skv.Prefix(c.ptable, 40))
+    with pytest.raises(ValueError):
+        skv.skv_prefix_attn(c.p, c.qd, c.pool, c.prefix, step.out, step.lse.cpu(), step.ws)
+    assert skv.lib().skv_launch_count() == n0

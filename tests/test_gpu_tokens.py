@@ -379,3 +379,30 @@ def test_append_in_a_graph_and_on_another_stream(skv):
         assert torch.equal(got[:n], q_out[:n])
         assert torch.equal(fresh.gpu_k, pool.gpu_k)
     assert int(step.status.item()) == 0
+
+
+def test_no_token_and_one_token(skv):
+    """Empty tensors do nothing; a lone token's stride has no meaning and is not looked at."""
+    p, r, fused, q, k, gam, pos, inv = _make(skv, (2, 2, 4, 128, "bf16", 0, 128, 0, 0, "qk"))
+    step = skv.TokenStep(p, r)
+    n0 = skv.lib().skv_launch_count()
+    none = lambda h: torch.zeros((0, h, 128), dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    a, b = step.norm_rope(none(4), none(2), torch.zeros(0, dtype=torch.int32, device="cuda"))
+    assert a.shape == (0, 4, 128) and b.shape == (0, 2, 128) and skv.lib().skv_launch_count() == n0
+    want = step.norm_rope(q.cuda().contiguous(), k.cuda().contiguous(), pos.cuda())
+    odd = [x[:1].cuda().as_strided((1, x.shape[1], 128), (13, 128, 1)) for x in (q.contiguous(), k.contiguous())]
+    got = step.norm_rope(*odd, pos[:1].cuda())
+    assert torch.equal(got[0], want[0][:1]) and torch.equal(got[1], want[1][:1])
+    got = step.norm_rope(*odd, pos[:1].cuda(), q_out=odd[0], k_out=odd[1])
+    assert torch.equal(got[0], want[0][:1]) and torch.equal(got[1], want[1][:1])
+
+
+def test_refuses_what_is_not_on_the_gpu(skv):
+    p, r, fused, q, k, gam, pos, inv = _make(skv, (2, 2, 4, 128, "bf16", 0, 128, 0, 0, "qk"))
+    step, n0 = skv.TokenStep(p, r), skv.lib().skv_launch_count()
+    for args in ((q, k, pos.cuda()), (q.cuda(), k, pos.cuda()), (q.cuda(), k.cuda(), pos)):
+        with pytest.raises(ValueError):
+            step.norm_rope(*args)
+    with pytest.raises(ValueError):
+        step.norm_rope(q.cuda(), k.cuda(), pos.cuda(), q_out=torch.empty_like(q.contiguous()))
+    assert skv.lib().skv_launch_count() == n0

@@ -117,3 +117,21 @@ def test_prefix_checks_its_table(B):
                 B.Prefix(torch.zeros(3, dtype=torch.int64), 48), B.Prefix(torch.zeros(6, dtype=torch.int32)[::2], 48)):
         with pytest.raises(ValueError):
             bad.check(p)
+
+
+def test_prefix_checks_its_length_and_device(B):
+    p = B.Problem(batch=4, n_kv_heads=2, n_q_heads=8, d_qk=128, d_v=128, max_len=100, topk=0, n_sink=0, n_local=0,
+                  block_size=16, seq_lens=torch.zeros(4, dtype=torch.int32))
+    table = torch.zeros(7, dtype=torch.int32)
+    B.Prefix(table, 100).check(p)
+    for n in (-1, 101, 2 ** 32 + 5):  # the last is 5 in 32 bits
+        with pytest.raises(ValueError):
+            B.Prefix(table, n).check(p)
+    with pytest.raises(ValueError):
+        B.Prefix(table.to("meta"), 100).check(p)
+
+
+def test_pairs_of_heads_and_requests_stay_in_32_bits(B):
+    over = dict(batch=65535, n_kv_heads=65535, n_q_heads=65535, n_idx_q_heads=65535, max_len=16)
+    assert _size(B, 0, **over)[0] == UNSUPPORTED
+    assert _size(B, 0, **{**over, "batch": 1000})[0] == 0

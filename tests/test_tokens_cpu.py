@@ -156,3 +156,75 @@ def test_binding_checks_types_and_shapes(B):
                 dict(inv_freq=torch.zeros(64), k_gamma=torch.zeros(64, dtype=torch.bfloat16))):
         with pytest.raises(ValueError):
             B.Rotary(rot_dim=128, **bad).check(p)
+
+
+def test_no_rows_may_be_null_pointers(B):
+    """What an empty tensor's address is."""
+    n0 = B.lib().skv_launch_count()
+    none = dict(n_tokens=0, q=None, k=None, v=None)
+    assert _append(B, tokens=none, q_out=None) == 0
+    assert _norm(B, tokens=none, q_out=None, k_out=None) == 0
+    assert B.lib().skv_launch_count() == n0
+
+
+def _problem(B, **over):
+    return B.Problem(**{**dict(batch=4, n_kv_heads=2, n_q_heads=8, d_qk=128, d_v=128, max_len=100, topk=0, n_sink=0,
+                               n_local=0, block_size=16, seq_lens=torch.zeros(4, dtype=torch.int32)), **over})
+
+
+def _pool(B, n=5, dtype=torch.bfloat16, **over):
+    kv = [torch.zeros((n, 2, 16, 128), dtype=dtype) for _ in range(2)]
+    return B.Pool(**{**dict(gpu_k=kv[0], gpu_v=kv[1], slot_table=torch.zeros((4, 7), dtype=torch.int32)), **over})
+
+
+def test_outputs_go_with_their_inputs(B):
+    fused = torch.zeros((4, 12 * 128), dtype=torch.bfloat16)
+    q = fused[:, :1024].view(4, 8, 128)
+    bf = torch.bfloat16
+    B._out_rows("q_out", q, q, 8, 128, bf)
+    B._out_rows("q_out", torch.zeros((4, 8, 128), dtype=bf), q, 8, 128, bf)
+    # packed rows from the input's own address on would be taken for the input in place
+    with pytest.raises(ValueError):
+        B._out_rows("q_out", fused.view(-1)[:4096].view(4, 8, 128), q, 8, 128, bf)
+    with pytest.raises(ValueError):
+        B._out_rows("q_out", torch.zeros((4, 12 * 128), dtype=bf)[:, :1024].view(4, 8, 128), q, 8, 128, bf)
+    with pytest.raises(ValueError):
+        B._out_rows("k_out", q, None, 8, 128, bf)
+
+
+def test_tensors_of_another_device(B):
+    """Nothing of one device's reaches a kernel of another's ("meta" stands for the other here)."""
+    p, rot = _problem(B), B.Rotary(torch.zeros(64), 128)
+    q, k, v = (torch.zeros((4, h, 128), dtype=torch.bfloat16) for h in (8, 2, 2))
+    ids = torch.zeros(4, dtype=torch.int32)
+    for i in range(5):
+        args = [q, k, v, ids, ids]
+        args[i] = args[i].to("meta")
+        with pytest.raises(ValueError):
+            B.c_tokens(p, *args)
+    with pytest.raises(ValueError):
+        B.Rotary(torch.zeros(64, device="meta"), 128).check(p)
+    with pytest.raises(ValueError):
+        B._out_rows("q_out", q.to("meta"), q, 8, 128, torch.bfloat16)
+    for name in ("gpu_k", "gpu_v", "slot_table"):
+        with pytest.raises(ValueError):
+            B.check_pool(p, _pool(B, **{name: getattr(_pool(B), name).to("meta")}))
+    import top_sparse_kv_gb300 as skv
+
+    with pytest.raises(ValueError):  # and the CPU's reach no kernel at all
+        skv.TokenStep(p, rot).norm_rope(q, k)
+
+
+def test_pool_is_the_problems(B):
+    p = _problem(B)
+    B.check_pool(p, _pool(B))
+    bad = [_pool(B, dtype=torch.float32), _pool(B, gpu_k=torch.zeros((5, 2, 8, 128), dtype=torch.bfloat16)),
+           _pool(B, slot_table=torch.zeros((3, 7), dtype=torch.int32)),
+           _pool(B, slot_table=torch.zeros((4, 7), dtype=torch.int64)),
+           _pool(B, slot_table=torch.zeros((4, 14), dtype=torch.int32)[:, ::2]),
+           _pool(B, host_k=torch.zeros((5, 1, 16, 128), dtype=torch.bfloat16))]
+    for pool in bad:
+        with pytest.raises(ValueError):
+            B.check_pool(p, pool)
+    with pytest.raises(ValueError):
+        B.check_pool(_problem(B, seq_lens=torch.zeros(3, dtype=torch.int32)), _pool(B))

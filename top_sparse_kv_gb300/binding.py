@@ -169,12 +169,48 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def raw_stream(stream=None) -> int:
+def raw_stream(device: int, stream=None) -> int:
     """The cudaStream_t of `stream`, or of the current stream, without building a Stream object
-    (torch.cuda.current_stream() costs more than a small kernel's launch)."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    (torch.cuda.current_stream() costs more than a small kernel's launch).  `device`: index of
+    the GPU that holds the call's tensors, which must be the current one and the stream's."""
+    if device < 0 or torch._C._cuda_getDevice() != device:
+        raise ValueError("the tensors must be on the current GPU")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device.index != device:
+        raise ValueError("the stream belongs to another GPU")
+    return stream.cuda_stream
+
+
+def same_device(p: "Problem", **tensors) -> int:
+    """The index of the problem's device (-1: the CPU), which has to hold the tensors too."""
+    for name, t in tensors.items():
+        if t is not None and t.device != p.seq_lens.device:
+            raise ValueError(f"{name}: on {t.device}, seq_lens on {p.seq_lens.device}")
+    return p.seq_lens.get_device()
+
+
+def check_lens(p: "Problem") -> None:
+    t = p.seq_lens
+    if t.dtype != torch.int32 or t.numel() < p.batch or not t.is_contiguous():
+        raise ValueError(f"seq_lens: contiguous int32 [{p.batch}] expected")
+
+
+def check_pool(p: "Problem", pool: "Pool") -> None:
+    """The pool's types, sizes and devices, which the C side cannot see."""
+    same_device(p, gpu_k=pool.gpu_k, gpu_v=pool.gpu_v, slot_table=pool.slot_table)
+    heads = 1 if pool.table_heads else p.n_kv_heads
+    for name, d in (("gpu_k", p.d_qk), ("gpu_v", p.d_v), ("host_k", p.d_qk), ("host_v", p.d_v)):
+        t = getattr(pool, name)
+        if t is None:
+            continue
+        rows = t.shape[0] * (p.n_kv_heads if name.startswith("host") else heads) * p.block_size
+        if t.dtype != element_type(p) or t.numel() != rows * d or not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous {element_type(p)} blocks of {p.block_size} rows of {d} expected")
+    if pool.slot_table.dtype != torch.int32 or not pool.slot_table.is_contiguous() \
+            or pool.slot_table.shape[0] < p.batch:
+        raise ValueError(f"slot_table: contiguous int32, a row for each of {p.batch} requests")
+    check_lens(p)
 
 
 def _check(fn: str, st: int):
@@ -514,7 +550,8 @@ class Rotary:
     k_gamma: Optional[torch.Tensor] = None
 
     def check(self, p: Problem) -> None:
-        """The tensors' types and sizes, which the C side cannot see."""
+        """The tensors' types, sizes and devices, which the C side cannot see."""
+        same_device(p, inv_freq=self.inv_freq, q_gamma=self.q_gamma, k_gamma=self.k_gamma)
         if self.rot_dim and (self.inv_freq is None or self.inv_freq.dtype != torch.float32
                              or self.inv_freq.numel() != self.rot_dim // 2 or not self.inv_freq.is_contiguous()):
             raise ValueError("inv_freq: contiguous float32 [rot_dim / 2]")
@@ -560,6 +597,10 @@ def c_tokens(p: Problem, q, k, v, positions, requests) -> CTokens:
     if first is None:
         raise ValueError("q or k is needed")
     n, dtype = first.shape[0], element_type(p)
+    if n >= 2 ** 31:
+        raise ValueError("at most 2^31 - 1 tokens")
+    check_lens(p)
+    same_device(p, q=q, k=k, v=v, positions=positions, requests=requests)
     qp, qs = _rows("q", q, n, p.n_q_heads, p.d_qk, dtype)
     kp, ks = _rows("k", k, n, p.n_kv_heads, p.d_qk, dtype)
     vp, vs = _rows("v", v, n, p.n_kv_heads, p.d_v, dtype)
@@ -570,10 +611,10 @@ def _out_rows(name: str, out, src, heads: int, d: int, dtype: torch.dtype):
     """Pointer of an output: packed rows, or the input itself (in place at its stride)."""
     if out is None:
         return None
+    if src is None or out.device != src.device:
+        raise ValueError(f"{name}: an output needs its input, on the same device")
     _, stride = _rows(name, out, src.shape[0], heads, d, dtype)
-    if out.data_ptr() == src.data_ptr() and stride == src.stride(0):
-        return out.data_ptr()
-    if stride != heads * d and src.shape[0] > 1:
+    if src.shape[0] > 1 and stride != (src.stride(0) if out.data_ptr() == src.data_ptr() else heads * d):
         raise ValueError(f"{name}: packed rows, or the input itself")
     return out.data_ptr()
 
@@ -581,20 +622,24 @@ def _out_rows(name: str, out, src, heads: int, d: int, dtype: torch.dtype):
 def skv_qk_norm_rope(p: Problem, rotary: Rotary, q, k, q_out, k_out, positions=None, requests=None, dev_status=None,
                      stream=None):
     rotary.check(p)
+    same_device(p, dev_status=dev_status)
     cp, cr, ct = p.c(), rotary.c(), c_tokens(p, q, k, None, positions, requests)
     qo = _out_rows("q_out", q_out, q, p.n_q_heads, p.d_qk, element_type(p))
     ko = _out_rows("k_out", k_out, k, p.n_kv_heads, p.d_qk, element_type(p))
     _check("skv_qk_norm_rope", lib().skv_qk_norm_rope(ctypes.byref(cp), ctypes.byref(cr), ctypes.byref(ct), qo, ko,
-                                                      _ptr(dev_status), _stream(stream)))
+                                                      _ptr(dev_status), raw_stream(p.seq_lens.get_device(), stream)))
 
 
 def skv_append_kv(p: Problem, rotary: Rotary, q, k, v, pool: Pool, q_out, positions=None, requests=None,
                   dev_status=None, stream=None):
     rotary.check(p)
+    check_pool(p, pool)
+    same_device(p, dev_status=dev_status)
     cp, cr, ct, cpool = p.c(), rotary.c(), c_tokens(p, q, k, v, positions, requests), pool.c()
     qo = _out_rows("q_out", q_out, q, p.n_q_heads, p.d_qk, element_type(p))
     _check("skv_append_kv", lib().skv_append_kv(ctypes.byref(cp), ctypes.byref(cr), ctypes.byref(ct),
-                                                ctypes.byref(cpool), qo, _ptr(dev_status), _stream(stream)))
+                                                ctypes.byref(cpool), qo, _ptr(dev_status),
+                                                raw_stream(p.seq_lens.get_device(), stream)))
 
 
 @dataclass
@@ -605,6 +650,9 @@ class Prefix:
     len: int
 
     def check(self, p: Problem) -> None:
+        if not 0 <= self.len <= p.max_len:
+            raise ValueError(f"prefix length {self.len} outside [0, {p.max_len}]")
+        same_device(p, table=self.table)
         need = (self.len + p.block_size - 1) // p.block_size
         if need and (self.table is None or self.table.dtype != torch.int32 or self.table.numel() < need
                      or not self.table.is_contiguous()):
@@ -624,10 +672,17 @@ def skv_prefix_workspace_size(p: Problem, prefix_len: int) -> int:
 
 def skv_prefix_attn(p: Problem, q, pool: Pool, prefix: Prefix, out, lse, ws, dev_status=None, stream=None):
     prefix.check(p)
+    check_pool(p, pool)
+    shape = (p.batch, p.n_q_heads)
+    for name, t, dtype, want in (("q", q, torch.bfloat16, shape + (p.d_qk,)), ("out", out, torch.bfloat16, shape + (p.d_v,)),
+                                 ("lse", lse, torch.float32, shape)):
+        if t is not None and (t.dtype != dtype or tuple(t.shape) != want or not t.is_contiguous()):
+            raise ValueError(f"{name}: contiguous {dtype} {list(want)} expected")
+    device = same_device(p, q=q, out=out, lse=lse, ws=ws, dev_status=dev_status)
     cp, cpool, cx = p.c(), pool.c(), prefix.c()
     _check("skv_prefix_attn", lib().skv_prefix_attn(
         ctypes.byref(cp), _ptr(q), ctypes.byref(cpool), ctypes.byref(cx), _ptr(out), _ptr(lse), _ptr(ws),
-        ws.numel() * ws.element_size(), _ptr(dev_status), _stream(stream)))
+        ws.numel() * ws.element_size(), _ptr(dev_status), raw_stream(device, stream)))
 
 
 def skv_status_string(status: int) -> str:

@@ -708,8 +708,8 @@ skv_status skv_paris_decode_step(const skv_problem* p, const skv_paris* paris, c
 // strides and pointers of one side's rows: `row` entries a token
 static skv_status check_rows(const void* ptr, int64_t stride, long long row, int elem, int32_t n_tokens) {
   if (!aligned16(ptr)) return SKV_ERR_INVALID_ARGUMENT;
-  if (n_tokens > 1 && stride < row) return SKV_ERR_INVALID_ARGUMENT;
-  if (stride < 0 || stride > (1LL << 40) || (stride * elem) % 16) return SKV_ERR_INVALID_ARGUMENT;
+  if (stride < 0 || stride > (1LL << 40)) return SKV_ERR_INVALID_ARGUMENT;
+  if (n_tokens > 1 && (stride < row || (stride * elem) % 16)) return SKV_ERR_INVALID_ARGUMENT;
   return SKV_OK;
 }
 
@@ -722,7 +722,8 @@ static skv_status check_tokens(const skv_problem* p, const skv_rotary* r, const 
   if (r->rot_dim > 0 && (!r->inv_freq || ((uintptr_t)r->inv_freq & 3u))) return SKV_ERR_INVALID_ARGUMENT;
   if (!aligned16(r->q_gamma) || !aligned16(r->k_gamma)) return SKV_ERR_INVALID_ARGUMENT;
   const int elem = p->dtype == SKV_DTYPE_F32 ? 4 : 2;
-  if ((t->q == nullptr) != (q_out == nullptr) || !aligned16(q_out)) return SKV_ERR_INVALID_ARGUMENT;
+  if (t->n_tokens > 0 && (t->q == nullptr) != (q_out == nullptr)) return SKV_ERR_INVALID_ARGUMENT;
+  if (!aligned16(q_out)) return SKV_ERR_INVALID_ARGUMENT;
   if (t->q) SKV_TRY(check_rows(t->q, t->q_stride, (long long)p->n_q_heads * p->d_qk, elem, t->n_tokens));
   if (t->k) SKV_TRY(check_rows(t->k, t->k_stride, (long long)p->n_kv_heads * p->d_qk, elem, t->n_tokens));
   // vectors of 8 entries lie wholly inside or outside every span
@@ -734,10 +735,10 @@ static skv_status check_tokens(const skv_problem* p, const skv_rotary* r, const 
 skv_status skv_qk_norm_rope(const skv_problem* p, const skv_rotary* rotary, const skv_tokens* tokens, void* q_out,
                             void* k_out, int32_t* dev_status, void* stream) {
   SKV_TRY(check_tokens(p, rotary, tokens, q_out));
+  if (tokens->n_tokens == 0) return SKV_OK;  // (buffers of no rows may be null)
   if ((tokens->k == nullptr) != (k_out == nullptr) || !aligned16(k_out)) return SKV_ERR_INVALID_ARGUMENT;
   if (!tokens->q && !tokens->k) return SKV_ERR_INVALID_ARGUMENT;
   if (!tokens->positions && !tokens->requests && tokens->n_tokens > p->batch) return SKV_ERR_INVALID_ARGUMENT;
-  if (tokens->n_tokens == 0) return SKV_OK;
   return launch_token_rows(*p, *rotary, *tokens, PoolView{}, q_out, k_out, dev_status, (cudaStream_t)stream);
 }
 
@@ -745,6 +746,7 @@ skv_status skv_append_kv(const skv_problem* p, const skv_rotary* rotary, const s
                          const skv_kv_pool* pool, void* q_out, int32_t* dev_status, void* stream) {
   SKV_TRY(check_tokens(p, rotary, tokens, q_out));
   SKV_TRY(check_pool(*p, pool));
+  if (tokens->n_tokens == 0) return SKV_OK;
   if (!tokens->k) return SKV_ERR_INVALID_ARGUMENT;
   if (pool->gpu_v != nullptr) {
     const int elem = p->dtype == SKV_DTYPE_F32 ? 4 : 2;
@@ -755,7 +757,6 @@ skv_status skv_append_kv(const skv_problem* p, const skv_rotary* rotary, const s
     return SKV_ERR_INVALID_ARGUMENT;  // the latent layout: one row a token
   }
   if (!tokens->requests && tokens->n_tokens > p->batch) return SKV_ERR_INVALID_ARGUMENT;
-  if (tokens->n_tokens == 0) return SKV_OK;
   return launch_token_rows(*p, *rotary, *tokens, view(pool), q_out, nullptr, dev_status, (cudaStream_t)stream);
 }
 
@@ -767,7 +768,8 @@ static skv_status check_prefix_problem(const skv_problem* p, int32_t prefix_len)
   if (p->dtype != SKV_DTYPE_BF16 || p->d_qk != 128 || p->d_v != 128) return SKV_ERR_UNSUPPORTED;
   if (p->n_q_heads / p->n_kv_heads > 128) return SKV_ERR_UNSUPPORTED;
   if (p->max_len > (1 << 30)) return SKV_ERR_UNSUPPORTED;  // tile positions stay in 32 bits
-  // merge blocks index grid.x
+  // (KV head, request) pairs and the merge's blocks stay in 32 bits
+  if ((long long)p->batch * p->n_kv_heads > 0x7fffffffLL - 256) return SKV_ERR_UNSUPPORTED;
   if (((long long)p->batch * (p->n_q_heads / p->n_kv_heads) + 31) / 32 * p->n_kv_heads > 0x7fffffffLL)
     return SKV_ERR_UNSUPPORTED;
   return SKV_OK;

@@ -723,6 +723,7 @@ __device__ __forceinline__ void mma_role(const Args& a, const Segs& segs, Bars& 
   const uint64_t dv = t5::desc_sw128(base + kQBufs * kStageB, kHalfB, kGroupB);
   const uint32_t ts = tm + slot * 128, to = tm + 256 + slot * 128;
   Steps gen{segs, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, slot, false, false, 0u};
+  pdl_wait();  // no bounded wait runs while the kernels before do
   bool ok = true;
   auto wait = [&](uint64_t* b, uint32_t parity) {
     if (ok) ok = wait_on(b, parity, abort, a.status);

@@ -193,6 +193,8 @@ class TokenStep:
 
     def __init__(self, problem: B.Problem, rotary: B.Rotary, pool: Optional[B.Pool] = None):
         rotary.check(problem)
+        if pool is not None:
+            B.check_pool(problem, pool)
         self.p, self.rotary, self.pool = problem, rotary, pool
         dev = problem.seq_lens.device
         self.status = torch.zeros((1,), dtype=torch.int32, device=dev)
@@ -201,14 +203,15 @@ class TokenStep:
         self._st = self.status.data_ptr()
         self._dtype = B.element_type(problem)
         self._norm_rope, self._append = B.lib().skv_qk_norm_rope, B.lib().skv_append_kv
-        self._seen = {}  # token layouts (types, shapes, strides) that have been checked
+        self._device = problem.seq_lens.get_device()
+        self._seen = {}  # token layouts (types, shapes, strides, devices) that have been checked
 
     def _tokens(self, q, k, v, positions, requests, q_out, k_out):
         """skv_tokens and the outputs' pointers; a layout is checked in full when it first comes."""
-        key = tuple((t.dtype, t.shape, t.stride()) if t is not None else None
+        key = tuple((t.dtype, t.shape, t.stride(), t.get_device()) if t is not None else None
                     for t in (q, k, v, positions, requests, q_out, k_out))
-        in_place = (q is not None and q_out.data_ptr() == q.data_ptr(), k_out is not None
-                    and k_out.data_ptr() == k.data_ptr())
+        in_place = (q is not None and q_out.data_ptr() == q.data_ptr(),
+                    k is not None and k_out is not None and k_out.data_ptr() == k.data_ptr())
         n = self._seen.get((key, in_place))
         if n is None:
             n = B.c_tokens(self.p, q, k, v, positions, requests).n_tokens
@@ -233,7 +236,7 @@ class TokenStep:
         Padding tokens' rows are not written."""
         q_out, k_out = self._out(q_out, q, self.p.n_q_heads), self._out(k_out, k, self.p.n_kv_heads)
         ct, qo, ko = self._tokens(q, k, None, positions, requests, q_out, k_out)
-        st = self._norm_rope(self._p, self._r, ctypes.byref(ct), qo, ko, self._st, B.raw_stream(stream))
+        st = self._norm_rope(self._p, self._r, ctypes.byref(ct), qo, ko, self._st, B.raw_stream(self._device, stream))
         if st:
             raise B.SkvError("skv_qk_norm_rope", st)
         return q_out, k_out
@@ -244,7 +247,7 @@ class TokenStep:
             raise ValueError("append() needs a pool")
         q_out = self._out(q_out, q, self.p.n_q_heads)
         ct, qo, _ = self._tokens(q, k, v, positions, requests, q_out, None)
-        st = self._append(self._p, self._r, ctypes.byref(ct), self._pool, qo, self._st, B.raw_stream(stream))
+        st = self._append(self._p, self._r, ctypes.byref(ct), self._pool, qo, self._st, B.raw_stream(self._device, stream))
         if st:
             raise B.SkvError("skv_append_kv", st)
         return q_out
@@ -258,7 +261,9 @@ class PrefixStep:
     def __init__(self, problem: B.Problem, pool: B.Pool, prefix: B.Prefix):
         prefix.check(problem)
         self.p, self.pool, self.prefix = problem, pool, prefix
+        B.check_pool(problem, pool)
         dev = problem.seq_lens.device
+        self._device = problem.seq_lens.get_device()
         self._shape = (problem.batch, problem.n_q_heads, problem.d_qk)
         self._p, self._pool, self._prefix = (ctypes.byref(x.c()) for x in (problem, pool, prefix))
         self.out = torch.empty((problem.batch, problem.n_q_heads, problem.d_v), dtype=pool.gpu_k.dtype, device=dev)
@@ -272,9 +277,10 @@ class PrefixStep:
 
     def run(self, q, stream=None):
         """(out, lse), the step's own buffers."""
-        if q.shape != self._shape or q.dtype != self.out.dtype or not q.is_contiguous():
-            raise ValueError(f"q: contiguous {self.out.dtype} {list(self._shape)} expected")
-        st = self._call(self._p, q.data_ptr(), self._pool, self._prefix, *self._tail, B.raw_stream(stream))
+        if q.shape != self._shape or q.dtype != self.out.dtype or not q.is_contiguous() \
+                or q.get_device() != self._device:
+            raise ValueError(f"q: contiguous {self.out.dtype} {list(self._shape)} on {self.out.device} expected")
+        st = self._call(self._p, q.data_ptr(), self._pool, self._prefix, *self._tail, B.raw_stream(self._device, stream))
         if st:
             raise B.SkvError("skv_prefix_attn", st)
         return self.out, self.lse
