@@ -87,6 +87,13 @@ CASES = [
     (11, 1, 4, 576, "f32", 8, 560, 0, 512, "qk"),
     (5, 1, 2, 1024, "bf16", 0, 1024, 0, 1024, "qk"),
     (5, 1, 2, 1024, "f32", 0, 1024, 0, 1024, "qk"),
+    # a norm of a part of the row whose entries turn with entries outside it
+    (33, 3, 21, 128, "bf16", 0, 128, 0, 64, "qk"),
+    (21, 2, 6, 128, "f32", 0, 128, 0, 40, "k"),
+    (700, 2, 6, 256, "bf16", 32, 192, 0, 104, "q"),
+    # more rows a token than a stage holds
+    (350, 16, 144, 256, "bf16", 0, 256, 0, 192, "qk"),
+    (320, 8, 200, 128, "f32", 0, 128, 1, 128, "qk"),
 ]
 
 

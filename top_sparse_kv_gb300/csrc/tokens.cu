@@ -152,9 +152,9 @@ __device__ __forceinline__ uint4 narrow(const float* x) {  // the one rounding
   return *reinterpret_cast<uint4*>(out);
 }
 
-// Rows of at most LPR vectors: LPR lanes a row (a vector a lane), normed whole or not at
-// all, a token's rows staged in shared memory.  Persistent CTAs of W row warps and one
-// that runs ahead: for every item -- a token, or a part of its rows where tokens are few --
+// Rows of at most LPR vectors: LPR lanes a row (a vector a lane), a token's rows staged in
+// shared memory.  Persistent CTAs of W row warps and one that runs ahead: for every item --
+// a token, or a part of its rows where tokens are few or its rows many --
 // it fetches the rows by bulk copies (they are consecutive in memory), looks up the
 // position and the pool rows and writes the coefficients A and B of queries and keys,
 // kTokStages items deep, so the row warps meet no latency but shared memory's.
@@ -171,8 +171,9 @@ struct alignas(16) TokenBars {
   int abort;
 };
 constexpr int kInfoBytes = 128;
-// Row warps and resident CTAs a SM: four warps of half-rows (bf16) share a token's fixed
-// costs better than eight (8,192 tokens 54 us against 59), whole-warp rows (fp32) take eight.
+// Row warps and resident CTAs a SM: with half-warp rows (bf16) four warps share a token's
+// fixed costs better than eight (8,192 tokens of 72 rows 54.0 us against 56.9), with whole-warp
+// rows eight are better than four (1,237 fp32 tokens of 48 rows 13.6 against 16.4).
 template <int LPR>
 constexpr int kRowWarps = LPR == 16 ? 4 : 8;
 template <int LPR>
@@ -180,8 +181,9 @@ constexpr int kTokCtas = LPR == 16 ? 4 : 3;
 constexpr int kTokSmemMax = kInfoBytes + kTokStages * (kInfoBytes + 4096 + kTokStageMax);
 static_assert(sizeof(StageInfo) <= kInfoBytes && sizeof(TokenBars) <= kInfoBytes, "");
 
-// PAIR: partners are neighbours of the same vector, else `half` entries away.
-template <typename T, int LPR, bool PAIR>
+// PAIR: partners are neighbours of the same vector, else `half` entries away.  PART: the norm
+// covers a part of the row (as a test at run time it costs 5 % of every other call).
+template <typename T, int LPR, bool PAIR, bool PART>
 __global__ void __launch_bounds__(32 * kRowWarps<LPR> + 32, kTokCtas<LPR>) token_rows_kernel(const TokenArgs a) {
   constexpr int W = kRowWarps<LPR>;
   constexpr int VE = Vec<T>::N, RPW = 32 / LPR, ELEM = sizeof(T);
@@ -197,7 +199,7 @@ __global__ void __launch_bounds__(32 * kRowWarps<LPR> + 32, kTokCtas<LPR>) token
   volatile int* abort = &bar.abort;
   auto stage = [&](int s) { return smem + kInfoBytes + s * stage_bytes; };
   auto weight = [&](const unsigned char* g, int j) -> float {
-    if (g == nullptr) return 1.f;
+    if (g == nullptr || j >= a.norm_dim) return 1.f;
     if constexpr (ELEM == 2)
       return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(g)[j] << 16);
     else
@@ -299,6 +301,7 @@ __global__ void __launch_bounds__(32 * kRowWarps<LPR> + 32, kTokCtas<LPR>) token
   const int sub = lane % LPR, mine = lane / LPR, e0 = sub * VE, w = e0 - a.rot_start;
   const bool in = half > 0 && w >= 0 && w < a.rot_dim, has = e0 < d;
   const int shift = w < half ? half : -half;
+  const bool own = e0 < a.norm_dim, theirs = e0 + shift < a.norm_dim;  // whether the norm covers these, their partners
   int n = 0;
   for (long long it = blockIdx.x; it < items; it += gridDim.x, ++n) {
     const int s = n % kTokStages;
@@ -344,9 +347,19 @@ __global__ void __launch_bounds__(32 * kRowWarps<LPR> + 32, kTokCtas<LPR>) token
             float ssq = 0.f;
 #pragma unroll
             for (int j = 0; j < VE; ++j) ssq = fmaf(x[j], x[j], ssq);
+            if (PART && !own) ssq = 0.f;
 #pragma unroll
             for (int off = LPR / 2; off >= 1; off >>= 1) ssq += __shfl_xor_sync(0xffffffffu, ssq, off);
             inv = rsqrtf(fmaf(ssq, a.inv_norm, a.eps));
+            if (PART) {
+              const float f = own ? inv : 1.f, g = theirs ? inv : 1.f;
+#pragma unroll
+              for (int j = 0; j < VE; ++j) {
+                x[j] *= f;
+                if (!PAIR) y[j] *= g;
+              }
+              inv = 1.f;
+            }
           }
 #pragma unroll
           for (int j = 0; j < VE; ++j) {
@@ -503,16 +516,17 @@ int parts_of(const TokenArgs& a, int per) {
 }
 
 template <typename T, int LPR>
-skv_status launch_short(TokenArgs& a, cudaStream_t st, bool* taken) {
-  const int rows = rows_of(a);
+skv_status launch_short(TokenArgs& a, cudaStream_t st) {
+  const int rows = rows_of(a), wide = (a.v != nullptr && a.dv > a.d ? a.dv : a.d) * (int)sizeof(T);
+  const int most = kTokStageMax / wide;  // rows a stage
   a.parts = parts_of(a, kRowWarps<LPR> * (32 / LPR));
-  const int per = (rows + a.parts - 1) / a.parts, wide = a.v != nullptr && a.dv > a.d ? a.dv : a.d;
-  const long long stage = (long long)per * wide * (int)sizeof(T);
-  *taken = stage <= kTokStageMax;
-  if (!*taken) return SKV_OK;
-  a.stage = (int)((stage + 127) & ~127LL);
+  if (a.parts < (rows + most - 1) / most) a.parts = (rows + most - 1) / most;
+  a.stage = ((rows + a.parts - 1) / a.parts * wide + 127) & ~127;
   const int smem = kInfoBytes + kTokStages * (kInfoBytes + 16 * a.d + a.stage);
-  const auto kernel = a.style == SKV_ROPE_PAIR ? token_rows_kernel<T, LPR, true> : token_rows_kernel<T, LPR, false>;
+  const bool part = a.norm_dim < a.d && (a.gq != nullptr || a.gk != nullptr);
+  const auto kernel = a.style == SKV_ROPE_PAIR
+                          ? (part ? token_rows_kernel<T, LPR, true, true> : token_rows_kernel<T, LPR, true, false>)
+                          : (part ? token_rows_kernel<T, LPR, false, true> : token_rows_kernel<T, LPR, false, false>);
   const skv_status prep = prepare_kernel((const void*)kernel, kTokSmemMax);
   if (prep != SKV_OK) return prep;
   const int fit = 228 * 1024 / (smem + 1024), blocks = fit < kTokCtas<LPR> ? fit : kTokCtas<LPR>;
@@ -578,24 +592,17 @@ skv_status launch_token_rows(const skv_problem& p, const skv_rotary& r, const sk
   a.parts = 1;
   a.stage = 0;
   const int d = a.v != nullptr && p.d_v > p.d_qk ? p.d_v : p.d_qk;
-  // Staged where a row is a vector a lane, is normed whole or not at all, and a token's rows
-  // fit a stage; else a warp a row.
-  const bool whole = (r.q_gamma == nullptr && r.k_gamma == nullptr) || a.norm_dim == p.d_qk;
-  bool taken = false;
-  skv_status done = SKV_OK;
+  // Staged where a row is a vector a lane, else a warp a row (measured on short rows, too:
+  // 8,192 tokens of 72 rows of 128 bf16 54 us staged, 289 us a warp a row; 1,237 of 48 rows
+  // of 128 fp32 13.6 against 17.7).
   if (p.dtype == SKV_DTYPE_F32) {
-    if (whole && d <= 128) done = launch_short<float, 32>(a, st, &taken);
-    if (taken || done != SKV_OK) return done;
+    if (d <= 128) return launch_short<float, 32>(a, st);
     if (d <= 256) return launch_long<float, 2>(a, st);
     if (d <= 640) return launch_long<float, 5>(a, st);
     return launch_long<float, 8>(a, st);
   }
-  if (whole && d <= 128)
-    done = launch_short<__nv_bfloat16, 16>(a, st, &taken);
-  else if (whole && d <= 256)
-    done = launch_short<__nv_bfloat16, 32>(a, st, &taken);
-  if (taken || done != SKV_OK) return done;
-  if (d <= 256) return launch_long<__nv_bfloat16, 1>(a, st);
+  if (d <= 128) return launch_short<__nv_bfloat16, 16>(a, st);
+  if (d <= 256) return launch_short<__nv_bfloat16, 32>(a, st);
   if (d <= 768) return launch_long<__nv_bfloat16, 3>(a, st);
   return launch_long<__nv_bfloat16, 4>(a, st);
 }
