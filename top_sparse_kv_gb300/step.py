@@ -204,27 +204,33 @@ class TokenStep:
         self._dtype = B.element_type(problem)
         self._norm_rope, self._append = B.lib().skv_qk_norm_rope, B.lib().skv_append_kv
         self._device = problem.seq_lens.get_device()
-        self._seen = {}  # token layouts (types, shapes, strides, devices) that have been checked
+        self._seen = None  # the token layout that has been checked
 
     def _tokens(self, q, k, v, positions, requests, q_out, k_out):
-        """skv_tokens and the outputs' pointers; a layout is checked in full when it first comes."""
-        key = tuple((t.dtype, t.shape, t.stride(), t.get_device()) if t is not None else None
-                    for t in (q, k, v, positions, requests, q_out, k_out))
-        in_place = (q is not None and q_out.data_ptr() == q.data_ptr(),
-                    k is not None and k_out is not None and k_out.data_ptr() == k.data_ptr())
-        n = self._seen.get((key, in_place))
-        if n is None:
-            n = B.c_tokens(self.p, q, k, v, positions, requests).n_tokens
+        """skv_tokens and the outputs' pointers.  A layout -- types, shapes, strides, devices, what is in
+        place -- is checked in full when it differs from the last one checked."""
+        tensors = (q, k, v, positions, requests, q_out, k_out)
+        ptr = [None if t is None else t.data_ptr() for t in tensors]
+        seen = [None if t is None else (t.dtype, t.shape, t.stride(), t.get_device()) for t in tensors]
+        seen.append(ptr[5] == ptr[0])
+        seen.append(ptr[6] == ptr[1])
+        if seen != self._seen:
+            B.c_tokens(self.p, q, k, v, positions, requests)
             if q_out is not None:
                 B._out_rows("q_out", q_out, q, self.p.n_q_heads, self.p.d_qk, self._dtype)
             if k_out is not None:
                 B._out_rows("k_out", k_out, k, self.p.n_kv_heads, self.p.d_qk, self._dtype)
-            if len(self._seen) > 64:
-                self._seen.clear()
-            self._seen[key, in_place] = n
-        ptr = [None if t is None else t.data_ptr() for t in (q, k, v, positions, requests, q_out, k_out)]
-        strides = [0 if e is None else e[2][0] for e in key[:3]]
-        return B.CTokens(n, 0, ptr[0], ptr[1], ptr[2], strides[0], strides[1], strides[2], ptr[3], ptr[4]), ptr[5], ptr[6]
+            self._seen = seen
+        layout, qs, ks, vs = None, 0, 0, 0
+        if q is not None:
+            layout = seen[0]
+            qs = layout[2][0]
+        if k is not None:
+            layout = seen[1]
+            ks = layout[2][0]
+        if v is not None:
+            vs = seen[2][2][0]
+        return B.CTokens(layout[1][0], 0, ptr[0], ptr[1], ptr[2], qs, ks, vs, ptr[3], ptr[4]), ptr[5], ptr[6]
 
     def _out(self, out, src, heads):
         if src is None or out is not None:
