@@ -7,14 +7,15 @@
 // products on the tcgen05 tensor cores, and the prefix crosses HBM once; a tail [P, L_b)
 // meets the G rows of its own request the same way.  Both are cut into tiles of 128 keys.
 //
-// prefix_attn_kernel, one persistent CTA an SM, 16 warps:
+// prefix_attn_kernel, one persistent CTA an SM, 13 warps:
 //   warps 0-3, 4-7   softmax of slot 0 / slot 1 (a thread a query row)
 //   warp 8           16 keys of a block of the GPU pool by one 4 KB TMA copy, into a ring of
 //                    32 KB K / V stages in the 128-byte-swizzled layout that the MMA reads
 //   warp 9           every other key -- at a history's edge, in the host pool (over UVA), of
 //                    blocks that 16 does not divide -- row by row, 16-byte cp.async with
-//                    zeros for what is not attended; and the key masks.  A warp of its own,
-//                    so that waiting for its rows to land holds back no TMA copy.
+//                    zeros for what is not attended (all keys this way: batch 8 on 32K keys
+//                    79 us, by TMA 33; batch 64 on 128K 566, by TMA 223); and the key masks.
+//                    A warp of its own, so that waiting for its rows holds back no TMA copy.
 //   warp 10          cuts the CTA's share into segments, published in a ring for the other
 //                    roles, and copies their query rows, by cp.async
 //   warps 11, 12     issue the MMAs of slot 0 / slot 1 (converged, one elected lane: the
@@ -37,6 +38,19 @@
 // consecutive CTAs.  A segment's O, m and l go to the workspace, at an index that grows
 // with both the CTA and the unit, so no two segments share one and no atomics are needed.
 // prefix_merge_kernel joins a row's partials by log-sum-exp, in a fixed order.
+//
+// What bounds it (8 KV heads of 8 query heads, CUDA graphs of 30 calls).  Few rows, long
+// prefix -- batch 8 on 32K keys, 33.3 us: HBM while the prefix streams (134 MB, 20 us), then
+// the tails, the start and the merge, a few us each.  Many rows -- batch 64 on 128K keys, 275
+// GFLOP in 223 us, 1.23 PFLOP/s: the chain of a slot's step.  Of about 3,300 cycles a pair of
+// steps, the maximum takes 700, the exponentials 1,300, and the other P V half, the next S and
+// the hand-overs between them 1,300, in which the other slot's MMAs have their turn; the
+// tensor pipe is busy 53 % of the time.  Instruction fetch was the bound before that: the roles
+// run different code on the same SM, so loops are rolled, waits out of line, call sites
+// single (unrolled over 64 keys the exponentials took 241 us in place of 226).
+// Slower in the same measure: S of 64 keys at a time, twice buffered (233; an S as two N = 64
+// MMAs costs more than one of N = 128, 234 by itself); sixteen softmax warps (244 against
+// 226); P V begun after 96 of 128 keys (226) or in three parts (229).
 #include <cuda.h>  // CUtensorMap and its enums
 
 #include "attn_common.cuh"
@@ -47,7 +61,7 @@ namespace {
 
 namespace px {
 constexpr int kCtas = 152;             // one CTA an SM of a GB300 (a function of the problem alone: sizes the workspace)
-constexpr int kThreads = 512;
+constexpr int kThreads = 416;
 constexpr int kTile = 128;             // keys a tile, query rows a tile
 constexpr int kStageB = kTile * 256;   // a K, V or Q tile, 32 KB: [group of 8 rows][half of the dims][8 rows][128 bytes]
 constexpr int kGroupB = 2048;          // a group of 8 rows
@@ -314,9 +328,6 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile
 // one barrier the parity it waits for could be that of two rounds before.  With two, the
 // round before on the same barrier (ten loads back) is over: the load that the warp saw
 // last was issued after it had been handed back.
-__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr) : "memory");
-}
 struct Bars {
   uint64_t seg[kSegs], seg_free[kSegs], full[2 * kRing], empty[kRing], qfull[kQBufs], qempty[kQBufs], mask[kMasks], s[2], p[2][2], o[2], x[2], turn[2], drain[2];
 };
@@ -753,7 +764,7 @@ __device__ __forceinline__ void mma_role(const Args& a, const Segs& segs, Bars& 
   };
   // The slots' MMAs go in turns, O of a step and S of the next together: shared between the
   // slots, the pipe would finish both late and the softmaxes would run, and wait, in phase
-  // (batch 64 on 128K keys: 322 us without turns).
+  // (batch 64 on 128K keys, when they came: 230 us with turns, 262 without).
   auto pass_turn = [&] {
     if ((threadIdx.x & 31) == 0) mbar_arrive(&bar.turn[slot ^ 1]);
   };
@@ -892,7 +903,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Segs segs, Bars& bar
             sum[i & 1] = add2(sum[i & 1], pack2(z0, z1));
             pk[i] = tc::pack_bf16(z0, z1);
           }
-          st16(ts + (c >> 1), pk);  // P of these keys, over S columns that have been read
+          t5::st16(ts + (c >> 1), pk);  // P of these keys, over S columns that have been read
           if (c < 96) t5::ld32_async(ts + c + 32, v);
           if (c == 32) {  // the first 64 keys' P V may start
             t5::st_wait();
@@ -1018,7 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
       mbar_init(&bar.turn[i], 1);
       mbar_init(&bar.drain[i], 1);
     }
-      fence_barrier_init();
+    fence_barrier_init();
     sh.abort = 0;
   }
   if (warp == 0) {
@@ -1058,7 +1069,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
 // partial is a coalesced float4.  A thread runs once over its share with a running maximum,
 // kMergeBatch partials' loads in flight at a time (bound by their latency: one round for
 // most shapes); the shares are joined through shared memory.  The order is fixed.  Four
-// shares where the rows are few, two where the CTAs fill the device without.
+// shares where the rows are few, two where the CTAs fill the device without (batch 8 on 32K
+// keys in all 33.5 us with four, 34.3 with two; batch 64 on 128K 234 and 225).
 constexpr int kMergeDims = 8;
 constexpr int kMergeBatch = 5;
 
