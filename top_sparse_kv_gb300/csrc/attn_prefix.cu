@@ -42,15 +42,19 @@
 // What bounds it (8 KV heads of 8 query heads, CUDA graphs of 30 calls).  Few rows, long
 // prefix -- batch 8 on 32K keys, 33.3 us: HBM while the prefix streams (134 MB, 20 us), then
 // the tails, the start and the merge, a few us each.  Many rows -- batch 64 on 128K keys, 275
-// GFLOP in 223 us, 1.23 PFLOP/s: the chain of a slot's step.  Of about 3,300 cycles a pair of
-// steps, the maximum takes 700, the exponentials 1,300, and the other P V half, the next S and
-// the hand-overs between them 1,300, in which the other slot's MMAs have their turn; the
-// tensor pipe is busy 53 % of the time.  Instruction fetch was the bound before that: the roles
-// run different code on the same SM, so loops are rolled, waits out of line, call sites
-// single (unrolled over 64 keys the exponentials took 241 us in place of 226).
+// GFLOP in 223 us, 1.23 PFLOP/s: the chain of a slot's step, 3,230 cycles.  The softmax takes
+// 1,900 of them (the maximum 600, then 20 cycles a pair of keys, where a warp alone needs 12.5
+// for the exponentials, sums and roundings without TMEM's latencies); the second half of P V
+// and the next S 980 (S reads 8 KB of shared memory an MMA, 128 bytes a cycle of its 64: it
+// runs a little below the pipe's rate); the hand-overs 330.  Both slots' MMAs together are
+// 2,400, in turns.  Instruction fetch was the bound before that: the roles run different code
+// on the same SM, so loops are rolled, waits out of line, call sites single (unrolled over 64
+// keys the exponentials took 241 us in place of 226).
 // Slower in the same measure: S of 64 keys at a time, twice buffered (233; an S as two N = 64
 // MMAs costs more than one of N = 128, 234 by itself); sixteen softmax warps (244 against
-// 226); P V begun after 96 of 128 keys (226) or in three parts (229).
+// 226); P V begun after 96 of 128 keys (226) or in three parts (229); the first tile's maximum
+// kept until a chunk of 32 keys outgrows it, without the pass for the maximum (236: the
+// test and the maximum cost the exponentials' loop more than the pass did).
 #include <cuda.h>  // CUtensorMap and its enums
 
 #include "attn_common.cuh"
