@@ -221,26 +221,20 @@ class TokenStep:
             if k_out is not None:
                 B._out_rows("k_out", k_out, k, self.p.n_kv_heads, self.p.d_qk, self._dtype)
             self._seen = seen
-        layout, qs, ks, vs = None, 0, 0, 0
-        if q is not None:
-            layout = seen[0]
-            qs = layout[2][0]
-        if k is not None:
-            layout = seen[1]
-            ks = layout[2][0]
-        if v is not None:
-            vs = seen[2][2][0]
-        return B.CTokens(layout[1][0], 0, ptr[0], ptr[1], ptr[2], qs, ks, vs, ptr[3], ptr[4]), ptr[5], ptr[6]
+        lq, lk, lv = seen[:3]
+        return (B.CTokens((lk or lq)[1][0], 0, ptr[0], ptr[1], ptr[2], lq[2][0] if lq else 0, lk[2][0] if lk else 0,
+                          lv[2][0] if lv else 0, ptr[3], ptr[4]), ptr[5], ptr[6])
 
-    def _out(self, out, src, heads):
-        if src is None or out is not None:
-            return out
+    def _new(self, src, heads):
         return torch.empty((src.shape[0], heads, self.p.d_qk), dtype=src.dtype, device=src.device)
 
     def norm_rope(self, q, k, positions=None, requests=None, q_out=None, k_out=None, stream=None):
         """(q_out, k_out): new tensors unless given; pass q and k themselves to work in place.
         Padding tokens' rows are not written."""
-        q_out, k_out = self._out(q_out, q, self.p.n_q_heads), self._out(k_out, k, self.p.n_kv_heads)
+        if q_out is None and q is not None:
+            q_out = self._new(q, self.p.n_q_heads)
+        if k_out is None and k is not None:
+            k_out = self._new(k, self.p.n_kv_heads)
         ct, qo, ko = self._tokens(q, k, None, positions, requests, q_out, k_out)
         st = self._norm_rope(self._p, self._r, ctypes.byref(ct), qo, ko, self._st, B.raw_stream(self._device, stream))
         if st:
@@ -251,7 +245,8 @@ class TokenStep:
         """Appends k and v to the pool; returns q_out (None without q)."""
         if self._pool is None:
             raise ValueError("append() needs a pool")
-        q_out = self._out(q_out, q, self.p.n_q_heads)
+        if q_out is None and q is not None:
+            q_out = self._new(q, self.p.n_q_heads)
         ct, qo, _ = self._tokens(q, k, v, positions, requests, q_out, None)
         st = self._append(self._p, self._r, ctypes.byref(ct), self._pool, qo, self._st, B.raw_stream(self._device, stream))
         if st:
