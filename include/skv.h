@@ -9,6 +9,10 @@
  *   attend  with split-K flash decoding and a log-sum-exp merge        skv_sparse_attn
  * and all four chained on one stream                                   skv_decode_step
  *
+ * Beside it: a step's new tokens, normed, rotated and appended to the pools
+ * (skv_qk_norm_rope, skv_append_kv), and dense attention over a prefix that the batch
+ * shares (skv_prefix_attn).
+ *
  * Conventions (every entry point):
  *  - The caller owns all memory.  Device buffers, pinned host pools and the
  *    workspace are allocated by the caller; the library allocates nothing,
@@ -31,7 +35,8 @@
  *    attended row gets zero weight) and completes.  dev_status is a device
  *    int32 the caller zeroes and reads after the stream has drained; it may
  *    be NULL (no reporting).
- *  - All tensors are dense row-major ("C order") and 16-byte aligned.
+ *  - All tensors are dense row-major ("C order") and 16-byte aligned (the rows of
+ *    skv_tokens have a stride from token to token).
  *    Element types: SKV_DTYPE_BF16 (bf16 storage, fp32 arithmetic) or
  *    SKV_DTYPE_F32 (fp32 storage and arithmetic) for q, keys, pools and out;
  *    scores and lse are always fp32; indices and tables int32.
@@ -614,11 +619,13 @@ typedef struct skv_rotary {
  * The tokens of one call.  q, k and v are rows of n_q_heads * d_qk, n_kv_heads * d_qk and
  * n_kv_heads * d_v entries (the heads packed), q_stride / k_stride / v_stride elements
  * apart from token to token: column ranges of one fused projection output are fine.
- * Base pointers are 16-byte aligned and strides are multiples of 16 bytes.
+ * Base pointers are 16-byte aligned and strides are multiples of 16 bytes (of a lone token
+ * the stride is not looked at; with n_tokens 0 the pointers may be NULL).
  *   q           NULL: the call has no queries.
  *   positions   device int32 [n_tokens]; a negative one marks a padding token: its rows
- *               (which must be there) may be read, nothing is written.  NULL: token i ends its request's history,
- *               position seq_lens[request] - 1 (a history of length 0: a padding token).
+ *               (which must be there) may be read, nothing is written.  NULL: token i ends
+ *               its request's history, position seq_lens[request] - 1 (a history of
+ *               length 0: a padding token).
  *   requests    device int32 [n_tokens]: the request (slot-table row) of each token, a
  *               negative one again padding.  NULL: token i is request i's.
  * A position outside [0, max_len) sets SKV_DEV_BAD_LENGTH and a request past the batch
@@ -675,8 +682,8 @@ skv_status skv_append_kv(const skv_problem *p, const skv_rotary *rotary, const s
  *          with len 0 (every request then attends through its own row alone).
  *   len    in [0, max_len].
  * A request is of length 0 (an unused row of the batch: out 0, lse -inf) or holds the
- * whole prefix (L_b >= len); a length between sets SKV_DEV_BAD_LENGTH and leaves out 0
- * and lse -inf.  An entry outside its pool sets SKV_DEV_BAD_SLOT and its rows get zero
+ * whole prefix (L_b >= len); a length between, or below 0, sets SKV_DEV_BAD_LENGTH and
+ * leaves out 0 and lse -inf; one past max_len sets it too and counts as max_len.  An entry outside its pool sets SKV_DEV_BAD_SLOT and its rows get zero
  * weight.  What lies in a pool past a history's end or the prefix's end is never used.
  * Of p, batch, the head counts, d_qk, d_v, max_len, block_size, dtype, sm_scale and
  * seq_lens are used.  bf16, d_qk = d_v = 128, K and V pools with one table row a request
