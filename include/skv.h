@@ -697,7 +697,8 @@ typedef struct skv_prefix {
   int32_t reserved;               /* 0 */
 } skv_prefix;
 
-/* Bytes of workspace skv_prefix_attn needs for this problem and prefix length. */
+/* Bytes of workspace skv_prefix_attn needs for this problem and prefix length.  A call has
+ * its workspace alone until it has run; calls in turn on one stream may share one. */
 skv_status skv_prefix_workspace_size(const skv_problem *p, int32_t prefix_len, size_t *bytes);
 
 skv_status skv_prefix_attn(const skv_problem *p, const void *q, const skv_kv_pool *pool, const skv_prefix *prefix,

@@ -50,15 +50,16 @@ def _problem(B, **over):
     return p
 
 
-def _call(B, q=FAKE, out=FAKE, ws=FAKE, ws_bytes=1 << 40, problem=None, pool=None, prefix=None):
+def _call(B, q=FAKE, out=FAKE, ws=FAKE, ws_bytes=1 << 40, problem=None, pool=None, prefix=None, lse=None,
+          dev_status=None):
     p = _problem(B, **(problem or {}))
     pl = B.CPool(FAKE, FAKE, 10, None, None, 0, FAKE, 63, 0)
     px = B.CPrefix(FAKE, 500, 0)
     for obj, over in ((pl, pool), (px, prefix)):
         for k, v in (over or {}).items():
             setattr(obj, k, v)
-    return B.lib().skv_prefix_attn(ctypes.byref(p), q, ctypes.byref(pl), ctypes.byref(px), out, None, ws, ws_bytes,
-                                   None, None)
+    return B.lib().skv_prefix_attn(ctypes.byref(p), q, ctypes.byref(pl), ctypes.byref(px), out, lse, ws, ws_bytes,
+                                   dev_status, None)
 
 
 @pytest.mark.parametrize("over,status", [
@@ -73,6 +74,10 @@ def _call(B, q=FAKE, out=FAKE, ws=FAKE, ws_bytes=1 << 40, problem=None, pool=Non
     (dict(q=None), INVALID),
     (dict(q=FAKE + 8), INVALID),
     (dict(out=None), INVALID),
+    (dict(lse=FAKE + 2), INVALID),
+    (dict(dev_status=FAKE + 2), INVALID),
+    (dict(problem=dict(seq_lens=FAKE + 2)), INVALID),
+    (dict(pool=dict(slot_table=FAKE + 2)), INVALID),
     (dict(ws=None), INVALID),
     (dict(ws=FAKE + 8), INVALID),
     (dict(ws_bytes=100), WORKSPACE),

@@ -58,15 +58,15 @@ def _args(B, problem=None, rotary=None, tokens=None, pool=None):
     return p, r, t, pl
 
 
-def _append(B, q_out=FAKE, **over):
+def _append(B, q_out=FAKE, dev_status=None, **over):
     p, r, t, pl = _args(B, **over)
-    return B.lib().skv_append_kv(ctypes.byref(p), ctypes.byref(r), ctypes.byref(t), ctypes.byref(pl), q_out, None,
+    return B.lib().skv_append_kv(ctypes.byref(p), ctypes.byref(r), ctypes.byref(t), ctypes.byref(pl), q_out, dev_status,
                                  None)
 
 
-def _norm(B, q_out=FAKE, k_out=FAKE, **over):
+def _norm(B, q_out=FAKE, k_out=FAKE, dev_status=None, **over):
     p, r, t, _ = _args(B, **over)
-    return B.lib().skv_qk_norm_rope(ctypes.byref(p), ctypes.byref(r), ctypes.byref(t), q_out, k_out, None, None)
+    return B.lib().skv_qk_norm_rope(ctypes.byref(p), ctypes.byref(r), ctypes.byref(t), q_out, k_out, dev_status, None)
 
 
 INVALID, UNSUPPORTED = 1, 2
@@ -89,6 +89,11 @@ BOTH = [
     (dict(rotary=dict(norm_dim=136)), INVALID),
     (dict(rotary=dict(inv_freq=None)), INVALID),
     (dict(rotary=dict(q_gamma=FAKE + 4)), INVALID),
+    (dict(rotary=dict(inv_freq=FAKE + 2)), INVALID),
+    (dict(tokens=dict(positions=FAKE + 2)), INVALID),
+    (dict(tokens=dict(requests=FAKE + 2)), INVALID),
+    (dict(problem=dict(seq_lens=FAKE + 2)), INVALID),
+    (dict(dev_status=FAKE + 2), INVALID),
     (dict(rotary=dict(rot_dim=120)), UNSUPPORTED),  # halves that split a vector
     (dict(rotary=dict(rot_dim=116, style=1)), UNSUPPORTED),
     (dict(rotary=dict(rot_start=4, rot_dim=64)), UNSUPPORTED),
@@ -113,6 +118,7 @@ def test_both_refuse(B, over, status):
     (dict(tokens=dict(v_stride=100)), INVALID),
     (dict(pool=dict(gpu_k=None)), INVALID),
     (dict(pool=dict(table_stride=62)), INVALID),
+    (dict(pool=dict(slot_table=FAKE + 2)), INVALID),
     (dict(pool=dict(gpu_v=None)), INVALID),          # the latent layout has one KV head
     (dict(problem=dict(d_v=1032)), UNSUPPORTED),
 ])

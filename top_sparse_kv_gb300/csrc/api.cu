@@ -705,6 +705,8 @@ skv_status skv_paris_decode_step(const skv_problem* p, const skv_paris* paris, c
 
 // ---------------------------------------------------------------- new tokens
 
+static bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
 // strides and pointers of one side's rows: `row` entries a token
 static skv_status check_rows(const void* ptr, int64_t stride, long long row, int elem, int32_t n_tokens) {
   if (!aligned16(ptr)) return SKV_ERR_INVALID_ARGUMENT;
@@ -719,7 +721,8 @@ static skv_status check_tokens(const skv_problem* p, const skv_rotary* r, const 
   if (r->style != SKV_ROPE_HALF && r->style != SKV_ROPE_PAIR) return SKV_ERR_INVALID_ARGUMENT;
   if (r->rot_start < 0 || r->rot_dim < 0 || r->norm_dim < 0 || !(r->eps >= 0.f)) return SKV_ERR_INVALID_ARGUMENT;
   if ((long long)r->rot_start + r->rot_dim > p->d_qk || r->norm_dim > p->d_qk) return SKV_ERR_INVALID_ARGUMENT;
-  if (r->rot_dim > 0 && (!r->inv_freq || ((uintptr_t)r->inv_freq & 3u))) return SKV_ERR_INVALID_ARGUMENT;
+  if (r->rot_dim > 0 && (!r->inv_freq || !aligned4(r->inv_freq))) return SKV_ERR_INVALID_ARGUMENT;
+  if (!aligned4(t->positions) || !aligned4(t->requests) || !aligned4(p->seq_lens)) return SKV_ERR_INVALID_ARGUMENT;
   if (!aligned16(r->q_gamma) || !aligned16(r->k_gamma)) return SKV_ERR_INVALID_ARGUMENT;
   const int elem = p->dtype == SKV_DTYPE_F32 ? 4 : 2;
   if (t->n_tokens > 0 && (t->q == nullptr) != (q_out == nullptr)) return SKV_ERR_INVALID_ARGUMENT;
@@ -735,6 +738,7 @@ static skv_status check_tokens(const skv_problem* p, const skv_rotary* r, const 
 skv_status skv_qk_norm_rope(const skv_problem* p, const skv_rotary* rotary, const skv_tokens* tokens, void* q_out,
                             void* k_out, int32_t* dev_status, void* stream) {
   SKV_TRY(check_tokens(p, rotary, tokens, q_out));
+  if (!aligned4(dev_status)) return SKV_ERR_INVALID_ARGUMENT;
   if (tokens->n_tokens == 0) return SKV_OK;  // (buffers of no rows may be null)
   if ((tokens->k == nullptr) != (k_out == nullptr) || !aligned16(k_out)) return SKV_ERR_INVALID_ARGUMENT;
   if (!tokens->q && !tokens->k) return SKV_ERR_INVALID_ARGUMENT;
@@ -746,6 +750,7 @@ skv_status skv_append_kv(const skv_problem* p, const skv_rotary* rotary, const s
                          const skv_kv_pool* pool, void* q_out, int32_t* dev_status, void* stream) {
   SKV_TRY(check_tokens(p, rotary, tokens, q_out));
   SKV_TRY(check_pool(*p, pool));
+  if (!aligned4(pool->slot_table) || !aligned4(dev_status)) return SKV_ERR_INVALID_ARGUMENT;
   if (tokens->n_tokens == 0) return SKV_OK;
   if (!tokens->k) return SKV_ERR_INVALID_ARGUMENT;
   if (pool->gpu_v != nullptr) {
@@ -787,7 +792,9 @@ skv_status skv_prefix_attn(const skv_problem* p, const void* q, const skv_kv_poo
   SKV_TRY(check_problem(p));
   SKV_TRY(check_pool(*p, pool));
   if (!prefix || prefix->reserved != 0) return SKV_ERR_INVALID_ARGUMENT;
-  if (prefix->len > 0 && (!prefix->table || ((uintptr_t)prefix->table & 3u))) return SKV_ERR_INVALID_ARGUMENT;
+  if (prefix->len > 0 && (!prefix->table || !aligned4(prefix->table))) return SKV_ERR_INVALID_ARGUMENT;
+  if (!aligned4(p->seq_lens) || !aligned4(pool->slot_table) || !aligned4(lse) || !aligned4(dev_status))
+    return SKV_ERR_INVALID_ARGUMENT;
   SKV_TRY(check_prefix_problem(p, prefix->len));
   SKV_TRY(no_head_table(pool));
   if (!pool->gpu_v) return SKV_ERR_UNSUPPORTED;  // latent rows
