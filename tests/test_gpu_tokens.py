@@ -413,3 +413,20 @@ def test_refuses_what_is_not_on_the_gpu(skv):
     with pytest.raises(ValueError):
         step.norm_rope(q.cuda(), k.cuda(), pos.cuda(), q_out=torch.empty_like(q.contiguous()))
     assert skv.lib().skv_launch_count() == n0
+
+
+def test_a_given_stream(skv):
+    """Calls on a stream that is not the current one, their outputs theirs: freed ones are not handed
+    to the current stream's work while the call may still write them."""
+    p, r, fused, q, k, gam, pos, inv = _make(skv, (777, 8, 64, 128, "bf16", 0, 128, 0, 0, "qk"))
+    step, side = skv.TokenStep(p, r), torch.cuda.Stream()
+    qd, kd, posd = q.cuda(), k.cuda(), pos.cuda()
+    want = step.norm_rope(qd, kd, posd)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        step.norm_rope(qd, kd, posd, stream=side)  # outputs dropped at once
+        mine = torch.full_like(want[0], 3.0)
+        assert bool((mine == 3.0).all())
+    got = step.norm_rope(qd, kd, posd, stream=side)
+    side.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -225,16 +225,20 @@ class TokenStep:
         return (B.CTokens((lk or lq)[1][0], 0, ptr[0], ptr[1], ptr[2], lq[2][0] if lq else 0, lk[2][0] if lk else 0,
                           lv[2][0] if lv else 0, ptr[3], ptr[4]), ptr[5], ptr[6])
 
-    def _new(self, src, heads):
+    def _new(self, src, heads, stream):
+        """An output, of the allocator's pool of the stream that writes it."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self._new(src, heads, None)
         return torch.empty((src.shape[0], heads, self.p.d_qk), dtype=src.dtype, device=src.device)
 
     def norm_rope(self, q, k, positions=None, requests=None, q_out=None, k_out=None, stream=None):
         """(q_out, k_out): new tensors unless given; pass q and k themselves to work in place.
         Padding tokens' rows are not written."""
         if q_out is None and q is not None:
-            q_out = self._new(q, self.p.n_q_heads)
+            q_out = self._new(q, self.p.n_q_heads, stream)
         if k_out is None and k is not None:
-            k_out = self._new(k, self.p.n_kv_heads)
+            k_out = self._new(k, self.p.n_kv_heads, stream)
         ct, qo, ko = self._tokens(q, k, None, positions, requests, q_out, k_out)
         st = self._norm_rope(self._p, self._r, ctypes.byref(ct), qo, ko, self._st, B.raw_stream(self._device, stream))
         if st:
@@ -246,7 +250,7 @@ class TokenStep:
         if self._pool is None:
             raise ValueError("append() needs a pool")
         if q_out is None and q is not None:
-            q_out = self._new(q, self.p.n_q_heads)
+            q_out = self._new(q, self.p.n_q_heads, stream)
         ct, qo, _ = self._tokens(q, k, v, positions, requests, q_out, None)
         st = self._append(self._p, self._r, ctypes.byref(ct), self._pool, qo, self._st, B.raw_stream(self._device, stream))
         if st:
