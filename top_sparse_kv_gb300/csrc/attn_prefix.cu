@@ -374,12 +374,12 @@ struct Segs {
 
 // ---------------------------------------------------------------------------- gather warps
 // The row warp's copies are announced on their stage's barrier by the warp once they have
-// landed: two copy groups fly while the next is issued, and a wait for a free stage
-// announces what is in flight first (what frees it may need those tiles).
+// landed: a load's fly while the next is issued, and a wait for a free stage announces what
+// is in flight first (what frees it may need those tiles).
 struct Rows {
   const Args& a;
   volatile int* abort;
-  uint64_t *older, *newer;  // barriers of the unannounced copy groups (null: none)
+  uint64_t* flying;  // barrier of the unannounced copies (null: none)
   bool ok;
 
   __device__ __forceinline__ void announce(uint64_t* b) {
@@ -389,23 +389,18 @@ struct Rows {
   }
   __device__ __forceinline__ void commit(uint64_t* b) {
     cp_async_commit();
-    if (older) {
-      cp_async_wait<2>();
-      announce(older);
+    if (flying) {
+      cp_async_wait<1>();
+      announce(flying);
     }
-    older = newer;
-    newer = b;
+    flying = b;
   }
   __device__ __forceinline__ void flush() {
-    if (older) {
-      cp_async_wait<1>();
-      announce(older);
-    }
-    if (newer) {
+    if (flying) {
       cp_async_wait<0>();
-      announce(newer);
+      announce(flying);
     }
-    older = newer = nullptr;
+    flying = nullptr;
   }
   __device__ __forceinline__ void wait_free(uint64_t* b, uint32_t parity) {
     if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return;
@@ -521,22 +516,31 @@ __device__ __forceinline__ void tma_role(const Args& a, const CUtensorMap* tk, c
   }
 }
 
+// Blocks of whole chunks of 16: a chunk's rows lie one behind another, 4 KB, so one table
+// entry places them and a copy instruction takes two rows (four lines; half a row a lane
+// would touch 32).  Other block sizes: an entry a row.
 __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, unsigned char* gbase, uint4* masks,
                                           volatile int* abort) {
   const int lane = threadIdx.x & 31;
   pdl_wait();
-  Rows g{a, abort, nullptr, nullptr, true};
-  const int r16 = lane >> 1, half = lane & 1;  // a lane copies half a row
-  const uint32_t row_off = (uint32_t)((r16 >> 3) * kGroupB + half * kHalfB + (r16 & 7) * 128);
+  Rows g{a, abort, nullptr, true};
+  const bool chunked = a.bs % kChunk == 0;
+  const int r16 = lane >> 1, half = lane & 1;    // other block sizes: a lane copies half a row
+  const int odd = lane >> 4, piece = lane & 15;  // chunks: 16 lanes a row
   int T = 0;
   uint32_t sq = 0, par = 1;
   auto advance = [&] {
     if (++sq == 2 * kRing) sq = 0;
     if (sq == 0 || sq == kRing) par ^= 1u;
   };
-  long long ref[4], before[4];  // lane l: rows l, l + 32, l + 64, l + 96 of this tile, of the tile whose V is owed
-  uint32_t whole_before = 0;
+  // lane l: rows l, l + 32, l + 64, l + 96 of this tile, of the tile whose V is owed; of
+  // chunks, lanes 0-7 the first row (in [0]) and which of the 16 are attended
+  long long ref[4], before[4];
+  uint32_t bits = 0, bits_before = 0, whole_before = 0;
   bool owed = false, more = true;
+  auto entry = [&](const Seg* s, int t) {  // of the chunk at t (0: none of it is attended)
+    return chunked && t < s->hi && t + kChunk > s->lo ? s->table[block_of(a, t)] : 0;
+  };
   while (g.ok && more) {
     if (!segs.ready()) g.flush();  // a wait that does not announce
     const Seg* s = segs.next();
@@ -544,24 +548,43 @@ __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, u
     if (!more && (!owed || *abort)) break;
     const int n = more ? s->n : 1, h = more ? s->h : 0;
     const bool two = more && s->n1 > 0;
-    int t0 = more ? s->t0 : 0, e = more ? chunk_entry(a, s, t0, lane) : -1;
-    uint32_t all = 0;
+    int t0 = more ? s->t0 : 0, e = more ? entry(s, t0 + kChunk * lane) : 0;
+    uint32_t all = 0, some = 0;  // four tiles' chunks: those that TMA takes; a lane each, the attended rows
+    long long first = -1;        // and the first row
     if (!more) advance();
 #pragma unroll 1
     for (int i = 0; g.ok && i < n; ++i, ++T, t0 += kTile) {
-      if (more && (i & 3) == 0) {
-        all = __ballot_sync(0xffffffffu, chunk_group(a, h, e, t0, lane) >= 0);
-        e = chunk_entry(a, s, t0 + 4 * kTile, lane);
+      if (more && chunked) {
+        if ((i & 3) == 0) {
+          const int t = t0 + kChunk * lane, lo = s->lo - t, hi = s->hi - t;
+          some = hi <= 0 || lo >= kChunk ? 0u : (hi >= kChunk ? 0xffffu : (1u << hi) - 1) & (lo > 0 ? ~0u << lo : ~0u);
+          first = some ? row_ref(a, h, e, t) : -1;
+          if (some && first < 0) {
+            flag(a.status, SKV_DEV_BAD_SLOT);
+            some = 0;
+          }
+          all = __ballot_sync(0xffffffffu, a.tma && some == 0xffffu && !(first & tc::kHostBit));
+          e = entry(s, t + 4 * kTile);
+        }
+        const int at = (8 * i + lane) & 31;
+        ref[0] = __shfl_sync(0xffffffffu, first, at);
+        bits = __shfl_sync(0xffffffffu, some, at);
       }
       const uint32_t whole = all & 0xffu;
       all >>= 8;
-      uint32_t mask[4] = {~0u, ~0u, ~0u, ~0u};
-      if (more && whole != 0xffu) {
+      uint32_t mask[4];
+      if (more && !chunked) {
+        int ent[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // all entries on their way at once
+          const int t = t0 + 32 * j + lane;
+          ent[j] = t >= s->lo && t < s->hi ? s->table[block_of(a, t)] : 0;
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int t = t0 + 32 * j + lane;
           const bool in = t >= s->lo && t < s->hi;
-          ref[j] = in ? row_ref(a, h, s->table[block_of(a, t)], t) : -1;
+          ref[j] = in ? row_ref(a, h, ent[j], t) : -1;
           if (in && ref[j] < 0) flag(a.status, SKV_DEV_BAD_SLOT);
           mask[j] = __ballot_sync(0xffffffffu, ref[j] >= 0);
         }
@@ -575,17 +598,36 @@ __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, u
         if (w == 0xffu) g.flush();  // nothing to put off: what is in flight comes first
         g.wait_free(&bar.empty[st], par);
         if (!g.ok) break;
-        if (u == 0 && lane == 0) {
-          masks[T % kMasks] = make_uint4(mask[0], mask[1], mask[2], mask[3]);
-          mbar_arrive(&bar.mask[T % kMasks]);
+        if (u == 0) {
+          if (chunked && lane < 8)
+            reinterpret_cast<uint16_t*>(masks + T % kMasks)[lane] = (uint16_t)bits;
+          else if (!chunked && lane == 0)
+            masks[T % kMasks] = make_uint4(mask[0], mask[1], mask[2], mask[3]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.mask[T % kMasks]);
         }
         if (w != 0xffu) {
           const unsigned char* gpu = (const unsigned char*)(u ? a.pool.gpu_v : a.pool.gpu_k);
           const unsigned char* host = (const unsigned char*)(u ? a.pool.host_v : a.pool.host_k);
-          unsigned char* to = gbase + (kQBufs + st) * kStageB + row_off;
+          unsigned char* to = gbase + (kQBufs + st) * kStageB;
 #pragma unroll 1
           for (int v = 0; v < kChunks; ++v, to += 2 * kGroupB) {
             if (w >> v & 1u) continue;
+            if (chunked) {
+              const long long r = __shfl_sync(0xffffffffu, old ? before[0] : ref[0], v);
+              const uint32_t on = __shfl_sync(0xffffffffu, old ? bits_before : bits, v);
+              const unsigned char* src =
+                  on ? ((r & tc::kHostBit) ? host : gpu) + (size_t)(r & tc::kRefRowMask) * tc::kRowBytes + lane * 16 : gpu;
+#pragma unroll
+              for (int k = 0; k < kChunk / 2; ++k) {
+                const int row = 2 * k + odd;
+                const bool live = on >> row & 1u;
+                tc::cp_async16_zfill(to + (piece >> 3) * kHalfB + (row >> 3) * kGroupB + (row & 7) * 128 +
+                                         (((piece ^ row) & 7) << 4),
+                                     live ? src + k * 2 * tc::kRowBytes : gpu, live);
+              }
+              continue;
+            }
             const long long mine = old ? (v < 4 ? (v < 2 ? before[0] : before[1]) : (v < 6 ? before[2] : before[3]))
                                        : (v < 4 ? (v < 2 ? ref[0] : ref[1]) : (v < 6 ? ref[2] : ref[3]));
             const long long r = __shfl_sync(0xffffffffu, mine, 16 * (v & 1) + r16);
@@ -593,9 +635,10 @@ __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, u
             const unsigned char* src = live ? ((r & tc::kHostBit) ? host : gpu) +
                                                   (size_t)(r & tc::kRefRowMask) * tc::kRowBytes + half * 128
                                             : gpu;
+            unsigned char* dst = to + (r16 >> 3) * kGroupB + half * kHalfB + (r16 & 7) * 128;
 #pragma unroll
             for (int c = 0; c < 8; ++c)
-              tc::cp_async16_zfill(to + ((c ^ (r16 & 7)) << 4), live ? src + c * 16 : src, live);
+              tc::cp_async16_zfill(dst + ((c ^ (r16 & 7)) << 4), live ? src + c * 16 : src, live);
           }
           g.commit(&bar.full[sq]);
         } else if (lane == 0) {
@@ -605,6 +648,7 @@ __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, u
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) before[j] = ref[j];
+      bits_before = bits;
       whole_before = whole;
       owed = !two;
     }
