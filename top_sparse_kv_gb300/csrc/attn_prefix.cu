@@ -616,8 +616,15 @@ __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, u
             if (chunked) {
               const long long r = __shfl_sync(0xffffffffu, old ? before[0] : ref[0], v);
               const uint32_t on = __shfl_sync(0xffffffffu, old ? bits_before : bits, v);
-              const unsigned char* src =
-                  on ? ((r & tc::kHostBit) ? host : gpu) + (size_t)(r & tc::kRefRowMask) * tc::kRowBytes + lane * 16 : gpu;
+              if (on == 0u) {  // nothing attended: V zeros (S of these keys is masked whatever K is)
+                if (u)
+#pragma unroll
+                  for (int k = 0; k < kChunk / 2; ++k)
+                    *reinterpret_cast<uint4*>(to + k * 512 + lane * 16) = make_uint4(0u, 0u, 0u, 0u);
+                continue;
+              }
+              const unsigned char* src = ((r & tc::kHostBit) ? host : gpu) +
+                                         (size_t)(r & tc::kRefRowMask) * tc::kRowBytes + lane * 16;
 #pragma unroll
               for (int k = 0; k < kChunk / 2; ++k) {
                 const int row = 2 * k + odd;
