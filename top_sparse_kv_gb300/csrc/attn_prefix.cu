@@ -356,9 +356,6 @@ struct Segs {
   const Seg* ring;
   volatile int* abort;
   int k;
-  __device__ __forceinline__ bool ready() const {
-    return __all_sync(0xffffffffu, mbar_try_wait(&bar.seg[k % kSegs], (uint32_t)(k / kSegs) & 1u));
-  }
   __device__ __forceinline__ const Seg* next() {
     const int i = k % kSegs;
     bool ok = wait_on(&bar.seg[i], (uint32_t)(k / kSegs) & 1u, abort, a.status);
@@ -373,42 +370,16 @@ struct Segs {
 };
 
 // ---------------------------------------------------------------------------- gather warps
-// The row warp's copies are announced on their stage's barrier by the warp once they have
-// landed: a load's fly while the next is issued, and a wait for a free stage announces what
-// is in flight first (what frees it may need those tiles).
-struct Rows {
-  const Args& a;
-  volatile int* abort;
-  uint64_t* flying;  // barrier of the unannounced copies (null: none)
-  bool ok;
-
-  __device__ __forceinline__ void announce(uint64_t* b) {
-    fence_proxy_async_smem();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(b);
-  }
-  __device__ __forceinline__ void commit(uint64_t* b) {
-    cp_async_commit();
-    if (flying) {
-      cp_async_wait<1>();
-      announce(flying);
-    }
-    flying = b;
-  }
-  __device__ __forceinline__ void flush() {
-    if (flying) {
-      cp_async_wait<0>();
-      announce(flying);
-    }
-    flying = nullptr;
-  }
-  __device__ __forceinline__ void wait_free(uint64_t* b, uint32_t parity) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return;
-    flush();
-    ok = wait_on(b, parity, abort, a.status);
-    ok = !__any_sync(0xffffffffu, !ok);
-  }
-};
+// Copies of single rows arrive on their barrier by themselves, a lane's when all it has
+// issued have landed.  They are the generic proxy's writes: who waits on the barrier orders
+// them before the MMA's reads by a proxy fence of its own.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+constexpr int kRowArrivals = 33;  // of the row warp on a stage: its lanes' copies, and what it stores
+__device__ __forceinline__ void arrive_many(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(kRowArrivals) : "memory");
+}
 
 __device__ __forceinline__ int block_of(const Args& a, int t) { return a.shift >= 0 ? t >> a.shift : t / a.bs; }
 __device__ __forceinline__ int in_block(const Args& a, int t) {
@@ -523,7 +494,7 @@ __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, u
                                           volatile int* abort) {
   const int lane = threadIdx.x & 31;
   pdl_wait();
-  Rows g{a, abort, nullptr, true};
+  bool ok = true;
   const bool chunked = a.bs % kChunk == 0;
   const int r16 = lane >> 1, half = lane & 1;    // other block sizes: a lane copies half a row
   const int odd = lane >> 4, piece = lane & 15;  // chunks: 16 lanes a row
@@ -541,8 +512,7 @@ __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, u
   auto entry = [&](const Seg* s, int t) {  // of the chunk at t (0: none of it is attended)
     return chunked && t < s->hi && t + kChunk > s->lo ? s->table[block_of(a, t)] : 0;
   };
-  while (g.ok && more) {
-    if (!segs.ready()) g.flush();  // a wait that does not announce
+  while (ok && more) {
     const Seg* s = segs.next();
     more = s != nullptr;
     if (!more && (!owed || *abort)) break;
@@ -553,7 +523,7 @@ __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, u
     long long first = -1;        // and the first row
     if (!more) advance();
 #pragma unroll 1
-    for (int i = 0; g.ok && i < n; ++i, ++T, t0 += kTile) {
+    for (int i = 0; ok && i < n; ++i, ++T, t0 += kTile) {
       if (more && chunked) {
         if ((i & 3) == 0) {
           const int t = t0 + kChunk * lane, lo = s->lo - t, hi = s->hi - t;
@@ -592,12 +562,12 @@ __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, u
       // this tile's K, a V that is owed, this tile's V with two row tiles
       const int loads = 1 + owed + two;
 #pragma unroll 1
-      for (int u = more ? 0 : 1; g.ok && u < loads; ++u) {
+      for (int u = more ? 0 : 1; ok && u < loads; ++u) {
         const bool old = u == 1 && owed;
         const uint32_t st = sq >= kRing ? sq - kRing : sq, w = old ? whole_before : whole;
-        if (w == 0xffu) g.flush();  // nothing to put off: what is in flight comes first
-        g.wait_free(&bar.empty[st], par);
-        if (!g.ok) break;
+        ok = wait_on(&bar.empty[st], par, abort, a.status);
+        ok = !__any_sync(0xffffffffu, !ok);
+        if (!ok) break;
         if (u == 0) {
           if (chunked && lane < 8)
             reinterpret_cast<uint16_t*>(masks + T % kMasks)[lane] = (uint16_t)bits;
@@ -647,9 +617,12 @@ __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, u
             for (int c = 0; c < 8; ++c)
               tc::cp_async16_zfill(dst + ((c ^ (r16 & 7)) << 4), live ? src + c * 16 : src, live);
           }
-          g.commit(&bar.full[sq]);
+          fence_proxy_async_smem();
+          cp_async_arrive(&bar.full[sq]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.full[sq]);
         } else if (lane == 0) {
-          mbar_arrive(&bar.full[sq]);
+          arrive_many(&bar.full[sq]);
         }
         advance();
       }
@@ -661,7 +634,8 @@ __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, u
     }
     if (more) segs.done();
   }
-  g.flush();
+  cp_async_commit();
+  cp_async_wait<0>();  // (copies that no MMA waited for, where the launch gave up)
 }
 
 // ---------------------------------------------------------------------------- segments and query rows
@@ -694,7 +668,11 @@ __device__ __forceinline__ void walk_role(const Args& a, Bars& bar, Seg* ring, u
     for (int u = 0; u < (s.n1 > 0 ? 2 : 1); ++u, ++nq) {
       const int buf = nq & 1;
       const bool ok = wait_on(&bar.qempty[buf], (uint32_t)((nq >> 1) & 1) ^ 1u, abort, a.status);
-      if (__any_sync(0xffffffffu, !ok)) return;
+      if (__any_sync(0xffffffffu, !ok)) {
+        cp_async_commit();
+        cp_async_wait<0>();
+        return;
+      }
       const int live = u ? s.n1 : s.n0;
 #pragma unroll 2
       for (int v = 0; v * kChunk < live; ++v) {
@@ -707,22 +685,14 @@ __device__ __forceinline__ void walk_role(const Args& a, Bars& bar, Seg* ring, u
           for (int c = 0; c < 8; ++c) cp_async16(dst + ((c ^ (r16 & 7)) << 4), src + c * 16);
         }
       }
-      cp_async_commit();
-      // the next segment goes out while the rows fly
-      if (u == (s.n1 > 0 ? 1 : 0)) {
-        walk.next(a, s2);
-        if (!publish(s2, ++k)) {
-          cp_async_wait<0>();
-          return;
-        }
-      }
-      cp_async_wait<0>();
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.qfull[buf]);
+      cp_async_arrive(&bar.qfull[buf]);
     }
+    walk.next(a, s2);
+    if (!publish(s2, ++k)) break;
     s = s2;
   }
+  cp_async_commit();
+  cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------------------- MMA warp
@@ -800,6 +770,7 @@ __device__ __forceinline__ void mma_role(const Args& a, const Segs& segs, Bars& 
     if (c & step::kFirst) wait(&bar.qfull[qb], (c >> step::kQPar) & 1u);
     if (!k_there) wait(&bar.full[ksq], (c >> step::kKPar) & 1u);
     if (!ok) return;
+    fence_proxy_async_smem();
     t5::fence_after();
     const uint64_t qd = dq + qb * (kStageB >> 4), kd = dk + ks * (kStageB >> 4);
     if (t5::elect_one()) {
@@ -826,6 +797,7 @@ __device__ __forceinline__ void mma_role(const Args& a, const Segs& segs, Bars& 
   auto issue_o = [&](uint32_t c, uint32_t p_par) {
     const uint32_t vsq = (c >> step::kV) & step::kSeq, vs = vsq >= kRing ? vsq - kRing : vsq;
     wait(&bar.full[vsq], (c >> step::kVPar) & 1u);
+    fence_proxy_async_smem();
     const uint64_t vd = dv + vs * (kStageB >> 4);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {  // 64 keys as soon as their P is there
@@ -1066,12 +1038,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
       mbar_init(&bar.seg_free[i], kSegReaders);
     }
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(&bar.full[i], 2);
-      mbar_init(&bar.full[kRing + i], 2);
+      mbar_init(&bar.full[i], 1 + kRowArrivals);
+      mbar_init(&bar.full[kRing + i], 1 + kRowArrivals);
       mbar_init(&bar.empty[i], 2);
     }
     for (int i = 0; i < kQBufs; ++i) {
-      mbar_init(&bar.qfull[i], 1);
+      mbar_init(&bar.qfull[i], 32);
       mbar_init(&bar.qempty[i], 2);
     }
     for (int i = 0; i < kMasks; ++i) mbar_init(&bar.mask[i], 1);
