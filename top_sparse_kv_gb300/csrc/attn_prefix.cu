@@ -674,7 +674,7 @@ __device__ __forceinline__ void walk_role(const Args& a, Bars& bar, Seg* ring, u
         return;
       }
       const int live = u ? s.n1 : s.n0;
-#pragma unroll 2
+#pragma unroll 1
       for (int v = 0; v * kChunk < live; ++v) {
         const int r = kChunk * v + r16;
         if (r < live) {
