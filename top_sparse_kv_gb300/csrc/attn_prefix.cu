@@ -881,15 +881,14 @@ __device__ __forceinline__ void softmax_role(const Args& a, Segs segs, Bars& bar
           t5::st_wait();
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-        for (int c = 0; c < 128; c += 64) {
-          uint32_t v[64];
-          t5::ld32_async(ts + c, v);
-          t5::ld32_async(ts + c + 32, v + 32);
-          t5::ld_wait32(v);
-          t5::ld_wait32(v + 32);
+        {
+          uint32_t v[128];
 #pragma unroll
-          for (int i = 0; i < 64; i += 8)
+          for (int c = 0; c < 128; c += 32) t5::ld32_async(ts + c, v + c);
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) t5::ld_wait32(v + c);
+#pragma unroll
+          for (int i = 0; i < 128; i += 8)
 #pragma unroll
             for (int u = 0; u < 4; ++u) mx[u] = max3(__float_as_uint(mx[u]), v[i + u], v[i + 4 + u]);
         }
