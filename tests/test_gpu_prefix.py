@@ -179,6 +179,23 @@ def test_matches_fp64(skv, case):
     assert torch.equal(o2, first[0])
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_any_shape(skv, seed):
+    """Batches of every kind: how the prefix's and the tails' tiles are cut over the CTAs, which
+    CTAs hold a unit's partials, single and paired row tiles, gangs."""
+    g = np.random.default_rng(1000 + seed)
+    H, G = int(g.choice([1, 2, 3, 4, 8])), int(g.choice([1, 2, 3, 5, 8, 16]))
+    B = int(np.exp(g.uniform(0, math.log(max(2, min(160, 2048 // G))))))
+    P = int(np.exp(g.uniform(0, math.log(12000)))) if seed % 6 else 0
+    longest = int(np.exp(g.uniform(0, math.log(1500))))
+    c = Case(skv, B, H, G, P, _tails(B, P, longest, 2000 + seed, empty=int(g.integers(0, B // 4 + 1))), seed=seed)
+    step = skv.PrefixStep(c.p, c.pool, c.prefix)
+    step.ws.fill_(255)  # NaN in every partial that is not written
+    out, lse = step.run(c.qd)
+    c.check(out, lse)
+    assert int(step.status.item()) == 0
+
+
 @pytest.mark.parametrize("shape", ["up", "down", "spikes"])
 def test_running_maximum(skv, shape):
     """Keys whose size grows, falls or jumps along the history: the maximum is renewed (or must
@@ -256,6 +273,39 @@ def test_offsets_past_32_bits(skv):
     assert (c.pool.gpu_k.numel() >> 31) >= 1
     step = skv.PrefixStep(c.p, c.pool, c.prefix)
     c.check(*step.run(c.qd))
+
+
+def test_millions_of_keys(skv):
+    """So many tail tiles that their cut is counted in 64 bits: one request's 5,000,000 positions all
+    name one block, so it attends that block's 16 keys 312,500 times; others have a few keys."""
+    H, n = 16, 5_000_000
+    c = Case(skv, 3, H, 1, 0, [200, 100, 0], seed=19, cap=208)
+    per = n // 16
+    table = torch.full((3, per), 2 ** 31 - 1, dtype=torch.int32)
+    table[:, :13] = c.pool.slot_table.cpu()
+    table[0] = table[0, 0]
+    k, v = c.keys[0][:16], c.vals[0][:16]
+    lens = torch.tensor([n, 100, 0], dtype=torch.int32).cuda()
+    p = skv.Problem(batch=3, n_kv_heads=H, n_q_heads=H, d_qk=D, d_v=D, max_len=n, topk=0, n_sink=0, n_local=0,
+                    block_size=16, seq_lens=lens)
+    step = skv.PrefixStep(p, skv.Pool(c.pool.gpu_k, c.pool.gpu_v, table.cuda()), skv.Prefix(None, 0))
+    step.ws.fill_(255)
+    out, lse = step.run(c.qd)
+    assert int(step.status.item()) == 0
+    q = c.q[0].double().view(H, 1, D)
+    kd, vd = k.double().transpose(0, 1), v.double().transpose(0, 1)
+    z = (q @ kd.transpose(1, 2) * D ** -0.5)[:, 0]
+    w = torch.softmax(z, -1)[:, None]
+    ref, A = (w @ vd)[:, 0], (w @ vd.abs())[:, 0]
+    dz = 130 * 2.0 ** -24 * D ** -0.5 * (q.abs() @ kd.abs().transpose(1, 2)).amax(-1)
+    # a CTA's slot adds up to 2,100 tiles one after the other, a tile's sums within 64 roundings
+    tol = 2.0 ** -8 * (A + ref.abs()) + A * (2 * dz + 2200 * 2.0 ** -24 + 2.0 ** -20)
+    assert bool(((out[0].cpu().double() - ref).abs() <= tol).all())
+    rl = torch.logsumexp(z, -1) + math.log(n // 16)
+    assert bool(((lse[0].cpu().double() - rl).abs() <= dz[:, 0] + 2200 * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -22 * rl).all())
+    c.keys[0] = None  # the others, as a short batch has them
+    out[0], lse[0] = 0, -math.inf
+    c.check(out, lse)
 
 
 def test_graphs_streams_and_workspaces(skv):

@@ -86,6 +86,7 @@ struct Plan {
   int rows, tiles, pairs, groups, gang, gangs;  // query rows, row tiles, pairs of them, groups of pairs, pairs a group
   int ntp;                                       // key tiles of the prefix
   int rp;                                        // rows of a prefix partial
+  int each;                                      // what a CTA's share of the prefix counts in tail tiles, at most 2^20
 };
 __host__ __device__ inline Plan plan_of(int B, int H, int G, int P) {
   Plan pl;
@@ -97,8 +98,16 @@ __host__ __device__ inline Plan plan_of(int B, int H, int G, int P) {
   pl.ntp = (P + kTile - 1) / kTile;
   pl.gangs = kCtas / pl.gang;
   const long long tp = (long long)H * pl.groups * pl.ntp;
-  if (tp < pl.gangs) pl.gangs = (int)tp;  // a gang has a tile at least: a unit's partials are consecutive
+  // A gang has a tile at least (a unit's partials are then those of consecutive gangs), and more
+  // than one before all CTAs are gangs: every gang of a unit leaves a partial a row, and CTAs
+  // without prefix have the more of the tails.  79 x 4 tiles, 203 rows: one tile at least 33.2 us,
+  // four 30.5, with tails of one key 22.0 and 20.7; 118 tiles: one 15.7 us, two 13.8, four 15.1;
+  // 56 tiles: one 11.2, two 11.7, four 13.2.
+  const int most = pl.gangs, least = 2 * tp <= most ? 1 : tp <= most ? 2 : 4;
+  if (tp < (long long)least * most) pl.gangs = (int)((tp + least - 1) / least);
   pl.rp = pl.rows < kTile ? pl.rows : kTile;
+  const long long each = pl.gangs ? (tp + pl.gangs - 1) / pl.gangs * (pl.tiles > 1 ? 2 : 1) : 0;
+  pl.each = (int)(each < 1 << 20 ? each : 1 << 20);
   return pl;
 }
 
@@ -165,23 +174,61 @@ struct Walk {
     const int lane = threadIdx.x & 31;
     const int per = (a.B + 31) / 32, b0 = lane * per < a.B ? lane * per : a.B, b1 = b0 + per < a.B ? b0 + per : a.B;
     long long mine = 0;
+    int tails = 0;
 #pragma unroll 4
-    for (int b = b0; b < b1; ++b) mine += tail_tiles(a, tail_end(a, b));
-    long long incl = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += o;
+    for (int b = b0; b < b1; ++b) {
+      const int n = tail_tiles(a, tail_end(a, b));
+      mine += n;
+      tails += n > 0;
     }
-    const long long total = __shfl_sync(0xffffffffu, incl, 31), ts = total * a.H;
-    const int sn = ts < kCtas ? (int)ts : kCtas;
-    if (scta >= sn) return;
-    const long long s0 = scta * ts / sn;
-    srem = (scta + 1) * ts / sn - s0;
-    const long long at = s0 % total;
-    long long lo = incl - mine;
+    long long at, lo;  // the first tile among one head's, the tiles before this lane's
+    if (__all_sync(0xffffffffu, mine * a.H < 1 << 19)) {
+      int incl = (int)mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
+      }
+      const int total = __shfl_sync(0xffffffffu, incl, 31), ts = total * a.H;  // below 2^24
+      // CTAs without tiles of the prefix, which stand first, take more: what makes all alike,
+      // with a tile of two row tiles counted as two and a tail's start as one.  They have a
+      // tile each before the others have any, so a unit's partials stay those of consecutive CTAs.
+      const int with = a.pl.gangs * a.pl.gang, without = kCtas - with;
+      const float starts = (float)(a.H * __reduce_add_sync(0xffffffffu, tails));
+      int share = (int)((float)ts * (1.f + (float)(with * a.pl.each) / ((float)ts + starts + 1.f)) *
+                        ((float)without / (float)kCtas));
+      share = share < without ? without : share;
+      share = share > ts || !with ? ts : share;
+      int place = scta, group = without, from = 0;
+      if (place >= without) {
+        from = share;
+        share = ts - share;
+        place -= without;
+        group = with;
+      }
+      const int sn = share < group ? share : group;
+      if (place >= sn) return;
+      const uint32_t s0 = from + (uint32_t)place * (uint32_t)share / (uint32_t)sn;
+      srem = from + (uint32_t)(place + 1) * (uint32_t)share / (uint32_t)sn - s0;
+      sh = s0 / (uint32_t)total;
+      at = s0 - (uint32_t)sh * total;
+      lo = incl - (int)mine;
+    } else {  // (so many tiles that the prefix's hardly count)
+      long long incl = mine;
+#pragma unroll 1
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
+      }
+      const long long total = __shfl_sync(0xffffffffu, incl, 31), ts = total * a.H;
+      const long long s0 = scta * ts / kCtas;
+      srem = (scta + 1) * ts / kCtas - s0;
+      sh = (int)(s0 / total);
+      at = s0 - sh * total;
+      lo = incl - mine;
+    }
     int fb = 0, ft = 0;
-    const bool here = at >= lo && at < incl;
+    const bool here = at >= lo && at < lo + mine;
     if (here)
       for (int b = b0; b < b1; ++b) {
         const int n = tail_tiles(a, tail_end(a, b));
@@ -193,7 +240,6 @@ struct Walk {
         lo += n;
       }
     const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
-    sh = (int)(s0 / total);
     sb = __shfl_sync(0xffffffffu, fb, src);
     stile = __shfl_sync(0xffffffffu, ft, src);
   }
