@@ -150,6 +150,9 @@ CASES = [
     (7, 3, 7, 1111, _tails(7, 1111, 64, 8), dict(bs=1)),
     (5, 2, 4, 97, _tails(5, 97, 50, 9), dict(bs=7)),
     (4, 2, 4, 200, _tails(4, 200, 300, 10), dict(bs=256)),
+    (20, 2, 8, 3000, _tails(20, 3000, 700, 21, 2), dict(bs=8)),
+    (40, 2, 8, 1500, _tails(40, 1500, 300, 22, 2), dict(bs=24, host=0.5)),
+    (40, 2, 8, 1500, _tails(40, 1500, 300, 23, 2), dict(bs=48, host=0.5)),
     (6, 2, 8, 500, _tails(6, 500, 200, 11), dict(host=0.4)),
     (6, 2, 8, 500, _tails(6, 500, 200, 12), dict(host=1.0)),
     (6, 2, 8, 512, _tails(6, 512, 200, 13), dict(own_prefix_rows=True)),

@@ -7,15 +7,14 @@
 // products on the tcgen05 tensor cores, and the prefix crosses HBM once; a tail [P, L_b)
 // meets the G rows of its own request the same way.  Both are cut into tiles of 128 keys.
 //
-// prefix_attn_kernel, one persistent CTA an SM, 13 warps:
+// prefix_attn_kernel, one persistent CTA an SM, 13 warps or 16:
 //   warps 0-3, 4-7   softmax of slot 0 / slot 1 (a thread a query row)
 //   warp 8           16 keys of a block of the GPU pool by one 4 KB TMA copy, into a ring of
 //                    32 KB K / V stages in the 128-byte-swizzled layout that the MMA reads
-//   warp 9           every other key -- at a history's edge, in the host pool (over UVA), of
+//   warp 9, 13-15    every other key -- at a history's edge, in the host pool (over UVA), of
 //                    blocks that 16 does not divide -- row by row, 16-byte cp.async with
-//                    zeros for what is not attended (all keys this way: batch 8 on 32K keys
-//                    79 us, by TMA 33; batch 64 on 128K 566, by TMA 223); and the key masks.
-//                    A warp of its own, so that waiting for its rows holds back no TMA copy.
+//                    zeros for what is not attended (batch 8 on 32K keys all this way 48 us, by
+//                    TMA 32); and the key masks
 //   warp 10          cuts the CTA's share into segments, published in a ring for the other
 //                    roles, and copies their query rows, by cp.async
 //   warps 11, 12     issue the MMAs of slot 0 / slot 1 (converged, one elected lane: the
@@ -40,16 +39,19 @@
 // prefix_merge_kernel joins a row's partials by log-sum-exp, in a fixed order.
 //
 // What bounds it (8 KV heads of 8 query heads, CUDA graphs of 30 calls).  Few rows, long
-// prefix -- batch 8 on 32K keys, 33.3 us: HBM while the prefix streams (134 MB, 20 us), then
+// prefix -- batch 8 on 32K keys, 32.4 us: HBM while the prefix streams (134 MB, 20 us), then
 // the tails, the start and the merge, a few us each.  Many rows -- batch 64 on 128K keys, 275
-// GFLOP in 223 us, 1.23 PFLOP/s: the chain of a slot's step, 3,230 cycles.  The softmax takes
+// GFLOP in 215 us, 1.28 PFLOP/s: the chain of a slot's step, 3,200 cycles.  The softmax takes
 // 1,900 of them (the maximum 600, then 20 cycles a pair of keys, where a warp alone needs 12.5
 // for the exponentials, sums and roundings without TMEM's latencies); the second half of P V
 // and the next S 980 (S reads 8 KB of shared memory an MMA, 128 bytes a cycle of its 64: it
 // runs a little below the pipe's rate); the hand-overs 330.  Both slots' MMAs together are
-// 2,400, in turns.  Instruction fetch was the bound before that: the roles run different code
-// on the same SM, so loops are rolled, waits out of line, call sites single (unrolled over 64
-// keys the exponentials took 241 us in place of 226).
+// 2,400, in turns; the tails of that case, 131 MB, take 22 us of it, near HBM's rate.  Small
+// calls -- 4 requests on 777 keys, 10.9 us -- are a chain of first times: a role's first pass
+// runs at some 25 cycles an instruction, so what lies on the way to the first S is short code.
+// Instruction fetch was the bound of long calls, too: the roles run different code on the same
+// SM, so loops are rolled, waits out of line, call sites single (unrolled over 64 keys the
+// exponentials took 241 us in place of 226).
 // Slower in the same measure: S of 64 keys at a time, twice buffered (233; an S as two N = 64
 // MMAs costs more than one of N = 128, 234 by itself); sixteen softmax warps (244 against
 // 226); P V begun after 96 of 128 keys (226) or in three parts (229); the first tile's maximum
@@ -65,7 +67,7 @@ namespace {
 
 namespace px {
 constexpr int kCtas = 152;             // one CTA an SM of a GB300 (a function of the problem alone: sizes the workspace)
-constexpr int kThreads = 416;
+constexpr int kRowWarps = 4;           // in place of one where rows come in bulk
 constexpr int kTile = 128;             // keys a tile, query rows a tile
 constexpr int kStageB = kTile * 256;   // a K, V or Q tile, 32 KB: [group of 8 rows][half of the dims][8 rows][128 bytes]
 constexpr int kGroupB = 2048;          // a group of 8 rows
@@ -76,7 +78,7 @@ constexpr int kRing = 5;               // K / V stages
 constexpr int kQBufs = 2;
 constexpr int kMasks = 8;              // key masks of the last tiles
 constexpr int kSegs = 4;               // segments published ahead
-constexpr int kSegReaders = 12;        // warps that read them: 8 softmax, TMA, rows, 2 MMA
+constexpr int kSegReaders = 11;        // warps that read them: 8 softmax, TMA, 2 MMA; and the row warps
 constexpr int kMaxGang = 4;            // pairs of row tiles that read the same keys together
 constexpr float kGrow = 8.f;           // log2 growth of a row's maximum that renews it
 constexpr uint32_t kTmemCols = 512;    // S0 S1 O0 O1, 128 columns each; P over the first 64 columns of S
@@ -422,7 +424,7 @@ struct Segs {
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-constexpr int kRowArrivals = 33;  // of the row warp on a stage: its lanes' copies, and what it stores
+constexpr int kRowArrivals = 33;  // of a row warp on a stage: its lanes' copies, and what it stores
 __device__ __forceinline__ void arrive_many(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(kRowArrivals) : "memory");
 }
@@ -535,9 +537,12 @@ __device__ __forceinline__ void tma_role(const Args& a, const CUtensorMap* tk, c
 
 // Blocks of whole chunks of 16: a chunk's rows lie one behind another, 4 KB, so one table
 // entry places them and a copy instruction takes two rows (four lines; half a row a lane
-// would touch 32).  Other block sizes: an entry a row.
+// would touch 32: batch 29's tails, with an entry a row, 38.2 us in place of 34.9).  Other
+// block sizes: an entry a row.
+// RW row warps, each takes every RW-th chunk of a load.
+template <int RW>
 __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, unsigned char* gbase, uint4* masks,
-                                          volatile int* abort) {
+                                          int part, volatile int* abort) {
   const int lane = threadIdx.x & 31;
   pdl_wait();
   bool ok = true;
@@ -576,7 +581,7 @@ __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, u
           some = hi <= 0 || lo >= kChunk ? 0u : (hi >= kChunk ? 0xffffu : (1u << hi) - 1) & (lo > 0 ? ~0u << lo : ~0u);
           first = some ? row_ref(a, h, e, t) : -1;
           if (some && first < 0) {
-            flag(a.status, SKV_DEV_BAD_SLOT);
+            if (part == 0) flag(a.status, SKV_DEV_BAD_SLOT);
             some = 0;
           }
           all = __ballot_sync(0xffffffffu, a.tma && some == 0xffffu && !(first & tc::kHostBit));
@@ -601,7 +606,7 @@ __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, u
           const int t = t0 + 32 * j + lane;
           const bool in = t >= s->lo && t < s->hi;
           ref[j] = in ? row_ref(a, h, ent[j], t) : -1;
-          if (in && ref[j] < 0) flag(a.status, SKV_DEV_BAD_SLOT);
+          if (in && ref[j] < 0 && part == 0) flag(a.status, SKV_DEV_BAD_SLOT);
           mask[j] = __ballot_sync(0xffffffffu, ref[j] >= 0);
         }
       }
@@ -614,7 +619,7 @@ __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, u
         ok = wait_on(&bar.empty[st], par, abort, a.status);
         ok = !__any_sync(0xffffffffu, !ok);
         if (!ok) break;
-        if (u == 0) {
+        if (u == 0 && part == 0) {
           if (chunked && lane < 8)
             reinterpret_cast<uint16_t*>(masks + T % kMasks)[lane] = (uint16_t)bits;
           else if (!chunked && lane == 0)
@@ -628,7 +633,7 @@ __device__ __forceinline__ void rows_role(const Args& a, Segs segs, Bars& bar, u
           unsigned char* to = gbase + (kQBufs + st) * kStageB;
 #pragma unroll 1
           for (int v = 0; v < kChunks; ++v, to += 2 * kGroupB) {
-            if (w >> v & 1u) continue;
+            if ((w >> v & 1u) || (v & (RW - 1)) != part) continue;
             if (chunked) {
               const long long r = __shfl_sync(0xffffffffu, old ? before[0] : ref[0], v);
               const uint32_t on = __shfl_sync(0xffffffffu, old ? bits_before : bits, v);
@@ -1065,7 +1070,8 @@ __device__ __forceinline__ void softmax_role(const Args& a, Segs segs, Bars& bar
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_constant__ CUtensorMap tk,
+template <int RW>
+__global__ void __launch_bounds__(384 + 32 * RW, 1) prefix_attn_kernel(const __grid_constant__ CUtensorMap tk,
                                                                   const __grid_constant__ CUtensorMap tv,
                                                                   const Args a) {
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -1080,11 +1086,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
   if (t == 0) {
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&bar.seg[i], 1);
-      mbar_init(&bar.seg_free[i], kSegReaders);
+      mbar_init(&bar.seg_free[i], kSegReaders + RW);
     }
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(&bar.full[i], 1 + kRowArrivals);
-      mbar_init(&bar.full[kRing + i], 1 + kRowArrivals);
+      mbar_init(&bar.full[i], 1 + RW * kRowArrivals);
+      mbar_init(&bar.full[kRing + i], 1 + RW * kRowArrivals);
       mbar_init(&bar.empty[i], 2);
     }
     for (int i = 0; i < kQBufs; ++i) {
@@ -1121,11 +1127,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
   } else {
     if (warp == 8)
       tma_role(a, &tk, &tv, segs, bar, base, &sh.abort);
-    else if (warp == 9)
-      rows_role(a, segs, bar, smem, sh.masks, &sh.abort);
+    else if (warp == 9 || warp >= 13)
+      rows_role<RW>(a, segs, bar, smem, sh.masks, RW == 1 || warp == 9 ? 0 : warp - 12, &sh.abort);
     else if (warp == 10)
       walk_role(a, bar, sh.ring, smem, &sh.abort);
-    else if (warp < 13)
+    else
       mma_role(a, segs, bar, base, tm, warp - 11, &sh.abort);
   }
   t5::fence_before();
@@ -1142,7 +1148,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
 // kMergeBatch partials' loads in flight at a time (bound by their latency: one round for
 // most shapes); the shares are joined through shared memory.  The order is fixed.  Four
 // shares where the rows are few, two where the CTAs fill the device without (batch 8 on 32K
-// keys in all 33.5 us with four, 34.3 with two; batch 64 on 128K 234 and 225).
+// keys in all 32.6 us with four, 33.8 with two; batch 64 on 128K 224 and 215).
 constexpr int kMergeDims = 8;
 constexpr int kMergeBatch = 5;
 
@@ -1336,8 +1342,6 @@ skv_status launch_prefix_attn(const skv_problem& p, const void* q, const PoolVie
   a.out = out;
   a.lse = lse;
   a.status = status;
-  const skv_status prep = prepare_kernel((const void*)prefix_attn_kernel, px::kSmem);
-  if (prep != SKV_OK) return prep;
   CUtensorMap tk, tv;
   const long long rows = pool.n_gpu * p.n_kv_heads * p.block_size;
   a.shift = -1;
@@ -1345,7 +1349,15 @@ skv_status launch_prefix_attn(const skv_problem& p, const void* q, const PoolVie
     if (p.block_size == 1 << i) a.shift = i;
   a.tma = p.block_size % kChunk == 0 && rows > 0 && rows / 8 < (1LL << 31);
   if (a.tma && (!encode_pool(&tk, pool.gpu_k, rows) || !encode_pool(&tv, pool.gpu_v, rows))) return SKV_ERR_CUDA;
-  if (launch_dependent(prefix_attn_kernel, dim3(kCtas), dim3(px::kThreads), px::kSmem, st, 1, tk, tv, a) != cudaSuccess)
+  // Four row warps where whole histories are theirs -- blocks that 16 does not divide, a host
+  // pool -- and one where they have the histories' ends alone: batch 8 on 32K keys, every key by
+  // rows, 47.8 us with four and 77.7 with one; batch 64 on 128K by TMA 219 with four, 215 with one.
+  const bool bulk = p.block_size % kChunk != 0 || pool.host_k != nullptr;
+  const auto kernel = bulk ? prefix_attn_kernel<kRowWarps> : prefix_attn_kernel<1>;
+  const skv_status prep = prepare_kernel((const void*)kernel, px::kSmem);
+  if (prep != SKV_OK) return prep;
+  if (launch_dependent(kernel, dim3(kCtas), dim3(384 + 32 * (bulk ? kRowWarps : 1)), px::kSmem, st, 1, tk, tv, a) !=
+      cudaSuccess)
     return SKV_ERR_CUDA;
   SKV_LAUNCH_CHECK();
   const long long blocks = (long long)((a.pl.rows + 31) / 32) * a.H;
