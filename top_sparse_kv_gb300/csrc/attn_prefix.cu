@@ -31,8 +31,8 @@
 //
 // Work is cut by key tiles: the CTAs form gangs (one member per pair of row tiles, so
 // that members read the same keys at the same time) and gang c takes the tiles
-// [c T / C, (c + 1) T / C) of all heads' prefixes; then CTA c takes its share of all
-// tails' tiles.  Each cut leaves every CTA that takes part a tile at least, so the segments
+// [c T / C, (c + 1) T / C) of all heads' prefixes; then come the tails' tiles, to the CTAs
+// without prefix first, so that all have alike.  Each cut leaves every CTA that takes part a tile at least, so the segments
 // of a unit -- runs of tiles of one head's prefix, or of one tail -- are those of
 // consecutive CTAs.  A segment's O, m and l go to the workspace, at an index that grows
 // with both the CTA and the unit, so no two segments share one and no atomics are needed.
