@@ -196,11 +196,13 @@ struct Walk {
       // with a tile of two row tiles counted as two and a tail's start as one.  They have a
       // tile each before the others have any, so a unit's partials stay those of consecutive CTAs.
       const int with = a.pl.gangs * a.pl.gang, without = kCtas - with;
-      const float starts = (float)(a.H * __reduce_add_sync(0xffffffffu, tails));
-      int share = (int)((float)ts * (1.f + (float)(with * a.pl.each) / ((float)ts + starts + 1.f)) *
-                        ((float)without / (float)kCtas));
-      share = share < without ? without : share;
-      share = share > ts || !with ? ts : share;
+      int share = ts;
+      if (with && ts > without) {
+        const float starts = (float)(a.H * __reduce_add_sync(0xffffffffu, tails));
+        share = (int)((float)ts * (1.f + (float)(with * a.pl.each) / ((float)ts + starts + 1.f)) *
+                      ((float)without / (float)kCtas));
+        share = share < without ? without : share > ts ? ts : share;
+      }
       int place = scta, group = without, from = 0;
       if (place >= without) {
         from = share;
