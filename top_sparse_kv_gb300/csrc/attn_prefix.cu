@@ -157,13 +157,22 @@ struct Walk {
   long long srem;            // tail tiles left
   int scta;                  // the CTA's place among those with tail tiles
   int sh, sb, stile;         // the next tail tile
+  int gang, member;          // the CTA's gang, its place in it
   bool scanned;
   __device__ __forceinline__ void init(const Args& a) {
     const Plan& pl = a.pl;
-    const int gang = blockIdx.x / pl.gang;
-    const long long tp = (long long)a.H * pl.groups * pl.ntp;
-    p0 = gang < pl.gangs ? gang * tp / pl.gangs : 0;
-    p1 = gang < pl.gangs ? (gang + 1) * tp / pl.gangs : 0;
+    gang = blockIdx.x;
+    member = 0;
+    if (pl.gang > 1) {
+      gang = blockIdx.x / pl.gang;
+      member = blockIdx.x - gang * pl.gang;
+    }
+    p0 = p1 = 0;
+    if (gang < pl.gangs) {
+      const long long tp = (long long)a.H * pl.groups * pl.ntp;
+      p0 = gang * tp / pl.gangs;
+      p1 = (gang + 1) * tp / pl.gangs;
+    }
     srem = 0;
     scta = kCtas - 1 - (int)blockIdx.x;  // the last CTAs take the tails (the first the prefix, where there are few tiles)
     sh = sb = stile = 0;
@@ -250,7 +259,6 @@ struct Walk {
   // the next segment of the prefix, which is cut without a look at memory
   __device__ __forceinline__ bool next_prefix(const Args& a, Seg& s) {
     const Plan& pl = a.pl;
-    const int c = blockIdx.x / pl.gang, member = blockIdx.x - c * pl.gang;
     while (p0 < p1) {
       const int up = (int)(p0 / pl.ntp), tile = (int)(p0 - (long long)up * pl.ntp);
       const long long left = p1 - p0;
@@ -260,7 +268,7 @@ struct Walk {
       if (pair >= pl.pairs) continue;  // the last group may be short of pairs
       const int r = pl.rows - pair * 2 * kTile;
       s.table = a.ptable;
-      s.part = (long long)(c + up) * pl.gang + member;
+      s.part = (long long)(gang + up) * pl.gang + member;
       s.n = n;
       s.t0 = tile * kTile;
       s.lo = 0;
