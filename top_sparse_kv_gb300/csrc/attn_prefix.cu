@@ -47,7 +47,7 @@
 // and the next S 980 (S reads 8 KB of shared memory an MMA, 128 bytes a cycle of its 64: it
 // runs a little below the pipe's rate); the hand-overs 330.  Both slots' MMAs together are
 // 2,400, in turns; the tails of that case, 131 MB, take 22 us of it, near HBM's rate.  Small
-// calls -- 4 requests on 777 keys, 10.9 us -- are a chain of first times: a role's first pass
+// calls -- 4 requests on 777 keys, 10.6 us -- are a chain of first times: a role's first pass
 // runs at some 25 cycles an instruction, so what lies on the way to the first S is short code.
 // Instruction fetch was the bound of long calls, too: the roles run different code on the same
 // SM, so loops are rolled, waits out of line, call sites single (unrolled over 64 keys the
