@@ -396,8 +396,9 @@ __global__ void __launch_bounds__(32 * kRowWarps<LPR> + 32, kTokCtas<LPR>) token
 
 // Longer rows: a warp a row, NV vectors a lane -- vector i of lane l is vector l + 32 i, the
 // next row's loads in flight while this one is turned.  Vectors that neither norm nor
-// rotation touch go as they are.  Bound by HBM latency: 2,048 tokens of 129 latent rows of 576
-// bf16, 608 MB, in 100.8 us, 6.0 TB/s, 0.89 of the copy rate.
+// rotation touch go as they are.  2,048 tokens of 129 latent rows of 576 bf16, 608 MB, take
+// 100.4 us, 6.0 TB/s, 0.89 of the copy rate; the warps' own chain of latencies is as long (in
+// place, with only the 64 turned entries of a row moved, the same rows took 97).
 template <typename T, int NV>
 __global__ void __launch_bounds__(32 * kLongWarps) token_long_rows_kernel(const TokenArgs a) {
   constexpr int VE = Vec<T>::N;
