@@ -329,7 +329,8 @@ skv_status skv_sparse_attn(const skv_problem* p, const void* q, const skv_kv_poo
   const size_t need = attn_workspace_bytes(r);
   if (ws_bytes < need) return SKV_ERR_WORKSPACE_TOO_SMALL;
   if (!ws || !aligned16(ws)) return SKV_ERR_INVALID_ARGUMENT;
-  return launch_attn(r, q, head_view(*p, pool), idx, out, lse, ws, dev_status, (cudaStream_t)stream);
+  return launch_attn(r, q, head_view(*p, pool), idx, out, lse, ws, dev_status, (cudaStream_t)stream, false, nullptr,
+                     nullptr, true);
 }
 
 static skv_status check_step(const skv_problem* p, const void* q, const void* q_score, const skv_index_src* index,

@@ -274,7 +274,11 @@ __global__ void __launch_bounds__(kThreads, tc::Ring<STAGES>::kCtasPerSm) attn_m
   constexpr int kStages = tc::Ring<STAGES>::kStages;
   constexpr int kMaxChunk = tc::Ring<STAGES>::kMaxChunk;
   // Before the selection is visible, only what no kernel of the step writes is read: the
-  // lengths and the query (the CTA may already be resident while the selection runs).
+  // lengths and the query (the CTA may already be resident while the selection runs; the
+  // step's first kernel, an ordinary launch, has seen the end of all that came before).
+  // Where the attention is a call's first kernel, what runs before it is not the step's own
+  // -- a norm or an append may still be writing the query -- and nothing is read early.
+  if (a.first) pdl_wait();
   using namespace tc;
   extern __shared__ __align__(128) unsigned char smem[];
   unsigned char* stages = smem;
@@ -873,7 +877,7 @@ uint32_t* attn_tickets(const skv_problem& p, void* ws) {
 
 skv_status launch_attn(const skv_problem& p, const void* q, const PoolView& pool, const int32_t* idx, void* out,
                        float* lse, void* ws, int32_t* status, cudaStream_t st, bool tickets_zeroed,
-                       const PrefetchView* pf, const BlockListView* bl) {
+                       const PrefetchView* pf, const BlockListView* bl, bool first) {
   if (pool.gpu_v == nullptr) return launch_attn_latent(p, q, pool, idx, out, lse, ws, status, st, pf);
   AttnArgs a = make_args(p, q, pool, idx, status);
   if (pf != nullptr) {  // staged host rows (bf16 tensor-core path only): K rows, then V rows, [rows, cap] each
@@ -886,6 +890,7 @@ skv_status launch_attn(const skv_problem& p, const void* q, const PoolView& pool
       return SKV_ERR_UNSUPPORTED;
     a.bl = *bl;
   }
+  a.first = first ? 1 : 0;
   a.n_splits = attn_splits(p);
   const int n = max_list(p);
   a.chunk = n > 0 ? (n + a.n_splits - 1) / a.n_splits : 1;

@@ -32,6 +32,7 @@ struct AttnArgs {
   PrefetchView pf;   // threshold prefetch (bf16 paged path): staged host rows (pf.map == nullptr: none)
   size_t pf_v_off;   // byte offset of the staged V rows inside pf.staging
   BlockListView bl;  // block-list mode (bf16 kernel) when bl.att != nullptr
+  int first;         // the attention is its call's first kernel: what came before may still write the queries
 };
 
 constexpr int kMergeMax = 1024;  // split partials of one head merged through shared memory (max n_splits)
@@ -260,6 +261,7 @@ inline AttnArgs make_args(const skv_problem& p, const void* q, const PoolView& p
   a.pf = PrefetchView{};
   a.pf_v_off = 0;
   a.bl = BlockListView{};
+  a.first = 1;  // (launch_attn: 0 behind the step's other kernels)
   a.dv = p.d_v;
   a.out_f32 = p.dtype == SKV_DTYPE_F32;
   a.n_splits = 1;

@@ -280,6 +280,11 @@ __device__ __forceinline__ void cp_async_wait() {
 // kernel has completed and its writes are visible, so only the launch and the CTA
 // placement overlap.  pdl_release() lets the next kernel be scheduled early.
 // Both are no-ops for an ordinary launch.
+// Two read before they wait: attn_mma_kernel lengths and queries, the ParisKV kernels
+// lengths.  That is sound behind an ordinary launch of the same call (a step's scoring) and
+// nowhere else -- the kernels of another call may be those tensors' writers.  Behind a
+// kernel that releases early every CTA waits, so a kernel's end implies the end of all
+// before it.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -467,10 +472,12 @@ int attn_splits(const skv_problem& p);
 struct PrefetchView;
 // bl: optional, bf16 only; the list comes from the chosen blocks (idx is then the list
 // the kernel writes, bl->att).
+// first: no kernel of the same call runs before (skv_sparse_attn), so nothing at all is read
+// before the kernels ahead on the stream have completed.
 skv_status launch_attn(const skv_problem& p, const void* q, const PoolView& pool, const int32_t* idx,
                        void* out, float* lse, void* ws, int32_t* status, cudaStream_t st,
                        bool tickets_zeroed = false, const PrefetchView* pf = nullptr,
-                       const BlockListView* bl = nullptr);
+                       const BlockListView* bl = nullptr, bool first = false);
 // the per-unit merge tickets inside the attention workspace (nullptr if the path has none)
 uint32_t* attn_tickets(const skv_problem& p, void* ws);
 
