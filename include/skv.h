@@ -444,7 +444,8 @@ skv_status skv_decode_step_prefetch(const skv_problem *p, const void *q, const v
  * cache.stats  device uint64 [3] or NULL: every call adds its attended tokens found in
  *              GPU slots, those read from the host, and its promotions.
  * The call updates pool->slot_table and the rows of pool->gpu_k in place (both must be
- * writable and used by no other work meanwhile).  Requirements: the latent layout
+ * writable and used by no other work meanwhile).  Slots are copies and are never written
+ * back: new tokens are appended by skv_append_kv_cached.  Requirements: the latent layout
  * (pool->gpu_v == NULL, block_size 1), batch <= 64, n_host_blocks >= batch * max_len;
  * else SKV_ERR_UNSUPPORTED.
  *
@@ -665,9 +666,23 @@ skv_status skv_qk_norm_rope(const skv_problem *p, const skv_rotary *rotary, cons
  * length.  The pools are written (they must be writable, and read by no other work
  * meanwhile); two tokens of one call must not name the same pool row.  requests NULL
  * needs n_tokens <= batch.  n_tokens 0 enqueues nothing.
+ * A row goes where the table names it and nowhere else: of a pool whose GPU slots a cache
+ * manages (skv_decode_step_cached, skv_cache_update), a row written to a slot alone is lost
+ * when the cache gives the slot to another -- such a pool takes skv_append_kv_cached.
  */
 skv_status skv_append_kv(const skv_problem *p, const skv_rotary *rotary, const skv_tokens *tokens,
                          const skv_kv_pool *pool, void *q_out, int32_t *dev_status, void *stream);
+
+/*
+ * skv_append_kv for a pool whose GPU slots a cache manages (skv_slot_cache): K and V rows
+ * whose table entry names a slot go to the host row that backs them too, so the host pool
+ * keeps every token and an evicted slot loses nothing, positions written again included.
+ * Both forms of the cache, with its requirements on p and pool (batch, max_len and the
+ * pool are those of the cached step); the host pools must be writable.  Same arguments
+ * and results as skv_append_kv otherwise.
+ */
+skv_status skv_append_kv_cached(const skv_problem *p, const skv_rotary *rotary, const skv_tokens *tokens,
+                                const skv_kv_pool *pool, void *q_out, int32_t *dev_status, void *stream);
 
 /* ------------------------------------------------------------------------------------
  * Attention of a batch that shares a prefix: every request attends its whole history,

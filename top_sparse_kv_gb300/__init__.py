@@ -31,6 +31,7 @@ from .binding import (  # noqa: F401
     SkvError,
     lib,
     skv_append_kv,
+    skv_append_kv_cached,
     skv_block_decode_step,
     skv_block_select,
     skv_block_summaries,

@@ -123,6 +123,8 @@ def _load():
                                   ctypes.POINTER(CParisIndex), ctypes.POINTER(CPool), VP, VP, VP, VP, SZ, VP, VP],
         "skv_qk_norm_rope": [P, ctypes.POINTER(CRotary), ctypes.POINTER(CTokens), VP, VP, VP, VP],
         "skv_append_kv": [P, ctypes.POINTER(CRotary), ctypes.POINTER(CTokens), ctypes.POINTER(CPool), VP, VP, VP],
+        "skv_append_kv_cached": [P, ctypes.POINTER(CRotary), ctypes.POINTER(CTokens), ctypes.POINTER(CPool), VP, VP,
+                                 VP],
         "skv_prefix_workspace_size": [P, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)],
         "skv_prefix_attn": [P, VP, ctypes.POINTER(CPool), ctypes.POINTER(CPrefix), VP, VP, VP, SZ, VP, VP],
         "skv_block_workspace_size": [P, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t),
@@ -251,7 +253,8 @@ class Problem:
 @dataclass
 class Pool:
     """Python mirror of skv_kv_pool; tensors are [n_blocks, H, block_size, d].  With
-    table_heads = 1 the table is [batch, H, stride] and the GPU pools [n_blocks, block_size, d]."""
+    table_heads = 1 the table is [batch, H, stride] and the GPU pools [n_blocks, block_size, d].
+    cached: a slot cache manages the GPU blocks (set when one is made for the pool)."""
 
     gpu_k: torch.Tensor
     gpu_v: Optional[torch.Tensor]
@@ -259,6 +262,7 @@ class Pool:
     host_k: Optional[torch.Tensor] = None
     host_v: Optional[torch.Tensor] = None
     table_heads: int = 0
+    cached: bool = False
 
     def c(self) -> CPool:
         return CPool(self.gpu_k.data_ptr(), None if self.gpu_v is None else self.gpu_v.data_ptr(),
@@ -423,6 +427,7 @@ class SlotCache:
             owner[t[m]] = (b[m] * p.max_len + pos[m])
         nb = ctypes.c_size_t(0)
         cp, cpool = p.c(), pool.c()
+        pool.cached = True
         _check("skv_cache_prepare", lib().skv_cache_prepare())
         _check("skv_cache_workspace_size", lib().skv_cache_workspace_size(ctypes.byref(cp), ctypes.byref(cpool),
                                                                           int(budget), ctypes.byref(nb)))
@@ -630,16 +635,26 @@ def skv_qk_norm_rope(p: Problem, rotary: Rotary, q, k, q_out, k_out, positions=N
                                                       _ptr(dev_status), raw_stream(p.seq_lens.get_device(), stream)))
 
 
-def skv_append_kv(p: Problem, rotary: Rotary, q, k, v, pool: Pool, q_out, positions=None, requests=None,
-                  dev_status=None, stream=None):
+def _append(fn: str, p: Problem, rotary: Rotary, q, k, v, pool: Pool, q_out, positions, requests, dev_status, stream):
     rotary.check(p)
     check_pool(p, pool)
     same_device(p, dev_status=dev_status)
     cp, cr, ct, cpool = p.c(), rotary.c(), c_tokens(p, q, k, v, positions, requests), pool.c()
     qo = _out_rows("q_out", q_out, q, p.n_q_heads, p.d_qk, element_type(p))
-    _check("skv_append_kv", lib().skv_append_kv(ctypes.byref(cp), ctypes.byref(cr), ctypes.byref(ct),
-                                                ctypes.byref(cpool), qo, _ptr(dev_status),
-                                                raw_stream(p.seq_lens.get_device(), stream)))
+    _check(fn, getattr(lib(), fn)(ctypes.byref(cp), ctypes.byref(cr), ctypes.byref(ct), ctypes.byref(cpool), qo,
+                                  _ptr(dev_status), raw_stream(p.seq_lens.get_device(), stream)))
+
+
+def skv_append_kv(p: Problem, rotary: Rotary, q, k, v, pool: Pool, q_out, positions=None, requests=None,
+                  dev_status=None, stream=None):
+    if pool.cached:
+        raise ValueError("a slot cache manages this pool: skv_append_kv_cached")
+    _append("skv_append_kv", p, rotary, q, k, v, pool, q_out, positions, requests, dev_status, stream)
+
+
+def skv_append_kv_cached(p: Problem, rotary: Rotary, q, k, v, pool: Pool, q_out, positions=None, requests=None,
+                         dev_status=None, stream=None):
+    _append("skv_append_kv_cached", p, rotary, q, k, v, pool, q_out, positions, requests, dev_status, stream)
 
 
 @dataclass

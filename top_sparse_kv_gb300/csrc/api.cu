@@ -747,8 +747,8 @@ skv_status skv_qk_norm_rope(const skv_problem* p, const skv_rotary* rotary, cons
   return launch_token_rows(*p, *rotary, *tokens, PoolView{}, q_out, k_out, dev_status, (cudaStream_t)stream);
 }
 
-skv_status skv_append_kv(const skv_problem* p, const skv_rotary* rotary, const skv_tokens* tokens,
-                         const skv_kv_pool* pool, void* q_out, int32_t* dev_status, void* stream) {
+static skv_status append(const skv_problem* p, const skv_rotary* rotary, const skv_tokens* tokens,
+                         const skv_kv_pool* pool, void* q_out, int32_t* dev_status, void* stream, bool cached) {
   SKV_TRY(check_tokens(p, rotary, tokens, q_out));
   SKV_TRY(check_pool(*p, pool));
   if (!aligned4(pool->slot_table) || !aligned4(dev_status)) return SKV_ERR_INVALID_ARGUMENT;
@@ -763,7 +763,20 @@ skv_status skv_append_kv(const skv_problem* p, const skv_rotary* rotary, const s
     return SKV_ERR_INVALID_ARGUMENT;  // the latent layout: one row a token
   }
   if (!tokens->requests && tokens->n_tokens > p->batch) return SKV_ERR_INVALID_ARGUMENT;
-  return launch_token_rows(*p, *rotary, *tokens, view(pool), q_out, nullptr, dev_status, (cudaStream_t)stream);
+  return launch_token_rows(*p, *rotary, *tokens, view(pool), q_out, nullptr, dev_status, (cudaStream_t)stream,
+                           cached);
+}
+
+skv_status skv_append_kv(const skv_problem* p, const skv_rotary* rotary, const skv_tokens* tokens,
+                         const skv_kv_pool* pool, void* q_out, int32_t* dev_status, void* stream) {
+  return append(p, rotary, tokens, pool, q_out, dev_status, stream, false);
+}
+
+skv_status skv_append_kv_cached(const skv_problem* p, const skv_rotary* rotary, const skv_tokens* tokens,
+                                const skv_kv_pool* pool, void* q_out, int32_t* dev_status, void* stream) {
+  SKV_TRY(check_cache_problem(p, pool, 0));
+  if (!pool->host_k || (pool->gpu_v && !pool->host_v)) return SKV_ERR_INVALID_ARGUMENT;
+  return append(p, rotary, tokens, pool, q_out, dev_status, stream, true);
 }
 
 // ---------------------------------------------------------------- shared prefix

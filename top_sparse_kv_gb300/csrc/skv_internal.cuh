@@ -521,9 +521,10 @@ skv_status launch_cache_update(const skv_problem& p, const PoolView& pool, const
                                cudaStream_t st);
 
 // new tokens: norm, rotation and the append to the pool (tokens.cu).  pool.table == nullptr:
-// no append, the keys go to k_out.
+// no append, the keys go to k_out.  cached: rows that go to GPU slots also go to the host rows
+// that back them.
 skv_status launch_token_rows(const skv_problem& p, const skv_rotary& r, const skv_tokens& t, const PoolView& pool,
-                             void* q_out, void* k_out, int32_t* status, cudaStream_t st);
+                             void* q_out, void* k_out, int32_t* status, cudaStream_t st, bool cached = false);
 
 // attention over a shared prefix and every request's own tail (attn_prefix.cu)
 size_t prefix_workspace_bytes(const skv_problem& p, int prefix_len);

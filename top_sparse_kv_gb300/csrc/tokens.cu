@@ -514,6 +514,44 @@ __global__ void __launch_bounds__(32 * kLongWarps) token_long_rows_kernel(const 
   }
 }
 
+// Beside a slot cache: what the append has put into GPU slots goes to the host rows that back
+// them as well, else it would be lost when the cache gives the slots to others (it copies
+// nothing back).  A warp a (token, KV head), after the append's kernel, so that one is the same
+// with and without a cache; at most a row of K and of V a token and head cross the link.
+__global__ void __launch_bounds__(256) token_backing_kernel(const TokenArgs a, int row_k, int row_v) {
+  pdl_release();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const long long warps = (long long)gridDim.x * (blockDim.x >> 5), items = (long long)a.n_tokens * a.H;
+  for (long long i = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; i < items; i += warps) {
+    const int tok = (int)(i / a.H), h = (int)(i - (long long)tok * a.H);
+    const Token t = token_of(a, tok, false);  // (reported by the append's kernel, bad entries too)
+    if (!t.live) continue;
+    const int j = t.pos / a.bs, off = t.pos % a.bs, e = table_row(a.pool, t.req, h, a.H)[j];
+    if (e < 0 || e >= a.pool.n_gpu) continue;
+    // block j of request b: host block b * stride + j of per-head tables, host row b * max_len + t of latent rows
+    const long long hb = (long long)t.req * (a.pool.per_head ? a.pool.stride : a.max_len) + j;
+    if (hb >= a.pool.n_host) continue;
+    const size_t from = gpu_block_row(a.pool, e, h, a.H, a.bs) + off, to = ((size_t)hb * a.H + h) * a.bs + off;
+    auto copy = [&](const void* gpu, const void* host, int bytes) {
+      const uint4* src = reinterpret_cast<const uint4*>((const unsigned char*)gpu + from * bytes);
+      uint4* dst = reinterpret_cast<uint4*>((unsigned char*)const_cast<void*>(host) + to * bytes);
+      for (int c = lane; c < bytes / 16; c += 32) dst[c] = src[c];
+    };
+    copy(a.pool.gpu_k, a.pool.host_k, row_k);
+    if (a.v) copy(a.pool.gpu_v, a.pool.host_v, row_v);
+  }
+}
+
+skv_status launch_backing(const TokenArgs& a, int elem, cudaStream_t st) {
+  const long long blocks = ((long long)a.n_tokens * a.H + 7) / 8, most = 8LL * num_sms();
+  if (launch_dependent(token_backing_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, st, 1, a,
+                       a.d * elem, a.dv * elem) != cudaSuccess)
+    return SKV_ERR_CUDA;
+  SKV_LAUNCH_CHECK();
+  return SKV_OK;
+}
+
 int rows_of(const TokenArgs& a) { return (a.q ? a.Hq : 0) + (a.k ? a.H : 0) + (a.v ? a.H : 0); }
 // few tokens: as many parts a token as it has rounds of `per` rows, up to about two CTAs an SM
 int parts_of(const TokenArgs& a, int per) {
@@ -557,10 +595,27 @@ skv_status launch_long(TokenArgs& a, cudaStream_t st) {
   return SKV_OK;
 }
 
+// Staged where a row is a vector a lane, else a warp a row (measured on short rows, too:
+// 8,192 tokens of 72 rows of 128 bf16 54 us staged, 289 us a warp a row; 1,237 of 48 rows
+// of 128 fp32 13.6 against 17.7).
+skv_status launch_rows(TokenArgs& a, bool f32, cudaStream_t st) {
+  const int d = a.v != nullptr && a.dv > a.d ? a.dv : a.d;
+  if (f32) {
+    if (d <= 128) return launch_short<float, 32>(a, st);
+    if (d <= 256) return launch_long<float, 2>(a, st);
+    if (d <= 640) return launch_long<float, 5>(a, st);
+    return launch_long<float, 8>(a, st);
+  }
+  if (d <= 128) return launch_short<__nv_bfloat16, 16>(a, st);
+  if (d <= 256) return launch_short<__nv_bfloat16, 32>(a, st);
+  if (d <= 768) return launch_long<__nv_bfloat16, 3>(a, st);
+  return launch_long<__nv_bfloat16, 4>(a, st);
+}
+
 }  // namespace
 
 skv_status launch_token_rows(const skv_problem& p, const skv_rotary& r, const skv_tokens& t, const PoolView& pool,
-                             void* q_out, void* k_out, int32_t* status, cudaStream_t st) {
+                             void* q_out, void* k_out, int32_t* status, cudaStream_t st, bool cached) {
   const int e = p.dtype == SKV_DTYPE_F32 ? 4 : 2;
   TokenArgs a;
   a.q = (const unsigned char*)t.q;
@@ -597,20 +652,8 @@ skv_status launch_token_rows(const skv_problem& p, const skv_rotary& r, const sk
   a.status = status;
   a.parts = 1;
   a.stage = 0;
-  const int d = a.v != nullptr && p.d_v > p.d_qk ? p.d_v : p.d_qk;
-  // Staged where a row is a vector a lane, else a warp a row (measured on short rows, too:
-  // 8,192 tokens of 72 rows of 128 bf16 54 us staged, 289 us a warp a row; 1,237 of 48 rows
-  // of 128 fp32 13.6 against 17.7).
-  if (p.dtype == SKV_DTYPE_F32) {
-    if (d <= 128) return launch_short<float, 32>(a, st);
-    if (d <= 256) return launch_long<float, 2>(a, st);
-    if (d <= 640) return launch_long<float, 5>(a, st);
-    return launch_long<float, 8>(a, st);
-  }
-  if (d <= 128) return launch_short<__nv_bfloat16, 16>(a, st);
-  if (d <= 256) return launch_short<__nv_bfloat16, 32>(a, st);
-  if (d <= 768) return launch_long<__nv_bfloat16, 3>(a, st);
-  return launch_long<__nv_bfloat16, 4>(a, st);
+  const skv_status rows = launch_rows(a, p.dtype == SKV_DTYPE_F32, st);
+  return rows == SKV_OK && cached ? launch_backing(a, e, st) : rows;
 }
 
 }  // namespace skv

@@ -189,7 +189,8 @@ class ParisStep:
 class TokenStep:
     """New tokens of a layer: `norm_rope()` norms and rotates queries and keys, `append()` also
     writes keys and values to the pool.  The problem, the rotary parameters and the pool are
-    marshalled once, here; every call marshals only its tokens.  Status bits add up in `status`."""
+    marshalled once, here; every call marshals only its tokens.  Status bits add up in `status`.
+    Appends to a pool with a slot cache (`pool.cached`) keep the host rows behind its slots current."""
 
     def __init__(self, problem: B.Problem, rotary: B.Rotary, pool: Optional[B.Pool] = None):
         rotary.check(problem)
@@ -202,7 +203,8 @@ class TokenStep:
         self._pool = None if pool is None else ctypes.byref(pool.c())
         self._st = self.status.data_ptr()
         self._dtype = B.element_type(problem)
-        self._norm_rope, self._append = B.lib().skv_qk_norm_rope, B.lib().skv_append_kv
+        self._norm_rope = B.lib().skv_qk_norm_rope
+        self._append, self._append_cached = B.lib().skv_append_kv, B.lib().skv_append_kv_cached
         self._device = problem.seq_lens.get_device()
         self._seen = None  # the token layout that has been checked
 
@@ -249,12 +251,13 @@ class TokenStep:
         """Appends k and v to the pool; returns q_out (None without q)."""
         if self._pool is None:
             raise ValueError("append() needs a pool")
+        call = self._append_cached if self.pool.cached else self._append
         if q_out is None and q is not None:
             q_out = self._new(q, self.p.n_q_heads, stream)
         ct, qo, _ = self._tokens(q, k, v, positions, requests, q_out, None)
-        st = self._append(self._p, self._r, ctypes.byref(ct), self._pool, qo, self._st, B.raw_stream(self._device, stream))
+        st = call(self._p, self._r, ctypes.byref(ct), self._pool, qo, self._st, B.raw_stream(self._device, stream))
         if st:
-            raise B.SkvError("skv_append_kv", st)
+            raise B.SkvError("skv_append_kv_cached" if self.pool.cached else "skv_append_kv", st)
         return q_out
 
 
