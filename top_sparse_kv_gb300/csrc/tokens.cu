@@ -304,7 +304,8 @@ __global__ void __launch_bounds__(32 * kRowWarps<LPR> + 32, kTokCtas<LPR>) token
   const int sub = lane % LPR, mine = lane / LPR, e0 = sub * VE, w = e0 - a.rot_start;
   const bool in = half > 0 && w >= 0 && w < a.rot_dim, has = e0 < d;
   const int shift = w < half ? half : -half;
-  const bool own = e0 < a.norm_dim, theirs = e0 + shift < a.norm_dim;  // whether the norm covers these, their partners
+  // whether the norm covers these, their partners (without any, the factor -- NaN perhaps -- meets no partner)
+  const bool own = e0 < a.norm_dim, theirs = in && e0 + shift < a.norm_dim;
   int n = 0;
   for (long long it = blockIdx.x; it < items; it += gridDim.x, ++n) {
     const int s = n % kTokStages;
