@@ -588,8 +588,9 @@ skv_status skv_paris_decode_step(const skv_problem *p, const skv_paris *paris, c
  *             (a, b) -> (a cos - b sin, b cos + a sin); pair i is
  *               SKV_ROPE_HALF   (rot_start + i, rot_start + i + rot_dim / 2)
  *               SKV_ROPE_PAIR   (rot_start + 2 i, rot_start + 2 i + 1).
- * inv_freq is taken as exact and the angle is reduced to a turn in 64-bit fixed point
- * before any fp32 arithmetic, so far positions lose nothing.
+ * inv_freq (of either sign, up to 2^14) is taken as exact and the angle is reduced to a
+ * turn in 64-bit fixed point, off by less than 2^-32 of a turn at any position, before any
+ * fp32 arithmetic: far positions and fast frequencies lose nothing.
  * ------------------------------------------------------------------------------------ */
 #define SKV_ROPE_HALF 0
 #define SKV_ROPE_PAIR 1

@@ -1,5 +1,6 @@
 """Norm and rotation at their edges."""
 
+import numpy as np
 import pytest
 import torch
 
@@ -52,3 +53,53 @@ def test_a_row_whose_norm_is_nan_keeps_its_untouched_entries(skv, d, nd, rs, rd,
     for got, x in zip(out, (q, k)):
         assert torch.equal(got.cpu()[..., plain], x[..., plain])
         assert bool(torch.isfinite(got.cpu()[[0, 4]]).all())
+
+
+def _pi(bits):
+    """pi * 2^bits by Machin's formula, in whole numbers."""
+    def arctan_inv(x):
+        total = term = (1 << (bits + 32)) // x
+        n, sign = 3, -1
+        while term:
+            term //= x * x
+            total += sign * (term // n)
+            n, sign = n + 2, -sign
+        return total
+
+    return (4 * (4 * arctan_inv(5) - arctan_inv(239))) >> 32
+
+
+def _exact_cos_sin(t, f):
+    """cos and sin of t * f with the angle reduced in 400-bit whole numbers."""
+    bits = 400
+    num, den = float(f).as_integer_ratio()
+    two_pi = 2 * _pi(bits)
+    ang = (t * num << bits) // den % two_pi
+    if 2 * ang > two_pi:
+        ang -= two_pi
+    x = ang / 2 ** bits  # in [-pi, pi], rounded once
+    return np.cos(x), np.sin(x)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_fast_frequencies_at_far_positions(skv, d):
+    """Frequencies to 1,000 radians a position, of either sign, at positions to 2^31: the fp32 row
+    (1, 0) turns into (cos, sin) of the exact angle.
+
+    Bounds: 2^-22 for the functions; the reduced angle is at most an eighth of a turn and rounded to
+    fp32, 2^-24 pi / 4; its turn is a fraction of 64 bits times a position below 2^31, off by at most
+    2^-32 turns: together below 2^-21."""
+    inv = torch.tensor([0.3, 0.75, 1.0, 2.0, 3.1, 5.5, 6.28, 6.2831855, 17.0, 99.5, 333.25, 1000.0, -0.4, -1.0, -5.0,
+                        -123.5], dtype=torch.float32)
+    inv = inv.repeat(d // 32)
+    pos = [0, 1, 12345, 2 ** 24 + 1, 10 ** 9 + 7, 2 ** 30 - 1, 2 ** 31 - 3, 2 ** 31 - 2]
+    x = torch.zeros((len(pos), 1, d))
+    x[..., :d // 2] = 1.0
+    rot = skv.Rotary(inv.cuda(), rot_dim=d)
+    out, _ = skv.TokenStep(_problem(skv, 1, 1, d, torch.float32, max_len=2 ** 31 - 1), rot).norm_rope(
+        x.cuda(), x.cuda(), torch.tensor(pos, dtype=torch.int32).cuda())
+    for i, t in enumerate(pos):
+        for j in range(16):
+            c, s = _exact_cos_sin(t, float(inv[j]))
+            assert abs(float(out[i, 0, j]) - c) <= 2.0 ** -21, (t, float(inv[j]))
+            assert abs(float(out[i, 0, d // 2 + j]) - s) <= 2.0 ** -21, (t, float(inv[j]))

@@ -40,14 +40,23 @@ struct TokenArgs {
 };
 
 // cos and sin of t * f: the turn t f / 2 pi as a 64-bit fraction, whose integer product
-// with t wraps modulo one turn by itself.  f / 2 pi carries 2^-53 relative error, so the
-// turn is off by less than 2^-24 at t = 2^31 and 2^-35 at t = 2^20.  The nearest quarter
-// turn comes off in integers too; what is left is at most an eighth of a turn, so its
-// fp32 rounding is at most 2^-25 of pi / 4.
+// with t wraps modulo one turn by itself.  One position's turn is f times 1 / 2 pi in two
+// parts, the large one's product exact by its remainder and put into place by its bits (fp64
+// instructions are scarce: four here); it is off by less than 2 * 2^-64 for |f| to 2^14, and
+// t's by less than 2^-32 wherever t lies.  (With one double f / 2 pi carries 2^-53 of itself,
+// times t: at t = 2^31 four parts in 2^24 of a turn for f = 6.)  The nearest quarter turn
+// comes off in integers too; what is left is at most an eighth of a turn, so its fp32
+// rounding is at most 2^-25 of pi / 4.
 __device__ __forceinline__ unsigned long long turn_of(float f) {  // one position's turn, of 2^64
-  double u = (double)f * 0.15915494309189533577;  // 1 / (2 pi)
-  u -= floor(u);
-  return __double2ull_rz(u * 18446744073709551616.0);
+  constexpr double kHi = 0.15915494309189535;  // 1 / 2 pi, and what it lacks
+  constexpr float kLo = -9.8393382e-18f;
+  const double hi = (double)f * kHi;
+  const float lo = fmaf(f, kLo, (float)fma((double)f, kHi, -hi));
+  const long long b = __double_as_longlong(hi);
+  const int up = (int)((b >> 52) & 0x7ff) - 1075 + 64;  // from the mantissa's last place to 2^-64
+  unsigned long long turn = (unsigned long long)((b & ((1ll << 52) - 1)) | (1ll << 52));
+  turn = up >= 0 ? (up < 64 ? turn << up : 0ull) : (up > -64 ? turn >> -up : 0ull);
+  return (b < 0 ? 0ull - turn : turn) + (unsigned long long)__float2ll_rn(lo * 18446744073709551616.f);
 }
 __device__ __forceinline__ float2 cos_sin_of(unsigned long long ph) {
   const unsigned long long near = ph + (1ull << 61);
