@@ -103,3 +103,29 @@ def test_fast_frequencies_at_far_positions(skv, d):
             c, s = _exact_cos_sin(t, float(inv[j]))
             assert abs(float(out[i, 0, j]) - c) <= 2.0 ** -21, (t, float(inv[j]))
             assert abs(float(out[i, 0, d // 2 + j]) - s) <= 2.0 ** -21, (t, float(inv[j]))
+
+
+@pytest.mark.parametrize("d", [128, 576])
+def test_padding_needs_no_request(skv, d):
+    """A token of a negative position is padding whatever its request says, in both calls."""
+    p = _problem(skv, 1, 2, d, torch.bfloat16, max_len=64, batch=2)
+    n = 4
+    q, k = (torch.randn((n, h, d), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda() for h in (2, 1))
+    pool_k = torch.zeros((8, 1, 16, d), dtype=torch.bfloat16, device="cuda")
+    pool = skv.Pool(pool_k, torch.zeros_like(pool_k), torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4))
+    step = skv.TokenStep(p, skv.Rotary(None), pool)
+    pos = torch.tensor([3, -1, -9, 5], dtype=torch.int32).cuda()
+    req = torch.tensor([0, 2, 2 ** 31 - 1, 1], dtype=torch.int32).cuda()
+    q_out, k_out = torch.full_like(q, 7.0), torch.full_like(k, 7.0)
+    step.norm_rope(q, k, pos, req, q_out=q_out, k_out=k_out)
+    step.append(None, k, k, pos, req)
+    assert int(step.status.item()) == 0
+    live = torch.tensor([True, False, False, True])
+    assert torch.equal(q_out[live], q[live]) and bool((q_out[~live] == 7.0).all())
+    assert torch.equal(k_out[live], k[live]) and bool((k_out[~live] == 7.0).all())
+    want = torch.zeros_like(pool_k)
+    want[0, :, 3], want[4, :, 5] = k[0], k[3]
+    assert torch.equal(pool_k, want)
+    # a live token past the batch is an error still
+    step.append(None, k, k, pos.abs(), req)
+    assert int(step.status.item()) == skv.SKV_DEV_BAD_INDEX

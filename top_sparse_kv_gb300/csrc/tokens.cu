@@ -90,7 +90,8 @@ __device__ __forceinline__ Token token_of(const TokenArgs& a, int tok, bool repo
   if (a.requests && t.req < 0) return t;
   const bool needs_req = a.pool.table != nullptr || a.positions == nullptr || a.requests != nullptr;
   if (needs_req && t.req >= a.B) {
-    if (reports) flag(a.status, SKV_DEV_BAD_INDEX);
+    // (a negative position: padding, whatever its request)
+    if (reports && (a.positions == nullptr || a.positions[tok] >= 0)) flag(a.status, SKV_DEV_BAD_INDEX);
     return t;
   }
   t.pos = a.positions ? a.positions[tok] : a.seq_lens[t.req] - 1;
