@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(32 * kRowWarps<LPR> + 32, kTokCtas<LPR>) token
   constexpr int W = kRowWarps<LPR>;
   constexpr int VE = Vec<T>::N, RPW = 32 / LPR, ELEM = sizeof(T);
   extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ unsigned long long turns[LPR * VE / 2];  // of one position, an angle each
   TokenBars& bar = *reinterpret_cast<TokenBars*>(smem);
   const int half = a.rot_dim >> 1, d = a.d;
   const int stage_bytes = kInfoBytes + 16 * d + a.stage;  // info; A, B of queries, of keys; rows
@@ -239,6 +240,7 @@ __global__ void __launch_bounds__(32 * kRowWarps<LPR> + 32, kTokCtas<LPR>) token
       t[d + j] = 0.f;
     }
   }
+  for (int i = threadIdx.x; i < half; i += 32 * W + 32) turns[i] = turn_of(a.inv_freq[i]);
   __syncthreads();
 
   if (warp == W) {
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(32 * kRowWarps<LPR> + 32, kTokCtas<LPR>) token
     for (int u = 0; u < kAngles; ++u) {
       const int i = lane + 32 * u;
       if (i < half) {
-        turn[u] = turn_of(a.inv_freq[i]);
+        turn[u] = turns[i];
         at[u][0] = a.rot_start + (PAIR ? 2 * i : i);
         at[u][1] = a.rot_start + (PAIR ? 2 * i + 1 : i + half);
 #pragma unroll
@@ -584,7 +586,8 @@ skv_status launch_short(TokenArgs& a, cudaStream_t st) {
                           : (part ? token_rows_kernel<T, LPR, false, true> : token_rows_kernel<T, LPR, false, false>);
   const skv_status prep = prepare_kernel((const void*)kernel, kTokSmemMax);
   if (prep != SKV_OK) return prep;
-  const int fit = 228 * 1024 / (smem + 1024), blocks = fit < kTokCtas<LPR> ? fit : kTokCtas<LPR>;
+  constexpr int kTurns = 8 * LPR * Vec<T>::N / 2;  // static shared memory
+  const int fit = 228 * 1024 / (smem + kTurns + 1024), blocks = fit < kTokCtas<LPR> ? fit : kTokCtas<LPR>;
   const long long items = (long long)a.n_tokens * a.parts, slots = (long long)num_sms() * blocks;
   if (launch_dependent(kernel, dim3((unsigned)(items < slots ? items : slots)), dim3(32 * kRowWarps<LPR> + 32), smem,
                        st, 1, a) != cudaSuccess)
