@@ -23,6 +23,10 @@ def _problem(skv, H, Hq, d, dtype, max_len=1 << 20, batch=1):
                        dtype=skv.SKV_DTYPE_F32 if dtype == torch.float32 else skv.SKV_DTYPE_BF16)
 
 
+def _bits(t):
+    return t.contiguous().view(torch.int32 if t.dtype == torch.float32 else torch.int16)
+
+
 PARTIAL = [
     # d, norm_dim, rot_start, rot_dim: the norm ends with the rotated span, inside it, before it, behind it
     (128, 64, 0, 64), (128, 32, 0, 64), (128, 40, 64, 32), (128, 96, 0, 32), (256, 128, 0, 128), (576, 512, 0, 64),
@@ -129,3 +133,22 @@ def test_padding_needs_no_request(skv, d):
     # a live token past the batch is an error still
     step.append(None, k, k, pos.abs(), req)
     assert int(step.status.item()) == skv.SKV_DEV_BAD_INDEX
+
+
+@pytest.mark.parametrize("style", ["half", "pair"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d,rs,rd", [(128, 0, 0), (128, 32, 64), (256, 0, 128), (576, 512, 64)])
+def test_untouched_entries_keep_their_bits(skv, d, rs, rd, dtype, style):
+    """Zeros of either sign, the smallest and the largest numbers, infinities."""
+    g = torch.Generator().manual_seed(d + rd)
+    x = torch.randn((4, 3, d), generator=g).to(dtype)
+    f = torch.finfo(dtype)
+    special = torch.tensor([0.0, -0.0, f.tiny, -f.tiny, f.max, -f.max, float("inf"), -float("inf")]).to(dtype)
+    x[1] = special.repeat(d // 8)
+    inv = (10000.0 ** (-torch.arange(0, rd, 2, dtype=torch.float64) / max(rd, 1))).float().cuda() if rd else None
+    rot = skv.Rotary(inv, rot_dim=rd, rot_start=rs, style=skv.SKV_ROPE_HALF if style == "half" else skv.SKV_ROPE_PAIR)
+    pos = torch.tensor([3, 5, 7, 11], dtype=torch.int32).cuda()
+    _, got = skv.TokenStep(_problem(skv, 3, 3, d, dtype), rot).norm_rope(None, x.cuda(), pos)
+    e = torch.arange(d)
+    plain = (e < rs) | (e >= rs + rd)
+    assert torch.equal(_bits(got.cpu()[..., plain]), _bits(x[..., plain]))

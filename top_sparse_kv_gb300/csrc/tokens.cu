@@ -179,7 +179,7 @@ struct StageInfo {
   int tok, r0, r1;  // the item's rows of the token
 };
 struct alignas(16) TokenBars {
-  unsigned char zeros[16];  // the partner of entries that are not turned
+  unsigned char zeros[16];  // the partner of entries that are not turned: -0, which adds to either zero nothing
   uint64_t full[kTokStages], empty[kTokStages];
   int abort;
 };
@@ -226,11 +226,12 @@ __global__ void __launch_bounds__(32 * kRowWarps<LPR> + 32, kTokCtas<LPR>) token
     }
     fence_barrier_init();
     bar.abort = 0;
-    *reinterpret_cast<uint4*>(bar.zeros) = make_uint4(0, 0, 0, 0);
+    constexpr uint32_t kNone = ELEM == 2 ? 0x80008000u : 0x80000000u;
+    *reinterpret_cast<uint4*>(bar.zeros) = make_uint4(kNone, kNone, kNone, kNone);
   }
   pdl_release();
   pdl_wait();
-  // entries that are not turned: A = g, B = 0 in every stage, for good
+  // entries that are not turned: A = g, B = 0 in every stage, for good (x g + 0 * -0 is x g, its zero's sign too)
   for (int i = threadIdx.x; i < 2 * d; i += 32 * W + 32) {
     const int k = i / d, j = i - k * d;
     const float g = weight(k ? a.gk : a.gq, j);
