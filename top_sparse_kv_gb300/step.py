@@ -190,6 +190,7 @@ class TokenStep:
     """New tokens of a layer: `norm_rope()` norms and rotates queries and keys, `append()` also
     writes keys and values to the pool.  The problem, the rotary parameters and the pool are
     marshalled once, here; every call marshals only its tokens.  Status bits add up in `status`.
+    Other tensors in their places need a new step; the marshalled ones live as long as this one.
     Appends to a pool with a slot cache (`pool.cached`) keep the host rows behind its slots current."""
 
     def __init__(self, problem: B.Problem, rotary: B.Rotary, pool: Optional[B.Pool] = None):
@@ -199,6 +200,7 @@ class TokenStep:
         self.p, self.rotary, self.pool = problem, rotary, pool
         dev = problem.seq_lens.device
         self.status = torch.zeros((1,), dtype=torch.int32, device=dev)
+        self._held = [*vars(problem).values(), *vars(rotary).values(), *(vars(pool).values() if pool else ())]
         self._p, self._r = ctypes.byref(problem.c()), ctypes.byref(rotary.c())
         self._pool = None if pool is None else ctypes.byref(pool.c())
         self._st = self.status.data_ptr()
@@ -264,7 +266,8 @@ class TokenStep:
 class PrefixStep:
     """Attention of a batch over a shared prefix and every request's own tail: owns the output,
     lse, workspace and status; `run(q)` is one skv_prefix_attn.  The problem, the pool and the
-    prefix are marshalled once, here."""
+    prefix are marshalled once, here; other tensors in their places need a new step, and the
+    marshalled ones live as long as this one."""
 
     def __init__(self, problem: B.Problem, pool: B.Pool, prefix: B.Prefix):
         prefix.check(problem)
@@ -273,6 +276,7 @@ class PrefixStep:
         dev = problem.seq_lens.device
         self._device = problem.seq_lens.get_device()
         self._shape = (problem.batch, problem.n_q_heads, problem.d_qk)
+        self._held = [*vars(problem).values(), *vars(pool).values(), *vars(prefix).values()]
         self._p, self._pool, self._prefix = (ctypes.byref(x.c()) for x in (problem, pool, prefix))
         self.out = torch.empty((problem.batch, problem.n_q_heads, problem.d_v), dtype=pool.gpu_k.dtype, device=dev)
         self.lse = torch.empty((problem.batch, problem.n_q_heads), dtype=torch.float32, device=dev)
