@@ -39,7 +39,10 @@
  *    skv_tokens have a stride from token to token).
  *    Element types: SKV_DTYPE_BF16 (bf16 storage, fp32 arithmetic) or
  *    SKV_DTYPE_F32 (fp32 storage and arithmetic) for q, keys, pools and out;
- *    scores and lse are always fp32; indices and tables int32.
+ *    scores and lse are always fp32; indices and tables int32.  Softmax weights of the
+ *    bf16 attentions meet V as bf16 on the tensor cores (their sum, the maximum and the
+ *    accumulation are fp32), so an output is off by up to 2^-8 of the weighted |V| beside
+ *    its own rounding.
  *
  * Regions of request b with history length L = seq_lens[b] (positions 0..L-1,
  * the current token included at L-1):
@@ -165,8 +168,8 @@ typedef struct skv_problem {
  *   e >= 0 : GPU block e holds this head's block only: gpu_k[e][t % block_size][:]
  *            (GPU pools [n_gpu_blocks, block_size, d])
  *   e <  0 : host block (-e - 1) as above (host pools keep every head).
- * Supported by skv_score, skv_gather, skv_sparse_attn, skv_decode_step and the slot
- * cache (skv_cache_*, skv_decode_step_cached), K and V pools (not the latent layout);
+ * Supported by skv_score, skv_gather, skv_sparse_attn, skv_decode_step, the slot cache
+ * (skv_cache_*, skv_decode_step_cached) and the appends, K and V pools (not the latent layout);
  * the other entry points return SKV_ERR_UNSUPPORTED.
  * table_heads = 0 (the default of a zeroed struct) is the shared table above.
  */
@@ -667,6 +670,9 @@ skv_status skv_qk_norm_rope(const skv_problem *p, const skv_rotary *rotary, cons
  * length.  The pools are written (they must be writable, and read by no other work
  * meanwhile); two tokens of one call must not name the same pool row.  requests NULL
  * needs n_tokens <= batch.  n_tokens 0 enqueues nothing.
+ * The pools alone are written: a score through the table (SKV_INDEX_PAGED) sees the new
+ * keys, but what a selection keeps beside them -- contiguous index keys, block summaries,
+ * ParisKV records -- is the caller's to renew for the new positions.
  * A row goes where the table names it and nowhere else: of a pool whose GPU slots a cache
  * manages (skv_decode_step_cached, skv_cache_update), a row written to a slot alone is lost
  * when the cache gives the slot to another -- such a pool takes skv_append_kv_cached.
@@ -699,8 +705,10 @@ skv_status skv_append_kv_cached(const skv_problem *p, const skv_rotary *rotary, 
  *   len    in [0, max_len].
  * A request is of length 0 (an unused row of the batch: out 0, lse -inf) or holds the
  * whole prefix (L_b >= len); a length between, or below 0, sets SKV_DEV_BAD_LENGTH and
- * leaves out 0 and lse -inf; one past max_len sets it too and counts as max_len.  An entry outside its pool sets SKV_DEV_BAD_SLOT and its rows get zero
- * weight.  What lies in a pool past a history's end or the prefix's end is never used.
+ * leaves out 0 and lse -inf; one past max_len sets it too and counts as max_len.  An
+ * entry outside its pool sets SKV_DEV_BAD_SLOT and its rows get zero weight.  What lies in
+ * a pool past a history's end or the prefix's end is never used.  Weights are bf16 at V, as
+ * everywhere on bf16.
  * Of p, batch, the head counts, d_qk, d_v, max_len, block_size, dtype, sm_scale and
  * seq_lens are used.  bf16, d_qk = d_v = 128, K and V pools with one table row a request
  * (table_heads 0), at most 128 query heads per KV head, else SKV_ERR_UNSUPPORTED.
