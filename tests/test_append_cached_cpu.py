@@ -3,6 +3,7 @@
 import ctypes
 
 import pytest
+import torch
 
 import __graft_entry__
 
@@ -58,3 +59,13 @@ def test_both_caches_are_taken(B):
 ])
 def test_refusals(B, latent, over, status):
     assert _call(B, latent, **over) == status
+
+
+def test_a_cache_that_cannot_be_made_leaves_the_pool_alone(B):
+    p = B.Problem(batch=4, n_kv_heads=2, n_q_heads=8, d_qk=128, d_v=128, max_len=100, topk=0, n_sink=0, n_local=0,
+                  block_size=1, seq_lens=torch.zeros(4, dtype=torch.int32))
+    k, v = (torch.zeros((28, 2, 1, 128), dtype=torch.bfloat16) for _ in range(2))
+    pool = B.Pool(k, v, torch.full((4, 100), -1, dtype=torch.int32))  # one table for all heads: no cache of it
+    with pytest.raises(B.SkvError):
+        B.SlotCache.from_table(p, pool, 4)
+    assert not pool.cached

@@ -427,10 +427,10 @@ class SlotCache:
             owner[t[m]] = (b[m] * p.max_len + pos[m])
         nb = ctypes.c_size_t(0)
         cp, cpool = p.c(), pool.c()
-        pool.cached = True
         _check("skv_cache_prepare", lib().skv_cache_prepare())
         _check("skv_cache_workspace_size", lib().skv_cache_workspace_size(ctypes.byref(cp), ctypes.byref(cpool),
                                                                           int(budget), ctypes.byref(nb)))
+        pool.cached = True  # appends keep the host rows behind its slots from now on
         return cls(owner=owner.to(torch.int32), prio=torch.full((n,), -1, dtype=torch.int32, device=dev),
                    step=torch.zeros((1,), dtype=torch.int32, device=dev), budget=int(budget),
                    ws=torch.empty((max(nb.value, 16),), dtype=torch.uint8, device=dev),
