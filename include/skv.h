@@ -11,7 +11,9 @@
  *
  * Beside it: a step's new tokens, normed, rotated and appended to the pools
  * (skv_qk_norm_rope, skv_append_kv), and dense attention over a prefix that the batch
- * shares (skv_prefix_attn).
+ * shares (skv_prefix_attn); the slot table kept on the GPU as requests grow and shrink
+ * (skv_update_tables); and the same steps over a cache in 4 bits (skv_append_kv4,
+ * skv_gather_kv4, skv_score_kv4, skv_attn_kv4, skv_decode_step_kv4).
  *
  * Conventions (every entry point):
  *  - The caller owns all memory.  Device buffers, pinned host pools and the
@@ -79,6 +81,7 @@ typedef int32_t skv_status;
 #define SKV_DEV_BAD_INDEX 2          /* a selected position is outside the candidate region */
 #define SKV_DEV_BAD_LENGTH 4         /* seq_lens[b] outside [0, max_len] (clamped)          */
 #define SKV_DEV_TIMEOUT 8            /* an internal pipeline wait gave up (never expected)  */
+#define SKV_DEV_NO_BLOCK 16          /* a request got no blocks: too few are free           */
 
 /* Element types. */
 #define SKV_DTYPE_BF16 0
@@ -727,6 +730,135 @@ skv_status skv_prefix_workspace_size(const skv_problem *p, int32_t prefix_len, s
 
 skv_status skv_prefix_attn(const skv_problem *p, const void *q, const skv_kv_pool *pool, const skv_prefix *prefix,
                            void *out, float *lse, void *ws, size_t ws_bytes, int32_t *dev_status, void *stream);
+
+/* ------------------------------------------------------------------------------------
+ * Block tables and slot maps, kept on the GPU: every request grows by its new tokens or
+ * gives its last ones back, blocks come off (and return to) a stack of free ones, and the
+ * step's tokens learn their positions, requests and pool rows -- what skv_append_kv and
+ * skv_append_kv4 take.  One call a step, nothing read back by the host; it can be captured.
+ *
+ * With L = seq_lens[b] before the call and n = n_new[b]:
+ *   n > 0  the request takes the positions [s, s + n), s = L, or `base` where L is 0 (an
+ *          unused row of the batch); its slot-table row gets free blocks for the indices
+ *          that its new length needs and its old one did not; its length becomes s + n.
+ *   n < 0  its last -n tokens go: the length becomes L + n, or 0 where no token past base
+ *          is left; blocks that no longer hold any are free again.  (n = -max_len: all go.)
+ *   n = 0  nothing.
+ * Table indices below base / block_size are the caller's (a prompt that requests share):
+ * they are neither read nor written; a block that base ends inside is the request's own.
+ * Blocks given back in a call serve its requests first.  In order: the blocks that requests
+ * need, b ascending and index ascending, come from those given back, the first request's
+ * first and its lowest index first, and then off the top of the stack; of the blocks given
+ * back, the rest go onto it, the last request's first and its highest index first -- so a
+ * call that takes back what the call before it gave leaves the stack as it was.
+ * A request is refused -- its length and table row stay, its tokens are padding, and a
+ * SKV_DEV_* bit is set -- when its length is not one (L < 0, L > max_len, 0 < L < base) or
+ * would pass max_len (SKV_DEV_BAD_LENGTH); when its rows would pass n_tokens
+ * (SKV_DEV_BAD_INDEX); or when the blocks needed by it and the requests before it (those
+ * refused for their rows or for want of blocks among them) are more than are free, and it needs any
+ * (SKV_DEV_NO_BLOCK).
+ *
+ * Rows of the step: the tokens of request 0, then request 1's, and so on (a refused one's
+ * rows stay in their place); n_tokens of them, the rows past the last token padding.
+ *   positions, requests  device int32 [n_tokens]; -1 of padding.
+ *   slots                device int64 [n_tokens] or NULL: the pool row of KV head 0's block,
+ *                        block * block_size + position % block_size; -1 of padding.
+ * The shared table form (one row a request); blocks of the GPU pool only.  An entry given
+ * back that is no block below n_blocks sets SKV_DEV_BAD_SLOT and goes onto the stack all
+ * the same; one that finds the stack full (of n_blocks entries) sets it and is dropped.
+ *
+ *   batch        requests, 1..4096 (more: SKV_ERR_UNSUPPORTED).
+ *   max_len, block_size, table_stride   as in skv_problem and skv_kv_pool.
+ *   base         positions that every request has before its own, in [0, max_len].
+ *   n_blocks     blocks that there are; the stack's room.
+ *   slot_table   device int32 [batch, table_stride], written in place.
+ *   seq_lens     device int32 [batch], written in place.
+ *   free_blocks  device int32 [n_blocks]: the stack, state[0] entries, the top last.
+ *   state        device int32 [4]: the stack's entries; zero; zero; zero (the call's own).
+ * The buffers are a call's own until it has run; calls in turn on one stream may share them.
+ * ------------------------------------------------------------------------------------ */
+typedef struct skv_tables {
+  int32_t batch;
+  int32_t max_len;
+  int32_t block_size;
+  int32_t base;
+  int32_t table_stride;
+  int32_t n_blocks;
+  int32_t *slot_table;
+  int32_t *seq_lens;
+  int32_t *free_blocks;
+  int32_t *state;
+} skv_tables;
+
+/* n_new device int32 [batch]; n_tokens 0: no rows (positions, requests and slots may be
+ * NULL, and a request that grows is refused). */
+skv_status skv_update_tables(const skv_tables *t, const int32_t *n_new, int32_t n_tokens, int32_t *positions,
+                             int32_t *requests, int64_t *slots, int32_t *dev_status, void *stream);
+
+/* ------------------------------------------------------------------------------------
+ * A cache in 4 bits.  A row of 128 entries is held in groups of `group` (32, 64 or 128)
+ * consecutive ones, each with a step s and a centre z in bf16 and a code c in 0..15 an entry:
+ *   x^ = s (c - 8) + z
+ * Of a row x in fp32 the append makes, per group, with lo and hi its least and largest entry,
+ *   s = bf16((hi - lo) / 15),  z = bf16((hi + lo) / 2 + s / 2),
+ *   c = 8 + the whole number next to (x - z) / s, ties to even, held to [-8, 7]  (8 where s is 0)
+ * so |x - x^| <= s / 2, and at a group's ends up to 2^-5 s + 2^-8 |z| more, what the rounding of s
+ * and z leaves them outside.  A group with an infinite or NaN entry, or whose hi - lo passes fp32, gets
+ * s = z = NaN: it reads as NaN.
+ *
+ * Pools are those of skv_kv_pool (both table forms, GPU and pinned host blocks, K and V)
+ * with bytes for elements: [n_blocks, n_kv_heads, block_size / 16, cell] (per-head tables:
+ * GPU pools without n_kv_heads), block_size a multiple of 16.  A cell is 16 tokens of one
+ * head, 1024 + 64 * (128 / group) bytes:
+ *   token r's codes   64 bytes at 64 r: entries 2 j and 2 j + 1 share byte j, the even one
+ *                     in its low half; byte j = 8 i + u stands at 64 r + 8 u + i
+ *   token r's steps   a word a group at 1024 + 4 (r * (128 / group) + group): s in its low
+ *                     half, z in its high half.
+ *
+ * d_qk = d_v = d_idx = 128, K and V pools (no latent layout), at most 16 query heads a KV
+ * head, block_size a multiple of 16, max_len at most 2^30, else SKV_ERR_UNSUPPORTED; a group
+ * other than the three is SKV_ERR_INVALID_ARGUMENT.  Slot caches, prefetch, block summaries and ParisKV
+ * do not take these pools.
+ * ------------------------------------------------------------------------------------ */
+
+/* skv_append_kv into 4 bits: K rows normed and rotated, V rows as they are, both in fp32
+ * until they are coded.  tokens and q_out of p->dtype (bf16 or fp32), as for skv_append_kv. */
+skv_status skv_append_kv4(const skv_problem *p, const skv_rotary *rotary, const skv_tokens *tokens,
+                          const skv_kv_pool *pool, int32_t group, void *q_out, int32_t *dev_status, void *stream);
+
+/* skv_gather from 4 bits: the attended rows' values x^ in p->dtype, list and shapes as for
+ * skv_gather.  idx may be NULL with topk 0 -- with n_sink 0 and n_local n, every request's
+ * last n rows; k_out or v_out may be NULL.  SKV_AGG_HEAD as for skv_gather. */
+skv_status skv_gather_kv4(const skv_problem *p, const skv_kv_pool *pool, int32_t group, const int32_t *idx,
+                          void *k_out, void *v_out, int32_t *dev_status, void *stream);
+
+/* skv_score from 4 bits: scores[b][h][t] = <q_bar, k^_t> in fp32 of the candidates, every
+ * group_agg, rows and untouched positions as for skv_score.  p->dtype is bf16, q_score
+ * [batch, n_idx_q_heads, 128], at most 16 scoring heads a KV head.  A key whose entry lies outside its pool scores NaN. */
+skv_status skv_score_kv4(const skv_problem *p, const void *q_score, const skv_kv_pool *pool, int32_t group,
+                         float *scores, int32_t *dev_status, void *stream);
+
+/* Bytes of workspace for skv_attn_kv4 and skv_decode_step_kv4 (skv_topk included). */
+skv_status skv_kv4_workspace_size(const skv_problem *p, size_t *bytes);
+
+/* Attention from 4 bits: over list(b,h) as skv_sparse_attn (SKV_AGG_HEAD: query head j's own
+ * list; with topk 0 any aligned pointer, which is not read), or, with idx NULL, over every
+ * position t < L_b whatever topk, n_sink and n_local.
+ *   z_t = sm_scale * <q, k^_t>,  out = sum_t softmax(z)_t v^_t,  lse = log sum_t exp(z_t)
+ * A request of length 0 (or an empty list) gives out 0 and lse -inf.  Entries outside their
+ * pool, positions outside the candidates: flagged, zero weight.  p->dtype is bf16.  Softmax
+ * weights times steps meet the codes as fp16 on the tensor cores (11 bits; a weight below
+ * 2^-32 of the largest counts as 0, steps from 2^-60 up keep that precision); centres, sums
+ * and the maximum are fp32.  Deterministic: the same inputs give the same bits. */
+skv_status skv_attn_kv4(const skv_problem *p, const void *q, const skv_kv_pool *pool, int32_t group,
+                        const int32_t *idx, void *out, float *lse, void *ws, size_t ws_bytes, int32_t *dev_status,
+                        void *stream);
+
+/* skv_score_kv4 (of q_score, or q where it is NULL), skv_topk and skv_attn_kv4 over the
+ * selection; scores and idx are outputs too. */
+skv_status skv_decode_step_kv4(const skv_problem *p, const void *q, const void *q_score, const skv_kv_pool *pool,
+                               int32_t group, float *scores, int32_t *idx, void *out, float *lse, void *ws,
+                               size_t ws_bytes, int32_t *dev_status, void *stream);
 
 #ifdef __cplusplus
 }

@@ -23,6 +23,7 @@ SKV_OK = 0
 STATUS_NAMES = {0: "ok", 1: "invalid argument", 2: "unsupported shape", 3: "CUDA error",
                 4: "workspace too small", 5: "device fault", 6: "timeout"}
 SKV_DEV_BAD_SLOT, SKV_DEV_BAD_INDEX, SKV_DEV_BAD_LENGTH, SKV_DEV_TIMEOUT = 1, 2, 4, 8
+SKV_DEV_NO_BLOCK = 16
 SKV_DTYPE_BF16, SKV_DTYPE_F32 = 0, 1
 SKV_AGG_MEAN = 0
 SKV_AGG_MAX = 1
@@ -85,6 +86,12 @@ class CPrefix(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("len", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class CTables(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "max_len", "block_size", "base", "table_stride", "n_blocks")] + [
+        (n, ctypes.c_void_p) for n in ("slot_table", "seq_lens", "free_blocks", "state")]
+
+
 class CPrefetch(ctypes.Structure):
     _fields_ = [("tau_ema", ctypes.c_void_p), ("epoch", ctypes.c_void_p), ("map", ctypes.c_void_p),
                 ("staging", ctypes.c_void_p), ("count", ctypes.c_void_p), ("stats", ctypes.c_void_p),
@@ -127,6 +134,14 @@ def _load():
                                  VP],
         "skv_prefix_workspace_size": [P, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)],
         "skv_prefix_attn": [P, VP, ctypes.POINTER(CPool), ctypes.POINTER(CPrefix), VP, VP, VP, SZ, VP, VP],
+        "skv_update_tables": [ctypes.POINTER(CTables), VP, ctypes.c_int32, VP, VP, VP, VP, VP],
+        "skv_append_kv4": [P, ctypes.POINTER(CRotary), ctypes.POINTER(CTokens), ctypes.POINTER(CPool),
+                           ctypes.c_int32, VP, VP, VP],
+        "skv_gather_kv4": [P, ctypes.POINTER(CPool), ctypes.c_int32, VP, VP, VP, VP, VP],
+        "skv_score_kv4": [P, VP, ctypes.POINTER(CPool), ctypes.c_int32, VP, VP, VP],
+        "skv_kv4_workspace_size": [P, ctypes.POINTER(ctypes.c_size_t)],
+        "skv_attn_kv4": [P, VP, ctypes.POINTER(CPool), ctypes.c_int32, VP, VP, VP, VP, SZ, VP, VP],
+        "skv_decode_step_kv4": [P, VP, VP, ctypes.POINTER(CPool), ctypes.c_int32, VP, VP, VP, VP, VP, SZ, VP, VP],
         "skv_block_workspace_size": [P, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t),
                                      ctypes.POINTER(ctypes.c_int32)],
         "skv_block_summaries": [P, ctypes.POINTER(CPool), VP, VP, VP],
@@ -202,7 +217,12 @@ def check_pool(p: "Problem", pool: "Pool") -> None:
     """The pool's types, sizes and devices, which the C side cannot see."""
     same_device(p, gpu_k=pool.gpu_k, gpu_v=pool.gpu_v, slot_table=pool.slot_table)
     heads = 1 if pool.table_heads else p.n_kv_heads
-    for name, d in (("gpu_k", p.d_qk), ("gpu_v", p.d_v), ("host_k", p.d_qk), ("host_v", p.d_v)):
+    if isinstance(pool, Kv4Pool):
+        pool.check(p)
+        sides = ()
+    else:
+        sides = (("gpu_k", p.d_qk), ("gpu_v", p.d_v), ("host_k", p.d_qk), ("host_v", p.d_v))
+    for name, d in sides:
         t = getattr(pool, name)
         if t is None:
             continue
@@ -213,6 +233,12 @@ def check_pool(p: "Problem", pool: "Pool") -> None:
             or pool.slot_table.shape[0] < p.batch:
         raise ValueError(f"slot_table: contiguous int32, a row for each of {p.batch} requests")
     check_lens(p)
+
+
+def check_pool4(p: "Problem", pool: "Kv4Pool") -> None:
+    if not isinstance(pool, Kv4Pool):
+        raise ValueError("a Kv4Pool expected")
+    check_pool(p, pool)
 
 
 def _check(fn: str, st: int):
@@ -271,6 +297,54 @@ class Pool:
                      None if self.host_v is None else self.host_v.data_ptr(),
                      0 if self.host_k is None else self.host_k.shape[0],
                      self.slot_table.data_ptr(), self.slot_table.shape[-1], self.table_heads)
+
+
+@dataclass
+class Kv4Pool(Pool):
+    """A pool in 4 bits: uint8 tensors [n_blocks, H, block_size / 16, cell] (with table_heads = 1 the
+    GPU ones [n_blocks, block_size / 16, cell]), cells as include/skv.h lays them out."""
+
+    group: int = 32
+
+    @staticmethod
+    def cell_bytes(group: int) -> int:
+        return 1024 + 64 * (128 // group)
+
+    @classmethod
+    def empty(cls, n_blocks: int, n_kv_heads: int, block_size: int, slot_table: torch.Tensor, group: int = 32,
+              n_host_blocks: int = 0) -> "Kv4Pool":
+        """Pools of n_blocks on the table's device (and n_host_blocks in pinned host memory)."""
+        per_head = slot_table.dim() == 3
+        cells = (block_size // 16, cls.cell_bytes(group))
+
+        def make(n, heads, **kw):
+            return torch.empty((n, *heads, *cells), dtype=torch.uint8, **kw) if n else None
+
+        gpu = [make(n_blocks, () if per_head else (n_kv_heads,), device=slot_table.device) for _ in range(2)]
+        host = [make(n_host_blocks, (n_kv_heads,), pin_memory=True) for _ in range(2)]
+        return cls(*gpu, slot_table, *host, table_heads=int(per_head), group=group)
+
+    def c(self) -> CPool:
+        raise ValueError("a pool in 4 bits: the calls named *_kv4 take it")
+
+    def c4(self) -> CPool:
+        return super().c()
+
+    def check(self, p: "Problem") -> None:
+        """The pools' types and sizes, which the C side cannot see."""
+        if self.group not in (32, 64, 128) or p.block_size % 16:
+            raise ValueError("group: 32, 64 or 128; block_size: a multiple of 16")
+        cells = p.block_size // 16 * self.cell_bytes(self.group)
+        for name in ("gpu_k", "gpu_v", "host_k", "host_v"):
+            t = getattr(self, name)
+            if t is None and name.startswith("host"):
+                continue
+            heads = 1 if self.table_heads and name.startswith("gpu") else p.n_kv_heads
+            if t is None or t.dtype != torch.uint8 or t.numel() != t.shape[0] * heads * cells or not t.is_contiguous():
+                raise ValueError(f"{name}: contiguous uint8 blocks of {heads} x {cells} bytes expected")
+        if self.gpu_v.shape[0] != self.gpu_k.shape[0] or (self.host_k is None) != (self.host_v is None) or (
+                self.host_k is not None and self.host_v.shape[0] != self.host_k.shape[0]):
+            raise ValueError("K and V pools of one size expected")
 
 
 @dataclass
@@ -412,6 +486,7 @@ class SlotCache:
     @classmethod
     def from_table(cls, p: "Problem", pool: "Pool", budget: int) -> "SlotCache":
         """Owners as the slot table names them, every slot unused so far."""
+        cp, cpool = p.c(), pool.c()
         n = pool.gpu_k.shape[0]
         dev = pool.gpu_k.device
         owner = torch.full((n,), -1, dtype=torch.int64, device=dev)
@@ -426,7 +501,6 @@ class SlotCache:
             m = t >= 0
             owner[t[m]] = (b[m] * p.max_len + pos[m])
         nb = ctypes.c_size_t(0)
-        cp, cpool = p.c(), pool.c()
         _check("skv_cache_prepare", lib().skv_cache_prepare())
         _check("skv_cache_workspace_size", lib().skv_cache_workspace_size(ctypes.byref(cp), ctypes.byref(cpool),
                                                                           int(budget), ctypes.byref(nb)))
@@ -655,6 +729,134 @@ def skv_append_kv(p: Problem, rotary: Rotary, q, k, v, pool: Pool, q_out, positi
 def skv_append_kv_cached(p: Problem, rotary: Rotary, q, k, v, pool: Pool, q_out, positions=None, requests=None,
                          dev_status=None, stream=None):
     _append("skv_append_kv_cached", p, rotary, q, k, v, pool, q_out, positions, requests, dev_status, stream)
+
+
+def skv_append_kv4(p: Problem, rotary: Rotary, q, k, v, pool: Kv4Pool, q_out, positions=None, requests=None,
+                   dev_status=None, stream=None):
+    rotary.check(p)
+    check_pool4(p, pool)
+    same_device(p, dev_status=dev_status)
+    cp, cr, ct, cpool = p.c(), rotary.c(), c_tokens(p, q, k, v, positions, requests), pool.c4()
+    qo = _out_rows("q_out", q_out, q, p.n_q_heads, p.d_qk, element_type(p))
+    _check("skv_append_kv4", lib().skv_append_kv4(
+        ctypes.byref(cp), ctypes.byref(cr), ctypes.byref(ct), ctypes.byref(cpool), pool.group, qo, _ptr(dev_status),
+        raw_stream(p.seq_lens.get_device(), stream)))
+
+
+def dense(p: Problem, name: str, t, dtype, shape) -> None:
+    """A tensor's type, shape, layout and device (None passes)."""
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()
+                          or t.device != p.seq_lens.device):
+        raise ValueError(f"{name}: contiguous {dtype} {list(shape)} on {p.seq_lens.device} expected")
+
+
+def list_heads(p: Problem) -> int:
+    """Rows of scores and lists a request: per KV head, or per query head under SKV_AGG_HEAD."""
+    return p.n_q_heads if p.group_agg == SKV_AGG_HEAD else p.n_kv_heads
+
+
+def skv_gather_kv4(p: Problem, pool: Kv4Pool, idx, k_out, v_out=None, dev_status=None, stream=None):
+    check_pool4(p, pool)
+    rows = (p.batch, list_heads(p))
+    dense(p, "idx", idx, torch.int32, rows + (p.topk,))
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        dense(p, name, t, element_type(p), rows + (p.n_sink + p.topk + p.n_local, 128))
+    device = same_device(p, dev_status=dev_status)
+    cp, cpool = p.c(), pool.c4()
+    _check("skv_gather_kv4", lib().skv_gather_kv4(
+        ctypes.byref(cp), ctypes.byref(cpool), pool.group, _ptr(idx), _ptr(k_out), _ptr(v_out), _ptr(dev_status),
+        raw_stream(device, stream)))
+
+
+def skv_score_kv4(p: Problem, q_score, pool: Kv4Pool, scores, dev_status=None, stream=None):
+    check_pool4(p, pool)
+    dense(p, "q_score", q_score, torch.bfloat16, (p.batch, p.n_idx_q_heads or p.n_q_heads, 128))
+    dense(p, "scores", scores, torch.float32, (p.batch, list_heads(p), p.max_len))
+    device = same_device(p, dev_status=dev_status)
+    cp, cpool = p.c(), pool.c4()
+    _check("skv_score_kv4", lib().skv_score_kv4(ctypes.byref(cp), _ptr(q_score), ctypes.byref(cpool), pool.group,
+                                                _ptr(scores), _ptr(dev_status), raw_stream(device, stream)))
+
+
+def skv_kv4_workspace_size(p: Problem) -> int:
+    n = ctypes.c_size_t(0)
+    cp = p.c()
+    _check("skv_kv4_workspace_size", lib().skv_kv4_workspace_size(ctypes.byref(cp), ctypes.byref(n)))
+    return n.value
+
+
+def list_ptr(p: Problem, idx) -> Optional[int]:
+    """A list's pointer: NULL means no list, so one of no entries (topk 0) gets another, never read."""
+    return None if idx is None else (idx if idx.numel() else p.seq_lens).data_ptr()
+
+
+def _attn_kv4(p: Problem, q, pool, idx, out, lse, ws, dev_status) -> int:
+    check_pool4(p, pool)
+    dense(p, "q", q, torch.bfloat16, (p.batch, p.n_q_heads, 128))
+    dense(p, "idx", idx, torch.int32, (p.batch, list_heads(p), p.topk))
+    dense(p, "out", out, torch.bfloat16, (p.batch, p.n_q_heads, 128))
+    dense(p, "lse", lse, torch.float32, (p.batch, p.n_q_heads))
+    return same_device(p, ws=ws, dev_status=dev_status)
+
+
+def skv_attn_kv4(p: Problem, q, pool: Kv4Pool, idx, out, lse, ws, dev_status=None, stream=None):
+    """idx None: over every position of each request's history."""
+    device = _attn_kv4(p, q, pool, idx, out, lse, ws, dev_status)
+    cp, cpool = p.c(), pool.c4()
+    _check("skv_attn_kv4", lib().skv_attn_kv4(
+        ctypes.byref(cp), _ptr(q), ctypes.byref(cpool), pool.group, list_ptr(p, idx), _ptr(out), _ptr(lse), _ptr(ws),
+        ws.numel() * ws.element_size(), _ptr(dev_status), raw_stream(device, stream)))
+
+
+def skv_decode_step_kv4(p: Problem, q, q_score, pool: Kv4Pool, scores, idx, out, lse, ws, dev_status=None,
+                        stream=None):
+    device = _attn_kv4(p, q, pool, idx, out, lse, ws, dev_status)
+    dense(p, "q_score", q_score, torch.bfloat16, (p.batch, p.n_idx_q_heads or p.n_q_heads, 128))
+    dense(p, "scores", scores, torch.float32, (p.batch, list_heads(p), p.max_len))
+    cp, cpool = p.c(), pool.c4()
+    _check("skv_decode_step_kv4", lib().skv_decode_step_kv4(
+        ctypes.byref(cp), _ptr(q), _ptr(q_score), ctypes.byref(cpool), pool.group, _ptr(scores), list_ptr(p, idx),
+        _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _ptr(dev_status), raw_stream(device, stream)))
+
+
+@dataclass
+class Tables:
+    """Block tables kept on the GPU; see skv_tables in include/skv.h.  seq_lens, batch, max_len and
+    block_size are the problem's."""
+
+    slot_table: torch.Tensor   # device int32 [batch, stride]
+    free_blocks: torch.Tensor  # device int32 [n_blocks]: the stack, state[0] entries
+    state: torch.Tensor        # device int32 [4]
+    base: int = 0
+
+    def check(self, p: Problem) -> None:
+        check_lens(p)
+        same_device(p, slot_table=self.slot_table, free_blocks=self.free_blocks, state=self.state)
+        for name, n in (("slot_table", p.batch), ("free_blocks", 0), ("state", 4)):
+            t = getattr(self, name)
+            if t.dtype != torch.int32 or not t.is_contiguous() or t.shape[0] < n:
+                raise ValueError(f"{name}: contiguous int32 expected")
+        if self.slot_table.dim() != 2:
+            raise ValueError("slot_table: [batch, stride], one row a request")
+
+    def c(self, p: Problem) -> CTables:
+        return CTables(p.batch, p.max_len, p.block_size, self.base, self.slot_table.shape[1],
+                       self.free_blocks.numel(), self.slot_table.data_ptr(), p.seq_lens.data_ptr(),
+                       self.free_blocks.data_ptr(), self.state.data_ptr())
+
+
+def skv_update_tables(p: Problem, tables: Tables, n_new, n_tokens: int = 0, positions=None, requests=None, slots=None,
+                      dev_status=None, stream=None):
+    tables.check(p)
+    dense(p, "n_new", n_new, torch.int32, (p.batch,))
+    for name, t, dtype in (("positions", positions, torch.int32), ("requests", requests, torch.int32),
+                           ("slots", slots, torch.int64)):
+        dense(p, name, t, dtype, (n_tokens,))
+    device = same_device(p, dev_status=dev_status)
+    ct = tables.c(p)
+    _check("skv_update_tables", lib().skv_update_tables(ctypes.byref(ct), _ptr(n_new), int(n_tokens), _ptr(positions),
+                                                        _ptr(requests), _ptr(slots), _ptr(dev_status),
+                                                        raw_stream(device, stream)))
 
 
 @dataclass

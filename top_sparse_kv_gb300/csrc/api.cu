@@ -748,7 +748,8 @@ skv_status skv_qk_norm_rope(const skv_problem* p, const skv_rotary* rotary, cons
 }
 
 static skv_status append(const skv_problem* p, const skv_rotary* rotary, const skv_tokens* tokens,
-                         const skv_kv_pool* pool, void* q_out, int32_t* dev_status, void* stream, bool cached) {
+                         const skv_kv_pool* pool, void* q_out, int32_t* dev_status, void* stream, bool cached,
+                         int32_t group = 0) {
   SKV_TRY(check_tokens(p, rotary, tokens, q_out));
   SKV_TRY(check_pool(*p, pool));
   if (!aligned4(pool->slot_table) || !aligned4(dev_status)) return SKV_ERR_INVALID_ARGUMENT;
@@ -764,7 +765,7 @@ static skv_status append(const skv_problem* p, const skv_rotary* rotary, const s
   }
   if (!tokens->requests && tokens->n_tokens > p->batch) return SKV_ERR_INVALID_ARGUMENT;
   return launch_token_rows(*p, *rotary, *tokens, view(pool), q_out, nullptr, dev_status, (cudaStream_t)stream,
-                           cached);
+                           cached, group);
 }
 
 skv_status skv_append_kv(const skv_problem* p, const skv_rotary* rotary, const skv_tokens* tokens,
@@ -816,6 +817,119 @@ skv_status skv_prefix_attn(const skv_problem* p, const void* q, const skv_kv_poo
   if (ws_bytes < prefix_workspace_bytes(*p, prefix->len)) return SKV_ERR_WORKSPACE_TOO_SMALL;
   if (!ws || !aligned16(ws)) return SKV_ERR_INVALID_ARGUMENT;
   return launch_prefix_attn(*p, q, view(pool), *prefix, out, lse, ws, dev_status, (cudaStream_t)stream);
+}
+
+// ---------------------------------------------------------------- block tables
+
+skv_status skv_update_tables(const skv_tables* t, const int32_t* n_new, int32_t n_tokens, int32_t* positions,
+                             int32_t* requests, int64_t* slots, int32_t* dev_status, void* stream) {
+  if (!t || t->batch < 1 || t->max_len < 0 || t->block_size < 1 || t->n_blocks < 0) return SKV_ERR_INVALID_ARGUMENT;
+  if (t->base < 0 || t->base > t->max_len || n_tokens < 0) return SKV_ERR_INVALID_ARGUMENT;
+  if (t->table_stride < ((long long)t->max_len + t->block_size - 1) / t->block_size) return SKV_ERR_INVALID_ARGUMENT;
+  if (!n_new || !t->slot_table || !t->seq_lens || !t->state || (!t->free_blocks && t->n_blocks > 0))
+    return SKV_ERR_INVALID_ARGUMENT;
+  if (!aligned4(n_new) || !aligned4(t->slot_table) || !aligned4(t->seq_lens) || !aligned4(t->free_blocks) ||
+      !aligned4(t->state) || !aligned4(dev_status))
+    return SKV_ERR_INVALID_ARGUMENT;
+  if (n_tokens > 0 && (!positions || !requests)) return SKV_ERR_INVALID_ARGUMENT;
+  if (!aligned16(positions) || !aligned16(requests) || !aligned16(slots)) return SKV_ERR_INVALID_ARGUMENT;
+  if (t->batch > tables_max_batch()) return SKV_ERR_UNSUPPORTED;
+  return launch_update_tables(*t, n_new, n_tokens, positions, requests, slots, dev_status, (cudaStream_t)stream);
+}
+
+// ---------------------------------------------------------------- a cache in 4 bits
+
+static skv_status check_kv4_problem(const skv_problem* p) {
+  SKV_TRY(check_problem(p));
+  if (p->d_qk != 128 || p->d_v != 128 || p->d_idx != 128) return SKV_ERR_UNSUPPORTED;
+  if (p->block_size % 16 || p->max_len > (1 << 30)) return SKV_ERR_UNSUPPORTED;
+  if (p->n_q_heads / p->n_kv_heads > 16) return SKV_ERR_UNSUPPORTED;
+  const long long n_att = (long long)p->n_sink + p->topk + p->n_local;
+  const long long rows = (long long)p->batch * (p->group_agg == SKV_AGG_HEAD ? p->n_q_heads : p->n_kv_heads);
+  // list places stay in 32 bits, rows of a list in 40
+  if (n_att > (1 << 30) || rows * n_att > (1LL << 40)) return SKV_ERR_UNSUPPORTED;
+  if ((long long)p->batch * p->n_q_heads > 0x7fffffffLL) return SKV_ERR_UNSUPPORTED;  // the merge's CTAs
+  return SKV_OK;
+}
+
+static skv_status check_kv4(const skv_problem* p, const skv_kv_pool* pool, int32_t group, const int32_t* dev_status) {
+  SKV_TRY(check_problem(p));
+  SKV_TRY(check_pool(*p, pool));
+  if (group != 32 && group != 64 && group != 128) return SKV_ERR_INVALID_ARGUMENT;
+  if (!aligned4(p->seq_lens) || !aligned4(pool->slot_table) || !aligned4(dev_status)) return SKV_ERR_INVALID_ARGUMENT;
+  SKV_TRY(check_kv4_problem(p));
+  if (!pool->gpu_v) return SKV_ERR_UNSUPPORTED;  // latent rows
+  return SKV_OK;
+}
+
+skv_status skv_append_kv4(const skv_problem* p, const skv_rotary* rotary, const skv_tokens* tokens,
+                          const skv_kv_pool* pool, int32_t group, void* q_out, int32_t* dev_status, void* stream) {
+  SKV_TRY(check_kv4(p, pool, group, dev_status));
+  return append(p, rotary, tokens, pool, q_out, dev_status, stream, false, group);
+}
+
+skv_status skv_gather_kv4(const skv_problem* p, const skv_kv_pool* pool, int32_t group, const int32_t* idx,
+                          void* k_out, void* v_out, int32_t* dev_status, void* stream) {
+  SKV_TRY(check_kv4(p, pool, group, dev_status));
+  if ((!idx && p->topk > 0) || !aligned4(idx) || !aligned16(k_out) || !aligned16(v_out))
+    return SKV_ERR_INVALID_ARGUMENT;
+  if (!k_out && !v_out) return SKV_ERR_INVALID_ARGUMENT;
+  return launch_kv4_gather(head_rows(*p), head_view(*p, pool), group, idx, k_out, v_out, dev_status,
+                           (cudaStream_t)stream);
+}
+
+skv_status skv_score_kv4(const skv_problem* p, const void* q_score, const skv_kv_pool* pool, int32_t group,
+                         float* scores, int32_t* dev_status, void* stream) {
+  SKV_TRY(check_kv4(p, pool, group, dev_status));
+  if (!q_score || !scores || !aligned16(q_score) || !aligned16(scores)) return SKV_ERR_INVALID_ARGUMENT;
+  if (p->dtype != SKV_DTYPE_BF16) return SKV_ERR_UNSUPPORTED;
+  return launch_kv4_score(*p, q_score, view(pool), group, scores, dev_status, (cudaStream_t)stream);
+}
+
+static size_t kv4_bytes(const skv_problem& r) {
+  const size_t a = kv4_attn_workspace_bytes(r), t = topk_workspace_bytes(r);
+  return a > t ? a : t;
+}
+
+skv_status skv_kv4_workspace_size(const skv_problem* p, size_t* bytes) {
+  SKV_TRY(check_kv4_problem(p));
+  if (!bytes) return SKV_ERR_INVALID_ARGUMENT;
+  *bytes = kv4_bytes(head_rows(*p));
+  return SKV_OK;
+}
+
+skv_status skv_attn_kv4(const skv_problem* p, const void* q, const skv_kv_pool* pool, int32_t group,
+                        const int32_t* idx, void* out, float* lse, void* ws, size_t ws_bytes, int32_t* dev_status,
+                        void* stream) {
+  SKV_TRY(check_kv4(p, pool, group, dev_status));
+  if (!q || !out || !aligned16(q) || !aligned16(out) || !aligned4(idx) || !aligned4(lse))
+    return SKV_ERR_INVALID_ARGUMENT;
+  if (p->dtype != SKV_DTYPE_BF16) return SKV_ERR_UNSUPPORTED;
+  // over the whole history the heads of a group attend the same keys, whatever the selection's rows
+  const skv_problem r = idx ? head_rows(*p) : *p;
+  if (ws_bytes < kv4_attn_workspace_bytes(r)) return SKV_ERR_WORKSPACE_TOO_SMALL;
+  if (!ws || !aligned16(ws)) return SKV_ERR_INVALID_ARGUMENT;
+  return launch_kv4_attn(r, q, idx ? head_view(*p, pool) : view(pool), group, idx, out, lse, ws, dev_status,
+                         (cudaStream_t)stream);
+}
+
+skv_status skv_decode_step_kv4(const skv_problem* p, const void* q, const void* q_score, const skv_kv_pool* pool,
+                               int32_t group, float* scores, int32_t* idx, void* out, float* lse, void* ws,
+                               size_t ws_bytes, int32_t* dev_status, void* stream) {
+  SKV_TRY(check_kv4(p, pool, group, dev_status));
+  const void* qs = q_score ? q_score : q;
+  if (!q || !scores || !idx || !out || !aligned16(q) || !aligned16(qs) || !aligned16(scores) || !aligned4(idx) ||
+      !aligned16(out) || !aligned4(lse))
+    return SKV_ERR_INVALID_ARGUMENT;
+  if (!q_score && p->n_idx_q_heads != p->n_q_heads) return SKV_ERR_INVALID_ARGUMENT;
+  if (p->dtype != SKV_DTYPE_BF16) return SKV_ERR_UNSUPPORTED;
+  const skv_problem r = head_rows(*p);
+  if (ws_bytes < kv4_bytes(r)) return SKV_ERR_WORKSPACE_TOO_SMALL;
+  if (!ws || !aligned16(ws)) return SKV_ERR_INVALID_ARGUMENT;
+  cudaStream_t st = (cudaStream_t)stream;
+  SKV_TRY(launch_kv4_score(*p, qs, view(pool), group, scores, dev_status, st));
+  SKV_TRY(launch_topk(r, scores, idx, ws, dev_status, st));
+  return launch_kv4_attn(r, q, head_view(*p, pool), group, idx, out, lse, ws, dev_status, st);
 }
 
 const char* skv_status_string(skv_status s) {

@@ -522,9 +522,24 @@ skv_status launch_cache_update(const skv_problem& p, const PoolView& pool, const
 
 // new tokens: norm, rotation and the append to the pool (tokens.cu).  pool.table == nullptr:
 // no append, the keys go to k_out.  cached: rows that go to GPU slots also go to the host rows
-// that back them.
+// that back them.  group > 0: the pool is in 4 bits (kv4.cuh), rows coded in groups of that many.
 skv_status launch_token_rows(const skv_problem& p, const skv_rotary& r, const skv_tokens& t, const PoolView& pool,
-                             void* q_out, void* k_out, int32_t* status, cudaStream_t st, bool cached = false);
+                             void* q_out, void* k_out, int32_t* status, cudaStream_t st, bool cached = false,
+                             int group = 0);
+
+// block tables from request lengths (tables.cu)
+int tables_max_batch();
+skv_status launch_update_tables(const skv_tables& t, const int32_t* n_new, int n_tokens, int32_t* positions,
+                                int32_t* requests, int64_t* slots, int32_t* status, cudaStream_t st);
+
+// a cache in 4 bits (kv4.cu)
+size_t kv4_attn_workspace_bytes(const skv_problem& p);
+skv_status launch_kv4_attn(const skv_problem& p, const void* q, const PoolView& pool, int group, const int32_t* idx,
+                           void* out, float* lse, void* ws, int32_t* status, cudaStream_t st);
+skv_status launch_kv4_score(const skv_problem& p, const void* q, const PoolView& pool, int group, float* scores,
+                            int32_t* status, cudaStream_t st);
+skv_status launch_kv4_gather(const skv_problem& p, const PoolView& pool, int group, const int32_t* idx, void* k_out,
+                             void* v_out, int32_t* status, cudaStream_t st);
 
 // attention over a shared prefix and every request's own tail (attn_prefix.cu)
 size_t prefix_workspace_bytes(const skv_problem& p, int prefix_len);

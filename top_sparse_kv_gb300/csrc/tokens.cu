@@ -15,7 +15,7 @@
 // row comes once a token: with g the weights an entry becomes f (x A + x' B), A = g cos,
 // B = -+ g' sin, x' its partner and f the row's 1 / rms.  Now 53.7 us, 5.6 TB/s, 0.83 of the
 // copy rate, at 66 % of the issue slots; 8 tokens are a launch, 3.6 us in a graph.
-#include "skv_internal.cuh"
+#include "kv4.cuh"
 
 namespace skv {
 namespace {
@@ -104,7 +104,9 @@ __device__ __forceinline__ Token token_of(const TokenArgs& a, int tok, bool repo
   return t;
 }
 
-// The pool rows of the token in KV head h's blocks: row addresses, null for a bad entry.
+// The pool rows of the token in KV head h's blocks: row addresses, null for a bad entry.  NG > 0
+// groups a row: of a pool in 4 bits, the addresses of the cells that hold them.
+template <int NG = 0>
 __device__ __forceinline__ void pool_rows(const TokenArgs& a, const Token& t, int h, int elem, unsigned char** k,
                                           unsigned char** v) {
   *k = *v = nullptr;
@@ -120,8 +122,9 @@ __device__ __forceinline__ void pool_rows(const TokenArgs& a, const Token& t, in
     flag(a.status, SKV_DEV_BAD_SLOT);
     return;
   }
-  *k = (unsigned char*)(gpu ? a.pool.gpu_k : a.pool.host_k) + row * a.d * elem;
-  if (a.v) *v = (unsigned char*)(gpu ? a.pool.gpu_v : a.pool.host_v) + row * a.dv * elem;
+  const size_t at = NG ? row / kCellTokens * kv4_cell(NG) : row * a.d * elem;
+  *k = (unsigned char*)(gpu ? a.pool.gpu_k : a.pool.host_k) + at;
+  if (a.v) *v = (unsigned char*)(gpu ? a.pool.gpu_v : a.pool.host_v) + (NG ? at : row * a.dv * elem);
 }
 
 // Where row r of the token (queries, keys, values in order) comes from and goes to (null: nowhere).
@@ -131,7 +134,7 @@ __device__ __forceinline__ const unsigned char* row_from(const TokenArgs& a, int
   if (r < nq + nk) return a.k + tok * a.ks + (size_t)(r - nq) * a.d * ELEM;
   return a.v + tok * a.vs + (size_t)(r - nq - nk) * a.dv * ELEM;
 }
-template <int ELEM>
+template <int ELEM, int NG = 0>
 __device__ __forceinline__ unsigned char* row_to(const TokenArgs& a, const Token& t, int tok, int r, int nq, int nk) {
   if (r < nq) return a.q_out + tok * a.qos + (size_t)r * a.d * ELEM;
   const bool is_v = r >= nq + nk;
@@ -139,7 +142,7 @@ __device__ __forceinline__ unsigned char* row_to(const TokenArgs& a, const Token
   if (a.pool.table == nullptr) return a.k_out + tok * a.kos + (size_t)h * a.d * ELEM;
   if (a.pool.per_head) {
     unsigned char *k, *v;
-    pool_rows(a, t, h, ELEM, &k, &v);
+    pool_rows<NG>(a, t, h, ELEM, &k, &v);
     return is_v ? v : k;
   }
   unsigned char* base = is_v ? t.v : t.k;
@@ -147,12 +150,12 @@ __device__ __forceinline__ unsigned char* row_to(const TokenArgs& a, const Token
 }
 
 // One shared table entry serves every head: looked up once a token.
-template <int ELEM>
+template <int ELEM, int NG = 0>
 __device__ __forceinline__ void find_pool_rows(const TokenArgs& a, Token& t) {
   if (a.pool.table == nullptr || a.pool.per_head) return;
-  pool_rows(a, t, 0, ELEM, &t.k, &t.v);
-  t.k_head = (size_t)a.bs * a.d * ELEM;
-  t.v_head = (size_t)a.bs * a.dv * ELEM;
+  pool_rows<NG>(a, t, 0, ELEM, &t.k, &t.v);
+  t.k_head = NG ? (size_t)(a.bs / kCellTokens) * kv4_cell(NG) : (size_t)a.bs * a.d * ELEM;
+  t.v_head = NG ? t.k_head : (size_t)a.bs * a.dv * ELEM;
 }
 
 template <typename T>
@@ -162,6 +165,43 @@ __device__ __forceinline__ uint4 narrow(const float* x) {  // the one rounding
 #pragma unroll
   for (int j = 0; j < VE; ++j) out[j] = from_float<T>(x[j]);
   return *reinterpret_cast<uint4*>(out);
+}
+
+// A row of 128 entries into its cell, VE = 128 / LPR of them a lane.  The lane's bytes are its
+// entries' pairs in order; the cell wants byte 8 i + u at 8 u + i, so lanes exchange bytes until
+// each holds neighbours of one u: lanes whose i differs in a bit give each other the bytes whose u
+// differs in the same bit.  Every lane of the row's LPR takes part; cell null: nothing is written.
+template <int VE, int LPR, int NG>
+__device__ __forceinline__ void put_row4(const float (&x)[VE], unsigned char* cell, int rc, int sub) {
+  constexpr int kLanes = LPR / NG;  // of a group
+  float lo = x[0], hi = x[0], s, z;
+#pragma unroll
+  for (int j = 1; j < VE; ++j) lo = min_nan(lo, x[j]), hi = max_nan(hi, x[j]);
+#pragma unroll
+  for (int off = 1; off < kLanes; off <<= 1) {
+    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+  }
+  const uint32_t word = kv4_word(lo, hi, &s, &z);
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < VE; ++j) w |= kv4_code(x[j], s, z) << (4 * j);
+  if constexpr (VE == 8) {  // sub: u's bit 2, i's bits 0, 1, 2; the word: u's bits 0, 1
+    uint32_t y = __shfl_xor_sync(0xffffffffu, w, 2);
+    w = __byte_perm(w, y, sub & 2 ? 0x3715 : 0x6240);
+    y = __shfl_xor_sync(0xffffffffu, w, 4);
+    w = __byte_perm(w, y, sub & 4 ? 0x3276 : 0x5410);
+    const int u = (sub & 1) * 4 + (sub >> 2 & 1) * 2 + (sub >> 1 & 1);
+    if (cell != nullptr) *reinterpret_cast<uint32_t*>(cell + rc * kCodeBytes + 8 * u + 4 * (sub >> 3)) = w;
+  } else {  // sub: u's bits 1, 2, i's bits 0, 1, 2; the half word: u's bit 0
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, w, 4);
+    w = __byte_perm(w, y, sub & 4 ? 0x15 : 0x40);
+    const int u = (sub & 3) * 2 + (sub >> 2 & 1);
+    if (cell != nullptr)
+      *reinterpret_cast<uint16_t*>(cell + rc * kCodeBytes + 8 * u + 4 * (sub >> 4) + 2 * (sub >> 3 & 1)) = (uint16_t)w;
+  }
+  if (cell != nullptr && sub % kLanes == 0)
+    reinterpret_cast<uint32_t*>(cell + kCellTokens * kCodeBytes)[rc * NG + sub / kLanes] = word;
 }
 
 // Rows of at most LPR vectors: LPR lanes a row (a vector a lane), a token's rows staged in
@@ -195,8 +235,9 @@ constexpr int kTokSmemMax = kInfoBytes + kTokStages * (kInfoBytes + 4096 + kTokS
 static_assert(sizeof(StageInfo) <= kInfoBytes && sizeof(TokenBars) <= kInfoBytes, "");
 
 // PAIR: partners are neighbours of the same vector, else `half` entries away.  PART: the norm
-// covers a part of the row (as a test at run time it costs 5 % of every other call).
-template <typename T, int LPR, bool PAIR, bool PART>
+// covers a part of the row (as a test at run time it costs 5 % of every other call).  NG > 0: K and V
+// rows go into a pool in 4 bits, NG groups a row.
+template <typename T, int LPR, bool PAIR, bool PART, int NG>
 __global__ void __launch_bounds__(32 * kRowWarps<LPR> + 32, kTokCtas<LPR>) token_rows_kernel(const TokenArgs a) {
   constexpr int W = kRowWarps<LPR>;
   constexpr int VE = Vec<T>::N, RPW = 32 / LPR, ELEM = sizeof(T);
@@ -283,7 +324,7 @@ __global__ void __launch_bounds__(32 * kRowWarps<LPR> + 32, kTokCtas<LPR>) token
       }
       Token t = token_of(a, tok, lane == 0 && r0 == 0);
       if (t.live) {
-        find_pool_rows<ELEM>(a, t);
+        find_pool_rows<ELEM, NG>(a, t);
 #pragma unroll
         for (int u = 0; u < kAngles; ++u)
           if (lane + 32 * u < half) {
@@ -385,8 +426,10 @@ __global__ void __launch_bounds__(32 * kRowWarps<LPR> + 32, kTokCtas<LPR>) token
             o[j] *= inv;
           }
           unsigned char* dst = q_to;
-          if (k) dst = on ? row_to<ELEM>(a, f.t, f.tok, r, nq, nk) : nullptr;
-          if (on && dst != nullptr) *reinterpret_cast<uint4*>(dst + e0 * ELEM) = narrow<T>(o);
+          if (k) dst = on ? row_to<ELEM, NG>(a, f.t, f.tok, r, nq, nk) : nullptr;
+          if (NG > 0 && k)
+            put_row4<VE, LPR, NG ? NG : 1>(o, dst, f.t.pos % kCellTokens, sub);
+          else if (on && dst != nullptr) *reinterpret_cast<uint4*>(dst + e0 * ELEM) = narrow<T>(o);
           src += W * RPW * rowb;
           q_to += W * RPW * rowb;
         }
@@ -394,13 +437,23 @@ __global__ void __launch_bounds__(32 * kRowWarps<LPR> + 32, kTokCtas<LPR>) token
       if (r1 > nq + nk) {  // values: as they are
         const int v0 = r0 > nq + nk ? r0 : nq + nk;
         const unsigned char* from = data + (r0 < nq + nk ? (nq + nk - r0) * rowb : 0);
-        for (int r = r0 + warp * RPW + mine; r < r1; r += W * RPW)
-          if (r >= v0 && e0 < a.dv) {
-            unsigned char* dst = row_to<ELEM>(a, f.t, f.tok, r, nq, nk);
-            if (dst != nullptr)
-              *reinterpret_cast<uint4*>(dst + e0 * ELEM) =
-                  *reinterpret_cast<const uint4*>(from + (r - v0) * vrowb + e0 * ELEM);
+        if constexpr (NG > 0) {
+          for (int rb = r0 + warp * RPW; rb < r1; rb += W * RPW) {
+            const int r = rb + mine;
+            const bool on = r >= v0 && r < r1;
+            float x[VE];
+            Vec<T>::widen(on ? *reinterpret_cast<const uint4*>(from + (r - v0) * vrowb + e0 * ELEM) : make_uint4(0, 0, 0, 0), x);
+            put_row4<VE, LPR, NG>(x, on ? row_to<ELEM, NG>(a, f.t, f.tok, r, nq, nk) : nullptr, f.t.pos % kCellTokens, sub);
           }
+        } else {
+          for (int r = r0 + warp * RPW + mine; r < r1; r += W * RPW)
+            if (r >= v0 && e0 < a.dv) {
+              unsigned char* dst = row_to<ELEM>(a, f.t, f.tok, r, nq, nk);
+              if (dst != nullptr)
+                *reinterpret_cast<uint4*>(dst + e0 * ELEM) =
+                    *reinterpret_cast<const uint4*>(from + (r - v0) * vrowb + e0 * ELEM);
+            }
+        }
       }
     }
     __syncwarp();
@@ -575,7 +628,7 @@ int parts_of(const TokenArgs& a, int per) {
   return (int)(want < most ? want : most);
 }
 
-template <typename T, int LPR>
+template <typename T, int LPR, int NG = 0>
 skv_status launch_short(TokenArgs& a, cudaStream_t st) {
   const int rows = rows_of(a), wide = (a.v != nullptr && a.dv > a.d ? a.dv : a.d) * (int)sizeof(T);
   const int most = kTokStageMax / wide;  // rows a stage
@@ -585,8 +638,8 @@ skv_status launch_short(TokenArgs& a, cudaStream_t st) {
   const int smem = kInfoBytes + kTokStages * (kInfoBytes + 16 * a.d + a.stage);
   const bool part = a.norm_dim < a.d && (a.gq != nullptr || a.gk != nullptr);
   const auto kernel = a.style == SKV_ROPE_PAIR
-                          ? (part ? token_rows_kernel<T, LPR, true, true> : token_rows_kernel<T, LPR, true, false>)
-                          : (part ? token_rows_kernel<T, LPR, false, true> : token_rows_kernel<T, LPR, false, false>);
+                          ? (part ? token_rows_kernel<T, LPR, true, true, NG> : token_rows_kernel<T, LPR, true, false, NG>)
+                          : (part ? token_rows_kernel<T, LPR, false, true, NG> : token_rows_kernel<T, LPR, false, false, NG>);
   const skv_status prep = prepare_kernel((const void*)kernel, kTokSmemMax);
   if (prep != SKV_OK) return prep;
   constexpr int kTurns = 8 * LPR * Vec<T>::N / 2;  // static shared memory
@@ -632,7 +685,7 @@ skv_status launch_rows(TokenArgs& a, bool f32, cudaStream_t st) {
 }  // namespace
 
 skv_status launch_token_rows(const skv_problem& p, const skv_rotary& r, const skv_tokens& t, const PoolView& pool,
-                             void* q_out, void* k_out, int32_t* status, cudaStream_t st, bool cached) {
+                             void* q_out, void* k_out, int32_t* status, cudaStream_t st, bool cached, int group) {
   const int e = p.dtype == SKV_DTYPE_F32 ? 4 : 2;
   TokenArgs a;
   a.q = (const unsigned char*)t.q;
@@ -669,7 +722,15 @@ skv_status launch_token_rows(const skv_problem& p, const skv_rotary& r, const sk
   a.status = status;
   a.parts = 1;
   a.stage = 0;
-  const skv_status rows = launch_rows(a, p.dtype == SKV_DTYPE_F32, st);
+  const bool f32 = p.dtype == SKV_DTYPE_F32;
+  if (group > 0) {  // (rows of 128)
+    if (f32)
+      return group == 32 ? launch_short<float, 32, 4>(a, st)
+                         : group == 64 ? launch_short<float, 32, 2>(a, st) : launch_short<float, 32, 1>(a, st);
+    return group == 32 ? launch_short<__nv_bfloat16, 16, 4>(a, st)
+                       : group == 64 ? launch_short<__nv_bfloat16, 16, 2>(a, st) : launch_short<__nv_bfloat16, 16, 1>(a, st);
+  }
+  const skv_status rows = launch_rows(a, f32, st);
   return rows == SKV_OK && cached ? launch_backing(a, e, st) : rows;
 }
 

@@ -191,22 +191,25 @@ class TokenStep:
     writes keys and values to the pool.  The problem, the rotary parameters and the pool are
     marshalled once, here; every call marshals only its tokens.  Status bits add up in `status`.
     Other tensors in their places need a new step; the marshalled ones live as long as this one.
-    Appends to a pool with a slot cache (`pool.cached`) keep the host rows behind its slots current."""
+    Appends to a pool with a slot cache (`pool.cached`) keep the host rows behind its slots current;
+    those to a Kv4Pool write 4 bits."""
 
     def __init__(self, problem: B.Problem, rotary: B.Rotary, pool: Optional[B.Pool] = None):
         rotary.check(problem)
         if pool is not None:
             B.check_pool(problem, pool)
+        self._kv4 = (pool.group,) if isinstance(pool, B.Kv4Pool) else ()
         self.p, self.rotary, self.pool = problem, rotary, pool
         dev = problem.seq_lens.device
         self.status = torch.zeros((1,), dtype=torch.int32, device=dev)
         self._held = [*vars(problem).values(), *vars(rotary).values(), *(vars(pool).values() if pool else ())]
         self._p, self._r = ctypes.byref(problem.c()), ctypes.byref(rotary.c())
-        self._pool = None if pool is None else ctypes.byref(pool.c())
+        self._pool = None if pool is None else ctypes.byref(pool.c4() if self._kv4 else pool.c())
         self._st = self.status.data_ptr()
         self._dtype = B.element_type(problem)
         self._norm_rope = B.lib().skv_qk_norm_rope
-        self._append, self._append_cached = B.lib().skv_append_kv, B.lib().skv_append_kv_cached
+        self._append = B.lib().skv_append_kv4 if self._kv4 else B.lib().skv_append_kv
+        self._append_cached = B.lib().skv_append_kv_cached
         self._device = problem.seq_lens.get_device()
         self._seen = None  # the token layout that has been checked
 
@@ -257,9 +260,10 @@ class TokenStep:
         if q_out is None and q is not None:
             q_out = self._new(q, self.p.n_q_heads, stream)
         ct, qo, _ = self._tokens(q, k, v, positions, requests, q_out, None)
-        st = call(self._p, self._r, ctypes.byref(ct), self._pool, qo, self._st, B.raw_stream(self._device, stream))
+        st = call(self._p, self._r, ctypes.byref(ct), self._pool, *self._kv4, qo, self._st,
+                  B.raw_stream(self._device, stream))
         if st:
-            raise B.SkvError("skv_append_kv_cached" if self.pool.cached else "skv_append_kv", st)
+            raise B.SkvError(call.__name__, st)
         return q_out
 
 
@@ -296,3 +300,159 @@ class PrefixStep:
         if st:
             raise B.SkvError("skv_prefix_attn", st)
         return self.out, self.lse
+
+
+class Kv4Step:
+    """Decode over a pool in 4 bits: `score()`, `topk()`, `attend()` over a selection, `attend_all()`
+    over whole histories, `gather()` of the attended rows' values, and `run()`, one
+    skv_decode_step_kv4.  Owns scores, idx, out, lse, workspace and status; problem and pool are
+    marshalled once, here, and live as long as the step."""
+
+    def __init__(self, problem: B.Problem, pool: B.Kv4Pool):
+        B.check_pool4(problem, pool)
+        self.p, self.pool = problem, pool
+        p, dev = problem, problem.seq_lens.device
+        self._device = p.seq_lens.get_device()
+        self._held = [*vars(problem).values(), *vars(pool).values()]
+        self._p, self._pool, self._group = ctypes.byref(p.c()), ctypes.byref(pool.c4()), pool.group
+        heads = B.list_heads(p)
+        self._shapes = dict(q=(p.batch, p.n_q_heads, 128), q_score=(p.batch, p.n_idx_q_heads or p.n_q_heads, 128),
+                            scores=(p.batch, heads, p.max_len), idx=(p.batch, heads, p.topk))
+        self._rows = (p.batch, heads, p.n_sink + p.topk + p.n_local, 128)
+        self.status = torch.zeros((1,), dtype=torch.int32, device=dev)
+        self.ws = torch.empty((max(B.skv_kv4_workspace_size(p), 16),), dtype=torch.uint8, device=dev)
+        self.out = torch.empty(self._shapes["q"], dtype=torch.bfloat16, device=dev)
+        self.lse = torch.empty(self._shapes["q"][:2], dtype=torch.float32, device=dev)
+        self._st, self._ws = self.status.data_ptr(), (self.ws.data_ptr(), self.ws.numel())
+        self._outs = (self.out.data_ptr(), self.lse.data_ptr())
+        self._scores = self._idx = None
+
+    @property
+    def scores(self) -> torch.Tensor:
+        """[batch, heads, max_len]; made when first used."""
+        if self._scores is None:
+            self._scores = torch.empty(self._shapes["scores"], dtype=torch.float32, device=self.p.seq_lens.device)
+        return self._scores
+
+    @property
+    def idx(self) -> torch.Tensor:
+        """[batch, heads, topk]; made when first used."""
+        if self._idx is None:
+            self._idx = torch.empty(self._shapes["idx"], dtype=torch.int32, device=self.p.seq_lens.device)
+        return self._idx
+
+    def _ptr(self, name, t, dtype):
+        shape = self._shapes[name]
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != self._device:
+            raise ValueError(f"{name}: contiguous {dtype} {list(shape)} on {self.p.seq_lens.device} expected")
+        return B.list_ptr(self.p, t)
+
+    def _go(self, name, *args, stream):
+        st = getattr(B.lib(), name)(self._p, *args, self._st, B.raw_stream(self._device, stream))
+        if st:
+            raise B.SkvError(name, st)
+
+    def score(self, q_score, scores=None, stream=None):
+        """Scores of the candidates into `scores` (the step's own unless given), which it returns."""
+        scores = self.scores if scores is None else scores
+        self._go("skv_score_kv4", self._ptr("q_score", q_score, torch.bfloat16), self._pool, self._group,
+                 self._ptr("scores", scores, torch.float32), stream=stream)
+        return scores
+
+    def topk(self, stream=None):
+        """The selection of the step's own scores, into idx."""
+        if self.p.topk == 0:
+            return self.idx
+        B.skv_topk(self.p, self.scores, self.idx, self.ws, self.status, stream)
+        return self.idx
+
+    def _attend(self, q, idx, stream):
+        self._go("skv_attn_kv4", self._ptr("q", q, torch.bfloat16), self._pool, self._group,
+                 None if idx is None else self._ptr("idx", idx, torch.int32), *self._outs, *self._ws, stream=stream)
+        return self.out, self.lse
+
+    def attend(self, q, idx=None, stream=None):
+        """(out, lse) over sink, selection (the step's own idx unless given) and window."""
+        return self._attend(q, self.idx if idx is None else idx, stream)
+
+    def attend_all(self, q, stream=None):
+        """(out, lse) over every position of each history."""
+        return self._attend(q, None, stream)
+
+    def run(self, q, q_score=None, stream=None):
+        """(out, lse) of one decode step; scores and idx hold its scores and selection."""
+        self._go("skv_decode_step_kv4", self._ptr("q", q, torch.bfloat16),
+                 None if q_score is None else self._ptr("q_score", q_score, torch.bfloat16), self._pool, self._group,
+                 self._ptr("scores", self.scores, torch.float32), self._ptr("idx", self.idx, torch.int32), *self._outs,
+                 *self._ws, stream=stream)
+        return self.out, self.lse
+
+    def gather(self, idx=None, k_out=None, v_out=None, stream=None):
+        """(k, v) [batch, heads, n_att, 128] of the problem's type: the attended rows' values; new tensors
+        unless given.  Without a selection (topk 0) those of sink and window."""
+        if idx is None and self.p.topk > 0:
+            idx = self.idx
+        new = [t if t is not None else self._new(stream) for t in (k_out, v_out)]
+        for name, t in zip(("k_out", "v_out"), new):
+            B.dense(self.p, name, t, B.element_type(self.p), self._rows)
+        self._go("skv_gather_kv4", self._pool, self._group,
+                 None if idx is None else self._ptr("idx", idx, torch.int32), new[0].data_ptr(), new[1].data_ptr(),
+                 stream=stream)
+        return tuple(new)
+
+    def _new(self, stream):
+        """An output, of the allocator's pool of the stream that writes it."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self._new(None)
+        return torch.empty(self._rows, dtype=B.element_type(self.p), device=self.p.seq_lens.device)
+
+
+class BlockTables:
+    """Slot table, lengths and free blocks of a batch, kept on the GPU: `update(n_new, n_tokens)` is one
+    skv_update_tables, whose positions and requests TokenStep.append() takes.  `free_blocks`: the
+    stack's room, its first n_free entries (all, unless given) the free blocks, the last the first
+    to be given.  The problem's seq_lens and the table are updated in place."""
+
+    def __init__(self, problem: B.Problem, slot_table: torch.Tensor, free_blocks: torch.Tensor,
+                 n_free: Optional[int] = None, base: int = 0):
+        dev = problem.seq_lens.device
+        n_free = free_blocks.numel() if n_free is None else n_free
+        if not 0 <= n_free <= free_blocks.numel():
+            raise ValueError("n_free: at most the stack's room")
+        self.state = torch.tensor([n_free, 0, 0, 0], dtype=torch.int32).to(dev)
+        self.p, self.tables = problem, B.Tables(slot_table, free_blocks, self.state, base)
+        self.tables.check(problem)
+        self.status = torch.zeros((1,), dtype=torch.int32, device=dev)
+        self._held = [*vars(problem).values(), *vars(self.tables).values()]
+        self._device = problem.seq_lens.get_device()
+        self._t, self._st = ctypes.byref(self.tables.c(problem)), self.status.data_ptr()
+        self._call = B.lib().skv_update_tables
+
+    @property
+    def n_free(self) -> torch.Tensor:
+        """Blocks on the stack, int32 [1] on the GPU."""
+        return self.state[:1]
+
+    def _new(self, n, stream):
+        """Outputs, of the allocator's pool of the stream that writes them."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self._new(n, None)
+        dev = self.p.seq_lens.device
+        return (torch.empty((n,), dtype=torch.int32, device=dev), torch.empty((n,), dtype=torch.int32, device=dev),
+                torch.empty((n,), dtype=torch.int64, device=dev))
+
+    def update(self, n_new, n_tokens: int = 0, out=None, stream=None):
+        """(positions, requests, slots) of the step's n_tokens rows: new tensors, unless given as `out`
+        (slots may be None there)."""
+        rows = self._new(n_tokens, stream) if out is None else out
+        B.dense(self.p, "n_new", n_new, torch.int32, (self.p.batch,))
+        if out is not None:
+            for name, t, dtype in zip(("positions", "requests", "slots"), out, (torch.int32, torch.int32, torch.int64)):
+                B.dense(self.p, name, t, dtype, (n_tokens,))
+        st = self._call(self._t, n_new.data_ptr(), n_tokens, *(None if t is None else t.data_ptr() for t in rows),
+                        self._st, B.raw_stream(self._device, stream))
+        if st:
+            raise B.SkvError("skv_update_tables", st)
+        return rows
