@@ -859,6 +859,10 @@ static skv_status check_kv4(const skv_problem* p, const skv_kv_pool* pool, int32
   if (!aligned4(p->seq_lens) || !aligned4(pool->slot_table) || !aligned4(dev_status)) return SKV_ERR_INVALID_ARGUMENT;
   SKV_TRY(check_kv4_problem(p));
   if (!pool->gpu_v) return SKV_ERR_UNSUPPORTED;  // latent rows
+  // a row's number stays in 31 bits (2^31 rows of K and V are more than a GPU holds)
+  const long long most = (1LL << 31) / p->block_size / p->n_kv_heads;
+  if (pool->n_gpu_blocks >= (pool->table_heads ? (1LL << 31) / p->block_size : most) || pool->n_host_blocks >= most)
+    return SKV_ERR_UNSUPPORTED;
   return SKV_OK;
 }
 

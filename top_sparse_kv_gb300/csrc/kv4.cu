@@ -10,12 +10,12 @@
 // masked out of its word is, as fp16, the subnormal c 2^-24 (from the low half of a byte) or
 // c 2^-20 (from the high half), exactly, so an operand register of two codes costs one AND, and
 // the powers of two go to the other operand (queries) or the result's rows (values).
-//   logit   sum_g s_g (sum_j q_j c_j) + sum_g (z_g - 8 s_g) sum_{j in g} q_j
-// The first term is a product per group, scaled in fp32; the second a product of the words
+//   logit   sum_g s_g (sum_j q_j c_j - 8 sum_j q_j) + sum_g z_g sum_{j in g} q_j
+// The first product comes per group, scaled in fp32; what is left is a product of the words
 // themselves -- a word is a pair of bf16 -- with the queries' group sums in three bf16 parts.
 // Queries go to fp16 under a power of two of their own: bf16's 8 bits fit, and what falls under
 // fp16's range is 2^-35 of the head's largest.
-//   out     sum_t w_tg c + sum_t p_t (z_tg - 8 s_tg),  w_tg = p_t s_tg in fp16
+//   out     sum_t w_tg (c - 8) + sum_t p_t z_tg,  w_tg = p_t s_tg in fp16
 // The maximum is a running one that moves only when a logit passes it by 2^7 (then everything
 // is rescaled), and so is the power of two above the steps.
 #include "attn_common.cuh"
@@ -35,6 +35,8 @@ struct Kv4Args {
   const int32_t* seq_lens;
   int B, H, Hq, G, heads;  // H: rows of the kernel a request; heads: the pool's
   int max_len, ns, nl, k, bs;
+  int cells, shift;        // of a block: its cells; log2 of its tokens, or -1
+  unsigned n_gpu, n_host;  // blocks there (0 without a host pool)
   int agg, Gi;             // scores
   float scale_log2;
   int32_t* status;
@@ -152,8 +154,6 @@ __device__ __forceinline__ void find_share(const Kv4Args& a, int min_tiles, long
 // another order and with their 16-byte chunks exchanged in pairs, so that the 8-byte loads of
 // the second product meet no bank twice; the loads of K's rows are consecutive as they are.
 
-constexpr long long kHostTile = 1LL << 62;
-
 __device__ __forceinline__ int v_place(int r) { return (r & 8) | ((r & 7) >> 1) | ((r & 1) << 2); }
 __device__ __forceinline__ int v_chunk(int place, int c) { return c ^ (place & 2); }
 
@@ -169,12 +169,11 @@ __device__ __forceinline__ void cp_async_cg16(uint32_t dst, const void* src) {
 // iteration, so that each step's load has a tile's time to arrive.
 struct Row {
   int t;            // position, as found (a selected one unchecked); -1: none
-  int e;            // its table entry
+  int e, block;     // its table entry, that one's index
   int b, h, L;
   bool listed;      // from the selection: to be checked
 };
 
-template <int MODE>
 __device__ __forceinline__ void row_position(const Kv4Args& a, const Cursor& c, bool on, int r, Row& w) {
   w.b = c.b;
   w.h = c.h;
@@ -183,16 +182,7 @@ __device__ __forceinline__ void row_position(const Kv4Args& a, const Cursor& c, 
   w.listed = false;
   if (!on) return;
   const int j = (c.tile << 4) + r;
-  if (MODE == kDense) {
-    w.t = j < c.L ? j : -1;
-    return;
-  }
   const Regions g = regions_of(c.L, a.ns, a.nl);
-  if (MODE == kScore) {
-    const int t = (g.s_end & ~15) + j;
-    w.t = t >= g.s_end && t < g.l_start ? t : -1;
-    return;
-  }
   if (j < g.s_end) {
     w.t = j;
   } else if (j < g.s_end + a.k) {
@@ -204,9 +194,8 @@ __device__ __forceinline__ void row_position(const Kv4Args& a, const Cursor& c, 
   }
 }
 
-template <int MODE>
 __device__ __forceinline__ void row_entry(const Kv4Args& a, bool reports, Row& w) {
-  if (MODE == kList && w.listed && w.t >= 0) {
+  if (w.listed && w.t >= 0) {
     const Regions g = regions_of(w.L, a.ns, a.nl);
     if (w.t < g.s_end || w.t >= g.l_start) {
       if (reports) flag(a.status, SKV_DEV_BAD_INDEX);
@@ -214,107 +203,169 @@ __device__ __forceinline__ void row_entry(const Kv4Args& a, bool reports, Row& w
     }
   }
   w.e = 0;
-  if (w.t >= 0) w.e = __ldg(table_row(a.pool, w.b, w.h / a.pool.hdiv, a.heads) + w.t / a.bs);
-}
-
-// The row's cell as a byte offset, its place in the cell in the low bits, kHostTile; -1: none.
-template <int NG>
-__device__ __forceinline__ long long row_address(const Kv4Args& a, bool reports, const Row& w) {
-  if (w.t < 0) return -1;
-  const int ph = w.h / a.pool.hdiv;
-  const long long e = w.e;
-  long long block;
-  bool host = false;
-  if (e >= 0 && e < a.pool.n_gpu) {
-    block = a.pool.per_head ? e : e * a.heads + ph;
-  } else if (e < 0 && a.pool.host_k != nullptr && -e - 1 < a.pool.n_host) {
-    block = (-e - 1) * a.heads + ph;
-    host = true;
-  } else {
-    if (reports) flag(a.status, SKV_DEV_BAD_SLOT);
-    return -1;
+  if (w.t >= 0) {
+    w.block = a.shift >= 0 ? w.t >> a.shift : w.t / a.bs;
+    w.e = __ldg(table_row(a.pool, w.b, a.pool.hdiv == 1 ? w.h : w.h / a.pool.hdiv, a.heads) + w.block);
   }
-  const long long cell = block * (a.bs >> 4) + ((w.t % a.bs) >> 4);
-  return cell * kv4_cell(NG) | (w.t & 15) | (host ? kHostTile : 0);
 }
 
-// Copies of a tile, a commit group of its own; the mask of its rows that are there goes to *mask.
-template <int NG, bool V>
-__device__ __forceinline__ void fetch(const Kv4Args& a, uint32_t stage, volatile uint32_t* mask, long long at) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t live = __ballot_sync(0xffffffffu, at >= 0) & 0xffffu;
-  if (lane == 0) *mask = live;
-  if (live != 0) {
-    const bool host = at >= 0 && (at & kHostTile);
-    const unsigned char* kb = (const unsigned char*)(host ? a.pool.host_k : a.pool.gpu_k);
-    const unsigned char* vb = (const unsigned char*)(host ? a.pool.host_v : a.pool.gpu_v);
-    const long long cell = at & ~(kHostTile | 15);
-    const int rc = (int)(at & 15);
-    const unsigned long long kr = (unsigned long long)(kb + cell + rc * kCodeBytes);
-    const unsigned long long vr = (unsigned long long)(vb + cell + rc * kCodeBytes);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = (lane >> 2) + 8 * i, c = lane & 3;
-      const unsigned long long ks = __shfl_sync(0xffffffffu, kr, r);
-      const unsigned long long vs = V ? __shfl_sync(0xffffffffu, vr, r) : 0ull;
-      if (live >> r & 1u) {
-        cp_async_cg16(stage + r * kCodeBytes + c * 16, (const void*)(ks + c * 16));
-        if (V) {
-          const int p = v_place(r);
-          cp_async_cg16(stage + kv4_cell(NG) + p * kCodeBytes + v_chunk(p, c) * 16, (const void*)(vs + c * 16));
-        }
-      }
-    }
-    const int r = lane & 15;
-    if (at >= 0 && (V || lane < 16)) {
-      const uint32_t dst = stage + (V && lane >= 16 ? kv4_cell(NG) : 0) + 16 * kCodeBytes + r * 4 * NG;
-      const unsigned char* src = (V && lane >= 16 ? vb : kb) + cell + 16 * kCodeBytes + rc * 4 * NG;
-      if (NG == 4)
-        cp_async_cg16(dst, src);
-      else
-        cp_async_ca<4 * NG>(dst, src);
-    }
+// The row's number in its pool, bit 31: the host's (pools have fewer than 2^31 rows).
+constexpr uint32_t kNoRow = 0xffffffffu;
+__device__ __forceinline__ uint32_t row_id(const Kv4Args& a, bool reports, const Row& w) {
+  if (w.t < 0) return kNoRow;
+  const uint32_t ph = a.pool.hdiv == 1 ? w.h : w.h / a.pool.hdiv, off = w.t - w.block * a.bs;
+  if (w.e >= 0) {
+    if ((uint32_t)w.e < a.n_gpu) return (a.pool.per_head ? w.e : w.e * a.heads + ph) * a.bs + off;
+  } else if (~(uint32_t)w.e < a.n_host) {
+    return ((~(uint32_t)w.e * a.heads + ph) * a.bs + off) | 0x80000000u;
   }
-  cp_async_commit();
+  if (reports) flag(a.status, SKV_DEV_BAD_SLOT);
+  return kNoRow;
 }
 
-// A warp's way through its tiles: it issues S - 1 tiles ahead of the one it computes.
+// Where a lane's 16-byte chunk of V's codes goes: chunk `lane` of the first eight rows (of the
+// others 512 bytes on).
+__device__ __forceinline__ uint32_t v_chunk_at(int lane) {
+  const int p = v_place(lane >> 2);
+  return p * kCodeBytes + v_chunk(p, lane & 3) * 16;
+}
+
+// Feeders: a warp issues its tiles' copies S - 1 tiles ahead of the one it computes, a commit
+// group a tile.  issue() is called once a tile (before it is computed, and S - 1 times at
+// the start); live() then tells which rows of the tile to be computed are there.
+
+// Whole cells: a history's tiles.  The entry of a tile is loaded when the one before it is
+// issued, so it has a tile's time to arrive.
 template <int MODE, int NG, bool V, int S>
-struct Feeder {
+struct CellFeeder {
   static constexpr int kStage = (V ? 2 : 1) * kv4_cell(NG);
   const Kv4Args& a;
-  uint32_t ring;
-  volatile uint32_t* masks;
-  Cursor c;     // of the row whose position is found next
-  int left;     // tiles whose positions are yet to be found
-  Row r1, r0;   // position found; entry on its way
-  int issued;
+  uint32_t to, end;  // the stage that is filled next, the ring's end
+  uint32_t v_at;
+  Cursor c;  // the tile that is issued next
+  int left, first, e;
+  uint32_t bad;  // of the tiles issued, the last in bit 0: no such block
 
-  __device__ __forceinline__ Feeder(const Kv4Args& args, uint32_t ring_, volatile uint32_t* masks_, Cursor at, int n)
-      : a(args), ring(ring_), masks(masks_), c(at), left(n), issued(0) {
+  __device__ __forceinline__ CellFeeder(const Kv4Args& args, uint32_t ring, uint32_t*, Cursor at, int n)
+      : a(args), to(ring), end(ring + S * kStage), v_at(v_chunk_at(threadIdx.x & 31)), c(at), left(n), bad(0) {
+    if (left > 0) {
+      settle<MODE>(a, c);
+      load();
+    }
+  }
+  __device__ __forceinline__ void load() {
+    first = MODE == kScore ? regions_of(c.L, a.ns, a.nl).s_end >> 4 : 0;
+    const int cell = first + c.tile, block = a.cells == 1 ? cell : cell / a.cells;
+    e = __ldg(table_row(a.pool, c.b, c.h, a.heads) + block);
+  }
+  __device__ __forceinline__ void issue() {
+    const int lane = threadIdx.x & 31;
+    bad <<= 1;
+    if (left > 0) {
+      const bool host = e < 0;
+      const unsigned block = host ? ~e : e;
+      if (block < (host ? a.n_host : a.n_gpu)) {
+        const long long unit = (long long)block * (a.pool.per_head && !host ? 1 : a.heads) +
+                               (a.pool.per_head && !host ? 0 : c.h);
+        long long cell = unit;
+        if (a.cells != 1) cell = unit * a.cells + (first + c.tile) % a.cells;
+        const long long at = cell * kv4_cell(NG) + lane * 16;
+        const unsigned char* k = (const unsigned char*)(host ? a.pool.host_k : a.pool.gpu_k) + at;
+        const uint32_t dst = to + lane * 16;
+        cp_async_cg16(dst, k);
+        cp_async_cg16(dst + 512, k + 512);
+        if (lane < 4 * NG) cp_async_cg16(dst + 1024, k + 1024);
+        if (V) {
+          const unsigned char* v = (const unsigned char*)(host ? a.pool.host_v : a.pool.gpu_v) + at;
+          cp_async_cg16(to + kv4_cell(NG) + v_at, v);
+          cp_async_cg16(to + kv4_cell(NG) + v_at + 512, v + 512);
+          if (lane < 4 * NG) cp_async_cg16(dst + kv4_cell(NG) + 1024, v + 1024);
+        }
+      } else {
+        if (lane == 0) flag(a.status, SKV_DEV_BAD_SLOT);
+        bad |= 1u;
+      }
+      if (--left > 0) {
+        c.tile += kW;
+        if (c.tile >= c.nt) settle<MODE>(a, c);
+        load();
+      }
+    }
+    cp_async_commit();
+    to = to + kStage == end ? end - S * kStage : to + kStage;
+  }
+  // tile `tile` of a request of L positions, S - 1 issues ago
+  __device__ __forceinline__ uint32_t live(int L, int tile, int) const {
+    if (bad >> (S - 1) & 1u) return 0u;
+    const int n = L - (tile << 4);
+    return n >= 16 ? 0xffffu : (1u << n) - 1u;
+  }
+};
+
+// Single rows: a list's tiles.  Lanes 0 .. 15 (and 16 .. 31 with them) find a row each, a step an
+// issue: its place's position, that one's entry, the row -- so each load has a tile's time to arrive.
+template <int MODE, int NG, bool V, int S>
+struct RowFeeder {
+  static constexpr int kStage = 2 * kv4_cell(NG);
+  const Kv4Args& a;
+  uint32_t to, end, v_at;
+  uint32_t* masks;
+  Cursor c;  // the tile whose positions are found next
+  int left, slot;
+  Row r1, r0;  // position on its way; entry on its way
+
+  __device__ __forceinline__ RowFeeder(const Kv4Args& args, uint32_t ring, uint32_t* masks_, Cursor at, int n)
+      : a(args), to(ring), end(ring + S * kStage), v_at(v_chunk_at(threadIdx.x & 31)), masks(masks_), c(at), left(n),
+        slot(0) {
     if (left > 0) settle<MODE>(a, c);
     position();
     advance();
   }
   __device__ __forceinline__ void position() {
-    row_position<MODE>(a, c, left > 0, threadIdx.x & 15, r1);
+    row_position(a, c, left > 0, threadIdx.x & 15, r1);
     if (--left > 0) {
       c.tile += kW;
-      settle<MODE>(a, c);
+      if (c.tile >= c.nt) settle<MODE>(a, c);
     }
   }
   __device__ __forceinline__ void advance() {
     r0 = r1;
-    row_entry<MODE>(a, (threadIdx.x & 31) < 16, r0);
+    row_entry(a, (threadIdx.x & 31) < 16, r0);
     position();
   }
   __device__ __forceinline__ void issue() {
-    const int s = issued % S;
-    const long long at = row_address<NG>(a, (threadIdx.x & 31) < 16, r0);
-    fetch<NG, V>(a, ring + s * kStage, masks + s, at);
-    ++issued;
+    const int lane = threadIdx.x & 31;
+    const uint32_t row = row_id(a, lane < 16, r0);
+    const uint32_t live = __ballot_sync(0xffffffffu, row != kNoRow) & 0xffffu;
+    if (lane == 0) masks[slot] = live;
+    auto at = [&](uint32_t r, bool v) {  // the row's cell
+      const unsigned char* base = (const unsigned char*)(r >> 31 ? (v ? a.pool.host_v : a.pool.host_k)
+                                                                 : (v ? a.pool.gpu_v : a.pool.gpu_k));
+      return base + (size_t)(r >> 4 & 0x7ffffffu) * kv4_cell(NG);
+    };
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t r = __shfl_sync(0xffffffffu, row, (lane >> 2) + 8 * i);
+      if (r != kNoRow) {
+        const int off = (int)(r & 15u) * kCodeBytes + (lane & 3) * 16;
+        cp_async_cg16(to + lane * 16 + 512 * i, at(r, false) + off);
+        cp_async_cg16(to + kv4_cell(NG) + v_at + 512 * i, at(r, true) + off);
+      }
+    }
+    if (row != kNoRow) {
+      const uint32_t dst = to + (lane >= 16 ? kv4_cell(NG) : 0) + 16 * kCodeBytes + (lane & 15) * 4 * NG;
+      const unsigned char* src = at(row, lane >= 16) + 16 * kCodeBytes + (row & 15u) * 4 * NG;
+      if (NG == 4)
+        cp_async_cg16(dst, src);
+      else
+        cp_async_ca<4 * NG>(dst, src);
+    }
+    cp_async_commit();
+    to = to + kStage == end ? end - S * kStage : to + kStage;
+    slot = slot == S - 1 ? 0 : slot + 1;
     advance();
   }
+  __device__ __forceinline__ uint32_t live(int, int, int stage) const { return masks[stage]; }
 };
 
 // ---------------------------------------------------------------------------- the products
@@ -363,12 +414,17 @@ __device__ __forceinline__ float centre_of(uint32_t w) { return __uint_as_float(
 
 // The four operand registers of two bytes' worth of codes, in the order low and high half of
 // the first byte, low and high half of the second: subnormal fp16 pairs, 2^-24 and 2^-20 a unit.
+// The upper one of a pair comes as 15 - c (the same instruction), and the other operand has its
+// sign turned there: u c + v c' as u c - v (15 - c') + 15 v.  Codes are 7.5 on average, and a
+// long sum of them all on one side of zero would lose to the tensor core's truncation what
+// the centring takes off again (a million keys: 1 % of the output); in pairs of either sign it
+// stays small.  With the codes' own 8, the first of a pair stands 8 too high, the second 7 too low.
 __device__ __forceinline__ void spread(uint32_t x, uint32_t* r) {
   const uint32_t y = x >> 8;
-  r[0] = x & 0x000f000fu;
-  r[1] = x & 0x00f000f0u;
-  r[2] = y & 0x000f000fu;
-  r[3] = y & 0x00f000f0u;
+  r[0] = (x & 0x000f000fu) ^ 0x000f0000u;
+  r[1] = (x & 0x00f000f0u) ^ 0x00f00000u;
+  r[2] = (y & 0x000f000fu) ^ 0x000f0000u;
+  r[3] = (y & 0x00f000f0u) ^ 0x00f00000u;
 }
 
 // A power of two that brings |x| <= mx under 2^10 (its own inverse is exact too).
@@ -387,32 +443,46 @@ struct QFrag {
   float unit[NT][2];  // what a logit of heads 2 t, 2 t + 1 comes in: 2^20 / their power of two
 };
 
-// the column's entries 16 j + 4 t .. + 3 for this lane are x[j][0..3], already under `scale`
-template <int NG>
-__device__ __forceinline__ void column(const float (&x)[8][4], uint32_t (&b)[8][2], uint32_t (&wz)[3], bool sums) {
-  const int t = threadIdx.x & 3;
-  float part[NG];
-#pragma unroll
-  for (int g = 0; g < NG; ++g) part[g] = 0.f;
+// the column's entries 16 j + 4 t .. + 3 for this lane are x[j][0..3], already under a power of
+// two; a register's pairs are entries 0 and 2, 1 and 3
+__device__ __forceinline__ void column(const float (&x)[8][4], uint32_t (&b)[8][2]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    b[j][0] = pack_f16(16.f * x[j][0], 16.f * x[j][2]);
-    b[j][1] = pack_f16(x[j][1], x[j][3]);
-    part[j * NG / 8] += (x[j][0] + x[j][1]) + (x[j][2] + x[j][3]);
+    b[j][0] = pack_f16(16.f * x[j][0], -16.f * x[j][2]);
+    b[j][1] = pack_f16(x[j][1], -x[j][3]);
   }
-  float mine = 0.f;
+}
+// what a word's halves meet: sums over the groups, of lane t the t-th group's
+template <int NG>
+__device__ __forceinline__ void column_sums(const float (&x)[8][4], uint32_t (&wz)[3], bool on) {
+  const int t = threadIdx.x & 3;
+  float lo[NG], hi[NG];
+#pragma unroll
+  for (int g = 0; g < NG; ++g) lo[g] = hi[g] = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    lo[j * NG / 8] += x[j][0] + x[j][1];
+    hi[j * NG / 8] += x[j][2] + x[j][3];
+  }
+  float s = 0.f, z = 0.f;
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
-    part[g] += __shfl_xor_sync(0xffffffffu, part[g], 1);
-    part[g] += __shfl_xor_sync(0xffffffffu, part[g], 2);
-    if (g == t) mine = part[g];
+#pragma unroll
+    for (int off = 1; off <= 2; off <<= 1) {
+      lo[g] += __shfl_xor_sync(0xffffffffu, lo[g], off);
+      hi[g] += __shfl_xor_sync(0xffffffffu, hi[g], off);
+    }
+    if (g == t) s = fmaf(7.f, hi[g], -8.f * lo[g]), z = lo[g] + hi[g];
   }
-  mine = sums && t < NG ? mine * 0x1p-20f : 0.f;  // in the products' unit
+  // in the products' unit
+  s = on && t < NG ? s * 0x1p-20f : 0.f;
+  z = on && t < NG ? z * 0x1p-20f : 0.f;
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
-    const float h = __bfloat162float(__float2bfloat16_rn(mine));
-    wz[i] = tc::pack_bf16(-8.f * h, h);
-    mine -= h;
+    const float sh = __bfloat162float(__float2bfloat16_rn(s)), zh = __bfloat162float(__float2bfloat16_rn(z));
+    wz[i] = tc::pack_bf16(sh, zh);
+    s -= sh;
+    z -= zh;
   }
 }
 
@@ -454,7 +524,8 @@ __device__ __forceinline__ void load_heads(const __nv_bfloat16* q, int n, QFrag<
     for (int j = 0; j < 8; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[j][i] *= s;
-    column<NG>(x, f.b[nt], f.wz[nt], true);
+    column(x, f.b[nt]);
+    column_sums<NG>(x, f.wz[nt], true);
     const float u = 0x1p20f / s;
     f.unit[nt][0] = __shfl_sync(0xffffffffu, u, 8 * t);
     f.unit[nt][1] = __shfl_sync(0xffffffffu, u, 8 * t + 4);
@@ -483,13 +554,16 @@ __device__ __forceinline__ void load_mean(const __nv_bfloat16* q, int n, QFrag<1
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[j][i] /= (float)n;
   const float s = fit(largest(x));
-  float whole[8][4];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[j][i] *= s;
+  column_sums<NG>(x, f.wz[0], g == 0);
 #pragma unroll
   for (int j = 0; j < 8; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float y = x[j][i] * s, part = 0.f;
-      whole[j][i] = y;
+      float y = x[j][i], part = 0.f;
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
         const float h = __half2float(__float2half_rn(y));
@@ -498,17 +572,14 @@ __device__ __forceinline__ void load_mean(const __nv_bfloat16* q, int n, QFrag<1
       }
       x[j][i] = part;
     }
-  uint32_t dummy[3];
-  column<NG>(x, f.b[0], dummy, false);
-  // (the parts' sums would do; the whole's is one column's)
-  uint32_t unused[8][2];
-  column<NG>(whole, unused, f.wz[0], g == 0);
+  column(x, f.b[0]);
   f.unit[0][0] = f.unit[0][1] = 0x1p20f / s;
 }
 
 // The logits of a tile, in the columns' units: c[nt][0..1] key g of heads 2 t, 2 t + 1; [2..3] key g + 8.
+// A row's logits depend on that row alone: those of rows that are not there are anything.
 template <int NG, int NT>
-__device__ __forceinline__ void logits(uint32_t stage, uint32_t mask, const QFrag<NT>& f, float (&c)[NT][4]) {
+__device__ __forceinline__ void logits(uint32_t stage, const QFrag<NT>& f, float (&c)[NT][4]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint4 k0 = lds128(stage + g * kCodeBytes + t * 16), k1 = lds128(stage + (g + 8) * kCodeBytes + t * 16);
   const uint32_t words = stage + 16 * kCodeBytes;
@@ -518,16 +589,6 @@ __device__ __forceinline__ void logits(uint32_t stage, uint32_t mask, const QFra
   uint32_t aw[4];
   aw[0] = t < NG ? lds32(words + (g * NG + t) * 4) : 0u;
   aw[1] = t < NG ? lds32(words + ((g + 8) * NG + t) * 4) : 0u;
-  if (mask != 0xffffu) {  // what lies in rows that are not there counts for nothing
-    const bool on0 = mask >> g & 1u, on1 = mask >> (g + 8) & 1u;
-#pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      w0[i] = on0 ? w0[i] : 0u;
-      w1[i] = on1 ? w1[i] : 0u;
-    }
-    aw[0] = on0 ? aw[0] : 0u;
-    aw[1] = on1 ? aw[1] : 0u;
-  }
   aw[2] = aw[0];
   aw[3] = aw[1];
 #pragma unroll
@@ -570,6 +631,7 @@ __device__ __forceinline__ void logits(uint32_t stage, uint32_t mask, const QFra
 template <int NG, int NT>
 struct State {
   float m[NT][2], l[NT][2];
+  float ref[NT][2], top[NT][2];  // -r; the logit in its column's unit past which the maximum moves
   float o[NT][8][4];  // rows 2 g (2^-24 a unit) and 2 g + 1 (2^-20) of entries 16 i, columns heads 2 t, 2 t + 1
   float z[NT][NG][2];
   int sigma;          // steps are below 2^(sigma + 1)
@@ -584,6 +646,8 @@ __device__ __forceinline__ void clear(State<NG, NT>& s) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       s.m[nt][i] = kFloor;
+      s.ref[nt][i] = -kFloor;
+      s.top[nt][i] = kFloor;
       s.l[nt][i] = 0.f;
 #pragma unroll
       for (int g = 0; g < NG; ++g) s.z[nt][g][i] = 0.f;
@@ -598,7 +662,8 @@ __device__ __forceinline__ void clear(State<NG, NT>& s) {
 
 // A maximum or a power of the steps that a tile has passed: everything in the new reference.
 template <int NG, int NT>
-__device__ __forceinline__ void rescale(State<NG, NT>& s, const float (&x)[NT][4], float smax) {
+__device__ __forceinline__ void rescale(State<NG, NT>& s, const float (&c)[NT][4], const float (&kf)[NT][2],
+                                        float smax) {
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, off));
   int e = (int)((__float_as_uint(smax) >> 23) & 255u) - 127;
@@ -611,12 +676,14 @@ __device__ __forceinline__ void rescale(State<NG, NT>& s, const float (&x)[NT][4
     float f[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float m = fmaxf(x[nt][i], x[nt][i + 2]);
+      float m = fmaxf(c[nt][i], c[nt][i + 2]) * kf[nt][i];
 #pragma unroll
       for (int off = 4; off <= 16; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
       m = fmaxf(m, s.m[nt][i]);
       f[i] = ex2(s.m[nt][i] - m + ds);
       s.m[nt][i] = m;
+      s.ref[nt][i] = 7.f - (float)sigma - m;
+      s.top[nt][i] = (m + 7.f) / kf[nt][i];
       s.l[nt][i] *= f[i];
 #pragma unroll
       for (int g = 0; g < NG; ++g) s.z[nt][g][i] *= f[i];
@@ -633,7 +700,7 @@ __device__ __forceinline__ void attend_tile(uint32_t stage, uint32_t mask, const
                                             State<NG, NT>& s) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   float c[NT][4];
-  logits<NG, NT>(stage, mask, f, c);
+  logits<NG, NT>(stage, f, c);
   const uint32_t vc = stage + kv4_cell(NG), words = vc + 16 * kCodeBytes;
   uint32_t w0[NG], w1[NG];
   lds_words<NG>(words + g * 4 * NG, w0);
@@ -654,29 +721,31 @@ __device__ __forceinline__ void attend_tile(uint32_t stage, uint32_t mask, const
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      c[nt][i] *= kf[nt][i & 1];
       if (mask != 0xffffu && !(i < 2 ? on0 : on1)) c[nt][i] = -INFINITY;
-      past |= c[nt][i] > s.m[nt][i & 1] + 7.f;
+      past |= c[nt][i] > s.top[nt][i & 1];
     }
-  if (__any_sync(0xffffffffu, past)) rescale<NG, NT>(s, c, smax);
-  const float ref = 7.f - (float)s.sigma;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[nt][i] = ex2(c[nt][i] - s.m[nt][i & 1] + ref);
+  if (__any_sync(0xffffffffu, past)) rescale<NG, NT>(s, c, kf, smax);
+  const float off = g & 1 ? 7.f : -8.f;  // (see spread)
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[nt][i] = ex2(fmaf(c[nt][i], kf[nt][i & 1], s.ref[nt][i & 1]));
     s.l[nt][0] += c[nt][0] + c[nt][2];
     s.l[nt][1] += c[nt][1] + c[nt][3];
+  }
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      const float z0 = centre_of(w0[i]), z1 = centre_of(w1[i]), s0 = step_of(w0[i]), s1 = step_of(w1[i]);
-      // (the codes come with 8 more than they stand for)
-      const float y0 = fmaf(-8.f, s0, z0), y1 = fmaf(-8.f, s1, z1);
+  for (int i = 0; i < NG; ++i) {
+    const float y0 = fmaf(off, step_of(w0[i]), centre_of(w0[i])), y1 = fmaf(off, step_of(w1[i]), centre_of(w1[i]));
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
       s.z[nt][i][0] = fmaf(c[nt][0], y0, fmaf(c[nt][2], y1, s.z[nt][i][0]));
       s.z[nt][i][1] = fmaf(c[nt][1], y0, fmaf(c[nt][3], y1, s.z[nt][i][1]));
     }
   }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[nt][i] = __uint_as_float(__float_as_uint(c[nt][i]) ^ (uint32_t)g << 31);
   // the second product: weights times steps, transposed, a group at a time
   uint2 v[4];
   {
@@ -721,12 +790,21 @@ struct AttnShape {
   static constexpr int kSmem = kRing + kOut;
 };
 
+template <int MODE, int NG, int S>
+struct Pick {
+  using type = CellFeeder<MODE, NG, true, S>;
+};
+template <int NG, int S>
+struct Pick<kList, NG, S> {
+  using type = RowFeeder<kList, NG, true, S>;
+};
+
 template <int NG, int NT, int MODE>
 __global__ void __launch_bounds__(32 * kW, AttnShape<NG, NT>::kCtas) kv4_attn_kernel(const Kv4Args a) {
   using Shape = AttnShape<NG, NT>;
   constexpr int S = Shape::kStages, HC = 8 * NT;  // columns
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ uint32_t s_mask[kW][S];
+  __shared__ uint32_t s_mask[MODE == kList ? kW : 1][S];
   __shared__ float2 s_ml[kW][HC], s_tot[HC];
   __shared__ float s_f[HC][kW];
   float* s_o = reinterpret_cast<float*>(smem + Shape::kRing);
@@ -741,11 +819,12 @@ __global__ void __launch_bounds__(32 * kW, AttnShape<NG, NT>::kCtas) kv4_attn_ke
   const int mine = t1 - t0 > warp ? (int)((t1 - t0 - warp + kW - 1) / kW) : 0;
   Cursor at = u;
   at.tile += warp;
-  const uint32_t ring = smem_u32(smem) + warp * S * 2 * kv4_cell(NG);
-  Feeder<MODE, NG, true, S> feed(a, ring, s_mask[warp], at, mine);
+  constexpr uint32_t kStage = 2 * kv4_cell(NG);
+  const uint32_t ring = smem_u32(smem) + warp * S * kStage;
+  typename Pick<MODE, NG, S>::type feed(a, ring, s_mask[MODE == kList ? warp : 0], at, mine);
 #pragma unroll 1
   for (int i = 0; i < S - 1; ++i) feed.issue();
-  int done = 0, seg = 0;
+  int done = 0, seg = 0, stage = 0;
   for (long long f = t0; f < t1; ++seg) {
     const long long first = f - u.tile, end = first + u.nt < t1 ? first + u.nt : t1;
     QFrag<NT> q;
@@ -759,8 +838,9 @@ __global__ void __launch_bounds__(32 * kW, AttnShape<NG, NT>::kCtas) kv4_attn_ke
       cp_async_wait<S - 2>();
       __syncwarp();
       feed.issue();  // into the stage of the tile before this one
-      const uint32_t mask = s_mask[warp][done % S];
-      if (mask != 0u) attend_tile<NG, NT>(ring + done % S * 2 * kv4_cell(NG), mask, q, kf, s);
+      const uint32_t mask = feed.live(u.L, (int)(t0 + warp + (long long)done * kW - first), stage);
+      if (mask != 0u) attend_tile<NG, NT>(ring + stage * kStage, mask, q, kf, s);
+      stage = stage == S - 1 ? 0 : stage + 1;
     }
     // the warp's sums, then the CTA's
     float* row = s_o + warp * HC * Shape::kRow;
@@ -886,7 +966,6 @@ template <int NG, int NT, int AGG>
 __global__ void __launch_bounds__(32 * kW, 2) kv4_score_kernel(const Kv4Args a) {
   constexpr int S = kScoreStages;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ uint32_t s_mask[kW][S];
   pdl_release();
   pdl_wait();
   long long T, t0, t1;
@@ -899,10 +978,10 @@ __global__ void __launch_bounds__(32 * kW, 2) kv4_score_kernel(const Kv4Args a) 
   Cursor at = u;
   at.tile += warp;
   const uint32_t ring = smem_u32(smem) + warp * S * kv4_cell(NG);
-  Feeder<kScore, NG, false, S> feed(a, ring, s_mask[warp], at, mine);
+  CellFeeder<kScore, NG, false, S> feed(a, ring, nullptr, at, mine);
 #pragma unroll 1
   for (int i = 0; i < S - 1; ++i) feed.issue();
-  int done = 0;
+  int done = 0, stage = 0;
   for (long long f = t0; f < t1;) {
     const long long first = f - u.tile, end = first + u.nt < t1 ? first + u.nt : t1;
     if (t0 + warp + (long long)done * kW < end) {
@@ -919,14 +998,15 @@ __global__ void __launch_bounds__(32 * kW, 2) kv4_score_kernel(const Kv4Args a) 
         cp_async_wait<S - 2>();
         __syncwarp();
         feed.issue();
-        const uint32_t mask = s_mask[warp][done % S];
+        const bool there = !(feed.bad >> (S - 1) & 1u);
         float c[NT][4];
-        logits<NG, NT>(ring + done % S * kv4_cell(NG), mask, q, c);
+        logits<NG, NT>(ring + stage * kv4_cell(NG), q, c);
+        stage = stage == S - 1 ? 0 : stage + 1;
         const int k0 = (rg.s_end & ~15) + (int)(t0 + warp + (long long)done * kW - first) * 16 + g;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {  // keys g, g + 8
           const int key = k0 + 8 * i;
-          const bool in = key >= rg.s_end && key < rg.l_start, there = mask >> (g + 8 * i) & 1u;
+          const bool in = key >= rg.s_end && key < rg.l_start;
           if constexpr (AGG == SKV_AGG_HEAD) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -985,12 +1065,12 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4Args a, T* k_o
     c.L = t == 0 && j == 0 && c.h == 0 ? load_len(a.seq_lens, c.b, a.max_len, a.status) : len_of(a, c.b);
     c.nt = 0;
     Row w;
-    row_position<kList>(a, c, true, j & 15, w);
-    row_entry<kList>(a, t == 0, w);
-    const long long at = row_address<NG>(a, t == 0, w);
-    const bool host = at >= 0 && (at & kHostTile);
-    const long long cell = at & ~(kHostTile | 15);
-    const int rc = (int)(at & 15);
+    row_position(a, c, true, j & 15, w);
+    row_entry(a, t == 0, w);
+    const uint32_t at = row_id(a, t == 0, w);
+    const bool host = at >> 31;
+    const size_t cell = (size_t)(at >> 4 & 0x7ffffffu) * kv4_cell(NG);
+    const int rc = (int)(at & 15u);
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
       T* out = kv ? v_out : k_out;
@@ -1001,7 +1081,7 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4Args a, T* k_o
       float s[NG], z[NG];
 #pragma unroll
       for (int i = 0; i < NG; ++i) s[i] = z[i] = 0.f;
-      if (at >= 0) {
+      if (at != kNoRow) {
         u = __ldg(reinterpret_cast<const uint4*>(src + cell + rc * kCodeBytes) + t);
         const uint32_t* words = reinterpret_cast<const uint32_t*>(src + cell + 16 * kCodeBytes) + rc * NG;
 #pragma unroll
@@ -1046,6 +1126,12 @@ Kv4Args kv4_args(const skv_problem& p, const void* q, const PoolView& pool, cons
   a.nl = p.n_local;
   a.k = p.topk;
   a.bs = p.block_size;
+  a.cells = p.block_size / kCellTokens;
+  a.shift = -1;
+  for (int i = 4; i < 31; ++i)
+    if (p.block_size == 1 << i) a.shift = i;
+  a.n_gpu = (unsigned)pool.n_gpu;
+  a.n_host = pool.host_k != nullptr ? (unsigned)pool.n_host : 0u;
   a.agg = p.group_agg;
   a.Gi = p.n_idx_q_heads / p.n_kv_heads;
   a.scale_log2 = (p.sm_scale > 0.f ? p.sm_scale : 1.f / sqrtf((float)p.d_qk)) * kLog2e;
