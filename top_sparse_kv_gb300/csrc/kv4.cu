@@ -37,6 +37,8 @@ struct Kv4Args {
   int max_len, ns, nl, k, bs;
   int cells, shift;        // of a block: its cells; log2 of its tokens, or -1
   unsigned n_gpu, n_host;  // blocks there (0 without a host pool)
+  unsigned block_bytes;    // of a GPU block (of K, of V)
+  int step_blocks, step_cells;  // kW tiles on
   int agg, Gi;             // scores
   float scale_log2;
   int32_t* status;
@@ -235,7 +237,9 @@ __device__ __forceinline__ uint32_t v_chunk_at(int lane) {
 // the start); live() then tells which rows of the tile to be computed are there.
 
 // Whole cells: a history's tiles.  The entry of a tile is loaded when the one before it is
-// issued, so it has a tile's time to arrive.
+// issued, so it has a tile's time to arrive.  What a unit's tiles share -- its table row, the
+// pools at its head -- is found when the unit is entered, and a block's number and the
+// cell in it move on without a division.
 template <int MODE, int NG, bool V, int S>
 struct CellFeeder {
   static constexpr int kStage = (V ? 2 : 1) * kv4_cell(NG);
@@ -243,52 +247,64 @@ struct CellFeeder {
   uint32_t to, end;  // the stage that is filled next, the ring's end
   uint32_t v_at;
   Cursor c;  // the tile that is issued next
-  int left, first, e;
+  int left, e;
+  int block, in;      // the tile's block, its cell there
+  const int32_t* row;  // the unit's entries
+  const unsigned char *k, *v;  // this lane's first chunk of the head's cells in GPU block 0
   uint32_t bad;  // of the tiles issued, the last in bit 0: no such block
 
   __device__ __forceinline__ CellFeeder(const Kv4Args& args, uint32_t ring, uint32_t*, Cursor at, int n)
       : a(args), to(ring), end(ring + S * kStage), v_at(v_chunk_at(threadIdx.x & 31)), c(at), left(n), bad(0) {
-    if (left > 0) {
-      settle<MODE>(a, c);
-      load();
+    if (left > 0) enter();
+  }
+  __device__ __forceinline__ void enter() {
+    settle<MODE>(a, c);
+    const int cell = (MODE == kScore ? regions_of(c.L, a.ns, a.nl).s_end >> 4 : 0) + c.tile;
+    block = cell / a.cells;
+    in = cell - block * a.cells;
+    row = table_row(a.pool, c.b, c.h, a.heads);
+    const size_t at = (a.pool.per_head ? 0 : (size_t)c.h * a.cells * kv4_cell(NG)) + (threadIdx.x & 31) * 16;
+    k = (const unsigned char*)a.pool.gpu_k + at;
+    v = (const unsigned char*)a.pool.gpu_v + at;
+    e = __ldg(row + block);
+  }
+  __device__ __forceinline__ void copy(const unsigned char* ks, const unsigned char* vs) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t dst = to + lane * 16;
+    cp_async_cg16(dst, ks);
+    cp_async_cg16(dst + 512, ks + 512);
+    if (V) {
+      cp_async_cg16(to + kv4_cell(NG) + v_at, vs);
+      cp_async_cg16(to + kv4_cell(NG) + v_at + 512, vs + 512);
+    }
+    if (lane < 4 * NG) {
+      cp_async_cg16(dst + 1024, ks + 1024);
+      if (V) cp_async_cg16(dst + kv4_cell(NG) + 1024, vs + 1024);
     }
   }
-  __device__ __forceinline__ void load() {
-    first = MODE == kScore ? regions_of(c.L, a.ns, a.nl).s_end >> 4 : 0;
-    const int cell = first + c.tile, block = a.cells == 1 ? cell : cell / a.cells;
-    e = __ldg(table_row(a.pool, c.b, c.h, a.heads) + block);
-  }
   __device__ __forceinline__ void issue() {
-    const int lane = threadIdx.x & 31;
     bad <<= 1;
     if (left > 0) {
-      const bool host = e < 0;
-      const unsigned block = host ? ~e : e;
-      if (block < (host ? a.n_host : a.n_gpu)) {
-        const long long unit = (long long)block * (a.pool.per_head && !host ? 1 : a.heads) +
-                               (a.pool.per_head && !host ? 0 : c.h);
-        long long cell = unit;
-        if (a.cells != 1) cell = unit * a.cells + (first + c.tile) % a.cells;
-        const long long at = cell * kv4_cell(NG) + lane * 16;
-        const unsigned char* k = (const unsigned char*)(host ? a.pool.host_k : a.pool.gpu_k) + at;
-        const uint32_t dst = to + lane * 16;
-        cp_async_cg16(dst, k);
-        cp_async_cg16(dst + 512, k + 512);
-        if (lane < 4 * NG) cp_async_cg16(dst + 1024, k + 1024);
-        if (V) {
-          const unsigned char* v = (const unsigned char*)(host ? a.pool.host_v : a.pool.gpu_v) + at;
-          cp_async_cg16(to + kv4_cell(NG) + v_at, v);
-          cp_async_cg16(to + kv4_cell(NG) + v_at + 512, v + 512);
-          if (lane < 4 * NG) cp_async_cg16(dst + kv4_cell(NG) + 1024, v + 1024);
-        }
+      if ((unsigned)e < a.n_gpu) {
+        const size_t at = (size_t)(unsigned)e * a.block_bytes + in * kv4_cell(NG);
+        copy(k + at, v + at);
+      } else if (e < 0 && ~(unsigned)e < a.n_host) {
+        const size_t at = (((size_t)~(unsigned)e * a.heads + c.h) * a.cells + in) * kv4_cell(NG) + (threadIdx.x & 31) * 16;
+        copy((const unsigned char*)a.pool.host_k + at, (const unsigned char*)a.pool.host_v + at);
       } else {
-        if (lane == 0) flag(a.status, SKV_DEV_BAD_SLOT);
+        if ((threadIdx.x & 31) == 0) flag(a.status, SKV_DEV_BAD_SLOT);
         bad |= 1u;
       }
       if (--left > 0) {
         c.tile += kW;
-        if (c.tile >= c.nt) settle<MODE>(a, c);
-        load();
+        if (c.tile >= c.nt) {
+          enter();
+        } else {
+          block += a.step_blocks;
+          in += a.step_cells;
+          if (in >= a.cells) in -= a.cells, ++block;
+          e = __ldg(row + block);
+        }
       }
     }
     cp_async_commit();
@@ -377,6 +393,21 @@ __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// the same of zero accumulators, which take no registers
+__device__ __forceinline__ void mma_f16_new(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_bf16_new(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -414,17 +445,12 @@ __device__ __forceinline__ float centre_of(uint32_t w) { return __uint_as_float(
 
 // The four operand registers of two bytes' worth of codes, in the order low and high half of
 // the first byte, low and high half of the second: subnormal fp16 pairs, 2^-24 and 2^-20 a unit.
-// The upper one of a pair comes as 15 - c (the same instruction), and the other operand has its
-// sign turned there: u c + v c' as u c - v (15 - c') + 15 v.  Codes are 7.5 on average, and a
-// long sum of them all on one side of zero would lose to the tensor core's truncation what
-// the centring takes off again (a million keys: 1 % of the output); in pairs of either sign it
-// stays small.  With the codes' own 8, the first of a pair stands 8 too high, the second 7 too low.
 __device__ __forceinline__ void spread(uint32_t x, uint32_t* r) {
   const uint32_t y = x >> 8;
-  r[0] = (x & 0x000f000fu) ^ 0x000f0000u;
-  r[1] = (x & 0x00f000f0u) ^ 0x00f00000u;
-  r[2] = (y & 0x000f000fu) ^ 0x000f0000u;
-  r[3] = (y & 0x00f000f0u) ^ 0x00f00000u;
+  r[0] = x & 0x000f000fu;
+  r[1] = x & 0x00f000f0u;
+  r[2] = y & 0x000f000fu;
+  r[3] = y & 0x00f000f0u;
 }
 
 // A power of two that brings |x| <= mx under 2^10 (its own inverse is exact too).
@@ -448,41 +474,32 @@ struct QFrag {
 __device__ __forceinline__ void column(const float (&x)[8][4], uint32_t (&b)[8][2]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    b[j][0] = pack_f16(16.f * x[j][0], -16.f * x[j][2]);
-    b[j][1] = pack_f16(x[j][1], -x[j][3]);
+    b[j][0] = pack_f16(16.f * x[j][0], 16.f * x[j][2]);
+    b[j][1] = pack_f16(x[j][1], x[j][3]);
   }
 }
 // what a word's halves meet: sums over the groups, of lane t the t-th group's
 template <int NG>
 __device__ __forceinline__ void column_sums(const float (&x)[8][4], uint32_t (&wz)[3], bool on) {
   const int t = threadIdx.x & 3;
-  float lo[NG], hi[NG];
+  float part[NG], z = 0.f;
 #pragma unroll
-  for (int g = 0; g < NG; ++g) lo[g] = hi[g] = 0.f;
+  for (int g = 0; g < NG; ++g) part[g] = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    lo[j * NG / 8] += x[j][0] + x[j][1];
-    hi[j * NG / 8] += x[j][2] + x[j][3];
-  }
-  float s = 0.f, z = 0.f;
+  for (int j = 0; j < 8; ++j) part[j * NG / 8] += (x[j][0] + x[j][1]) + (x[j][2] + x[j][3]);
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
-#pragma unroll
-    for (int off = 1; off <= 2; off <<= 1) {
-      lo[g] += __shfl_xor_sync(0xffffffffu, lo[g], off);
-      hi[g] += __shfl_xor_sync(0xffffffffu, hi[g], off);
-    }
-    if (g == t) s = fmaf(7.f, hi[g], -8.f * lo[g]), z = lo[g] + hi[g];
+    part[g] += __shfl_xor_sync(0xffffffffu, part[g], 1);
+    part[g] += __shfl_xor_sync(0xffffffffu, part[g], 2);
+    if (g == t) z = part[g];
   }
   // in the products' unit
-  s = on && t < NG ? s * 0x1p-20f : 0.f;
   z = on && t < NG ? z * 0x1p-20f : 0.f;
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
-    const float sh = __bfloat162float(__float2bfloat16_rn(s)), zh = __bfloat162float(__float2bfloat16_rn(z));
-    wz[i] = tc::pack_bf16(sh, zh);
-    s -= sh;
-    z -= zh;
+    const float h = __bfloat162float(__float2bfloat16_rn(z));
+    wz[i] = tc::pack_bf16(-8.f * h, h);
+    z -= h;
   }
 }
 
@@ -593,8 +610,7 @@ __device__ __forceinline__ void logits(uint32_t stage, const QFrag<NT>& f, float
   aw[3] = aw[1];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
-    tc::mma_bf16(c[nt], aw, f.wz[nt][0], f.wz[nt][1]);
+    mma_bf16_new(c[nt], aw, f.wz[nt][0], f.wz[nt][1]);
     tc::mma_bf16(c[nt], aw, f.wz[nt][2], 0u);
   }
   float acc[NT][4];
@@ -611,8 +627,10 @@ __device__ __forceinline__ void logits(uint32_t stage, const QFrag<NT>& f, float
       constexpr int kSteps = 8 / NG;  // of a group
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        if (j % kSteps == 0) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-        mma_f16(acc[nt], ar, f.b[nt][j][0], f.b[nt][j][1]);
+        if (j % kSteps == 0)
+          mma_f16_new(acc[nt], ar, f.b[nt][j][0], f.b[nt][j][1]);
+        else
+          mma_f16(acc[nt], ar, f.b[nt][j][0], f.b[nt][j][1]);
         if (j % kSteps == kSteps - 1) {
           const float s0 = step_of(w0[j / kSteps]), s1 = step_of(w1[j / kSteps]);
           c[nt][0] = fmaf(s0, acc[nt][0], c[nt][0]);
@@ -713,9 +731,10 @@ __device__ __forceinline__ void attend_tile(uint32_t stage, uint32_t mask, const
       w1[i] = on1 ? w1[i] : 0u;
     }
   }
-  float smax = 0.f;
-#pragma unroll
-  for (int i = 0; i < NG; ++i) smax = fmaxf(smax, fmaxf(fabsf(step_of(w0[i])), fabsf(step_of(w1[i]))));
+  // (each lane of a quad looks at a group's step)
+  const uint32_t mine = words + (t & (NG - 1)) * 4;
+  const float smax = fmaxf(on0 ? fabsf(step_of(lds32(mine + g * 4 * NG))) : 0.f,
+                           on1 ? fabsf(step_of(lds32(mine + (g + 8) * 4 * NG))) : 0.f);
   bool past = smax >= __uint_as_float((uint32_t)(s.sigma + 128) << 23);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -725,7 +744,11 @@ __device__ __forceinline__ void attend_tile(uint32_t stage, uint32_t mask, const
       past |= c[nt][i] > s.top[nt][i & 1];
     }
   if (__any_sync(0xffffffffu, past)) rescale<NG, NT>(s, c, kf, smax);
-  const float off = g & 1 ? 7.f : -8.f;  // (see spread)
+  // Every other key's codes come as 15 - c and its weights negative: w c - w' (15 - c') + 15 w'.  Codes
+  // are 7.5 on average, and a long sum of them on one side of zero would lose to the tensor core's
+  // truncation what the centring takes off again (a million keys: 1 % of the output).  With the
+  // codes' own 8, the even keys' stand 8 too high and the odd ones' 7 too low.
+  const float off = g & 1 ? 7.f : -8.f, sign = g & 1 ? -1.f : 1.f;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -745,13 +768,15 @@ __device__ __forceinline__ void attend_tile(uint32_t stage, uint32_t mask, const
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[nt][i] = __uint_as_float(__float_as_uint(c[nt][i]) ^ (uint32_t)g << 31);
+    for (int i = 0; i < 4; ++i) c[nt][i] *= sign;
   // the second product: weights times steps, transposed, a group at a time
   uint2 v[4];
   {
     const uint32_t row = vc + t * kCodeBytes + (v_chunk(t, g >> 1) << 4) + ((g & 1) << 3);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = lds64(row + i * 4 * kCodeBytes);  // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+    v[1] = make_uint2(~v[1].x, ~v[1].y);
+    v[3] = make_uint2(~v[3].x, ~v[3].y);
   }
   uint32_t wb[NT][2];
 #pragma unroll
@@ -824,7 +849,7 @@ __global__ void __launch_bounds__(32 * kW, AttnShape<NG, NT>::kCtas) kv4_attn_ke
   typename Pick<MODE, NG, S>::type feed(a, ring, s_mask[MODE == kList ? warp : 0], at, mine);
 #pragma unroll 1
   for (int i = 0; i < S - 1; ++i) feed.issue();
-  int done = 0, seg = 0, stage = 0;
+  int next = warp, seg = 0, stage = 0;  // next: this warp's next tile of the share
   for (long long f = t0; f < t1; ++seg) {
     const long long first = f - u.tile, end = first + u.nt < t1 ? first + u.nt : t1;
     QFrag<NT> q;
@@ -834,11 +859,12 @@ __global__ void __launch_bounds__(32 * kW, AttnShape<NG, NT>::kCtas) kv4_attn_ke
     for (int nt = 0; nt < NT; ++nt) kf[nt][0] = q.unit[nt][0] * a.scale_log2, kf[nt][1] = q.unit[nt][1] * a.scale_log2;
     State<NG, NT> s;
     clear(s);
-    for (; t0 + warp + (long long)done * kW < end; ++done) {
+    const int last = (int)(end - t0), base = (int)(first - t0);  // (a share has fewer tiles than 2^31)
+    for (; next < last; next += kW) {
       cp_async_wait<S - 2>();
       __syncwarp();
       feed.issue();  // into the stage of the tile before this one
-      const uint32_t mask = feed.live(u.L, (int)(t0 + warp + (long long)done * kW - first), stage);
+      const uint32_t mask = feed.live(u.L, next - base, stage);
       if (mask != 0u) attend_tile<NG, NT>(ring + stage * kStage, mask, q, kf, s);
       stage = stage == S - 1 ? 0 : stage + 1;
     }
@@ -981,10 +1007,11 @@ __global__ void __launch_bounds__(32 * kW, 2) kv4_score_kernel(const Kv4Args a) 
   CellFeeder<kScore, NG, false, S> feed(a, ring, nullptr, at, mine);
 #pragma unroll 1
   for (int i = 0; i < S - 1; ++i) feed.issue();
-  int done = 0, stage = 0;
+  int next = warp, stage = 0;
   for (long long f = t0; f < t1;) {
     const long long first = f - u.tile, end = first + u.nt < t1 ? first + u.nt : t1;
-    if (t0 + warp + (long long)done * kW < end) {
+    const int last = (int)(end - t0);
+    if (next < last) {
       QFrag<NT> q;
       const __nv_bfloat16* qp = a.q + ((size_t)u.b * a.H + u.h) * a.Gi * kD;
       if constexpr (AGG == SKV_AGG_MEAN)
@@ -994,7 +1021,8 @@ __global__ void __launch_bounds__(32 * kW, 2) kv4_score_kernel(const Kv4Args a) 
       const Regions rg = regions_of(u.L, a.ns, a.nl);
       const int rows = AGG == SKV_AGG_HEAD ? a.Gi : 1;  // score rows of the unit
       float* out = a.scores + ((size_t)u.b * a.H + u.h) * rows * a.max_len;
-      for (; t0 + warp + (long long)done * kW < end; ++done) {
+      int k0 = (rg.s_end & ~15) + (next - (int)(first - t0)) * 16 + g;
+      for (; next < last; next += kW, k0 += 16 * kW) {
         cp_async_wait<S - 2>();
         __syncwarp();
         feed.issue();
@@ -1002,7 +1030,6 @@ __global__ void __launch_bounds__(32 * kW, 2) kv4_score_kernel(const Kv4Args a) 
         float c[NT][4];
         logits<NG, NT>(ring + stage * kv4_cell(NG), q, c);
         stage = stage == S - 1 ? 0 : stage + 1;
-        const int k0 = (rg.s_end & ~15) + (int)(t0 + warp + (long long)done * kW - first) * 16 + g;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {  // keys g, g + 8
           const int key = k0 + 8 * i;
@@ -1109,7 +1136,8 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4Args a, T* k_o
 
 // ---------------------------------------------------------------------------- host
 
-Kv4Args kv4_args(const skv_problem& p, const void* q, const PoolView& pool, const int32_t* idx, int32_t* status) {
+Kv4Args kv4_args(const skv_problem& p, const void* q, const PoolView& pool, int group, const int32_t* idx,
+                 int32_t* status) {
   Kv4Args a = {};
   a.q = (const __nv_bfloat16*)q;
   a.pool = pool;
@@ -1130,6 +1158,9 @@ Kv4Args kv4_args(const skv_problem& p, const void* q, const PoolView& pool, cons
   a.shift = -1;
   for (int i = 4; i < 31; ++i)
     if (p.block_size == 1 << i) a.shift = i;
+  a.step_blocks = kW / a.cells;
+  a.step_cells = kW % a.cells;
+  a.block_bytes = (unsigned)((pool.per_head ? 1 : a.heads) * a.cells * kv4_cell(kD / group));
   a.n_gpu = (unsigned)pool.n_gpu;
   a.n_host = pool.host_k != nullptr ? (unsigned)pool.n_host : 0u;
   a.agg = p.group_agg;
@@ -1200,7 +1231,7 @@ size_t kv4_attn_workspace_bytes(const skv_problem& p) {
 
 skv_status launch_kv4_attn(const skv_problem& p, const void* q, const PoolView& pool, int group, const int32_t* idx,
                            void* out, float* lse, void* ws, int32_t* status, cudaStream_t st) {
-  Kv4Args a = kv4_args(p, q, pool, idx, status);
+  Kv4Args a = kv4_args(p, q, pool, group, idx, status);
   a.out = (__nv_bfloat16*)out;
   a.lse = lse;
   a.ws = (float*)ws;
@@ -1217,7 +1248,7 @@ skv_status launch_kv4_attn(const skv_problem& p, const void* q, const PoolView& 
 
 skv_status launch_kv4_score(const skv_problem& p, const void* q, const PoolView& pool, int group, float* scores,
                             int32_t* status, cudaStream_t st) {
-  Kv4Args a = kv4_args(p, q, pool, nullptr, status);
+  Kv4Args a = kv4_args(p, q, pool, group, nullptr, status);
   a.scores = scores;
   const long long tiles = (long long)a.B * a.H * (((long long)p.max_len + 15) / 16 + 1);
 #define KV4_SCORE(NG)                                                                 \
@@ -1230,7 +1261,7 @@ skv_status launch_kv4_score(const skv_problem& p, const void* q, const PoolView&
 
 skv_status launch_kv4_gather(const skv_problem& p, const PoolView& pool, int group, const int32_t* idx, void* k_out,
                              void* v_out, int32_t* status, cudaStream_t st) {
-  const Kv4Args a = kv4_args(p, nullptr, pool, idx, status);
+  const Kv4Args a = kv4_args(p, nullptr, pool, group, idx, status);
   const int n_att = p.n_sink + p.topk + p.n_local;
   if (n_att == 0) return SKV_OK;
   const bool f32 = p.dtype == SKV_DTYPE_F32;
