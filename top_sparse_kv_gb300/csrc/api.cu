@@ -863,7 +863,6 @@ static skv_status check_kv4(const skv_problem* p, const skv_kv_pool* pool, int32
   const long long most = (1LL << 31) / p->block_size / p->n_kv_heads;
   if (pool->n_gpu_blocks >= (pool->table_heads ? (1LL << 31) / p->block_size : most) || pool->n_host_blocks >= most)
     return SKV_ERR_UNSUPPORTED;
-  if (p->n_kv_heads * (long long)p->block_size >= 1LL << 24) return SKV_ERR_UNSUPPORTED;  // a block's bytes: 32 bits
   return SKV_OK;
 }
 

@@ -3,7 +3,7 @@
 //   score      <q, k^_t>,  k^ = s (c - 8) + z a group
 //   attention  softmax(scale <q, k^_t>) over the history or a list, times v^_t
 //
-// Both walk tiles of 16 keys.  Keys are the rows and the query heads the columns of a
+// Both walk tiles of 16 keys, a cell.  Keys are the rows and the query heads the columns of a
 // product S^T = K Q^T (m16n8k16): with at most 16 heads a KV head this wastes nothing of the
 // tensor core's 16 rows, and what it gives -- keys by heads -- is, transposed in registers
 // (movmatrix), the second operand of O^T = V^T P^T.  Codes never become numbers in memory: a nibble
@@ -25,7 +25,7 @@ namespace skv {
 namespace {
 
 constexpr int kW = 8;  // warps a CTA
-constexpr int kMaxParts = 320;  // CTAs of an attention at most
+constexpr int kMaxParts = 512;  // CTAs at most
 constexpr int kSlotFloats = 16 * (kD + 2);  // a partial: O of 16 heads, then their (reference, sum)
 
 struct Kv4Args {
@@ -37,8 +37,7 @@ struct Kv4Args {
   int max_len, ns, nl, k, bs;
   int cells, shift;        // of a block: its cells; log2 of its tokens, or -1
   unsigned n_gpu, n_host;  // blocks there (0 without a host pool)
-  unsigned block_bytes;    // of a GPU block (of K, of V)
-  int step_blocks, step_cells;  // kW tiles on
+  unsigned block_cells;    // of a GPU block
   int agg, Gi;             // scores
   float scale_log2;
   int32_t* status;
@@ -51,7 +50,8 @@ struct Kv4Args {
 
 enum { kDense, kList, kScore };
 
-// What a request of length L has to walk: tiles of 16 keys or list entries.
+// What a request of length L has to walk: tiles of 16 keys, or of 16 list entries (scores: from the
+// candidates' first cell on).
 template <int MODE>
 __device__ __forceinline__ int tiles_of(const Kv4Args& a, int L) {
   if (MODE == kDense) return (L + 15) >> 4;
@@ -84,63 +84,88 @@ __device__ __forceinline__ void settle(const Kv4Args& a, Cursor& c) {  // tile m
   }
 }
 
-// The CTAs' shares of T tiles: CTA c of n takes [T c / n, T (c + 1) / n).
-__device__ __forceinline__ long long share(long long T, int n, int c) { return T * c / n; }
-__device__ __forceinline__ int holder(long long T, int n, long long tile) { return (int)(((tile + 1) * n - 1) / T); }
+// The CTAs' shares.  A unit weighs its tiles and kUnit more, what entering and ending it takes of
+// a CTA's time (short histories: a CTA of many units would be last by far); of the weight W, CTA
+// c of n takes [W c / n, W (c + 1) / n), the tiles that lie there.  A unit's first kUnit places
+// hold no tile.
+constexpr int kUnit = 16;
+__device__ __forceinline__ long long share(long long W, int n, int c) { return W * c / n; }
+__device__ __forceinline__ int holder(long long W, int n, long long place) { return (int)(((place + 1) * n - 1) / W); }
+
+struct Share {
+  long long weight;  // of all units
+  long long place;   // the first unit's, among the weights
+  int ctas, tiles;   // CTAs that have a share; this one's tiles
+};
 
 // Every thread of the CTA gets the walk's length and the place where this CTA's share starts.
-template <int MODE>
-__device__ __forceinline__ void find_share(const Kv4Args& a, int min_tiles, long long* total, int* ctas,
-                                           long long* t0, long long* t1, Cursor* c) {
-  __shared__ long long s_warp[kW];
+template <int MODE, int THREADS>
+__device__ __forceinline__ Share find_share(const Kv4Args& a, Cursor* c) {
+  constexpr int kWarpsHere = THREADS / 32, kLeast = 2 * kW;  // weight of a CTA at least
+  __shared__ long long s_sum[2][kWarpsHere], s_tiles[2], s_place;
   __shared__ int s_at[3];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per = (a.B + kW * 32 - 1) / (kW * 32), b0 = threadIdx.x * per, b1 = b0 + per < a.B ? b0 + per : a.B;
-  long long mine = 0;
+  const int per = (a.B + THREADS - 1) / THREADS, b0 = threadIdx.x * per, b1 = b0 + per < a.B ? b0 + per : a.B;
+  long long tiles = 0, units = 0;
   for (int b = b0; b < b1; ++b) {
     const int L = blockIdx.x == 0 ? load_len(a.seq_lens, b, a.max_len, a.status) : len_of(a, b);
-    mine += tiles_of<MODE>(a, L);
+    const int nt = tiles_of<MODE>(a, L);
+    tiles += nt;
+    units += nt > 0;
   }
-  long long x = mine;
+  long long x = tiles, y = units;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, x, off);
-    if (lane >= off) x += u;
+    const long long p = __shfl_up_sync(0xffffffffu, x, off), q = __shfl_up_sync(0xffffffffu, y, off);
+    if (lane >= off) x += p, y += q;
   }
-  if (lane == 31) s_warp[warp] = x;
-  if (threadIdx.x == 0) s_at[0] = -1;
+  if (lane == 31) s_sum[0][warp] = x, s_sum[1][warp] = y;
+  if (threadIdx.x == 0) s_at[0] = -1, s_tiles[0] = s_tiles[1] = 0;
   __syncthreads();
-  long long before = 0, sum = 0;
+  long long all = 0, all_units = 0;
+  x -= tiles;
+  y -= units;
 #pragma unroll
-  for (int w = 0; w < kW; ++w) {
-    if (w == warp) before = sum;
-    sum += s_warp[w];
+  for (int w = 0; w < kWarpsHere; ++w) {
+    if (w == warp) x += all, y += all_units;
+    all += s_sum[0][w];
+    all_units += s_sum[1][w];
   }
-  before += x - mine;
-  const long long T = sum * a.H;
-  long long n = (T + min_tiles - 1) / min_tiles;
+  Share r;
+  r.weight = (all + kUnit * all_units) * a.H;
+  long long n = (r.weight + kLeast - 1) / kLeast;
   n = n < 1 ? 1 : n > gridDim.x ? gridDim.x : n;
-  *total = T;
-  *ctas = (int)n;
-  *t0 = *t1 = 0;
+  r.ctas = (int)n;
+  // the tiles before a share's ends: one thread's requests hold each
+  const long long before = (x + kUnit * y) * a.H, after = before + (tiles + kUnit * units) * a.H;
   if (blockIdx.x < n) {
-    *t0 = share(T, (int)n, blockIdx.x);
-    *t1 = share(T, (int)n, blockIdx.x + 1);
-  }
-  if (*t1 > *t0 && before * a.H <= *t0 && *t0 < (before + mine) * a.H) {  // one thread's requests hold it
-    long long at = *t0 - before * a.H;
-    for (int b = b0; b < b1; ++b) {
-      const int nt = tiles_of<MODE>(a, len_of(a, b));
-      if (at < (long long)nt * a.H) {
-        s_at[0] = b;
-        s_at[1] = (int)(at / nt);
-        s_at[2] = (int)(at % nt);
-        break;
+#pragma unroll 1
+    for (int end = 0; end < 2; ++end) {
+      const long long at = share(r.weight, (int)n, blockIdx.x + end);
+      if (end == 1 && at == r.weight && threadIdx.x == 0) s_tiles[1] = all * a.H;
+      if (at < before || at >= after) continue;
+      long long off = at - before, t = x * a.H;
+      for (int b = b0; b < b1; ++b) {
+        const int nt = tiles_of<MODE>(a, len_of(a, b)), w = nt > 0 ? nt + kUnit : 0;
+        if (off < (long long)w * a.H) {
+          const int h = (int)(off / w), in = (int)(off - (long long)h * w), tile = in > kUnit ? in - kUnit : 0;
+          s_tiles[end] = t + (long long)h * nt + tile;
+          if (end == 0) {
+            s_at[0] = b;
+            s_at[1] = h;
+            s_at[2] = tile;
+            s_place = at - in;
+          }
+          break;
+        }
+        off -= (long long)w * a.H;
+        t += (long long)nt * a.H;
       }
-      at -= (long long)nt * a.H;
     }
   }
   __syncthreads();
+  r.tiles = (int)(s_tiles[1] - s_tiles[0]);  // (a share has fewer tiles than 2^31)
+  r.place = s_place;
   c->b = s_at[0];
   if (c->b >= 0) {
     c->h = s_at[1];
@@ -148,16 +173,14 @@ __device__ __forceinline__ void find_share(const Kv4Args& a, int min_tiles, long
     c->L = len_of(a, c->b);
     c->nt = tiles_of<MODE>(a, c->L);
   }
+  return r;
 }
 
 // ---------------------------------------------------------------------------- a warp's ring
 //
-// A stage holds a tile as cells: K's codes and words, then V's.  V's rows of codes stand in
-// another order and with their 16-byte chunks exchanged in pairs, so that the 8-byte loads of
-// the second product meet no bank twice; the loads of K's rows are consecutive as they are.
-
-__device__ __forceinline__ int v_place(int r) { return (r & 8) | ((r & 7) >> 1) | ((r & 1) << 2); }
-__device__ __forceinline__ int v_chunk(int place, int c) { return c ^ (place & 2); }
+// Tile i of a CTA's share is warp i % kW's.  A warp fetches its own tiles, S of them ahead, into a
+// ring of its own: a stage is the cell of K, then the cell of V, as they lie in the pool.
+// (A warp that feeds the others leaves them 96 registers of 128: the products spill.)
 
 template <int BYTES>
 __device__ __forceinline__ void cp_async_ca(uint32_t dst, const void* src) {
@@ -167,8 +190,7 @@ __device__ __forceinline__ void cp_async_cg16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// The row of lane (lane & 15) on its way from its place in the walk to its address, a step an
-// iteration, so that each step's load has a tile's time to arrive.
+// A lane's row on its way from its place in a list to its number.
 struct Row {
   int t;            // position, as found (a selected one unchecked); -1: none
   int e, block;     // its table entry, that one's index
@@ -225,163 +247,175 @@ __device__ __forceinline__ uint32_t row_id(const Kv4Args& a, bool reports, const
   return kNoRow;
 }
 
-// Where a lane's 16-byte chunk of V's codes goes: chunk `lane` of the first eight rows (of the
-// others 512 bytes on).
-__device__ __forceinline__ uint32_t v_chunk_at(int lane) {
-  const int p = v_place(lane >> 2);
-  return p * kCodeBytes + v_chunk(p, lane & 3) * 16;
-}
+// Feeders.  issue() starts the next tile's copies, a commit group, into the ring's next stage; S - 1
+// times at first, then once a tile before it is computed.  rows() then tells which of the 16 rows of the tile
+// to be computed are there.  (Bulk copies with an mbarrier a stage cost more: the polls of a
+// barrier take issue slots that the products need -- 8 requests of 32K keys, 95 us against 85.)
 
-// Feeders: a warp issues its tiles' copies S - 1 tiles ahead of the one it computes, a commit
-// group a tile.  issue() is called once a tile (before it is computed, and S - 1 times at
-// the start); live() then tells which rows of the tile to be computed are there.
-
-// Whole cells: a history's tiles.  The entry of a tile is loaded when the one before it is
-// issued, so it has a tile's time to arrive.  What a unit's tiles share -- its table row, the
-// pools at its head -- is found when the unit is entered, and a block's number and the
-// cell in it move on without a division.
+// A history's tiles: whole cells.  The warp finds 32 tiles at a time, a lane a tile; the entries of
+// the next 32 are loaded when these are started.
 template <int MODE, int NG, bool V, int S>
 struct CellFeeder {
-  static constexpr int kStage = (V ? 2 : 1) * kv4_cell(NG);
+  static constexpr int kCell = kv4_cell(NG), kStage = (V ? 2 : 1) * kCell;
+  static constexpr uint32_t kNone = 0xffffffffu, kHost = 0x80000000u;
   const Kv4Args& a;
-  uint32_t to, end;  // the stage that is filled next, the ring's end
-  uint32_t v_at;
-  Cursor c;  // the tile that is issued next
-  int left, e;
-  int block, in;      // the tile's block, its cell there
-  const int32_t* row;  // the unit's entries
-  const unsigned char *k, *v;  // this lane's first chunk of the head's cells in GPU block 0
-  uint32_t bad;  // of the tiles issued, the last in bit 0: no such block
+  Cursor& at;              // the next tile to be found (shared memory)
+  uint32_t to, end;        // this lane's chunk of the next stage; past the last one
+  uint32_t cell;           // this lane's tile: its cell's number in its pool
+  int e;                   // its tile of the next 32: entry, the cell's number in block 0
+  uint32_t in;
+  int left, ahead, lane_up;  // tiles from these 32 on; not found; the lane whose tile is next
+  uint32_t gone;             // of the tiles issued, the last in bit 0: no such block
 
-  __device__ __forceinline__ CellFeeder(const Kv4Args& args, uint32_t ring, uint32_t*, Cursor at, int n)
-      : a(args), to(ring), end(ring + S * kStage), v_at(v_chunk_at(threadIdx.x & 31)), c(at), left(n), bad(0) {
-    if (left > 0) enter();
+  __device__ __forceinline__ CellFeeder(const Kv4Args& args, Cursor& at_, uint32_t*, uint32_t ring, Cursor c, int n)
+      : a(args), at(at_), to(ring + (threadIdx.x & 31) * 16), end(to + S * kStage), cell(kNone), e(0), in(kNone), left(n), ahead(n), lane_up(0),
+        gone(0) {
+    if ((threadIdx.x & 31) == 0) at = c;
+    __syncwarp();
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) turn();
   }
-  __device__ __forceinline__ void enter() {
-    settle<MODE>(a, c);
-    const int cell = (MODE == kScore ? regions_of(c.L, a.ns, a.nl).s_end >> 4 : 0) + c.tile;
-    block = cell / a.cells;
-    in = cell - block * a.cells;
-    row = table_row(a.pool, c.b, c.h, a.heads);
-    const size_t at = (a.pool.per_head ? 0 : (size_t)c.h * a.cells * kv4_cell(NG)) + (threadIdx.x & 31) * 16;
-    k = (const unsigned char*)a.pool.gpu_k + at;
-    v = (const unsigned char*)a.pool.gpu_v + at;
-    e = __ldg(row + block);
-  }
-  __device__ __forceinline__ void copy(const unsigned char* ks, const unsigned char* vs) {
+  // the next 32 tiles' places and entries
+  __device__ __forceinline__ void find() {
     const int lane = threadIdx.x & 31;
-    const uint32_t dst = to + lane * 16;
-    cp_async_cg16(dst, ks);
-    cp_async_cg16(dst + 512, ks + 512);
+    Cursor c = at;
+    __syncwarp();
+    c.tile += lane * kW;
+    in = kNone;
+    if (lane < ahead) {
+      settle<MODE>(a, c);
+      const int i = (MODE == kScore ? regions_of(c.L, a.ns, a.nl).s_end >> 4 : 0) + c.tile;
+      const int block = a.shift >= 0 ? i >> (a.shift - 4) : i / a.cells;
+      in = c.h * a.cells + (i - block * a.cells);
+      e = __ldg(table_row(a.pool, c.b, c.h, a.heads) + block);
+      if (a.pool.per_head && e >= 0) in -= c.h * a.cells;
+      if (lane == 31) {
+        c.tile += kW;
+        at = c;
+      }
+    }
+    __syncwarp();
+    ahead -= 32;
+  }
+  // what was found becomes what is issued
+  __device__ __forceinline__ void turn() {
+    cell = kNone;
+    if (in != kNone) {
+      if ((unsigned)e < a.n_gpu)
+        cell = (unsigned)e * a.block_cells + in;
+      else if (e < 0 && ~(unsigned)e < a.n_host)
+        cell = (~(unsigned)e * (unsigned)(a.heads * a.cells) + in) | kHost;
+      else
+        flag(a.status, SKV_DEV_BAD_SLOT);
+    }
+    find();
+  }
+  __device__ __forceinline__ void copy(const void* kp, const void* vp, uint32_t c) {
+    const int lane = threadIdx.x & 31;
+    const size_t off = (size_t)c * kCell + lane * 16;
+    const unsigned char *k = (const unsigned char*)kp + off, *v = (const unsigned char*)vp + off;
+    cp_async_cg16(to, k);
+    cp_async_cg16(to + 512, k + 512);
     if (V) {
-      cp_async_cg16(to + kv4_cell(NG) + v_at, vs);
-      cp_async_cg16(to + kv4_cell(NG) + v_at + 512, vs + 512);
+      cp_async_cg16(to + kCell, v);
+      cp_async_cg16(to + kCell + 512, v + 512);
     }
     if (lane < 4 * NG) {
-      cp_async_cg16(dst + 1024, ks + 1024);
-      if (V) cp_async_cg16(dst + kv4_cell(NG) + 1024, vs + 1024);
+      cp_async_cg16(to + 1024, k + 1024);
+      if (V) cp_async_cg16(to + kCell + 1024, v + 1024);
     }
   }
   __device__ __forceinline__ void issue() {
-    bad <<= 1;
-    if (left > 0) {
-      if ((unsigned)e < a.n_gpu) {
-        const size_t at = (size_t)(unsigned)e * a.block_bytes + in * kv4_cell(NG);
-        copy(k + at, v + at);
-      } else if (e < 0 && ~(unsigned)e < a.n_host) {
-        const size_t at = (((size_t)~(unsigned)e * a.heads + c.h) * a.cells + in) * kv4_cell(NG) + (threadIdx.x & 31) * 16;
-        copy((const unsigned char*)a.pool.host_k + at, (const unsigned char*)a.pool.host_v + at);
-      } else {
-        if ((threadIdx.x & 31) == 0) flag(a.status, SKV_DEV_BAD_SLOT);
-        bad |= 1u;
+    gone <<= 1;
+    if (lane_up < left) {
+      if (lane_up == 32) {
+        left -= 32;
+        lane_up = 0;
+        turn();
       }
-      if (--left > 0) {
-        c.tile += kW;
-        if (c.tile >= c.nt) {
-          enter();
-        } else {
-          block += a.step_blocks;
-          in += a.step_cells;
-          if (in >= a.cells) in -= a.cells, ++block;
-          e = __ldg(row + block);
-        }
-      }
+      const uint32_t c = __shfl_sync(0xffffffffu, cell, lane_up++);
+      if (c < kHost)
+        copy(a.pool.gpu_k, a.pool.gpu_v, c);
+      else if (c != kNone)
+        copy(a.pool.host_k, a.pool.host_v, c & ~kHost);
+      else
+        gone |= 1u;
     }
     cp_async_commit();
     to = to + kStage == end ? end - S * kStage : to + kStage;
   }
-  // tile `tile` of a request of L positions, S - 1 issues ago
-  __device__ __forceinline__ uint32_t live(int L, int tile, int) const {
-    if (bad >> (S - 1) & 1u) return 0u;
+  // of tile `tile` of a request of L positions, S - 1 issues ago
+  __device__ __forceinline__ uint32_t rows(int L, int tile, int) const {
     const int n = L - (tile << 4);
-    return n >= 16 ? 0xffffu : (1u << n) - 1u;
+    return gone >> (S - 1) & 1u ? 0u : n >= 16 ? 0xffffu : (1u << n) - 1u;
   }
 };
 
-// Single rows: a list's tiles.  Lanes 0 .. 15 (and 16 .. 31 with them) find a row each, a step an
-// issue: its place's position, that one's entry, the row -- so each load has a tile's time to arrive.
-template <int MODE, int NG, bool V, int S>
+// A list's tiles: rows, by 16-byte copies.  A lane finds a row of two tiles (this warp's next and the one
+// after) in three steps -- its place's position, that one's entry, the row -- so each load has two
+// tiles' time to arrive.
+template <int NG, int S>
 struct RowFeeder {
-  static constexpr int kStage = 2 * kv4_cell(NG);
+  static constexpr int kCell = kv4_cell(NG), kStage = 2 * kCell;
   const Kv4Args& a;
-  uint32_t to, end, v_at;
   uint32_t* masks;
-  Cursor c;  // the tile whose positions are found next
-  int left, slot;
-  Row r1, r0;  // position on its way; entry on its way
+  uint32_t to, end;  // the next stage; past the last one
+  Cursor c;  // this half warp's next tile
+  int left, half;
+  uint32_t row;  // this lane's, of the tiles that are issued; then: position on its way, entry on its way
+  Row r1, r0;
 
-  __device__ __forceinline__ RowFeeder(const Kv4Args& args, uint32_t ring, uint32_t* masks_, Cursor at, int n)
-      : a(args), to(ring), end(ring + S * kStage), v_at(v_chunk_at(threadIdx.x & 31)), masks(masks_), c(at), left(n),
-        slot(0) {
-    if (left > 0) settle<MODE>(a, c);
-    position();
-    advance();
-  }
-  __device__ __forceinline__ void position() {
-    row_position(a, c, left > 0, threadIdx.x & 15, r1);
-    if (--left > 0) {
-      c.tile += kW;
-      if (c.tile >= c.nt) settle<MODE>(a, c);
-    }
-  }
-  __device__ __forceinline__ void advance() {
-    r0 = r1;
-    row_entry(a, (threadIdx.x & 31) < 16, r0);
-    position();
+  __device__ __forceinline__ RowFeeder(const Kv4Args& args, Cursor&, uint32_t* masks_, uint32_t ring_, Cursor at, int n)
+      : a(args), masks(masks_), to(ring_), end(ring_ + S * kStage), c(at), left(n), half(-2), row(kNoRow) {
+    c.tile += (threadIdx.x >> 4 & 1) * kW;
+    left -= threadIdx.x >> 4 & 1;
+    r0.t = r1.t = -1;
   }
   __device__ __forceinline__ void issue() {
     const int lane = threadIdx.x & 31;
-    const uint32_t row = row_id(a, lane < 16, r0);
-    const uint32_t live = __ballot_sync(0xffffffffu, row != kNoRow) & 0xffffu;
-    if (lane == 0) masks[slot] = live;
+    if (half <= 0) {  // (at the start: three times)
+#pragma unroll 1
+      for (; half <= 0; ++half) {
+        row = row_id(a, true, r0);
+        r0 = r1;
+        row_entry(a, true, r0);
+        if (left > 0 && c.tile >= c.nt) settle<kList>(a, c);
+        row_position(a, c, left > 0, lane & 15, r1);
+        left -= 2;
+        c.tile += 2 * kW;
+      }
+      half = 0;
+    }
+    const uint32_t live = __ballot_sync(0xffffffffu, row != kNoRow) >> (16 * half) & 0xffffu;
+    if (lane == 0) masks[(to - (end - S * kStage)) / kStage] = live;
     auto at = [&](uint32_t r, bool v) {  // the row's cell
       const unsigned char* base = (const unsigned char*)(r >> 31 ? (v ? a.pool.host_v : a.pool.host_k)
                                                                  : (v ? a.pool.gpu_v : a.pool.gpu_k));
-      return base + (size_t)(r >> 4 & 0x7ffffffu) * kv4_cell(NG);
+      return base + (size_t)(r >> 4 & 0x7ffffffu) * kCell;
     };
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t r = __shfl_sync(0xffffffffu, row, (lane >> 2) + 8 * i);
+    for (int j = 0; j < 2; ++j) {  // rows 8 j .. 8 j + 7, four lanes each
+      const uint32_t r = __shfl_sync(0xffffffffu, row, (lane >> 2) + 8 * j + 16 * half);
       if (r != kNoRow) {
         const int off = (int)(r & 15u) * kCodeBytes + (lane & 3) * 16;
-        cp_async_cg16(to + lane * 16 + 512 * i, at(r, false) + off);
-        cp_async_cg16(to + kv4_cell(NG) + v_at + 512 * i, at(r, true) + off);
+        cp_async_cg16(to + lane * 16 + 512 * j, at(r, false) + off);
+        cp_async_cg16(to + kCell + lane * 16 + 512 * j, at(r, true) + off);
       }
     }
-    if (row != kNoRow) {
-      const uint32_t dst = to + (lane >= 16 ? kv4_cell(NG) : 0) + 16 * kCodeBytes + (lane & 15) * 4 * NG;
-      const unsigned char* src = at(row, lane >= 16) + 16 * kCodeBytes + (row & 15u) * 4 * NG;
+    const uint32_t r = __shfl_sync(0xffffffffu, row, (lane & 15) + 16 * half);
+    if (r != kNoRow) {  // K's words, V's
+      const uint32_t dst = to + (lane >> 4) * kCell + 16 * kCodeBytes + (lane & 15) * 4 * NG;
+      const unsigned char* src = at(r, lane >= 16) + 16 * kCodeBytes + (r & 15u) * 4 * NG;
       if (NG == 4)
         cp_async_cg16(dst, src);
       else
         cp_async_ca<4 * NG>(dst, src);
     }
     cp_async_commit();
+    half = half == 0 ? 1 : 0;
     to = to + kStage == end ? end - S * kStage : to + kStage;
-    slot = slot == S - 1 ? 0 : slot + 1;
-    advance();
   }
-  __device__ __forceinline__ uint32_t live(int, int, int stage) const { return masks[stage]; }
+  __device__ __forceinline__ uint32_t rows(int, int, int stage) const { return masks[stage]; }
 };
 
 // ---------------------------------------------------------------------------- the products
@@ -428,12 +462,12 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(addr));
   return u;
 }
-template <int NG>
+template <int N>
 __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* w) {
-  if constexpr (NG == 4) {
+  if constexpr (N == 4) {
     const uint4 u = lds128(addr);
     w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-  } else if constexpr (NG == 2) {
+  } else if constexpr (N == 2) {
     const uint2 u = lds64(addr);
     w[0] = u.x, w[1] = u.y;
   } else {
@@ -469,137 +503,112 @@ struct QFrag {
   float unit[NT][2];  // what a logit of heads 2 t, 2 t + 1 comes in: 2^20 / their power of two
 };
 
-// the column's entries 16 j + 4 t .. + 3 for this lane are x[j][0..3], already under a power of
-// two; a register's pairs are entries 0 and 2, 1 and 3
-__device__ __forceinline__ void column(const float (&x)[8][4], uint32_t (&b)[8][2]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    b[j][0] = pack_f16(16.f * x[j][0], 16.f * x[j][2]);
-    b[j][1] = pack_f16(x[j][1], x[j][3]);
-  }
-}
-// what a word's halves meet: sums over the groups, of lane t the t-th group's
-template <int NG>
-__device__ __forceinline__ void column_sums(const float (&x)[8][4], uint32_t (&wz)[3], bool on) {
-  const int t = threadIdx.x & 3;
-  float part[NG], z = 0.f;
-#pragma unroll
-  for (int g = 0; g < NG; ++g) part[g] = 0.f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) part[j * NG / 8] += (x[j][0] + x[j][1]) + (x[j][2] + x[j][3]);
-#pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    part[g] += __shfl_xor_sync(0xffffffffu, part[g], 1);
-    part[g] += __shfl_xor_sync(0xffffffffu, part[g], 2);
-    if (g == t) z = part[g];
-  }
-  // in the products' unit
-  z = on && t < NG ? z * 0x1p-20f : 0.f;
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const float h = __bfloat162float(__float2bfloat16_rn(z));
-    wz[i] = tc::pack_bf16(-8.f * h, h);
-    z -= h;
-  }
-}
+// A CTA makes them together, warp j the j-th k-step, and every warp takes its lanes' copies.
+template <int NT>
+struct QShared {
+  uint32_t b[NT][8][2][32], wz[NT][3][32];
+  float largest[8 * NT][kW], part[8][8 * NT];  // of a head: of each warp's entries; sums of a k-step
+};
 
-// the largest |x| of a column (its four lanes hold all entries)
-__device__ __forceinline__ float largest(const float (&x)[8][4]) {
-  float m = 0.f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(x[j][i]));
-  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-}
-
-__device__ __forceinline__ void load_q4(const __nv_bfloat16* p, float (&x)[4]) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  x[0] = __uint_as_float(u.x << 16);
-  x[1] = __uint_as_float(u.x & 0xffff0000u);
-  x[2] = __uint_as_float(u.y << 16);
-  x[3] = __uint_as_float(u.y & 0xffff0000u);
-}
-
-// heads j0 .. j0 + n of a request's queries as columns
-template <int NG, int NT>
-__device__ __forceinline__ void load_heads(const __nv_bfloat16* q, int n, QFrag<NT>& f) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+// MEAN: the mean of the n heads in three fp16 parts, columns 0, 1 and 2; else a column a head.
+template <int NG, int NT, bool MEAN>
+__device__ __forceinline__ void make_queries(const __nv_bfloat16* q, int n, QShared<NT>& s, QFrag<NT>& f) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  float x[NT][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    float x[8][4];
-    const bool on = 8 * nt + g < n;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[j][i] = 0.f;
-      if (on) load_q4(q + (size_t)(8 * nt + g) * kD + 16 * j + 4 * t, x[j]);
+    for (int i = 0; i < 4; ++i) x[nt][i] = 0.f;
+    const int head = 8 * nt + g;
+#pragma unroll 1
+    for (int h = MEAN ? 0 : head; h < n; ++h) {
+      const uint2 u = *reinterpret_cast<const uint2*>(q + (size_t)h * kD + 16 * warp + 4 * t);
+      x[nt][0] += __uint_as_float(u.x << 16);
+      x[nt][1] += __uint_as_float(u.x & 0xffff0000u);
+      x[nt][2] += __uint_as_float(u.y << 16);
+      x[nt][3] += __uint_as_float(u.y & 0xffff0000u);
+      if (!MEAN) break;
     }
-    const float s = fit(largest(x));
+    if (MEAN) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+      for (int i = 0; i < 4; ++i) x[nt][i] /= (float)n;
+    }
+    float m = fmaxf(fmaxf(fabsf(x[nt][0]), fabsf(x[nt][1])), fmaxf(fabsf(x[nt][2]), fabsf(x[nt][3])));
+    float sum = (x[nt][0] + x[nt][1]) + (x[nt][2] + x[nt][3]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[j][i] *= s;
-    column(x, f.b[nt]);
-    column_sums<NG>(x, f.wz[nt], true);
-    const float u = 0x1p20f / s;
-    f.unit[nt][0] = __shfl_sync(0xffffffffu, u, 8 * t);
-    f.unit[nt][1] = __shfl_sync(0xffffffffu, u, 8 * t + 4);
+    for (int off = 1; off <= 2; off <<= 1) {
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+      sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    }
+    if (t == 0) {
+      s.largest[head][warp] = m;
+      s.part[warp][head] = sum;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int head = 8 * nt + g;
+    const float4* lg = reinterpret_cast<const float4*>(s.largest[head]);
+    const float4 u = lg[0], v = lg[1];
+    const float scale = fit(fmaxf(fmaxf(fmaxf(u.x, u.y), fmaxf(u.z, u.w)), fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w))));
+    const float unit = 0x1p20f / scale;
+    f.unit[nt][0] = __shfl_sync(0xffffffffu, unit, 8 * t);
+    f.unit[nt][1] = __shfl_sync(0xffffffffu, unit, 8 * t + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float y = x[nt][i] * scale;
+      if (MEAN) {
+#pragma unroll 1
+        for (int k = 0; k < 3; ++k) {
+          const float h = __half2float(__float2half_rn(y));
+          if (k == g) x[nt][i] = h;
+          y -= h;
+        }
+        if (g >= 3) x[nt][i] = 0.f;
+      } else {
+        x[nt][i] = y;
+      }
+    }
+    s.b[nt][warp][0][lane] = pack_f16(16.f * x[nt][0], 16.f * x[nt][2]);
+    s.b[nt][warp][1][lane] = pack_f16(x[nt][1], x[nt][3]);
+    if (warp == 0) {  // the t-th group's sum, in the products' unit
+      float z = 0.f;
+      if (t < NG && (!MEAN || g == 0)) {
+#pragma unroll 1
+        for (int j = t * 8 / NG; j < (t + 1) * 8 / NG; ++j) z += s.part[j][head];
+      }
+      z *= scale * 0x1p-20f;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const float h = __bfloat162float(__float2bfloat16_rn(z));
+        s.wz[nt][i][lane] = tc::pack_bf16(-8.f * h, h);
+        z -= h;
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f.b[nt][j][0] = s.b[nt][j][0][lane], f.b[nt][j][1] = s.b[nt][j][1][lane];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) f.wz[nt][i] = s.wz[nt][i][lane];
   }
 }
 
-// the mean of n heads in three fp16 parts, columns 0, 1 and 2
-template <int NG>
-__device__ __forceinline__ void load_mean(const __nv_bfloat16* q, int n, QFrag<1>& f) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  float x[8][4];
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[j][i] = 0.f;
-  for (int h = 0; h < n; ++h)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float y[4];
-      load_q4(q + (size_t)h * kD + 16 * j + 4 * t, y);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[j][i] += y[i];
-    }
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[j][i] /= (float)n;
-  const float s = fit(largest(x));
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[j][i] *= s;
-  column_sums<NG>(x, f.wz[0], g == 0);
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float y = x[j][i], part = 0.f;
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const float h = __half2float(__float2half_rn(y));
-        if (k == g) part = h;
-        y -= h;
-      }
-      x[j][i] = part;
-    }
-  column(x, f.b[0]);
-  f.unit[0][0] = f.unit[0][1] = 0x1p20f / s;
-}
+// The key of the operands' row r: every second pair exchanged, so that the 16-byte loads of K's
+// codes meet no bank twice (rows 2 i and 2 i + 1 half a line apart) and the 8-byte loads of V's,
+// at rows 0, 2, 4, 6, only in pairs.
+__device__ __forceinline__ int key_of(int r) { return r ^ (r >> 1 & 1); }
 
-// The logits of a tile, in the columns' units: c[nt][0..1] key g of heads 2 t, 2 t + 1; [2..3] key g + 8.
-// A row's logits depend on that row alone: those of rows that are not there are anything.
+// The logits of a cell, in the columns' units: c[nt][0..1] key key_of(g) of heads 2 t, 2 t + 1; [2..3]
+// the key 8 on.  A row's logits depend on that row alone: those of rows that are not there are anything.
 template <int NG, int NT>
-__device__ __forceinline__ void logits(uint32_t stage, const QFrag<NT>& f, float (&c)[NT][4]) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const uint4 k0 = lds128(stage + g * kCodeBytes + t * 16), k1 = lds128(stage + (g + 8) * kCodeBytes + t * 16);
-  const uint32_t words = stage + 16 * kCodeBytes;
+__device__ __forceinline__ void logits(uint32_t cell, const QFrag<NT>& f, float (&c)[NT][4]) {
+  const int lane = threadIdx.x & 31, g = key_of(lane >> 2), t = lane & 3;
+  const uint4 k0 = lds128(cell + g * kCodeBytes + t * 16), k1 = lds128(cell + (g + 8) * kCodeBytes + t * 16);
+  const uint32_t words = cell + 16 * kCodeBytes;
   uint32_t w0[NG], w1[NG];
   lds_words<NG>(words + g * 4 * NG, w0);
   lds_words<NG>(words + (g + 8) * 4 * NG, w1);
@@ -645,11 +654,11 @@ __device__ __forceinline__ void logits(uint32_t stage, const QFrag<NT>& f, float
 
 // ---------------------------------------------------------------------------- attention
 
-// A warp's state of a unit: p_t = 2^(x_t - r), r = the running maximum + the steps' power - 7.
+// A warp's state of a unit: p_t = 2^(x_t + ref), ref = 7 - sigma - the running maximum.
 template <int NG, int NT>
 struct State {
-  float m[NT][2], l[NT][2];
-  float ref[NT][2], top[NT][2];  // -r; the logit in its column's unit past which the maximum moves
+  float l[NT][2], ref[NT][2];
+  float top[NT][2];   // the logit, in its column's unit, past which the maximum moves
   float o[NT][8][4];  // rows 2 g (2^-24 a unit) and 2 g + 1 (2^-20) of entries 16 i, columns heads 2 t, 2 t + 1
   float z[NT][NG][2];
   int sigma;          // steps are below 2^(sigma + 1)
@@ -663,10 +672,9 @@ __device__ __forceinline__ void clear(State<NG, NT>& s) {
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      s.m[nt][i] = kFloor;
+      s.l[nt][i] = 0.f;
       s.ref[nt][i] = -kFloor;
       s.top[nt][i] = kFloor;
-      s.l[nt][i] = 0.f;
 #pragma unroll
       for (int g = 0; g < NG; ++g) s.z[nt][g][i] = 0.f;
     }
@@ -678,17 +686,14 @@ __device__ __forceinline__ void clear(State<NG, NT>& s) {
   s.sigma = kSigmaMin;
 }
 
-// A maximum or a power of the steps that a tile has passed: everything in the new reference.
+// A maximum or a power of the steps that a cell has passed: everything in the new reference.
 template <int NG, int NT>
-__device__ __forceinline__ void rescale(State<NG, NT>& s, const float (&c)[NT][4], const float (&kf)[NT][2],
-                                        float smax) {
+__device__ __forceinline__ void rescale(State<NG, NT>& s, const float (&c)[NT][4], const float (&kf)[NT][2], float smax) {
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, off));
   int e = (int)((__float_as_uint(smax) >> 23) & 255u) - 127;
   e = e > kSigmaMax ? kSigmaMax : e;
   const int sigma = e > s.sigma ? e : s.sigma;
-  const float ds = (float)(s.sigma - sigma);
-  s.sigma = sigma;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     float f[2];
@@ -697,10 +702,10 @@ __device__ __forceinline__ void rescale(State<NG, NT>& s, const float (&c)[NT][4
       float m = fmaxf(c[nt][i], c[nt][i + 2]) * kf[nt][i];
 #pragma unroll
       for (int off = 4; off <= 16; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-      m = fmaxf(m, s.m[nt][i]);
-      f[i] = ex2(s.m[nt][i] - m + ds);
-      s.m[nt][i] = m;
-      s.ref[nt][i] = 7.f - (float)sigma - m;
+      m = fmaxf(m, (7.f - (float)s.sigma) - s.ref[nt][i]);  // (the floor stays about itself)
+      const float ref = (7.f - (float)sigma) - m;
+      f[i] = ex2(ref - s.ref[nt][i]);
+      s.ref[nt][i] = ref;
       s.top[nt][i] = (m + 7.f) / kf[nt][i];
       s.l[nt][i] *= f[i];
 #pragma unroll
@@ -711,43 +716,48 @@ __device__ __forceinline__ void rescale(State<NG, NT>& s, const float (&c)[NT][4
 #pragma unroll
       for (int j = 0; j < 4; ++j) s.o[nt][i][j] *= f[j & 1];
   }
+  s.sigma = sigma;
 }
 
+// A cell's keys into the state.  The weights p_t meet the centres in fp32 and, times the steps, the
+// codes on the tensor core.  Every other row's codes come as 15 - c and its weights negative:
+// w c - w' (15 - c') + 15 w'.  Codes are 7.5 on average, and a long sum of them on one side of zero would lose
+// to the tensor core's truncation what the centring takes off again (a million keys: 1 % of the
+// output).  With the codes' own 8, the even keys' stand 8 too high and the odd ones' 7 too low.
 template <int NG, int NT>
-__device__ __forceinline__ void attend_tile(uint32_t stage, uint32_t mask, const QFrag<NT>& f, const float (&kf)[NT][2],
+__device__ __forceinline__ void attend_cell(uint32_t cell, uint32_t mask, const QFrag<NT>& f, const float (&kf)[NT][2],
                                             State<NG, NT>& s) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  constexpr int kCell = kv4_cell(NG), kLook = NG == 4 ? 2 : 1;  // words a lane looks at for the largest step
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, key = key_of(g);
   float c[NT][4];
-  logits<NG, NT>(stage, f, c);
-  const uint32_t vc = stage + kv4_cell(NG), words = vc + 16 * kCodeBytes;
+  logits<NG, NT>(cell, f, c);
+  const uint32_t words = cell + kCell + 16 * kCodeBytes;
+  uint32_t look[kLook];
+  lds_words<kLook>(words + (NG == 1 ? lane & 15 : lane) * 4 * kLook, look);
+  float smax = fabsf(step_of(look[0]));
+  if (kLook == 2) smax = fmaxf(smax, fabsf(step_of(look[kLook - 1])));
   uint32_t w0[NG], w1[NG];
-  lds_words<NG>(words + g * 4 * NG, w0);
-  lds_words<NG>(words + (g + 8) * 4 * NG, w1);
-  const bool on0 = mask >> g & 1u, on1 = mask >> (g + 8) & 1u;
-  if (mask != 0xffffu) {
+  lds_words<NG>(words + key * 4 * NG, w0);
+  lds_words<NG>(words + (key + 8) * 4 * NG, w1);
+  if (mask != 0xffffu) {  // what lies in rows that are not there counts for nothing
+    const bool on0 = mask >> key & 1u, on1 = mask >> (key + 8) & 1u;
+    if (!(mask >> (NG == 1 ? lane & 15 : lane >> 1) & 1u)) smax = 0.f;
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
       w0[i] = on0 ? w0[i] : 0u;
       w1[i] = on1 ? w1[i] : 0u;
     }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[nt][i] = (i < 2 ? on0 : on1) ? c[nt][i] : -INFINITY;
   }
-  // (each lane of a quad looks at a group's step)
-  const uint32_t mine = words + (t & (NG - 1)) * 4;
-  const float smax = fmaxf(on0 ? fabsf(step_of(lds32(mine + g * 4 * NG))) : 0.f,
-                           on1 ? fabsf(step_of(lds32(mine + (g + 8) * 4 * NG))) : 0.f);
   bool past = smax >= __uint_as_float((uint32_t)(s.sigma + 128) << 23);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (mask != 0xffffu && !(i < 2 ? on0 : on1)) c[nt][i] = -INFINITY;
-      past |= c[nt][i] > s.top[nt][i & 1];
-    }
+    for (int i = 0; i < 2; ++i) past |= fmaxf(c[nt][i], c[nt][i + 2]) > s.top[nt][i];
   if (__any_sync(0xffffffffu, past)) rescale<NG, NT>(s, c, kf, smax);
-  // Every other key's codes come as 15 - c and its weights negative: w c - w' (15 - c') + 15 w'.  Codes
-  // are 7.5 on average, and a long sum of them on one side of zero would lose to the tensor core's
-  // truncation what the centring takes off again (a million keys: 1 % of the output).  With the
-  // codes' own 8, the even keys' stand 8 too high and the odd ones' 7 too low.
   const float off = g & 1 ? 7.f : -8.f, sign = g & 1 ? -1.f : 1.f;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -769,12 +779,11 @@ __device__ __forceinline__ void attend_tile(uint32_t stage, uint32_t mask, const
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[nt][i] *= sign;
-  // the second product: weights times steps, transposed, a group at a time
   uint2 v[4];
-  {
-    const uint32_t row = vc + t * kCodeBytes + (v_chunk(t, g >> 1) << 4) + ((g & 1) << 3);
+  {  // the keys of rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9: two apart from each other's, in one order or the other
+    const uint32_t row = cell + kCell + 2 * t * kCodeBytes + (g << 3), even = (t & 1) * kCodeBytes, odd = kCodeBytes - even;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = lds64(row + i * 4 * kCodeBytes);  // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+    for (int i = 0; i < 4; ++i) v[i] = lds64(row + (i & 1 ? odd : even) + (i >> 1) * 8 * kCodeBytes);
     v[1] = make_uint2(~v[1].x, ~v[1].y);
     v[3] = make_uint2(~v[3].x, ~v[3].y);
   }
@@ -805,13 +814,13 @@ __device__ __forceinline__ void attend_tile(uint32_t stage, uint32_t mask, const
 
 template <int NG, int NT>
 struct AttnShape {
-  // Stages and CTAs a SM: one column tile, 16 warps with two tiles of 2.5 KB ahead of them each;
-  // two column tiles take the registers of two CTAs, and one stage more.
-  static constexpr int kStages = NT == 1 ? 3 : 4;
+  // Stages of 2.5 KB a warp and CTAs a SM: one column tile, 16 warps a SM with up to four tiles each
+  // on their way; two column tiles take the registers of two CTAs.
+  static constexpr int kStages = NT == 1 ? 4 : 6;
   static constexpr int kCtas = NT == 1 ? 2 : 1;
   static constexpr int kRing = kW * kStages * 2 * kv4_cell(NG);
   static constexpr int kRow = kD + 4;  // floats of a head's partial row: heads 2 t, 2 t + 2 an eighth of the banks apart
-  static constexpr int kOut = kW * 8 * NT * kRow * 4;
+  static constexpr int kOut = kW / 2 * 8 * NT * kRow * 4;
   static constexpr int kSmem = kRing + kOut;
 };
 
@@ -821,97 +830,124 @@ struct Pick {
 };
 template <int NG, int S>
 struct Pick<kList, NG, S> {
-  using type = RowFeeder<kList, NG, true, S>;
+  using type = RowFeeder<NG, S>;
 };
 
 template <int NG, int NT, int MODE>
 __global__ void __launch_bounds__(32 * kW, AttnShape<NG, NT>::kCtas) kv4_attn_kernel(const Kv4Args a) {
   using Shape = AttnShape<NG, NT>;
   constexpr int S = Shape::kStages, HC = 8 * NT;  // columns
+  constexpr int kStage = 2 * kv4_cell(NG);
   extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ Cursor s_at[kW];
   __shared__ uint32_t s_mask[MODE == kList ? kW : 1][S];
   __shared__ float2 s_ml[kW][HC], s_tot[HC];
   __shared__ float s_f[HC][kW];
+  __shared__ __align__(16) QShared<NT> s_q;
   float* s_o = reinterpret_cast<float*>(smem + Shape::kRing);
   pdl_release();
   pdl_wait();
-  long long T, t0, t1;
-  int n;
   Cursor u;
-  find_share<MODE>(a, kW, &T, &n, &t0, &t1, &u);
-  if (t1 <= t0) return;
+  const Share mine = find_share<MODE, 32 * kW>(a, &u);
+  if (mine.tiles == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int mine = t1 - t0 > warp ? (int)((t1 - t0 - warp + kW - 1) / kW) : 0;
+  const int share = mine.tiles;
   Cursor at = u;
   at.tile += warp;
-  constexpr uint32_t kStage = 2 * kv4_cell(NG);
   const uint32_t ring = smem_u32(smem) + warp * S * kStage;
-  typename Pick<MODE, NG, S>::type feed(a, ring, s_mask[MODE == kList ? warp : 0], at, mine);
+  typename Pick<MODE, NG, S>::type feed(a, s_at[warp], s_mask[MODE == kList ? warp : 0], ring, at,
+                                        share > warp ? (share - warp + kW - 1) / kW : 0);
 #pragma unroll 1
   for (int i = 0; i < S - 1; ++i) feed.issue();
-  int next = warp, seg = 0, stage = 0;  // next: this warp's next tile of the share
-  for (long long f = t0; f < t1; ++seg) {
-    const long long first = f - u.tile, end = first + u.nt < t1 ? first + u.nt : t1;
+  long long place = mine.place;  // of the unit among the weights
+  int stage = 0;
+  // units of the share: tiles [from, to) of it, the unit's first at `base`
+  for (int from = 0, seg = 0; from < share; ++seg) {
+    const int base = from - u.tile, to = u.nt - u.tile < share - from ? base + u.nt : share;
     QFrag<NT> q;
-    load_heads<NG, NT>(a.q + ((size_t)u.b * a.Hq + (size_t)u.h * a.G) * kD, a.G, q);
     float kf[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) kf[nt][0] = q.unit[nt][0] * a.scale_log2, kf[nt][1] = q.unit[nt][1] * a.scale_log2;
     State<NG, NT> s;
     clear(s);
-    const int last = (int)(end - t0), base = (int)(first - t0);  // (a share has fewer tiles than 2^31)
-    for (; next < last; next += kW) {
-      cp_async_wait<S - 2>();
-      __syncwarp();
-      feed.issue();  // into the stage of the tile before this one
-      const uint32_t mask = feed.live(u.L, next - base, stage);
-      if (mask != 0u) attend_tile<NG, NT>(ring + stage * kStage, mask, q, kf, s);
-      stage = stage == S - 1 ? 0 : stage + 1;
-    }
-    // the warp's sums, then the CTA's
-    float* row = s_o + warp * HC * Shape::kRow;
+    make_queries<NG, NT, false>(a.q + ((size_t)u.b * a.Hq + (size_t)u.h * a.G) * kD, a.G, s_q, q);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int head = 8 * nt + 2 * t + i;
+      for (int i = 0; i < 2; ++i) kf[nt][i] = q.unit[nt][i] * a.scale_log2;
+    // this warp's tiles
+#pragma unroll 1
+    for (int i = from + ((warp - from) & (kW - 1)); i < to; i += kW) {
+      cp_async_wait<S - 2>();
+      __syncwarp();
+      feed.issue();  // into the stage of the tile before this one
+      const uint32_t mask = feed.rows(u.L, i - base, stage);
+      if (mask != 0u) attend_cell<NG, NT>(ring + stage * kStage, mask, q, kf, s);
+      stage = stage == S - 1 ? 0 : stage + 1;
+    }
+    // the warp's sums, then the CTA's: every warp's output under the CTA's reference, the upper
+    // warps' rows added to by the lower ones
+#pragma unroll 1
+    for (int off = 4; off <= 16; off <<= 1) {
 #pragma unroll
-        for (int off = 4; off <= 16; off <<= 1) {
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
           s.l[nt][i] += __shfl_xor_sync(0xffffffffu, s.l[nt][i], off);
 #pragma unroll
           for (int k = 0; k < NG; ++k) s.z[nt][k][i] += __shfl_xor_sync(0xffffffffu, s.z[nt][k][i], off);
         }
-        if (g == 0) s_ml[warp][head] = make_float2(s.m[nt][i] + ((float)s.sigma - 7.f), s.l[nt][i]);
+    }
+    if (g == 0) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float z = s.z[nt][j * NG / 8][i];
-          *reinterpret_cast<float2*>(row + head * Shape::kRow + 16 * j + 2 * g) =
-              make_float2(fmaf(s.o[nt][j][i], 0x1p24f, z), fmaf(s.o[nt][j][i + 2], 0x1p20f, z));
-        }
-      }
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) s_ml[warp][8 * nt + 2 * t + i] = make_float2(-s.ref[nt][i], s.l[nt][i]);
+    }
     __syncthreads();
     if (threadIdx.x < HC * kW) {
       const int head = threadIdx.x >> 3, w = threadIdx.x & 7;
-      const float2 v = s_ml[w][head];
-      float m = v.x;
+      const float2 x = s_ml[w][head];
+      float m = x.x;
 #pragma unroll
       for (int off = 1; off < 8; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-      const float fw = ex2(v.x - m);
-      float l = fw * v.y;
+      const float fw = ex2(x.x - m);
+      float l = fw * x.y;
 #pragma unroll
       for (int off = 1; off < 8; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
       s_f[head][w] = fw;
       if (w == 0) s_tot[head] = make_float2(m, l);
     }
     __syncthreads();
-    const bool whole = first >= t0 && first + u.nt <= t1;
+    float* out = s_o + warp % (kW / 2) * HC * Shape::kRow + 2 * g;
+#pragma unroll 1
+    for (int half = 1; half >= 0; --half) {
+      if (warp / (kW / 2) == half) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int head = 8 * nt + 2 * t + i;
+            const float fw = s_f[head][warp];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              float2* to_row = reinterpret_cast<float2*>(out + head * Shape::kRow + 16 * j);
+              const float z = s.z[nt][j * NG / 8][i];
+              const float2 y = half ? make_float2(0.f, 0.f) : *to_row;
+              *to_row = make_float2(fmaf(fw, fmaf(s.o[nt][j][i], 0x1p24f, z), y.x),
+                                    fmaf(fw, fmaf(s.o[nt][j][i + 2], 0x1p20f, z), y.y));
+            }
+          }
+      }
+      __syncthreads();
+    }
+    const bool whole = base >= 0 && base + u.nt <= share;
     const size_t hq = (size_t)u.b * a.Hq + (size_t)u.h * a.G;
     float* slot = a.ws + ((size_t)blockIdx.x * 2 + (seg > 0)) * kSlotFloats;
     const int d = threadIdx.x & (kD - 1);
+#pragma unroll 1
     for (int head = threadIdx.x / kD; head < a.G; head += 32 * kW / kD) {
       float o = 0.f;
 #pragma unroll
-      for (int w = 0; w < kW; ++w) o = fmaf(s_f[head][w], s_o[(w * HC + head) * Shape::kRow + d], o);
+      for (int w = 0; w < kW / 2; ++w) o += s_o[(w * HC + head) * Shape::kRow + d];
       const float2 tot = s_tot[head];
       if (whole) {
         a.out[(hq + head) * kD + d] = __float2bfloat16_rn(tot.y == 0.f ? 0.f : o / tot.y);
@@ -921,16 +957,17 @@ __global__ void __launch_bounds__(32 * kW, AttnShape<NG, NT>::kCtas) kv4_attn_ke
         if (d == 0) *reinterpret_cast<float2*>(slot + 16 * kD + 2 * head) = tot;
       }
     }
-    if (threadIdx.x == 0 && first >= t0)
-      a.desc[(size_t)u.b * a.H + u.h] = make_int2((int)blockIdx.x | (seg > 0 ? 1 << 30 : 0), holder(T, n, first + u.nt - 1));
+    if (threadIdx.x == 0 && base >= 0)
+      a.desc[(size_t)u.b * a.H + u.h] =
+          make_int2((int)blockIdx.x | (seg > 0 ? 1 << 30 : 0), holder(mine.weight, mine.ctas, place + kUnit + u.nt - 1));
     __syncthreads();
-    f = end;
-    if (f < t1) {
+    from = to;
+    if (from < share) {
+      place += kUnit + u.nt;
       u.tile = u.nt;
       settle<MODE>(a, u);
     }
   }
-  cp_async_wait<0>();
 }
 
 // The units that no CTA held alone: their partials joined, a CTA a head; the empty ones: zeros.
@@ -986,91 +1023,91 @@ __global__ void __launch_bounds__(kD) kv4_merge_kernel(const Kv4Args a) {
 
 // ---------------------------------------------------------------------------- scores
 
-constexpr int kScoreStages = 4;
+// Stages of 1.25 KB a warp and CTAs a SM.
+constexpr int kScoreStages = 6, kScoreCtas = 3;
 
 template <int NG, int NT, int AGG>
-__global__ void __launch_bounds__(32 * kW, 2) kv4_score_kernel(const Kv4Args a) {
-  constexpr int S = kScoreStages;
+__global__ void __launch_bounds__(32 * kW, NT == 1 ? kScoreCtas : 2) kv4_score_kernel(const Kv4Args a) {
+  constexpr int S = kScoreStages, kCell = kv4_cell(NG);
   extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ Cursor s_at[kW];
+  __shared__ __align__(16) QShared<NT> s_q;
   pdl_release();
   pdl_wait();
-  long long T, t0, t1;
-  int n;
   Cursor u;
-  find_share<kScore>(a, kW, &T, &n, &t0, &t1, &u);
-  if (t1 <= t0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int mine = t1 - t0 > warp ? (int)((t1 - t0 - warp + kW - 1) / kW) : 0;
+  const Share mine = find_share<kScore, 32 * kW>(a, &u);
+  if (mine.tiles == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = key_of(lane >> 2), t = lane & 3;
+  const int share = mine.tiles;
   Cursor at = u;
   at.tile += warp;
-  const uint32_t ring = smem_u32(smem) + warp * S * kv4_cell(NG);
-  CellFeeder<kScore, NG, false, S> feed(a, ring, nullptr, at, mine);
+  const uint32_t ring = smem_u32(smem) + warp * S * kCell;
+  CellFeeder<kScore, NG, false, S> feed(a, s_at[warp], nullptr, ring, at, share > warp ? (share - warp + kW - 1) / kW : 0);
 #pragma unroll 1
   for (int i = 0; i < S - 1; ++i) feed.issue();
-  int next = warp, stage = 0;
-  for (long long f = t0; f < t1;) {
-    const long long first = f - u.tile, end = first + u.nt < t1 ? first + u.nt : t1;
-    const int last = (int)(end - t0);
-    if (next < last) {
-      QFrag<NT> q;
-      const __nv_bfloat16* qp = a.q + ((size_t)u.b * a.H + u.h) * a.Gi * kD;
-      if constexpr (AGG == SKV_AGG_MEAN)
-        load_mean<NG>(qp, a.Gi, q);
-      else
-        load_heads<NG, NT>(qp, a.Gi, q);
-      const Regions rg = regions_of(u.L, a.ns, a.nl);
-      const int rows = AGG == SKV_AGG_HEAD ? a.Gi : 1;  // score rows of the unit
-      float* out = a.scores + ((size_t)u.b * a.H + u.h) * rows * a.max_len;
-      int k0 = (rg.s_end & ~15) + (next - (int)(first - t0)) * 16 + g;
-      for (; next < last; next += kW, k0 += 16 * kW) {
-        cp_async_wait<S - 2>();
-        __syncwarp();
-        feed.issue();
-        const bool there = !(feed.bad >> (S - 1) & 1u);
-        float c[NT][4];
-        logits<NG, NT>(ring + stage * kv4_cell(NG), q, c);
-        stage = stage == S - 1 ? 0 : stage + 1;
+  int stage = 0;
+  for (int from = 0; from < share;) {
+    const int base = from - u.tile, to = u.nt - u.tile < share - from ? base + u.nt : share;
+    const Regions rg = regions_of(u.L, a.ns, a.nl);
+    const size_t unit = (size_t)u.b * a.H + u.h;
+    QFrag<NT> q;
+    make_queries<NG, NT, AGG == SKV_AGG_MEAN>(a.q + unit * a.Gi * kD, a.Gi, s_q, q);
+    int i = from + ((warp - from) & (kW - 1));
+    // the keys of this lane's rows: key, and 8 on
+    int key = (rg.s_end & ~15) + (i - base) * 16 + g;
+    float* out = a.scores + unit * (AGG == SKV_AGG_HEAD ? a.Gi : 1) * a.max_len + key;
+#pragma unroll 1
+    for (; i < to; i += kW, key += 16 * kW, out += 16 * kW) {
+      cp_async_wait<S - 2>();
+      __syncwarp();
+      feed.issue();
+      float c[NT][4];
+      logits<NG, NT>(ring + stage * kCell, q, c);
+      const bool gone = feed.gone >> (S - 1) & 1u;
+      stage = stage == S - 1 ? 0 : stage + 1;
+      if constexpr (AGG == SKV_AGG_HEAD) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {  // keys g, g + 8
-          const int key = k0 + 8 * i;
-          const bool in = key >= rg.s_end && key < rg.l_start;
-          if constexpr (AGG == SKV_AGG_HEAD) {
+        for (int half = 0; half < 2; ++half)
+          if (key + 8 * half >= rg.s_end && key + 8 * half < rg.l_start) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
                 const int head = 8 * nt + 2 * t + j;
-                if (in && head < a.Gi)
-                  out[(size_t)head * a.max_len + key] = there ? c[nt][2 * i + j] * q.unit[nt][j] : NAN;
+                if (head < a.Gi)
+                  out[(size_t)head * a.max_len + 8 * half] = gone ? NAN : c[nt][2 * half + j] * q.unit[nt][j];
               }
-          } else {
-            float v;
-            if constexpr (AGG == SKV_AGG_MAX) {
-              v = -INFINITY;
+          }
+      } else {
+        float x[2];
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
+        for (int half = 0; half < 2; ++half) {
+          if constexpr (AGG == SKV_AGG_MAX) {
+            x[half] = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  const float x = c[nt][2 * i + j] * q.unit[nt][j];
-                  if (8 * nt + 2 * t + j < a.Gi) v = max_nan(v, x);
-                }
-              v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, 1));
-              v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, 2));
-            } else {  // columns 0, 1 here, 2 in the next lane
-              v = (__shfl_down_sync(0xffffffffu, c[0][2 * i], 1) + c[0][2 * i + 1] + c[0][2 * i]) * q.unit[0][0];
-            }
-            if (t == 0 && in) out[key] = there ? v : NAN;
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                if (8 * nt + 2 * t + j < a.Gi) x[half] = max_nan(x[half], c[nt][2 * half + j] * q.unit[nt][j]);
+            x[half] = max_nan(x[half], __shfl_xor_sync(0xffffffffu, x[half], 1));
+            x[half] = max_nan(x[half], __shfl_xor_sync(0xffffffffu, x[half], 2));
+          } else {  // columns 0 and 1, and 2 (3: none), in neighbouring lanes
+            const float y = c[0][2 * half] + c[0][2 * half + 1];
+            x[half] = (y + __shfl_xor_sync(0xffffffffu, y, 1)) * q.unit[0][0];
           }
         }
+        // lane 0 of a quad writes the one key, lane 1 the other
+        const int mine_key = key + 8 * t;
+        if (t < 2 && mine_key >= rg.s_end && mine_key < rg.l_start) out[8 * t] = gone ? NAN : x[t & 1];
       }
     }
-    f = end;
-    if (f < t1) {
+    from = to;
+    if (from < share) {
       u.tile = u.nt;
       settle<kScore>(a, u);
     }
+    __syncthreads();  // the queries' words have been read
   }
-  cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------------------- gather
@@ -1136,8 +1173,7 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4Args a, T* k_o
 
 // ---------------------------------------------------------------------------- host
 
-Kv4Args kv4_args(const skv_problem& p, const void* q, const PoolView& pool, int group, const int32_t* idx,
-                 int32_t* status) {
+Kv4Args kv4_args(const skv_problem& p, const void* q, const PoolView& pool, const int32_t* idx, int32_t* status) {
   Kv4Args a = {};
   a.q = (const __nv_bfloat16*)q;
   a.pool = pool;
@@ -1158,9 +1194,7 @@ Kv4Args kv4_args(const skv_problem& p, const void* q, const PoolView& pool, int 
   a.shift = -1;
   for (int i = 4; i < 31; ++i)
     if (p.block_size == 1 << i) a.shift = i;
-  a.step_blocks = kW / a.cells;
-  a.step_cells = kW % a.cells;
-  a.block_bytes = (unsigned)((pool.per_head ? 1 : a.heads) * a.cells * kv4_cell(kD / group));
+  a.block_cells = (unsigned)((pool.per_head ? 1 : a.heads) * a.cells);
   a.n_gpu = (unsigned)pool.n_gpu;
   a.n_host = pool.host_k != nullptr ? (unsigned)pool.n_host : 0u;
   a.agg = p.group_agg;
@@ -1170,9 +1204,10 @@ Kv4Args kv4_args(const skv_problem& p, const void* q, const PoolView& pool, int 
   return a;
 }
 
-// CTAs for at most `tiles` tiles: all that are resident at once, a tile a warp at least
-unsigned grid_of(long long tiles, int ctas) {
-  long long n = (tiles + kW - 1) / kW, most = (long long)num_sms() * ctas;
+// CTAs for at most `units` units of `tiles` tiles: all that are resident at once, two tiles a warp (or a
+// unit's start) at least
+unsigned grid_of(long long units, long long tiles, int ctas) {
+  long long n = (units * (tiles + kUnit) + 2 * kW - 1) / (2 * kW), most = (long long)num_sms() * ctas;
   if (most > kMaxParts) most = kMaxParts;
   n = n < most ? n : most;
   return (unsigned)(n < 1 ? 1 : n);
@@ -1184,7 +1219,7 @@ skv_status launch_attn(const Kv4Args& a, long long tiles, cudaStream_t st) {
   const auto kernel = kv4_attn_kernel<NG, NT, MODE>;
   const skv_status prep = prepare_kernel((const void*)kernel, Shape::kSmem);
   if (prep != SKV_OK) return prep;
-  if (launch_dependent(kernel, dim3(grid_of(tiles, Shape::kCtas)), dim3(32 * kW), Shape::kSmem, st, 1, a) !=
+  if (launch_dependent(kernel, dim3(grid_of((long long)a.B * a.H, tiles, Shape::kCtas)), dim3(32 * kW), Shape::kSmem, st, 1, a) !=
       cudaSuccess)
     return SKV_ERR_CUDA;
   SKV_LAUNCH_CHECK();
@@ -1203,7 +1238,7 @@ skv_status launch_scores(const Kv4Args& a, long long tiles, cudaStream_t st) {
   constexpr int kSmem = kW * kScoreStages * kv4_cell(NG);
   const skv_status prep = prepare_kernel((const void*)(wide ? kernel2 : kernel), kSmem);
   if (prep != SKV_OK) return prep;
-  if (launch_dependent(wide ? kernel2 : kernel, dim3(grid_of(tiles, 2)), dim3(32 * kW), kSmem, st, 1, a) != cudaSuccess)
+  if (launch_dependent(wide ? kernel2 : kernel, dim3(grid_of((long long)a.B * a.H, tiles, wide ? 2 : kScoreCtas)), dim3(32 * kW), kSmem, st, 1, a) != cudaSuccess)
     return SKV_ERR_CUDA;
   SKV_LAUNCH_CHECK();
   return SKV_OK;
@@ -1231,14 +1266,14 @@ size_t kv4_attn_workspace_bytes(const skv_problem& p) {
 
 skv_status launch_kv4_attn(const skv_problem& p, const void* q, const PoolView& pool, int group, const int32_t* idx,
                            void* out, float* lse, void* ws, int32_t* status, cudaStream_t st) {
-  Kv4Args a = kv4_args(p, q, pool, group, idx, status);
+  Kv4Args a = kv4_args(p, q, pool, idx, status);
   a.out = (__nv_bfloat16*)out;
   a.lse = lse;
   a.ws = (float*)ws;
   a.desc = reinterpret_cast<int2*>((unsigned char*)ws + parts_bytes());
   const bool list = idx != nullptr;
   const long long n = list ? (long long)p.n_sink + p.topk + p.n_local : p.max_len;
-  const long long tiles = (long long)a.B * a.H * ((n + 15) / 16);
+  const long long tiles = (n + 15) / 16;
 #define KV4_ATTN(NG)                                                                                            \
   (a.G > 8 ? (list ? launch_attn<NG, 2, kList>(a, tiles, st) : launch_attn<NG, 2, kDense>(a, tiles, st))        \
            : (list ? launch_attn<NG, 1, kList>(a, tiles, st) : launch_attn<NG, 1, kDense>(a, tiles, st)))
@@ -1248,9 +1283,9 @@ skv_status launch_kv4_attn(const skv_problem& p, const void* q, const PoolView& 
 
 skv_status launch_kv4_score(const skv_problem& p, const void* q, const PoolView& pool, int group, float* scores,
                             int32_t* status, cudaStream_t st) {
-  Kv4Args a = kv4_args(p, q, pool, group, nullptr, status);
+  Kv4Args a = kv4_args(p, q, pool, nullptr, status);
   a.scores = scores;
-  const long long tiles = (long long)a.B * a.H * (((long long)p.max_len + 15) / 16 + 1);
+  const long long tiles = ((long long)p.max_len + 15) / 16 + 1;
 #define KV4_SCORE(NG)                                                                 \
   (p.group_agg == SKV_AGG_MEAN  ? launch_scores<NG, SKV_AGG_MEAN>(a, tiles, st)       \
    : p.group_agg == SKV_AGG_MAX ? launch_scores<NG, SKV_AGG_MAX>(a, tiles, st)        \
@@ -1261,7 +1296,7 @@ skv_status launch_kv4_score(const skv_problem& p, const void* q, const PoolView&
 
 skv_status launch_kv4_gather(const skv_problem& p, const PoolView& pool, int group, const int32_t* idx, void* k_out,
                              void* v_out, int32_t* status, cudaStream_t st) {
-  const Kv4Args a = kv4_args(p, nullptr, pool, group, idx, status);
+  const Kv4Args a = kv4_args(p, nullptr, pool, idx, status);
   const int n_att = p.n_sink + p.topk + p.n_local;
   if (n_att == 0) return SKV_OK;
   const bool f32 = p.dtype == SKV_DTYPE_F32;
