@@ -89,8 +89,11 @@ __device__ __forceinline__ void settle(const Kv4Args& a, Cursor& c) {  // tile m
 // c of n takes [W c / n, W (c + 1) / n), the tiles that lie there.  A unit's first kUnit places
 // hold no tile.
 constexpr int kUnit = 16;
-__device__ __forceinline__ long long share(long long W, int n, int c) { return W * c / n; }
-__device__ __forceinline__ int holder(long long W, int n, long long place) { return (int)(((place + 1) * n - 1) / W); }
+__device__ __forceinline__ long long quotient(long long x, long long y) {  // (64 bits: hundreds of cycles)
+  return (x | y) >> 32 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
+}
+__device__ __forceinline__ long long share(long long W, int n, int c) { return quotient(W * c, n); }
+__device__ __forceinline__ int holder(long long W, int n, long long place) { return (int)quotient((place + 1) * n - 1, W); }
 
 struct Share {
   long long weight;  // of all units
@@ -133,7 +136,7 @@ __device__ __forceinline__ Share find_share(const Kv4Args& a, Cursor* c) {
   }
   Share r;
   r.weight = (all + kUnit * all_units) * a.H;
-  long long n = (r.weight + kLeast - 1) / kLeast;
+  long long n = (r.weight + kLeast - 1) / kLeast;  // (a power of two)
   n = n < 1 ? 1 : n > gridDim.x ? gridDim.x : n;
   r.ctas = (int)n;
   // the tiles before a share's ends: one thread's requests hold each
@@ -148,7 +151,7 @@ __device__ __forceinline__ Share find_share(const Kv4Args& a, Cursor* c) {
       for (int b = b0; b < b1; ++b) {
         const int nt = tiles_of<MODE>(a, len_of(a, b)), w = nt > 0 ? nt + kUnit : 0;
         if (off < (long long)w * a.H) {
-          const int h = (int)(off / w), in = (int)(off - (long long)h * w), tile = in > kUnit ? in - kUnit : 0;
+          const int h = (int)quotient(off, w), in = (int)(off - (long long)h * w), tile = in > kUnit ? in - kUnit : 0;
           s_tiles[end] = t + (long long)h * nt + tile;
           if (end == 0) {
             s_at[0] = b;
@@ -510,11 +513,10 @@ struct QShared {
   float largest[8 * NT][kW], part[8][8 * NT];  // of a head: of each warp's entries; sums of a k-step
 };
 
-// MEAN: the mean of the n heads in three fp16 parts, columns 0, 1 and 2; else a column a head.
-template <int NG, int NT, bool MEAN>
-__device__ __forceinline__ void make_queries(const __nv_bfloat16* q, int n, QShared<NT>& s, QFrag<NT>& f) {
+// This warp's k-step of the columns: entries 16 warp + 4 t .. of head 8 nt + g.  MEAN: of the heads' sum.
+template <int NT, bool MEAN>
+__device__ __forceinline__ void load_queries(const __nv_bfloat16* q, int n, float (&x)[NT][4]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  float x[NT][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -529,6 +531,16 @@ __device__ __forceinline__ void make_queries(const __nv_bfloat16* q, int n, QSha
       x[nt][3] += __uint_as_float(u.y & 0xffff0000u);
       if (!MEAN) break;
     }
+  }
+}
+
+// MEAN: the mean of the n heads in three fp16 parts, columns 0, 1 and 2; else a column a head.
+template <int NG, int NT, bool MEAN>
+__device__ __forceinline__ void make_queries(float (&x)[NT][4], int n, QShared<NT>& s, QFrag<NT>& f) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int head = 8 * nt + g;
     if (MEAN) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[nt][i] /= (float)n;
@@ -814,13 +826,13 @@ __device__ __forceinline__ void attend_cell(uint32_t cell, uint32_t mask, const 
 
 template <int NG, int NT>
 struct AttnShape {
-  // Stages of 2.5 KB a warp and CTAs a SM: one column tile, 16 warps a SM with up to four tiles each
-  // on their way; two column tiles take the registers of two CTAs.
-  static constexpr int kStages = NT == 1 ? 4 : 6;
+  // Stages of 2.5 KB a warp and CTAs a SM: one column tile, 16 warps a SM with two or three tiles each
+  // on their way (four stages: no faster); two column tiles take the registers of two CTAs.
+  static constexpr int kStages = NT == 1 ? 3 : 6;
   static constexpr int kCtas = NT == 1 ? 2 : 1;
   static constexpr int kRing = kW * kStages * 2 * kv4_cell(NG);
   static constexpr int kRow = kD + 4;  // floats of a head's partial row: heads 2 t, 2 t + 2 an eighth of the banks apart
-  static constexpr int kOut = kW / 2 * 8 * NT * kRow * 4;
+  static constexpr int kOut = kW * 8 * NT * kRow * 4;
   static constexpr int kSmem = kRing + kOut;
 };
 
@@ -841,8 +853,7 @@ __global__ void __launch_bounds__(32 * kW, AttnShape<NG, NT>::kCtas) kv4_attn_ke
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Cursor s_at[kW];
   __shared__ uint32_t s_mask[MODE == kList ? kW : 1][S];
-  __shared__ float2 s_ml[kW][HC], s_tot[HC];
-  __shared__ float s_f[HC][kW];
+  __shared__ float2 s_ml[HC][kW];
   __shared__ __align__(16) QShared<NT> s_q;
   float* s_o = reinterpret_cast<float*>(smem + Shape::kRing);
   pdl_release();
@@ -855,6 +866,9 @@ __global__ void __launch_bounds__(32 * kW, AttnShape<NG, NT>::kCtas) kv4_attn_ke
   Cursor at = u;
   at.tile += warp;
   const uint32_t ring = smem_u32(smem) + warp * S * kStage;
+  auto queries = [&]() { return a.q + ((size_t)u.b * a.Hq + (size_t)u.h * a.G) * kD; };
+  float x[NT][4];
+  load_queries<NT, false>(queries(), a.G, x);
   typename Pick<MODE, NG, S>::type feed(a, s_at[warp], s_mask[MODE == kList ? warp : 0], ring, at,
                                         share > warp ? (share - warp + kW - 1) / kW : 0);
 #pragma unroll 1
@@ -868,7 +882,8 @@ __global__ void __launch_bounds__(32 * kW, AttnShape<NG, NT>::kCtas) kv4_attn_ke
     float kf[NT][2];
     State<NG, NT> s;
     clear(s);
-    make_queries<NG, NT, false>(a.q + ((size_t)u.b * a.Hq + (size_t)u.h * a.G) * kD, a.G, s_q, q);
+    if (seg > 0) load_queries<NT, false>(queries(), a.G, x);
+    make_queries<NG, NT, false>(x, a.G, s_q, q);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -883,8 +898,7 @@ __global__ void __launch_bounds__(32 * kW, AttnShape<NG, NT>::kCtas) kv4_attn_ke
       if (mask != 0u) attend_cell<NG, NT>(ring + stage * kStage, mask, q, kf, s);
       stage = stage == S - 1 ? 0 : stage + 1;
     }
-    // the warp's sums, then the CTA's: every warp's output under the CTA's reference, the upper
-    // warps' rows added to by the lower ones
+    // the warp's sums and its output under its own reference; the CTA's below
 #pragma unroll 1
     for (int off = 4; off <= 16; off <<= 1) {
 #pragma unroll
@@ -896,65 +910,46 @@ __global__ void __launch_bounds__(32 * kW, AttnShape<NG, NT>::kCtas) kv4_attn_ke
           for (int k = 0; k < NG; ++k) s.z[nt][k][i] += __shfl_xor_sync(0xffffffffu, s.z[nt][k][i], off);
         }
     }
-    if (g == 0) {
+    float* row = s_o + warp * HC * Shape::kRow + 2 * g;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) s_ml[warp][8 * nt + 2 * t + i] = make_float2(-s.ref[nt][i], s.l[nt][i]);
-    }
-    __syncthreads();
-    if (threadIdx.x < HC * kW) {
-      const int head = threadIdx.x >> 3, w = threadIdx.x & 7;
-      const float2 x = s_ml[w][head];
-      float m = x.x;
+      for (int i = 0; i < 2; ++i) {
+        const int head = 8 * nt + 2 * t + i;
+        if (g == 0) s_ml[head][warp] = make_float2(-s.ref[nt][i], s.l[nt][i]);
 #pragma unroll
-      for (int off = 1; off < 8; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-      const float fw = ex2(x.x - m);
-      float l = fw * x.y;
-#pragma unroll
-      for (int off = 1; off < 8; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-      s_f[head][w] = fw;
-      if (w == 0) s_tot[head] = make_float2(m, l);
-    }
-    __syncthreads();
-    float* out = s_o + warp % (kW / 2) * HC * Shape::kRow + 2 * g;
-#pragma unroll 1
-    for (int half = 1; half >= 0; --half) {
-      if (warp / (kW / 2) == half) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int head = 8 * nt + 2 * t + i;
-            const float fw = s_f[head][warp];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              float2* to_row = reinterpret_cast<float2*>(out + head * Shape::kRow + 16 * j);
-              const float z = s.z[nt][j * NG / 8][i];
-              const float2 y = half ? make_float2(0.f, 0.f) : *to_row;
-              *to_row = make_float2(fmaf(fw, fmaf(s.o[nt][j][i], 0x1p24f, z), y.x),
-                                    fmaf(fw, fmaf(s.o[nt][j][i + 2], 0x1p20f, z), y.y));
-            }
-          }
+        for (int j = 0; j < 8; ++j) {
+          const float z = s.z[nt][j * NG / 8][i];
+          *reinterpret_cast<float2*>(row + head * Shape::kRow + 16 * j) =
+              make_float2(fmaf(s.o[nt][j][i], 0x1p24f, z), fmaf(s.o[nt][j][i + 2], 0x1p20f, z));
+        }
       }
-      __syncthreads();
-    }
+    __syncthreads();
     const bool whole = base >= 0 && base + u.nt <= share;
     const size_t hq = (size_t)u.b * a.Hq + (size_t)u.h * a.G;
     float* slot = a.ws + ((size_t)blockIdx.x * 2 + (seg > 0)) * kSlotFloats;
     const int d = threadIdx.x & (kD - 1);
 #pragma unroll 1
     for (int head = threadIdx.x / kD; head < a.G; head += 32 * kW / kD) {
-      float o = 0.f;
+      float2 x[kW];
+      float m = kFloor, l = 0.f, o = 0.f;
 #pragma unroll
-      for (int w = 0; w < kW / 2; ++w) o += s_o[(w * HC + head) * Shape::kRow + d];
-      const float2 tot = s_tot[head];
+      for (int w = 0; w < kW; ++w) {
+        x[w] = s_ml[head][w];
+        m = fmaxf(m, x[w].x);
+      }
+#pragma unroll
+      for (int w = 0; w < kW; ++w) {
+        const float fw = ex2(x[w].x - m);
+        l = fmaf(fw, x[w].y, l);
+        o = fmaf(fw, s_o[(w * HC + head) * Shape::kRow + d], o);
+      }
       if (whole) {
-        a.out[(hq + head) * kD + d] = __float2bfloat16_rn(tot.y == 0.f ? 0.f : o / tot.y);
-        if (d == 0 && a.lse) a.lse[hq + head] = tot.y == 0.f ? -INFINITY : kLn2 * (tot.x + log2f(tot.y));
+        a.out[(hq + head) * kD + d] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
+        if (d == 0 && a.lse) a.lse[hq + head] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
       } else {
         slot[head * kD + d] = o;
-        if (d == 0) *reinterpret_cast<float2*>(slot + 16 * kD + 2 * head) = tot;
+        if (d == 0) *reinterpret_cast<float2*>(slot + 16 * kD + 2 * head) = make_float2(m, l);
       }
     }
     if (threadIdx.x == 0 && base >= 0)
@@ -973,50 +968,58 @@ __global__ void __launch_bounds__(32 * kW, AttnShape<NG, NT>::kCtas) kv4_attn_ke
 // The units that no CTA held alone: their partials joined, a CTA a head; the empty ones: zeros.
 template <int MODE>
 __global__ void __launch_bounds__(kD) kv4_merge_kernel(const Kv4Args a) {
-  __shared__ float s_f[kMaxParts];
-  __shared__ float s_red[2][kD / 32];
+  __shared__ float2 s_ml[kMaxParts];
+  __shared__ float s_red[kD / 32];
   pdl_release();
   pdl_wait();
   const long long unit = blockIdx.x / a.G;
   const int head = blockIdx.x - (int)unit * a.G, b = (int)(unit / a.H), h = (int)(unit - (long long)b * a.H);
   const int d = threadIdx.x, lane = d & 31, warp = d >> 5;
   const size_t hq = (size_t)b * a.Hq + (size_t)h * a.G + head;
+  const int2 span = a.desc[unit];  // (of an empty unit: anything)
   if (tiles_of<MODE>(a, len_of(a, b)) == 0) {
     a.out[hq * kD + d] = __float2bfloat16_rn(0.f);
     if (d == 0 && a.lse) a.lse[hq] = -INFINITY;
     return;
   }
-  const int2 span = a.desc[unit];
   const int c0 = span.x & ((1 << 30) - 1), parts = span.y - c0 + 1;
   if (parts == 1) return;
-  const float* slots = a.ws + (size_t)c0 * 2 * kSlotFloats;
+  const float* slots = a.ws + (size_t)c0 * 2 * kSlotFloats + head * kD + d;
+  const float2* sums = reinterpret_cast<const float2*>(a.ws + (size_t)c0 * 2 * kSlotFloats + 16 * kD + 2 * head);
   const size_t first = span.x >> 30 ? kSlotFloats : 0;  // the others begin with this unit
-  auto slot = [&](int i) { return slots + (i == 0 ? first : (size_t)i * 2 * kSlotFloats); };
+  auto at = [&](int i) { return i == 0 ? first : (size_t)i * 2 * kSlotFloats; };
+  constexpr int kAhead = 8;  // outputs on their way beside the sums
+  float ahead[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) ahead[i] = i < parts ? __ldcg(slots + at(i)) : 0.f;
   float m = kFloor;
-  for (int i = d; i < parts; i += kD) m = fmaxf(m, slot(i)[16 * kD + 2 * head]);
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  if (lane == 0) s_red[0][warp] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kD / 32; ++w) m = fmaxf(m, s_red[0][w]);
-  float l = 0.f;
   for (int i = d; i < parts; i += kD) {
-    const float2 v = *reinterpret_cast<const float2*>(slot(i) + 16 * kD + 2 * head);
-    const float f = ex2(v.x - m);
-    s_f[i] = f;
-    l = fmaf(f, v.y, l);
+    const float2 v = __ldcg(reinterpret_cast<const float2*>(reinterpret_cast<const float*>(sums) + at(i)));
+    s_ml[i] = v;
+    m = fmaxf(m, v.x);
   }
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-  if (lane == 0) s_red[1][warp] = l;
+  for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  if (lane == 0) s_red[warp] = m;
   __syncthreads();
-  l = 0.f;
 #pragma unroll
-  for (int w = 0; w < kD / 32; ++w) l += s_red[1][w];
-  float o = 0.f;
+  for (int w = 0; w < kD / 32; ++w) m = fmaxf(m, s_red[w]);
+  float l = 0.f, o = 0.f;
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (i < parts) {
+      const float2 v = s_ml[i];
+      const float f = ex2(v.x - m);
+      l = fmaf(f, v.y, l);
+      o = fmaf(f, ahead[i], o);
+    }
 #pragma unroll 8
-  for (int i = 0; i < parts; ++i) o = fmaf(s_f[i], slot(i)[head * kD + d], o);
+  for (int i = kAhead; i < parts; ++i) {
+    const float2 v = s_ml[i];
+    const float f = ex2(v.x - m);
+    l = fmaf(f, v.y, l);
+    o = fmaf(f, __ldcg(slots + at(i)), o);
+  }
   a.out[hq * kD + d] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
   if (d == 0 && a.lse) a.lse[hq] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
 }
@@ -1051,7 +1054,9 @@ __global__ void __launch_bounds__(32 * kW, NT == 1 ? kScoreCtas : 2) kv4_score_k
     const Regions rg = regions_of(u.L, a.ns, a.nl);
     const size_t unit = (size_t)u.b * a.H + u.h;
     QFrag<NT> q;
-    make_queries<NG, NT, AGG == SKV_AGG_MEAN>(a.q + unit * a.Gi * kD, a.Gi, s_q, q);
+    float x[NT][4];
+    load_queries<NT, AGG == SKV_AGG_MEAN>(a.q + unit * a.Gi * kD, a.Gi, x);
+    make_queries<NG, NT, AGG == SKV_AGG_MEAN>(x, a.Gi, s_q, q);
     int i = from + ((warp - from) & (kW - 1));
     // the keys of this lane's rows: key, and 8 on
     int key = (rg.s_end & ~15) + (i - base) * 16 + g;
@@ -1120,6 +1125,7 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4Args a, T* k_o
   const int lane = threadIdx.x & 31, t = lane & 3;
   const long long rows = (long long)a.B * a.H * n_att, warps = (long long)gridDim.x * 8;
   for (long long r = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * 8 + (lane >> 2); r < rows; r += warps * 8) {
+    const uint32_t live = __activemask();  // (whole quads)
     const long long unit = r / n_att;
     const int j = (int)(r - unit * n_att);
     Cursor c;
@@ -1135,37 +1141,58 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4Args a, T* k_o
     const bool host = at >> 31;
     const size_t cell = (size_t)(at >> 4 & 0x7ffffffu) * kv4_cell(NG);
     const int rc = (int)(at & 15u);
+    uint4 codes[2];
+    uint32_t words[2][NG];
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {  // both sides' loads together
+      codes[kv] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < NG; ++i) words[kv][i] = 0u;
+      if (at != kNoRow && (kv ? v_out : k_out) != nullptr) {
+        const unsigned char* src =
+            (const unsigned char*)(kv ? (host ? a.pool.host_v : a.pool.gpu_v) : (host ? a.pool.host_k : a.pool.gpu_k)) + cell;
+        codes[kv] = __ldg(reinterpret_cast<const uint4*>(src + rc * kCodeBytes) + t);
+        const unsigned char* w = src + 16 * kCodeBytes + rc * 4 * NG;
+        if constexpr (NG == 4) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(w));
+          words[kv][0] = x.x, words[kv][1] = x.y, words[kv][2] = x.z, words[kv][3] = x.w;
+        } else if constexpr (NG == 2) {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(w));
+          words[kv][0] = x.x, words[kv][1] = x.y;
+        } else {
+          words[kv][0] = __ldg(reinterpret_cast<const uint32_t*>(w));
+        }
+      }
+    }
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
       T* out = kv ? v_out : k_out;
       if (out == nullptr) continue;
-      const unsigned char* src =
-          (const unsigned char*)(kv ? (host ? a.pool.host_v : a.pool.gpu_v) : (host ? a.pool.host_k : a.pool.gpu_k));
-      uint4 u = make_uint4(0, 0, 0, 0);
+      const uint4 u = codes[kv];
       float s[NG], z[NG];
 #pragma unroll
-      for (int i = 0; i < NG; ++i) s[i] = z[i] = 0.f;
-      if (at != kNoRow) {
-        u = __ldg(reinterpret_cast<const uint4*>(src + cell + rc * kCodeBytes) + t);
-        const uint32_t* words = reinterpret_cast<const uint32_t*>(src + cell + 16 * kCodeBytes) + rc * NG;
+      for (int i = 0; i < NG; ++i) s[i] = step_of(words[kv][i]), z[i] = centre_of(words[kv][i]);
+      // 2^23 + c by its bits (conversions are a quarter rate)
+      auto value = [&](uint32_t b, int sh, int group) {
+        return fmaf(s[group], __uint_as_float((b >> sh & 15u) | 0x4b000000u) - 8388616.f, z[group]);
+      };
 #pragma unroll
-        for (int i = 0; i < NG; ++i) {
-          const uint32_t x = __ldg(words + i);
-          s[i] = step_of(x);
-          z[i] = centre_of(x);
+      for (int i = 0; i < 8; i += 2) {  // entries 4 t .. of spans i and i + 1
+        const uint32_t b0 = i < 4 ? u.x : u.y, b1 = i < 4 ? u.z : u.w;
+        const int sh = 8 * (i & 3), g0 = i * NG / 8, g1 = (i + 1) * NG / 8;
+        const float4 x = make_float4(value(b0, sh, g0), value(b0, sh + 4, g0), value(b1, sh, g0), value(b1, sh + 4, g0));
+        const float4 y = make_float4(value(b0, sh + 8, g1), value(b0, sh + 12, g1), value(b1, sh + 8, g1), value(b1, sh + 12, g1));
+        T* to = out + (size_t)r * kD + 16 * i;
+        if constexpr (sizeof(T) == 4) {
+          *reinterpret_cast<float4*>(to + 4 * t) = x;
+          *reinterpret_cast<float4*>(to + 16 + 4 * t) = y;
+        } else {  // the even lane of a pair takes eight entries of the one span, the odd lane of the other
+          const uint32_t x0 = tc::pack_bf16(x.x, x.y), x1 = tc::pack_bf16(x.z, x.w);
+          const uint32_t y0 = tc::pack_bf16(y.x, y.y), y1 = tc::pack_bf16(y.z, y.w);
+          const uint32_t p0 = __shfl_xor_sync(live, t & 1 ? x0 : y0, 1), p1 = __shfl_xor_sync(live, t & 1 ? x1 : y1, 1);
+          *reinterpret_cast<uint4*>(to + (t & 1 ? 16 + 4 * (t - 1) : 4 * t)) =
+              t & 1 ? make_uint4(p0, p1, y0, y1) : make_uint4(x0, x1, p0, p1);
         }
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t b0 = (i < 4 ? u.x : u.y) >> (8 * (i & 3)), b1 = (i < 4 ? u.z : u.w) >> (8 * (i & 3));
-        const float si = s[i * NG / 8], zi = z[i * NG / 8];
-        const float x[4] = {fmaf(si, (float)(int)(b0 & 15u) - 8.f, zi), fmaf(si, (float)(int)(b0 >> 4 & 15u) - 8.f, zi),
-                            fmaf(si, (float)(int)(b1 & 15u) - 8.f, zi), fmaf(si, (float)(int)(b1 >> 4 & 15u) - 8.f, zi)};
-        T* to = out + (size_t)r * kD + 16 * i + 4 * t;
-        if constexpr (sizeof(T) == 4)
-          *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
-        else
-          *reinterpret_cast<uint2*>(to) = make_uint2(tc::pack_bf16(x[0], x[1]), tc::pack_bf16(x[2], x[3]));
       }
     }
   }

@@ -7,7 +7,8 @@
 // slot map, new table entries, blocks going back onto the stack; each finds its request by
 // bisection.  A new block is computed where it is needed rather than read back from the
 // table, so no CTA waits for another's writes; lengths and the stack's count, which all of them
-// read, are written by the last CTA to finish (a ticket in the state).
+// read, are written when all of them have: by the first CTA of a cluster after its barrier, of
+// more CTAs by the last to finish (a ticket in the state).
 #include "skv_internal.cuh"
 
 namespace skv {
@@ -15,6 +16,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kMaxBatch = 4096;
+constexpr unsigned kCluster = 8;  // as many CTAs are one cluster, and wait for each other by its barrier
 
 struct TableArgs {
   skv_tables t;
@@ -25,30 +27,38 @@ struct TableArgs {
   int32_t* status;
 };
 
-// Sums of a and b over the block's threads before this one; the totals go to *ta and *tb.
-__device__ __forceinline__ void block_scan(long long& a, long long& b, long long* warp_a, long long* warp_b,
-                                           long long* ta, long long* tb) {
+// Sums of N values over the block's threads before this one; the totals go to all.
+template <int N>
+__device__ __forceinline__ void block_scan(long long (&a)[N], long long (*warps)[N], long long (&all)[N]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = a, y = b;
+  long long x[N];
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, x, off), v = __shfl_up_sync(0xffffffffu, y, off);
-    if (lane >= off) x += u, y += v;
-  }
-  __syncthreads();  // the words of the scan before have been read
-  if (lane == 31) warp_a[warp] = x, warp_b[warp] = y;
+  for (int i = 0; i < N; ++i) x[i] = a[i];
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const long long u = __shfl_up_sync(0xffffffffu, x[i], off);
+      if (lane >= off) x[i] += u;
+    }
+  if (lane == 31)
+#pragma unroll
+    for (int i = 0; i < N; ++i) warps[warp][i] = x[i];
   __syncthreads();
-  long long pa = 0, pb = 0, sa = 0, sb = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w == warp) pa = sa, pb = sb;
-    sa += warp_a[w];
-    sb += warp_b[w];
+  for (int i = 0; i < N; ++i) {
+    x[i] -= a[i];
+    all[i] = 0;
   }
-  a = pa + x - a;
-  b = pb + y - b;
-  *ta = sa;
-  *tb = sb;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (w == warp) x[i] += all[i];
+      all[i] += warps[w][i];
+    }
+#pragma unroll
+  for (int i = 0; i < N; ++i) a[i] = x[i];
 }
 
 __device__ __forceinline__ int saturate(long long x) { return x > 0x7fffffffLL ? 0x7fffffff : (int)x; }
@@ -66,9 +76,9 @@ __device__ __forceinline__ int find(const int* sums, int B, int i) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kThreads) update_tables_kernel(const TableArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) update_tables_kernel(const TableArgs a) {
   extern __shared__ int smem[];
-  __shared__ long long warp_a[kThreads / 32], warp_b[kThreads / 32];
+  __shared__ long long s_asked[kThreads / 32][3], s_given[kThreads / 32][1];
   __shared__ int s_last;
   const skv_tables& t = a.t;
   const int B = t.batch, bs = t.block_size;
@@ -86,7 +96,7 @@ __global__ void __launch_bounds__(kThreads) update_tables_kernel(const TableArgs
   const int first = t.base / bs;
   const int per = (B + kThreads - 1) / kThreads, b0 = threadIdx.x * per, b1 = b0 + per < B ? b0 + per : B;
   // what each request asks for
-  long long n_rows = 0, n_back = 0;
+  long long asked[3] = {0, 0, 0};  // rows, blocks back, blocks needed
   for (int b = b0; b < b1; ++b) {
     const int L = t.seq_lens[b], n = a.n_new[b];
     const bool bad = L < 0 || L > t.max_len || (L > 0 && L < t.base);
@@ -114,26 +124,24 @@ __global__ void __launch_bounds__(kThreads) update_tables_kernel(const TableArgs
     }
     given[b] = need;
     freed[b] = back;
-    n_rows += n > 0 ? n : 0;
-    n_back += back;
+    asked[0] += n > 0 ? n : 0;
+    asked[1] += back;
+    asked[2] += need;
   }
-  long long all_rows, all_back, all_need, all_given;
-  block_scan(n_rows, n_back, warp_a, warp_b, &all_rows, &all_back);
-  long long n_need = 0, none = 0;
-  for (int b = b0; b < b1; ++b) n_need += given[b];
-  block_scan(n_need, none, warp_a, warp_b, &all_need, &all_given);
+  long long all[3], all_given[1];
+  block_scan<3>(asked, s_asked, all);
   // who gets it
-  long long n_given = 0;
-  const long long free = count + all_back;
+  long long before[1] = {0};
+  const long long free = count + all[1];
   for (int b = b0; b < b1; ++b) {
     const int n = a.n_new[b], need = given[b], back = freed[b];
-    n_need += need;
-    rows[b] = saturate(n_rows);
-    freed[b] = saturate(n_back);
-    n_rows += n > 0 ? n : 0;
-    n_back += back;
+    asked[2] += need;
+    rows[b] = saturate(asked[0]);
+    freed[b] = saturate(asked[1]);
+    asked[0] += n > 0 ? n : 0;
+    asked[1] += back;
     if (start[b] >= 0) {
-      const bool fits = n_rows <= a.n_tokens, blocks = need == 0 || n_need <= free;
+      const bool fits = asked[0] <= a.n_tokens, blocks = need == 0 || asked[2] <= free;
       if (!fits && reports) flag(a.status, SKV_DEV_BAD_INDEX);
       if (fits && !blocks && reports) flag(a.status, SKV_DEV_NO_BLOCK);
       if (fits && blocks) {
@@ -143,20 +151,18 @@ __global__ void __launch_bounds__(kThreads) update_tables_kernel(const TableArgs
         given[b] = 0;
       }
     }
-    n_given += given[b];
+    before[0] += given[b];
   }
-  long long before = n_given;
-  none = 0;
-  block_scan(before, none, warp_a, warp_b, &all_given, &all_need);
+  block_scan<1>(before, s_given, all_given);
   for (int b = b0; b < b1; ++b) {
     const int g = given[b];
-    given[b] = saturate(before);
-    before += g;
+    given[b] = saturate(before[0]);
+    before[0] += g;
   }
   if (threadIdx.x == 0) {
-    rows[B] = saturate(all_rows);
-    given[B] = saturate(all_given);
-    freed[B] = saturate(all_back);
+    rows[B] = saturate(all[0]);
+    given[B] = saturate(all_given[0]);
+    freed[B] = saturate(all[1]);
   }
   __syncthreads();
   const int K = given[B], R = freed[B];
@@ -230,19 +236,22 @@ __global__ void __launch_bounds__(kThreads) update_tables_kernel(const TableArgs
   }
   // lengths and the count, once every CTA has read them
   __syncthreads();
-  if (gridDim.x > 1) {
+  if (gridDim.x > kCluster) {
     if (threadIdx.x == 0) {
       __threadfence();
       s_last = atomicAdd(&t.state[1], 1) == (int)gridDim.x - 1;
     }
     __syncthreads();
     if (!s_last) return;
+  } else if (gridDim.x > 1) {
+    cluster_sync();
+    if (blockIdx.x > 0) return;
   }
   for (int b = b0; b < b1; ++b) t.seq_lens[b] = lens[b];
   if (threadIdx.x == 0) {
     const long long left = (long long)count + R - K;
     t.state[0] = left < t.n_blocks ? (int)left : t.n_blocks;
-    if (gridDim.x > 1) t.state[1] = 0;
+    if (gridDim.x > kCluster) t.state[1] = 0;
   }
 }
 
@@ -256,16 +265,18 @@ skv_status launch_update_tables(const skv_tables& t, const int32_t* n_new, int n
   const int smem = 6 * 4 * (t.batch + 1);
   const skv_status prep = prepare_kernel((const void*)update_tables_kernel, 6 * 4 * (kMaxBatch + 1));
   if (prep != SKV_OK) return prep;
-  // a sweep of rows or of blocks a CTA (what a call gives back is known on the device only)
+  // A sweep of rows a CTA, or of the blocks that come with them, two CTAs a SM at most.  Without rows
+  // the call gives blocks back, how many is known on the device only: as for all that the tables
+  // hold, a CTA a SM at most.
   const long long entries = (long long)t.batch * t.table_stride;
-  const long long blocks = entries < t.n_blocks ? entries : t.n_blocks;
-  long long ctas = ((long long)n_tokens + 4 * kThreads - 1) / (4 * kThreads);
-  const long long by_blocks = (blocks + 8 * kThreads - 1) / (8 * kThreads);
-  if (ctas < by_blocks) ctas = by_blocks;
+  const long long blocks = n_tokens > 0 ? n_tokens / t.block_size + t.batch : entries < t.n_blocks ? entries : t.n_blocks;
+  long long ctas = ((long long)n_tokens + 4 * kThreads - 1) / (4 * kThreads), more = (blocks + 8 * kThreads - 1) / (8 * kThreads);
+  if (more > num_sms()) more = num_sms();
+  if (ctas < more) ctas = more;
   if (ctas < 1) ctas = 1;
-  if (ctas > num_sms()) ctas = num_sms();
-  if (launch_dependent(update_tables_kernel, dim3((unsigned)ctas), dim3(kThreads), (size_t)smem, st, 1, a) !=
-      cudaSuccess)
+  if (ctas > 2 * num_sms()) ctas = 2 * num_sms();
+  if (launch_dependent(update_tables_kernel, dim3((unsigned)ctas), dim3(kThreads), (size_t)smem, st,
+                       ctas <= kCluster ? (int)ctas : 1, a) != cudaSuccess)
     return SKV_ERR_CUDA;
   SKV_LAUNCH_CHECK();
   return SKV_OK;

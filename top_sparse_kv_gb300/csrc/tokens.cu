@@ -183,9 +183,10 @@ __device__ __forceinline__ void put_row4(const float (&x)[VE], unsigned char* ce
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
   }
   const uint32_t word = kv4_word(lo, hi, &s, &z);
+  const float inv = kv4_inverse(s);
   uint32_t w = 0;
 #pragma unroll
-  for (int j = 0; j < VE; ++j) w |= kv4_code(x[j], s, z) << (4 * j);
+  for (int j = 0; j < VE; ++j) w += kv4_code(x[j], s, z, inv) << (4 * j);
   if constexpr (VE == 8) {  // sub: u's bit 2, i's bits 0, 1, 2; the word: u's bits 0, 1
     uint32_t y = __shfl_xor_sync(0xffffffffu, w, 2);
     w = __byte_perm(w, y, sub & 2 ? 0x3715 : 0x6240);
@@ -438,7 +439,10 @@ __global__ void __launch_bounds__(32 * kRowWarps<LPR> + 32, kTokCtas<LPR>) token
         const int v0 = r0 > nq + nk ? r0 : nq + nk;
         const unsigned char* from = data + (r0 < nq + nk ? (nq + nk - r0) * rowb : 0);
         if constexpr (NG > 0) {
-          for (int rb = r0 + warp * RPW; rb < r1; rb += W * RPW) {
+          // (every lane takes part in a row's exchange: whole passes, from the first that holds a value row)
+          int rb = r0 + warp * RPW;
+          if (v0 >= rb + RPW) rb += (v0 - rb + W * RPW - RPW) / (W * RPW) * (W * RPW);
+          for (; rb < r1; rb += W * RPW) {
             const int r = rb + mine;
             const bool on = r >= v0 && r < r1;
             float x[VE];
