@@ -1117,27 +1117,50 @@ __global__ void __launch_bounds__(32 * kW, NT == 1 ? kScoreCtas : 2) kv4_score_k
 
 // ---------------------------------------------------------------------------- gather
 
-// Four lanes a row: 16 bytes of codes each, four consecutive entries of every 16.
+// Eight codes (the bytes of a word, low half first) as pairs of bf16 values, the pair of a byte
+// together: 128 + c by its bits, 136 off, and one fused product with the step and the centre
+// (the first two bytes' word, the last two's).
+__device__ __forceinline__ void values_of(uint32_t codes, uint32_t word01, uint32_t word23, uint32_t (&out)[4]) {
+  const uint32_t lo = codes & 0x0f0f0f0fu, hi = codes >> 4 & 0x0f0f0f0fu, bias = 0x43084308u;
+  const auto two = [](const uint32_t& x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t c;  // (a selector's top bit: copies of a byte's sign, here 0)
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(c) : "r"(lo), "r"(hi), "r"(0x8480 + i * 0x101));
+    c |= 0x43004300u;
+    const uint32_t word = i < 2 ? word01 : word23, s = __byte_perm(word, word, 0x1010), z = __byte_perm(word, word, 0x3232);
+    const __nv_bfloat162 v = __hfma2(__hsub2(two(c), two(bias)), two(s), two(z));
+    out[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+// Four lanes a row: 16 bytes of codes each, four consecutive entries of every 16.  Finding a row is a
+// step a round: its place's position, that one's entry, the row.
 template <int NG, typename T>
 __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4Args a, T* k_out, T* v_out, int n_att) {
   pdl_release();
   pdl_wait();
   const int lane = threadIdx.x & 31, t = lane & 3;
-  const long long rows = (long long)a.B * a.H * n_att, warps = (long long)gridDim.x * 8;
-  for (long long r = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * 8 + (lane >> 2); r < rows; r += warps * 8) {
-    const uint32_t live = __activemask();  // (whole quads)
-    const long long unit = r / n_att;
+  const long long rows = (long long)a.B * a.H * n_att, stride = (long long)gridDim.x * 64;
+  auto position = [&](long long r, Row& w) {
+    w.t = -1;
+    if (r >= rows) return;
+    const long long unit = quotient(r, n_att);
     const int j = (int)(r - unit * n_att);
     Cursor c;
-    c.b = (int)(unit / a.H);
+    c.b = (int)quotient(unit, a.H);
     c.h = (int)(unit - (long long)c.b * a.H);
     c.tile = j >> 4;
     c.L = t == 0 && j == 0 && c.h == 0 ? load_len(a.seq_lens, c.b, a.max_len, a.status) : len_of(a, c.b);
-    c.nt = 0;
-    Row w;
     row_position(a, c, true, j & 15, w);
-    row_entry(a, t == 0, w);
-    const uint32_t at = row_id(a, t == 0, w);
+  };
+  const long long r0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * 8 + (lane >> 2);
+  Row w0, w1;
+  position(r0, w0);
+  row_entry(a, t == 0, w0);
+  position(r0 + stride, w1);
+  for (long long r = r0; r - (lane >> 2) < rows; r += stride) {  // (a warp's lanes together)
+    const uint32_t at = row_id(a, t == 0, w0);
     const bool host = at >> 31;
     const size_t cell = (size_t)(at >> 4 & 0x7ffffffu) * kv4_cell(NG);
     const int rc = (int)(at & 15u);
@@ -1164,34 +1187,42 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4Args a, T* k_o
         }
       }
     }
+    w0 = w1;
+    row_entry(a, t == 0, w0);
+    position(r + 2 * stride, w1);
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
       T* out = kv ? v_out : k_out;
       if (out == nullptr) continue;
       const uint4 u = codes[kv];
-      float s[NG], z[NG];
 #pragma unroll
-      for (int i = 0; i < NG; ++i) s[i] = step_of(words[kv][i]), z[i] = centre_of(words[kv][i]);
-      // 2^23 + c by its bits (conversions are a quarter rate)
-      auto value = [&](uint32_t b, int sh, int group) {
-        return fmaf(s[group], __uint_as_float((b >> sh & 15u) | 0x4b000000u) - 8388616.f, z[group]);
-      };
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {  // entries 4 t .. of spans i and i + 1
-        const uint32_t b0 = i < 4 ? u.x : u.y, b1 = i < 4 ? u.z : u.w;
-        const int sh = 8 * (i & 3), g0 = i * NG / 8, g1 = (i + 1) * NG / 8;
-        const float4 x = make_float4(value(b0, sh, g0), value(b0, sh + 4, g0), value(b1, sh, g0), value(b1, sh + 4, g0));
-        const float4 y = make_float4(value(b0, sh + 8, g1), value(b0, sh + 12, g1), value(b1, sh + 8, g1), value(b1, sh + 12, g1));
-        T* to = out + (size_t)r * kD + 16 * i;
+      for (int i = 0; i < 8; i += 4) {  // spans i .. i + 3
+        const uint32_t b0 = i ? u.y : u.x, b1 = i ? u.w : u.z;  // their bytes: entries 4 t, + 1; + 2, + 3
         if constexpr (sizeof(T) == 4) {
-          *reinterpret_cast<float4*>(to + 4 * t) = x;
-          *reinterpret_cast<float4*>(to + 16 + 4 * t) = y;
-        } else {  // the even lane of a pair takes eight entries of the one span, the odd lane of the other
-          const uint32_t x0 = tc::pack_bf16(x.x, x.y), x1 = tc::pack_bf16(x.z, x.w);
-          const uint32_t y0 = tc::pack_bf16(y.x, y.y), y1 = tc::pack_bf16(y.z, y.w);
-          const uint32_t p0 = __shfl_xor_sync(live, t & 1 ? x0 : y0, 1), p1 = __shfl_xor_sync(live, t & 1 ? x1 : y1, 1);
-          *reinterpret_cast<uint4*>(to + (t & 1 ? 16 + 4 * (t - 1) : 4 * t)) =
-              t & 1 ? make_uint4(p0, p1, y0, y1) : make_uint4(x0, x1, p0, p1);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t w = words[kv][(i + k) * NG / 8];
+            const float s = step_of(w), z = centre_of(w);
+            auto value = [&](uint32_t b, int sh) {  // 2^23 + c by its bits (conversions are a quarter rate)
+              return fmaf(s, __uint_as_float((b >> sh & 15u) | 0x4b000000u) - 8388616.f, z);
+            };
+            if (r < rows)
+              *reinterpret_cast<float4*>(out + (size_t)r * kD + 16 * (i + k) + 4 * t) =
+                  make_float4(value(b0, 8 * k), value(b0, 8 * k + 4), value(b1, 8 * k), value(b1, 8 * k + 4));
+          }
+        } else {
+          uint32_t x[4], y[4];
+          const uint32_t w01 = words[kv][i * NG / 8], w23 = words[kv][(i + 2) * NG / 8];
+          values_of(b0, w01, w23, x);
+          values_of(b1, w01, w23, y);
+#pragma unroll
+          for (int k = 0; k < 4; k += 2) {  // the even lane of a pair takes eight entries of span i + k, the odd lane of the next
+            const uint32_t p0 = __shfl_xor_sync(0xffffffffu, t & 1 ? x[k] : x[k + 1], 1);
+            const uint32_t p1 = __shfl_xor_sync(0xffffffffu, t & 1 ? y[k] : y[k + 1], 1);
+            if (r < rows)
+              *reinterpret_cast<uint4*>(out + (size_t)r * kD + 16 * (i + k) + (t & 1 ? 16 + 4 * (t - 1) : 4 * t)) =
+                  t & 1 ? make_uint4(p0, p1, x[k + 1], y[k + 1]) : make_uint4(x[k], y[k], p0, p1);
+          }
         }
       }
     }

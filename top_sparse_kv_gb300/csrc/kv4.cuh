@@ -43,26 +43,17 @@ __device__ __forceinline__ uint32_t kv4_word(float lo, float hi, float* s, float
   *z = __bfloat162float(zb);
   return (uint32_t)__bfloat16_as_ushort(sb) | ((uint32_t)__bfloat16_as_ushort(zb) << 16);
 }
-// The whole number next to (x - z) / s, ties to even, held to [-8, 7], and 8 more.  By the reciprocal:
-// the nearest whole number to the product (in the low bits of a sum with 1.5 * 2^23) is off only
-// next to a border, and the remainder, exact to half a step of itself, tells.  (Divisions and conversions of eight
-// entries a lane made 8,192 tokens' append 85 us, these 64.)
-__device__ __forceinline__ float kv4_inverse(float s) { return s >= 0x1p-100f ? 1.f / s : 0.f; }
+// The whole number next to (x - z) / s, ties to even, held to [-8, 7], and 8 more; 8 where s is 0.
+__device__ __forceinline__ uint32_t kv4_code(float x, float s, float z) {
+  return (uint32_t)((s > 0.f ? (int)fminf(fmaxf(rintf((x - z) / s), -8.f), 7.f) : 0) + 8);
+}
+// The same of many entries by s's reciprocal: a product with it, corrected by its own remainder, is the
+// quotient as a division rounds it (Markstein's correction), borders and all; the whole number is in the low
+// bits of its sum with 1.5 * 2^23 (entries lie within 2^18 steps of z).  For steps from 2^-100 up.
 __device__ __forceinline__ uint32_t kv4_code(float x, float s, float z, float inv) {
-  constexpr float kWhole = 12582912.f;
-  const float d = x - z;
-  int c;
-  if (inv > 0.f) {
-    // far entries first: what lies past the ends of the range is at an end
-    float y = fminf(fmaxf(fmaf(d, inv, kWhole), kWhole - 8.f), kWhole + 7.f);
-    const float n = y - kWhole, r = fmaf(-n, s, d), over = fabsf(r) - 0.5f * s;
-    c = __float_as_int(y) - 0x4b400000;
-    if (over >= 0.f && (over > 0.f || (c & 1))) c += r > 0.f ? 1 : -1;
-    c = c < -8 ? -8 : c > 7 ? 7 : c;
-  } else {  // steps under 2^-100, of 0 too
-    c = s > 0.f ? (int)fminf(fmaxf(rintf(d / s), -8.f), 7.f) : 0;
-  }
-  return (uint32_t)(c + 8);
+  const float d = x - z, q = d * inv, y = fmaf(fmaf(-q, s, d), inv, q) + 12582912.f;
+  const int c = __float_as_int(y) - (0x4b400000 - 8);
+  return (uint32_t)(c < 0 ? 0 : c > 15 ? 15 : c);
 }
 
 }  // namespace skv

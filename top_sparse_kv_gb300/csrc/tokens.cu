@@ -183,10 +183,20 @@ __device__ __forceinline__ void put_row4(const float (&x)[VE], unsigned char* ce
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
   }
   const uint32_t word = kv4_word(lo, hi, &s, &z);
-  const float inv = kv4_inverse(s);
   uint32_t w = 0;
+  const float inv = 1.f / s;
 #pragma unroll
   for (int j = 0; j < VE; ++j) w += kv4_code(x[j], s, z, inv) << (4 * j);
+  if (__any_sync(0xffffffffu, s < 0x1p-100f)) {  // (a step of 0 among them)
+    w = 0;
+#pragma unroll 1
+    for (int j = VE - 1; j >= 0; --j) {
+      float y = x[0];
+#pragma unroll
+      for (int i = 1; i < VE; ++i) y = j == i ? x[i] : y;
+      w = w << 4 | kv4_code(y, s, z);
+    }
+  }
   if constexpr (VE == 8) {  // sub: u's bit 2, i's bits 0, 1, 2; the word: u's bits 0, 1
     uint32_t y = __shfl_xor_sync(0xffffffffu, w, 2);
     w = __byte_perm(w, y, sub & 2 ? 0x3715 : 0x6240);
