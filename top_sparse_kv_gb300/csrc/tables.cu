@@ -25,47 +25,55 @@ struct TableArgs {
   int32_t *positions, *requests;
   long long* slots;
   int32_t* status;
+  int shift;  // log2 of the tokens of a block, or -1
 };
+
+// A short call is over before all its instructions have been fetched (64 requests and their 64
+// tokens: 7 us with the loops below unrolled and sums in 64 bits, most of it fetching), so there is
+// one copy of everything.  Sums are held at 2^31 - 1: what lies past it is past every limit.
+__device__ __forceinline__ unsigned add(unsigned x, unsigned y) { return min(x + y, 0x7fffffffu); }
 
 // Sums of N values over the block's threads before this one; the totals go to all.
 template <int N>
-__device__ __forceinline__ void block_scan(long long (&a)[N], long long (*warps)[N], long long (&all)[N]) {
+__device__ __forceinline__ void block_scan(unsigned (&a)[N], unsigned (*warps)[kThreads / 32], unsigned (&all)[N]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x[N];
+  unsigned x[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) x[i] = a[i];
+#pragma unroll 1
+  for (int level = 0; level < 2; ++level) {
+#pragma unroll 1
+    for (int off = 1; off < 32; off <<= 1)
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1)
+      for (int i = 0; i < N; ++i) {
+        const unsigned u = __shfl_up_sync(0xffffffffu, x[i], off);
+        if (lane >= off) x[i] = add(x[i], u);
+      }
+    if (level == 1) break;
+    if (lane == 31)
+#pragma unroll
+      for (int i = 0; i < N; ++i) warps[i][warp] = x[i];
+    __syncthreads();
+    // this thread's own, to be kept; then the warps' sums
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const long long u = __shfl_up_sync(0xffffffffu, x[i], off);
-      if (lane >= off) x[i] += u;
+      const unsigned own = __shfl_up_sync(0xffffffffu, x[i], 1);
+      a[i] = lane ? own : 0u;
+      x[i] = lane < kThreads / 32 ? warps[i][lane] : 0u;
     }
-  if (lane == 31)
-#pragma unroll
-    for (int i = 0; i < N; ++i) warps[warp][i] = x[i];
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    x[i] -= a[i];
-    all[i] = 0;
   }
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w)
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (w == warp) x[i] += all[i];
-      all[i] += warps[w][i];
-    }
-#pragma unroll
-  for (int i = 0; i < N; ++i) a[i] = x[i];
+  for (int i = 0; i < N; ++i) {
+    const unsigned before = __shfl_sync(0xffffffffu, x[i], warp ? warp - 1 : 0);
+    if (warp) a[i] = add(a[i], before);
+    all[i] = __shfl_sync(0xffffffffu, x[i], kThreads / 32 - 1);
+  }
 }
 
-__device__ __forceinline__ int saturate(long long x) { return x > 0x7fffffffLL ? 0x7fffffff : (int)x; }
-
 // the last request whose sum is at most i (sums ascend from sums[0] = 0; requests of nothing are passed over)
-__device__ __forceinline__ int find(const int* sums, int B, int i) {
+__device__ __forceinline__ int find(const unsigned* sums, int B, unsigned i) {
   int lo = 0, hi = B;
+#pragma unroll 1
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (sums[mid] <= i)
@@ -77,18 +85,21 @@ __device__ __forceinline__ int find(const int* sums, int B, int i) {
 }
 
 __global__ void __launch_bounds__(kThreads, 2) update_tables_kernel(const TableArgs a) {
-  extern __shared__ int smem[];
-  __shared__ long long s_asked[kThreads / 32][3], s_given[kThreads / 32][1];
+  extern __shared__ unsigned smem[];
+  __shared__ unsigned s_asked[3][kThreads / 32], s_given[1][kThreads / 32];
   __shared__ int s_last;
   const skv_tables& t = a.t;
   const int B = t.batch, bs = t.block_size;
-  int* rows = smem;               // [B + 1] rows of the step before each request (saturated)
-  int* given = rows + B + 1;      // [B + 1] blocks given to requests before
-  int* freed = given + B + 1;     // [B + 1] blocks given back by requests before
-  int* start = freed + B + 1;     // [B] first new position; -1: no tokens, or refused
-  int* from = start + B;          // [B] table index of its first new block, or of the first it gives back
-  int* lens = from + B;           // [B] the new length
+  unsigned* rows = smem;              // [B + 1] rows of the step before each request
+  unsigned* given = rows + B + 1;     // [B + 1] blocks given to requests before
+  unsigned* freed = given + B + 1;    // [B + 1] blocks given back by requests before
+  int* start = reinterpret_cast<int*>(freed + B + 1);  // [B] first new position; -1: no tokens, or refused
+  int* from = start + B;              // [B] table index of its first new block, or of the first it gives back
+  int* lens = from + B;               // [B] the new length
   const bool reports = blockIdx.x == 0;
+  auto blocks_of = [&](int n) {  // that hold n tokens
+    return a.shift >= 0 ? (int)(((unsigned)n + (unsigned)bs - 1) >> a.shift) : (int)(((unsigned)n + (unsigned)bs - 1) / (unsigned)bs);
+  };
   pdl_release();
   pdl_wait();
   int count = t.state[0];
@@ -96,54 +107,53 @@ __global__ void __launch_bounds__(kThreads, 2) update_tables_kernel(const TableA
   const int first = t.base / bs;
   const int per = (B + kThreads - 1) / kThreads, b0 = threadIdx.x * per, b1 = b0 + per < B ? b0 + per : B;
   // what each request asks for
-  long long asked[3] = {0, 0, 0};  // rows, blocks back, blocks needed
+  unsigned asked[3] = {0, 0, 0};  // rows, blocks back, blocks needed
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     const int L = t.seq_lens[b], n = a.n_new[b];
     const bool bad = L < 0 || L > t.max_len || (L > 0 && L < t.base);
-    const int have = !bad && L > t.base ? (int)(((long long)L + bs - 1) / bs) : first;
-    lens[b] = L;
-    start[b] = -1;
-    from[b] = have;
-    int need = 0, back = 0;
+    const int have = !bad && L > t.base ? blocks_of(L) : first;
+    int need = 0, back = 0, s = -1, at = have, len = L;
     if (n != 0 && bad) {
       if (reports) flag(a.status, SKV_DEV_BAD_LENGTH);
     } else if (n > 0) {
-      const int s = L == 0 ? t.base : L;
+      s = L == 0 ? t.base : L;
       if (s > t.max_len - n) {
+        s = -1;
         if (reports) flag(a.status, SKV_DEV_BAD_LENGTH);
       } else {
-        start[b] = s;
-        need = (int)(((long long)s + n + bs - 1) / bs) - have;
+        need = blocks_of(s + n) - have;
       }
     } else if (n < 0) {
       const long long left = (long long)L + n;
-      const int keep = left > t.base ? (int)((left + bs - 1) / bs) : first;
-      lens[b] = left > t.base ? (int)left : 0;
-      from[b] = keep;
-      back = have - keep;
+      len = left > t.base ? (int)left : 0;
+      at = len > 0 ? blocks_of(len) : first;
+      back = have - at;
     }
+    lens[b] = len;
+    start[b] = s;
+    from[b] = at;
     given[b] = need;
     freed[b] = back;
-    asked[0] += n > 0 ? n : 0;
-    asked[1] += back;
-    asked[2] += need;
+    asked[0] = add(asked[0], n > 0 ? n : 0);
+    asked[1] = add(asked[1], back);
+    asked[2] = add(asked[2], need);
   }
-  long long all[3], all_given[1];
+  unsigned all[3], all_given[1], before[1] = {0};
   block_scan<3>(asked, s_asked, all);
   // who gets it
-  long long before[1] = {0};
-  const long long free = count + all[1];
+  const unsigned free = add((unsigned)count, all[1]);
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     const int n = a.n_new[b], need = given[b], back = freed[b];
-    asked[2] += need;
-    rows[b] = saturate(asked[0]);
-    freed[b] = saturate(asked[1]);
-    asked[0] += n > 0 ? n : 0;
-    asked[1] += back;
+    rows[b] = asked[0];
+    freed[b] = asked[1];
+    asked[0] = add(asked[0], n > 0 ? n : 0);
+    asked[1] = add(asked[1], back);
+    asked[2] = add(asked[2], need);
     if (start[b] >= 0) {
-      const bool fits = asked[0] <= a.n_tokens, blocks = need == 0 || asked[2] <= free;
-      if (!fits && reports) flag(a.status, SKV_DEV_BAD_INDEX);
-      if (fits && !blocks && reports) flag(a.status, SKV_DEV_NO_BLOCK);
+      const bool fits = asked[0] <= (unsigned)a.n_tokens, blocks = need == 0 || asked[2] <= free;
+      if (!(fits && blocks) && reports) flag(a.status, fits ? SKV_DEV_NO_BLOCK : SKV_DEV_BAD_INDEX);
       if (fits && blocks) {
         lens[b] = start[b] + n;
       } else {
@@ -151,18 +161,19 @@ __global__ void __launch_bounds__(kThreads, 2) update_tables_kernel(const TableA
         given[b] = 0;
       }
     }
-    before[0] += given[b];
+    before[0] = add(before[0], given[b]);
   }
   block_scan<1>(before, s_given, all_given);
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    const int g = given[b];
-    given[b] = saturate(before[0]);
-    before[0] += g;
+    const unsigned g = given[b];
+    given[b] = before[0];
+    before[0] = add(before[0], g);
   }
   if (threadIdx.x == 0) {
-    rows[B] = saturate(all[0]);
-    given[B] = saturate(all_given[0]);
-    freed[B] = saturate(all[1]);
+    rows[B] = all[0];
+    given[B] = all_given[0];
+    freed[B] = all[1];
   }
   __syncthreads();
   const int K = given[B], R = freed[B];
@@ -178,61 +189,81 @@ __global__ void __launch_bounds__(kThreads, 2) update_tables_kernel(const TableA
   auto block_at = [&](int i) { return i < R ? back_at(i) : t.free_blocks[count - 1 - (i - R)]; };
 
   const long long step = (long long)gridDim.x * kThreads, me = (long long)blockIdx.x * kThreads + threadIdx.x;
-  // the slot map: four rows a thread, one bisection
-  for (long long r0 = me * 4; r0 < a.n_tokens; r0 += step * 4) {
-    int pos[4], req[4];
-    long long slot[4];
-    int b = r0 < rows[B] ? find(rows, B, (int)r0) : B;
-    int last = -1, e = 0;  // the table index that e was found for (of request b)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const long long r = r0 + i;
-      pos[i] = req[i] = -1;
-      slot[i] = -1;
-      if (r >= a.n_tokens || r >= rows[B]) continue;
-      while (b + 1 < B && rows[b + 1] <= r) ++b, last = -1;
-      if (start[b] < 0) continue;
-      const int p = start[b] + (int)(r - rows[b]);
-      pos[i] = p;
-      req[i] = b;
-      if (a.slots != nullptr) {
-        const int j = p / bs;
-        if (j != last) {
-          e = j < from[b] ? t.slot_table[(size_t)b * t.table_stride + j] : block_at(given[b] + j - from[b]);
-          last = j;
+  // the slot map: a row a thread, or four where there are more rows than threads: then of one or two
+  // requests mostly, and of two blocks at most where a block is four tokens or more
+  const int width = a.n_tokens > step ? 4 : 1;
+#pragma unroll 1
+  for (long long r0 = me * width; r0 < a.n_tokens; r0 += step * width) {
+    const int last = (int)(a.n_tokens - r0 < width ? a.n_tokens - r0 : width);
+#pragma unroll 1
+    for (int i = 0; i < last;) {  // runs of one request's rows, or of none
+      const int b = r0 + i < rows[B] ? find(rows, B, (unsigned)(r0 + i)) : B;
+      const int end = b < B && rows[b + 1] < r0 + last ? (int)(rows[b + 1] - r0) : last, n = end - i;
+      const bool on = b < B && start[b] >= 0;
+      int p = on ? start[b] + (int)(r0 + i - rows[b]) : 0;
+      // the blocks of the run's first and last row
+      int e[2] = {0, 0}, j0 = 0;
+      if (on && a.slots != nullptr) {
+        j0 = a.shift >= 0 ? p >> a.shift : p / bs;
+        const int j1 = blocks_of(p + n) - 1;
+#pragma unroll 1
+        for (int j = j0; j <= j1; j += j1 > j0 ? j1 - j0 : 1) {
+          const int x = j < from[b] ? t.slot_table[(size_t)b * t.table_stride + j] : block_at(given[b] + j - from[b]);
+          if (j == j0) e[0] = x;
+          e[1] = x;
         }
-        slot[i] = (long long)e * bs + (p - j * bs);
       }
-    }
-    if (r0 + 4 <= a.n_tokens) {
-      *reinterpret_cast<int4*>(a.positions + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-      *reinterpret_cast<int4*>(a.requests + r0) = make_int4(req[0], req[1], req[2], req[3]);
-      if (a.slots != nullptr) {
-        *reinterpret_cast<longlong2*>(a.slots + r0) = make_longlong2(slot[0], slot[1]);
-        *reinterpret_cast<longlong2*>(a.slots + r0 + 2) = make_longlong2(slot[2], slot[3]);
-      }
-    } else {
+      if (n == 4 && bs >= 4) {
+        const long long r = r0;
+        *reinterpret_cast<int4*>(a.positions + r) = on ? make_int4(p, p + 1, p + 2, p + 3) : make_int4(-1, -1, -1, -1);
+        const int q = on ? b : -1;
+        *reinterpret_cast<int4*>(a.requests + r) = make_int4(q, q, q, q);
+        if (a.slots != nullptr) {
+          long long s[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (r0 + i < a.n_tokens) {
-          a.positions[r0 + i] = pos[i];
-          a.requests[r0 + i] = req[i];
-          if (a.slots != nullptr) a.slots[r0 + i] = slot[i];
+          for (int k = 0; k < 4; ++k) {
+            const int in = p + k - j0 * bs;
+            s[k] = !on ? -1 : in < bs ? (long long)e[0] * bs + in : (long long)e[1] * bs + (in - bs);
+          }
+          *reinterpret_cast<longlong2*>(a.slots + r) = make_longlong2(s[0], s[1]);
+          *reinterpret_cast<longlong2*>(a.slots + r + 2) = make_longlong2(s[2], s[3]);
         }
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < n; ++k, ++p) {
+          const long long r = r0 + i + k;
+          a.positions[r] = on ? p : -1;
+          a.requests[r] = on ? b : -1;
+          if (a.slots != nullptr) {
+            int in = p - j0 * bs, x = in < bs ? e[0] : e[1];
+            if (on && bs < 4) {  // more than two blocks in a run
+              const int j = p / bs;
+              x = j < from[b] ? t.slot_table[(size_t)b * t.table_stride + j] : block_at(given[b] + j - from[b]);
+              in = p - j * bs;
+            }
+            a.slots[r] = on ? (long long)x * bs + (in < bs ? in : in - bs) : -1;
+          }
+        }
+      }
+      i = end;
     }
   }
-  // new table entries
-  for (long long i = me; i < K; i += step) {
-    const int b = find(given, B, (int)i);
-    t.slot_table[(size_t)b * t.table_stride + from[b] + ((int)i - given[b])] = block_at((int)i);
-  }
-  // the stack takes what is left of the blocks given back
-  for (long long i = me; i < (long long)R - K; i += step) {
-    const int e = back_at(R - 1 - (int)i);
-    if (count + i < t.n_blocks)
-      t.free_blocks[count + i] = e;
-    else
-      flag(a.status, SKV_DEV_BAD_SLOT);
+  // new table entries; then the stack takes what is left of the blocks given back
+#pragma unroll 1
+  for (long long i = me; i < K || i < (long long)R - K; i += step) {
+    const bool out = i < K;
+    const int e = block_at(out ? (int)i : R - 1 - (int)i);
+    if (out) {
+      const int b = find(given, B, (int)i);
+      t.slot_table[(size_t)b * t.table_stride + from[b] + ((int)i - given[b])] = e;
+    }
+    if (i < (long long)R - K) {
+      const int f = out ? back_at(R - 1 - (int)i) : e;
+      if (count + i < t.n_blocks)
+        t.free_blocks[count + i] = f;
+      else
+        flag(a.status, SKV_DEV_BAD_SLOT);
+    }
   }
   // lengths and the count, once every CTA has read them
   __syncthreads();
@@ -247,6 +278,7 @@ __global__ void __launch_bounds__(kThreads, 2) update_tables_kernel(const TableA
     cluster_sync();
     if (blockIdx.x > 0) return;
   }
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) t.seq_lens[b] = lens[b];
   if (threadIdx.x == 0) {
     const long long left = (long long)count + R - K;
@@ -261,16 +293,18 @@ int tables_max_batch() { return kMaxBatch; }
 
 skv_status launch_update_tables(const skv_tables& t, const int32_t* n_new, int n_tokens, int32_t* positions,
                                 int32_t* requests, int64_t* slots, int32_t* status, cudaStream_t st) {
-  TableArgs a{t, n_new, n_tokens, positions, requests, reinterpret_cast<long long*>(slots), status};
+  TableArgs a{t, n_new, n_tokens, positions, requests, reinterpret_cast<long long*>(slots), status, -1};
+  for (int i = 0; i < 31; ++i)
+    if (t.block_size == 1 << i) a.shift = i;
   const int smem = 6 * 4 * (t.batch + 1);
   const skv_status prep = prepare_kernel((const void*)update_tables_kernel, 6 * 4 * (kMaxBatch + 1));
   if (prep != SKV_OK) return prep;
-  // A sweep of rows a CTA, or of the blocks that come with them, two CTAs a SM at most.  Without rows
-  // the call gives blocks back, how many is known on the device only: as for all that the tables
-  // hold, a CTA a SM at most.
+  // A sweep of rows a CTA, two CTAs a SM at most; the blocks that come with them are fewer.  Without rows
+  // the call gives blocks back, how many is known on the device only: a sweep of a sixteenth of what
+  // the tables hold, a CTA a SM at most.
   const long long entries = (long long)t.batch * t.table_stride;
-  const long long blocks = n_tokens > 0 ? n_tokens / t.block_size + t.batch : entries < t.n_blocks ? entries : t.n_blocks;
-  long long ctas = ((long long)n_tokens + 4 * kThreads - 1) / (4 * kThreads), more = (blocks + 8 * kThreads - 1) / (8 * kThreads);
+  const long long blocks = n_tokens > 0 ? 0 : entries < t.n_blocks ? entries : t.n_blocks;
+  long long ctas = ((long long)n_tokens + 4 * kThreads - 1) / (4 * kThreads), more = (blocks + 16 * kThreads - 1) / (16 * kThreads);
   if (more > num_sms()) more = num_sms();
   if (ctas < more) ctas = more;
   if (ctas < 1) ctas = 1;

@@ -7,6 +7,7 @@ single skv_decode_step call enqueued on the current stream.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional
 
@@ -311,64 +312,66 @@ class Kv4Step:
     def __init__(self, problem: B.Problem, pool: B.Kv4Pool):
         B.check_pool4(problem, pool)
         self.p, self.pool = problem, pool
-        p, dev = problem, problem.seq_lens.device
+        p, self._dev, lib = problem, problem.seq_lens.device, B.lib()
         self._device = p.seq_lens.get_device()
         self._held = [*vars(problem).values(), *vars(pool).values()]
         self._p, self._pool, self._group = ctypes.byref(p.c()), ctypes.byref(pool.c4()), pool.group
         heads = B.list_heads(p)
-        self._shapes = dict(q=(p.batch, p.n_q_heads, 128), q_score=(p.batch, p.n_idx_q_heads or p.n_q_heads, 128),
-                            scores=(p.batch, heads, p.max_len), idx=(p.batch, heads, p.topk))
-        self._rows = (p.batch, heads, p.n_sink + p.topk + p.n_local, 128)
-        self.status = torch.zeros((1,), dtype=torch.int32, device=dev)
-        self.ws = torch.empty((max(B.skv_kv4_workspace_size(p), 16),), dtype=torch.uint8, device=dev)
-        self.out = torch.empty(self._shapes["q"], dtype=torch.bfloat16, device=dev)
-        self.lse = torch.empty(self._shapes["q"][:2], dtype=torch.float32, device=dev)
-        self._st, self._ws = self.status.data_ptr(), (self.ws.data_ptr(), self.ws.numel())
-        self._outs = (self.out.data_ptr(), self.lse.data_ptr())
+        self._q = torch.Size((p.batch, p.n_q_heads, 128))
+        self._q_score = torch.Size((p.batch, p.n_idx_q_heads or p.n_q_heads, 128))
+        self._s, self._i = torch.Size((p.batch, heads, p.max_len)), torch.Size((p.batch, heads, p.topk))
+        self._rows = torch.Size((p.batch, heads, p.n_sink + p.topk + p.n_local, 128))
+        self._type = B.element_type(p)
+        self.status = torch.zeros((1,), dtype=torch.int32, device=self._dev)
+        self.ws = torch.empty((max(B.skv_kv4_workspace_size(p), 16),), dtype=torch.uint8, device=self._dev)
+        self.out = torch.empty(self._q, dtype=torch.bfloat16, device=self._dev)
+        self.lse = torch.empty(self._q[:2], dtype=torch.float32, device=self._dev)
+        self._st = self.status.data_ptr()
+        self._outs = (self.out.data_ptr(), self.lse.data_ptr(), self.ws.data_ptr(), self.ws.numel(), self._st)
+        self._score, self._attn = lib.skv_score_kv4, lib.skv_attn_kv4
+        self._step, self._gather = lib.skv_decode_step_kv4, lib.skv_gather_kv4
         self._scores = self._idx = None
 
     @property
     def scores(self) -> torch.Tensor:
         """[batch, heads, max_len]; made when first used."""
         if self._scores is None:
-            self._scores = torch.empty(self._shapes["scores"], dtype=torch.float32, device=self.p.seq_lens.device)
+            self._scores = torch.empty(self._s, dtype=torch.float32, device=self._dev)
         return self._scores
 
     @property
     def idx(self) -> torch.Tensor:
         """[batch, heads, topk]; made when first used."""
         if self._idx is None:
-            self._idx = torch.empty(self._shapes["idx"], dtype=torch.int32, device=self.p.seq_lens.device)
+            self._idx = torch.empty(self._i, dtype=torch.int32, device=self._dev)
         return self._idx
 
-    def _ptr(self, name, t, dtype):
-        shape = self._shapes[name]
+    def _ptr(self, name, t, dtype, shape):
         if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != self._device:
-            raise ValueError(f"{name}: contiguous {dtype} {list(shape)} on {self.p.seq_lens.device} expected")
+            raise ValueError(f"{name}: contiguous {dtype} {list(shape)} on {self._dev} expected")
         return B.list_ptr(self.p, t)
-
-    def _go(self, name, *args, stream):
-        st = getattr(B.lib(), name)(self._p, *args, self._st, B.raw_stream(self._device, stream))
-        if st:
-            raise B.SkvError(name, st)
 
     def score(self, q_score, scores=None, stream=None):
         """Scores of the candidates into `scores` (the step's own unless given), which it returns."""
         scores = self.scores if scores is None else scores
-        self._go("skv_score_kv4", self._ptr("q_score", q_score, torch.bfloat16), self._pool, self._group,
-                 self._ptr("scores", scores, torch.float32), stream=stream)
+        st = self._score(self._p, self._ptr("q_score", q_score, torch.bfloat16, self._q_score), self._pool, self._group,
+                         self._ptr("scores", scores, torch.float32, self._s), self._st, B.raw_stream(self._device, stream))
+        if st:
+            raise B.SkvError("skv_score_kv4", st)
         return scores
 
     def topk(self, stream=None):
         """The selection of the step's own scores, into idx."""
-        if self.p.topk == 0:
-            return self.idx
-        B.skv_topk(self.p, self.scores, self.idx, self.ws, self.status, stream)
+        if self.p.topk > 0:
+            B.skv_topk(self.p, self.scores, self.idx, self.ws, self.status, stream)
         return self.idx
 
     def _attend(self, q, idx, stream):
-        self._go("skv_attn_kv4", self._ptr("q", q, torch.bfloat16), self._pool, self._group,
-                 None if idx is None else self._ptr("idx", idx, torch.int32), *self._outs, *self._ws, stream=stream)
+        st = self._attn(self._p, self._ptr("q", q, torch.bfloat16, self._q), self._pool, self._group,
+                        None if idx is None else self._ptr("idx", idx, torch.int32, self._i), *self._outs,
+                        B.raw_stream(self._device, stream))
+        if st:
+            raise B.SkvError("skv_attn_kv4", st)
         return self.out, self.lse
 
     def attend(self, q, idx=None, stream=None):
@@ -381,10 +384,12 @@ class Kv4Step:
 
     def run(self, q, q_score=None, stream=None):
         """(out, lse) of one decode step; scores and idx hold its scores and selection."""
-        self._go("skv_decode_step_kv4", self._ptr("q", q, torch.bfloat16),
-                 None if q_score is None else self._ptr("q_score", q_score, torch.bfloat16), self._pool, self._group,
-                 self._ptr("scores", self.scores, torch.float32), self._ptr("idx", self.idx, torch.int32), *self._outs,
-                 *self._ws, stream=stream)
+        st = self._step(self._p, self._ptr("q", q, torch.bfloat16, self._q),
+                        None if q_score is None else self._ptr("q_score", q_score, torch.bfloat16, self._q_score),
+                        self._pool, self._group, self.scores.data_ptr(), B.list_ptr(self.p, self.idx), *self._outs,
+                        B.raw_stream(self._device, stream))
+        if st:
+            raise B.SkvError("skv_decode_step_kv4", st)
         return self.out, self.lse
 
     def gather(self, idx=None, k_out=None, v_out=None, stream=None):
@@ -392,20 +397,16 @@ class Kv4Step:
         unless given.  Without a selection (topk 0) those of sink and window."""
         if idx is None and self.p.topk > 0:
             idx = self.idx
-        new = [t if t is not None else self._new(stream) for t in (k_out, v_out)]
-        for name, t in zip(("k_out", "v_out"), new):
-            B.dense(self.p, name, t, B.element_type(self.p), self._rows)
-        self._go("skv_gather_kv4", self._pool, self._group,
-                 None if idx is None else self._ptr("idx", idx, torch.int32), new[0].data_ptr(), new[1].data_ptr(),
-                 stream=stream)
-        return tuple(new)
-
-    def _new(self, stream):
-        """An output, of the allocator's pool of the stream that writes it."""
-        if stream is not None:
-            with torch.cuda.stream(stream):
-                return self._new(None)
-        return torch.empty(self._rows, dtype=B.element_type(self.p), device=self.p.seq_lens.device)
+        ip = None if idx is None else self._ptr("idx", idx, torch.int32, self._i)
+        if k_out is None or v_out is None:
+            with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():  # (its allocator's pool)
+                k_out = torch.empty(self._rows, dtype=self._type, device=self._dev) if k_out is None else k_out
+                v_out = torch.empty(self._rows, dtype=self._type, device=self._dev) if v_out is None else v_out
+        st = self._gather(self._p, self._pool, self._group, ip, self._ptr("k_out", k_out, self._type, self._rows),
+                          self._ptr("v_out", v_out, self._type, self._rows), self._st, B.raw_stream(self._device, stream))
+        if st:
+            raise B.SkvError("skv_gather_kv4", st)
+        return k_out, v_out
 
 
 class BlockTables:
@@ -425,7 +426,8 @@ class BlockTables:
         self.tables.check(problem)
         self.status = torch.zeros((1,), dtype=torch.int32, device=dev)
         self._held = [*vars(problem).values(), *vars(self.tables).values()]
-        self._device = problem.seq_lens.get_device()
+        self._dev, self._device, self._batch = dev, problem.seq_lens.get_device(), torch.Size((problem.batch,))
+        self._none = tuple(torch.empty(0, dtype=t, device=dev) for t in (torch.int32, torch.int32, torch.int64))
         self._t, self._st = ctypes.byref(self.tables.c(problem)), self.status.data_ptr()
         self._call = B.lib().skv_update_tables
 
@@ -436,23 +438,29 @@ class BlockTables:
 
     def _new(self, n, stream):
         """Outputs, of the allocator's pool of the stream that writes them."""
+        if n == 0:
+            return self._none
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self._new(n, None)
-        dev = self.p.seq_lens.device
-        return (torch.empty((n,), dtype=torch.int32, device=dev), torch.empty((n,), dtype=torch.int32, device=dev),
-                torch.empty((n,), dtype=torch.int64, device=dev))
+        return (torch.empty(n, dtype=torch.int32, device=self._dev), torch.empty(n, dtype=torch.int32, device=self._dev),
+                torch.empty(n, dtype=torch.int64, device=self._dev))
 
     def update(self, n_new, n_tokens: int = 0, out=None, stream=None):
         """(positions, requests, slots) of the step's n_tokens rows: new tensors, unless given as `out`
         (slots may be None there)."""
-        rows = self._new(n_tokens, stream) if out is None else out
-        B.dense(self.p, "n_new", n_new, torch.int32, (self.p.batch,))
-        if out is not None:
+        if n_new.dtype != torch.int32 or n_new.shape != self._batch or not n_new.is_contiguous() \
+                or n_new.get_device() != self._device:
+            raise ValueError(f"n_new: contiguous int32 {list(self._batch)} on {self._dev} expected")
+        if out is None:
+            rows = self._new(n_tokens, stream)
+        else:
+            rows = out
             for name, t, dtype in zip(("positions", "requests", "slots"), out, (torch.int32, torch.int32, torch.int64)):
                 B.dense(self.p, name, t, dtype, (n_tokens,))
-        st = self._call(self._t, n_new.data_ptr(), n_tokens, *(None if t is None else t.data_ptr() for t in rows),
-                        self._st, B.raw_stream(self._device, stream))
+        at, req, slots = rows
+        st = self._call(self._t, n_new.data_ptr(), n_tokens, at.data_ptr(), req.data_ptr(),
+                        None if slots is None else slots.data_ptr(), self._st, B.raw_stream(self._device, stream))
         if st:
             raise B.SkvError("skv_update_tables", st)
         return rows
