@@ -24,7 +24,6 @@
 namespace skv {
 namespace {
 
-constexpr int kW = 8;  // warps a CTA
 constexpr int kMaxParts = 512;  // CTAs at most
 constexpr int kSlotFloats = 16 * (kD + 2);  // a partial: O of 16 heads, then their (reference, sum)
 
@@ -88,7 +87,7 @@ __device__ __forceinline__ void settle(const Kv4Args& a, Cursor& c) {  // tile m
 // a CTA's time (short histories: a CTA of many units would be last by far); of the weight W, CTA
 // c of n takes [W c / n, W (c + 1) / n), the tiles that lie there.  A unit's first kUnit places
 // hold no tile.
-constexpr int kUnit = 16;
+constexpr int kUnit = 16, kLeast = 16;  // (a CTA weighs kLeast at least)
 __device__ __forceinline__ long long quotient(long long x, long long y) {  // (64 bits: hundreds of cycles)
   return (x | y) >> 32 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
 }
@@ -102,13 +101,12 @@ struct Share {
 };
 
 // Every thread of the CTA gets the walk's length and the place where this CTA's share starts.
-template <int MODE, int THREADS>
+template <int MODE, int W>
 __device__ __forceinline__ Share find_share(const Kv4Args& a, Cursor* c) {
-  constexpr int kWarpsHere = THREADS / 32, kLeast = 2 * kW;  // weight of a CTA at least
-  __shared__ long long s_sum[2][kWarpsHere], s_tiles[2], s_place;
+  __shared__ long long s_sum[2][W], s_tiles[2], s_place;
   __shared__ int s_at[3];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per = (a.B + THREADS - 1) / THREADS, b0 = threadIdx.x * per, b1 = b0 + per < a.B ? b0 + per : a.B;
+  const int per = (a.B + 32 * W - 1) / (32 * W), b0 = threadIdx.x * per, b1 = b0 + per < a.B ? b0 + per : a.B;
   long long tiles = 0, units = 0;
   for (int b = b0; b < b1; ++b) {
     const int L = blockIdx.x == 0 ? load_len(a.seq_lens, b, a.max_len, a.status) : len_of(a, b);
@@ -128,8 +126,9 @@ __device__ __forceinline__ Share find_share(const Kv4Args& a, Cursor* c) {
   long long all = 0, all_units = 0;
   x -= tiles;
   y -= units;
-#pragma unroll
-  for (int w = 0; w < kWarpsHere; ++w) {
+  const int warps = a.B < 32 * W ? (a.B + 31) >> 5 : W;  // that have a request
+#pragma unroll 1
+  for (int w = 0; w < warps; ++w) {
     if (w == warp) x += all, y += all_units;
     all += s_sum[0][w];
     all_units += s_sum[1][w];
@@ -181,7 +180,7 @@ __device__ __forceinline__ Share find_share(const Kv4Args& a, Cursor* c) {
 
 // ---------------------------------------------------------------------------- a warp's ring
 //
-// Tile i of a CTA's share is warp i % kW's.  A warp fetches its own tiles, S of them ahead, into a
+// Tile i of a CTA's share is warp i % W's.  A warp fetches its own tiles, S of them ahead, into a
 // ring of its own: a stage is the cell of K, then the cell of V, as they lie in the pool.
 // (A warp that feeds the others leaves them 96 registers of 128: the products spill.)
 
@@ -257,7 +256,7 @@ __device__ __forceinline__ uint32_t row_id(const Kv4Args& a, bool reports, const
 
 // A history's tiles: whole cells.  The warp finds 32 tiles at a time, a lane a tile; the entries of
 // the next 32 are loaded when these are started.
-template <int MODE, int NG, bool V, int S>
+template <int MODE, int NG, bool V, int W, int S>
 struct CellFeeder {
   static constexpr int kCell = kv4_cell(NG), kStage = (V ? 2 : 1) * kCell;
   static constexpr uint32_t kNone = 0xffffffffu, kHost = 0x80000000u;
@@ -283,7 +282,7 @@ struct CellFeeder {
     const int lane = threadIdx.x & 31;
     Cursor c = at;
     __syncwarp();
-    c.tile += lane * kW;
+    c.tile += lane * W;
     in = kNone;
     if (lane < ahead) {
       settle<MODE>(a, c);
@@ -293,7 +292,7 @@ struct CellFeeder {
       e = __ldg(table_row(a.pool, c.b, c.h, a.heads) + block);
       if (a.pool.per_head && e >= 0) in -= c.h * a.cells;
       if (lane == 31) {
-        c.tile += kW;
+        c.tile += W;
         at = c;
       }
     }
@@ -357,7 +356,7 @@ struct CellFeeder {
 // A list's tiles: rows, by 16-byte copies.  A lane finds a row of two tiles (this warp's next and the one
 // after) in three steps -- its place's position, that one's entry, the row -- so each load has two
 // tiles' time to arrive.
-template <int NG, int S>
+template <int NG, int W, int S>
 struct RowFeeder {
   static constexpr int kCell = kv4_cell(NG), kStage = 2 * kCell;
   const Kv4Args& a;
@@ -370,7 +369,7 @@ struct RowFeeder {
 
   __device__ __forceinline__ RowFeeder(const Kv4Args& args, Cursor&, uint32_t* masks_, uint32_t ring_, Cursor at, int n)
       : a(args), masks(masks_), to(ring_), end(ring_ + S * kStage), c(at), left(n), half(-2), row(kNoRow) {
-    c.tile += (threadIdx.x >> 4 & 1) * kW;
+    c.tile += (threadIdx.x >> 4 & 1) * W;
     left -= threadIdx.x >> 4 & 1;
     r0.t = r1.t = -1;
   }
@@ -385,7 +384,7 @@ struct RowFeeder {
         if (left > 0 && c.tile >= c.nt) settle<kList>(a, c);
         row_position(a, c, left > 0, lane & 15, r1);
         left -= 2;
-        c.tile += 2 * kW;
+        c.tile += 2 * W;
       }
       half = 0;
     }
@@ -481,13 +480,17 @@ __device__ __forceinline__ float step_of(uint32_t w) { return __uint_as_float(w 
 __device__ __forceinline__ float centre_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 // The four operand registers of two bytes' worth of codes, in the order low and high half of
-// the first byte, low and high half of the second: subnormal fp16 pairs, 2^-24 and 2^-20 a unit.
+// the first byte, low and high half of the second: subnormal fp16 pairs, 2^-24 and 2^-20 a unit.  The second byte,
+// brought down by a permutation that clears what is above it, is a subnormal itself, and BYTE leaves it in the
+// high half's place: 16 high + low, 2^-24 a unit, of which a sum of products gives the low
+// half's back once at the end (a mask a register less: a million keys 211 -> 204 us).
+template <bool BYTE>
 __device__ __forceinline__ void spread(uint32_t x, uint32_t* r) {
-  const uint32_t y = x >> 8;
+  const uint32_t y = __byte_perm(x, 0u, 0x4341);
   r[0] = x & 0x000f000fu;
   r[1] = x & 0x00f000f0u;
   r[2] = y & 0x000f000fu;
-  r[3] = y & 0x00f000f0u;
+  r[3] = BYTE ? y : y & 0x00f000f0u;
 }
 
 // A power of two that brings |x| <= mx under 2^10 (its own inverse is exact too).
@@ -497,8 +500,12 @@ __device__ __forceinline__ float fit(float mx) {
   return __uint_as_float((uint32_t)e << 23);
 }
 
-// Queries as the second operand: columns are heads, k-step j the entries 16 j .. 16 j + 15 in
-// the order that the codes come in; wz: the group sums, three bf16 parts, against words.
+// Queries as the second operand: columns are heads, k-steps 16 entries in the order that the codes
+// come in; wz: the group sums, three bf16 parts, against words.  Groups of 32: k-step j has
+// the entries 16 j .. 16 j + 15, a lane's register of codes one byte each of its two runs of eight.
+// Larger groups: k-step 4 a + 2 b + c has of the spans 4 a + c and 4 a + c + 2 the
+// bytes b of each lane, and a register of codes comes from one word as it is (a million keys in groups
+// of 128: 215 -> 211 us).
 template <int NT>
 struct QFrag {
   uint32_t b[NT][8][2];
@@ -506,11 +513,11 @@ struct QFrag {
   float unit[NT][2];  // what a logit of heads 2 t, 2 t + 1 comes in: 2^20 / their power of two
 };
 
-// A CTA makes them together, warp j the j-th k-step, and every warp takes its lanes' copies.
+// A CTA makes them together, warp j < 8 the j-th k-step, and every warp takes its lanes' copies.
 template <int NT>
 struct QShared {
   uint32_t b[NT][8][2][32], wz[NT][3][32];
-  float largest[8 * NT][kW], part[8][8 * NT];  // of a head: of each warp's entries; sums of a k-step
+  float largest[8 * NT][8], part[8][8 * NT];  // of a head: of each warp's entries; sums of a k-step
 };
 
 // This warp's k-step of the columns: entries 16 warp + 4 t .. of head 8 nt + g.  MEAN: of the heads' sum.
@@ -523,7 +530,7 @@ __device__ __forceinline__ void load_queries(const __nv_bfloat16* q, int n, floa
     for (int i = 0; i < 4; ++i) x[nt][i] = 0.f;
     const int head = 8 * nt + g;
 #pragma unroll 1
-    for (int h = MEAN ? 0 : head; h < n; ++h) {
+    for (int h = MEAN ? 0 : head; h < n && warp < 8; ++h) {
       const uint2 u = *reinterpret_cast<const uint2*>(q + (size_t)h * kD + 16 * warp + 4 * t);
       x[nt][0] += __uint_as_float(u.x << 16);
       x[nt][1] += __uint_as_float(u.x & 0xffff0000u);
@@ -552,7 +559,7 @@ __device__ __forceinline__ void make_queries(float (&x)[NT][4], int n, QShared<N
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
       sum += __shfl_xor_sync(0xffffffffu, sum, off);
     }
-    if (t == 0) {
+    if (t == 0 && warp < 8) {
       s.largest[head][warp] = m;
       s.part[warp][head] = sum;
     }
@@ -582,8 +589,17 @@ __device__ __forceinline__ void make_queries(float (&x)[NT][4], int n, QShared<N
         x[nt][i] = y;
       }
     }
-    s.b[nt][warp][0][lane] = pack_f16(16.f * x[nt][0], 16.f * x[nt][2]);
-    s.b[nt][warp][1][lane] = pack_f16(x[nt][1], x[nt][3]);
+    if (warp < 8) {
+      if (NG == 4) {
+        s.b[nt][warp][0][lane] = pack_f16(16.f * x[nt][0], 16.f * x[nt][2]);
+        s.b[nt][warp][1][lane] = pack_f16(x[nt][1], x[nt][3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          reinterpret_cast<__half*>(&s.b[nt][(warp & 4) + (i & 2) + (warp & 1)][i & 1][lane])[warp >> 1 & 1] =
+              __float2half_rn(i & 1 ? x[nt][i] : 16.f * x[nt][i]);
+      }
+    }
     if (warp == 0) {  // the t-th group's sum, in the products' unit
       float z = 0.f;
       if (t < NG && (!MEAN || g == 0)) {
@@ -636,11 +652,14 @@ __device__ __forceinline__ void logits(uint32_t cell, const QFrag<NT>& f, float 
   }
   float acc[NT][4];
 #pragma unroll
-  for (int jj = 0; jj < 4; ++jj) {  // two k-steps: bytes 2 jj, 2 jj + 1 of the lane's two runs of eight
-    const uint32_t sel = jj & 1 ? 0x7632u : 0x5410u;
+  for (int jj = 0; jj < 4; ++jj) {  // two k-steps
     uint32_t r0[4], r1[4];
-    spread(__byte_perm(jj < 2 ? k0.x : k0.y, jj < 2 ? k0.z : k0.w, sel), r0);
-    spread(__byte_perm(jj < 2 ? k1.x : k1.y, jj < 2 ? k1.z : k1.w, sel), r1);
+    auto codes = [&](const uint4& k) {
+      const uint32_t x = jj < 2 ? k.x : k.y, z = jj < 2 ? k.z : k.w;
+      return NG == 4 ? __byte_perm(x, z, jj & 1 ? 0x7632u : 0x5410u) : jj & 1 ? z : x;
+    };
+    spread<false>(codes(k0), r0);
+    spread<false>(codes(k1), r1);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int j = 2 * jj + i;
@@ -671,7 +690,7 @@ template <int NG, int NT>
 struct State {
   float l[NT][2], ref[NT][2];
   float top[NT][2];   // the logit, in its column's unit, past which the maximum moves
-  float o[NT][8][4];  // rows 2 g (2^-24 a unit) and 2 g + 1 (2^-20) of entries 16 i, columns heads 2 t, 2 t + 1
+  float o[NT][8][4];  // rows 2 g (2^-24 a unit) and 2 g + 1 (2^-20; i odd: both, 2^-24) of entries 16 i, columns heads 2 t, 2 t + 1
   float z[NT][NG][2];
   int sigma;          // steps are below 2^(sigma + 1)
 };
@@ -804,8 +823,8 @@ __device__ __forceinline__ void attend_cell(uint32_t cell, uint32_t mask, const 
   for (int jj = 0; jj < 4; ++jj) {
     const uint32_t sel = jj & 1 ? 0x7632u : 0x5410u;
     uint32_t r0[4], r1[4];
-    spread(__byte_perm(jj < 2 ? v[0].x : v[0].y, jj < 2 ? v[1].x : v[1].y, sel), r0);
-    spread(__byte_perm(jj < 2 ? v[2].x : v[2].y, jj < 2 ? v[3].x : v[3].y, sel), r1);
+    spread<true>(__byte_perm(jj < 2 ? v[0].x : v[0].y, jj < 2 ? v[1].x : v[1].y, sel), r0);
+    spread<true>(__byte_perm(jj < 2 ? v[2].x : v[2].y, jj < 2 ? v[3].x : v[3].y, sel), r1);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int j = 2 * jj + i;
@@ -824,42 +843,46 @@ __device__ __forceinline__ void attend_cell(uint32_t cell, uint32_t mask, const 
   }
 }
 
-template <int NG, int NT>
+template <int NG, int NT, int MODE>
 struct AttnShape {
-  // Stages of 2.5 KB a warp and CTAs a SM: one column tile, 16 warps a SM with two or three tiles each
-  // on their way (four stages: no faster); two column tiles take the registers of two CTAs.
-  static constexpr int kStages = NT == 1 ? 3 : 6;
-  static constexpr int kCtas = NT == 1 ? 2 : 1;
+  // Warps of a CTA, CTAs a SM, stages of 2.5 KB a warp.  A CTA a SM: of two the schedulers serve the one that came first first,
+  // it ends at 80 % of the time and leaves the SM half empty (a million keys, 8 warps in either: 231 us; 12 or
+  // 16 warps in one: 215, 8: 258), and 12 warps are no slower than 16 while the products keep 168
+  // registers (8 requests of 32K: 78 us against 81).  A list's rows arrive late rather, and two CTAs
+  // hide more of that (8 requests' 3,409 rows of 32K: 26.8 us, one of 12 or 16 warps 28.8).  Two column tiles take all
+  // the registers of 8 warps.
+  static constexpr int kCtas = NT == 1 && MODE == kList ? 2 : 1;
+  static constexpr int kW = NT == 1 && MODE == kDense ? 12 : 8, kStages = NT == 2 ? 6 : MODE == kDense ? 5 : 3;
   static constexpr int kRing = kW * kStages * 2 * kv4_cell(NG);
   static constexpr int kRow = kD + 4;  // floats of a head's partial row: heads 2 t, 2 t + 2 an eighth of the banks apart
   static constexpr int kOut = kW * 8 * NT * kRow * 4;
   static constexpr int kSmem = kRing + kOut;
 };
 
-template <int MODE, int NG, int S>
+template <int MODE, int NG, int W, int S>
 struct Pick {
-  using type = CellFeeder<MODE, NG, true, S>;
+  using type = CellFeeder<MODE, NG, true, W, S>;
 };
-template <int NG, int S>
-struct Pick<kList, NG, S> {
-  using type = RowFeeder<NG, S>;
+template <int NG, int W, int S>
+struct Pick<kList, NG, W, S> {
+  using type = RowFeeder<NG, W, S>;
 };
 
 template <int NG, int NT, int MODE>
-__global__ void __launch_bounds__(32 * kW, AttnShape<NG, NT>::kCtas) kv4_attn_kernel(const Kv4Args a) {
-  using Shape = AttnShape<NG, NT>;
-  constexpr int S = Shape::kStages, HC = 8 * NT;  // columns
+__global__ void __launch_bounds__(32 * AttnShape<NG, NT, MODE>::kW, AttnShape<NG, NT, MODE>::kCtas) kv4_attn_kernel(const Kv4Args a) {
+  using Shape = AttnShape<NG, NT, MODE>;
+  constexpr int W = Shape::kW, S = Shape::kStages, HC = 8 * NT;  // columns
   constexpr int kStage = 2 * kv4_cell(NG);
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ Cursor s_at[kW];
-  __shared__ uint32_t s_mask[MODE == kList ? kW : 1][S];
-  __shared__ float2 s_ml[HC][kW];
+  __shared__ Cursor s_at[W];
+  __shared__ uint32_t s_mask[MODE == kList ? W : 1][S];
+  __shared__ float2 s_ml[HC][W];
   __shared__ __align__(16) QShared<NT> s_q;
   float* s_o = reinterpret_cast<float*>(smem + Shape::kRing);
   pdl_release();
   pdl_wait();
   Cursor u;
-  const Share mine = find_share<MODE, 32 * kW>(a, &u);
+  const Share mine = find_share<MODE, W>(a, &u);
   if (mine.tiles == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int share = mine.tiles;
@@ -869,12 +892,12 @@ __global__ void __launch_bounds__(32 * kW, AttnShape<NG, NT>::kCtas) kv4_attn_ke
   auto queries = [&]() { return a.q + ((size_t)u.b * a.Hq + (size_t)u.h * a.G) * kD; };
   float x[NT][4];
   load_queries<NT, false>(queries(), a.G, x);
-  typename Pick<MODE, NG, S>::type feed(a, s_at[warp], s_mask[MODE == kList ? warp : 0], ring, at,
-                                        share > warp ? (share - warp + kW - 1) / kW : 0);
+  typename Pick<MODE, NG, W, S>::type feed(a, s_at[warp], s_mask[MODE == kList ? warp : 0], ring, at,
+                                        share > warp ? (share - warp + W - 1) / W : 0);
 #pragma unroll 1
   for (int i = 0; i < S - 1; ++i) feed.issue();
   long long place = mine.place;  // of the unit among the weights
-  int stage = 0;
+  int stage = 0, next = warp;  // this warp's next tile
   // units of the share: tiles [from, to) of it, the unit's first at `base`
   for (int from = 0, seg = 0; from < share; ++seg) {
     const int base = from - u.tile, to = u.nt - u.tile < share - from ? base + u.nt : share;
@@ -890,11 +913,11 @@ __global__ void __launch_bounds__(32 * kW, AttnShape<NG, NT>::kCtas) kv4_attn_ke
       for (int i = 0; i < 2; ++i) kf[nt][i] = q.unit[nt][i] * a.scale_log2;
     // this warp's tiles
 #pragma unroll 1
-    for (int i = from + ((warp - from) & (kW - 1)); i < to; i += kW) {
+    for (; next < to; next += W) {
       cp_async_wait<S - 2>();
       __syncwarp();
       feed.issue();  // into the stage of the tile before this one
-      const uint32_t mask = feed.rows(u.L, i - base, stage);
+      const uint32_t mask = feed.rows(u.L, next - base, stage);
       if (mask != 0u) attend_cell<NG, NT>(ring + stage * kStage, mask, q, kf, s);
       stage = stage == S - 1 ? 0 : stage + 1;
     }
@@ -921,7 +944,7 @@ __global__ void __launch_bounds__(32 * kW, AttnShape<NG, NT>::kCtas) kv4_attn_ke
         for (int j = 0; j < 8; ++j) {
           const float z = s.z[nt][j * NG / 8][i];
           *reinterpret_cast<float2*>(row + head * Shape::kRow + 16 * j) =
-              make_float2(fmaf(s.o[nt][j][i], 0x1p24f, z), fmaf(s.o[nt][j][i + 2], 0x1p20f, z));
+              make_float2(fmaf(s.o[nt][j][i], 0x1p24f, z), fmaf(j & 1 ? s.o[nt][j][i + 2] - s.o[nt][j][i] : s.o[nt][j][i + 2], 0x1p20f, z));
         }
       }
     __syncthreads();
@@ -930,16 +953,16 @@ __global__ void __launch_bounds__(32 * kW, AttnShape<NG, NT>::kCtas) kv4_attn_ke
     float* slot = a.ws + ((size_t)blockIdx.x * 2 + (seg > 0)) * kSlotFloats;
     const int d = threadIdx.x & (kD - 1);
 #pragma unroll 1
-    for (int head = threadIdx.x / kD; head < a.G; head += 32 * kW / kD) {
-      float2 x[kW];
+    for (int head = threadIdx.x / kD; head < a.G; head += 32 * W / kD) {
+      float2 x[W];
       float m = kFloor, l = 0.f, o = 0.f;
 #pragma unroll
-      for (int w = 0; w < kW; ++w) {
+      for (int w = 0; w < W; ++w) {
         x[w] = s_ml[head][w];
         m = fmaxf(m, x[w].x);
       }
 #pragma unroll
-      for (int w = 0; w < kW; ++w) {
+      for (int w = 0; w < W; ++w) {
         const float fw = ex2(x[w].x - m);
         l = fmaf(fw, x[w].y, l);
         o = fmaf(fw, s_o[(w * HC + head) * Shape::kRow + d], o);
@@ -1026,29 +1049,30 @@ __global__ void __launch_bounds__(kD) kv4_merge_kernel(const Kv4Args a) {
 
 // ---------------------------------------------------------------------------- scores
 
-// Stages of 1.25 KB a warp and CTAs a SM.
-constexpr int kScoreStages = 6, kScoreCtas = 3;
+// Warps of a CTA, CTAs a SM, stages of 1.25 KB a warp.  (8 requests of 32K: 47 us, three CTAs of six stages 49, one of
+// 24 warps 51, of 16 warps 49.5.)
+constexpr int kScoreW = 8, kScoreCtas = 2, kScoreStages = 8;
 
 template <int NG, int NT, int AGG>
-__global__ void __launch_bounds__(32 * kW, NT == 1 ? kScoreCtas : 2) kv4_score_kernel(const Kv4Args a) {
-  constexpr int S = kScoreStages, kCell = kv4_cell(NG);
+__global__ void __launch_bounds__(32 * kScoreW, kScoreCtas) kv4_score_kernel(const Kv4Args a) {
+  constexpr int W = kScoreW, S = kScoreStages, kCell = kv4_cell(NG);
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ Cursor s_at[kW];
+  __shared__ Cursor s_at[W];
   __shared__ __align__(16) QShared<NT> s_q;
   pdl_release();
   pdl_wait();
   Cursor u;
-  const Share mine = find_share<kScore, 32 * kW>(a, &u);
+  const Share mine = find_share<kScore, W>(a, &u);
   if (mine.tiles == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = key_of(lane >> 2), t = lane & 3;
   const int share = mine.tiles;
   Cursor at = u;
   at.tile += warp;
   const uint32_t ring = smem_u32(smem) + warp * S * kCell;
-  CellFeeder<kScore, NG, false, S> feed(a, s_at[warp], nullptr, ring, at, share > warp ? (share - warp + kW - 1) / kW : 0);
+  CellFeeder<kScore, NG, false, W, S> feed(a, s_at[warp], nullptr, ring, at, share > warp ? (share - warp + W - 1) / W : 0);
 #pragma unroll 1
   for (int i = 0; i < S - 1; ++i) feed.issue();
-  int stage = 0;
+  int stage = 0, next = warp;
   for (int from = 0; from < share;) {
     const int base = from - u.tile, to = u.nt - u.tile < share - from ? base + u.nt : share;
     const Regions rg = regions_of(u.L, a.ns, a.nl);
@@ -1057,12 +1081,11 @@ __global__ void __launch_bounds__(32 * kW, NT == 1 ? kScoreCtas : 2) kv4_score_k
     float x[NT][4];
     load_queries<NT, AGG == SKV_AGG_MEAN>(a.q + unit * a.Gi * kD, a.Gi, x);
     make_queries<NG, NT, AGG == SKV_AGG_MEAN>(x, a.Gi, s_q, q);
-    int i = from + ((warp - from) & (kW - 1));
     // the keys of this lane's rows: key, and 8 on
-    int key = (rg.s_end & ~15) + (i - base) * 16 + g;
+    int key = (rg.s_end & ~15) + (next - base) * 16 + g;
     float* out = a.scores + unit * (AGG == SKV_AGG_HEAD ? a.Gi : 1) * a.max_len + key;
 #pragma unroll 1
-    for (; i < to; i += kW, key += 16 * kW, out += 16 * kW) {
+    for (; next < to; next += W, key += 16 * W, out += 16 * W) {
       cp_async_wait<S - 2>();
       __syncwarp();
       feed.issue();
@@ -1262,10 +1285,9 @@ Kv4Args kv4_args(const skv_problem& p, const void* q, const PoolView& pool, cons
   return a;
 }
 
-// CTAs for at most `units` units of `tiles` tiles: all that are resident at once, two tiles a warp (or a
-// unit's start) at least
+// CTAs for at most `units` units of `tiles` tiles
 unsigned grid_of(long long units, long long tiles, int ctas) {
-  long long n = (units * (tiles + kUnit) + 2 * kW - 1) / (2 * kW), most = (long long)num_sms() * ctas;
+  long long n = (units * (tiles + kUnit) + kLeast - 1) / kLeast, most = (long long)num_sms() * ctas;
   if (most > kMaxParts) most = kMaxParts;
   n = n < most ? n : most;
   return (unsigned)(n < 1 ? 1 : n);
@@ -1273,11 +1295,11 @@ unsigned grid_of(long long units, long long tiles, int ctas) {
 
 template <int NG, int NT, int MODE>
 skv_status launch_attn(const Kv4Args& a, long long tiles, cudaStream_t st) {
-  using Shape = AttnShape<NG, NT>;
+  using Shape = AttnShape<NG, NT, MODE>;
   const auto kernel = kv4_attn_kernel<NG, NT, MODE>;
   const skv_status prep = prepare_kernel((const void*)kernel, Shape::kSmem);
   if (prep != SKV_OK) return prep;
-  if (launch_dependent(kernel, dim3(grid_of((long long)a.B * a.H, tiles, Shape::kCtas)), dim3(32 * kW), Shape::kSmem, st, 1, a) !=
+  if (launch_dependent(kernel, dim3(grid_of((long long)a.B * a.H, tiles, Shape::kCtas)), dim3(32 * Shape::kW), Shape::kSmem, st, 1, a) !=
       cudaSuccess)
     return SKV_ERR_CUDA;
   SKV_LAUNCH_CHECK();
@@ -1293,10 +1315,10 @@ skv_status launch_scores(const Kv4Args& a, long long tiles, cudaStream_t st) {
   const bool wide = AGG != SKV_AGG_MEAN && a.Gi > 8;
   const auto kernel = kv4_score_kernel<NG, 1, AGG>;
   const auto kernel2 = kv4_score_kernel<NG, AGG == SKV_AGG_MEAN ? 1 : 2, AGG>;
-  constexpr int kSmem = kW * kScoreStages * kv4_cell(NG);
+  constexpr int kSmem = kScoreW * kScoreStages * kv4_cell(NG);
   const skv_status prep = prepare_kernel((const void*)(wide ? kernel2 : kernel), kSmem);
   if (prep != SKV_OK) return prep;
-  if (launch_dependent(wide ? kernel2 : kernel, dim3(grid_of((long long)a.B * a.H, tiles, wide ? 2 : kScoreCtas)), dim3(32 * kW), kSmem, st, 1, a) != cudaSuccess)
+  if (launch_dependent(wide ? kernel2 : kernel, dim3(grid_of((long long)a.B * a.H, tiles, kScoreCtas)), dim3(32 * kScoreW), kSmem, st, 1, a) != cudaSuccess)
     return SKV_ERR_CUDA;
   SKV_LAUNCH_CHECK();
   return SKV_OK;
