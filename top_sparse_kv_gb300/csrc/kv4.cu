@@ -100,16 +100,19 @@ struct Share {
   int ctas, tiles;   // CTAs that have a share; this one's tiles
 };
 
-// Every thread of the CTA gets the walk's length and the place where this CTA's share starts.
+// Every thread of the CTA gets the walk's length and the place where this CTA's share starts.  Either half
+// of the threads sums the requests up, and the thread of each whose requests hold an end of the
+// share finds the unit there (one after the other, the two ends take a microsecond).
 template <int MODE, int W>
 __device__ __forceinline__ Share find_share(const Kv4Args& a, Cursor* c) {
+  constexpr int kHalf = 16 * W;
   __shared__ long long s_sum[2][W], s_tiles[2], s_place;
-  __shared__ int s_at[3];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per = (a.B + 32 * W - 1) / (32 * W), b0 = threadIdx.x * per, b1 = b0 + per < a.B ? b0 + per : a.B;
+  __shared__ Cursor s_at;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, end = threadIdx.x >= kHalf ? 1 : 0;
+  const int per = (a.B + kHalf - 1) / kHalf, b0 = (threadIdx.x - end * kHalf) * per, b1 = b0 + per < a.B ? b0 + per : a.B;
   long long tiles = 0, units = 0;
   for (int b = b0; b < b1; ++b) {
-    const int L = blockIdx.x == 0 ? load_len(a.seq_lens, b, a.max_len, a.status) : len_of(a, b);
+    const int L = blockIdx.x == 0 && end == 0 ? load_len(a.seq_lens, b, a.max_len, a.status) : len_of(a, b);
     const int nt = tiles_of<MODE>(a, L);
     tiles += nt;
     units += nt > 0;
@@ -121,14 +124,14 @@ __device__ __forceinline__ Share find_share(const Kv4Args& a, Cursor* c) {
     if (lane >= off) x += p, y += q;
   }
   if (lane == 31) s_sum[0][warp] = x, s_sum[1][warp] = y;
-  if (threadIdx.x == 0) s_at[0] = -1, s_tiles[0] = s_tiles[1] = 0;
+  if (threadIdx.x == 0) s_tiles[0] = s_tiles[1] = 0;
   __syncthreads();
   long long all = 0, all_units = 0;
   x -= tiles;
   y -= units;
-  const int warps = a.B < 32 * W ? (a.B + 31) >> 5 : W;  // that have a request
+  const int first = end * (W / 2), warps = a.B < kHalf ? (a.B + 31) >> 5 : W / 2;  // that have a request
 #pragma unroll 1
-  for (int w = 0; w < warps; ++w) {
+  for (int w = first; w < first + warps; ++w) {
     if (w == warp) x += all, y += all_units;
     all += s_sum[0][w];
     all_units += s_sum[1][w];
@@ -141,21 +144,21 @@ __device__ __forceinline__ Share find_share(const Kv4Args& a, Cursor* c) {
   // the tiles before a share's ends: one thread's requests hold each
   const long long before = (x + kUnit * y) * a.H, after = before + (tiles + kUnit * units) * a.H;
   if (blockIdx.x < n) {
-#pragma unroll 1
-    for (int end = 0; end < 2; ++end) {
-      const long long at = share(r.weight, (int)n, blockIdx.x + end);
-      if (end == 1 && at == r.weight && threadIdx.x == 0) s_tiles[1] = all * a.H;
-      if (at < before || at >= after) continue;
+    const long long at = share(r.weight, (int)n, blockIdx.x + end);
+    if (at == r.weight && threadIdx.x == kHalf) s_tiles[1] = all * a.H;
+    if (at >= before && at < after) {
       long long off = at - before, t = x * a.H;
       for (int b = b0; b < b1; ++b) {
-        const int nt = tiles_of<MODE>(a, len_of(a, b)), w = nt > 0 ? nt + kUnit : 0;
+        const int L = len_of(a, b), nt = tiles_of<MODE>(a, L), w = nt > 0 ? nt + kUnit : 0;
         if (off < (long long)w * a.H) {
           const int h = (int)quotient(off, w), in = (int)(off - (long long)h * w), tile = in > kUnit ? in - kUnit : 0;
           s_tiles[end] = t + (long long)h * nt + tile;
           if (end == 0) {
-            s_at[0] = b;
-            s_at[1] = h;
-            s_at[2] = tile;
+            s_at.b = b;
+            s_at.h = h;
+            s_at.tile = tile;
+            s_at.nt = nt;
+            s_at.L = L;
             s_place = at - in;
           }
           break;
@@ -168,13 +171,7 @@ __device__ __forceinline__ Share find_share(const Kv4Args& a, Cursor* c) {
   __syncthreads();
   r.tiles = (int)(s_tiles[1] - s_tiles[0]);  // (a share has fewer tiles than 2^31)
   r.place = s_place;
-  c->b = s_at[0];
-  if (c->b >= 0) {
-    c->h = s_at[1];
-    c->tile = s_at[2];
-    c->L = len_of(a, c->b);
-    c->nt = tiles_of<MODE>(a, c->L);
-  }
+  *c = s_at;
   return r;
 }
 
@@ -529,13 +526,20 @@ __device__ __forceinline__ void load_queries(const __nv_bfloat16* q, int n, floa
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[nt][i] = 0.f;
     const int head = 8 * nt + g;
+    constexpr int kTogether = MEAN ? 4 : 1;  // loads on their way
 #pragma unroll 1
-    for (int h = MEAN ? 0 : head; h < n && warp < 8; ++h) {
-      const uint2 u = *reinterpret_cast<const uint2*>(q + (size_t)h * kD + 16 * warp + 4 * t);
-      x[nt][0] += __uint_as_float(u.x << 16);
-      x[nt][1] += __uint_as_float(u.x & 0xffff0000u);
-      x[nt][2] += __uint_as_float(u.y << 16);
-      x[nt][3] += __uint_as_float(u.y & 0xffff0000u);
+    for (int h = MEAN ? 0 : head; h < n && warp < 8; h += kTogether) {
+      uint2 u[kTogether];
+#pragma unroll
+      for (int k = 0; k < kTogether; ++k)
+        u[k] = h + k < n ? *reinterpret_cast<const uint2*>(q + (size_t)(h + k) * kD + 16 * warp + 4 * t) : make_uint2(0u, 0u);
+#pragma unroll
+      for (int k = 0; k < kTogether; ++k) {
+        x[nt][0] += __uint_as_float(u[k].x << 16);
+        x[nt][1] += __uint_as_float(u[k].x & 0xffff0000u);
+        x[nt][2] += __uint_as_float(u[k].y << 16);
+        x[nt][3] += __uint_as_float(u[k].y & 0xffff0000u);
+      }
       if (!MEAN) break;
     }
   }
@@ -1049,9 +1053,8 @@ __global__ void __launch_bounds__(kD) kv4_merge_kernel(const Kv4Args a) {
 
 // ---------------------------------------------------------------------------- scores
 
-// Warps of a CTA, CTAs a SM, stages of 1.25 KB a warp.  (8 requests of 32K: 47 us, three CTAs of six stages 49, one of
-// 24 warps 51, of 16 warps 49.5.)
-constexpr int kScoreW = 8, kScoreCtas = 2, kScoreStages = 8;
+// Warps of a CTA, CTAs a SM, stages of 1.25 KB a warp.  (8 requests of 32K: 41 us; three CTAs: 45.)
+constexpr int kScoreW = 8, kScoreCtas = 2, kScoreStages = 6;
 
 template <int NG, int NT, int AGG>
 __global__ void __launch_bounds__(32 * kScoreW, kScoreCtas) kv4_score_kernel(const Kv4Args a) {
@@ -1069,6 +1072,9 @@ __global__ void __launch_bounds__(32 * kScoreW, kScoreCtas) kv4_score_kernel(con
   Cursor at = u;
   at.tile += warp;
   const uint32_t ring = smem_u32(smem) + warp * S * kCell;
+  auto queries = [&]() { return a.q + ((size_t)u.b * a.H + u.h) * a.Gi * kD; };
+  float x[NT][4];
+  load_queries<NT, AGG == SKV_AGG_MEAN>(queries(), a.Gi, x);
   CellFeeder<kScore, NG, false, W, S> feed(a, s_at[warp], nullptr, ring, at, share > warp ? (share - warp + W - 1) / W : 0);
 #pragma unroll 1
   for (int i = 0; i < S - 1; ++i) feed.issue();
@@ -1078,8 +1084,7 @@ __global__ void __launch_bounds__(32 * kScoreW, kScoreCtas) kv4_score_kernel(con
     const Regions rg = regions_of(u.L, a.ns, a.nl);
     const size_t unit = (size_t)u.b * a.H + u.h;
     QFrag<NT> q;
-    float x[NT][4];
-    load_queries<NT, AGG == SKV_AGG_MEAN>(a.q + unit * a.Gi * kD, a.Gi, x);
+    if (from > 0) load_queries<NT, AGG == SKV_AGG_MEAN>(queries(), a.Gi, x);
     make_queries<NG, NT, AGG == SKV_AGG_MEAN>(x, a.Gi, s_q, q);
     // the keys of this lane's rows: key, and 8 on
     int key = (rg.s_end & ~15) + (next - base) * 16 + g;
