@@ -181,12 +181,26 @@ __device__ __forceinline__ Share find_share(const Kv4Args& a, Cursor* c) {
 // ring of its own: a stage is the cell of K, then the cell of V, as they lie in the pool.
 // (A warp that feeds the others leaves them 96 registers of 128: the products spill.)
 
-template <int BYTES>
-__device__ __forceinline__ void cp_async_ca(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
-}
 __device__ __forceinline__ void cp_async_cg16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Rows lie alone: of a line of 128 bytes, which L2 fetches otherwise, the half with the row (3,409 rows of
+// 32K in lists, gathered: 91 -> 52 MB read of HBM).
+template <int BYTES>
+__device__ __forceinline__ void cp_async_row(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global.L2::64B [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+template <int WORDS>
+__device__ __forceinline__ void load_row(const void* src, uint32_t* w) {
+  if constexpr (WORDS == 4)
+    asm("ld.global.nc.L2::64B.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(src));
+  else if constexpr (WORDS == 2)
+    asm("ld.global.nc.L2::64B.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(src));
+  else
+    asm("ld.global.nc.L2::64B.u32 %0, [%1];" : "=r"(w[0]) : "l"(src));
 }
 
 // A lane's row on its way from its place in a list to its number.
@@ -397,18 +411,15 @@ struct RowFeeder {
       const uint32_t r = __shfl_sync(0xffffffffu, row, (lane >> 2) + 8 * j + 16 * half);
       if (r != kNoRow) {
         const int off = (int)(r & 15u) * kCodeBytes + (lane & 3) * 16;
-        cp_async_cg16(to + lane * 16 + 512 * j, at(r, false) + off);
-        cp_async_cg16(to + kCell + lane * 16 + 512 * j, at(r, true) + off);
+        cp_async_row<16>(to + lane * 16 + 512 * j, at(r, false) + off);
+        cp_async_row<16>(to + kCell + lane * 16 + 512 * j, at(r, true) + off);
       }
     }
     const uint32_t r = __shfl_sync(0xffffffffu, row, (lane & 15) + 16 * half);
     if (r != kNoRow) {  // K's words, V's
       const uint32_t dst = to + (lane >> 4) * kCell + 16 * kCodeBytes + (lane & 15) * 4 * NG;
       const unsigned char* src = at(r, lane >= 16) + 16 * kCodeBytes + (r & 15u) * 4 * NG;
-      if (NG == 4)
-        cp_async_cg16(dst, src);
-      else
-        cp_async_ca<4 * NG>(dst, src);
+      cp_async_row<4 * NG>(dst, src);
     }
     cp_async_commit();
     half = half == 0 ? 1 : 0;
@@ -1192,27 +1203,18 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4Args a, T* k_o
     const bool host = at >> 31;
     const size_t cell = (size_t)(at >> 4 & 0x7ffffffu) * kv4_cell(NG);
     const int rc = (int)(at & 15u);
-    uint4 codes[2];
-    uint32_t words[2][NG];
+    uint32_t codes[2][4], words[2][NG];
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {  // both sides' loads together
-      codes[kv] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) codes[kv][i] = 0u;
 #pragma unroll
       for (int i = 0; i < NG; ++i) words[kv][i] = 0u;
       if (at != kNoRow && (kv ? v_out : k_out) != nullptr) {
         const unsigned char* src =
             (const unsigned char*)(kv ? (host ? a.pool.host_v : a.pool.gpu_v) : (host ? a.pool.host_k : a.pool.gpu_k)) + cell;
-        codes[kv] = __ldg(reinterpret_cast<const uint4*>(src + rc * kCodeBytes) + t);
-        const unsigned char* w = src + 16 * kCodeBytes + rc * 4 * NG;
-        if constexpr (NG == 4) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(w));
-          words[kv][0] = x.x, words[kv][1] = x.y, words[kv][2] = x.z, words[kv][3] = x.w;
-        } else if constexpr (NG == 2) {
-          const uint2 x = __ldg(reinterpret_cast<const uint2*>(w));
-          words[kv][0] = x.x, words[kv][1] = x.y;
-        } else {
-          words[kv][0] = __ldg(reinterpret_cast<const uint32_t*>(w));
-        }
+        load_row<4>(src + rc * kCodeBytes + t * 16, codes[kv]);
+        load_row<NG>(src + 16 * kCodeBytes + rc * 4 * NG, words[kv]);
       }
     }
     w0 = w1;
@@ -1222,10 +1224,9 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4Args a, T* k_o
     for (int kv = 0; kv < 2; ++kv) {
       T* out = kv ? v_out : k_out;
       if (out == nullptr) continue;
-      const uint4 u = codes[kv];
 #pragma unroll
       for (int i = 0; i < 8; i += 4) {  // spans i .. i + 3
-        const uint32_t b0 = i ? u.y : u.x, b1 = i ? u.w : u.z;  // their bytes: entries 4 t, + 1; + 2, + 3
+        const uint32_t b0 = codes[kv][i / 4], b1 = codes[kv][i / 4 + 2];  // their bytes: entries 4 t, + 1; + 2, + 3
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
