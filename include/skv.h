@@ -834,7 +834,10 @@ skv_status skv_gather_kv4(const skv_problem *p, const skv_kv_pool *pool, int32_t
 
 /* skv_score from 4 bits: scores[b][h][t] = <q_bar, k^_t> in fp32 of the candidates, every
  * group_agg, rows and untouched positions as for skv_score.  p->dtype is bf16, q_score
- * [batch, n_idx_q_heads, 128], at most 16 scoring heads a KV head.  A key whose entry lies outside its pool scores NaN. */
+ * [batch, n_idx_q_heads, 128]; SKV_AGG_MAX and SKV_AGG_HEAD: at most 16 scoring heads a KV
+ * head.  A key whose entry lies outside its pool scores NaN.  Here and in the attention a query
+ * head's results are of its own entries alone; one that is infinite or NaN makes them NaN,
+ * and entries from 2^117 up count as infinite where their logits leave fp32. */
 skv_status skv_score_kv4(const skv_problem *p, const void *q_score, const skv_kv_pool *pool, int32_t group,
                          float *scores, int32_t *dev_status, void *stream);
 

@@ -380,6 +380,38 @@ def test_hard_values(skv, kind):
     c.check(out, lse)
 
 
+def test_small_scale(skv):
+    """Zero queries under a scale that takes their logits' unit out of fp32: equal weights, masked rows none."""
+    c = Case(skv, [23, 300], 2, 4, k=5, ns=4, nl=9, sm_scale=1e-30)
+    c.q[:, ::3] = 0
+    c.check(*c.step.attend_all(c.q.cuda()))
+    idx = torch.tensor([[4, 9, 13, -1, -1], [5, 100, 17, 250, -1]], dtype=torch.int32).unsqueeze(1).repeat(1, 2, 1)
+    c.check(*c.step.attend(c.q.cuda(), idx.contiguous().cuda()),
+            lambda b, r: kv4_ref.attended(c.lens[b], 4, 9, [t for t in idx[b, r].tolist() if t >= 0]))
+    assert int(c.step.status.item()) == 0
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_query_that_is_no_number(skv, bad):
+    """A query head with such an entry: NaN, and the other heads as without it."""
+    c = Case(skv, [77, 1000], 2, 4, agg=2)
+    want, lse = (x.clone() for x in c.step.attend_all(c.q.cuda()))
+    c.q[0, 1, 40] = bad
+    c.q[1, 6, 127] = bad
+    out, l = c.step.attend_all(c.q.cuda())
+    hit = torch.zeros(2, 8, dtype=torch.bool, device="cuda")
+    hit[0, 1] = hit[1, 6] = True
+    assert out[hit].isnan().all() and l[hit].isnan().all()
+    assert torch.equal(out[~hit], want[~hit]) and torch.equal(l[~hit], lse[~hit])
+    for agg in (0, 1, 2):
+        p = skv.Problem(**{**vars(c.p), "group_agg": agg})
+        scores = torch.zeros((2, 8 if agg == 2 else 2, c.max_len), device="cuda")
+        skv.skv_score_kv4(p, c.q.cuda(), c.pool, scores)
+        rows = hit if agg == 2 else hit.view(2, 2, 4).any(-1)
+        for b, L in enumerate(c.lens):
+            assert scores[b, rows[b], :L].isnan().all() and scores[b, ~rows[b], :L].isfinite().all()
+
+
 def test_far_blocks(skv):
     """Blocks past 4 GB of the pool."""
     H, bs = 8, 16

@@ -925,7 +925,7 @@ __global__ void __launch_bounds__(32 * AttnShape<NG, NT, MODE>::kW, AttnShape<NG
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) kf[nt][i] = q.unit[nt][i] * a.scale_log2;
+      for (int i = 0; i < 2; ++i) kf[nt][i] = fmaxf(q.unit[nt][i] * a.scale_log2, 0x1p-126f);  // (0 times a masked logit is no number)
     // this warp's tiles
 #pragma unroll 1
     for (; next < to; next += W) {
