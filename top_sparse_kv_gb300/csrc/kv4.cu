@@ -204,57 +204,58 @@ __device__ __forceinline__ void load_row(const void* src, uint32_t* w) {
 }
 
 // A lane's row on its way from its place in a list to its number.
-struct Row {
-  int t;            // position, as found (a selected one unchecked); -1: none
-  int e, block;     // its table entry, that one's index
-  int b, h, L;
-  bool listed;      // from the selection: to be checked
+struct Position {
+  int t, lo, hi;   // as found, -1: none; where it has to lie
+  uint32_t table;  // its row of the table
+  int h;           // the pool's head
+};
+struct Entry {
+  int e, off;  // its table entry; in the block, -1: none
+  int h;
 };
 
-__device__ __forceinline__ void row_position(const Kv4Args& a, const Cursor& c, bool on, int r, Row& w) {
-  w.b = c.b;
-  w.h = c.h;
-  w.L = c.L;
+// of the j-th place of a unit's list
+__device__ __forceinline__ void row_position(const Kv4Args& a, const Cursor& c, bool on, int j, Position& w) {
   w.t = -1;
-  w.listed = false;
   if (!on) return;
-  const int j = (c.tile << 4) + r;
   const Regions g = regions_of(c.L, a.ns, a.nl);
+  w.h = a.pool.hdiv == 1 ? c.h : c.h / a.pool.hdiv;
+  w.table = a.pool.per_head ? (uint32_t)c.b * a.heads + w.h : c.b;
+  w.lo = 0;
+  w.hi = c.L;
   if (j < g.s_end) {
     w.t = j;
   } else if (j < g.s_end + a.k) {
     w.t = __ldg(a.idx + ((size_t)c.b * a.H + c.h) * a.k + (j - g.s_end));
-    w.listed = true;
+    w.lo = g.s_end;
+    w.hi = g.l_start;
   } else {
     const int t = g.l_start + (j - g.s_end - a.k);
     w.t = t < c.L ? t : -1;
   }
 }
 
-__device__ __forceinline__ void row_entry(const Kv4Args& a, bool reports, Row& w) {
-  if (w.listed && w.t >= 0) {
-    const Regions g = regions_of(w.L, a.ns, a.nl);
-    if (w.t < g.s_end || w.t >= g.l_start) {
-      if (reports) flag(a.status, SKV_DEV_BAD_INDEX);
-      w.t = -1;
-    }
+__device__ __forceinline__ void row_entry(const Kv4Args& a, bool reports, const Position& p, Entry& w) {
+  w.off = -1;
+  if (p.t < 0) return;
+  if (p.t < p.lo || p.t >= p.hi) {
+    if (reports) flag(a.status, SKV_DEV_BAD_INDEX);
+    return;
   }
-  w.e = 0;
-  if (w.t >= 0) {
-    w.block = a.shift >= 0 ? w.t >> a.shift : w.t / a.bs;
-    w.e = __ldg(table_row(a.pool, w.b, a.pool.hdiv == 1 ? w.h : w.h / a.pool.hdiv, a.heads) + w.block);
-  }
+  const int block = a.shift >= 0 ? p.t >> a.shift : p.t / a.bs;
+  w.off = p.t - block * a.bs;
+  w.h = p.h;
+  w.e = __ldg(a.pool.table + (size_t)p.table * a.pool.stride + block);
 }
 
 // The row's number in its pool, bit 31: the host's (pools have fewer than 2^31 rows).
 constexpr uint32_t kNoRow = 0xffffffffu;
-__device__ __forceinline__ uint32_t row_id(const Kv4Args& a, bool reports, const Row& w) {
-  if (w.t < 0) return kNoRow;
-  const uint32_t ph = a.pool.hdiv == 1 ? w.h : w.h / a.pool.hdiv, off = w.t - w.block * a.bs;
+__device__ __forceinline__ uint32_t row_id(const Kv4Args& a, bool reports, const Entry& w) {
+  if (w.off < 0) return kNoRow;
   if (w.e >= 0) {
-    if ((uint32_t)w.e < a.n_gpu) return (a.pool.per_head ? w.e : w.e * a.heads + ph) * a.bs + off;
+    if ((uint32_t)w.e < a.n_gpu) return (a.pool.per_head ? w.e : w.e * a.heads + w.h) * a.bs + w.off;
   } else if (~(uint32_t)w.e < a.n_host) {
-    return ((~(uint32_t)w.e * a.heads + ph) * a.bs + off) | 0x80000000u;
+    return ((~(uint32_t)w.e * a.heads + w.h) * a.bs + w.off) | 0x80000000u;
   }
   if (reports) flag(a.status, SKV_DEV_BAD_SLOT);
   return kNoRow;
@@ -376,24 +377,24 @@ struct RowFeeder {
   Cursor c;  // this half warp's next tile
   int left, half;
   uint32_t row;  // this lane's, of the tiles that are issued; then: position on its way, entry on its way
-  Row r1, r0;
+  Position position;
+  Entry entry;
 
   __device__ __forceinline__ RowFeeder(const Kv4Args& args, Cursor&, uint32_t* masks_, uint32_t ring_, Cursor at, int n)
       : a(args), masks(masks_), to(ring_), end(ring_ + S * kStage), c(at), left(n), half(-2), row(kNoRow) {
     c.tile += (threadIdx.x >> 4 & 1) * W;
     left -= threadIdx.x >> 4 & 1;
-    r0.t = r1.t = -1;
+    position.t = entry.off = -1;
   }
   __device__ __forceinline__ void issue() {
     const int lane = threadIdx.x & 31;
     if (half <= 0) {  // (at the start: three times)
 #pragma unroll 1
       for (; half <= 0; ++half) {
-        row = row_id(a, true, r0);
-        r0 = r1;
-        row_entry(a, true, r0);
+        row = row_id(a, true, entry);
+        row_entry(a, true, position, entry);
         if (left > 0 && c.tile >= c.nt) settle<kList>(a, c);
-        row_position(a, c, left > 0, lane & 15, r1);
+        row_position(a, c, left > 0, (c.tile << 4) + (lane & 15), position);
         left -= 2;
         c.tile += 2 * W;
       }
@@ -1176,12 +1177,12 @@ __device__ __forceinline__ void values_of(uint32_t codes, uint32_t word01, uint3
 // Four lanes a row: 16 bytes of codes each, four consecutive entries of every 16.  Finding a row is a
 // step a round: its place's position, that one's entry, the row.
 template <int NG, typename T>
-__global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4Args a, T* k_out, T* v_out, int n_att) {
+__global__ void __launch_bounds__(256, 5) kv4_gather_kernel(const Kv4Args a, T* k_out, T* v_out, int n_att) {
   pdl_release();
   pdl_wait();
   const int lane = threadIdx.x & 31, t = lane & 3;
   const long long rows = (long long)a.B * a.H * n_att, stride = (long long)gridDim.x * 64;
-  auto position = [&](long long r, Row& w) {
+  auto find = [&](long long r, Position& w) {
     w.t = -1;
     if (r >= rows) return;
     const long long unit = quotient(r, n_att);
@@ -1189,17 +1190,17 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4Args a, T* k_o
     Cursor c;
     c.b = (int)quotient(unit, a.H);
     c.h = (int)(unit - (long long)c.b * a.H);
-    c.tile = j >> 4;
     c.L = t == 0 && j == 0 && c.h == 0 ? load_len(a.seq_lens, c.b, a.max_len, a.status) : len_of(a, c.b);
-    row_position(a, c, true, j & 15, w);
+    row_position(a, c, true, j, w);
   };
   const long long r0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * 8 + (lane >> 2);
-  Row w0, w1;
-  position(r0, w0);
-  row_entry(a, t == 0, w0);
-  position(r0 + stride, w1);
+  Position position;
+  Entry entry;
+  find(r0, position);
+  row_entry(a, t == 0, position, entry);
+  find(r0 + stride, position);
   for (long long r = r0; r - (lane >> 2) < rows; r += stride) {  // (a warp's lanes together)
-    const uint32_t at = row_id(a, t == 0, w0);
+    const uint32_t at = row_id(a, t == 0, entry);
     const bool host = at >> 31;
     const size_t cell = (size_t)(at >> 4 & 0x7ffffffu) * kv4_cell(NG);
     const int rc = (int)(at & 15u);
@@ -1217,9 +1218,8 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4Args a, T* k_o
         load_row<NG>(src + 16 * kCodeBytes + rc * 4 * NG, words[kv]);
       }
     }
-    w0 = w1;
-    row_entry(a, t == 0, w0);
-    position(r + 2 * stride, w1);
+    row_entry(a, t == 0, position, entry);
+    find(r + 2 * stride, position);
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
       T* out = kv ? v_out : k_out;
