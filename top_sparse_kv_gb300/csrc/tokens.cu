@@ -122,9 +122,9 @@ __device__ __forceinline__ void pool_rows(const TokenArgs& a, const Token& t, in
     flag(a.status, SKV_DEV_BAD_SLOT);
     return;
   }
-  const size_t at = NG ? row / kCellTokens * kv4_cell(NG) : row * a.d * elem;
-  *k = (unsigned char*)(gpu ? a.pool.gpu_k : a.pool.host_k) + at;
-  if (a.v) *v = (unsigned char*)(gpu ? a.pool.gpu_v : a.pool.host_v) + (NG ? at : row * a.dv * elem);
+  *k = (unsigned char*)(gpu ? a.pool.gpu_k : a.pool.host_k) + (NG ? row / kCellTokens * kv4_cell(NG) : row * a.d * elem);
+  if (a.v)
+    *v = (unsigned char*)(gpu ? a.pool.gpu_v : a.pool.host_v) + (NG ? row / kCellTokens * kv4_cell(NG) : row * a.dv * elem);
 }
 
 // Where row r of the token (queries, keys, values in order) comes from and goes to (null: nowhere).
@@ -438,9 +438,11 @@ __global__ void __launch_bounds__(32 * kRowWarps<LPR> + 32, kTokCtas<LPR>) token
           }
           unsigned char* dst = q_to;
           if (k) dst = on ? row_to<ELEM, NG>(a, f.t, f.tok, r, nq, nk) : nullptr;
-          if (NG > 0 && k)
-            put_row4<VE, LPR, NG ? NG : 1>(o, dst, f.t.pos % kCellTokens, sub);
-          else if (on && dst != nullptr) *reinterpret_cast<uint4*>(dst + e0 * ELEM) = narrow<T>(o);
+          if constexpr (NG > 0) {
+            if (k) put_row4<VE, LPR, NG>(o, dst, f.t.pos % kCellTokens, sub);
+            if (k) dst = nullptr;
+          }
+          if (on && dst != nullptr) *reinterpret_cast<uint4*>(dst + e0 * ELEM) = narrow<T>(o);
           src += W * RPW * rowb;
           q_to += W * RPW * rowb;
         }
