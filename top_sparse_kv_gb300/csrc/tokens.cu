@@ -122,9 +122,14 @@ __device__ __forceinline__ void pool_rows(const TokenArgs& a, const Token& t, in
     flag(a.status, SKV_DEV_BAD_SLOT);
     return;
   }
-  *k = (unsigned char*)(gpu ? a.pool.gpu_k : a.pool.host_k) + (NG ? row / kCellTokens * kv4_cell(NG) : row * a.d * elem);
-  if (a.v)
-    *v = (unsigned char*)(gpu ? a.pool.gpu_v : a.pool.host_v) + (NG ? row / kCellTokens * kv4_cell(NG) : row * a.dv * elem);
+  if constexpr (NG > 0) {
+    const size_t at = row / kCellTokens * kv4_cell(NG);
+    *k = (unsigned char*)(gpu ? a.pool.gpu_k : a.pool.host_k) + at;
+    if (a.v) *v = (unsigned char*)(gpu ? a.pool.gpu_v : a.pool.host_v) + at;
+  } else {
+    *k = (unsigned char*)(gpu ? a.pool.gpu_k : a.pool.host_k) + row * a.d * elem;
+    if (a.v) *v = (unsigned char*)(gpu ? a.pool.gpu_v : a.pool.host_v) + row * a.dv * elem;
+  }
 }
 
 // Where row r of the token (queries, keys, values in order) comes from and goes to (null: nowhere).
@@ -439,10 +444,13 @@ __global__ void __launch_bounds__(32 * kRowWarps<LPR> + 32, kTokCtas<LPR>) token
           unsigned char* dst = q_to;
           if (k) dst = on ? row_to<ELEM, NG>(a, f.t, f.tok, r, nq, nk) : nullptr;
           if constexpr (NG > 0) {
-            if (k) put_row4<VE, LPR, NG>(o, dst, f.t.pos % kCellTokens, sub);
-            if (k) dst = nullptr;
+            if (k)
+              put_row4<VE, LPR, NG>(o, dst, f.t.pos % kCellTokens, sub);
+            else if (on && dst != nullptr)
+              *reinterpret_cast<uint4*>(dst + e0 * ELEM) = narrow<T>(o);
+          } else {
+            if (on && dst != nullptr) *reinterpret_cast<uint4*>(dst + e0 * ELEM) = narrow<T>(o);
           }
-          if (on && dst != nullptr) *reinterpret_cast<uint4*>(dst + e0 * ELEM) = narrow<T>(o);
           src += W * RPW * rowb;
           q_to += W * RPW * rowb;
         }
