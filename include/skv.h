@@ -817,8 +817,8 @@ skv_status skv_update_tables(const skv_tables *t, const int32_t *n_new, int32_t 
  *
  * d_qk = d_v = d_idx = 128, K and V pools (no latent layout), at most 16 query heads a KV
  * head, block_size a multiple of 16, max_len at most 2^30, each pool under 2^31 rows, else
- * SKV_ERR_UNSUPPORTED; a group other than the three is SKV_ERR_INVALID_ARGUMENT.  Slot caches, prefetch, block summaries and ParisKV
- * do not take these pools.
+ * SKV_ERR_UNSUPPORTED; a group other than the three is SKV_ERR_INVALID_ARGUMENT.  Slot caches,
+ * prefetch, block summaries and ParisKV do not take these pools.
  * ------------------------------------------------------------------------------------ */
 
 /* skv_append_kv into 4 bits: K rows normed and rotated, V rows as they are, both in fp32

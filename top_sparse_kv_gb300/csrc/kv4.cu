@@ -706,7 +706,9 @@ template <int NG, int NT>
 struct State {
   float l[NT][2], ref[NT][2];
   float top[NT][2];   // the logit, in its column's unit, past which the maximum moves
-  float o[NT][8][4];  // rows 2 g (2^-24 a unit) and 2 g + 1 (2^-20; i odd: both, 2^-24) of entries 16 i, columns heads 2 t, 2 t + 1
+  // rows 2 g (2^-24 a unit) and 2 g + 1 (2^-20; i odd: 16 of it and the other, 2^-24) of entries
+  // 16 i, columns heads 2 t, 2 t + 1
+  float o[NT][8][4];
   float z[NT][NG][2];
   int sigma;          // steps are below 2^(sigma + 1)
 };
@@ -861,12 +863,12 @@ __device__ __forceinline__ void attend_cell(uint32_t cell, uint32_t mask, const 
 
 template <int NG, int NT, int MODE>
 struct AttnShape {
-  // Warps of a CTA, CTAs a SM, stages of 2.5 KB a warp.  A CTA a SM: of two the schedulers serve the one that came first first,
-  // it ends at 80 % of the time and leaves the SM half empty (a million keys, 8 warps in either: 231 us; 12 or
-  // 16 warps in one: 215, 8: 258), and 12 warps are no slower than 16 while the products keep 168
-  // registers (8 requests of 32K: 78 us against 81).  A list's rows arrive late rather, and two CTAs
-  // hide more of that (8 requests' 3,409 rows of 32K: 26.8 us, one of 12 or 16 warps 28.8).  Two column tiles take all
-  // the registers of 8 warps.
+  // Warps of a CTA, CTAs a SM, stages of 2.5 KB a warp.  One CTA a SM: of two, the schedulers serve the
+  // one that came first before the other, it ends at 80 % of the time and leaves the SM half empty
+  // (a million keys, 8 warps in either: 231 us; 12 or 16 warps in one 215, 8 warps 258); 12 warps are
+  // no slower than 16, and the products keep 168 registers (8 requests of 32K: 78 us against 81).
+  // A list's rows arrive late rather, and two CTAs hide more of that (3,409 rows of 32K for 8
+  // requests: 26.8 us, one CTA 28.8).  Two column tiles take all the registers of 8 warps.
   static constexpr int kCtas = NT == 1 && MODE == kList ? 2 : 1;
   static constexpr int kW = NT == 1 && MODE == kDense ? 12 : 8, kStages = NT == 2 ? 6 : MODE == kDense ? 5 : 3;
   static constexpr int kRing = kW * kStages * 2 * kv4_cell(NG);
@@ -884,6 +886,14 @@ struct Pick<kList, NG, W, S> {
   using type = RowFeeder<NG, W, S>;
 };
 
+// Persistent CTAs, a share each of the tiles of all units; a warp computes its own tiles.  Measured
+// (8 KV heads): 8 requests of 32K keys in groups of 32, 8 query heads each, 336 MB, 74 us (4.5 TB/s); a
+// million keys in groups of 128, 4 query heads, 1,141 MB, 203 us (5.6 TB/s); lists of 3,409 rows of 32K
+// for the 8 requests, 52 MB read, 23 us; 4 requests to 777 keys 10.7 us a call.  The instructions of
+// a tile bound it: 350 in groups of 32, 146 of them masks, permutations and shifts at half the
+// issue rate, and 18 products; on cells from L2 alone the first of these takes 2 us less, with
+// the copies alone 60 (a million keys: 178).  4 us pass before the first product: lengths, the
+// share's ends, table, cells.
 template <int NG, int NT, int MODE>
 __global__ void __launch_bounds__(32 * AttnShape<NG, NT, MODE>::kW, AttnShape<NG, NT, MODE>::kCtas) kv4_attn_kernel(const Kv4Args a) {
   using Shape = AttnShape<NG, NT, MODE>;
@@ -926,7 +936,7 @@ __global__ void __launch_bounds__(32 * AttnShape<NG, NT, MODE>::kW, AttnShape<NG
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) kf[nt][i] = fmaxf(q.unit[nt][i] * a.scale_log2, 0x1p-126f);  // (0 times a masked logit is no number)
+      for (int i = 0; i < 2; ++i) kf[nt][i] = fmaxf(q.unit[nt][i] * a.scale_log2, 0x1p-126f);  // (0 times -inf: NaN)
     // this warp's tiles
 #pragma unroll 1
     for (; next < to; next += W) {
@@ -958,9 +968,9 @@ __global__ void __launch_bounds__(32 * AttnShape<NG, NT, MODE>::kW, AttnShape<NG
         if (g == 0) s_ml[head][warp] = make_float2(-s.ref[nt][i], s.l[nt][i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float z = s.z[nt][j * NG / 8][i];
+          const float z = s.z[nt][j * NG / 8][i], lo = s.o[nt][j][i], hi = s.o[nt][j][i + 2];
           *reinterpret_cast<float2*>(row + head * Shape::kRow + 16 * j) =
-              make_float2(fmaf(s.o[nt][j][i], 0x1p24f, z), fmaf(j & 1 ? s.o[nt][j][i + 2] - s.o[nt][j][i] : s.o[nt][j][i + 2], 0x1p20f, z));
+              make_float2(fmaf(lo, 0x1p24f, z), fmaf(j & 1 ? hi - lo : hi, 0x1p20f, z));
         }
       }
     __syncthreads();
@@ -1004,7 +1014,9 @@ __global__ void __launch_bounds__(32 * AttnShape<NG, NT, MODE>::kW, AttnShape<NG
   }
 }
 
-// The units that no CTA held alone: their partials joined, a CTA a head; the empty ones: zeros.
+// The units that no CTA held alone: their partials joined, a CTA a head; the empty ones: zeros.  A launch and two
+// loads' latency, 2 us behind the attention's last CTA (by the last CTA to finish, it would need counters that
+// somebody zeroes).
 template <int MODE>
 __global__ void __launch_bounds__(kD) kv4_merge_kernel(const Kv4Args a) {
   __shared__ float2 s_ml[kMaxParts];
@@ -1068,6 +1080,9 @@ __global__ void __launch_bounds__(kD) kv4_merge_kernel(const Kv4Args a) {
 // Warps of a CTA, CTAs a SM, stages of 1.25 KB a warp.  (8 requests of 32K: 41 us; three CTAs: 45.)
 constexpr int kScoreW = 8, kScoreCtas = 2, kScoreStages = 6;
 
+// 8 requests of 32K keys in groups of 32, 8 KV heads of 8: 167 MB read, 38 us a call, 4.6 TB/s.  Of 41 in a
+// graph, 36 without the products, 34 without the stores too, 39.5 on cells from L2: a start of 5 us, then HBM and the
+// 194 instructions of a tile at 60 % of the issue slots, neither hidden by the other entirely.
 template <int NG, int NT, int AGG>
 __global__ void __launch_bounds__(32 * kScoreW, kScoreCtas) kv4_score_kernel(const Kv4Args a) {
   constexpr int W = kScoreW, S = kScoreStages, kCell = kv4_cell(NG);
@@ -1175,7 +1190,9 @@ __device__ __forceinline__ void values_of(uint32_t codes, uint32_t word01, uint3
 }
 
 // Four lanes a row: 16 bytes of codes each, four consecutive entries of every 16.  Finding a row is a
-// step a round: its place's position, that one's entry, the row.
+// step a round: its place's position, that one's entry, the row.  3,409 rows of K and V for 64 heads of requests
+// of 32K: 52 MB read, 112 MB written, 28.5 us; what rows that lie alone leave of HBM's rate, and the 5 us
+// until the first ones are found.
 template <int NG, typename T>
 __global__ void __launch_bounds__(256, 5) kv4_gather_kernel(const Kv4Args a, T* k_out, T* v_out, int n_att) {
   pdl_release();

