@@ -461,6 +461,66 @@ def test_streams_and_graphs(skv):
     c.check(c.step.out, c.step.lse)
 
 
+@pytest.mark.parametrize("seed", range(16))
+def test_shapes_at_random(skv, seed):
+    """Whole histories, lists, gathers and scores of batches, heads, groups, blocks and tables drawn together."""
+    rng = np.random.default_rng(100 + seed)
+    B = int(rng.choice([1, 2, 5, 17, 130, 400]))
+    longest = int(rng.choice([1, 15, 16, 40, 600]) if B > 5 else rng.choice([1, 17, 300, 4000]))
+    lens = [int(x) for x in rng.integers(0, longest + 1, B)]
+    if rng.random() < 0.3:
+        lens = [x if rng.random() < 0.2 else 0 for x in lens]
+    H, G, agg = int(rng.integers(1, 4)), int(rng.integers(1, 17)), int(rng.integers(0, 3))
+    per_head = bool(rng.random() < 0.4)
+    k, ns, nl = int(rng.choice([0, 1, 16, 33, 200])), int(rng.choice([0, 1, 4, 19])), int(rng.choice([0, 1, 17, 128]))
+    c = Case(skv, lens, H, G, k=k, ns=ns, nl=nl, agg=agg, group=int(rng.choice([32, 64, 128])),
+             bs=int(rng.choice([16, 32, 48, 80, 256])), host=float(rng.choice([0.0, 0.0, 0.5])), per_head=per_head,
+             max_len=longest + int(rng.integers(0, 100)), seed=seed)
+    q = c.q.cuda()
+    c.check(*c.step.attend_all(q))
+    heads = H * G if agg == 2 else H
+    idx = _selection(c, rng, k, heads, bool(rng.random() < 0.5))
+    if k + ns + nl:
+        out = [x.clone() for x in c.step.attend(q, _dev(idx))]
+        c.check(*out, lambda b, r: kv4_ref.attended(lens[b], ns, nl, [t for t in idx[b, r] if t >= 0]))
+        again = c.step.attend(q, _dev(idx))
+        assert torch.equal(out[0], again[0]) and torch.equal(out[1], again[1])
+        kk, vv = c.step.gather(_dev(idx))
+        for b in {0, B // 2, B - 1}:
+            if lens[b] == 0:
+                assert not kk[b].any() and not vv[b].any()
+                continue
+            for r in range(heads):
+                full = kv4_ref.attended(lens[b], ns, nl, idx[b, r])
+                at = np.array(full + [-1] * (ns + k + nl - len(full)), np.int64)
+                for kv, got in ((0, kk), (1, vv)):
+                    want = kv4_ref.values(*c.unit(kv, b, r // G if agg == 2 else r, np.maximum(at, 0))) * (at >= 0)[:, None]
+                    err = np.abs(got[b, r].double().cpu().numpy() - want)
+                    assert np.all(err <= (HALF + 2.0 ** -23) * np.abs(want) + 1e-37)
+    scores = torch.full((B, heads, c.max_len), 7.0, device="cuda")
+    c.step.score(q, scores)
+    assert_scores(c, scores, c.q, agg, G, 7.0)
+    assert int(c.step.status.item()) == 0
+
+
+def test_two_at_once(skv):
+    """Steps of their own over one pool, on two streams, none waiting for the other."""
+    c = Case(skv, [3000, 90, 0, 2000], 2, 8, k=60, ns=4, nl=32)
+    q = [c.q.cuda(), torch.flip(c.q, (0,)).contiguous().cuda()]
+    steps, streams = [skv.Kv4Step(c.p, c.pool) for _ in q], [torch.cuda.Stream() for _ in q]
+    want = [[x.clone() for x in (*s.attend_all(x), *s.run(x))] for s, x in zip(steps, q)]
+    for s in steps:
+        s.out.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, x, st in zip(steps, q, streams):
+            s.attend_all(x, stream=st)
+            s.run(x, stream=st)
+    torch.cuda.synchronize()
+    for s, w in zip(steps, want):
+        assert torch.equal(s.out, w[2]) and torch.equal(s.lse, w[3]) and int(s.status.item()) == 0
+
+
 # ---------------------------------------------------------------------------- append
 
 
