@@ -358,9 +358,8 @@ struct CellFeeder {
     cp_async_commit();
     to = to + kStage == end ? end - S * kStage : to + kStage;
   }
-  // of tile `tile` of a request of L positions, S - 1 issues ago
-  __device__ __forceinline__ uint32_t rows(int L, int tile, int) const {
-    const int n = L - (tile << 4);
+  // of the tile S - 1 issues ago, n rows before its request's end
+  __device__ __forceinline__ uint32_t rows(int n, int) const {
     return gone >> (S - 1) & 1u ? 0u : n >= 16 ? 0xffffu : (1u << n) - 1u;
   }
 };
@@ -426,7 +425,7 @@ struct RowFeeder {
     half = half == 0 ? 1 : 0;
     to = to + kStage == end ? end - S * kStage : to + kStage;
   }
-  __device__ __forceinline__ uint32_t rows(int, int, int stage) const { return masks[stage]; }
+  __device__ __forceinline__ uint32_t rows(int, int stage) const { return masks[stage]; }
 };
 
 // ---------------------------------------------------------------------------- the products
@@ -863,14 +862,16 @@ __device__ __forceinline__ void attend_cell(uint32_t cell, uint32_t mask, const 
 
 template <int NG, int NT, int MODE>
 struct AttnShape {
-  // Warps of a CTA, CTAs a SM, stages of 2.5 KB a warp.  One CTA a SM: of two, the schedulers serve the
-  // one that came first before the other, it ends at 80 % of the time and leaves the SM half empty
-  // (a million keys, 8 warps in either: 231 us; 12 or 16 warps in one 215, 8 warps 258); 12 warps are
-  // no slower than 16, and the products keep 168 registers (8 requests of 32K: 78 us against 81).
-  // A list's rows arrive late rather, and two CTAs hide more of that (3,409 rows of 32K for 8
-  // requests: 26.8 us, one CTA 28.8).  Two column tiles take all the registers of 8 warps.
+  // Warps of a CTA, CTAs a SM, stages of 2.2 to 2.5 KB a warp.  One CTA a SM: of two, the schedulers serve
+  // the one that came first before the other, it ends at 80 % of the time and leaves the SM half empty
+  // (a million keys in groups of 128, 8 warps in either: 231 us; 12 or 16 warps in one 215, 8 warps
+  // 258).  16 warps have 128 registers each, 12 have 168: groups of 128 fit in the first (201 us with
+  // 12, 198 with 16), those of 32 and 64 do not (8 requests of 32K: 73 us with 12, 74 with 16).  A
+  // list's rows arrive late rather, and two CTAs hide more of that (3,409 rows of 32K for 8 requests:
+  // 26.8 us, one CTA 28.8).  Two column tiles take all the registers of 8 warps.
   static constexpr int kCtas = NT == 1 && MODE == kList ? 2 : 1;
-  static constexpr int kW = NT == 1 && MODE == kDense ? 12 : 8, kStages = NT == 2 ? 6 : MODE == kDense ? 5 : 3;
+  static constexpr int kW = NT == 2 || MODE == kList ? 8 : NG == 1 ? 16 : 12;
+  static constexpr int kStages = NT == 2 ? 6 : MODE == kList || NG == 1 ? 3 : 5;
   static constexpr int kRing = kW * kStages * 2 * kv4_cell(NG);
   static constexpr int kRow = kD + 4;  // floats of a head's partial row: heads 2 t, 2 t + 2 an eighth of the banks apart
   static constexpr int kOut = kW * 8 * NT * kRow * 4;
@@ -904,34 +905,41 @@ __global__ void __launch_bounds__(32 * AttnShape<NG, NT, MODE>::kW, AttnShape<NG
   __shared__ uint32_t s_mask[MODE == kList ? W : 1][S];
   __shared__ float2 s_ml[HC][W];
   __shared__ __align__(16) QShared<NT> s_q;
+  // the walk's state between units, which the products need no registers for
+  __shared__ Cursor s_unit;
+  __shared__ long long s_at_place;  // of the unit among the weights
   float* s_o = reinterpret_cast<float*>(smem + Shape::kRing);
   pdl_release();
   pdl_wait();
-  Cursor u;
-  const Share mine = find_share<MODE, W>(a, &u);
+  Cursor at;
+  const Share mine = find_share<MODE, W>(a, &at);
   if (mine.tiles == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int share = mine.tiles;
-  Cursor at = u;
-  at.tile += warp;
   const uint32_t ring = smem_u32(smem) + warp * S * kStage;
-  auto queries = [&]() { return a.q + ((size_t)u.b * a.Hq + (size_t)u.h * a.G) * kD; };
+  auto queries = [&](const Cursor& u) { return a.q + ((size_t)u.b * a.Hq + (size_t)u.h * a.G) * kD; };
   float x[NT][4];
-  load_queries<NT, false>(queries(), a.G, x);
+  load_queries<NT, false>(queries(at), a.G, x);
+  if (threadIdx.x == 0) {
+    s_unit = at;
+    s_at_place = mine.place;
+  }
+  at.tile += warp;
   typename Pick<MODE, NG, W, S>::type feed(a, s_at[warp], s_mask[MODE == kList ? warp : 0], ring, at,
                                         share > warp ? (share - warp + W - 1) / W : 0);
 #pragma unroll 1
   for (int i = 0; i < S - 1; ++i) feed.issue();
-  long long place = mine.place;  // of the unit among the weights
   int stage = 0, next = warp;  // this warp's next tile
+  __syncthreads();
   // units of the share: tiles [from, to) of it, the unit's first at `base`
   for (int from = 0, seg = 0; from < share; ++seg) {
-    const int base = from - u.tile, to = u.nt - u.tile < share - from ? base + u.nt : share;
+    const int base = from - s_unit.tile, left = s_unit.nt - s_unit.tile, to = left < share - from ? from + left : share;
+    const uint32_t rows = (uint32_t)s_unit.L + 16u * (uint32_t)base;  // where the unit's rows end, 16 a tile from the share's first
     QFrag<NT> q;
     float kf[NT][2];
     State<NG, NT> s;
     clear(s);
-    if (seg > 0) load_queries<NT, false>(queries(), a.G, x);
+    if (seg > 0) load_queries<NT, false>(queries(s_unit), a.G, x);
     make_queries<NG, NT, false>(x, a.G, s_q, q);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -943,7 +951,7 @@ __global__ void __launch_bounds__(32 * AttnShape<NG, NT, MODE>::kW, AttnShape<NG
       cp_async_wait<S - 2>();
       __syncwarp();
       feed.issue();  // into the stage of the tile before this one
-      const uint32_t mask = feed.rows(u.L, next - base, stage);
+      const uint32_t mask = feed.rows((int)(rows - 16u * (uint32_t)next), stage);
       if (mask != 0u) attend_cell<NG, NT>(ring + stage * kStage, mask, q, kf, s);
       stage = stage == S - 1 ? 0 : stage + 1;
     }
@@ -974,6 +982,7 @@ __global__ void __launch_bounds__(32 * AttnShape<NG, NT, MODE>::kW, AttnShape<NG
         }
       }
     __syncthreads();
+    const Cursor u = s_unit;
     const bool whole = base >= 0 && base + u.nt <= share;
     const size_t hq = (size_t)u.b * a.Hq + (size_t)u.h * a.G;
     float* slot = a.ws + ((size_t)blockIdx.x * 2 + (seg > 0)) * kSlotFloats;
@@ -1003,13 +1012,18 @@ __global__ void __launch_bounds__(32 * AttnShape<NG, NT, MODE>::kW, AttnShape<NG
     }
     if (threadIdx.x == 0 && base >= 0)
       a.desc[(size_t)u.b * a.H + u.h] =
-          make_int2((int)blockIdx.x | (seg > 0 ? 1 << 30 : 0), holder(mine.weight, mine.ctas, place + kUnit + u.nt - 1));
+          make_int2((int)blockIdx.x | (seg > 0 ? 1 << 30 : 0), holder(mine.weight, mine.ctas, s_at_place + kUnit + u.nt - 1));
     __syncthreads();
     from = to;
     if (from < share) {
-      place += kUnit + u.nt;
-      u.tile = u.nt;
-      settle<MODE>(a, u);
+      if (threadIdx.x == 0) {
+        s_at_place += kUnit + u.nt;
+        Cursor n = u;
+        n.tile = n.nt;
+        settle<MODE>(a, n);
+        s_unit = n;
+      }
+      __syncthreads();
     }
   }
 }
