@@ -888,8 +888,8 @@ struct Pick<kList, NG, W, S> {
 };
 
 // Persistent CTAs, a share each of the tiles of all units; a warp computes its own tiles.  Measured
-// (8 KV heads): 8 requests of 32K keys in groups of 32, 8 query heads each, 336 MB, 74 us (4.5 TB/s); a
-// million keys in groups of 128, 4 query heads, 1,141 MB, 203 us (5.6 TB/s); lists of 3,409 rows of 32K
+// (8 KV heads): 8 requests of 32K keys in groups of 32, 8 query heads each, 336 MB, 73 us (4.6 TB/s); a
+// million keys in groups of 128, 4 query heads, 1,141 MB, 201 us (5.7 TB/s); lists of 3,409 rows of 32K
 // for the 8 requests, 52 MB read, 23 us; 4 requests to 777 keys 10.7 us a call.  The instructions of
 // a tile bound it: 350 in groups of 32, 146 of them masks, permutations and shifts at half the
 // issue rate, and 18 products; on cells from L2 alone the first of these takes 2 us less, with
