@@ -658,3 +658,54 @@ def test_append_refusals(skv):
     step.append(None, k, k, pos, req)
     assert int(step.status.item()) == skv.SKV_DEV_BAD_SLOT | skv.SKV_DEV_BAD_LENGTH | skv.SKV_DEV_BAD_INDEX
     assert torch.equal(c.pool.gpu_k, old[0]) and torch.equal(c.pool.gpu_v, old[1])
+
+
+@pytest.mark.parametrize("grown", [False, True])
+def test_written_then_read(skv, grown):
+    """The same rows written over and read back many times with nothing waiting between, and (grown) entries of a
+    table that its own kernel moves every time: each read sees the write ahead of it on the stream."""
+    B, H, G, bs, n = 24, 2, 4, 16, 24 * 16
+    lens = torch.full((B,), 0 if grown else 16, dtype=torch.int32, device="cuda")
+    p = skv.Problem(batch=B, n_kv_heads=H, n_q_heads=H * G, d_qk=D, d_v=D, max_len=64, topk=0, n_sink=0, n_local=16,
+                    block_size=bs, seq_lens=lens)
+    table = torch.zeros((B, 4), dtype=torch.int32, device="cuda")
+    table[:, 0] = torch.arange(B)
+    pool = skv.Kv4Pool.empty(3 * B, H, bs, table)
+    free = torch.arange(3 * B, dtype=torch.int32, device="cuda")
+    tables = skv.BlockTables(p, table, free) if grown else None
+    step = skv.Kv4Step(p, pool)
+    tokens = skv.TokenStep(p, skv.Rotary(None, rot_dim=0), pool)
+    at = torch.arange(16, dtype=torch.int32, device="cuda").repeat(B)
+    req = torch.arange(B, dtype=torch.int32, device="cuda").repeat_interleave(16)
+    q = torch.randn((B, H * G, D), device="cuda").to(torch.bfloat16)
+    rows = [torch.randn((2, n, H, D), device="cuda").to(torch.bfloat16) for _ in range(30)]
+    more, less = (torch.full((B,), x, dtype=torch.int32, device="cuda") for x in (16, -64))
+
+    def once(x, waits):
+        a, r = (at, req) if tables is None else tables.update(more, n)[:2]
+        if waits:
+            torch.cuda.synchronize()
+        tokens.append(None, x[0], x[1], a, r)
+        if waits:
+            torch.cuda.synchronize()
+        got = [*step.gather(), *(y.clone() for y in step.attend_all(q))]
+        if waits:
+            torch.cuda.synchronize()
+        if tables is not None:
+            tables.update(less)
+            # the stack's top changes places with its bottom: the next blocks are others
+            free.copy_(free.roll(5))
+        return got
+
+    want = [once(x, True) for x in rows]
+    got = [once(x, False) for x in rows]
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(x, y) for x, y in zip(w, g))
+    for x, g in zip(rows, got):  # a step of the 15th of a group's range at most, its halves' roundings on top
+        for kv in range(2):
+            y = x[kv].double().view(B, 16, H, D).transpose(1, 2)
+            span = y.view(B, H, 16, 4, 32)
+            tol = (span.amax(-1) - span.amin(-1)) / 15 * 0.6 + 2.0 ** -7 * span.abs().amax(-1)
+            assert ((g[kv].double() - y).abs().view(span.shape) <= tol.unsqueeze(-1)).all()
+    assert int(step.status.item()) == 0 and int(tokens.status.item()) == 0

@@ -60,7 +60,7 @@ __device__ __forceinline__ int tiles_of(const Kv4Args& a, int L) {
 }
 
 __device__ __forceinline__ int len_of(const Kv4Args& a, int b) {
-  const int L = __ldg(a.seq_lens + b);
+  const int L = a.seq_lens[b];
   return L < 0 ? 0 : L > a.max_len ? a.max_len : L;
 }
 
@@ -193,14 +193,16 @@ __device__ __forceinline__ void cp_async_row(uint32_t dst, const void* src) {
   else
     asm volatile("cp.async.ca.shared.global.L2::64B [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
+// (Plain loads here as of tables, lists and lengths: kernels start before those ahead of them on the stream end,
+// and what these write is not constant for a kernel's whole life.)
 template <int WORDS>
 __device__ __forceinline__ void load_row(const void* src, uint32_t* w) {
   if constexpr (WORDS == 4)
-    asm("ld.global.nc.L2::64B.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(src));
+    asm("ld.global.L2::64B.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(src));
   else if constexpr (WORDS == 2)
-    asm("ld.global.nc.L2::64B.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(src));
+    asm("ld.global.L2::64B.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(src));
   else
-    asm("ld.global.nc.L2::64B.u32 %0, [%1];" : "=r"(w[0]) : "l"(src));
+    asm("ld.global.L2::64B.u32 %0, [%1];" : "=r"(w[0]) : "l"(src));
 }
 
 // A lane's row on its way from its place in a list to its number.
@@ -226,7 +228,7 @@ __device__ __forceinline__ void row_position(const Kv4Args& a, const Cursor& c, 
   if (j < g.s_end) {
     w.t = j;
   } else if (j < g.s_end + a.k) {
-    w.t = __ldg(a.idx + ((size_t)c.b * a.H + c.h) * a.k + (j - g.s_end));
+    w.t = a.idx[((size_t)c.b * a.H + c.h) * a.k + (j - g.s_end)];
     w.lo = g.s_end;
     w.hi = g.l_start;
   } else {
@@ -245,7 +247,7 @@ __device__ __forceinline__ void row_entry(const Kv4Args& a, bool reports, const 
   const int block = a.shift >= 0 ? p.t >> a.shift : p.t / a.bs;
   w.off = p.t - block * a.bs;
   w.h = p.h;
-  w.e = __ldg(a.pool.table + (size_t)p.table * a.pool.stride + block);
+  w.e = a.pool.table[(size_t)p.table * a.pool.stride + block];
 }
 
 // The row's number in its pool, bit 31: the host's (pools have fewer than 2^31 rows).
@@ -301,7 +303,7 @@ struct CellFeeder {
       const int i = (MODE == kScore ? regions_of(c.L, a.ns, a.nl).s_end >> 4 : 0) + c.tile;
       const int block = a.shift >= 0 ? i >> (a.shift - 4) : i / a.cells;
       in = c.h * a.cells + (i - block * a.cells);
-      e = __ldg(table_row(a.pool, c.b, c.h, a.heads) + block);
+      e = table_row(a.pool, c.b, c.h, a.heads)[block];
       if (a.pool.per_head && e >= 0) in -= c.h * a.cells;
       if (lane == 31) {
         c.tile += W;
