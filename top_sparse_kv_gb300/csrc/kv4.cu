@@ -1096,7 +1096,7 @@ __global__ void __launch_bounds__(kD) kv4_merge_kernel(const Kv4Args a) {
 // Warps of a CTA, CTAs a SM, stages of 1.25 KB a warp.  (8 requests of 32K: 41 us; three CTAs: 45.)
 constexpr int kScoreW = 8, kScoreCtas = 2, kScoreStages = 6;
 
-// 8 requests of 32K keys in groups of 32, 8 KV heads of 8: 167 MB read, 38 us a call, 4.6 TB/s.  Of 41 in a
+// 8 requests of 32K keys in groups of 32, 8 KV heads of 8: 167 MB read, 39 us a call, 4.5 TB/s.  Of 41 in a
 // graph, 36 without the products, 34 without the stores too, 39.5 on cells from L2: a start of 5 us, then HBM and the
 // 194 instructions of a tile at 60 % of the issue slots, neither hidden by the other entirely.
 template <int NG, int NT, int AGG>
