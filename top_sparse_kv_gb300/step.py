@@ -332,19 +332,31 @@ class Kv4Step:
         self._step, self._gather = lib.skv_decode_step_kv4, lib.skv_gather_kv4
         self._scores = self._idx = None
 
+    def _new(self, shape, dtype, stream):
+        """A tensor of the allocator's pool of the stream that writes it: the current stream's may hand out
+        memory that work queued there has still to use."""
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            return torch.empty(shape, dtype=dtype, device=self._dev)
+
+    def _own_scores(self, stream):
+        if self._scores is None:
+            self._scores = self._new(self._s, torch.float32, stream)
+        return self._scores
+
+    def _own_idx(self, stream):
+        if self._idx is None:
+            self._idx = self._new(self._i, torch.int32, stream)
+        return self._idx
+
     @property
     def scores(self) -> torch.Tensor:
-        """[batch, heads, max_len]; made when first used."""
-        if self._scores is None:
-            self._scores = torch.empty(self._s, dtype=torch.float32, device=self._dev)
-        return self._scores
+        """[batch, heads, max_len]; made when first used, for the stream of that use."""
+        return self._own_scores(None)
 
     @property
     def idx(self) -> torch.Tensor:
-        """[batch, heads, topk]; made when first used."""
-        if self._idx is None:
-            self._idx = torch.empty(self._i, dtype=torch.int32, device=self._dev)
-        return self._idx
+        """[batch, heads, topk]; made when first used, for the stream of that use."""
+        return self._own_idx(None)
 
     def _ptr(self, name, t, dtype, shape):
         if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != self._device:
@@ -353,7 +365,7 @@ class Kv4Step:
 
     def score(self, q_score, scores=None, stream=None):
         """Scores of the candidates into `scores` (the step's own unless given), which it returns."""
-        scores = self.scores if scores is None else scores
+        scores = self._own_scores(stream) if scores is None else scores
         st = self._score(self._p, self._ptr("q_score", q_score, torch.bfloat16, self._q_score), self._pool, self._group,
                          self._ptr("scores", scores, torch.float32, self._s), self._st, B.raw_stream(self._device, stream))
         if st:
@@ -362,9 +374,10 @@ class Kv4Step:
 
     def topk(self, stream=None):
         """The selection of the step's own scores, into idx."""
+        idx = self._own_idx(stream)
         if self.p.topk > 0:
-            B.skv_topk(self.p, self.scores, self.idx, self.ws, self.status, stream)
-        return self.idx
+            B.skv_topk(self.p, self._own_scores(stream), idx, self.ws, self.status, stream)
+        return idx
 
     def _attend(self, q, idx, stream):
         st = self._attn(self._p, self._ptr("q", q, torch.bfloat16, self._q), self._pool, self._group,
@@ -376,7 +389,7 @@ class Kv4Step:
 
     def attend(self, q, idx=None, stream=None):
         """(out, lse) over sink, selection (the step's own idx unless given) and window."""
-        return self._attend(q, self.idx if idx is None else idx, stream)
+        return self._attend(q, self._own_idx(stream) if idx is None else idx, stream)
 
     def attend_all(self, q, stream=None):
         """(out, lse) over every position of each history."""
@@ -386,8 +399,8 @@ class Kv4Step:
         """(out, lse) of one decode step; scores and idx hold its scores and selection."""
         st = self._step(self._p, self._ptr("q", q, torch.bfloat16, self._q),
                         None if q_score is None else self._ptr("q_score", q_score, torch.bfloat16, self._q_score),
-                        self._pool, self._group, self.scores.data_ptr(), B.list_ptr(self.p, self.idx), *self._outs,
-                        B.raw_stream(self._device, stream))
+                        self._pool, self._group, self._own_scores(stream).data_ptr(),
+                        B.list_ptr(self.p, self._own_idx(stream)), *self._outs, B.raw_stream(self._device, stream))
         if st:
             raise B.SkvError("skv_decode_step_kv4", st)
         return self.out, self.lse
@@ -396,12 +409,10 @@ class Kv4Step:
         """(k, v) [batch, heads, n_att, 128] of the problem's type: the attended rows' values; new tensors
         unless given.  Without a selection (topk 0) those of sink and window."""
         if idx is None and self.p.topk > 0:
-            idx = self.idx
+            idx = self._own_idx(stream)
         ip = None if idx is None else self._ptr("idx", idx, torch.int32, self._i)
-        if k_out is None or v_out is None:
-            with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():  # (its allocator's pool)
-                k_out = torch.empty(self._rows, dtype=self._type, device=self._dev) if k_out is None else k_out
-                v_out = torch.empty(self._rows, dtype=self._type, device=self._dev) if v_out is None else v_out
+        k_out = self._new(self._rows, self._type, stream) if k_out is None else k_out
+        v_out = self._new(self._rows, self._type, stream) if v_out is None else v_out
         st = self._gather(self._p, self._pool, self._group, ip, self._ptr("k_out", k_out, self._type, self._rows),
                           self._ptr("v_out", v_out, self._type, self._rows), self._st, B.raw_stream(self._device, stream))
         if st:
