@@ -850,9 +850,10 @@ skv_status skv_kv4_workspace_size(const skv_problem *p, size_t *bytes);
  *   z_t = sm_scale * <q, k^_t>,  out = sum_t softmax(z)_t v^_t,  lse = log sum_t exp(z_t)
  * A request of length 0 (or an empty list) gives out 0 and lse -inf.  Entries outside their
  * pool, positions outside the candidates: flagged, zero weight.  p->dtype is bf16.  Softmax
- * weights times steps meet the codes as fp16 on the tensor cores (11 bits; a weight below
- * 2^-32 of the largest counts as 0, steps from 2^-60 up keep that precision); centres, sums
- * and the maximum are fp32.  Deterministic: the same inputs give the same bits. */
+ * weights times steps meet the codes as fp16 on the tensor cores: 11 bits, and what lies below
+ * 2^-21 of the largest such product of its own query head and channel group is held to 2^-32
+ * of that; centres, sums and the maximum are fp32.  Deterministic: the same inputs give the
+ * same bits. */
 skv_status skv_attn_kv4(const skv_problem *p, const void *q, const skv_kv_pool *pool, int32_t group,
                         const int32_t *idx, void *out, float *lse, void *ws, size_t ws_bytes, int32_t *dev_status,
                         void *stream);

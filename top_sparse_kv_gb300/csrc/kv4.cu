@@ -16,8 +16,8 @@
 // Queries go to fp16 under a power of two of their own: bf16's 8 bits fit, and what falls under
 // fp16's range is 2^-35 of the head's largest.
 //   out     sum_t w_tg (c - 8) + sum_t p_t z_tg,  w_tg = p_t s_tg in fp16
-// The maximum is a running one that moves only when a logit passes it by 2^7 (then everything
-// is rescaled), and so is the power of two above the steps.
+// The maximum is a running one that moves only when a logit passes it by 2^7 (then the head's sums
+// are rescaled); w comes under a power of two that follows the largest of its head and group.
 #include "attn_common.cuh"
 #include "kv4.cuh"
 
@@ -459,6 +459,18 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+// the larger magnitudes of two pairs (a NaN gives way)
+__device__ __forceinline__ uint32_t max_abs(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("{\n\t.reg .b32 x, y;\n\tabs.f16x2 x, %1;\n\tabs.f16x2 y, %2;\n\tmax.f16x2 %0, x, y;\n\t}" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -702,22 +714,29 @@ __device__ __forceinline__ void logits(uint32_t cell, const QFrag<NT>& f, float 
 
 // ---------------------------------------------------------------------------- attention
 
-// A warp's state of a unit: p_t = 2^(x_t + ref), ref = 7 - sigma - the running maximum.
+// A warp's state of a unit: p_t = 2^(x_t + ref), ref = - the running maximum, a whole number.  The operand of a
+// key, head and group, w = p s 2^e, has a power of two of its own, which keeps the largest one so far
+// between 2^7 and 2^15: fp16 holds it to 11 bits, and what lies under 2^-21 of that largest to 2^-32 of it.  (A power
+// that heads or groups share goes by the largest product of all, and others' may be lost.)
 template <int NG, int NT>
 struct State {
   float l[NT][2], ref[NT][2];
   float top[NT][2];   // the logit, in its column's unit, past which the maximum moves
   // rows 2 g (2^-24 a unit) and 2 g + 1 (2^-20; i odd: 16 of it and the other, 2^-24) of entries
-  // 16 i, columns heads 2 t, 2 t + 1
+  // 16 i, columns heads 2 t, 2 t + 1; times 2^e
   float o[NT][8][4];
   float z[NT][NG][2];
-  int sigma;          // steps are below 2^(sigma + 1)
+  float pw[NT][NG][2];  // 2^e; negative where this lane's keys are the complemented ones
 };
 constexpr float kFloor = -3.0e38f;
-constexpr int kSigmaMin = -60, kSigmaMax = 120;
+constexpr int kPowMin = -100, kPowMax = 110;  // of e: weights times it stay in fp32, and so does its inverse
+
+__device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23 & 255u) - 127; }
+__device__ __forceinline__ float power_of(int e) { return e < -126 ? 0.f : __uint_as_float((uint32_t)(e + 127) << 23); }
 
 template <int NG, int NT>
 __device__ __forceinline__ void clear(State<NG, NT>& s) {
+  const float pw = threadIdx.x & 4 ? -power_of(kPowMax) : power_of(kPowMax);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -726,47 +745,91 @@ __device__ __forceinline__ void clear(State<NG, NT>& s) {
       s.ref[nt][i] = -kFloor;
       s.top[nt][i] = kFloor;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) s.z[nt][g][i] = 0.f;
+      for (int g = 0; g < NG; ++g) s.z[nt][g][i] = 0.f, s.pw[nt][g][i] = pw;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s.o[nt][i][j] = 0.f;
   }
-  s.sigma = kSigmaMin;
 }
 
-// A maximum or a power of the steps that a cell has passed: everything in the new reference.
+// A logit of the cell has passed its head's maximum by 2^7: that head's sums in a new reference.  All factors are powers
+// of two.  The operands' powers take up the difference, so that the outputs stay -- but for what
+// would take them past their end.
 template <int NG, int NT>
-__device__ __forceinline__ void rescale(State<NG, NT>& s, const float (&c)[NT][4], const float (&kf)[NT][2], float smax) {
+__device__ __forceinline__ void move_maximum(State<NG, NT>& s, const float (&c)[NT][4], const float (&kf)[NT][2]) {
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, off));
-  int e = (int)((__float_as_uint(smax) >> 23) & 255u) - 127;
-  e = e > kSigmaMax ? kSigmaMax : e;
-  const int sigma = e > s.sigma ? e : s.sigma;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    float f[2];
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float m = fmaxf(c[nt][i], c[nt][i + 2]) * kf[nt][i];
+      float m = fmaxf(c[nt][i], c[nt][i + 2]);
 #pragma unroll
       for (int off = 4; off <= 16; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-      m = fmaxf(m, (7.f - (float)s.sigma) - s.ref[nt][i]);  // (the floor stays about itself)
-      const float ref = (7.f - (float)sigma) - m;
-      f[i] = ex2(ref - s.ref[nt][i]);
-      s.ref[nt][i] = ref;
-      s.top[nt][i] = (m + 7.f) / kf[nt][i];
-      s.l[nt][i] *= f[i];
+      if (m > s.top[nt][i]) {
+        m = ceilf(m * kf[nt][i]);
+        const float down = fmaxf(-m - s.ref[nt][i], -1000.f), f = power_of((int)down);
+        const bool first = s.ref[nt][i] == -kFloor;
+        s.ref[nt][i] = -m;
+        s.top[nt][i] = (m + 7.f) / kf[nt][i];
+        if (first) continue;  // (nothing to bring down)
+        s.l[nt][i] *= f;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) s.z[nt][g][i] *= f[i];
+        for (int g = 0; g < NG; ++g) {
+          s.z[nt][g][i] *= f;
+          const int room = kPowMax - exponent_of(s.pw[nt][g][i]), up = min((int)-down, room);
+          s.pw[nt][g][i] = __uint_as_float(__float_as_uint(s.pw[nt][g][i]) + ((uint32_t)up << 23));
+          if (up < (int)-down) {
+            const float k = power_of((int)down + up);
+#pragma unroll
+            for (int j = g * 8 / NG; j < (g + 1) * 8 / NG; ++j) s.o[nt][j][i] *= k, s.o[nt][j][i + 2] *= k;
+          }
+        }
+      }
     }
+}
+
+// An operand of the cell has reached 2^15: its head's and group's power of two goes down, and the outputs with it.
+template <int NG, int NT>
+__device__ __forceinline__ void lower_powers(State<NG, NT>& s, const float (&p)[NT][4], const uint32_t (&w0)[NG], const uint32_t (&w1)[NG]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s.o[nt][i][j] *= f[j & 1];
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float m = fmaxf(p[nt][i] * fabsf(step_of(w0[g])), p[nt][i + 2] * fabsf(step_of(w1[g])));
+#pragma unroll
+        for (int off = 4; off <= 16; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        if (m * fabsf(s.pw[nt][g][i]) >= 0x1p15f) {
+          const int e = max(7 - exponent_of(m), kPowMin);
+          const float k = power_of(e - exponent_of(s.pw[nt][g][i]));
+          s.pw[nt][g][i] = copysignf(power_of(e), s.pw[nt][g][i]);
+#pragma unroll
+          for (int j = g * 8 / NG; j < (g + 1) * 8 / NG; ++j) s.o[nt][j][i] *= k, s.o[nt][j][i + 2] *= k;
+        }
+      }
+}
+
+// The cell's operands, keys by heads; true where one has reached 2^15.
+template <int NG, int NT>
+__device__ __forceinline__ bool weigh(const State<NG, NT>& s, const float (&p)[NT][4], const uint32_t (&w0)[NG], const uint32_t (&w1)[NG],
+                                      uint32_t (&w)[NT][NG][2]) {
+  uint32_t most = 0u;
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    const float s0 = step_of(w0[g]), s1 = step_of(w1[g]);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {  // (the power first: a weight that is 0 stays 0 whatever the step)
+      const float2 e = make_float2(s.pw[nt][g][0], s.pw[nt][g][1]);
+      const float2 x = mul2(mul2(make_float2(p[nt][0], p[nt][1]), e), make_float2(s0, s0));
+      const float2 y = mul2(mul2(make_float2(p[nt][2], p[nt][3]), e), make_float2(s1, s1));
+      w[nt][g][0] = pack_f16(x.x, x.y);
+      w[nt][g][1] = pack_f16(y.x, y.y);
+      most = max_abs(most, max_abs(w[nt][g][0], w[nt][g][1]));
+    }
   }
-  s.sigma = sigma;
+  return (most + 0x08000800u) & 0x80008000u;
 }
 
 // A cell's keys into the state.  The weights p_t meet the centres in fp32 and, times the steps, the
@@ -777,21 +840,16 @@ __device__ __forceinline__ void rescale(State<NG, NT>& s, const float (&c)[NT][4
 template <int NG, int NT>
 __device__ __forceinline__ void attend_cell(uint32_t cell, uint32_t mask, const QFrag<NT>& f, const float (&kf)[NT][2],
                                             State<NG, NT>& s) {
-  constexpr int kCell = kv4_cell(NG), kLook = NG == 4 ? 2 : 1;  // words a lane looks at for the largest step
+  constexpr int kCell = kv4_cell(NG);
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, key = key_of(g);
   float c[NT][4];
   logits<NG, NT>(cell, f, c);
   const uint32_t words = cell + kCell + 16 * kCodeBytes;
-  uint32_t look[kLook];
-  lds_words<kLook>(words + (NG == 1 ? lane & 15 : lane) * 4 * kLook, look);
-  float smax = fabsf(step_of(look[0]));
-  if (kLook == 2) smax = fmaxf(smax, fabsf(step_of(look[kLook - 1])));
   uint32_t w0[NG], w1[NG];
   lds_words<NG>(words + key * 4 * NG, w0);
   lds_words<NG>(words + (key + 8) * 4 * NG, w1);
   if (mask != 0xffffu) {  // what lies in rows that are not there counts for nothing
     const bool on0 = mask >> key & 1u, on1 = mask >> (key + 8) & 1u;
-    if (!(mask >> (NG == 1 ? lane & 15 : lane >> 1) & 1u)) smax = 0.f;
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
       w0[i] = on0 ? w0[i] : 0u;
@@ -802,13 +860,12 @@ __device__ __forceinline__ void attend_cell(uint32_t cell, uint32_t mask, const 
 #pragma unroll
       for (int i = 0; i < 4; ++i) c[nt][i] = (i < 2 ? on0 : on1) ? c[nt][i] : -INFINITY;
   }
-  bool past = smax >= __uint_as_float((uint32_t)(s.sigma + 128) << 23);
+  bool past = false;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int i = 0; i < 2; ++i) past |= fmaxf(c[nt][i], c[nt][i + 2]) > s.top[nt][i];
-  if (__any_sync(0xffffffffu, past)) rescale<NG, NT>(s, c, kf, smax);
-  const float off = g & 1 ? 7.f : -8.f, sign = g & 1 ? -1.f : 1.f;
+  if (__any_sync(0xffffffffu, past)) move_maximum<NG, NT>(s, c, kf);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -816,6 +873,12 @@ __device__ __forceinline__ void attend_cell(uint32_t cell, uint32_t mask, const 
     s.l[nt][0] += c[nt][0] + c[nt][2];
     s.l[nt][1] += c[nt][1] + c[nt][3];
   }
+  uint32_t w[NT][NG][2];
+  if (__any_sync(0xffffffffu, weigh<NG, NT>(s, c, w0, w1, w))) {
+    lower_powers<NG, NT>(s, c, w0, w1);
+    weigh<NG, NT>(s, c, w0, w1, w);
+  }
+  const float off = g & 1 ? 7.f : -8.f;
 #pragma unroll
   for (int i = 0; i < NG; ++i) {
     const float y0 = fmaf(off, step_of(w0[i]), centre_of(w0[i])), y1 = fmaf(off, step_of(w1[i]), centre_of(w1[i]));
@@ -825,10 +888,6 @@ __device__ __forceinline__ void attend_cell(uint32_t cell, uint32_t mask, const 
       s.z[nt][i][1] = fmaf(c[nt][1], y0, fmaf(c[nt][3], y1, s.z[nt][i][1]));
     }
   }
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[nt][i] *= sign;
   uint2 v[4];
   {  // the keys of rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9: two apart from each other's, in one order or the other
     const uint32_t row = cell + kCell + 2 * t * kCodeBytes + (g << 3), even = (t & 1) * kCodeBytes, odd = kCodeBytes - even;
@@ -851,9 +910,8 @@ __device__ __forceinline__ void attend_cell(uint32_t cell, uint32_t mask, const 
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if (j % kSteps == 0) {
-          const float s0 = step_of(w0[j / kSteps]), s1 = step_of(w1[j / kSteps]);
-          wb[nt][0] = tc::movmatrix_t(pack_f16(c[nt][0] * s0, c[nt][1] * s0));
-          wb[nt][1] = tc::movmatrix_t(pack_f16(c[nt][2] * s1, c[nt][3] * s1));
+          wb[nt][0] = tc::movmatrix_t(w[nt][j / kSteps][0]);
+          wb[nt][1] = tc::movmatrix_t(w[nt][j / kSteps][1]);
         }
         const uint32_t ar[4] = {r0[2 * i], r0[2 * i + 1], r1[2 * i], r1[2 * i + 1]};
         mma_f16(s.o[nt][j], ar, wb[nt][0], wb[nt][1]);
@@ -979,8 +1037,9 @@ __global__ void __launch_bounds__(32 * AttnShape<NG, NT, MODE>::kW, AttnShape<NG
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float z = s.z[nt][j * NG / 8][i], lo = s.o[nt][j][i], hi = s.o[nt][j][i + 2];
+          const float unit = power_of(24 - exponent_of(s.pw[nt][j * NG / 8][i]));
           *reinterpret_cast<float2*>(row + head * Shape::kRow + 16 * j) =
-              make_float2(fmaf(lo, 0x1p24f, z), fmaf(j & 1 ? hi - lo : hi, 0x1p20f, z));
+              make_float2(fmaf(lo, unit, z), fmaf(j & 1 ? hi - lo : hi, 0x1p-4f * unit, z));
         }
       }
     __syncthreads();
