@@ -852,8 +852,9 @@ skv_status skv_kv4_workspace_size(const skv_problem *p, size_t *bytes);
  * pool, positions outside the candidates: flagged, zero weight.  p->dtype is bf16.  Softmax
  * weights times steps meet the codes as fp16 on the tensor cores: 11 bits, and what lies below
  * 2^-21 of the largest such product of its own query head and channel group is held to 2^-32
- * of that; centres, sums and the maximum are fp32.  Deterministic: the same inputs give the
- * same bits. */
+ * of that (value steps from 2^-75 up; smaller ones in turn to fewer bits); centres, sums and
+ * the maximum are fp32, which holds the sums of values up to 2^116, or of up to 2^20 keys'
+ * up to 2^126.  Deterministic: the same inputs give the same bits. */
 skv_status skv_attn_kv4(const skv_problem *p, const void *q, const skv_kv_pool *pool, int32_t group,
                         const int32_t *idx, void *out, float *lse, void *ws, size_t ws_bytes, int32_t *dev_status,
                         void *stream);

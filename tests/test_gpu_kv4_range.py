@@ -168,3 +168,20 @@ def test_weights_against_steps(skv, G, group, listed, falling):
         return skewed(rng, t) * np.exp2(-at(t))[:, None]
 
     attend(build(skv, G, group, k, v, lambda rng, g: 8 * u + 0.1 * rng.standard_normal((g, D)), listed), listed)
+
+
+@pytest.mark.parametrize("G,group,listed", SHAPES)
+@pytest.mark.parametrize("e", [-110, -70, 60, 100, 118, 120, 125])
+@pytest.mark.parametrize("kind", ["constant", "one group", "steps"])
+def test_magnitudes(skv, G, group, listed, kind, e):
+    """Values from the ends of fp32: groups of one value (steps of 0), one of them beside others, and steps themselves."""
+    def v(rng, t):
+        x = skewed(rng, t)
+        if kind == "steps":
+            return x * 2.0 ** e
+        if kind == "one group":
+            x[:, :group] = 1.5 * 2.0 ** e
+            return x
+        return np.full((len(t), D), -1.25 * 2.0 ** e)
+
+    attend(build(skv, G, group, normal, v, listed=listed), listed)

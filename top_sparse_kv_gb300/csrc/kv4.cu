@@ -714,7 +714,8 @@ __device__ __forceinline__ void logits(uint32_t cell, const QFrag<NT>& f, float 
 
 // ---------------------------------------------------------------------------- attention
 
-// A warp's state of a unit: p_t = 2^(x_t + ref), ref = - the running maximum, a whole number.  The operand of a
+// A warp's state of a unit: p_t = 2^(x_t + ref), ref = -27 - the running maximum, whole numbers.  (A weight is
+// 2^-20 at the most and their sum under 2^10 whatever the keys: values up to 2^116 times it stay in fp32.)  The operand of a
 // key, head and group, w = p s 2^e, has a power of two of its own, which keeps the largest one so far
 // between 2^7 and 2^15: fp16 holds it to 11 bits, and what lies under 2^-21 of that largest to 2^-32 of it.  (A power
 // that heads or groups share goes by the largest product of all, and others' may be lost.)
@@ -729,10 +730,16 @@ struct State {
   float pw[NT][NG][2];  // 2^e; negative where this lane's keys are the complemented ones
 };
 constexpr float kFloor = -3.0e38f;
-constexpr int kPowMin = -100, kPowMax = 110;  // of e: weights times it stay in fp32, and so does its inverse
+// e ends here: weights times it stay in fp32, and steps from 2^-75 up have their largest operand at 2^7.  (It begins
+// at -97: a product lies below 2^105.)
+constexpr int kPowMax = 110;
+constexpr int kShift = 27;
 
 __device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23 & 255u) - 127; }
 __device__ __forceinline__ float power_of(int e) { return e < -126 ? 0.f : __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// of a sum of weights l under the reference -m
+__device__ __forceinline__ float lse_of(float m, float l) { return kLn2 * ((m - (float)kShift) + log2f(l * power_of(kShift))); }
 
 template <int NG, int NT>
 __device__ __forceinline__ void clear(State<NG, NT>& s) {
@@ -768,9 +775,9 @@ __device__ __forceinline__ void move_maximum(State<NG, NT>& s, const float (&c)[
       for (int off = 4; off <= 16; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
       if (m > s.top[nt][i]) {
         m = ceilf(m * kf[nt][i]);
-        const float down = fmaxf(-m - s.ref[nt][i], -1000.f), f = power_of((int)down);
+        const float ref = -(float)kShift - m, down = fmaxf(ref - s.ref[nt][i], -1000.f), f = power_of((int)down);
         const bool first = s.ref[nt][i] == -kFloor;
-        s.ref[nt][i] = -m;
+        s.ref[nt][i] = ref;
         s.top[nt][i] = (m + 7.f) / kf[nt][i];
         if (first) continue;  // (nothing to bring down)
         s.l[nt][i] *= f;
@@ -802,7 +809,7 @@ __device__ __forceinline__ void lower_powers(State<NG, NT>& s, const float (&p)[
 #pragma unroll
         for (int off = 4; off <= 16; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
         if (m * fabsf(s.pw[nt][g][i]) >= 0x1p15f) {
-          const int e = max(7 - exponent_of(m), kPowMin);
+          const int e = 7 - exponent_of(m);
           const float k = power_of(e - exponent_of(s.pw[nt][g][i]));
           s.pw[nt][g][i] = copysignf(power_of(e), s.pw[nt][g][i]);
 #pragma unroll
@@ -1065,7 +1072,7 @@ __global__ void __launch_bounds__(32 * AttnShape<NG, NT, MODE>::kW, AttnShape<NG
       }
       if (whole) {
         a.out[(hq + head) * kD + d] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
-        if (d == 0 && a.lse) a.lse[hq + head] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
+        if (d == 0 && a.lse) a.lse[hq + head] = l == 0.f ? -INFINITY : lse_of(m, l);
       } else {
         slot[head * kD + d] = o;
         if (d == 0) *reinterpret_cast<float2*>(slot + 16 * kD + 2 * head) = make_float2(m, l);
@@ -1147,7 +1154,7 @@ __global__ void __launch_bounds__(kD) kv4_merge_kernel(const Kv4Args a) {
     o = fmaf(f, __ldcg(slots + at(i)), o);
   }
   a.out[hq * kD + d] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
-  if (d == 0 && a.lse) a.lse[hq] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
+  if (d == 0 && a.lse) a.lse[hq] = l == 0.f ? -INFINITY : lse_of(m, l);
 }
 
 // ---------------------------------------------------------------------------- scores
