@@ -23,8 +23,9 @@ def skv():
     return m
 
 
-def attention(q, kv, vv, scale):
-    """(out, lse, tolerance of out, of lse), as kv4_ref.attention, but the fp16 operands held to what their own head
+def attention(q, kv, vv, scale, count=None, adds=None):
+    """(out, lse, tolerance of out, of lse) of rows that occur count times each (once), their sums of at most `adds`
+    additions in turn (as many as rows, and 64), as kv4_ref.attention, but the fp16 operands held to what their own head
     and channel group needs.
 
     A weight times a step, w = p s, is fp16 under a power of two that keeps the largest w of its head and
@@ -35,17 +36,20 @@ def attention(q, kv, vv, scale):
     other terms -- the sums' 2^-23 of their own group's parts, the output's rounding -- are kv4_ref.attention's."""
     k, v = kv4_ref.values(*kv), kv4_ref.values(*vv)
     rep = lambda a: np.repeat(np.abs(a), D // a.shape[-1], -1)  # noqa: E731
-    n = k.shape[0]
+    count = np.ones(k.shape[0]) if count is None else count
+    n = count.sum()
+    adds = n + 64 if adds is None else adds
     x = scale * (q @ k.T)
     dx = scale * 160 * 2.0 ** -23 * (np.abs(q) @ (23 * rep(kv[1]) + rep(kv[2])).T)
-    m = x.max(-1, keepdims=True)
-    p = np.exp(x - m)
+    m = x[:, count > 0].max(-1, keepdims=True)
+    p = np.where(count > 0, np.exp(np.minimum(x - m, 0)), 0)
+    largest = (p[:, :, None] * rep(vv[1])[None, :, ::D // vv[1].shape[-1]]).max(1).repeat(D // vv[1].shape[-1], -1)
+    p = p * count
     l = p.sum(-1, keepdims=True)
     out = p @ v / l
     part = 23 * rep(vv[1]) + rep(vv[2])
-    rel = 2.0 ** -20 + (n + 64) * 2.0 ** -23
+    rel = 2.0 ** -20 + adds * 2.0 ** -23
     off = (p * dx) @ part / l + (p * dx).sum(-1, keepdims=True) / l * np.abs(out)
-    largest = (p[:, :, None] * rep(vv[1])[None]).max(1)
     tol = (p @ (15 * rep(vv[1]))) / l * 2.0 ** -11 + rel * (p @ part) / l + off
     tol = tol + n * 15 * (2.0 ** -32 * largest / l + 2.0 ** (-25 - 110 + 28))
     lse = (m + np.log(l))[:, 0]
