@@ -741,6 +741,7 @@ skv_status skv_prefix_attn(const skv_problem *p, const void *q, const skv_kv_poo
  *   n > 0  the request takes the positions [s, s + n), s = L, or `base` where L is 0 (an
  *          unused row of the batch); its slot-table row gets free blocks for the indices
  *          that its new length needs and its old one did not; its length becomes s + n.
+ *          (A request of length base, the prefix alone, has no block of its own, like one of 0.)
  *   n < 0  its last -n tokens go: the length becomes L + n, or 0 where no token past base
  *          is left; blocks that no longer hold any are free again.  (n = -max_len: all go.)
  *   n = 0  nothing.
