@@ -37,7 +37,7 @@ struct Kv4Args {
   int cells, shift;        // of a block: its cells; log2 of its tokens, or -1
   unsigned n_gpu, n_host;  // blocks there (0 without a host pool)
   unsigned block_cells;    // of a GPU block
-  int agg, Gi;             // scores
+  int Gi;                  // scores: heads a KV head
   float scale_log2;
   int32_t* status;
   float* scores;
@@ -1383,7 +1383,6 @@ Kv4Args kv4_args(const skv_problem& p, const void* q, const PoolView& pool, cons
   a.block_cells = (unsigned)((pool.per_head ? 1 : a.heads) * a.cells);
   a.n_gpu = (unsigned)pool.n_gpu;
   a.n_host = pool.host_k != nullptr ? (unsigned)pool.n_host : 0u;
-  a.agg = p.group_agg;
   a.Gi = p.n_idx_q_heads / p.n_kv_heads;
   a.scale_log2 = (p.sm_scale > 0.f ? p.sm_scale : 1.f / sqrtf((float)p.d_qk)) * kLog2e;
   a.status = status;
