@@ -177,7 +177,9 @@ __device__ __forceinline__ uint4 narrow(const float* x) {  // the one rounding
 // each holds neighbours of one u: lanes whose i differs in a bit give each other the bytes whose u
 // differs in the same bit.  Every lane of the row's LPR takes part; cell null: nothing is written.
 // 8,192 tokens of 64 query, 8 key and 8 value heads of 128 bf16 go in 78 us, 323 MB, bound by issue (65 %
-// of the slots; the query rows, norm and rotation alone, are most of it); 64 tokens in 5.
+// of the slots; the query rows, norm and rotation alone, are most of it); 64 tokens in 5.  Codes come by a
+// reciprocal, for steps under 2^-100 by a division an entry.  8,192 tokens of 8 query heads and one KV head, half
+// a warp idle at every row: 48 us; 16 and two: 42.
 template <int VE, int LPR, int NG>
 __device__ __forceinline__ void put_row4(const float (&x)[VE], unsigned char* cell, int rc, int sub) {
   constexpr int kLanes = LPR / NG;  // of a group
@@ -194,7 +196,8 @@ __device__ __forceinline__ void put_row4(const float (&x)[VE], unsigned char* ce
   const float inv = 1.f / s;
 #pragma unroll
   for (int j = 0; j < VE; ++j) w += kv4_code(x[j], s, z, inv) << (4 * j);
-  if (__any_sync(0xffffffffu, s < 0x1p-100f)) {  // (a step of 0 among them)
+  // (a step of 0 among them; lanes without a row have one too, and no say)
+  if (__any_sync(0xffffffffu, cell != nullptr && s < 0x1p-100f)) {
     w = 0;
 #pragma unroll 1
     for (int j = VE - 1; j >= 0; --j) {
