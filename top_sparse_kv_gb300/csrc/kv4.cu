@@ -934,10 +934,11 @@ struct AttnShape {
   // Warps of a CTA, CTAs a SM, stages of 2.2 to 2.5 KB a warp.  One CTA a SM: of two, the schedulers serve
   // the one that came first before the other, it ends at 80 % of the time and leaves the SM half empty
   // (a million keys in groups of 128, 8 warps in either: 231 us; 12 or 16 warps in one 215, 8 warps
-  // 258).  16 warps have 128 registers each, 12 have 168: groups of 128 fit in the first (201 us with
-  // 12, 198 with 16), those of 32 and 64 do not (8 requests of 32K: 73 us with 12, 74 with 16).  A
+  // 258).  16 warps have 128 registers each, 12 have 168: groups of 128 fit in the first (211 us with
+  // 12, 201 with 16), those of 32 and 64 do not (8 requests of 32K: 78 us with 12, 82 with 16).  A
   // list's rows arrive late rather, and two CTAs hide more of that (3,409 rows of 32K for 8 requests:
-  // 26.8 us, one CTA 28.8).  Two column tiles take all the registers of 8 warps.
+  // 26.8 us, one CTA 28.8), although groups of 32 and 64 spill there (100 and 12 bytes a thread).  Two column
+  // tiles take all the registers of 8 warps.
   static constexpr int kCtas = NT == 1 && MODE == kList ? 2 : 1;
   static constexpr int kW = NT == 2 || MODE == kList ? 8 : NG == 1 ? 16 : 12;
   static constexpr int kStages = NT == 2 ? 6 : MODE == kList || NG == 1 ? 3 : 5;
@@ -957,13 +958,12 @@ struct Pick<kList, NG, W, S> {
 };
 
 // Persistent CTAs, a share each of the tiles of all units; a warp computes its own tiles.  Measured
-// (8 KV heads): 8 requests of 32K keys in groups of 32, 8 query heads each, 336 MB, 73 us (4.6 TB/s); a
-// million keys in groups of 128, 4 query heads, 1,141 MB, 201 us (5.7 TB/s); lists of 3,409 rows of 32K
-// for the 8 requests, 52 MB read, 23 us; 4 requests to 777 keys 10.7 us a call.  The instructions of
-// a tile bound it: 350 in groups of 32, 146 of them masks, permutations and shifts at half the
-// issue rate, and 18 products; on cells from L2 alone the first of these takes 2 us less, with
-// the copies alone 60 (a million keys: 178).  4 us pass before the first product: lengths, the
-// share's ends, table, cells.
+// (8 KV heads): 8 requests of 32K keys in groups of 32, 8 query heads each, 336 MB, 75 us (4.5 TB/s); a
+// million keys in groups of 128, 4 query heads, 1,141 MB, 199 us (5.7 TB/s); lists of 3,409 rows of 32K
+// for the 8 requests, 52 MB read, 24.5 us; 4 requests to 777 keys 11.3 us a call.  The instructions of
+// a tile and how they wait for each other bound it: 360 in groups of 32, 154 of them masks, permutations and
+// shifts at half the issue rate, and 18 products, at 60 % of the issue slots; the copies alone take 60
+// (a million keys: 178).  4 us pass before the first product: lengths, the share's ends, table, cells.
 template <int NG, int NT, int MODE>
 __global__ void __launch_bounds__(32 * AttnShape<NG, NT, MODE>::kW, AttnShape<NG, NT, MODE>::kCtas) kv4_attn_kernel(const Kv4Args a) {
   using Shape = AttnShape<NG, NT, MODE>;
@@ -1098,7 +1098,8 @@ __global__ void __launch_bounds__(32 * AttnShape<NG, NT, MODE>::kW, AttnShape<NG
   }
 }
 
-// The units that no CTA held alone: their partials joined, a CTA a head; the empty ones: zeros.  A launch and two
+// The units that no CTA held alone: their partials joined, a CTA a head; the empty ones: zeros; the others' CTAs
+// return (of many short requests that is most of the grid).  A launch and two
 // loads' latency, 2 us behind the attention's last CTA (by the last CTA to finish, it would need counters that
 // somebody zeroes).
 template <int MODE>
