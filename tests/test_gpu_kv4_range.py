@@ -189,3 +189,17 @@ def test_magnitudes(skv, G, group, listed, kind, e):
         return np.full((len(t), D), -1.25 * 2.0 ** e)
 
     attend(build(skv, G, group, normal, v, listed=listed), listed)
+
+
+@pytest.mark.parametrize("G,group,listed", SHAPES)
+def test_heads_alone(skv, G, group, listed):
+    """A head's bits are of its own query, whatever maxima and operands the heads beside it meet."""
+    def v(rng, t):
+        return skewed(rng, t) * np.exp2(rng.integers(-12, 12, (len(t), 1)))
+
+    c = build(skv, G, group, normal, v, listed=listed)
+    first = attend(c, listed)
+    c.q[:, ::2] *= 40
+    out, lse = attend(c, listed)
+    assert torch.equal(out[:, 1::2], first[0][:, 1::2]) and torch.equal(lse[:, 1::2], first[1][:, 1::2])
+    assert not torch.equal(out[:, ::2], first[0][:, ::2])
